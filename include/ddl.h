@@ -277,6 +277,142 @@ int ddl_stack_decode_noalloc(const ddl_shape* shape, ddl_wtype wtype, const ddl_
                              const float* resid_in, const uint16_t* x_bf16, float* resid_out,
                              uint16_t* out_bf16, void* stream);
 
+/* ------------------------------------------------------------ 8-bit KV cache
+ * A paged KV cache of half the bytes: 8-bit codes with one fp32 scale for
+ * each block of DDL_KV8_BLOCK consecutive tokens and K/V head (value = code *
+ * scale), and what a serving step does with it: place the step's rows
+ * (ddl_page_plan), store them (ddl_kv8_append), attend (ddl_kv8_attention).
+ * Lengths, positions, page tables and slots are device arrays: no call of
+ * this section copies from the host or waits for the device, so a captured
+ * step can be replayed while they change.  None of these calls keeps anything
+ * in a workspace from one call to the next. */
+
+#define DDL_KV8_BLOCK 16        /* tokens that share a scale */
+#define DDL_KV8_MAX_HEADS 1024  /* H_kv */
+#define DDL_KV8_MAX_REQS 4096   /* requests of a call */
+#define DDL_KV8_MAX_APPEND 65536 /* rows of one append */
+#define DDL_KV8_MAX_ROWS 64     /* rows of one request in an attention call */
+
+/* Code types.  E4M3: 1 sign, 4 exponent, 3 mantissa bits, largest 448, no
+ * infinity, NaN 0x7F / 0xFF.  INT8: two's complement, -127 .. 127. */
+typedef enum { DDL_KV8_E4M3 = 0, DDL_KV8_INT8 = 1 } ddl_kv8_type;
+
+/* Element types of rows that enter or leave these calls. */
+typedef enum { DDL_T_F32 = 0, DDL_T_BF16 = 1, DDL_T_F16 = 2 } ddl_dtype;
+
+/* One layer's cache (device pointers).  k, v: codes [pages][H_kv][page_size]
+ * [head_dim]; k_scale, v_scale: fp32 [pages][H_kv][page_size / 16].
+ * page_size: a power of two in [16, 2^20] (DDL_ERR_ARG); pages * page_size <
+ * 2^31 (DDL_ERR_UNSUPPORTED); head_dim 64 or 128, 1 <= H_kv <=
+ * DDL_KV8_MAX_HEADS (DDL_ERR_SHAPE).  Slot t of a sequence is row t %
+ * page_size of page page_table[t / page_size]; the *slot index* of a row is
+ * page * page_size + t % page_size. */
+typedef struct {
+    uint8_t* k;
+    uint8_t* v;
+    float* k_scale;
+    float* v_scale;
+    int64_t pages;
+    int32_t page_size;
+    int32_t type; /* ddl_kv8_type */
+} ddl_kv8;
+
+/* Page tables and slot maps of one step, from the requests' lengths.  Request
+ * r holds old_len[r] tokens and brings add_len[r] rows; it needs need[r] =
+ * ceil((old + add) / page_size) - ceil(old / page_size) new pages.
+ *  - A request is refused with status[r] = 1 when old < 0, add < 0 or old +
+ *    add > pages_per_seq * page_size; else with 2 when need[r] > 0 and the sum
+ *    of need over it and all earlier requests not refused with 1 exceeds
+ *    n_free; else with 3 when add > 0 and the same sum of add exceeds T.  So
+ *    no request overtakes an earlier one that found no room, unless it needs
+ *    none.  All others are admitted: status[r] = 0.
+ *  - Admitted requests take free_pages[0 .. used) in request order; the new
+ *    ids go to page_table[r][ceil(old / page_size) ...].  Other entries stay.
+ *    The entries of the old tokens must be there already.
+ *  - row_off[0 .. R]: rows before each request (refused ones have none);
+ *    kv_len[r] = old + add of an admitted request, else old (clamped to
+ *    [0, pages_per_seq * page_size]); for row i of the step (i < row_off[R])
+ *    row_pos[i] = its position and slot[i] = its slot index; both -1 behind
+ *    the last row, up to T.  used[0] = row count of free pages taken.
+ * All pointers device int32: old_len, add_len, kv_len, status [R]; row_off
+ * [R + 1]; row_pos, slot [T]; free_pages [n_free] (distinct ids, none in use);
+ * page_table [R][pages_per_seq]; used [1].  1 <= R <= DDL_KV8_MAX_REQS
+ * (DDL_ERR_UNSUPPORTED above), T >= 0, n_free >= 0, 4-byte aligned.  Outputs
+ * must not overlap inputs or one another (DDL_ERR_ARG where kv_len is
+ * old_len or add_len); page_table is both. */
+int ddl_page_plan(const int32_t* old_len, const int32_t* add_len, int32_t R, int32_t page_size,
+                  const int32_t* free_pages, int32_t n_free, int32_t* page_table,
+                  int32_t pages_per_seq, int32_t* row_off, int32_t* kv_len, int32_t* row_pos,
+                  int32_t* slot, int32_t T, int32_t* used, int32_t* status, void* stream);
+
+/* Store T rows of K and V at their slot indices (negative: a padding row,
+ * skipped).  Per (16-token block, head), for K and V alike: fresh = the
+ * smallest power of two (>= 2^-126) with max|x| / fresh <= 448 (E4M3) or 127
+ * (INT8) over the call's rows of the block, 0 if they are all zero; scale =
+ * max(fresh, the block's old scale if the first of these rows is not the
+ * block's first token); new codes are x / scale rounded to nearest, ties to
+ * even.  When the scale grows, the codes of the block's earlier tokens are
+ * multiplied by old / new and rounded again (for scales written by this call
+ * a power of two: E4M3 codes keep their value unless they become subnormal).
+ * The block's tokens after the rows have no defined content.
+ * Infinite x take the largest code of their sign, NaN the E4M3 NaN or INT8 0;
+ * neither counts for the scale.
+ *  - A run of rows of one block that are neighbours in the slot map, as
+ *    ddl_page_plan lays them out, is stored as said above; separate runs of
+ *    one block are stored one after the other, in map order.  Where a slot
+ *    occurs twice the last row counts.
+ *  - A slot >= pages * page_size is skipped and sets *bad_out (device int32,
+ *    may be NULL, never cleared by the call) to 1.
+ * k_new, v_new: device [T][H_kv][head_dim] of `dtype`, heads contiguous, rows
+ * k_stride / v_stride elements apart (>= H_kv * head_dim and a multiple of 8),
+ * 16-byte aligned.  slot: device int32 [T], 1 <= T <= DDL_KV8_MAX_APPEND
+ * (DDL_ERR_UNSUPPORTED above). */
+int ddl_kv8_append(const ddl_kv8* kv, int32_t H_kv, int32_t head_dim, ddl_dtype dtype, const void* k_new,
+                   int64_t k_stride, const void* v_new, int64_t v_stride, const int32_t* slot, int32_t T,
+                   int32_t* bad_out, void* stream);
+
+/* Attention over an 8-bit paged cache.  Request r has n = q_off[r + 1] -
+ * q_off[r] rows (q_off NULL: one row each, row r), the newest tokens of its
+ * kv_len[r]: row i sits at position p = kv_len[r] - n + i, and head h of it
+ * attends, with K/V head floor(h / (H_q / H_kv)), to the keys j with
+ * 0 <= j <= p, and p - j < window when window > 0:
+ *     s_j = scale q . k_j;  softcap > 0: s_j = softcap tanh(s_j / softcap);
+ *     slopes: s_j -= slopes[h] (p - j);
+ *     out = sum_j exp(s_j) v_j / sum_j exp(s_j),  lse = log sum_j exp(s_j).
+ * A row without keys gives zeros and lse = -inf.  Rows of q that belong to no
+ * request are neither read nor written.  A NaN code among the keys a row sees
+ * gives NaN in its output; whatever lies in slots it does not see has no
+ * effect.
+ *  - H_q % H_kv == 0, H_q / H_kv <= 8, head_dim 64 or 128 (DDL_ERR_SHAPE).
+ *  - q, out: device [T][H_q][head_dim] of `dtype`, heads contiguous, rows
+ *    q_stride / out_stride elements apart (>= H_q * head_dim, a multiple of 8),
+ *    16-byte aligned.  Scores, softmax and sums are fp32.  lse: device fp32
+ *    [T][H_q] or NULL.  out must not overlap q.
+ *  - 1 <= R <= DDL_KV8_MAX_REQS.  max_rows: a bound on n, <= DDL_KV8_MAX_ROWS
+ *    (1 without q_off).  max_len >= 1: a bound on kv_len.  Both only size the
+ *    launch; a request beyond them (or beyond its table row, or with rows
+ *    outside [0, T)) is computed on what lies within them, and a page id
+ *    outside the pool counts as a block without keys; either sets *bad_out
+ *    (device int32, may be NULL, never cleared by the call) to 1.
+ *  - scale: finite; softcap >= 0, window >= 0 (0: none); slopes: device fp32
+ *    [H_q] or NULL.
+ *  - workspace: device, >= ddl_kv8_attention_workspace_bytes(...) of the same
+ *    sizes (0 for invalid ones; it depends on the device's SM count).  Calls
+ *    sharing a workspace must be ordered on one stream. */
+typedef struct {
+    float scale;
+    float softcap;
+    int32_t window;
+    const float* slopes;
+} ddl_attn_opts;
+size_t ddl_kv8_attention_workspace_bytes(int32_t H_q, int32_t H_kv, int32_t head_dim, int32_t R, int32_t T,
+                                         int32_t max_rows, int32_t max_len);
+int ddl_kv8_attention(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, int32_t head_dim, ddl_dtype dtype,
+                      const ddl_attn_opts* opts, int32_t R, int32_t T, int32_t max_rows, int32_t max_len,
+                      const int32_t* q_off, const int32_t* kv_len, const int32_t* page_table,
+                      int32_t pages_per_seq, const void* q, int64_t q_stride, void* out, int64_t out_stride,
+                      float* lse, int32_t* bad_out, void* workspace, size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------ token step
  * The steps on either side of the layer stack in the primer's §1.2
  * decode step: the last token's embedding row before it, and after it a token

@@ -1,0 +1,773 @@
+// ddl_kv8_attn.cu -- attention over the 8-bit paged KV cache.
+//
+// For a query row q at position p and the keys j it sees,
+//     s_j = scale q . k_j  (capped, biased),  out = sum_j e^{s_j} v_j / sum_j e^{s_j},
+// with k_j = ks code_j and one scale ks for 16 tokens.  One pass over the
+// codes with a running maximum m and sum l per query (base 2: s log2 e).
+//
+// A warp takes 16 tokens (one scale block) x 8 queries at a time, the queries
+// being the heads of one K/V head's group times the request's rows:
+//  - S^T = K Q^T on m16n8k16 MMAs with the 16 tokens as M.  The order of the
+//    head dimensions inside the contraction is free as long as K and Q agree,
+//    so lane (g, t) takes hd/4 *neighbouring* bytes of token rows g and g + 8:
+//    the codes go from global memory straight into registers, 16 bytes a load,
+//    and each 4 of them become the lane's part of one k-step of A.
+//  - O^T += V^T P^T with the head dimensions as M.  Lane (g, t) takes the
+//    hd/8 neighbouring bytes at hd/8 g of tokens 2t, 2t+1, 2t+8, 2t+9; byte
+//    permutes pair the tokens and conversion gives A.  P^T comes from the S^T
+//    accumulators by movmatrix.
+// So no code passes through shared memory and both streams are read in whole
+// 128-byte rows.  e4m3 and int8 codes are exact in fp16.  Q is scaled by a
+// power of two per query and split into fp16 high part and (fp32 rows only)
+// remainder: bf16 and fp16 values fit the high part (down to 2^-26 of the
+// row's largest).  P (with V's scale, relative to the largest seen by the warp)
+// is likewise one fp16 (16-bit outputs: its 2^-12 is below their own rounding)
+// or two.  Scores, m, l and O are fp32.
+//
+// Work: a CTA of 8 warps takes one chunk of tokens of one (request, K/V head)
+// and up to 8 tiles of 8 queries; with fewer tiles the warps share out the
+// chunk's blocks.  Chunks of one request are joined by a second kernel from
+// fp32 records (max, sum, O) in the workspace, in chunk order.
+#include <cuda_bf16.h>
+
+#include <mutex>
+
+#include "ddl_kv8.h"
+
+namespace ddl {
+namespace {
+
+constexpr int ATT_WARPS = 8;
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+// P's fp16 values carry 2^11: with the running maximum allowed to lag by
+// 2^M_LAG they stay below 2^16, and what rounds off below fp16's smallest
+// subnormal is 2^-36 of the largest weight.
+constexpr float P_SCALE = 2048.f;
+constexpr float M_LAG = 4.f;
+
+struct AttArgs {
+  const uint8_t *k, *v;
+  const float *ks, *vs;
+  const int32_t *q_off, *kv_len, *table;
+  const void* q;
+  void* out;
+  float* lse;
+  int32_t* bad;
+  float *rec_o, *rec_ml;  // [T * H_q][nsplit][hd], [..][2]
+  const float* slopes;
+  int64_t pages, q_stride, out_stride;
+  float scale, softcap;
+  int32_t window;
+  int32_t R, T, Hq, Hkv, GH, hd, pshift, per, max_rows, max_len;
+  int32_t nsplit, chunk;  // chunk: blocks of 16 tokens a CTA takes
+  int32_t nq, nqc;        // query tiles of 8 a CTA takes (a power of two <= 8), CTAs over the query tiles
+};
+
+// A request's rows and keys as the kernels compute them (clamped to what the
+// launch and the tables allow).
+struct Req {
+  int32_t row0, n, len;  // first row of q, rows, tokens
+  int32_t p0;            // position of its first row (negative: it has no keys)
+  int32_t b0, b1;        // blocks of 16 tokens that any of its rows sees: [b0, b1)
+  bool bad;
+};
+__device__ __forceinline__ Req load_req(const AttArgs& A, int r) {
+  Req q;
+  int64_t row0 = r, n = 1;
+  if (A.q_off) {
+    row0 = A.q_off[r];
+    n = (int64_t)A.q_off[r + 1] - row0;
+  }
+  int64_t len = A.kv_len[r];
+  const int64_t cap = (int64_t)A.per << A.pshift;
+  q.bad = false;
+  if (row0 < 0 || n < 0 || row0 + n > A.T) {
+    q.bad = true;
+    n = 0;
+    row0 = 0;
+  }
+  if (len < 0 || len > A.max_len || len > cap) {
+    q.bad = true;
+    len = len < 0 ? 0 : len;
+    len = len > A.max_len ? A.max_len : len;
+    len = len > cap ? cap : len;
+  }
+  q.row0 = (int32_t)row0;
+  q.len = (int32_t)len;
+  q.p0 = (int32_t)(len - n);  // (n <= T)
+  int64_t lo = A.window > 0 ? len - n - A.window + 1 : 0;
+  lo = lo < 0 ? 0 : lo;
+  if (n > A.max_rows) {
+    q.bad = true;
+    n = A.max_rows;  // its first rows
+  }
+  q.n = (int32_t)n;
+  q.b0 = (int32_t)(lo >> 4);
+  q.b1 = n > 0 ? (int32_t)((len + 15) >> 4) : q.b0;
+  if (q.b1 < q.b0) q.b1 = q.b0;
+  return q;
+}
+
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+// 16 bytes of codes, read once by this warp (or again soon by the warps of
+// the same CTA that hold other queries).
+__device__ __forceinline__ uint4 ld_codes16(const uint8_t* p) {
+  return __ldg(reinterpret_cast<const uint4*>(p));
+}
+
+// Bytes lo16 / hi16 of w (two codes) as fp16 pairs.
+template <int CT>
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if (CT == DDL_KV8_E4M3) {
+    lo = e4m3x2_f16x2((uint16_t)(w & 0xffffu));
+    hi = e4m3x2_f16x2((uint16_t)(w >> 16));
+  } else {  // 1024 + (c + 128) - 1152 = c, exact in fp16
+    const uint32_t u = w ^ 0x80808080u;
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+  }
+}
+
+// Byte mask of the e4m3 NaN codes (low 7 bits all set) of four codes.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  const uint32_t top = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+  return (top >> 7) * 255u;
+}
+
+template <int DT>
+__device__ __forceinline__ float load_elem(const void* p, int64_t i) {
+  if (DT == DDL_T_F32) return reinterpret_cast<const float*>(p)[i];
+  const uint16_t b = reinterpret_cast<const uint16_t*>(p)[i];
+  if (DT == DDL_T_BF16) return bf16_bits_to_f32(b);
+  return __half2float(__ushort_as_half(b));
+}
+// Four neighbouring elements (8- or 16-byte aligned).
+template <int DT>
+__device__ __forceinline__ float4 load_elem4(const void* p, int64_t i) {
+  if (DT == DDL_T_F32) return *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + i);
+  const uint2 u = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p) + i);
+  if (DT == DDL_T_BF16) return make_float4(bf16lo_f32(u.x), bf16hi_f32(u.x), bf16lo_f32(u.y), bf16hi_f32(u.y));
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+template <int DT>
+__device__ __forceinline__ void store_elem4(void* p, int64_t i, float4 v) {
+  if (DT == DDL_T_F32) {
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + i) = v;
+  } else {
+    uint2 u;
+    if (DT == DDL_T_BF16) u = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    else u = make_uint2(pack_f16x2(v.x, v.y), pack_f16x2(v.z, v.w));
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p) + i) = u;
+  }
+}
+
+// tanh from its definition 1 - 2 / (e^{2x} + 1): an absolute error of a few
+// 2^-24, which times the cap is the score's own fp32 rounding.
+__device__ __forceinline__ float cap_tanh(float x) { return 1.f - __fdividef(2.f, __expf(2.f * x) + 1.f); }
+
+template <int CT, int DT, int HD, bool EX>
+__global__ void __launch_bounds__(ATT_WARPS * 32, 2) kv8_attention_kernel(const __grid_constant__ AttArgs A) {
+  constexpr int KS = HD / 16;        // k-steps of the score MMAs
+  constexpr int NV = HD / 64;        // 16-byte loads of a K row per lane
+  constexpr int MT = HD / 16;        // M tiles of the output MMAs
+  constexpr bool HL = DT == DDL_T_F32;
+  constexpr int OROW = HD + 4;
+  __shared__ float so[ATT_WARPS][8][OROW];
+  __shared__ float sml[ATT_WARPS][8][2];
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  int bid = blockIdx.x;
+  const int split = bid % A.nsplit;
+  bid /= A.nsplit;
+  const int qc = bid % A.nqc;
+  bid /= A.nqc;
+  const int h = bid % A.Hkv, r = bid / A.Hkv;
+  const Req rq = load_req(A, r);
+  if (rq.bad && A.bad && threadIdx.x == 0) atomicOr(A.bad, 1);
+  const int nqueries = rq.n * A.GH;
+  if (qc * A.nq * 8 >= nqueries) return;  // no rows in these tiles
+  const int c0 = rq.b0 + split * A.chunk;
+  const int c1 = min(rq.b1, c0 + A.chunk);
+  if (c0 >= rq.b1 && split > 0) return;  // (chunk 0 writes the rows of a request without keys)
+  const int groups = ATT_WARPS / A.nq;   // warps that share a tile's blocks
+  const int tile = qc * A.nq + warp % A.nq, kg = warp / A.nq;
+  const bool live = tile * 8 < nqueries;
+
+  // queries of this lane: column g of Q^T's fragments, columns 2t, 2t + 1 of the scores
+  uint32_t qh[KS][2], ql[HL ? KS : 1][2];
+  float qf = 0.f;  // 2^e of query g
+  {
+    const int qi = tile * 8 + g;
+    const bool has = qi < nqueries;
+    const int row = has ? qi / A.GH : 0, head = h * A.GH + (has ? qi % A.GH : 0);
+    const int64_t at = (int64_t)(rq.row0 + row) * A.q_stride + (int64_t)head * HD + t * (HD / 4);
+    float4 f[KS];
+    float mx = 0.f;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      f[s] = has ? load_elem4<DT>(A.q, at + 4 * s) : make_float4(0.f, 0.f, 0.f, 0.f);
+      mx = fmaxf(mx, fmaxf(fmaxf(fabsf(f[s].x), fabsf(f[s].y)), fmaxf(fabsf(f[s].z), fabsf(f[s].w))));
+    }
+    mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
+    int e = (int)((__float_as_uint(mx) >> 23) & 255u) - 127 - 12;  // the largest lands in [2^12, 2^13)
+    e = e < -100 ? -100 : e > 115 ? 115 : e;
+    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+    qf = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const float4 v = make_float4(f[s].x * down, f[s].y * down, f[s].z * down, f[s].w * down);
+      qh[s][0] = pack_f16x2(v.x, v.y);
+      qh[s][1] = pack_f16x2(v.z, v.w);
+      if (HL) {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&qh[s][0]));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&qh[s][1]));
+        ql[HL ? s : 0][0] = pack_f16x2(v.x - a.x, v.y - a.y);
+        ql[HL ? s : 0][1] = pack_f16x2(v.z - b.x, v.w - b.y);
+      }
+    }
+  }
+  // per score column: factor, the last and first key it sees, slope
+  float cf[2], slope[2];
+  int hi[2], lo[2];
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int qi = tile * 8 + 2 * t + c;
+    const bool has = qi < nqueries;
+    const int row = has ? qi / A.GH : 0;
+    const int p = rq.p0 + row;
+    hi[c] = has ? p : -1;
+    lo[c] = A.window > 0 ? p - A.window + 1 : 0;
+    const float q2 = __shfl_sync(FULL, qf, 4 * (2 * t + c));
+    cf[c] = q2 * A.scale;
+    slope[c] = EX && A.slopes && has ? A.slopes[h * A.GH + qi % A.GH] * LOG2E : 0.f;
+    if (!EX) cf[c] *= LOG2E;
+    else if (A.softcap > 0.f) cf[c] = __fdiv_rn(cf[c], A.softcap);
+    else cf[c] *= LOG2E;
+  }
+  // keys that every column of the tile sees: blocks inside need no masks
+  int all_hi = min(hi[0], hi[1]), all_lo = max(lo[0], lo[1]), any_hi = max(hi[0], hi[1]);
+  {
+    const bool h0 = tile * 8 + 2 * t < nqueries, h1 = tile * 8 + 2 * t + 1 < nqueries;
+    all_hi = h0 ? (h1 ? all_hi : hi[0]) : 0x7fffffff;
+    all_lo = h0 ? (h1 ? all_lo : lo[0]) : 0;
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      all_hi = min(all_hi, __shfl_xor_sync(FULL, all_hi, o));
+      all_lo = max(all_lo, __shfl_xor_sync(FULL, all_lo, o));
+      any_hi = max(any_hi, __shfl_xor_sync(FULL, any_hi, o));
+    }
+  }
+
+  float o[MT][4];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
+  float mrun[2] = {-INFINITY, -INFINITY}, lrun[2] = {0.f, 0.f};
+  float vref = 0.f;  // the largest V scale so far: P carries scale / vref
+
+  const int nb = live && c1 > c0 + kg ? (c1 - c0 - kg + groups - 1) / groups : 0;  // this warp's blocks
+  // block i of this warp: c0 + kg + i * groups; lane l holds the page row and
+  // the scales of blocks 32 w + l (this batch of 32) and the next batch's rows
+  const int bshift = A.pshift - 4, bmask = (1 << bshift) - 1;
+  auto block_row = [&](int i) -> int32_t {  // the block's index in the pool's [page][head][block] view, -1: none
+    int64_t idx = -1;
+    if (i < nb) {
+      const int b = c0 + kg + i * groups;
+      const int32_t page = A.table[(int64_t)r * A.per + (b >> bshift)];
+      if (page >= 0 && page < A.pages) return page;
+      if (A.bad) atomicOr(A.bad, 1);
+    }
+    return (int32_t)idx;
+  };
+  auto flat = [&](int32_t page, int i) -> int64_t {  // index of the block among all heads' blocks
+    const int b = c0 + kg + i * groups;
+    return (((int64_t)page * A.Hkv + h) << bshift) + (b & bmask);
+  };
+  int32_t page_l = block_row(lane), page_n = -1;
+  float ks_l = 0.f, vs_l = 0.f;
+  if (page_l >= 0) {
+    const int64_t f = flat(page_l, lane);
+    ks_l = A.ks[f];
+    vs_l = A.vs[f];
+  }
+  uint4 kb[2][NV], vb[4];  // K: rows g, g + 8; V: tokens 2t, 2t+1, 2t+8, 2t+9
+  auto load_k = [&](int64_t f) {
+    const uint8_t* p = A.k + f * (16 * HD) + t * (HD / 4);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int u = 0; u < NV; ++u) kb[j][u] = ld_codes16(p + (g + 8 * j) * HD + 16 * u);
+  };
+  auto load_v = [&](int64_t f) {
+    const uint8_t* p = A.v + f * (16 * HD) + g * (HD / 8);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint8_t* row = p + (2 * t + (j & 1) + (j >> 1) * 8) * HD;
+      if (HD == 128) {
+        vb[j] = ld_codes16(row);
+      } else {
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(row));
+        vb[j].x = x.x;
+        vb[j].y = x.y;
+      }
+    }
+  };
+  int32_t page0 = __shfl_sync(FULL, page_l, 0);
+  if (nb > 0) {
+    const int64_t f = flat(page0 < 0 ? 0 : page0, 0);
+    load_k(f);
+    load_v(f);
+  }
+
+#pragma unroll 1
+  for (int i = 0; i < nb; ++i) {
+    const int l = i & 31;
+    if (l == 16) page_n = block_row((i & ~31) + 32 + lane);  // the next batch's rows, long before they are used
+    const int32_t page = __shfl_sync(FULL, page_l, l);
+    const float ks = __shfl_sync(FULL, ks_l, l), vs = __shfl_sync(FULL, vs_l, l);
+    if (l == 31) {  // on to the next batch
+      page_l = page_n;
+      ks_l = vs_l = 0.f;
+      if (page_l >= 0) {
+        const int64_t f = flat(page_l, i + 1 + lane);
+        ks_l = A.ks[f];
+        vs_l = A.vs[f];
+      }
+    }
+    const int32_t pnext = __shfl_sync(FULL, page_l, (i + 1) & 31);
+    const int64_t fnext = flat(pnext < 0 ? 0 : pnext, i + 1);
+    const bool more = i + 1 < nb;
+    const int key0 = (c0 + kg + i * groups) * 16;
+
+    // scores of tokens g (c 0, 1) and g + 8 (c 2, 3) for queries 2t, 2t + 1
+    float c[4] = {0.f, 0.f, 0.f, 0.f}, c2[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const uint4 x = kb[0][s / 4], y = kb[1][s / 4];
+      const uint32_t wx = (s & 3) == 0 ? x.x : (s & 3) == 1 ? x.y : (s & 3) == 2 ? x.z : x.w;
+      const uint32_t wy = (s & 3) == 0 ? y.x : (s & 3) == 1 ? y.y : (s & 3) == 2 ? y.z : y.w;
+      uint32_t a0, a1, a2, a3;
+      codes_f16<CT>(wx, a0, a2);
+      codes_f16<CT>(wy, a1, a3);
+      mma_f16((s & 1) ? c2 : c, a0, a1, a2, a3, qh[s][0], qh[s][1]);
+      if (HL) mma_f16((s & 1) ? c2 : c, a0, a1, a2, a3, ql[HL ? s : 0][0], ql[HL ? s : 0][1]);
+    }
+    if (more) load_k(fnext);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int col = j & 1;
+      float s = (c[j] + c2[j]) * ks * cf[col];
+      if (EX) {
+        if (A.softcap > 0.f) s = A.softcap * LOG2E * cap_tanh(s);
+        s -= slope[col] * (float)(hi[col] - (key0 + g + (j >> 1) * 8));
+      }
+      c[j] = s;
+    }
+    const bool edge = page < 0 || key0 + 15 > all_hi || key0 < all_lo;
+    if (edge) {  // some column does not see some token, or the block is missing
+      const int first = page < 0 ? 0x7fffffff : key0;
+      uint32_t dead = 0;  // this lane's V tokens that nobody sees
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int key = key0 + 2 * t + (j & 1) + (j >> 1) * 8;
+        if (page < 0 || key > any_hi) dead |= 1u << j;
+      }
+      uint32_t nan = 0;  // ... that hold a NaN code
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t w[4] = {vb[j].x, vb[j].y, HD == 128 ? vb[j].z : 0u, HD == 128 ? vb[j].w : 0u};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if ((dead >> j) & 1u) w[u] = 0u;
+          if (CT == DDL_KV8_E4M3) {
+            const uint32_t m = nan_bytes(w[u]);
+            if (m) nan |= 1u << (2 * t + (j & 1) + (j >> 1) * 8);
+            w[u] &= ~m;
+          }
+        }
+        vb[j].x = w[0];
+        vb[j].y = w[1];
+        if (HD == 128) {
+          vb[j].z = w[2];
+          vb[j].w = w[3];
+        }
+      }
+      // a NaN in V reaches exactly the queries that see its token, through their scores
+      if (CT == DDL_KV8_E4M3) nan = __reduce_or_sync(FULL, nan);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int off = g + (j >> 1) * 8, key = key0 + off, col = j & 1;
+        if (first == 0x7fffffff || key > hi[col] || key < lo[col]) c[j] = -INFINITY;
+        else if ((nan >> off) & 1u) c[j] = __uint_as_float(0x7fffffffu);
+      }
+    }
+    // running maximum: raised only when some score passes it by M_LAG
+    const float t0 = fmaxf(c[0], c[2]), t1 = fmaxf(c[1], c[3]);
+    if (__any_sync(FULL, t0 > mrun[0] + M_LAG || t1 > mrun[1] + M_LAG)) {
+      float n0 = t0, n1 = t1;
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) {
+        n0 = fmaxf(n0, __shfl_xor_sync(FULL, n0, x));
+        n1 = fmaxf(n1, __shfl_xor_sync(FULL, n1, x));
+      }
+      n0 = fmaxf(n0, mrun[0]);
+      n1 = fmaxf(n1, mrun[1]);
+      const float a0 = mrun[0] == -INFINITY ? 0.f : exp2f(mrun[0] - n0);
+      const float a1 = mrun[1] == -INFINITY ? 0.f : exp2f(mrun[1] - n1);
+      mrun[0] = n0;
+      mrun[1] = n1;
+      lrun[0] *= a0;
+      lrun[1] *= a1;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        o[m][0] *= a0;
+        o[m][1] *= a1;
+        o[m][2] *= a0;
+        o[m][3] *= a1;
+      }
+    }
+    if (vs > vref) {  // O is in units of vref
+      const float f = __fdiv_rn(vref, vs);
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[m][x] *= f;
+      vref = vs;
+    }
+    const float wv = vref > 0.f ? __fdiv_rn(vs, vref) * P_SCALE : 0.f;
+    const float m0 = mrun[0] == -INFINITY ? 0.f : mrun[0], m1 = mrun[1] == -INFINITY ? 0.f : mrun[1];
+    const float p0 = exp2f(c[0] - m0), p1 = exp2f(c[1] - m1), p2 = exp2f(c[2] - m0), p3 = exp2f(c[3] - m1);
+    lrun[0] += p0 + p2;
+    lrun[1] += p1 + p3;
+    const float w0 = p0 * wv, w1 = p1 * wv, w2 = p2 * wv, w3 = p3 * wv;
+    const uint32_t u0 = pack_f16x2(w0, w1), u1 = pack_f16x2(w2, w3);
+    const uint32_t ph0 = movmatrix_trans(u0), ph1 = movmatrix_trans(u1);
+    uint32_t pl0 = 0, pl1 = 0;
+    if (HL) {
+      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u0));
+      const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u1));
+      pl0 = movmatrix_trans(pack_f16x2(w0 - a.x, w1 - a.y));
+      pl1 = movmatrix_trans(pack_f16x2(w2 - b.x, w3 - b.y));
+    }
+#pragma unroll
+    for (int w = 0; w < HD / 32; ++w) {  // four head dimensions of the lane: two M tiles
+      const uint32_t x0 = w == 0 ? vb[0].x : w == 1 ? vb[0].y : w == 2 ? vb[0].z : vb[0].w;
+      const uint32_t x1 = w == 0 ? vb[1].x : w == 1 ? vb[1].y : w == 2 ? vb[1].z : vb[1].w;
+      const uint32_t x2 = w == 0 ? vb[2].x : w == 1 ? vb[2].y : w == 2 ? vb[2].z : vb[2].w;
+      const uint32_t x3 = w == 0 ? vb[3].x : w == 1 ? vb[3].y : w == 2 ? vb[3].z : vb[3].w;
+      uint32_t a[4], b[4];  // tiles 2 w and 2 w + 1
+      codes_f16<CT>(__byte_perm(x0, x1, 0x5140), a[0], a[1]);
+      codes_f16<CT>(__byte_perm(x2, x3, 0x5140), a[2], a[3]);
+      codes_f16<CT>(__byte_perm(x0, x1, 0x7362), b[0], b[1]);
+      codes_f16<CT>(__byte_perm(x2, x3, 0x7362), b[2], b[3]);
+      mma_f16(o[2 * w], a[0], a[1], a[2], a[3], ph0, ph1);
+      mma_f16(o[2 * w + 1], b[0], b[1], b[2], b[3], ph0, ph1);
+      if (HL) {
+        mma_f16(o[2 * w], a[0], a[1], a[2], a[3], pl0, pl1);
+        mma_f16(o[2 * w + 1], b[0], b[1], b[2], b[3], pl0, pl1);
+      }
+    }
+    if (more) load_v(fnext);
+  }
+
+  // the warp's record: lane (g, t) holds head dimensions hd/8 g + ... of queries 2t, 2t + 1
+#pragma unroll
+  for (int x = 4; x < 32; x <<= 1) {
+    lrun[0] += __shfl_xor_sync(FULL, lrun[0], x);
+    lrun[1] += __shfl_xor_sync(FULL, lrun[1], x);
+  }
+  const float back = vref * (1.f / P_SCALE);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    float* row = &so[warp][2 * t + c][g * (HD / 8)];
+#pragma unroll
+    for (int m = 0; m < MT; m += 2)
+      *reinterpret_cast<float4*>(row + 2 * m) =
+          make_float4(o[m][c] * back, o[m][2 + c] * back, o[m + 1][c] * back, o[m + 1][2 + c] * back);
+    if (g == 0) {
+      sml[warp][2 * t + c][0] = mrun[c];
+      sml[warp][2 * t + c][1] = lrun[c];
+    }
+  }
+  __syncthreads();
+  // the tile's warps joined (in warp order): thread = (tile, query, 4 head dimensions)
+  constexpr int DQ = HD / 4;
+  for (int x = threadIdx.x; x < A.nq * 8 * DQ; x += ATT_WARPS * 32) {
+    const int d = x % DQ, qq = (x / DQ) & 7, tl = x / (8 * DQ);
+    const int qi = (qc * A.nq + tl) * 8 + qq;
+    if (qi >= nqueries) continue;
+    float m = -INFINITY;
+    for (int w = 0; w < groups; ++w) m = fmaxf(m, sml[tl + w * A.nq][qq][0]);
+    const float mref = m == -INFINITY ? 0.f : m;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    for (int w = 0; w < groups; ++w) {
+      const int wp = tl + w * A.nq;
+      const float f = exp2f(sml[wp][qq][0] - mref);
+      const float4 v = *reinterpret_cast<const float4*>(&so[wp][qq][4 * d]);
+      l = fmaf(f, sml[wp][qq][1], l);
+      acc.x = fmaf(f, v.x, acc.x);
+      acc.y = fmaf(f, v.y, acc.y);
+      acc.z = fmaf(f, v.z, acc.z);
+      acc.w = fmaf(f, v.w, acc.w);
+    }
+    const int row = qi / A.GH, head = h * A.GH + qi % A.GH;
+    const int64_t rh = (int64_t)(rq.row0 + row) * A.Hq + head;
+    if (A.nsplit == 1) {
+      const float inv = l != 0.f ? 1.f / l : 0.f;  // (NaN stays NaN)
+      store_elem4<DT>(A.out, (int64_t)(rq.row0 + row) * A.out_stride + (int64_t)head * HD + 4 * d,
+                      make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+      if (d == 0 && A.lse) A.lse[rh] = (m + log2f(l)) * LN2;
+    } else {
+      *reinterpret_cast<float4*>(A.rec_o + (rh * A.nsplit + split) * HD + 4 * d) = acc;
+      if (d == 0) *reinterpret_cast<float2*>(A.rec_ml + (rh * A.nsplit + split) * 2) = make_float2(m, l);
+    }
+  }
+}
+
+// Joins the chunks' records of a (row, head) in chunk order; one warp each.
+template <int DT, int HD>
+__global__ void __launch_bounds__(256) kv8_join_kernel(const __grid_constant__ AttArgs A) {
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int per_req = A.max_rows * A.Hq;
+  const int64_t gw = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int r = (int)(gw / per_req), x = (int)(gw % per_req);
+  if (r >= A.R) return;
+  const Req rq = load_req(A, r);
+  const int row = x / A.Hq, head = x % A.Hq;
+  if (row >= rq.n) return;
+  int ns = (rq.b1 - rq.b0 + A.chunk - 1) / A.chunk;
+  ns = ns < 1 ? 1 : ns > A.nsplit ? A.nsplit : ns;
+  const int64_t rh = (int64_t)(rq.row0 + row) * A.Hq + head;
+  const float2* ml = reinterpret_cast<const float2*>(A.rec_ml + rh * A.nsplit * 2);
+  float m = -INFINITY;
+  for (int s = lane; s < ns; s += 32) m = fmaxf(m, __ldcg(ml + s).x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
+  const float mref = m == -INFINITY ? 0.f : m;
+  constexpr int W = HD / 32;
+  float acc[W], l = 0.f;
+#pragma unroll
+  for (int w = 0; w < W; ++w) acc[w] = 0.f;
+  const float* ro = A.rec_o + rh * A.nsplit * HD + lane * W;
+  for (int s0 = 0; s0 < ns; s0 += 32) {
+    const int cnt = ns - s0 < 32 ? ns - s0 : 32;
+    float2 mine = lane < cnt ? __ldcg(ml + s0 + lane) : make_float2(-INFINITY, 0.f);
+    const float fl = exp2f(mine.x - mref);
+#pragma unroll 4
+    for (int s = 0; s < cnt; ++s) {
+      const float f = __shfl_sync(FULL, fl, s), ls = __shfl_sync(FULL, mine.y, s);
+      l = fmaf(f, ls, l);
+      if (W == 4) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(ro + (int64_t)(s0 + s) * HD));
+        acc[0] = fmaf(f, v.x, acc[0]);
+        acc[1] = fmaf(f, v.y, acc[1]);
+        acc[W - 2] = fmaf(f, v.z, acc[W - 2]);
+        acc[W - 1] = fmaf(f, v.w, acc[W - 1]);
+      } else {
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(ro + (int64_t)(s0 + s) * HD));
+        acc[0] = fmaf(f, v.x, acc[0]);
+        acc[1] = fmaf(f, v.y, acc[1]);
+      }
+    }
+  }
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  const int64_t at = (int64_t)(rq.row0 + row) * A.out_stride + (int64_t)head * HD + lane * W;
+  if (W == 4) {
+    store_elem4<DT>(A.out, at, make_float4(acc[0] * inv, acc[1] * inv, acc[W - 2] * inv, acc[W - 1] * inv));
+  } else if (DT == DDL_T_F32) {
+    *reinterpret_cast<float2*>(reinterpret_cast<float*>(A.out) + at) = make_float2(acc[0] * inv, acc[1] * inv);
+  } else {
+    *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(A.out) + at) =
+        DT == DDL_T_BF16 ? pack_bf16x2(acc[0] * inv, acc[1] * inv) : pack_f16x2(acc[0] * inv, acc[1] * inv);
+  }
+  if (lane == 0 && A.lse) A.lse[rh] = (m + log2f(l)) * LN2;
+}
+
+// ------------------------------------------------------------------ host
+int g_att_sms[64];
+std::mutex g_att_mu;
+
+int att_sms(int& sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_status(e);
+  if (dev < 0 || dev >= 64) return DDL_ERR_UNSUPPORTED;
+  std::lock_guard<std::mutex> lk(g_att_mu);
+  if (!g_att_sms[dev]) {
+    int n = 0;
+    if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return cuda_status(e);
+    g_att_sms[dev] = n;
+  }
+  sms = g_att_sms[dev];
+  return DDL_OK;
+}
+
+struct AttPlan {
+  int32_t nq, nqc, nsplit, chunk;
+  int64_t rec_ml, total;  // workspace offsets
+};
+
+int check_sizes(int32_t H_q, int32_t H_kv, int32_t hd, int32_t R, int32_t T, int32_t max_rows, int32_t max_len) {
+  if (hd != 64 && hd != 128) return DDL_ERR_SHAPE;
+  if (H_kv < 1 || H_kv > DDL_KV8_MAX_HEADS || H_q < H_kv || H_q % H_kv || H_q / H_kv > DDL_MAX_GROUP_HEADS)
+    return DDL_ERR_SHAPE;
+  if (R < 1 || T < 1 || max_rows < 1 || max_len < 1) return DDL_ERR_ARG;
+  if (R > DDL_KV8_MAX_REQS || max_rows > DDL_KV8_MAX_ROWS) return DDL_ERR_UNSUPPORTED;
+  return DDL_OK;
+}
+
+// The launch: query tiles per CTA, and chunks of the key axis.  One (request,
+// K/V head) is split until the grid holds every SM's two CTAs once, in chunks of at
+// least one block per warp; long axes of a full grid are cut into chunks of at
+// most 1024 tokens all the same, so that ragged lengths spread evenly.
+int att_plan(int32_t H_q, int32_t H_kv, int32_t hd, int32_t R, int32_t T, int32_t max_rows, int32_t max_len,
+             int32_t window, AttPlan& p) {
+  int sms = 0;
+  const int st = att_sms(sms);
+  if (st) return st;
+  const int tiles = (max_rows * (H_q / H_kv) + 7) / 8;
+  p.nq = 1;
+  while (p.nq < ATT_WARPS && p.nq < tiles) p.nq *= 2;
+  p.nqc = (tiles + p.nq - 1) / p.nq;
+  int64_t keys = max_len;
+  if (window > 0 && (int64_t)window + max_rows + 15 < keys) keys = (int64_t)window + max_rows + 15;
+  const int64_t blocks = (keys + 15) / 16;
+  const int64_t units = (int64_t)R * H_kv * p.nqc, groups = ATT_WARPS / p.nq;
+  int64_t want = 2 * sms / units;
+  if (want < 1) want = 1;
+  int64_t chunk = (blocks + want - 1) / want;
+  chunk = (chunk + groups - 1) / groups * groups;
+  if (chunk > 64) chunk = 64;
+  if (chunk < groups) chunk = groups;
+  p.chunk = (int32_t)chunk;
+  p.nsplit = (int32_t)((blocks + chunk - 1) / chunk);
+  if (units * p.nsplit > 0x7fffffffLL) return DDL_ERR_UNSUPPORTED;
+  const int64_t rows = (int64_t)T * H_q;
+  p.rec_ml = p.nsplit > 1 ? align256(rows * p.nsplit * hd * 4) : 0;
+  p.total = p.nsplit > 1 ? align256(p.rec_ml + rows * p.nsplit * 2 * 4) : 256;
+  return DDL_OK;
+}
+
+template <int CT, int DT, int HD>
+const void* att_fn(bool ex) {
+  return ex ? (const void*)kv8_attention_kernel<CT, DT, HD, true> : (const void*)kv8_attention_kernel<CT, DT, HD, false>;
+}
+template <int CT, int DT>
+const void* att_fn(int hd, bool ex) {
+  return hd == 128 ? att_fn<CT, DT, 128>(ex) : att_fn<CT, DT, 64>(ex);
+}
+template <int CT>
+const void* att_fn(int dt, int hd, bool ex) {
+  return dt == DDL_T_F32 ? att_fn<CT, DDL_T_F32>(hd, ex) : dt == DDL_T_BF16 ? att_fn<CT, DDL_T_BF16>(hd, ex)
+                                                                           : att_fn<CT, DDL_T_F16>(hd, ex);
+}
+template <int DT>
+const void* join_fn(int hd) {
+  return hd == 128 ? (const void*)kv8_join_kernel<DT, 128> : (const void*)kv8_join_kernel<DT, 64>;
+}
+
+}  // namespace
+}  // namespace ddl
+
+using namespace ddl;
+
+extern "C" size_t ddl_kv8_attention_workspace_bytes(int32_t H_q, int32_t H_kv, int32_t head_dim, int32_t R, int32_t T,
+                                                    int32_t max_rows, int32_t max_len) {
+  if (check_sizes(H_q, H_kv, head_dim, R, T, max_rows, max_len)) return 0;
+  AttPlan p;
+  if (att_plan(H_q, H_kv, head_dim, R, T, max_rows, max_len, 0, p)) return 0;
+  return (size_t)p.total;
+}
+
+extern "C" int ddl_kv8_attention(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, int32_t head_dim, ddl_dtype dtype,
+                                 const ddl_attn_opts* opts, int32_t R, int32_t T, int32_t max_rows, int32_t max_len,
+                                 const int32_t* q_off, const int32_t* kv_len, const int32_t* page_table,
+                                 int32_t pages_per_seq, const void* q, int64_t q_stride, void* out,
+                                 int64_t out_stride, float* lse, int32_t* bad_out, void* workspace, size_t ws_bytes,
+                                 void* stream) {
+  int st = check_kv8(kv, H_kv, head_dim);
+  if (st) return st;
+  if ((st = check_sizes(H_q, H_kv, head_dim, R, T, max_rows, max_len))) return st;
+  if (!opts || !kv_len || !page_table || !q || !out) return DDL_ERR_ARG;
+  if (!workspace) return DDL_ERR_WORKSPACE;
+  if (!dtype_bytes(dtype)) return DDL_ERR_UNSUPPORTED;
+  if (pages_per_seq < 1 || out == q) return DDL_ERR_ARG;
+  if (!q_off && (max_rows != 1 || T < R)) return DDL_ERR_ARG;
+  if ((int64_t)pages_per_seq * kv->page_size > 0x7fffffffLL) return DDL_ERR_UNSUPPORTED;
+  if (!(fabsf(opts->scale) < INFINITY) || !(opts->softcap >= 0.f && opts->softcap < INFINITY) || opts->window < 0)
+    return DDL_ERR_ARG;
+  const int64_t w = (int64_t)H_q * head_dim;
+  if (q_stride < w || out_stride < w || q_stride % 8 || out_stride % 8) return DDL_ERR_ARG;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return DDL_ERR_ALIGN;
+  for (const void* p : {(const void*)q_off, (const void*)kv_len, (const void*)page_table, (const void*)lse,
+                        (const void*)bad_out, (const void*)opts->slopes})
+    if ((uintptr_t)p & 3u) return DDL_ERR_ALIGN;
+  AttPlan pl, full;
+  if ((st = att_plan(H_q, H_kv, head_dim, R, T, max_rows, max_len, 0, full))) return st;
+  if ((st = att_plan(H_q, H_kv, head_dim, R, T, max_rows, max_len, opts->window, pl))) return st;
+  if (ws_bytes < (size_t)full.total) return DDL_ERR_WORKSPACE;
+  if (pl.total > full.total) pl = full;  // (a window needs no more records than the whole axis)
+  AttArgs a;
+  a.k = kv->k;
+  a.v = kv->v;
+  a.ks = kv->k_scale;
+  a.vs = kv->v_scale;
+  a.q_off = q_off;
+  a.kv_len = kv_len;
+  a.table = page_table;
+  a.q = q;
+  a.out = out;
+  a.lse = lse;
+  a.bad = bad_out;
+  a.rec_o = (float*)workspace;
+  a.rec_ml = (float*)((uint8_t*)workspace + pl.rec_ml);
+  a.slopes = opts->slopes;
+  a.pages = kv->pages;
+  a.q_stride = q_stride;
+  a.out_stride = out_stride;
+  a.scale = opts->scale;
+  a.softcap = opts->softcap;
+  a.window = opts->window;
+  a.R = R;
+  a.T = T;
+  a.Hq = H_q;
+  a.Hkv = H_kv;
+  a.GH = H_q / H_kv;
+  a.hd = head_dim;
+  a.pshift = log2_of(kv->page_size);
+  a.per = pages_per_seq;
+  a.max_rows = max_rows;
+  a.max_len = max_len;
+  a.nsplit = pl.nsplit;
+  a.chunk = pl.chunk;
+  a.nq = pl.nq;
+  a.nqc = pl.nqc;
+  const bool ex = opts->softcap > 0.f || opts->slopes;
+  const void* fn = kv->type == DDL_KV8_E4M3 ? att_fn<DDL_KV8_E4M3>(dtype, head_dim, ex)
+                                            : att_fn<DDL_KV8_INT8>(dtype, head_dim, ex);
+  void* args[] = {&a};
+  const int64_t ctas = (int64_t)R * H_kv * pl.nqc * pl.nsplit;
+  st = cuda_status(launch_pdl(fn, dim3((unsigned)ctas), dim3(ATT_WARPS * 32), args, 0, (cudaStream_t)stream));
+  if (st || pl.nsplit == 1) return st;
+  const int64_t warps = (int64_t)R * max_rows * H_q;
+  fn = dtype == DDL_T_F32 ? join_fn<DDL_T_F32>(head_dim) : dtype == DDL_T_BF16 ? join_fn<DDL_T_BF16>(head_dim)
+                                                                              : join_fn<DDL_T_F16>(head_dim);
+  return cuda_status(
+      launch_pdl(fn, dim3((unsigned)((warps + 7) / 8)), dim3(256), args, 0, (cudaStream_t)stream));
+}

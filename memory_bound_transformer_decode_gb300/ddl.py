@@ -27,7 +27,8 @@ EXPORTED = ("ddl_quantize_int4", "ddl_packed_layer_bytes", "ddl_pack_layer", "dd
             "ddl_test_hold_barrier", "ddl_set_trace", "ddl_read_device_status", "ddl_status_string",
             "ddl_last_cuda_error", "ddl_embed", "ddl_packed_head_bytes", "ddl_pack_head",
             "ddl_head_workspace_bytes", "ddl_lm_head", "ddl_stack_decode_ragged",
-            "ddl_stack_prefill", "ddl_stack_decode_paged", "ddl_stack_prefill_paged")
+            "ddl_stack_prefill", "ddl_stack_decode_paged", "ddl_stack_prefill_paged",
+            "ddl_page_plan", "ddl_kv8_append", "ddl_kv8_attention_workspace_bytes", "ddl_kv8_attention")
 
 
 class DDLError(RuntimeError):
@@ -65,6 +66,17 @@ class KV(ctypes.Structure):
 
 class KVPages(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("pages", ctypes.c_int64)]
+
+
+class KV8(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("type", ctypes.c_int32)]
+
+
+class AttnOpts(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("slopes", ctypes.c_void_p)]
 
 
 class WsView(ctypes.Structure):
@@ -132,6 +144,12 @@ def load(build_if_missing: bool = False):
         lib.ddl_head_workspace_bytes.restype = sz
         lib.ddl_lm_head.argtypes = [i32, i64, ctypes.c_int, vp, vp, ctypes.c_float, i32, vp, i32,
                                     ctypes.c_float, vp, vp, vp, vp, vp, sz, vp]
+        lib.ddl_page_plan.argtypes = [vp, vp, i32, i32, vp, i32, vp, i32, vp, vp, vp, vp, i32, vp, vp, vp]
+        lib.ddl_kv8_append.argtypes = [P(KV8), i32, i32, ctypes.c_int, vp, i64, vp, i64, vp, i32, vp, vp]
+        lib.ddl_kv8_attention_workspace_bytes.argtypes = [i32] * 7
+        lib.ddl_kv8_attention_workspace_bytes.restype = sz
+        lib.ddl_kv8_attention.argtypes = [P(KV8), i32, i32, i32, ctypes.c_int, P(AttnOpts), i32, i32, i32, i32, vp,
+                                          vp, vp, i32, vp, i64, vp, i64, vp, vp, vp, sz, vp]
         for name in EXPORTED:
             if not hasattr(lib, name):
                 raise RuntimeError(f"{path} does not export {name}")
@@ -415,6 +433,157 @@ def ws_tensor(workspace: torch.Tensor, offset: int, n: int) -> torch.Tensor:
     """fp32 view of n floats at byte offset `offset` of a workspace tensor."""
     assert offset % 4 == 0
     return workspace.view(torch.uint8)[offset: offset + 4 * n].view(torch.float32)
+
+
+# ------------------------------------------------------------------ 8-bit KV cache
+
+T_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+KV8_TYPES = {torch.float8_e4m3fn: 0, torch.int8: 1}
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _i32(name: str, t, dev, n: int | None = None):
+    """Checks a contiguous int32 tensor (of n entries) on device `dev`."""
+    _need(t.dtype is torch.int32 and t.device == dev and t.is_contiguous() and (n is None or t.numel() == n),
+          f"{name}: a contiguous int32 tensor{'' if n is None else f' of {n} entries'} on {dev}")
+
+
+def _run_on(dev, name: str, fn, stream, *args):
+    """Calls fn(*args, stream) with `dev` as the current device, on `stream` or
+    that device's current stream."""
+    if dev.type != "cuda":
+        raise ValueError(f"{name}: tensors on a CUDA device")
+    s = stream.cuda_stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, s)
+    if st != 0:
+        raise DDLError(name, st, _lib)
+
+
+def _kv8(pool) -> tuple:
+    """(KV8, H_kv, head_dim) of a pool (k, v, k_scale, v_scale): codes
+    [pages, H_kv, page_size, hd] float8_e4m3fn or int8, scales fp32
+    [pages, H_kv, page_size / 16]."""
+    k, v, ks, vs = pool
+    _need(k.dim() == 4 and k.dtype in KV8_TYPES and v.dtype is k.dtype and v.shape == k.shape,
+          "pool: k and v [pages, H_kv, page_size, head_dim] of one 8-bit type")
+    pages, H, P, hd = k.shape
+    _need(ks.dtype is torch.float32 and vs.dtype is torch.float32 and ks.shape == vs.shape
+          and tuple(ks.shape) == (pages, H, P // 16), "pool: scales fp32 [pages, H_kv, page_size / 16]")
+    _need(k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous(),
+          "pool: contiguous tensors")
+    _need(v.device == k.device and ks.device == k.device and vs.device == k.device, "pool: tensors of one device")
+    return KV8(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, P, KV8_TYPES[k.dtype]), H, hd
+
+
+def _rows(name: str, x, dev, heads: int, hd: int):
+    """Checks rows [T, heads, hd] whose heads are contiguous; returns their stride."""
+    _need(x.dim() == 3 and x.shape[1] == heads and x.shape[2] == hd and x.dtype in T_DTYPES and x.device == dev,
+          f"{name}: [T, {heads}, {hd}] fp32, bf16 or fp16 on {dev}")
+    T = x.shape[0]
+    st = x.stride()
+    _need((st[2] == 1) and (heads == 1 or st[1] == hd), f"{name}: a row's heads are contiguous")
+    return st[0] if T > 1 else heads * hd
+
+
+def ddl_page_plan(old_len: torch.Tensor, add_len: torch.Tensor, free_pages: torch.Tensor, page_table: torch.Tensor,
+                  page_size: int, *, row_off: torch.Tensor, kv_len: torch.Tensor, row_pos: torch.Tensor,
+                  slot: torch.Tensor, used: torch.Tensor, status: torch.Tensor, stream=None):
+    """Page tables and slot maps of one step, from the requests' lengths (all
+    int32 device tensors): request r holds old_len[r] tokens and brings
+    add_len[r] rows.  Writes new pages from free_pages into page_table [R,
+    pages_per_seq], and row_off [R + 1], kv_len [R], row_pos and slot [T],
+    used [1], status [R]."""
+    lib = load()
+    dev, R, T = page_table.device, old_len.numel(), slot.numel()
+    _need(page_table.dim() == 2 and page_table.shape[0] == R, "page_table: [R, pages_per_seq]")
+    for name, t, n in (("old_len", old_len, R), ("add_len", add_len, R), ("free_pages", free_pages, None),
+                       ("page_table", page_table, None), ("row_off", row_off, R + 1), ("kv_len", kv_len, R),
+                       ("row_pos", row_pos, T), ("slot", slot, T), ("used", used, 1), ("status", status, R)):
+        _i32(name, t, dev, n)
+    _run_on(dev, "ddl_page_plan", lib.ddl_page_plan, stream, old_len.data_ptr(), add_len.data_ptr(), R,
+            int(page_size), free_pages.data_ptr(), free_pages.numel(), page_table.data_ptr(), page_table.shape[1],
+            row_off.data_ptr(), kv_len.data_ptr(), row_pos.data_ptr(), slot.data_ptr(), T, used.data_ptr(),
+            status.data_ptr())
+
+
+def ddl_kv8_append(pool, k_new: torch.Tensor, v_new: torch.Tensor, slot: torch.Tensor,
+                   bad: torch.Tensor | None = None, stream=None):
+    """Quantize the rows k_new, v_new [T, H_kv, hd] into an 8-bit pool (k, v,
+    k_scale, v_scale) at the slot indices slot [T] (int32; negative: skipped).
+    bad: optional int32 [1] device flag set to 1 by a slot past the pool."""
+    lib = load()
+    kv, H, hd = _kv8(pool)
+    dev, T = pool[0].device, slot.numel()
+    ks, vs = _rows("k_new", k_new, dev, H, hd), _rows("v_new", v_new, dev, H, hd)
+    _need(k_new.dtype is v_new.dtype and k_new.shape[0] == T and v_new.shape[0] == T,
+          "k_new, v_new: one type, a row for each slot")
+    _i32("slot", slot, dev)
+    if bad is not None:
+        _i32("bad", bad, dev, 1)
+    _run_on(dev, "ddl_kv8_append", lib.ddl_kv8_append, stream, kv, H, hd, T_DTYPES[k_new.dtype], k_new.data_ptr(), ks,
+            v_new.data_ptr(), vs, slot.data_ptr(), T, None if bad is None else bad.data_ptr())
+
+
+def ddl_kv8_attention_workspace_bytes(H_q: int, H_kv: int, hd: int, R: int, T: int, max_rows: int,
+                                      max_len: int) -> int:
+    n = int(load().ddl_kv8_attention_workspace_bytes(H_q, H_kv, hd, R, T, max_rows, max_len))
+    if n == 0:
+        raise DDLError("ddl_kv8_attention_workspace_bytes", 1, _lib)
+    return n
+
+
+def ddl_kv8_attention(pool, q: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor, max_len: int, *,
+                      q_off: torch.Tensor | None = None, max_rows: int = 1, scale: float | None = None,
+                      softcap: float = 0.0, window: int = 0, slopes: torch.Tensor | None = None,
+                      out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None, bad: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """Attention of the rows q [T, H_q, hd] over an 8-bit pool: request r's
+    rows (q_off[r] .. q_off[r + 1], or row r alone) are the newest of its
+    kv_len[r] tokens, whose pages page_table [R, pages_per_seq] names.
+    max_len bounds kv_len, max_rows the rows of a request.  scale: 1 / sqrt(hd)
+    by default; softcap, window, slopes as in ddl.h.  Returns out (zeros where
+    a new one is made and a row belongs to no request)."""
+    lib = load()
+    kv, H, hd = _kv8(pool)
+    dev = pool[0].device
+    _need(q.dim() == 3, "q: [T, H_q, hd]")
+    T, H_q, R = q.shape[0], q.shape[1], kv_len.numel()
+    qs = _rows("q", q, dev, H_q, hd)
+    if out is None:
+        out = torch.zeros((T, H_q, hd), dtype=q.dtype, device=dev)
+    os_ = _rows("out", out, dev, H_q, hd)
+    _need(out.dtype is q.dtype and out.shape[0] == T, "out: as q")
+    _i32("kv_len", kv_len, dev)
+    _i32("page_table", page_table, dev)
+    _need(page_table.dim() == 2 and page_table.shape[0] == R, "page_table: [R, pages_per_seq]")
+    if q_off is not None:
+        _i32("q_off", q_off, dev, R + 1)
+    if bad is not None:
+        _i32("bad", bad, dev, 1)
+    for name, t, n in (("slopes", slopes, H_q), ("lse", lse, T * H_q)):
+        _need(t is None or (t.dtype is torch.float32 and t.device == dev and t.is_contiguous() and t.numel() == n),
+              f"{name}: fp32, {n} entries, on {dev}")
+    if workspace is None:
+        workspace = torch.empty(ddl_kv8_attention_workspace_bytes(H_q, H, hd, R, T, max_rows, max_len),
+                                dtype=torch.uint8, device=dev)
+    _need(workspace.device == dev and workspace.is_contiguous(), f"workspace: contiguous, on {dev}")
+    opts = AttnOpts(hd ** -0.5 if scale is None else float(scale), float(softcap), int(window),
+                    None if slopes is None else slopes.data_ptr())
+    _run_on(dev, "ddl_kv8_attention", lib.ddl_kv8_attention, stream, kv, H_q, H, hd, T_DTYPES[q.dtype], opts, R, T,
+            int(max_rows), int(max_len), None if q_off is None else q_off.data_ptr(), kv_len.data_ptr(),
+            page_table.data_ptr(), page_table.shape[1], q.data_ptr(), qs, out.data_ptr(), os_,
+            None if lse is None else lse.data_ptr(), None if bad is None else bad.data_ptr(), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
+    return out
 
 
 # ------------------------------------------------------------------ token step
