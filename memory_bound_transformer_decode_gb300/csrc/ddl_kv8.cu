@@ -474,7 +474,7 @@ extern "C" int ddl_page_plan(const int32_t* old_len, const int32_t* add_len, int
   PlanArgs a = {old_len, add_len, free_pages, page_table, row_off, kv_len, row_pos, slot, used, status,
                 R, log2_of(page_size), n_free, pages_per_seq, T};
   const int nt = R <= 128 && T <= 1024 ? 128 : 512;
-  int64_t ctas = ((int64_t)T + 4 * nt - 1) / (4 * nt);  // (a new page has a row, so there are at most T of them)
+  int64_t ctas = ((int64_t)T + nt - 1) / nt;  // (a new page has a row, so there are at most T of them)
   ctas = ctas < 1 ? 1 : ctas > 152 ? 152 : ctas;
   void* args[] = {&a};
   const size_t smem = (size_t)(2 * (R + 1)) * 4;

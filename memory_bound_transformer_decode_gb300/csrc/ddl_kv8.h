@@ -40,6 +40,19 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint16_t w) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(w));
   return r;
 }
+// Four e4m3 codes as two fp16 pairs.
+__device__ __forceinline__ void e4m3x4_f16x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+// 2^x with results below 2^-126 flushed to zero.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // Two fp32 values as e4m3 codes, round to nearest even, saturating at 448
 // (NaN stays NaN); `lo` in the low byte.
 __device__ __forceinline__ uint32_t f32x2_e4m3x2(float lo, float hi) {

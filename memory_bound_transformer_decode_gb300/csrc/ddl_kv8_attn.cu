@@ -9,9 +9,9 @@
 // being the heads of one K/V head's group times the request's rows:
 //  - S^T = K Q^T on m16n8k16 MMAs with the 16 tokens as M.  The order of the
 //    head dimensions inside the contraction is free as long as K and Q agree,
-//    so lane (g, t) takes hd/4 *neighbouring* bytes of token rows g and g + 8:
-//    the codes go from global memory straight into registers, 16 bytes a load,
-//    and each 4 of them become the lane's part of one k-step of A.
+//    so lane (g, t) takes bytes 16t .. 16t + 15 of each 64 of token rows g and
+//    g + 8: the codes go from global memory straight into registers, 16 bytes a
+//    load, and each 4 of them become the lane's part of one k-step of A.
 //  - O^T += V^T P^T with the head dimensions as M.  Lane (g, t) takes the
 //    hd/8 neighbouring bytes at hd/8 g of tokens 2t, 2t+1, 2t+8, 2t+9; byte
 //    permutes pair the tokens and conversion gives A.  P^T comes from the S^T
@@ -24,10 +24,16 @@
 // is likewise one fp16 (16-bit outputs: its 2^-12 is below their own rounding)
 // or two.  Scores, m, l and O are fp32.
 //
-// Work: a CTA of 8 warps takes one chunk of tokens of one (request, K/V head)
-// and up to 8 tiles of 8 queries; with fewer tiles the warps share out the
-// chunk's blocks.  Chunks of one request are joined by a second kernel from
-// fp32 records (max, sum, O) in the workspace, in chunk order.
+// Work.  A *unit* is the blocks of one request for one K/V head and up to 8
+// tiles of 8 queries; a CTA of 8 warps gives each tile 8 / tiles warps, which
+// take the unit's blocks in turn and join their results in shared memory.
+// Short axes (at most WHOLE_BLOCKS blocks) take one CTA a unit and one launch.
+// Else the blocks of all units, laid end to end (request, head, tiles), are cut
+// into equal contiguous shares, one per CTA, two CTAs per SM: ragged lengths
+// and any number of requests fill the machine evenly, and a CTA pays for the
+// start and the end of a unit only two or three times.  A unit that lies in one
+// share is written at once; the others leave a record (max, sum, O in fp32)
+// per share, joined in share order by a second kernel.
 #include <cuda_bf16.h>
 
 #include <mutex>
@@ -54,15 +60,24 @@ struct AttArgs {
   void* out;
   float* lse;
   int32_t* bad;
-  float *rec_o, *rec_ml;  // [T * H_q][nsplit][hd], [..][2]
+  float *rec_o, *rec_ml;  // records [share + unit][query of the unit][hd], [..][2]
+  int64_t* prefix;        // [R + 1] blocks of all units before each request
   const float* slopes;
   int64_t pages, q_stride, out_stride;
   float scale, softcap;
   int32_t window;
   int32_t R, T, Hq, Hkv, GH, hd, pshift, per, max_rows, max_len;
-  int32_t nsplit, chunk;  // chunk: blocks of 16 tokens a CTA takes
-  int32_t nq, nqc;        // query tiles of 8 a CTA takes (a power of two <= 8), CTAs over the query tiles
+  int32_t whole;    // one CTA a unit, else shares
+  int32_t ctas;     // shares at most
+  int32_t nq, nqc;  // query tiles of 8 a unit has (a power of two <= 8), units over a request's query tiles
 };
+
+// Shares (range_lo and owner_of of the W blocks in n parts): at least MIN_SHARE blocks each.
+constexpr int MIN_SHARE = 16;
+__device__ __forceinline__ int64_t share_count(int64_t W, int ctas) {
+  const int64_t most = (W + MIN_SHARE - 1) / MIN_SHARE;
+  return most < 1 ? 1 : most < ctas ? most : ctas;
+}
 
 // A request's rows and keys as the kernels compute them (clamped to what the
 // launch and the tables allow).
@@ -115,18 +130,25 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
   return d;
 }
 
-// 16 bytes of codes, read once by this warp (or again soon by the warps of
-// the same CTA that hold other queries).
+// 16 (8) bytes of codes, read once by this warp (or again soon by the warps of
+// the same CTA that hold other queries).  Volatile: they are issued where they
+// stand, a block ahead of their use, and not moved down to it.
 __device__ __forceinline__ uint4 ld_codes16(const uint8_t* p) {
-  return __ldg(reinterpret_cast<const uint4*>(p));
+  uint4 v;
+  asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ld_codes8(const uint8_t* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
 }
 
 // Bytes lo16 / hi16 of w (two codes) as fp16 pairs.
 template <int CT>
 __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if (CT == DDL_KV8_E4M3) {
-    lo = e4m3x2_f16x2((uint16_t)(w & 0xffffu));
-    hi = e4m3x2_f16x2((uint16_t)(w >> 16));
+    e4m3x4_f16x2(w, lo, hi);
   } else {  // 1024 + (c + 128) - 1152 = c, exact in fp16
     const uint32_t u = w ^ 0x80808080u;
     const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
@@ -177,48 +199,79 @@ __device__ __forceinline__ void store_elem4(void* p, int64_t i, float4 v) {
 // 2^-24, which times the cap is the score's own fp32 rounding.
 __device__ __forceinline__ float cap_tanh(float x) { return 1.f - __fdividef(2.f, __expf(2.f * x) + 1.f); }
 
+// Units of request q: K/V heads times groups of query tiles.
+__device__ __forceinline__ int unit_groups(const AttArgs& A, const Req& q) {
+  return (q.n * A.GH + 8 * A.nq - 1) / (8 * A.nq);
+}
+
 template <int CT, int DT, int HD, bool EX>
-__global__ void __launch_bounds__(ATT_WARPS * 32, 2) kv8_attention_kernel(const __grid_constant__ AttArgs A) {
-  constexpr int KS = HD / 16;        // k-steps of the score MMAs
-  constexpr int NV = HD / 64;        // 16-byte loads of a K row per lane
-  constexpr int MT = HD / 16;        // M tiles of the output MMAs
-  constexpr bool HL = DT == DDL_T_F32;
-  constexpr int OROW = HD + 4;
-  __shared__ float so[ATT_WARPS][8][OROW];
-  __shared__ float sml[ATT_WARPS][8][2];
-  pdl_trigger();
-  pdl_wait();
+struct Att {
+  static constexpr int KS = HD / 16;  // k-steps of the score MMAs
+  static constexpr int NV = HD / 64;  // 16-byte loads of a K row per lane
+  static constexpr int MT = HD / 16;  // M tiles of the output MMAs
+  static constexpr bool HL = DT == DDL_T_F32;
+  static constexpr int OROW = HD + 4;
+  struct Smem {
+    float o[ATT_WARPS][8][OROW];
+    float ml[ATT_WARPS][8][2];
+  };
+  static __device__ __forceinline__ void segment(const AttArgs& A, Smem& S, int r, const Req& rq, int h, int qc,
+                                                 int c0, int c1, bool direct, int64_t rec);
+};
+
+// Blocks [c0, c1) of the unit (request r, K/V head h, query tiles qc); the
+// result goes to the output (direct: they are all of the unit's blocks) or to
+// record `rec`.
+template <int CT, int DT, int HD, bool EX>
+__device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, Smem& S, int r, const Req& rq, int h,
+                                                             int qc, int c0, int c1, bool direct, int64_t rec) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  int bid = blockIdx.x;
-  const int split = bid % A.nsplit;
-  bid /= A.nsplit;
-  const int qc = bid % A.nqc;
-  bid /= A.nqc;
-  const int h = bid % A.Hkv, r = bid / A.Hkv;
-  const Req rq = load_req(A, r);
-  if (rq.bad && A.bad && threadIdx.x == 0) atomicOr(A.bad, 1);
   const int nqueries = rq.n * A.GH;
-  if (qc * A.nq * 8 >= nqueries) return;  // no rows in these tiles
-  const int c0 = rq.b0 + split * A.chunk;
-  const int c1 = min(rq.b1, c0 + A.chunk);
-  if (c0 >= rq.b1 && split > 0) return;  // (chunk 0 writes the rows of a request without keys)
   const int groups = ATT_WARPS / A.nq;   // warps that share a tile's blocks
   const int tile = qc * A.nq + warp % A.nq, kg = warp / A.nq;
   const bool live = tile * 8 < nqueries;
 
+  const int nb = live && c1 > c0 + kg ? (c1 - c0 - kg + groups - 1) / groups : 0;  // this warp's blocks
+  // block i of this warp: c0 + kg + i * groups; lane l holds the page row and
+  // the scales of blocks 32 w + l (this batch of 32) and the next batch's rows
+  const int bshift = A.pshift - 4, bmask = (1 << bshift) - 1;
+  auto block_row = [&](int i) -> int32_t {  // the block's index in the pool's [page][head][block] view, -1: none
+    int64_t idx = -1;
+    if (i < nb) {
+      const int b = c0 + kg + i * groups;
+      const int32_t page = A.table[(int64_t)r * A.per + (b >> bshift)];
+      if (page >= 0 && page < A.pages) return page;
+      if (A.bad) atomicOr(A.bad, 1);
+    }
+    return (int32_t)idx;
+  };
+  auto flat = [&](int32_t page, int i) -> int64_t {  // index of the block among all heads' blocks
+    const int b = c0 + kg + i * groups;
+    return (((int64_t)page * A.Hkv + h) << bshift) + (b & bmask);
+  };
+  int32_t page_l = block_row(lane), page_n = -1;
+  float ks_l = 0.f, vs_l = 0.f;
+  if (page_l >= 0) {
+    const int64_t f = flat(page_l, lane);
+    ks_l = A.ks[f];
+    vs_l = A.vs[f];
+  }
   // queries of this lane: column g of Q^T's fragments, columns 2t, 2t + 1 of the scores
-  uint32_t qh[KS][2], ql[HL ? KS : 1][2];
+  // (the remainders wait in shared memory, in the place of the warp's later record)
+  uint32_t qh[KS][2];
+  uint2* const ql = reinterpret_cast<uint2*>(&S.o[warp][0][0]) + lane;
+  static_assert(KS * 32 * sizeof(uint2) <= sizeof(S.o[0]), "remainders of Q");
   float qf = 0.f;  // 2^e of query g
   {
     const int qi = tile * 8 + g;
     const bool has = qi < nqueries;
     const int row = has ? qi / A.GH : 0, head = h * A.GH + (has ? qi % A.GH : 0);
-    const int64_t at = (int64_t)(rq.row0 + row) * A.q_stride + (int64_t)head * HD + t * (HD / 4);
+    const int64_t at = (int64_t)(rq.row0 + row) * A.q_stride + (int64_t)head * HD + t * 16;
     float4 f[KS];
     float mx = 0.f;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
-      f[s] = has ? load_elem4<DT>(A.q, at + 4 * s) : make_float4(0.f, 0.f, 0.f, 0.f);
+      f[s] = has ? load_elem4<DT>(A.q, at + 64 * (s >> 2) + 4 * (s & 3)) : make_float4(0.f, 0.f, 0.f, 0.f);
       mx = fmaxf(mx, fmaxf(fmaxf(fabsf(f[s].x), fabsf(f[s].y)), fmaxf(fabsf(f[s].z), fabsf(f[s].w))));
     }
     mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
@@ -235,8 +288,7 @@ __global__ void __launch_bounds__(ATT_WARPS * 32, 2) kv8_attention_kernel(const 
       if (HL) {
         const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&qh[s][0]));
         const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&qh[s][1]));
-        ql[HL ? s : 0][0] = pack_f16x2(v.x - a.x, v.y - a.y);
-        ql[HL ? s : 0][1] = pack_f16x2(v.z - b.x, v.w - b.y);
+        ql[s * 32] = make_uint2(pack_f16x2(v.x - a.x, v.y - a.y), pack_f16x2(v.z - b.x, v.w - b.y));
       }
     }
   }
@@ -276,40 +328,15 @@ __global__ void __launch_bounds__(ATT_WARPS * 32, 2) kv8_attention_kernel(const 
 #pragma unroll
   for (int m = 0; m < MT; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
   float mrun[2] = {-INFINITY, -INFINITY}, lrun[2] = {0.f, 0.f};
-  float vref = 0.f;  // the largest V scale so far: P carries scale / vref
+  float vref = 0.f, winv = 0.f;  // the largest V scale so far and P_SCALE / vref: P carries scale / vref
 
-  const int nb = live && c1 > c0 + kg ? (c1 - c0 - kg + groups - 1) / groups : 0;  // this warp's blocks
-  // block i of this warp: c0 + kg + i * groups; lane l holds the page row and
-  // the scales of blocks 32 w + l (this batch of 32) and the next batch's rows
-  const int bshift = A.pshift - 4, bmask = (1 << bshift) - 1;
-  auto block_row = [&](int i) -> int32_t {  // the block's index in the pool's [page][head][block] view, -1: none
-    int64_t idx = -1;
-    if (i < nb) {
-      const int b = c0 + kg + i * groups;
-      const int32_t page = A.table[(int64_t)r * A.per + (b >> bshift)];
-      if (page >= 0 && page < A.pages) return page;
-      if (A.bad) atomicOr(A.bad, 1);
-    }
-    return (int32_t)idx;
-  };
-  auto flat = [&](int32_t page, int i) -> int64_t {  // index of the block among all heads' blocks
-    const int b = c0 + kg + i * groups;
-    return (((int64_t)page * A.Hkv + h) << bshift) + (b & bmask);
-  };
-  int32_t page_l = block_row(lane), page_n = -1;
-  float ks_l = 0.f, vs_l = 0.f;
-  if (page_l >= 0) {
-    const int64_t f = flat(page_l, lane);
-    ks_l = A.ks[f];
-    vs_l = A.vs[f];
-  }
   uint4 kb[2][NV], vb[4];  // K: rows g, g + 8; V: tokens 2t, 2t+1, 2t+8, 2t+9
   auto load_k = [&](int64_t f) {
-    const uint8_t* p = A.k + f * (16 * HD) + t * (HD / 4);
+    const uint8_t* p = A.k + f * (16 * HD) + t * 16;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int u = 0; u < NV; ++u) kb[j][u] = ld_codes16(p + (g + 8 * j) * HD + 16 * u);
+      for (int u = 0; u < NV; ++u) kb[j][u] = ld_codes16(p + (g + 8 * j) * HD + 64 * u);
   };
   auto load_v = [&](int64_t f) {
     const uint8_t* p = A.v + f * (16 * HD) + g * (HD / 8);
@@ -319,7 +346,7 @@ __global__ void __launch_bounds__(ATT_WARPS * 32, 2) kv8_attention_kernel(const 
       if (HD == 128) {
         vb[j] = ld_codes16(row);
       } else {
-        const uint2 x = __ldg(reinterpret_cast<const uint2*>(row));
+        const uint2 x = ld_codes8(row);
         vb[j].x = x.x;
         vb[j].y = x.y;
       }
@@ -363,7 +390,10 @@ __global__ void __launch_bounds__(ATT_WARPS * 32, 2) kv8_attention_kernel(const 
       codes_f16<CT>(wx, a0, a2);
       codes_f16<CT>(wy, a1, a3);
       mma_f16((s & 1) ? c2 : c, a0, a1, a2, a3, qh[s][0], qh[s][1]);
-      if (HL) mma_f16((s & 1) ? c2 : c, a0, a1, a2, a3, ql[HL ? s : 0][0], ql[HL ? s : 0][1]);
+      if (HL) {
+        const uint2 q2 = ql[s * 32];
+        mma_f16((s & 1) ? c2 : c, a0, a1, a2, a3, q2.x, q2.y);
+      }
     }
     if (more) load_k(fnext);
 #pragma unroll
@@ -425,8 +455,8 @@ __global__ void __launch_bounds__(ATT_WARPS * 32, 2) kv8_attention_kernel(const 
       }
       n0 = fmaxf(n0, mrun[0]);
       n1 = fmaxf(n1, mrun[1]);
-      const float a0 = mrun[0] == -INFINITY ? 0.f : exp2f(mrun[0] - n0);
-      const float a1 = mrun[1] == -INFINITY ? 0.f : exp2f(mrun[1] - n1);
+      const float a0 = mrun[0] == -INFINITY ? 0.f : exp2_fast(mrun[0] - n0);
+      const float a1 = mrun[1] == -INFINITY ? 0.f : exp2_fast(mrun[1] - n1);
       mrun[0] = n0;
       mrun[1] = n1;
       lrun[0] *= a0;
@@ -446,10 +476,11 @@ __global__ void __launch_bounds__(ATT_WARPS * 32, 2) kv8_attention_kernel(const 
 #pragma unroll
         for (int x = 0; x < 4; ++x) o[m][x] *= f;
       vref = vs;
+      winv = __fdiv_rn(P_SCALE, vs);
     }
-    const float wv = vref > 0.f ? __fdiv_rn(vs, vref) * P_SCALE : 0.f;
+    const float wv = vs * winv;
     const float m0 = mrun[0] == -INFINITY ? 0.f : mrun[0], m1 = mrun[1] == -INFINITY ? 0.f : mrun[1];
-    const float p0 = exp2f(c[0] - m0), p1 = exp2f(c[1] - m1), p2 = exp2f(c[2] - m0), p3 = exp2f(c[3] - m1);
+    const float p0 = exp2_fast(c[0] - m0), p1 = exp2_fast(c[1] - m1), p2 = exp2_fast(c[2] - m0), p3 = exp2_fast(c[3] - m1);
     lrun[0] += p0 + p2;
     lrun[1] += p1 + p3;
     const float w0 = p0 * wv, w1 = p1 * wv, w2 = p2 * wv, w3 = p3 * wv;
@@ -490,16 +521,17 @@ __global__ void __launch_bounds__(ATT_WARPS * 32, 2) kv8_attention_kernel(const 
     lrun[1] += __shfl_xor_sync(FULL, lrun[1], x);
   }
   const float back = vref * (1.f / P_SCALE);
+  __syncwarp();
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
-    float* row = &so[warp][2 * t + c][g * (HD / 8)];
+    float* row = &S.o[warp][2 * t + c][g * (HD / 8)];
 #pragma unroll
     for (int m = 0; m < MT; m += 2)
       *reinterpret_cast<float4*>(row + 2 * m) =
           make_float4(o[m][c] * back, o[m][2 + c] * back, o[m + 1][c] * back, o[m + 1][2 + c] * back);
     if (g == 0) {
-      sml[warp][2 * t + c][0] = mrun[c];
-      sml[warp][2 * t + c][1] = lrun[c];
+      S.ml[warp][2 * t + c][0] = mrun[c];
+      S.ml[warp][2 * t + c][1] = lrun[c];
     }
   }
   __syncthreads();
@@ -510,15 +542,15 @@ __global__ void __launch_bounds__(ATT_WARPS * 32, 2) kv8_attention_kernel(const 
     const int qi = (qc * A.nq + tl) * 8 + qq;
     if (qi >= nqueries) continue;
     float m = -INFINITY;
-    for (int w = 0; w < groups; ++w) m = fmaxf(m, sml[tl + w * A.nq][qq][0]);
+    for (int w = 0; w < groups; ++w) m = fmaxf(m, S.ml[tl + w * A.nq][qq][0]);
     const float mref = m == -INFINITY ? 0.f : m;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
     for (int w = 0; w < groups; ++w) {
       const int wp = tl + w * A.nq;
-      const float f = exp2f(sml[wp][qq][0] - mref);
-      const float4 v = *reinterpret_cast<const float4*>(&so[wp][qq][4 * d]);
-      l = fmaf(f, sml[wp][qq][1], l);
+      const float f = exp2_fast(S.ml[wp][qq][0] - mref);
+      const float4 v = *reinterpret_cast<const float4*>(&S.o[wp][qq][4 * d]);
+      l = fmaf(f, S.ml[wp][qq][1], l);
       acc.x = fmaf(f, v.x, acc.x);
       acc.y = fmaf(f, v.y, acc.y);
       acc.z = fmaf(f, v.z, acc.z);
@@ -526,77 +558,199 @@ __global__ void __launch_bounds__(ATT_WARPS * 32, 2) kv8_attention_kernel(const 
     }
     const int row = qi / A.GH, head = h * A.GH + qi % A.GH;
     const int64_t rh = (int64_t)(rq.row0 + row) * A.Hq + head;
-    if (A.nsplit == 1) {
+    if (direct) {
       const float inv = l != 0.f ? 1.f / l : 0.f;  // (NaN stays NaN)
       store_elem4<DT>(A.out, (int64_t)(rq.row0 + row) * A.out_stride + (int64_t)head * HD + 4 * d,
                       make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-      if (d == 0 && A.lse) A.lse[rh] = (m + log2f(l)) * LN2;
+      if (d == 0 && A.lse) A.lse[(int64_t)(rq.row0 + row) * A.Hq + head] = (m + log2f(l)) * LN2;
     } else {
-      *reinterpret_cast<float4*>(A.rec_o + (rh * A.nsplit + split) * HD + 4 * d) = acc;
-      if (d == 0) *reinterpret_cast<float2*>(A.rec_ml + (rh * A.nsplit + split) * 2) = make_float2(m, l);
+      const int64_t at = rec * (A.nq * 8) + tl * 8 + qq;
+      *reinterpret_cast<float4*>(A.rec_o + at * HD + 4 * d) = acc;
+      if (d == 0) *reinterpret_cast<float2*>(A.rec_ml + at * 2) = make_float2(m, l);
     }
   }
 }
 
-// Joins the chunks' records of a (row, head) in chunk order; one warp each.
-template <int DT, int HD>
-__global__ void __launch_bounds__(256) kv8_join_kernel(const __grid_constant__ AttArgs A) {
+template <int CT, int DT, int HD, bool EX>
+__global__ void __launch_bounds__(ATT_WARPS * 32, 2) kv8_attention_kernel(const __grid_constant__ AttArgs A) {
+  using K = Att<CT, DT, HD, EX>;
+  __shared__ typename K::Smem S;
+  extern __shared__ int64_t pre[];  // [R + 1], shares only
   pdl_trigger();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int per_req = A.max_rows * A.Hq;
-  const int64_t gw = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int r = (int)(gw / per_req), x = (int)(gw % per_req);
-  if (r >= A.R) return;
+  const int tid = threadIdx.x;
+  if (A.whole) {
+    int bid = blockIdx.x;
+    const int qc = bid % A.nqc;
+    bid /= A.nqc;
+    const int h = bid % A.Hkv, r = bid / A.Hkv;
+    const Req rq = load_req(A, r);
+    if (rq.bad && A.bad && tid == 0) atomicOr(A.bad, 1);
+    if (qc < unit_groups(A, rq)) K::segment(A, S, r, rq, h, qc, rq.b0, rq.b1, true, 0);
+    return;
+  }
+  // blocks before each request: every CTA adds them up (R <= 4096 lengths from L2)
+  __shared__ int64_t wsum[ATT_WARPS];
+  const int lane = tid & 31, warp = tid >> 5;
+  int64_t base = 0;
+  for (int r0 = 0; r0 < A.R; r0 += ATT_WARPS * 32) {
+    const int r = r0 + tid;
+    int64_t w = 0;
+    if (r < A.R) {
+      const Req rq = load_req(A, r);
+      w = (int64_t)(rq.b1 - rq.b0) * A.Hkv * unit_groups(A, rq);
+      if (blockIdx.x == 0 && rq.bad && A.bad) atomicOr(A.bad, 1);
+    }
+    int64_t inc = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(FULL, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    int64_t before = base, all = 0;
+#pragma unroll
+    for (int v = 0; v < ATT_WARPS; ++v) {
+      if (v < warp) before += wsum[v];
+      all += wsum[v];
+    }
+    if (r < A.R) pre[r] = before + inc - w;
+    base += all;
+    __syncthreads();
+  }
+  const int64_t W = base;
+  if (tid == 0) pre[A.R] = W;
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int r = tid; r <= A.R; r += ATT_WARPS * 32) A.prefix[r] = pre[r];
+  const int64_t n = share_count(W, A.ctas);
+  if ((int64_t)blockIdx.x >= n || W == 0) return;
+  int64_t x, end;
+  if (W < (1 << 22)) {  // (32-bit divisions: n <= 1024)
+    x = (uint32_t)W * blockIdx.x / (uint32_t)n;
+    end = (uint32_t)W * (blockIdx.x + 1) / (uint32_t)n;
+  } else {
+    x = range_lo(W, n, blockIdx.x);
+    end = range_lo(W, n, blockIdx.x + 1);
+  }
+  int r = 0;
+  for (int hi = A.R; hi - r > 1;) {  // the last r with pre[r] <= x
+    const int mid = (r + hi) >> 1;
+    if (pre[mid] <= x) r = mid;
+    else hi = mid;
+  }
+  while (x < end) {
+    while (pre[r + 1] <= x) ++r;
+    const Req rq = load_req(A, r);
+    const int nb = rq.b1 - rq.b0, per_head = unit_groups(A, rq);
+    const int64_t in = x - pre[r];
+    const int unit = in < (1ll << 31) ? (int)((uint32_t)in / (uint32_t)nb) : (int)(in / nb);
+    const int b = (int)(in - (int64_t)unit * nb);
+    const int64_t left = end - x;
+    const int cnt = left < nb - b ? (int)left : nb - b;
+    K::segment(A, S, r, rq, unit / per_head, unit % per_head, rq.b0 + b, rq.b0 + b + cnt, cnt == nb,
+               blockIdx.x + (int64_t)r * A.Hkv * A.nqc + unit);
+    x += cnt;
+    __syncthreads();  // the next segment writes the shared records
+  }
+}
+
+// Joins the records of one tile of 8 queries of a unit, in share order.  The
+// records of one query stand 2 KB and more apart and are few (a unit's
+// shares); what counts is that their loads go out together: PAR groups of
+// 8 hd / 4 threads each take every PAR-th record, 8 at a time.
+template <int DT, int HD, int PAR>
+__global__ void __launch_bounds__(2 * HD * PAR) kv8_join_kernel(const __grid_constant__ AttArgs A) {
+  constexpr int DQ = HD / 4, NT = 8 * DQ;
+  __shared__ float4 so[PAR > 1 ? PAR : 1][PAR > 1 ? NT : 1];
+  __shared__ float2 sml[PAR > 1 ? PAR : 1][8];
+  pdl_trigger();
+  pdl_wait();
+  int bid = blockIdx.x;
+  const int tl = bid % A.nq;
+  bid /= A.nq;
+  const int qc = bid % A.nqc;
+  bid /= A.nqc;
+  const int h = bid % A.Hkv, r = bid / A.Hkv;
   const Req rq = load_req(A, r);
-  const int row = x / A.Hq, head = x % A.Hq;
-  if (row >= rq.n) return;
-  int ns = (rq.b1 - rq.b0 + A.chunk - 1) / A.chunk;
-  ns = ns < 1 ? 1 : ns > A.nsplit ? A.nsplit : ns;
-  const int64_t rh = (int64_t)(rq.row0 + row) * A.Hq + head;
-  const float2* ml = reinterpret_cast<const float2*>(A.rec_ml + rh * A.nsplit * 2);
-  float m = -INFINITY;
-  for (int s = lane; s < ns; s += 32) m = fmaxf(m, __ldcg(ml + s).x);
+  const int per_head = unit_groups(A, rq), nb = rq.b1 - rq.b0;
+  const int64_t W = A.prefix[A.R], p0 = A.prefix[r];
+  if (qc >= per_head) return;
+  const int e = threadIdx.x % NT, grp = threadIdx.x / NT, d = e % DQ, qq = e / DQ;
+  const int qi = (qc * A.nq + tl) * 8 + qq;
+  const bool has = qi < rq.n * A.GH;
+  const int unit = h * per_head + qc;
+  float m = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (nb > 0) {
+    const int64_t n = share_count(W, A.ctas), lo = p0 + (int64_t)unit * nb;
+    int i0, i1;
+    if (W < (1 << 22)) {
+      i0 = (int)owner32((uint32_t)W, (uint32_t)n, (uint32_t)lo);
+      i1 = (int)owner32((uint32_t)W, (uint32_t)n, (uint32_t)(lo + nb - 1));
+    } else {
+      i0 = (int)owner_of(W, n, lo);
+      i1 = (int)owner_of(W, n, lo + nb - 1);
+    }
+    if (i0 == i1) return;  // written at once
+    const int64_t u = (int64_t)r * A.Hkv * A.nqc + unit;
+    for (int i = i0 + grp; has && i <= i1; i += 8 * PAR) {
+      float2 ml[8];
+      float4 v[8];
 #pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
-  const float mref = m == -INFINITY ? 0.f : m;
-  constexpr int W = HD / 32;
-  float acc[W], l = 0.f;
+      for (int k = 0; k < 8; ++k) {
+        const int64_t at = (i + k * PAR + u) * (A.nq * 8) + tl * 8 + qq;
+        const bool in = i + k * PAR <= i1;
+        ml[k] = in ? __ldcg(reinterpret_cast<const float2*>(A.rec_ml) + at) : make_float2(-INFINITY, 0.f);
+        v[k] = in ? __ldcg(reinterpret_cast<const float4*>(A.rec_o + at * HD) + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      float nm = m;
 #pragma unroll
-  for (int w = 0; w < W; ++w) acc[w] = 0.f;
-  const float* ro = A.rec_o + rh * A.nsplit * HD + lane * W;
-  for (int s0 = 0; s0 < ns; s0 += 32) {
-    const int cnt = ns - s0 < 32 ? ns - s0 : 32;
-    float2 mine = lane < cnt ? __ldcg(ml + s0 + lane) : make_float2(-INFINITY, 0.f);
-    const float fl = exp2f(mine.x - mref);
-#pragma unroll 4
-    for (int s = 0; s < cnt; ++s) {
-      const float f = __shfl_sync(FULL, fl, s), ls = __shfl_sync(FULL, mine.y, s);
-      l = fmaf(f, ls, l);
-      if (W == 4) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(ro + (int64_t)(s0 + s) * HD));
-        acc[0] = fmaf(f, v.x, acc[0]);
-        acc[1] = fmaf(f, v.y, acc[1]);
-        acc[W - 2] = fmaf(f, v.z, acc[W - 2]);
-        acc[W - 1] = fmaf(f, v.w, acc[W - 1]);
-      } else {
-        const float2 v = __ldcg(reinterpret_cast<const float2*>(ro + (int64_t)(s0 + s) * HD));
-        acc[0] = fmaf(f, v.x, acc[0]);
-        acc[1] = fmaf(f, v.y, acc[1]);
+      for (int k = 0; k < 8; ++k) nm = fmaxf(nm, ml[k].x);
+      const float ref = nm == -INFINITY ? 0.f : nm, f0 = exp2_fast(m - ref);
+      l *= f0;
+      acc = make_float4(acc.x * f0, acc.y * f0, acc.z * f0, acc.w * f0);
+      m = nm;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float f = exp2_fast(ml[k].x - ref);
+        l = fmaf(f, ml[k].y, l);
+        acc.x = fmaf(f, v[k].x, acc.x);
+        acc.y = fmaf(f, v[k].y, acc.y);
+        acc.z = fmaf(f, v[k].z, acc.z);
+        acc.w = fmaf(f, v[k].w, acc.w);
       }
     }
   }
-  const float inv = l != 0.f ? 1.f / l : 0.f;
-  const int64_t at = (int64_t)(rq.row0 + row) * A.out_stride + (int64_t)head * HD + lane * W;
-  if (W == 4) {
-    store_elem4<DT>(A.out, at, make_float4(acc[0] * inv, acc[1] * inv, acc[W - 2] * inv, acc[W - 1] * inv));
-  } else if (DT == DDL_T_F32) {
-    *reinterpret_cast<float2*>(reinterpret_cast<float*>(A.out) + at) = make_float2(acc[0] * inv, acc[1] * inv);
-  } else {
-    *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(A.out) + at) =
-        DT == DDL_T_BF16 ? pack_bf16x2(acc[0] * inv, acc[1] * inv) : pack_f16x2(acc[0] * inv, acc[1] * inv);
+  if (PAR > 1) {
+    so[PAR > 1 ? grp : 0][PAR > 1 ? e : 0] = acc;
+    if (d == 0) sml[PAR > 1 ? grp : 0][qq] = make_float2(m, l);
+    __syncthreads();
+    if (grp > 0) return;
+    m = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < PAR; ++k) m = fmaxf(m, sml[k][qq].x);
+    const float ref = m == -INFINITY ? 0.f : m;
+    l = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < PAR; ++k) {
+      const float f = exp2_fast(sml[k][qq].x - ref);
+      const float4 v = so[PAR > 1 ? k : 0][PAR > 1 ? e : 0];
+      l = fmaf(f, sml[k][qq].y, l);
+      acc.x = fmaf(f, v.x, acc.x);
+      acc.y = fmaf(f, v.y, acc.y);
+      acc.z = fmaf(f, v.z, acc.z);
+      acc.w = fmaf(f, v.w, acc.w);
+    }
   }
-  if (lane == 0 && A.lse) A.lse[rh] = (m + log2f(l)) * LN2;
+  if (!has) return;
+  const int row = qi / A.GH, head = h * A.GH + qi % A.GH;
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  store_elem4<DT>(A.out, (int64_t)(rq.row0 + row) * A.out_stride + (int64_t)head * HD + 4 * d,
+                  make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+  if (d == 0 && A.lse) A.lse[(int64_t)(rq.row0 + row) * A.Hq + head] = (m + log2f(l)) * LN2;
 }
 
 // ------------------------------------------------------------------ host
@@ -618,9 +772,11 @@ int att_sms(int& sms) {
   return DDL_OK;
 }
 
+constexpr int WHOLE_BLOCKS = 32;
+
 struct AttPlan {
-  int32_t nq, nqc, nsplit, chunk;
-  int64_t rec_ml, total;  // workspace offsets
+  int32_t nq, nqc, whole, ctas, deep;  // deep: a unit may have many shares
+  int64_t rec_ml, prefix, total;       // workspace offsets
 };
 
 int check_sizes(int32_t H_q, int32_t H_kv, int32_t hd, int32_t R, int32_t T, int32_t max_rows, int32_t max_len) {
@@ -632,12 +788,7 @@ int check_sizes(int32_t H_q, int32_t H_kv, int32_t hd, int32_t R, int32_t T, int
   return DDL_OK;
 }
 
-// The launch: query tiles per CTA, and chunks of the key axis.  One (request,
-// K/V head) is split until the grid holds every SM's two CTAs once, in chunks of at
-// least one block per warp; long axes of a full grid are cut into chunks of at
-// most 1024 tokens all the same, so that ragged lengths spread evenly.
-int att_plan(int32_t H_q, int32_t H_kv, int32_t hd, int32_t R, int32_t T, int32_t max_rows, int32_t max_len,
-             int32_t window, AttPlan& p) {
+int att_plan(int32_t H_q, int32_t H_kv, int32_t hd, int32_t R, int32_t max_rows, int32_t max_len, AttPlan& p) {
   int sms = 0;
   const int st = att_sms(sms);
   if (st) return st;
@@ -645,22 +796,21 @@ int att_plan(int32_t H_q, int32_t H_kv, int32_t hd, int32_t R, int32_t T, int32_
   p.nq = 1;
   while (p.nq < ATT_WARPS && p.nq < tiles) p.nq *= 2;
   p.nqc = (tiles + p.nq - 1) / p.nq;
-  int64_t keys = max_len;
-  if (window > 0 && (int64_t)window + max_rows + 15 < keys) keys = (int64_t)window + max_rows + 15;
-  const int64_t blocks = (keys + 15) / 16;
-  const int64_t units = (int64_t)R * H_kv * p.nqc, groups = ATT_WARPS / p.nq;
-  int64_t want = 2 * sms / units;
-  if (want < 1) want = 1;
-  int64_t chunk = (blocks + want - 1) / want;
-  chunk = (chunk + groups - 1) / groups * groups;
-  if (chunk > 64) chunk = 64;
-  if (chunk < groups) chunk = groups;
-  p.chunk = (int32_t)chunk;
-  p.nsplit = (int32_t)((blocks + chunk - 1) / chunk);
-  if (units * p.nsplit > 0x7fffffffLL) return DDL_ERR_UNSUPPORTED;
-  const int64_t rows = (int64_t)T * H_q;
-  p.rec_ml = p.nsplit > 1 ? align256(rows * p.nsplit * hd * 4) : 0;
-  p.total = p.nsplit > 1 ? align256(p.rec_ml + rows * p.nsplit * 2 * 4) : 256;
+  const int64_t blocks = ((int64_t)max_len + 15) / 16, units = (int64_t)R * H_kv * p.nqc;
+  p.whole = blocks <= WHOLE_BLOCKS;
+  p.rec_ml = p.prefix = 0;
+  p.total = 256;
+  p.ctas = (int32_t)units;
+  p.deep = 0;
+  if (p.whole) return DDL_OK;
+  const int64_t most = (units * blocks + MIN_SHARE - 1) / MIN_SHARE;
+  p.ctas = (int32_t)(most < 2 * sms ? most : 2 * sms);
+  if (p.ctas > 1024) return DDL_ERR_UNSUPPORTED;  // (the kernels' 32-bit share arithmetic)
+  p.deep = units * 8 <= p.ctas;
+  const int64_t queries = (units + p.ctas) * p.nq * 8;  // of all records
+  p.rec_ml = align256(queries * hd * 4);
+  p.prefix = align256(p.rec_ml + queries * 2 * 4);
+  p.total = align256(p.prefix + (int64_t)(R + 1) * 8);
   return DDL_OK;
 }
 
@@ -678,8 +828,9 @@ const void* att_fn(int dt, int hd, bool ex) {
                                                                            : att_fn<CT, DDL_T_F16>(hd, ex);
 }
 template <int DT>
-const void* join_fn(int hd) {
-  return hd == 128 ? (const void*)kv8_join_kernel<DT, 128> : (const void*)kv8_join_kernel<DT, 64>;
+const void* join_fn(int hd, bool deep) {
+  if (hd == 128) return deep ? (const void*)kv8_join_kernel<DT, 128, 4> : (const void*)kv8_join_kernel<DT, 128, 1>;
+  return deep ? (const void*)kv8_join_kernel<DT, 64, 4> : (const void*)kv8_join_kernel<DT, 64, 1>;
 }
 
 }  // namespace
@@ -691,7 +842,7 @@ extern "C" size_t ddl_kv8_attention_workspace_bytes(int32_t H_q, int32_t H_kv, i
                                                     int32_t max_rows, int32_t max_len) {
   if (check_sizes(H_q, H_kv, head_dim, R, T, max_rows, max_len)) return 0;
   AttPlan p;
-  if (att_plan(H_q, H_kv, head_dim, R, T, max_rows, max_len, 0, p)) return 0;
+  if (att_plan(H_q, H_kv, head_dim, R, max_rows, max_len, p)) return 0;
   return (size_t)p.total;
 }
 
@@ -718,11 +869,9 @@ extern "C" int ddl_kv8_attention(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, i
   for (const void* p : {(const void*)q_off, (const void*)kv_len, (const void*)page_table, (const void*)lse,
                         (const void*)bad_out, (const void*)opts->slopes})
     if ((uintptr_t)p & 3u) return DDL_ERR_ALIGN;
-  AttPlan pl, full;
-  if ((st = att_plan(H_q, H_kv, head_dim, R, T, max_rows, max_len, 0, full))) return st;
-  if ((st = att_plan(H_q, H_kv, head_dim, R, T, max_rows, max_len, opts->window, pl))) return st;
-  if (ws_bytes < (size_t)full.total) return DDL_ERR_WORKSPACE;
-  if (pl.total > full.total) pl = full;  // (a window needs no more records than the whole axis)
+  AttPlan pl;
+  if ((st = att_plan(H_q, H_kv, head_dim, R, max_rows, max_len, pl))) return st;
+  if (ws_bytes < (size_t)pl.total) return DDL_ERR_WORKSPACE;
   AttArgs a;
   a.k = kv->k;
   a.v = kv->v;
@@ -737,6 +886,7 @@ extern "C" int ddl_kv8_attention(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, i
   a.bad = bad_out;
   a.rec_o = (float*)workspace;
   a.rec_ml = (float*)((uint8_t*)workspace + pl.rec_ml);
+  a.prefix = (int64_t*)((uint8_t*)workspace + pl.prefix);
   a.slopes = opts->slopes;
   a.pages = kv->pages;
   a.q_stride = q_stride;
@@ -754,20 +904,23 @@ extern "C" int ddl_kv8_attention(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, i
   a.per = pages_per_seq;
   a.max_rows = max_rows;
   a.max_len = max_len;
-  a.nsplit = pl.nsplit;
-  a.chunk = pl.chunk;
+  a.whole = pl.whole;
+  a.ctas = pl.ctas;
   a.nq = pl.nq;
   a.nqc = pl.nqc;
   const bool ex = opts->softcap > 0.f || opts->slopes;
   const void* fn = kv->type == DDL_KV8_E4M3 ? att_fn<DDL_KV8_E4M3>(dtype, head_dim, ex)
                                             : att_fn<DDL_KV8_INT8>(dtype, head_dim, ex);
   void* args[] = {&a};
-  const int64_t ctas = (int64_t)R * H_kv * pl.nqc * pl.nsplit;
-  st = cuda_status(launch_pdl(fn, dim3((unsigned)ctas), dim3(ATT_WARPS * 32), args, 0, (cudaStream_t)stream));
-  if (st || pl.nsplit == 1) return st;
-  const int64_t warps = (int64_t)R * max_rows * H_q;
-  fn = dtype == DDL_T_F32 ? join_fn<DDL_T_F32>(head_dim) : dtype == DDL_T_BF16 ? join_fn<DDL_T_BF16>(head_dim)
-                                                                              : join_fn<DDL_T_F16>(head_dim);
-  return cuda_status(
-      launch_pdl(fn, dim3((unsigned)((warps + 7) / 8)), dim3(256), args, 0, (cudaStream_t)stream));
+  const size_t smem = pl.whole ? 0 : (size_t)(R + 1) * 8;
+  if (smem > 8192 && (st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                            (DDL_KV8_MAX_REQS + 1) * 8))))
+    return st;  // (beside the static 34 KB more than 48 KB)
+  st = cuda_status(launch_pdl(fn, dim3((unsigned)pl.ctas), dim3(ATT_WARPS * 32), args, smem, (cudaStream_t)stream));
+  if (st || pl.whole) return st;
+  fn = dtype == DDL_T_F32    ? join_fn<DDL_T_F32>(head_dim, pl.deep)
+       : dtype == DDL_T_BF16 ? join_fn<DDL_T_BF16>(head_dim, pl.deep)
+                             : join_fn<DDL_T_F16>(head_dim, pl.deep);
+  return cuda_status(launch_pdl(fn, dim3((unsigned)(R * H_kv * pl.nqc * pl.nq)),
+                                dim3((unsigned)(2 * head_dim * (pl.deep ? 4 : 1))), args, 0, (cudaStream_t)stream));
 }

@@ -436,29 +436,34 @@ def ws_tensor(workspace: torch.Tensor, offset: int, n: int) -> torch.Tensor:
 
 
 # ------------------------------------------------------------------ 8-bit KV cache
+# A serving step makes these calls once a layer, and their kernels take a few
+# microseconds: the checks below cost about as much as the launch, so they
+# compare integers and types directly and build messages only on failure.
 
 T_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 KV8_TYPES = {torch.float8_e4m3fn: 0, torch.int8: 1}
 
 
-def _need(ok: bool, what: str):
-    if not ok:
-        raise ValueError(what)
+def _i32(name: str, t, dev: int, n: int):
+    """Data pointer of a contiguous int32 tensor of n entries (n < 0: any) on CUDA device `dev`."""
+    if t.dtype is not torch.int32 or t.get_device() != dev or not t.is_contiguous() or (n >= 0 and t.numel() != n):
+        raise ValueError(f"{name}: a contiguous int32 tensor{f' of {n} entries' if n >= 0 else ''} on cuda:{dev}")
+    return t.data_ptr()
 
 
-def _i32(name: str, t, dev, n: int | None = None):
-    """Checks a contiguous int32 tensor (of n entries) on device `dev`."""
-    _need(t.dtype is torch.int32 and t.device == dev and t.is_contiguous() and (n is None or t.numel() == n),
-          f"{name}: a contiguous int32 tensor{'' if n is None else f' of {n} entries'} on {dev}")
+def _f32(name: str, t, dev: int, n: int):
+    if t is None:
+        return None
+    if t.dtype is not torch.float32 or t.get_device() != dev or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{name}: a contiguous fp32 tensor of {n} entries on cuda:{dev}")
+    return t.data_ptr()
 
 
-def _run_on(dev, name: str, fn, stream, *args):
-    """Calls fn(*args, stream) with `dev` as the current device, on `stream` or
-    that device's current stream."""
-    if dev.type != "cuda":
-        raise ValueError(f"{name}: tensors on a CUDA device")
-    s = stream.cuda_stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev.index:
+def _run_on(dev: int, name: str, fn, stream, *args):
+    """fn(*args, stream) with CUDA device `dev` as the current one, on `stream`
+    or that device's current stream."""
+    s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+    if torch._C._cuda_getDevice() == dev:
         st = fn(*args, s)
     else:
         with torch.cuda.device(dev):
@@ -467,29 +472,34 @@ def _run_on(dev, name: str, fn, stream, *args):
         raise DDLError(name, st, _lib)
 
 
-def _kv8(pool) -> tuple:
-    """(KV8, H_kv, head_dim) of a pool (k, v, k_scale, v_scale): codes
-    [pages, H_kv, page_size, hd] float8_e4m3fn or int8, scales fp32
-    [pages, H_kv, page_size / 16]."""
+def _kv8(pool):
+    """(KV8, H_kv, head_dim, device index) of a pool (k, v, k_scale, v_scale):
+    codes [pages, H_kv, page_size, hd] float8_e4m3fn or int8, scales fp32
+    [pages, H_kv, page_size / 16], contiguous, on one CUDA device."""
     k, v, ks, vs = pool
-    _need(k.dim() == 4 and k.dtype in KV8_TYPES and v.dtype is k.dtype and v.shape == k.shape,
-          "pool: k and v [pages, H_kv, page_size, head_dim] of one 8-bit type")
-    pages, H, P, hd = k.shape
-    _need(ks.dtype is torch.float32 and vs.dtype is torch.float32 and ks.shape == vs.shape
-          and tuple(ks.shape) == (pages, H, P // 16), "pool: scales fp32 [pages, H_kv, page_size / 16]")
-    _need(k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous(),
-          "pool: contiguous tensors")
-    _need(v.device == k.device and ks.device == k.device and vs.device == k.device, "pool: tensors of one device")
-    return KV8(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, P, KV8_TYPES[k.dtype]), H, hd
+    shape, dev, code = k.shape, k.get_device(), KV8_TYPES.get(k.dtype, -1)
+    if code < 0 or len(shape) != 4 or v.dtype is not k.dtype or v.shape != shape:
+        raise ValueError("pool: k and v [pages, H_kv, page_size, head_dim] of one 8-bit type")
+    pages, H, P, hd = shape
+    if (ks.dtype is not torch.float32 or vs.dtype is not torch.float32 or ks.shape != (pages, H, P // 16)
+            or vs.shape != ks.shape):
+        raise ValueError("pool: scales fp32 [pages, H_kv, page_size / 16]")
+    if not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
+        raise ValueError("pool: contiguous tensors")
+    if dev < 0 or v.get_device() != dev or ks.get_device() != dev or vs.get_device() != dev:
+        raise ValueError("pool: tensors of one CUDA device")
+    return KV8(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, P, code), H, hd, dev
 
 
-def _rows(name: str, x, dev, heads: int, hd: int):
-    """Checks rows [T, heads, hd] whose heads are contiguous; returns their stride."""
-    _need(x.dim() == 3 and x.shape[1] == heads and x.shape[2] == hd and x.dtype in T_DTYPES and x.device == dev,
-          f"{name}: [T, {heads}, {hd}] fp32, bf16 or fp16 on {dev}")
-    T = x.shape[0]
+def _rows(name: str, x, dev: int, heads: int, hd: int, dtype, T: int) -> int:
+    """Row stride of rows [T, heads, hd] whose heads are contiguous."""
+    if x.dtype is not dtype or x.get_device() != dev or x.shape != (T, heads, hd) or dtype not in T_DTYPES:
+        raise ValueError(f"{name}: [{T}, {heads}, {hd}] {dtype} (fp32, bf16 or fp16) on cuda:{dev}")
+    if x.is_contiguous():
+        return heads * hd
     st = x.stride()
-    _need((st[2] == 1) and (heads == 1 or st[1] == hd), f"{name}: a row's heads are contiguous")
+    if st[2] != 1 or (heads > 1 and st[1] != hd):
+        raise ValueError(f"{name}: a row's heads are contiguous")
     return st[0] if T > 1 else heads * hd
 
 
@@ -501,17 +511,16 @@ def ddl_page_plan(old_len: torch.Tensor, add_len: torch.Tensor, free_pages: torc
     add_len[r] rows.  Writes new pages from free_pages into page_table [R,
     pages_per_seq], and row_off [R + 1], kv_len [R], row_pos and slot [T],
     used [1], status [R]."""
-    lib = load()
-    dev, R, T = page_table.device, old_len.numel(), slot.numel()
-    _need(page_table.dim() == 2 and page_table.shape[0] == R, "page_table: [R, pages_per_seq]")
-    for name, t, n in (("old_len", old_len, R), ("add_len", add_len, R), ("free_pages", free_pages, None),
-                       ("page_table", page_table, None), ("row_off", row_off, R + 1), ("kv_len", kv_len, R),
-                       ("row_pos", row_pos, T), ("slot", slot, T), ("used", used, 1), ("status", status, R)):
-        _i32(name, t, dev, n)
-    _run_on(dev, "ddl_page_plan", lib.ddl_page_plan, stream, old_len.data_ptr(), add_len.data_ptr(), R,
-            int(page_size), free_pages.data_ptr(), free_pages.numel(), page_table.data_ptr(), page_table.shape[1],
-            row_off.data_ptr(), kv_len.data_ptr(), row_pos.data_ptr(), slot.data_ptr(), T, used.data_ptr(),
-            status.data_ptr())
+    lib = _lib or load()
+    dev, R, T, n_free = page_table.get_device(), old_len.numel(), slot.numel(), free_pages.numel()
+    if page_table.dim() != 2 or page_table.shape[0] != R or dev < 0:
+        raise ValueError("page_table: [R, pages_per_seq] on a CUDA device")
+    per = page_table.shape[1]
+    _run_on(dev, "ddl_page_plan", lib.ddl_page_plan, stream, _i32("old_len", old_len, dev, R),
+            _i32("add_len", add_len, dev, R), R, page_size, _i32("free_pages", free_pages, dev, n_free), n_free,
+            _i32("page_table", page_table, dev, -1), per, _i32("row_off", row_off, dev, R + 1),
+            _i32("kv_len", kv_len, dev, R), _i32("row_pos", row_pos, dev, T), _i32("slot", slot, dev, T), T,
+            _i32("used", used, dev, 1), _i32("status", status, dev, R))
 
 
 def ddl_kv8_append(pool, k_new: torch.Tensor, v_new: torch.Tensor, slot: torch.Tensor,
@@ -519,17 +528,12 @@ def ddl_kv8_append(pool, k_new: torch.Tensor, v_new: torch.Tensor, slot: torch.T
     """Quantize the rows k_new, v_new [T, H_kv, hd] into an 8-bit pool (k, v,
     k_scale, v_scale) at the slot indices slot [T] (int32; negative: skipped).
     bad: optional int32 [1] device flag set to 1 by a slot past the pool."""
-    lib = load()
-    kv, H, hd = _kv8(pool)
-    dev, T = pool[0].device, slot.numel()
-    ks, vs = _rows("k_new", k_new, dev, H, hd), _rows("v_new", v_new, dev, H, hd)
-    _need(k_new.dtype is v_new.dtype and k_new.shape[0] == T and v_new.shape[0] == T,
-          "k_new, v_new: one type, a row for each slot")
-    _i32("slot", slot, dev)
-    if bad is not None:
-        _i32("bad", bad, dev, 1)
-    _run_on(dev, "ddl_kv8_append", lib.ddl_kv8_append, stream, kv, H, hd, T_DTYPES[k_new.dtype], k_new.data_ptr(), ks,
-            v_new.data_ptr(), vs, slot.data_ptr(), T, None if bad is None else bad.data_ptr())
+    lib = _lib or load()
+    kv, H, hd, dev = _kv8(pool)
+    T, dtype = slot.numel(), k_new.dtype
+    ks, vs = _rows("k_new", k_new, dev, H, hd, dtype, T), _rows("v_new", v_new, dev, H, hd, dtype, T)
+    _run_on(dev, "ddl_kv8_append", lib.ddl_kv8_append, stream, kv, H, hd, T_DTYPES[dtype], k_new.data_ptr(), ks,
+            v_new.data_ptr(), vs, _i32("slot", slot, dev, T), T, None if bad is None else _i32("bad", bad, dev, 1))
 
 
 def ddl_kv8_attention_workspace_bytes(H_q: int, H_kv: int, hd: int, R: int, T: int, max_rows: int,
@@ -552,37 +556,30 @@ def ddl_kv8_attention(pool, q: torch.Tensor, kv_len: torch.Tensor, page_table: t
     max_len bounds kv_len, max_rows the rows of a request.  scale: 1 / sqrt(hd)
     by default; softcap, window, slopes as in ddl.h.  Returns out (zeros where
     a new one is made and a row belongs to no request)."""
-    lib = load()
-    kv, H, hd = _kv8(pool)
-    dev = pool[0].device
-    _need(q.dim() == 3, "q: [T, H_q, hd]")
-    T, H_q, R = q.shape[0], q.shape[1], kv_len.numel()
-    qs = _rows("q", q, dev, H_q, hd)
+    lib = _lib or load()
+    kv, H, hd, dev = _kv8(pool)
+    if q.dim() != 3 or page_table.dim() != 2:
+        raise ValueError("q: [T, H_q, hd]; page_table: [R, pages_per_seq]")
+    T, H_q, _ = q.shape
+    R, dtype = kv_len.numel(), q.dtype
+    qs = _rows("q", q, dev, H_q, hd, dtype, T)
     if out is None:
-        out = torch.zeros((T, H_q, hd), dtype=q.dtype, device=dev)
-    os_ = _rows("out", out, dev, H_q, hd)
-    _need(out.dtype is q.dtype and out.shape[0] == T, "out: as q")
-    _i32("kv_len", kv_len, dev)
-    _i32("page_table", page_table, dev)
-    _need(page_table.dim() == 2 and page_table.shape[0] == R, "page_table: [R, pages_per_seq]")
-    if q_off is not None:
-        _i32("q_off", q_off, dev, R + 1)
-    if bad is not None:
-        _i32("bad", bad, dev, 1)
-    for name, t, n in (("slopes", slopes, H_q), ("lse", lse, T * H_q)):
-        _need(t is None or (t.dtype is torch.float32 and t.device == dev and t.is_contiguous() and t.numel() == n),
-              f"{name}: fp32, {n} entries, on {dev}")
+        out = torch.zeros((T, H_q, hd), dtype=dtype, device=q.device)
+    os_ = _rows("out", out, dev, H_q, hd, dtype, T)
+    rows_in_table, per = page_table.shape
+    if rows_in_table != R:
+        raise ValueError("page_table: a row for each entry of kv_len")
     if workspace is None:
         workspace = torch.empty(ddl_kv8_attention_workspace_bytes(H_q, H, hd, R, T, max_rows, max_len),
-                                dtype=torch.uint8, device=dev)
-    _need(workspace.device == dev and workspace.is_contiguous(), f"workspace: contiguous, on {dev}")
-    opts = AttnOpts(hd ** -0.5 if scale is None else float(scale), float(softcap), int(window),
-                    None if slopes is None else slopes.data_ptr())
-    _run_on(dev, "ddl_kv8_attention", lib.ddl_kv8_attention, stream, kv, H_q, H, hd, T_DTYPES[q.dtype], opts, R, T,
-            int(max_rows), int(max_len), None if q_off is None else q_off.data_ptr(), kv_len.data_ptr(),
-            page_table.data_ptr(), page_table.shape[1], q.data_ptr(), qs, out.data_ptr(), os_,
-            None if lse is None else lse.data_ptr(), None if bad is None else bad.data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size())
+                                dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: contiguous, on cuda:{dev}")
+    opts = AttnOpts(hd ** -0.5 if scale is None else scale, softcap, window, _f32("slopes", slopes, dev, H_q))
+    _run_on(dev, "ddl_kv8_attention", lib.ddl_kv8_attention, stream, kv, H_q, H, hd, T_DTYPES[dtype], opts, R, T,
+            max_rows, max_len, None if q_off is None else _i32("q_off", q_off, dev, R + 1),
+            _i32("kv_len", kv_len, dev, R), _i32("page_table", page_table, dev, -1), per, q.data_ptr(), qs,
+            out.data_ptr(), os_, _f32("lse", lse, dev, T * H_q), None if bad is None else _i32("bad", bad, dev, 1),
+            workspace.data_ptr(), workspace.nbytes)
     return out
 
 
