@@ -2480,6 +2480,7 @@ static std::mutex g_mu;
 static DevInfo g_dev[64];
 static int g_launch_mode = 0;  // 0 automatic, 1 one launch per stage
 static uint64_t g_wait_ns = WAIT_LIMIT_NS;  // limit of every bounded device wait
+uint64_t wait_limit_ns() { return g_wait_ns; }
 static int g_hold_stage = -1;  // test hook: the grid barrier before this flattened stage never completes
 static uint64_t* g_trace = nullptr;
 static size_t g_trace_bytes = 0;
@@ -2590,7 +2591,7 @@ static int plan(const ddl_shape* s, int wtype, int B, int64_t s_max, int C, MatG
 }
 
 // cuTensorMapEncodeTiled from the driver, found once through the runtime.
-static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {

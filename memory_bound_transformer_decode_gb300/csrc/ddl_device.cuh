@@ -144,6 +144,11 @@ __device__ __forceinline__ uint64_t policy_evict_first() {
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
   return p;
 }
+__device__ __forceinline__ uint64_t policy_evict_normal() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
 // Order this thread's earlier generic-proxy shared-memory accesses before
 // later async-proxy (TMA) writes to the same memory.
 __device__ __forceinline__ void fence_proxy_async_smem() {

@@ -1,6 +1,7 @@
 // ddl_internal.h -- host-side helpers shared by the library's translation units:
 // argument validation, CUDA error capture and the packed-layer geometry.
 #pragma once
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include <string.h>
@@ -11,6 +12,8 @@
 namespace ddl {
 
 void set_cuda_error(cudaError_t e);  // records cudaGetErrorString(e) for ddl_last_cuda_error
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // from the driver, NULL if it has none
+uint64_t wait_limit_ns();            // limit of every bounded device wait
 int noalloc_scratch(void** out);     // device address of ddl_stack_decode_noalloc's static scratch
 
 inline int cuda_status(cudaError_t e) {

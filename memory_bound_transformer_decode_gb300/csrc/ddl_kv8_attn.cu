@@ -38,91 +38,17 @@
 
 #include <mutex>
 
-#include "ddl_kv8.h"
+#include "ddl_kv8_attn.h"
 
 namespace ddl {
 namespace {
 
 constexpr int ATT_WARPS = 8;
-constexpr float LOG2E = 1.4426950408889634f;
-constexpr float LN2 = 0.6931471805599453f;
 // P's fp16 values carry 2^11: with the running maximum allowed to lag by
 // 2^M_LAG they stay below 2^16, and what rounds off below fp16's smallest
 // subnormal is 2^-36 of the largest weight.
 constexpr float P_SCALE = 2048.f;
 constexpr float M_LAG = 4.f;
-
-struct AttArgs {
-  const uint8_t *k, *v;
-  const float *ks, *vs;
-  const int32_t *q_off, *kv_len, *table;
-  const void* q;
-  void* out;
-  float* lse;
-  int32_t* bad;
-  float *rec_o, *rec_ml;  // records [share + unit][query of the unit][hd], [..][2]
-  int64_t* prefix;        // [R + 1] blocks of all units before each request
-  const float* slopes;
-  int64_t pages, q_stride, out_stride;
-  float scale, softcap;
-  int32_t window;
-  int32_t R, T, Hq, Hkv, GH, hd, pshift, per, max_rows, max_len;
-  int32_t whole;    // one CTA a unit, else shares
-  int32_t ctas;     // shares at most
-  int32_t nq, nqc;  // query tiles of 8 a unit has (a power of two <= 8), units over a request's query tiles
-};
-
-// Shares (range_lo and owner_of of the W blocks in n parts): at least MIN_SHARE blocks each.
-constexpr int MIN_SHARE = 16;
-__device__ __forceinline__ int64_t share_count(int64_t W, int ctas) {
-  const int64_t most = (W + MIN_SHARE - 1) / MIN_SHARE;
-  return most < 1 ? 1 : most < ctas ? most : ctas;
-}
-
-// A request's rows and keys as the kernels compute them (clamped to what the
-// launch and the tables allow).
-struct Req {
-  int32_t row0, n, len;  // first row of q, rows, tokens
-  int32_t p0;            // position of its first row (negative: it has no keys)
-  int32_t b0, b1;        // blocks of 16 tokens that any of its rows sees: [b0, b1)
-  bool bad;
-};
-__device__ __forceinline__ Req load_req(const AttArgs& A, int r) {
-  Req q;
-  int64_t row0 = r, n = 1;
-  if (A.q_off) {
-    row0 = A.q_off[r];
-    n = (int64_t)A.q_off[r + 1] - row0;
-  }
-  int64_t len = A.kv_len[r];
-  const int64_t cap = (int64_t)A.per << A.pshift;
-  q.bad = false;
-  if (row0 < 0 || n < 0 || row0 + n > A.T) {
-    q.bad = true;
-    n = 0;
-    row0 = 0;
-  }
-  if (len < 0 || len > A.max_len || len > cap) {
-    q.bad = true;
-    len = len < 0 ? 0 : len;
-    len = len > A.max_len ? A.max_len : len;
-    len = len > cap ? cap : len;
-  }
-  q.row0 = (int32_t)row0;
-  q.len = (int32_t)len;
-  q.p0 = (int32_t)(len - n);  // (n <= T)
-  int64_t lo = A.window > 0 ? len - n - A.window + 1 : 0;
-  lo = lo < 0 ? 0 : lo;
-  if (n > A.max_rows) {
-    q.bad = true;
-    n = A.max_rows;  // its first rows
-  }
-  q.n = (int32_t)n;
-  q.b0 = (int32_t)(lo >> 4);
-  q.b1 = n > 0 ? (int32_t)((len + 15) >> 4) : q.b0;
-  if (q.b1 < q.b0) q.b1 = q.b0;
-  return q;
-}
 
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
   uint32_t d;
@@ -158,50 +84,6 @@ __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi
     lo = *reinterpret_cast<const uint32_t*>(&x);
     hi = *reinterpret_cast<const uint32_t*>(&y);
   }
-}
-
-// Byte mask of the e4m3 NaN codes (low 7 bits all set) of four codes.
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
-  const uint32_t top = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-  return (top >> 7) * 255u;
-}
-
-template <int DT>
-__device__ __forceinline__ float load_elem(const void* p, int64_t i) {
-  if (DT == DDL_T_F32) return reinterpret_cast<const float*>(p)[i];
-  const uint16_t b = reinterpret_cast<const uint16_t*>(p)[i];
-  if (DT == DDL_T_BF16) return bf16_bits_to_f32(b);
-  return __half2float(__ushort_as_half(b));
-}
-// Four neighbouring elements (8- or 16-byte aligned).
-template <int DT>
-__device__ __forceinline__ float4 load_elem4(const void* p, int64_t i) {
-  if (DT == DDL_T_F32) return *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + i);
-  const uint2 u = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p) + i);
-  if (DT == DDL_T_BF16) return make_float4(bf16lo_f32(u.x), bf16hi_f32(u.x), bf16lo_f32(u.y), bf16hi_f32(u.y));
-  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
-  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
-  return make_float4(a.x, a.y, b.x, b.y);
-}
-template <int DT>
-__device__ __forceinline__ void store_elem4(void* p, int64_t i, float4 v) {
-  if (DT == DDL_T_F32) {
-    *reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + i) = v;
-  } else {
-    uint2 u;
-    if (DT == DDL_T_BF16) u = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-    else u = make_uint2(pack_f16x2(v.x, v.y), pack_f16x2(v.z, v.w));
-    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p) + i) = u;
-  }
-}
-
-// tanh from its definition 1 - 2 / (e^{2x} + 1): an absolute error of a few
-// 2^-24, which times the cap is the score's own fp32 rounding.
-__device__ __forceinline__ float cap_tanh(float x) { return 1.f - __fdividef(2.f, __expf(2.f * x) + 1.f); }
-
-// Units of request q: K/V heads times groups of query tiles.
-__device__ __forceinline__ int unit_groups(const AttArgs& A, const Req& q) {
-  return (q.n * A.GH + 8 * A.nq - 1) / (8 * A.nq);
 }
 
 template <int CT, int DT, int HD, bool EX>
@@ -265,7 +147,7 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
   {
     const int qi = tile * 8 + g;
     const bool has = qi < nqueries;
-    const int row = has ? qi / A.GH : 0, head = h * A.GH + (has ? qi % A.GH : 0);
+    const int row = has ? group_row(A, qi) : 0, head = h * A.GH + (has ? qi - row * A.GH : 0);
     const int64_t at = (int64_t)(rq.row0 + row) * A.q_stride + (int64_t)head * HD + t * 16;
     float4 f[KS];
     float mx = 0.f;
@@ -299,13 +181,13 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
   for (int c = 0; c < 2; ++c) {
     const int qi = tile * 8 + 2 * t + c;
     const bool has = qi < nqueries;
-    const int row = has ? qi / A.GH : 0;
+    const int row = has ? group_row(A, qi) : 0;
     const int p = rq.p0 + row;
     hi[c] = has ? p : -1;
     lo[c] = A.window > 0 ? p - A.window + 1 : 0;
     const float q2 = __shfl_sync(FULL, qf, 4 * (2 * t + c));
     cf[c] = q2 * A.scale;
-    slope[c] = EX && A.slopes && has ? A.slopes[h * A.GH + qi % A.GH] * LOG2E : 0.f;
+    slope[c] = EX && A.slopes && has ? A.slopes[h * A.GH + qi - row * A.GH] * LOG2E : 0.f;
     if (!EX) cf[c] *= LOG2E;
     else if (A.softcap > 0.f) cf[c] = __fdiv_rn(cf[c], A.softcap);
     else cf[c] *= LOG2E;
@@ -556,7 +438,7 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
       acc.z = fmaf(f, v.z, acc.z);
       acc.w = fmaf(f, v.w, acc.w);
     }
-    const int row = qi / A.GH, head = h * A.GH + qi % A.GH;
+    const int row = group_row(A, qi), head = h * A.GH + qi - row * A.GH;
     const int64_t rh = (int64_t)(rq.row0 + row) * A.Hq + head;
     if (direct) {
       const float inv = l != 0.f ? 1.f / l : 0.f;  // (NaN stays NaN)
@@ -589,51 +471,12 @@ __global__ void __launch_bounds__(ATT_WARPS * 32, 2) kv8_attention_kernel(const 
     if (qc < unit_groups(A, rq)) K::segment(A, S, r, rq, h, qc, rq.b0, rq.b1, true, 0);
     return;
   }
-  // blocks before each request: every CTA adds them up (R <= 4096 lengths from L2)
   __shared__ int64_t wsum[ATT_WARPS];
-  const int lane = tid & 31, warp = tid >> 5;
-  int64_t base = 0;
-  for (int r0 = 0; r0 < A.R; r0 += ATT_WARPS * 32) {
-    const int r = r0 + tid;
-    int64_t w = 0;
-    if (r < A.R) {
-      const Req rq = load_req(A, r);
-      w = (int64_t)(rq.b1 - rq.b0) * A.Hkv * unit_groups(A, rq);
-      if (blockIdx.x == 0 && rq.bad && A.bad) atomicOr(A.bad, 1);
-    }
-    int64_t inc = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(FULL, inc, o);
-      if (lane >= o) inc += y;
-    }
-    if (lane == 31) wsum[warp] = inc;
-    __syncthreads();
-    int64_t before = base, all = 0;
-#pragma unroll
-    for (int v = 0; v < ATT_WARPS; ++v) {
-      if (v < warp) before += wsum[v];
-      all += wsum[v];
-    }
-    if (r < A.R) pre[r] = before + inc - w;
-    base += all;
-    __syncthreads();
-  }
-  const int64_t W = base;
-  if (tid == 0) pre[A.R] = W;
-  __syncthreads();
-  if (blockIdx.x == 0)
-    for (int r = tid; r <= A.R; r += ATT_WARPS * 32) A.prefix[r] = pre[r];
+  const int64_t W = unit_prefix<ATT_WARPS * 32>(A, pre, wsum);
   const int64_t n = share_count(W, A.ctas);
   if ((int64_t)blockIdx.x >= n || W == 0) return;
   int64_t x, end;
-  if (W < (1 << 22)) {  // (32-bit divisions: n <= 1024)
-    x = (uint32_t)W * blockIdx.x / (uint32_t)n;
-    end = (uint32_t)W * (blockIdx.x + 1) / (uint32_t)n;
-  } else {
-    x = range_lo(W, n, blockIdx.x);
-    end = range_lo(W, n, blockIdx.x + 1);
-  }
+  share_bounds(W, n, x, end);
   int r = 0;
   for (int hi = A.R; hi - r > 1;) {  // the last r with pre[r] <= x
     const int mid = (r + hi) >> 1;
@@ -643,48 +486,45 @@ __global__ void __launch_bounds__(ATT_WARPS * 32, 2) kv8_attention_kernel(const 
   while (x < end) {
     while (pre[r + 1] <= x) ++r;
     const Req rq = load_req(A, r);
-    const int nb = rq.b1 - rq.b0, per_head = unit_groups(A, rq);
-    const int64_t in = x - pre[r];
-    const int unit = in < (1ll << 31) ? (int)((uint32_t)in / (uint32_t)nb) : (int)(in / nb);
-    const int b = (int)(in - (int64_t)unit * nb);
-    const int64_t left = end - x;
-    const int cnt = left < nb - b ? (int)left : nb - b;
-    K::segment(A, S, r, rq, unit / per_head, unit % per_head, rq.b0 + b, rq.b0 + b + cnt, cnt == nb,
+    int unit, c0, cnt;
+    if (!share_segment(A, rq, pre[r], x, end, unit, c0, cnt)) continue;
+    const int per_head = unit_groups(A, rq), h = per_head == 1 ? unit : unit / per_head;
+    K::segment(A, S, r, rq, h, unit - h * per_head, c0, c0 + cnt, cnt == rq.b1 - rq.b0,
                blockIdx.x + (int64_t)r * A.Hkv * A.nqc + unit);
-    x += cnt;
     __syncthreads();  // the next segment writes the shared records
   }
 }
 
-// Joins the records of one tile of 8 queries of a unit, in share order.  The
-// records of one query stand 2 KB and more apart and are few (a unit's
-// shares); what counts is that their loads go out together: PAR groups of
-// 8 hd / 4 threads each take every PAR-th record, 8 at a time.
+// Joins the records of a query, in share order.  They stand 4 KB and more
+// apart and are a unit's shares, two or three in a full batch and tens when one
+// request is spread over the machine: the time is that of one round trip to L2
+// if their loads go out together.  So PAR warps take a query, warp w of them
+// every PAR-th record, four at a time, each lane hd / 32 head dimensions.
 template <int DT, int HD, int PAR>
-__global__ void __launch_bounds__(2 * HD * PAR) kv8_join_kernel(const __grid_constant__ AttArgs A) {
-  constexpr int DQ = HD / 4, NT = 8 * DQ;
-  __shared__ float4 so[PAR > 1 ? PAR : 1][PAR > 1 ? NT : 1];
-  __shared__ float2 sml[PAR > 1 ? PAR : 1][8];
+__global__ void __launch_bounds__(256) kv8_join_kernel(const __grid_constant__ AttArgs A) {
+  constexpr int E = HD / 32;
+  __shared__ float so[8][HD];
+  __shared__ float2 sml[8];
   pdl_trigger();
   pdl_wait();
-  int bid = blockIdx.x;
-  const int tl = bid % A.nq;
-  bid /= A.nq;
-  const int qc = bid % A.nqc;
-  bid /= A.nqc;
-  const int h = bid % A.Hkv, r = bid / A.Hkv;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, par = warp % PAR;
+  const int nq8 = A.nq * 8;
+  uint32_t id = blockIdx.x * (8 / PAR) + warp / PAR;  // (request, head, group of tiles, query)
+  const uint32_t per_req = (uint32_t)A.Hkv * A.nqc * nq8;
+  const int r = (int)(id / per_req);
+  if (r >= A.R) return;  // (PAR = 1 only: a CTA's queries of one request are 8 / PAR times some)
+  id -= (uint32_t)r * per_req;
+  const int x = (int)(id % nq8), u = (int)(id / nq8), h = u / A.nqc, qc = u - h * A.nqc;
   const Req rq = load_req(A, r);
-  const int per_head = unit_groups(A, rq), nb = rq.b1 - rq.b0;
   const int64_t W = A.prefix[A.R], p0 = A.prefix[r];
-  if (qc >= per_head) return;
-  const int e = threadIdx.x % NT, grp = threadIdx.x / NT, d = e % DQ, qq = e / DQ;
-  const int qi = (qc * A.nq + tl) * 8 + qq;
-  const bool has = qi < rq.n * A.GH;
-  const int unit = h * per_head + qc;
-  float m = -INFINITY, l = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int per_head = unit_groups(A, rq), nb = rq.b1 - rq.b0;
+  const int qi = qc * nq8 + x, unit = h * per_head + qc;
+  if (qc >= per_head || qi >= rq.n * A.GH) return;
+  float m = -INFINITY, l = 0.f, acc[E];
+#pragma unroll
+  for (int k = 0; k < E; ++k) acc[k] = 0.f;
   if (nb > 0) {
-    const int64_t n = share_count(W, A.ctas), lo = p0 + (int64_t)unit * nb;
+    const int64_t n = share_count(W, A.ctas), lo = p0 + (int64_t)unit * (nb + UNIT_COST) + UNIT_COST;
     int i0, i1;
     if (W < (1 << 22)) {
       i0 = (int)owner32((uint32_t)W, (uint32_t)n, (uint32_t)lo);
@@ -694,63 +534,76 @@ __global__ void __launch_bounds__(2 * HD * PAR) kv8_join_kernel(const __grid_con
       i1 = (int)owner_of(W, n, lo + nb - 1);
     }
     if (i0 == i1) return;  // written at once
-    const int64_t u = (int64_t)r * A.Hkv * A.nqc + unit;
-    for (int i = i0 + grp; has && i <= i1; i += 8 * PAR) {
-      float2 ml[8];
-      float4 v[8];
+    const int64_t rec0 = ((int64_t)r * A.Hkv * A.nqc + unit) * nq8 + x;
+    for (int i = i0 + par; i <= i1; i += 4 * PAR) {
+      float2 ml[4];
+      float v[4][E];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int64_t at = (i + k * PAR + u) * (A.nq * 8) + tl * 8 + qq;
-        const bool in = i + k * PAR <= i1;
-        ml[k] = in ? __ldcg(reinterpret_cast<const float2*>(A.rec_ml) + at) : make_float2(-INFINITY, 0.f);
-        v[k] = in ? __ldcg(reinterpret_cast<const float4*>(A.rec_o + at * HD) + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < 4; ++k) {
+        const int j = i + k * PAR;
+        const int64_t at = rec0 + (int64_t)j * nq8;
+        ml[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[k][e] = 0.f;
+        if (j <= i1) {
+          ml[k] = __ldcg(reinterpret_cast<const float2*>(A.rec_ml) + at);
+          if (E == 4) {
+            const float4 f = __ldcg(reinterpret_cast<const float4*>(A.rec_o + at * HD) + lane);
+            v[k][0] = f.x; v[k][1] = f.y; v[k][E - 2] = f.z; v[k][E - 1] = f.w;
+          } else {
+            const float2 f = __ldcg(reinterpret_cast<const float2*>(A.rec_o + at * HD) + lane);
+            v[k][0] = f.x; v[k][1] = f.y;
+          }
+        }
       }
       float nm = m;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) nm = fmaxf(nm, ml[k].x);
+      for (int k = 0; k < 4; ++k) nm = fmaxf(nm, ml[k].x);
       const float ref = nm == -INFINITY ? 0.f : nm, f0 = exp2_fast(m - ref);
       l *= f0;
-      acc = make_float4(acc.x * f0, acc.y * f0, acc.z * f0, acc.w * f0);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] *= f0;
       m = nm;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < 4; ++k) {
         const float f = exp2_fast(ml[k].x - ref);
         l = fmaf(f, ml[k].y, l);
-        acc.x = fmaf(f, v[k].x, acc.x);
-        acc.y = fmaf(f, v[k].y, acc.y);
-        acc.z = fmaf(f, v[k].z, acc.z);
-        acc.w = fmaf(f, v[k].w, acc.w);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(f, v[k][e], acc[e]);
       }
     }
   }
-  if (PAR > 1) {
-    so[PAR > 1 ? grp : 0][PAR > 1 ? e : 0] = acc;
-    if (d == 0) sml[PAR > 1 ? grp : 0][qq] = make_float2(m, l);
+  if (PAR > 1) {  // (all warps of the CTA are here: they share the query)
+#pragma unroll
+    for (int e = 0; e < E; ++e) so[warp][lane * E + e] = acc[e];
+    if (lane == 0) sml[warp] = make_float2(m, l);
     __syncthreads();
-    if (grp > 0) return;
+    if (warp > 0) return;
     m = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < PAR; ++k) m = fmaxf(m, sml[k][qq].x);
+    for (int k = 0; k < 8; ++k) m = fmaxf(m, sml[k].x);
     const float ref = m == -INFINITY ? 0.f : m;
     l = 0.f;
-    acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < PAR; ++k) {
-      const float f = exp2_fast(sml[k][qq].x - ref);
-      const float4 v = so[PAR > 1 ? k : 0][PAR > 1 ? e : 0];
-      l = fmaf(f, sml[k][qq].y, l);
-      acc.x = fmaf(f, v.x, acc.x);
-      acc.y = fmaf(f, v.y, acc.y);
-      acc.z = fmaf(f, v.z, acc.z);
-      acc.w = fmaf(f, v.w, acc.w);
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float f = exp2_fast(sml[k].x - ref);
+      l = fmaf(f, sml[k].y, l);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(f, so[k][lane * E + e], acc[e]);
     }
   }
-  if (!has) return;
-  const int row = qi / A.GH, head = h * A.GH + qi % A.GH;
+  const int row = group_row(A, qi), head = h * A.GH + qi - row * A.GH;
   const float inv = l != 0.f ? 1.f / l : 0.f;
-  store_elem4<DT>(A.out, (int64_t)(rq.row0 + row) * A.out_stride + (int64_t)head * HD + 4 * d,
-                  make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-  if (d == 0 && A.lse) A.lse[(int64_t)(rq.row0 + row) * A.Hq + head] = (m + log2f(l)) * LN2;
+  const int64_t at = (int64_t)(rq.row0 + row) * A.out_stride + (int64_t)head * HD + lane * E;
+  if (E == 4) {
+    store_elem4<DT>(A.out, at, make_float4(acc[0] * inv, acc[1] * inv, acc[E - 2] * inv, acc[E - 1] * inv));
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) store_elem<DT>(A.out, at + e, acc[e] * inv);
+  }
+  if (lane == 0 && A.lse) A.lse[(int64_t)(rq.row0 + row) * A.Hq + head] = (m + log2f(l)) * LN2;
 }
 
 // ------------------------------------------------------------------ host
@@ -776,6 +629,7 @@ constexpr int WHOLE_BLOCKS = 32;
 
 struct AttPlan {
   int32_t nq, nqc, whole, ctas, deep;  // deep: a unit may have many shares
+  bool tc;                             // the tcgen05 kernel
   int64_t rec_ml, prefix, total;       // workspace offsets
 };
 
@@ -788,13 +642,15 @@ int check_sizes(int32_t H_q, int32_t H_kv, int32_t hd, int32_t R, int32_t T, int
   return DDL_OK;
 }
 
-int att_plan(int32_t H_q, int32_t H_kv, int32_t hd, int32_t R, int32_t max_rows, int32_t max_len, AttPlan& p) {
+int att_plan(bool tc, int32_t H_q, int32_t H_kv, int32_t hd, int32_t R, int32_t max_rows, int32_t max_len,
+             AttPlan& p) {
   int sms = 0;
   const int st = att_sms(sms);
   if (st) return st;
   const int tiles = (max_rows * (H_q / H_kv) + 7) / 8;
   p.nq = 1;
-  while (p.nq < ATT_WARPS && p.nq < tiles) p.nq *= 2;
+  p.tc = tc;
+  while (p.nq < (tc ? 4 : ATT_WARPS) && p.nq < tiles) p.nq *= 2;
   p.nqc = (tiles + p.nq - 1) / p.nq;
   const int64_t blocks = ((int64_t)max_len + 15) / 16, units = (int64_t)R * H_kv * p.nqc;
   p.whole = blocks <= WHOLE_BLOCKS;
@@ -803,7 +659,7 @@ int att_plan(int32_t H_q, int32_t H_kv, int32_t hd, int32_t R, int32_t max_rows,
   p.ctas = (int32_t)units;
   p.deep = 0;
   if (p.whole) return DDL_OK;
-  const int64_t most = (units * blocks + MIN_SHARE - 1) / MIN_SHARE;
+  const int64_t most = (units * (blocks + UNIT_COST) + MIN_SHARE - 1) / MIN_SHARE;
   p.ctas = (int32_t)(most < 2 * sms ? most : 2 * sms);
   if (p.ctas > 1024) return DDL_ERR_UNSUPPORTED;  // (the kernels' 32-bit share arithmetic)
   p.deep = units * 8 <= p.ctas;
@@ -829,8 +685,8 @@ const void* att_fn(int dt, int hd, bool ex) {
 }
 template <int DT>
 const void* join_fn(int hd, bool deep) {
-  if (hd == 128) return deep ? (const void*)kv8_join_kernel<DT, 128, 4> : (const void*)kv8_join_kernel<DT, 128, 1>;
-  return deep ? (const void*)kv8_join_kernel<DT, 64, 4> : (const void*)kv8_join_kernel<DT, 64, 1>;
+  if (hd == 128) return deep ? (const void*)kv8_join_kernel<DT, 128, 8> : (const void*)kv8_join_kernel<DT, 128, 1>;
+  return deep ? (const void*)kv8_join_kernel<DT, 64, 8> : (const void*)kv8_join_kernel<DT, 64, 1>;
 }
 
 }  // namespace
@@ -841,9 +697,10 @@ using namespace ddl;
 extern "C" size_t ddl_kv8_attention_workspace_bytes(int32_t H_q, int32_t H_kv, int32_t head_dim, int32_t R, int32_t T,
                                                     int32_t max_rows, int32_t max_len) {
   if (check_sizes(H_q, H_kv, head_dim, R, T, max_rows, max_len)) return 0;
-  AttPlan p;
-  if (att_plan(H_q, H_kv, head_dim, R, max_rows, max_len, p)) return 0;
-  return (size_t)p.total;
+  AttPlan p, q;  // of either kernel: the code type is not known here
+  if (att_plan(false, H_q, H_kv, head_dim, R, max_rows, max_len, p)) return 0;
+  if (att_plan(true, H_q, H_kv, head_dim, R, max_rows, max_len, q)) return 0;
+  return (size_t)(p.total > q.total ? p.total : q.total);
 }
 
 extern "C" int ddl_kv8_attention(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, int32_t head_dim, ddl_dtype dtype,
@@ -870,7 +727,9 @@ extern "C" int ddl_kv8_attention(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, i
                         (const void*)bad_out, (const void*)opts->slopes})
     if ((uintptr_t)p & 3u) return DDL_ERR_ALIGN;
   AttPlan pl;
-  if ((st = att_plan(H_q, H_kv, head_dim, R, max_rows, max_len, pl))) return st;
+  const int64_t pool_rows = kv->pages * kv->page_size * H_kv;
+  const bool tc = kv->type == DDL_KV8_E4M3 && head_dim == 128 && pool_rows < (1ll << 31);
+  if ((st = att_plan(tc, H_q, H_kv, head_dim, R, max_rows, max_len, pl))) return st;
   if (ws_bytes < (size_t)pl.total) return DDL_ERR_WORKSPACE;
   AttArgs a;
   a.k = kv->k;
@@ -899,6 +758,7 @@ extern "C" int ddl_kv8_attention(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, i
   a.Hq = H_q;
   a.Hkv = H_kv;
   a.GH = H_q / H_kv;
+  a.gmul = (65536 + a.GH - 1) / a.GH;
   a.hd = head_dim;
   a.pshift = log2_of(kv->page_size);
   a.per = pages_per_seq;
@@ -909,18 +769,23 @@ extern "C" int ddl_kv8_attention(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, i
   a.nq = pl.nq;
   a.nqc = pl.nqc;
   const bool ex = opts->softcap > 0.f || opts->slopes;
-  const void* fn = kv->type == DDL_KV8_E4M3 ? att_fn<DDL_KV8_E4M3>(dtype, head_dim, ex)
-                                            : att_fn<DDL_KV8_INT8>(dtype, head_dim, ex);
+  const void* fn = nullptr;
   void* args[] = {&a};
-  const size_t smem = pl.whole ? 0 : (size_t)(R + 1) * 8;
-  if (smem > 8192 && (st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                            (DDL_KV8_MAX_REQS + 1) * 8))))
-    return st;  // (beside the static 34 KB more than 48 KB)
-  st = cuda_status(launch_pdl(fn, dim3((unsigned)pl.ctas), dim3(ATT_WARPS * 32), args, smem, (cudaStream_t)stream));
+  if (tc) {
+    st = kv8_tc_launch(a, dtype, ex, pool_rows, stream);
+  } else {
+    fn = kv->type == DDL_KV8_E4M3 ? att_fn<DDL_KV8_E4M3>(dtype, head_dim, ex) : att_fn<DDL_KV8_INT8>(dtype, head_dim, ex);
+    const size_t smem = pl.whole ? 0 : (size_t)(R + 1) * 8;
+    if (smem > 8192 && (st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                              (DDL_KV8_MAX_REQS + 1) * 8))))
+      return st;  // (beside the static 34 KB more than 48 KB)
+    st = cuda_status(launch_pdl(fn, dim3((unsigned)pl.ctas), dim3(ATT_WARPS * 32), args, smem, (cudaStream_t)stream));
+  }
   if (st || pl.whole) return st;
   fn = dtype == DDL_T_F32    ? join_fn<DDL_T_F32>(head_dim, pl.deep)
        : dtype == DDL_T_BF16 ? join_fn<DDL_T_BF16>(head_dim, pl.deep)
                              : join_fn<DDL_T_F16>(head_dim, pl.deep);
-  return cuda_status(launch_pdl(fn, dim3((unsigned)(R * H_kv * pl.nqc * pl.nq)),
-                                dim3((unsigned)(2 * head_dim * (pl.deep ? 4 : 1))), args, 0, (cudaStream_t)stream));
+  const int64_t queries = (int64_t)R * H_kv * pl.nqc * pl.nq * 8;
+  return cuda_status(launch_pdl(fn, dim3((unsigned)(pl.deep ? queries : queries / 8)), dim3(256), args, 0,
+                                (cudaStream_t)stream));
 }

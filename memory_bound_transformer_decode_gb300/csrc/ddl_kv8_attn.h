@@ -1,0 +1,231 @@
+// ddl_kv8_attn.h -- what the two attention kernels over the 8-bit cache (warp
+// MMAs, tcgen05) and the kernel that joins their records share: arguments,
+// requests, the split into shares, elements of rows.
+#pragma once
+#include <cuda.h>
+
+#include "ddl_kv8.h"
+
+namespace ddl {
+
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+
+struct AttArgs {
+  const uint8_t *k, *v;
+  const float *ks, *vs;
+  const int32_t *q_off, *kv_len, *table;
+  const void* q;
+  void* out;
+  float* lse;
+  int32_t* bad;
+  float *rec_o, *rec_ml;  // records [share + unit][query of the unit][hd], [..][2]
+  int64_t* prefix;        // [R + 1] blocks of all units before each request
+  const float* slopes;
+  int64_t pages, q_stride, out_stride;
+  float scale, softcap;
+  int32_t window;
+  int32_t R, T, Hq, Hkv, GH, gmul, hd, pshift, per, max_rows, max_len;
+  int32_t whole;    // one CTA a unit, else shares
+  int32_t ctas;     // shares at most
+  int32_t nq, nqc;  // query tiles of 8 a unit has (a power of two <= 8), units over a request's query tiles
+};
+
+// Shares.  Beginning and ending a unit (Q, the join of the warps, the record)
+// costs a CTA about as much as UNIT_COST blocks, so a unit of nb blocks weighs
+// UNIT_COST + nb, its block j standing at UNIT_COST + j; the weights of all
+// units, end to end, are cut (range_lo, owner_of) into equal parts of at least
+// MIN_SHARE.
+constexpr int UNIT_COST = 24, MIN_SHARE = UNIT_COST + 16;
+__device__ __forceinline__ int64_t share_count(int64_t W, int ctas) {
+  const int64_t most = (W + MIN_SHARE - 1) / MIN_SHARE;
+  return most < 1 ? 1 : most < ctas ? most : ctas;
+}
+
+__device__ __forceinline__ void share_bounds(int64_t W, int64_t n, int64_t& x, int64_t& end) {
+  if (W < (1 << 22)) {  // (32-bit divisions: n <= 1024)
+    x = (uint32_t)W * blockIdx.x / (uint32_t)n;
+    end = (uint32_t)W * (blockIdx.x + 1) / (uint32_t)n;
+  } else {
+    x = range_lo(W, n, blockIdx.x);
+    end = range_lo(W, n, blockIdx.x + 1);
+  }
+}
+
+// A request's rows and keys as the kernels compute them (clamped to what the
+// launch and the tables allow).
+struct Req {
+  int32_t row0, n, len;  // first row of q, rows, tokens
+  int32_t p0;            // position of its first row (negative: it has no keys)
+  int32_t b0, b1;        // blocks of 16 tokens that any of its rows sees: [b0, b1)
+  bool bad;
+};
+__device__ __forceinline__ Req load_req(const AttArgs& A, int r) {
+  Req q;
+  int64_t row0 = r, n = 1;
+  if (A.q_off) {
+    row0 = A.q_off[r];
+    n = (int64_t)A.q_off[r + 1] - row0;
+  }
+  int64_t len = A.kv_len[r];
+  const int64_t cap = (int64_t)A.per << A.pshift;
+  q.bad = false;
+  if (row0 < 0 || n < 0 || row0 + n > A.T) {
+    q.bad = true;
+    n = 0;
+    row0 = 0;
+  }
+  if (len < 0 || len > A.max_len || len > cap) {
+    q.bad = true;
+    len = len < 0 ? 0 : len;
+    len = len > A.max_len ? A.max_len : len;
+    len = len > cap ? cap : len;
+  }
+  q.row0 = (int32_t)row0;
+  q.len = (int32_t)len;
+  q.p0 = (int32_t)(len - n);  // (n <= T)
+  int64_t lo = A.window > 0 ? len - n - A.window + 1 : 0;
+  lo = lo < 0 ? 0 : lo;
+  if (n > A.max_rows) {
+    q.bad = true;
+    n = A.max_rows;  // its first rows
+  }
+  q.n = (int32_t)n;
+  q.b0 = (int32_t)(lo >> 4);
+  q.b1 = n > 0 ? (int32_t)((len + 15) >> 4) : q.b0;
+  if (q.b1 < q.b0) q.b1 = q.b0;
+  return q;
+}
+
+// Units of request q: K/V heads times groups of query tiles.
+__device__ __forceinline__ int unit_groups(const AttArgs& A, const Req& q) {
+  return (q.n * A.GH + 8 * A.nq - 1) / (8 * A.nq);
+}
+
+// Byte mask of the e4m3 NaN codes (low 7 bits all set) of four codes.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  const uint32_t top = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+  return (top >> 7) * 255u;
+}
+
+// Weight of request q's units.
+__device__ __forceinline__ int64_t req_weight(const AttArgs& A, const Req& q) {
+  const int nb = q.b1 - q.b0;
+  return nb > 0 ? (int64_t)(nb + UNIT_COST) * A.Hkv * unit_groups(A, q) : 0;
+}
+// Row of a request that its query qi (row * group + head of the group) belongs to: qi / GH, qi < 512.
+__device__ __forceinline__ int group_row(const AttArgs& A, int qi) { return (int)((uint32_t)qi * (uint32_t)A.gmul >> 16); }
+
+// Weights before each request into pre[0 .. R] (every CTA adds them up: R <=
+// 4096 lengths from L2); returns their sum.  CTA 0 leaves them for the join
+// and reports bad requests.  wsum: a word per warp.
+template <int NT>
+__device__ __forceinline__ int64_t unit_prefix(const AttArgs& A, int64_t* pre, int64_t* wsum) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int64_t base = 0;
+  if (A.R <= 32) {  // each warp for itself, without a barrier (all write the same values)
+    int64_t w = 0;
+    if (lane < A.R) {
+      const Req rq = load_req(A, lane);
+      w = req_weight(A, rq);
+      if (blockIdx.x == 0 && warp == 0 && rq.bad && A.bad) atomicOr(A.bad, 1);
+    }
+    int64_t inc = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(FULL, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane < A.R) pre[lane + 1] = inc;
+    if (lane == 0) pre[0] = 0;
+    base = __shfl_sync(FULL, inc, 31);
+    __syncwarp();
+  } else {
+    for (int r0 = 0; r0 < A.R; r0 += NT) {
+      const int r = r0 + tid;
+      int64_t w = 0;
+      if (r < A.R) {
+        const Req rq = load_req(A, r);
+        w = req_weight(A, rq);
+        if (blockIdx.x == 0 && rq.bad && A.bad) atomicOr(A.bad, 1);
+      }
+      int64_t inc = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(FULL, inc, o);
+        if (lane >= o) inc += y;
+      }
+      if (lane == 31) wsum[warp] = inc;
+      __syncthreads();
+      int64_t before = base, all = 0;
+#pragma unroll
+      for (int v = 0; v < NT / 32; ++v) {
+        if (v < warp) before += wsum[v];
+        all += wsum[v];
+      }
+      if (r < A.R) pre[r] = before + inc - w;
+      base += all;
+      __syncthreads();
+    }
+    if (tid == 0) pre[A.R] = base;
+    __syncthreads();
+  }
+  if (blockIdx.x == 0)
+    for (int r = tid; r <= A.R; r += NT) A.prefix[r] = pre[r];
+  return base;
+}
+
+// The unit of request q (weights from p0 on) at weight x and the run of its
+// blocks up to `end`: unit, first block, count; moves x past it.  False if the
+// run has no blocks.
+__device__ __forceinline__ bool share_segment(const AttArgs& A, const Req& q, int64_t p0, int64_t& x, int64_t end,
+                                              int& unit, int& first, int& count) {
+  const int nb = q.b1 - q.b0, w = nb + UNIT_COST;
+  const int64_t in = x - p0;
+  unit = in < (1ll << 31) ? (int)((uint32_t)in / (uint32_t)w) : (int)(in / w);
+  const int at = (int)(in - (int64_t)unit * w);
+  const int to = end - x < w - at ? at + (int)(end - x) : w;
+  const int b0 = at > UNIT_COST ? at - UNIT_COST : 0, b1 = to > UNIT_COST ? to - UNIT_COST : 0;
+  first = q.b0 + b0;
+  count = b1 - b0;
+  x += to - at;
+  return count > 0;
+}
+
+// Four neighbouring elements (8- or 16-byte aligned).
+template <int DT>
+__device__ __forceinline__ float4 load_elem4(const void* p, int64_t i) {
+  if (DT == DDL_T_F32) return *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + i);
+  const uint2 u = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p) + i);
+  if (DT == DDL_T_BF16) return make_float4(bf16lo_f32(u.x), bf16hi_f32(u.x), bf16lo_f32(u.y), bf16hi_f32(u.y));
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+template <int DT>
+__device__ __forceinline__ void store_elem4(void* p, int64_t i, float4 v) {
+  if (DT == DDL_T_F32) {
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + i) = v;
+  } else {
+    uint2 u;
+    if (DT == DDL_T_BF16) u = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    else u = make_uint2(pack_f16x2(v.x, v.y), pack_f16x2(v.z, v.w));
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p) + i) = u;
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void store_elem(void* p, int64_t i, float v) {
+  if (DT == DDL_T_F32) reinterpret_cast<float*>(p)[i] = v;
+  else if (DT == DDL_T_BF16) reinterpret_cast<uint16_t*>(p)[i] = f32_to_bf16_bits(v);
+  else reinterpret_cast<__half*>(p)[i] = __float2half_rn(v);
+}
+
+// tanh from its definition 1 - 2 / (e^{2x} + 1): an absolute error of a few
+// 2^-24, which times the cap is the score's own fp32 rounding.
+__device__ __forceinline__ float cap_tanh(float x) { return 1.f - __fdividef(2.f, __expf(2.f * x) + 1.f); }
+
+// The tcgen05 kernel (e4m3, head_dim 128): rows of the pool's view < 2^31.
+int kv8_tc_launch(const AttArgs& a, int dtype, bool ex, int64_t rows, void* stream);
+
+}  // namespace ddl

@@ -1,0 +1,692 @@
+// ddl_kv8_tc.cu -- attention over the 8-bit paged cache on the 5th-generation
+// tensor cores: e4m3 codes, head_dim 128 (ddl_kv8_attn.cu has the mathematics,
+// the units and shares, and the kernel for int8 codes and head_dim 64).
+//
+// The codes are never converted: K and V tiles of 128 tokens go by TMA from
+// the pages into shared memory and are the A operands of kind::f8f6f4 MMAs,
+//     S^T [128 tokens x N] = K [tokens x hd] Q^T,
+//     O^T [128 head dims x N] += V^T [hd x tokens] P^T,
+// with V read as an M-major operand, so that nothing is transposed either.
+// The warp-MMA kernel spends most of its issue slots on turning codes into
+// fp16 fragments (about 370 instructions a warp per 16 tokens and 8 queries,
+// bound by them and not by HBM); here 128 tokens and 8 queries cost four warps
+// about 200 each.
+//
+// Q and P, which are not e4m3, are split into e4m3 limbs, each the rounding of
+// what the ones before leave: a limb holds 4 significant bits, so bf16 is two
+// limbs exactly.  The B operand has 16 columns per 8 queries: group A holds
+// limbs 1 .. L (one MMA pass each, summed in the accumulator), group B the
+// next L, scaled by 16^L so that e4m3's narrow range does not cut them off, in
+// the same passes.  L = 2 for 16-bit rows (Q 2^-16, P three limbs: 2^-12, below
+// the output's own rounding), 3 for fp32 rows (2^-24).  What falls below
+// e4m3's smallest subnormal in group B is 2^-26 of a row's largest q and 2^-25
+// of the largest weight (L = 2).
+//
+// Roles: one or two warpgroups softmax (thread = token of the tile, then head
+// dimension of the output; 8 or 16 queries each), a warp copies, a warp issues
+// MMAs.  Bounds: HBM for one tile of 8
+// queries, softmax issue slots for many.
+#include <cuda_bf16.h>
+#include <cudaTypedefs.h>
+
+#include "ddl_kv8_attn.h"
+
+namespace ddl {
+namespace {
+
+constexpr int TOK = 128, TBLK = TOK / KV8_BLOCK;  // tokens and blocks of a tile
+constexpr uint32_t KBYTES = TOK * 128;
+
+// P carries 2^7; with the running maximum lagging by less than 2^1 it stays
+// within 2^8 <= 448.
+constexpr float TP_SCALE = 128.f, T_LAG = 1.f;
+
+struct TcAtt {
+  AttArgs A;
+  uint64_t wait_ns;
+  alignas(64) CUtensorMap kmap, vmap;
+};
+
+template <int NT, int L>
+struct Geo {
+  static constexpr int STAGES = NT == 1 ? 3 : 2;
+  static constexpr int NQ = 8 * NT;             // queries
+  static constexpr int QW = NT == 1 ? 8 : 16;   // of a softmax thread
+  static constexpr int WG = NQ / QW;            // softmax warpgroups
+  static constexpr int THREADS = 128 * WG + 64;
+  static constexpr int N = 16 * NT;             // B columns
+  static constexpr uint32_t OPB = NT * 2048u;   // bytes of one pass's Q or P operand
+  static constexpr uint32_t Q_OFF = STAGES * 2 * KBYTES, P_OFF = Q_OFF + L * OPB, SH_OFF = P_OFF + L * OPB;
+  static constexpr uint32_t COLS = NT == 1 ? 64 : NT == 2 ? 128 : 256;  // S twice, O: 48 NT columns
+};
+
+struct Meta {  // of a stage's tile
+  float ks[TBLK], vs[TBLK];
+  float vmax;
+  uint32_t ok;  // bit b: block b is there
+};
+
+template <int NT, int L>
+struct Shared {
+  Meta meta[Geo<NT, L>::STAGES];
+  alignas(16) float cf[8 * NT], slope[8 * NT], m[8 * NT], al[8 * NT];
+  int32_t hi[8 * NT], lo[8 * NT];
+  float wred[4][8 * NT];
+  uint32_t nan[2][4];
+  uint64_t fullk[3], fullv[3], empty[3], sfull[2], pfull, pvdone, qfull, fin;
+  int64_t wsum[12];
+  uint32_t tslot;
+  int abort;
+};
+
+// Operand descriptor: layout 0 no swizzle, 2 the 128-byte swizzle.
+__device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo, uint32_t sbo, uint32_t layout) {
+  return umma_sdesc(addr, lbo, sbo) | ((uint64_t)layout << 61);
+}
+// kind::f8f6f4 with e4m3 operands and fp32 accumulators.
+__device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+// Barriers of one softmax warpgroup (1 + wg) and of all of them (3, `n` threads),
+// and the same with an OR of a predicate.
+__device__ __forceinline__ void ssync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+__device__ __forceinline__ bool ssync_or(int id, int n, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbar.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(n), "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+// Largest of the warp's values (a NaN counts as the largest).
+__device__ __forceinline__ float warp_fmax(float x) {
+  const int b = __float_as_int(x), k = b ^ ((b >> 31) & 0x7fffffff);  // ordered as the values
+  const int t = __reduce_max_sync(FULL, k);
+  return __int_as_float(t ^ ((t >> 31) & 0x7fffffff));
+}
+
+// Eight values as e4m3 codes (byte i = value i), and what they leave.
+__device__ __forceinline__ uint2 limb8(float (&v)[8], bool rest) {
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t a = f32x2_e4m3x2(v[4 * i], v[4 * i + 1]), b = f32x2_e4m3x2(v[4 * i + 2], v[4 * i + 3]);
+    w[i] = __byte_perm(a, b, 0x5410);
+    if (rest) {
+      uint32_t lo, hi;
+      e4m3x4_f16x2(w[i], lo, hi);
+      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+      const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+      v[4 * i] -= x.x;
+      v[4 * i + 1] -= x.y;
+      v[4 * i + 2] -= y.x;
+      v[4 * i + 3] -= y.y;
+    }
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// A CTA's segments: runs of blocks of one unit.
+struct Segs {
+  int64_t x, end;
+  int r;
+  // the current segment
+  Req rq;
+  int h, qc, c0, c1;
+  bool direct;
+  int64_t rec;
+  __device__ __forceinline__ bool next(const AttArgs& A, const int64_t* pre) {
+    if (x >= end) return false;
+    if (A.whole) {
+      int bid = blockIdx.x;
+      qc = bid % A.nqc;
+      bid /= A.nqc;
+      h = bid % A.Hkv;
+      r = bid / A.Hkv;
+      rq = load_req(A, r);
+      x = end;
+      if (qc >= unit_groups(A, rq)) return false;
+      c0 = rq.b0;
+      c1 = rq.b1;
+      direct = true;
+      rec = 0;
+      return true;
+    }
+    for (;;) {
+      while (pre[r + 1] <= x) ++r;
+      rq = load_req(A, r);
+      int unit, cnt;
+      if (!share_segment(A, rq, pre[r], x, end, unit, c0, cnt)) {
+        if (x >= end) return false;
+        continue;
+      }
+      const int per_head = unit_groups(A, rq);
+      h = per_head == 1 ? unit : unit / per_head;
+      qc = unit - h * per_head;
+      c1 = c0 + cnt;
+      direct = cnt == rq.b1 - rq.b0;
+      rec = blockIdx.x + (int64_t)r * A.Hkv * A.nqc + unit;
+      return true;
+    }
+  }
+};
+
+template <int DT, bool EX, int NT>
+__global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) kv8_tc_kernel(const __grid_constant__ TcAtt P) {
+  constexpr int L = DT == DDL_T_F32 ? 3 : 2;
+  constexpr int PL = DT == DDL_T_F32 ? 6 : 3;  // limbs of P
+  constexpr float BSCALE = DT == DDL_T_F32 ? 4096.f : 256.f;  // 16^L
+  using G = Geo<NT, L>;
+  constexpr int NQ = G::NQ, QW = G::QW, WG = G::WG, NS = 128 * WG;  // NS: softmax threads
+  constexpr int CW = 4 * WG, MW = 4 * WG + 1;                         // the copying and the MMA warp
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Shared<NT, L>& S = *reinterpret_cast<Shared<NT, L>*>(smem + G::SH_OFF);
+  int64_t* const pre = reinterpret_cast<int64_t*>(smem + G::SH_OFF + ((sizeof(Shared<NT, L>) + 15) & ~size_t(15)));
+  const AttArgs& A = P.A;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t sb = smem_addr(smem);
+  const uint32_t fullk = smem_addr(S.fullk), fullv = smem_addr(S.fullv), empty = smem_addr(S.empty);
+  const uint32_t sfull = smem_addr(S.sfull), pfull = smem_addr(&S.pfull), pvdone = smem_addr(&S.pvdone);
+  const uint32_t qfull = smem_addr(&S.qfull);
+  pdl_trigger();
+  if (tid == 0) {
+    for (int i = 0; i < G::STAGES; ++i) {
+      mbar_init(fullk + 8 * i, 1);
+      mbar_init(fullv + 8 * i, 1);
+      mbar_init(empty + 8 * i, 1);
+    }
+    mbar_init(sfull, 1);
+    mbar_init(sfull + 8, 1);
+    mbar_init(pfull, 4 * WG);
+    mbar_init(pvdone, 1);
+    mbar_init(qfull, 4 * WG);
+    mbar_init(smem_addr(&S.fin), 1);
+    S.abort = 0;
+  }
+  mbar_init_fence();
+  if (warp == MW) tmem_alloc(smem_addr(&S.tslot), G::COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = S.tslot, tO = tm + 2 * G::N;
+  pdl_wait();
+  Segs first;
+  first.x = 0;
+  first.end = 1;
+  first.r = 0;
+  if (!A.whole) {
+    const int64_t W = unit_prefix<G::THREADS>(A, pre, S.wsum);
+    const int64_t n = share_count(W, A.ctas);
+    if ((int64_t)blockIdx.x >= n || W == 0) {
+      first.end = 0;
+    } else {
+      share_bounds(W, n, first.x, first.end);
+      for (int hi = A.R; hi - first.r > 1;) {  // the last r with pre[r] <= x
+        const int mid = (first.r + hi) >> 1;
+        if (pre[mid] <= first.x) first.r = mid;
+        else hi = mid;
+      }
+    }
+  } else if (tid == 0 && A.bad) {
+    if (load_req(A, blockIdx.x / A.nqc / A.Hkv).bad) atomicOr(A.bad, 1);
+  }
+  auto fail = [&]() {
+    if (lane == 0 && A.bad) atomicOr(A.bad, 2);
+    *reinterpret_cast<volatile int*>(&S.abort) = 1;
+  };
+  auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+      if (__all_sync(FULL, mbar_try_wait(bar, parity))) return true;
+      if ((it & 1023u) == 0) {
+        const uint64_t now = __shfl_sync(FULL, globaltimer(), 0);
+        if (t0 == 0) t0 = now;
+        if (now - t0 > P.wait_ns || __any_sync(FULL, *reinterpret_cast<volatile int*>(&S.abort))) {
+          fail();
+          return false;
+        }
+      }
+    }
+  };
+
+  if (warp == CW) {  // -------------------------------------------------- copies
+    const uint64_t policy = A.nqc == 1 ? policy_evict_first() : policy_evict_normal();
+    const int bshift = A.pshift - 4, bmask = (1 << bshift) - 1;
+    uint32_t tc = 0;
+    bool ok = true;
+    Segs s = first;
+    while (ok && s.next(A, pre)) {
+      const int nblk = s.c1 - s.c0;
+      auto page_of = [&](int i) -> int32_t {  // page of block i of the segment, -1: none
+        if (i >= nblk) return -1;
+        const int32_t page = A.table[(int64_t)s.r * A.per + ((s.c0 + i) >> bshift)];
+        if (page >= 0 && page < A.pages) return page;
+        if (A.bad) atomicOr(A.bad, 1);
+        return -1;
+      };
+      int32_t page = page_of(lane), page_n = -1;
+      for (int g0 = 0; ok && g0 < nblk; g0 += 32) {  // lane l: block g0 + l
+        const int sub = (s.c0 + g0 + lane) & bmask;
+        const int64_t head = (int64_t)page * A.Hkv + s.h;
+        float ks = 0.f, vs = 0.f;
+        if (page >= 0) {
+          ks = A.ks[(head << bshift) + sub];
+          vs = A.vs[(head << bshift) + sub];
+        }
+        const int32_t row = (int32_t)((head << A.pshift) + (sub << 4));
+        page_n = page_of(g0 + 32 + lane);
+        float vmax = vs;  // of the lane's tile
+#pragma unroll
+        for (int o = 1; o < TBLK; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(FULL, vmax, o));
+        const uint32_t there = __ballot_sync(FULL, page >= 0);
+        for (int t = 0; t < 4 && g0 + t * TBLK < nblk; ++t, ++tc) {
+          const uint32_t st = tc % G::STAGES, k = tc / G::STAGES;
+          if (k > 0 && !wait(empty + 8 * st, (k - 1) & 1)) {
+            ok = false;
+            break;
+          }
+          const uint32_t okm = (there >> (t * TBLK)) & 0xffu, bytes = (uint32_t)__popc(okm) * 2048u;
+          const bool mine = (lane / TBLK) == t;
+          if (mine) {
+            S.meta[st].ks[lane % TBLK] = ks;
+            S.meta[st].vs[lane % TBLK] = vs;
+            if (lane % TBLK == 0) {
+              S.meta[st].vmax = vmax;
+              S.meta[st].ok = okm;
+            }
+          }
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive_expect_tx(fullk + 8 * st, bytes);
+            mbar_arrive_expect_tx(fullv + 8 * st, bytes);
+          }
+          __syncwarp();
+          if (mine && page >= 0) {
+            const uint32_t dst = sb + st * 2 * KBYTES + (lane % TBLK) * 2048u;
+            tensor2d_g2s(dst, &P.kmap, 0, row, fullk + 8 * st, policy);
+            tensor2d_g2s(dst + KBYTES, &P.vmap, 0, row, fullv + 8 * st, policy);
+          }
+        }
+        page = page_n;
+      }
+    }
+    // copies in flight land before the CTA leaves (bounded)
+    if (lane == 0)
+      for (uint32_t j = tc > G::STAGES ? tc - G::STAGES : 0; j < tc; ++j) {
+        if (!mbar_wait_thread(fullk + 8 * (j % G::STAGES), (j / G::STAGES) & 1, P.wait_ns)) break;
+        if (!mbar_wait_thread(fullv + 8 * (j % G::STAGES), (j / G::STAGES) & 1, P.wait_ns)) break;
+      }
+  } else if (warp == MW) {  // ------------------------------------------ MMA issue
+    constexpr uint32_t IDESC_S = (1u << 4) | ((uint32_t)(G::N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+    constexpr uint32_t IDESC_O = IDESC_S | (1u << 15) | (1u << 16);  // A and B M/N-major
+    const uint64_t kd = sdesc(sb, 16, 1024, 2), vd = sdesc(sb + KBYTES, 16384, 1024, 2);
+    const uint64_t qd = sdesc(sb + G::Q_OFF, 16, 1024, 2), pd = sdesc(sb + G::P_OFF, 128, 2048, 0);
+    uint32_t tc = 0, sg = 0;
+    bool ok = true;
+    Segs s = first;
+    auto scores = [&](uint32_t i) -> bool {  // S of tile i
+      const uint32_t st = i % G::STAGES;
+      if (!wait(fullk + 8 * st, (i / G::STAGES) & 1)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t a = kd + (uint64_t)(st * (2 * KBYTES >> 4));
+        const uint32_t d = tm + (i & 1) * G::N;
+#pragma unroll
+        for (int p = 0; p < L; ++p)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)  // 32 head dimensions each
+            umma_f8(d, a + 2 * k, qd + (uint64_t)(p * (G::OPB >> 4)) + 2 * k, IDESC_S, p + k > 0 ? 1u : 0u);
+        umma_commit(sfull + 8 * (i & 1));
+      }
+      __syncwarp();
+      return true;
+    };
+    while (ok && s.next(A, pre)) {
+      const int nt = (s.c1 - s.c0 + TBLK - 1) / TBLK;
+      if (!(ok = wait(qfull, sg & 1))) break;
+      ++sg;
+      if (nt > 0) ok = scores(tc);
+      for (int i = 0; ok && i < nt; ++i, ++tc) {
+        if (i + 1 < nt && !(ok = scores(tc + 1))) break;
+        const uint32_t st = tc % G::STAGES;
+        if (!(ok = wait(fullv + 8 * st, (tc / G::STAGES) & 1))) break;
+        if (!(ok = wait(pfull, tc & 1))) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t a = vd + (uint64_t)(st * (2 * KBYTES >> 4));
+#pragma unroll
+          for (int p = 0; p < L; ++p)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)  // 32 tokens each
+              umma_f8(tO, a + k * (4096 >> 4), pd + (uint64_t)(p * (G::OPB >> 4)) + k * (512 >> 4), IDESC_O,
+                      i + p + k > 0 ? 1u : 0u);
+          umma_commit(empty + 8 * st);
+          umma_commit(pvdone);
+        }
+        __syncwarp();
+      }
+    }
+    // every MMA issued has completed before tensor memory is released
+    if (elect_one()) umma_commit(smem_addr(&S.fin));
+    __syncwarp();
+    mbar_wait_thread(smem_addr(&S.fin), 0, P.wait_ns);
+    __syncwarp();
+  } else {  // ------------------------------------------------------------ softmax
+    const int wg = warp >> 2, tok = tid & 127, x0 = wg * QW;  // queries x0 .. x0 + QW - 1 of the unit
+    uint32_t tc = 0;
+    bool ok = true;
+    Segs s = first;
+    const uint32_t tlane = (uint32_t)(32 * (warp & 3)) << 16, tSq = tm + tlane + 2 * x0, tOq = tO + tlane + 2 * x0;
+    // A wait that gives up makes its warp go on without waiting; the warps
+    // leave together at the segment's end (so none is left at a barrier).
+    while (s.next(A, pre)) {
+      const int nqueries = s.rq.n * A.GH, q0 = s.qc * NQ;
+      const int nblk = s.c1 - s.c0, nt = (nblk + TBLK - 1) / TBLK;
+      ssync(3, NS);  // the previous segment's readers of the shared values are done
+      // Q's limbs: 16 lanes a query, 8 head dimensions each
+#pragma unroll 1
+      for (int x = warp * 2 + (lane >> 4); x < NQ; x += 8 * WG) {
+        const int qi = q0 + x, c = lane & 15;
+        const bool has = qi < nqueries;
+        const int row = has ? group_row(A, qi) : 0, head = s.h * A.GH + (has ? qi - row * A.GH : 0);
+        float v[8];
+        if (has) {
+          const int64_t at = (int64_t)(s.rq.row0 + row) * A.q_stride + (int64_t)head * 128 + c * 8;
+          const float4 a = load_elem4<DT>(A.q, at), b = load_elem4<DT>(A.q, at + 4);
+          v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+          v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = 0.f;
+        }
+        float mx = 0.f;
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          mx = fmaxf(mx, fabsf(v[i]));
+          bad = bad || !(fabsf(v[i]) < INFINITY);
+        }
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
+        int e = (int)((__float_as_uint(mx) >> 23) & 255u) - 127 - 7;  // the largest lands in [2^7, 2^8)
+        e = e < -100 ? -100 : e > 120 ? 120 : e;
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= down;
+        if (bad) v[0] = __uint_as_float(0x7fffffffu);  // (an infinity would saturate)
+        const int n = (x >> 3) * 16 + (x & 7);
+#pragma unroll
+        for (int p = 0; p < 2 * L; ++p) {
+          const uint2 w = limb8(v, true);
+          if (p == L - 1) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] *= BSCALE;
+          }
+          const int nn = n + (p >= L ? 8 : 0);
+          *reinterpret_cast<uint2*>(smem + G::Q_OFF + (p % L) * G::OPB + nn * 128 + (((c >> 1) ^ (nn & 7)) << 4) +
+                                    (c & 1) * 8) = w;
+        }
+        if (c == 0) {
+          const int p = s.rq.p0 + row;
+          float cf = up * A.scale;
+          if (EX && A.softcap > 0.f) cf = __fdiv_rn(cf, A.softcap);
+          else cf *= LOG2E;
+          S.cf[x] = cf;
+          S.slope[x] = EX && A.slopes && has ? A.slopes[head] * LOG2E : 0.f;
+          S.hi[x] = has ? p : -1;
+          S.lo[x] = A.window > 0 ? p - A.window + 1 : 0;
+          S.m[x] = -INFINITY;
+        }
+      }
+      fence_proxy_async_smem();
+      ssync(3, NS);
+      if (lane == 0) mbar_arrive(qfull);
+      const int last = (nqueries < q0 + NQ ? nqueries : q0 + NQ) - 1;
+      const int all_hi = s.rq.p0 + group_row(A, q0), any_hi = s.rq.p0 + group_row(A, last);
+      const int all_lo = A.window > 0 ? any_hi - A.window + 1 : 0;
+
+      float l[QW];
+#pragma unroll
+      for (int q = 0; q < QW; ++q) l[q] = 0.f;
+      float vref = 0.f, winv = 0.f;
+      for (int i = 0; i < nt; ++i, ++tc) {
+        const uint32_t st = tc % G::STAGES;
+        ok = ok && wait(fullk + 8 * st, (tc / G::STAGES) & 1);  // (the tile's scales)
+        const Meta& M = S.meta[st];
+        const int blk = tok >> 4;
+        const float ks = M.ks[blk], vs = M.vs[blk], vmax = M.vmax;
+        const uint32_t okm = M.ok;
+        const int key0 = (s.c0 + i * TBLK) * 16, key = key0 + tok;
+        ok = ok && wait(sfull + 8 * (tc & 1), (tc >> 1) & 1);
+        tc_fence_after();
+        float sc[QW];
+#pragma unroll
+        for (int j = 0; j < QW / 8; ++j) {
+          uint32_t v[16];
+          tmem_ld_32x32b_x16(tSq + (tc & 1) * G::N + 16 * j, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            sc[8 * j + q] = fmaf(__uint_as_float(v[8 + q]), 1.f / BSCALE, __uint_as_float(v[q])) * ks;
+        }
+#pragma unroll
+        for (int q = 0; q < QW; ++q) {
+          sc[q] *= S.cf[x0 + q];
+          if (EX) {
+            if (A.softcap > 0.f) sc[q] = A.softcap * LOG2E * cap_tanh(sc[q]);
+            sc[q] -= S.slope[x0 + q] * (float)(S.hi[x0 + q] - key);
+          }
+        }
+        if (okm != 0xffu || key0 + TOK - 1 > all_hi || key0 < all_lo) {  // some query does not see some token
+          // V rows that no query sees must not hold NaN codes, and a NaN code of
+          // one that some see reaches exactly those, through their scores
+          const bool there = (okm >> blk) & 1u, dead = !there || key > any_hi;
+          if (wg == 0) {
+            ok = ok && wait(fullv + 8 * st, (tc / G::STAGES) & 1);
+            uint4* row = reinterpret_cast<uint4*>(smem + st * 2 * KBYTES + KBYTES + tok * 128);
+            bool nan = false;
+#pragma unroll 2
+            for (int c = 0; c < 8; ++c) {
+              uint4 w = dead ? make_uint4(0u, 0u, 0u, 0u) : row[c];
+              const uint32_t a = nan_bytes(w.x), b = nan_bytes(w.y), d = nan_bytes(w.z), e = nan_bytes(w.w);
+              nan = nan || (a | b | d | e);
+              w = make_uint4(w.x & ~a, w.y & ~b, w.z & ~d, w.w & ~e);
+              if (dead || (a | b | d | e)) row[c] = w;
+            }
+            const uint32_t nans = __ballot_sync(FULL, nan);
+            if (lane == 0) S.nan[tc & 1][warp] = nans;
+          }
+          ssync(3, NS);
+          const bool nan = (S.nan[tc & 1][warp & 3] >> lane) & 1u;
+#pragma unroll
+          for (int q = 0; q < QW; ++q) {
+            if (dead || key > S.hi[x0 + q] || key < S.lo[x0 + q]) sc[q] = -INFINITY;
+            else if (nan) sc[q] = __uint_as_float(0x7fffffffu);
+          }
+        }
+        bool over = vmax > vref;
+#pragma unroll
+        for (int q = 0; q < QW; ++q) over = over || sc[q] > S.m[x0 + q] + T_LAG;
+        bool waited = tc == 0;
+        if (ssync_or(1 + wg, 128, over)) {  // raise the running maximum (and V's reference): O and l in the new units
+#pragma unroll
+          for (int q = 0; q < QW; ++q) {
+            const float x = warp_fmax(sc[q]);
+            if (lane == 0) S.wred[warp & 3][x0 + q] = x;
+          }
+          ssync(1 + wg, 128);
+          if (tok < QW) {
+            const int x = x0 + tok;
+            const float old = S.m[x];
+            const float top = fmaxf(fmaxf(S.wred[0][x], S.wred[1][x]), fmaxf(S.wred[2][x], S.wred[3][x]));
+            const float nm = fmaxf(old, top);
+            S.al[x] = old == -INFINITY ? 0.f : exp2_fast(old - nm);
+            S.m[x] = nm;
+          }
+          if (!waited) ok = ok && wait(pvdone, (tc - 1) & 1);
+          waited = true;
+          const float nref = fmaxf(vmax, vref), fv = nref > 0.f ? __fdiv_rn(vref, nref) : 0.f;
+          vref = nref;
+          winv = nref > 0.f ? __fdiv_rn(TP_SCALE, nref) : 0.f;
+          ssync(1 + wg, 128);
+#pragma unroll
+          for (int q = 0; q < QW; ++q) l[q] *= S.al[x0 + q];
+          if (i > 0) {
+            tc_fence_after();
+#pragma unroll
+            for (int j = 0; j < QW / 8; ++j) {
+              uint32_t v[16];
+              tmem_ld_32x32b_x16(tOq + 16 * j, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int q = 0; q < 16; ++q)
+                v[q] = __float_as_uint(__uint_as_float(v[q]) * (S.al[x0 + 8 * j + (q & 7)] * fv));
+              tmem_st_32x32b_x16(tOq + 16 * j, v);
+            }
+            tmem_st_wait();
+          }
+        }
+        // the tile's weights, and their limbs as the PV operand
+        if (!waited) ok = ok && wait(pvdone, (tc - 1) & 1);
+        const float wv = vs * winv;
+#pragma unroll
+        for (int j = 0; j < QW / 8; ++j) {
+          float w[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float m = S.m[x0 + 8 * j + q];
+            const float p = exp2_fast(sc[8 * j + q] - (m == -INFINITY ? 0.f : m));
+            l[8 * j + q] += p;
+            w[q] = p * wv;
+          }
+          uint2 a[L], b[L];
+#pragma unroll
+          for (int p = 0; p < 2 * L; ++p) {
+            uint2 c = make_uint2(0u, 0u);
+            if (p < PL) c = limb8(w, p + 1 < PL);
+            if (p == L - 1) {
+#pragma unroll
+              for (int q = 0; q < 8; ++q) w[q] *= BSCALE;
+            }
+            if (p < L) a[p] = c;
+            else b[p - L] = c;
+          }
+#pragma unroll
+          for (int p = 0; p < L; ++p)
+            *reinterpret_cast<uint4*>(smem + G::P_OFF + p * G::OPB + (x0 / 8 + j) * 2048 + tok * 16) =
+                make_uint4(a[p].x, a[p].y, b[p].x, b[p].y);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pfull);
+      }
+      // the result: thread = head dimension
+#pragma unroll
+      for (int q = 0; q < QW; ++q) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) l[q] += __shfl_xor_sync(FULL, l[q], o);
+        if (lane == 0) S.wred[warp & 3][x0 + q] = l[q];
+      }
+      if (nt > 0) ok = ok && wait(pvdone, (tc - 1) & 1);
+      tc_fence_after();
+      if (ssync_or(3, NS, !ok)) break;
+      const float back = vref * (1.f / TP_SCALE);
+#pragma unroll
+      for (int j = 0; j < QW / 8; ++j) {
+        uint32_t v[16];
+        if (nt > 0) {
+          tmem_ld_32x32b_x16(tOq + 16 * j, v);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int q = 0; q < 16; ++q) v[q] = 0u;
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const int x = x0 + 8 * j + q, qi = q0 + x;
+          if (qi >= nqueries) continue;
+          const float o = fmaf(__uint_as_float(v[8 + q]), 1.f / BSCALE, __uint_as_float(v[q])) * back;
+          const float lq = (S.wred[0][x] + S.wred[1][x]) + (S.wred[2][x] + S.wred[3][x]);
+          if (s.direct) {
+            const int row = group_row(A, qi), head = s.h * A.GH + qi - row * A.GH;
+            const float inv = lq != 0.f ? 1.f / lq : 0.f;  // (NaN stays NaN)
+            store_elem<DT>(A.out, (int64_t)(s.rq.row0 + row) * A.out_stride + (int64_t)head * 128 + tok, o * inv);
+            if (tok == 0 && A.lse) A.lse[(int64_t)(s.rq.row0 + row) * A.Hq + head] = (S.m[x] + log2f(lq)) * LN2;
+          } else {
+            const int64_t at = s.rec * NQ + x;
+            A.rec_o[at * 128 + tok] = o;
+            if (tok == 0) *reinterpret_cast<float2*>(A.rec_ml + at * 2) = make_float2(S.m[x], lq);
+          }
+        }
+      }
+      tc_fence_before();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == MW) {
+    tc_fence_after();
+    tmem_dealloc(tm, G::COLS);
+  }
+}
+
+template <int DT, bool EX>
+const void* tc_fn(int nt) {
+  return nt == 1 ? (const void*)kv8_tc_kernel<DT, EX, 1> : nt == 2 ? (const void*)kv8_tc_kernel<DT, EX, 2>
+                                                                   : (const void*)kv8_tc_kernel<DT, EX, 4>;
+}
+template <int NT>
+size_t tc_smem(bool f32) {
+  return f32 ? Geo<NT, 3>::SH_OFF + sizeof(Shared<NT, 3>) : Geo<NT, 2>::SH_OFF + sizeof(Shared<NT, 2>);
+}
+
+int encode_map(CUtensorMap* m, const uint8_t* base, int64_t rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return DDL_ERR_CUDA;
+  const cuuint64_t dims[2] = {128, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {128};
+  const cuuint32_t box[2] = {128, KV8_BLOCK};
+  const cuuint32_t es[2] = {1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides, box, es,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? DDL_OK : DDL_ERR_CUDA;
+}
+
+}  // namespace
+
+// rows: of the pool's [pages * H_kv * page_size][128] view, < 2^31.
+int kv8_tc_launch(const AttArgs& a, int dtype, bool ex, int64_t rows, void* stream) {
+  TcAtt p;
+  p.A = a;
+  p.wait_ns = wait_limit_ns();
+  int st;
+  if ((st = encode_map(&p.kmap, a.k, rows)) || (st = encode_map(&p.vmap, a.v, rows))) return st;
+  const int threads = a.nq == 1 ? Geo<1, 2>::THREADS : a.nq == 2 ? Geo<2, 2>::THREADS : Geo<4, 2>::THREADS;
+  const void* fn = dtype == DDL_T_F32    ? (ex ? tc_fn<DDL_T_F32, true>(a.nq) : tc_fn<DDL_T_F32, false>(a.nq))
+                   : dtype == DDL_T_BF16 ? (ex ? tc_fn<DDL_T_BF16, true>(a.nq) : tc_fn<DDL_T_BF16, false>(a.nq))
+                                         : (ex ? tc_fn<DDL_T_F16, true>(a.nq) : tc_fn<DDL_T_F16, false>(a.nq));
+  const bool f32 = dtype == DDL_T_F32;
+  const size_t smem = (a.nq == 1 ? tc_smem<1>(f32) : a.nq == 2 ? tc_smem<2>(f32) : tc_smem<4>(f32)) + 16 +
+                      (a.whole ? 0 : (size_t)(a.R + 1) * 8);
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  if (e != cudaSuccess) return cuda_status(e);
+  void* args[] = {&p};
+  return cuda_status(launch_pdl(fn, dim3((unsigned)a.ctas), dim3((unsigned)threads), args, smem, (cudaStream_t)stream));
+}
+
+}  // namespace ddl

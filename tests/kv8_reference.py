@@ -139,9 +139,14 @@ def attention(pool, q, q_off, kv_len, table, scale, softcap=0.0, window=0, slope
     magnitudes (tensor cores truncate), q held to 2^-21; the score's scaling,
     cap (tanh from exp within 2^-21 of the cap) and bias rounded in fp32; e^s
     within 2^-21 and the running maximum's rescaling within another 2^-21.
-    The weights are rounded to fp16 for 16-bit outputs (2^-11), to two fp16
-    parts for fp32 ones (2^-21), the sums over n keys within n 2^-23 of their
-    magnitudes, and the output once to its type: half a step, eps / 2 of the
+    The weights are rounded to at least 2^-11 of themselves for 16-bit outputs,
+    2^-21 for fp32 ones, but no finer than an absolute F = 2^-25 (fp32: 2^-29)
+    of the largest weight, in units of the largest V scale: that is half the
+    smallest e4m3 step, 2^-10, over the weights' scale 2^7 and the last limbs'
+    2^8 (2^12).  Such a weight p_j changes by at most min(p_j, F vmax / vs_j).
+    (p_j relative to the running maximum: at most twice that to the true one;
+    the sum of weights is at least 1.)  The sums over n keys are within n 2^-23
+    of their magnitudes, and the output once to its type: half a step, eps / 2 of the
     value, or of the smallest normal number where the value lies below it
     (the steps stop shrinking there: fp16's are 2^-24)."""
     k, v, ks, vs = pool
@@ -153,6 +158,7 @@ def attention(pool, q, q_off, kv_len, table, scale, softcap=0.0, window=0, slope
     lse = torch.full((T, H_q), math.nan, dtype=torch.float64, device=dev)
     tol, tol_l = torch.zeros_like(out), torch.zeros_like(lse)
     p_round = 2.0 ** -21 if q.dtype == torch.float32 else 2.0 ** -11
+    floor = 2.0 ** -29 if q.dtype == torch.float32 else 2.0 ** -25
     eps = torch.finfo(q.dtype).eps / 2
     P = k.shape[2]
     table = np.asarray(table)
@@ -186,13 +192,18 @@ def attention(pool, q, q_off, kv_len, table, scale, softcap=0.0, window=0, slope
         none = ~seen.any(-1)
         top = s.amax(-1, keepdim=True)
         w = torch.exp(s - torch.where(top == -math.inf, 0.0, top))
+        top_w = w
         l = w.sum(-1, keepdim=True)
         w = w / torch.where(l == 0, 1.0, l)
         o = torch.einsum("hgnk,hkd->hgnd", w, vv)
         A = torch.einsum("hgnk,hkd->hgnd", w, vv.abs())
         wd = w * torch.where(seen, d, 0.0)
         E = torch.einsum("hgnk,hkd->hgnd", wd, vv.abs()) + o.abs() * wd.sum(-1, keepdim=True)
-        E = E + A * (p_round + (L + 64) * 2.0 ** -23) + 2.0 ** -34 * vv.abs().amax()
+        sv = vs[torch.as_tensor(ids, device=dev)].double().transpose(0, 1)
+        sv = sv.reshape(H, -1).repeat_interleave(BLOCK, -1)[:, :L]
+        tiny = floor * sv.amax(-1, keepdim=True) / sv.clamp(min=1e-300)
+        least = torch.minimum(2 * top_w, tiny[:, None, None, :])
+        E = E + A * (p_round + (L + 64) * 2.0 ** -23) + torch.einsum("hgnk,hkd->hgnd", least, vv.abs())
         ll = (top + torch.log(l))[..., 0]
         dl = wd.sum(-1) + (L + 64) * 2.0 ** -23 + ll.abs().nan_to_num(posinf=0.0) * 2.0 ** -21 + 2.0 ** -21
         o = torch.where(none[:, None], 0.0, o) if none.ndim == 1 else o
