@@ -186,44 +186,44 @@ struct AppendArgs {
   const int32_t* slot;
   int32_t* bad;
   int64_t slots;       // pages * page_size
-  int32_t T, H, pshift, span, ppc;
+  int32_t T, H, pshift, span, ppc, vec;  // vec: the map is 16-byte aligned
 };
 
-// Four (hd 128) or two (hd 64) neighbouring elements of a row as fp32.
+// Four (hd 128) or two (hd 64) neighbouring elements of a row, as they are
+// stored (a 16-bit row takes half the registers until it is used), and as fp32.
 template <int DT, int W>
-__device__ __forceinline__ void load_row(const void* base, int64_t at, float (&v)[W]) {
-  if (DT == DDL_T_F32) {
-    const float* p = reinterpret_cast<const float*>(base) + at;
-    if (W == 4) {
-      const float4 f = *reinterpret_cast<const float4*>(p);
-      v[0] = f.x; v[1] = f.y; v[W - 2] = f.z; v[W - 1] = f.w;
+struct Raw {
+  static constexpr int N = DT == DDL_T_F32 ? W : W / 2;
+  uint32_t w[N];
+  __device__ __forceinline__ void load(const void* base, int64_t at) {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint8_t*>(base) +
+                                                          at * (DT == DDL_T_F32 ? 4 : 2));
+    if (N == 4) {
+      const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+      w[0] = u.x; w[N > 1 ? 1 : 0] = u.y; w[N > 2 ? 2 : 0] = u.z; w[N - 1] = u.w;
+    } else if (N == 2) {
+      const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+      w[0] = u.x; w[N - 1] = u.y;
     } else {
-      const float2 f = *reinterpret_cast<const float2*>(p);
-      v[0] = f.x; v[1] = f.y;
+      w[0] = __ldg(p);
     }
-  } else {
-    const uint16_t* p = reinterpret_cast<const uint16_t*>(base) + at;
-    uint32_t w[W / 2];
-    if (W == 4) {
-      const uint2 u = *reinterpret_cast<const uint2*>(p);
-      w[0] = u.x;
-      w[W / 2 - 1] = u.y;
-    } else {
-      w[0] = *reinterpret_cast<const uint32_t*>(p);
-    }
+  }
+  __device__ __forceinline__ void floats(float (&v)[W]) const {
 #pragma unroll
-    for (int i = 0; i < W / 2; ++i) {
-      if (DT == DDL_T_BF16) {
-        v[2 * i] = bf16lo_f32(w[i]);
-        v[2 * i + 1] = bf16hi_f32(w[i]);
+    for (int i = 0; i < N; ++i) {
+      if (DT == DDL_T_F32) {
+        v[i] = __uint_as_float(w[i]);
+      } else if (DT == DDL_T_BF16) {
+        v[(2 * i) % W] = bf16lo_f32(w[i]);
+        v[(2 * i + 1) % W] = bf16hi_f32(w[i]);
       } else {
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
+        v[(2 * i) % W] = f.x;
+        v[(2 * i + 1) % W] = f.y;
       }
     }
   }
-}
+};
 
 template <int CT, int W>
 __device__ __forceinline__ uint32_t encode(const float (&v)[W]) {
@@ -281,30 +281,48 @@ struct Divider {
 // requests) must not race: every CTA looks through the whole map for the
 // blocks that begin in its window.  A run whose block occurs earlier is left
 // to that occurrence's warp, which stores all runs of the block in map order.
-// The look is T / 1024 loads of 16 bytes a thread from L2, and the reason for
-// the limit on T.
+// The look is T / 1024 loads of 16 bytes a thread from L2, while the first run's
+// rows are on their way; it is the reason for the limit on T.
 struct RunSeen {
   int first, count;  // lowest row and number of rows of the block in the whole map
 };
 
 template <int CT, int DT, int HD>
-struct RunStore {
+struct Run {
   static constexpr int W = HD / 32;
-  static constexpr int BATCH = 8;  // rows in registers at a time, twice
+  static constexpr int ROWS = 16;  // rows in registers
+  int i, block, n, low;            // first row, block, rows, lowest token of the block among them
+  int32_t mine;                    // slot of row i + lane
+  float was;                       // the block's scale (0 when low is its first token)
+  float* sp;
+  uint8_t* rows;                   // the block's codes, this lane's columns
+  const void* x;
+  int64_t stride, col;
+  Raw<DT, W> v[ROWS];
 
-  // Store the run of rows i .. in block `block` (row i lies in it); returns its length.
-  static __device__ __forceinline__ int store(const AppendArgs& A, int kv, int h, int i, int block) {
+  // The run of neighbouring rows in `block` that begins at row i: its rows and
+  // the block's scale on their way into registers.
+  __device__ __forceinline__ void load(const AppendArgs& A, int kv, int h, int first, int blk) {
     const int lane = threadIdx.x & 31;
-    uint8_t* const code = A.code[kv];
-    const void* const x = A.x[kv];
-    const int64_t stride = A.stride[kv], col = (int64_t)h * HD + lane * W;
-    // rows of the run: the lanes' slots from row i on that lie in the block
-    const int32_t mine = i + lane < A.T ? A.slot[i + lane] : -1;
+    i = first;
+    block = blk;
+    x = A.x[kv];
+    stride = A.stride[kv];
+    col = (int64_t)h * HD + lane * W;
+    v[0].load(x, (int64_t)i * stride + col);
+    mine = i + lane < A.T ? A.slot[i + lane] : -1;
     const uint32_t in = __ballot_sync(FULL, mine >= 0 && (mine >> 4) == block);
-    int n = in == FULL ? 32 : __ffs(~in) - 1;
-    int low = lane < n ? (mine & 15) : 15;
+    n = in == FULL ? 32 : __ffs(~in) - 1;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) low = min(low, __shfl_xor_sync(FULL, low, o));
+    for (int b = 1; b < ROWS; ++b)
+      if (b < n) v[b].load(x, (int64_t)(i + b) * stride + col);
+    const int64_t page = block >> (A.pshift - 4);
+    const int sub = block & ((1 << (A.pshift - 4)) - 1);
+    const int64_t row = ((page * A.H + h) << A.pshift) + ((int64_t)sub << 4);  // of the pool's [rows][hd] view
+    sp = A.scale[kv] + (row >> 4);
+    rows = A.code[kv] + row * HD + lane * W;
+    was = *sp;
+    low = __reduce_min_sync(FULL, lane < n ? (mine & 15) : 15);
     if (n == 32) {  // (only with repeated slots)
       for (int e = i + 32; e < A.T; ++e) {
         const int32_t s = A.slot[e];
@@ -313,35 +331,39 @@ struct RunStore {
         low = min(low, (int)(s & 15));
       }
     }
-    const int64_t page = block >> (A.pshift - 4);
-    const int sub = block & ((1 << (A.pshift - 4)) - 1);
-    const int64_t row = ((page * A.H + h) << A.pshift) + ((int64_t)sub << 4);  // of the pool's [rows][hd] view
-    float* const sp = A.scale[kv] + (row >> 4);
-    const float was = low > 0 ? *sp : 0.f;
-    float v[2][BATCH][W];
-    float amax = 0.f;
-    auto top = [&](const float (&r)[W]) {
+    if (low == 0) was = 0.f;
+  }
+
+  __device__ __forceinline__ void put(const Divider& by, int32_t s, const Raw<DT, W>& r) {
+    float c[W];
+    r.floats(c);
+#pragma unroll
+    for (int w = 0; w < W; ++w) c[w] = by(c[w]);
+    store_codes<W>(rows + (s & 15) * HD, encode<CT, W>(c));
+  }
+
+  __device__ __forceinline__ void store(const AppendArgs& A) {
+    const int lane = threadIdx.x & 31;
+    uint32_t top = 0;  // largest finite magnitude, as bits (ordered as the values)
+    auto add = [&](const Raw<DT, W>& r) {
+      float f[W];
+      r.floats(f);
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        const float a = fabsf(r[w]);
-        amax = a < INFINITY ? fmaxf(amax, a) : amax;
+        const uint32_t a = __float_as_uint(f[w]) & 0x7fffffffu;
+        top = a < 0x7f800000u ? max(top, a) : top;
       }
     };
-    for (int b0 = 2 * BATCH; b0 < n; ++b0) {  // (only with repeated slots)
-      load_row<DT, W>(x, (int64_t)(i + b0) * stride + col, v[0][0]);
-      top(v[0][0]);
+#pragma unroll
+    for (int b = 0; b < ROWS; ++b)
+      if (b < n) add(v[b]);
+    Raw<DT, W> t;
+    for (int b = ROWS; b < n; ++b) {  // (only with repeated slots)
+      t.load(x, (int64_t)(i + b) * stride + col);
+      add(t);
     }
-#pragma unroll
-    for (int b = 0; b < 2 * BATCH; ++b)
-      if (b < n) load_row<DT, W>(x, (int64_t)(i + b) * stride + col, v[b / BATCH][b % BATCH]);
-#pragma unroll
-    for (int b = 0; b < 2 * BATCH; ++b)
-      if (b < n) top(v[b / BATCH][b % BATCH]);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, o));
-    const float fresh = pow2_scale<CT>(amax);
+    const float fresh = pow2_scale<CT>(__uint_as_float(__reduce_max_sync(FULL, top)));
     const float now = was > fresh ? was : fresh;
-    uint8_t* const rows = code + row * HD + lane * W;
     if (low > 0 && now != was) {  // the block's earlier tokens move to the larger scale
       const float ratio = was > 0.f ? __fdiv_rn(was, now) : 0.f;
       for (int o = 0; o < low; ++o) {
@@ -365,76 +387,135 @@ struct RunStore {
       }
     }
     const Divider by(now);
-    auto put = [&](int32_t s, const float (&r)[W]) {
-      float c[W];
 #pragma unroll
-      for (int w = 0; w < W; ++w) c[w] = by(r[w]);
-      store_codes<W>(rows + (s & 15) * HD, encode<CT, W>(c));
-    };
-#pragma unroll
-    for (int b = 0; b < 2 * BATCH; ++b)
-      if (b < n) put(__shfl_sync(FULL, mine, b), v[b / BATCH][b % BATCH]);
-    for (int b0 = 2 * BATCH; b0 < n; ++b0) {
-      load_row<DT, W>(x, (int64_t)(i + b0) * stride + col, v[0][0]);
-      put(A.slot[i + b0], v[0][0]);
+    for (int b = 0; b < ROWS; ++b)
+      if (b < n) put(by, __shfl_sync(FULL, mine, b), v[b]);
+    for (int b = ROWS; b < n; ++b) {
+      t.load(x, (int64_t)(i + b) * stride + col);
+      put(by, A.slot[i + b], t);
     }
     if (lane == 0 && (low == 0 || now != was)) *sp = now;
     __syncwarp();
-    return n;
   }
 };
 
 constexpr int APPEND_SPAN = 16;  // rows of a window at most
 
+// Where in the whole map do the blocks of the runs that begin at the CTA's rows
+// occur?  (block: lane l's, of the window's row l; mine: the warp speaks for it.)
+__device__ __forceinline__ void look_up(const AppendArgs& A, int32_t block, bool mine, int win, int2* begun,
+                                        RunSeen* seen, int& count) {
+  const int tid = threadIdx.x;
+  if (tid == 0) count = 0;
+  __syncthreads();
+  if (mine && block >= 0) {
+    const int k = atomicAdd(&count, 1), at = win * A.span + (tid & 31);
+    begun[k] = make_int2(block, at);
+    seen[at] = {0x7fffffff, 0};
+  }
+  __syncthreads();
+  // where else in the map do these blocks occur?
+  auto look = [&](int e, int32_t s, int2 b) {
+    if (s >= 0 && (s >> 4) == b.x) {
+      atomicMin(&seen[b.y].first, e);
+      atomicAdd(&seen[b.y].count, 1);
+    }
+  };
+  const int nb = count;
+  if (A.vec) {  // 16 bytes a load, four loads on their way together
+    const int n4 = (A.T + 3) >> 2;
+    for (int e = tid; e < n4; e += 4 * 256) {
+      int4 s[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int f = e + 256 * u, left = A.T - 4 * f;  // (the last one may be cut)
+        s[u] = make_int4(-1, -1, -1, -1);
+        if (left >= 4) {
+          s[u] = __ldg(reinterpret_cast<const int4*>(A.slot) + f);
+        } else if (left > 0) {
+          s[u].x = A.slot[4 * f];
+          if (left > 1) s[u].y = A.slot[4 * f + 1];
+          if (left > 2) s[u].z = A.slot[4 * f + 2];
+        }
+      }
+      for (int k = 0; k < nb; ++k) {
+        const int2 b = begun[k];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int at = 4 * (e + 256 * u);
+          look(at, s[u].x, b);
+          look(at + 1, s[u].y, b);
+          look(at + 2, s[u].z, b);
+          look(at + 3, s[u].w, b);
+        }
+      }
+    }
+  } else {
+    for (int e = tid; e < A.T; e += 256) {
+      const int32_t s = A.slot[e];
+      for (int k = 0; k < nb; ++k) look(e, s, begun[k]);
+    }
+  }
+  __syncthreads();
+}
+
 template <int CT, int DT, int HD>
-__global__ void __launch_bounds__(256) kv8_append_kernel(const __grid_constant__ AppendArgs A) {
+__global__ void __launch_bounds__(256, DT == DDL_T_F32 && HD == 128 ? 2 : 3) kv8_append_kernel(const __grid_constant__ AppendArgs A) {
   __shared__ RunSeen seen[8 * APPEND_SPAN];
-  __shared__ int32_t blocks[8 * APPEND_SPAN];  // of the runs that begin at the CTA's rows, -1: none begins
+  __shared__ int2 begun[8 * APPEND_SPAN];  // runs that begin at the CTA's rows: block, row
+  __shared__ int count;
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // warps: A.ppc pairs of each of 8 / ppc windows
   const int win = warp / A.ppc, nwin = 8 / A.ppc, pair = blockIdx.y * A.ppc + warp % A.ppc;
-  const int c0 = blockIdx.x * nwin * A.span, nrow = min(nwin * A.span, A.T - c0);
-  if (tid < nrow) {
-    const int32_t s = A.slot[c0 + tid], sb = c0 + tid > 0 ? A.slot[c0 + tid - 1] : -1;
+  const int c0 = blockIdx.x * nwin * A.span;
+  const bool mine = win < nwin && pair < 2 * A.H && c0 + win * A.span < A.T;
+  // the warp's own window: which runs begin there, and the first one's rows
+  int32_t block = -1;  // lane l: of the run that begins at the window's row l
+  if (mine && lane < A.span && c0 + win * A.span + lane < A.T) {
+    const int e = c0 + win * A.span + lane;
+    const int32_t s = A.slot[e], sb = e > 0 ? A.slot[e - 1] : -1;
     const bool outside = s >= A.slots;
-    if (outside && A.bad && blockIdx.y == 0) atomicOr(A.bad, 1);
-    blocks[tid] = s >= 0 && !outside && (sb < 0 || (sb >> 4) != (s >> 4)) ? s >> 4 : -1;
-    seen[tid].first = 0x7fffffff;
-    seen[tid].count = 0;
+    if (outside && A.bad && pair == 0) atomicOr(A.bad, 1);
+    if (s >= 0 && !outside && (sb < 0 || (sb >> 4) != (s >> 4))) block = s >> 4;
   }
-  __syncthreads();
-  for (int e = tid; e < A.T; e += 4 * 256) {  // four at a time, so that their loads go out together
-    int32_t b[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) b[u] = e + 256 * u < A.T ? A.slot[e + 256 * u] : -1;
-    for (int k = 0; k < nrow; ++k) {
-      const int32_t want = blocks[k];
-      if (want < 0) continue;
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (b[u] >= 0 && (b[u] >> 4) == want) {
-          atomicMin(&seen[k].first, e + 256 * u);
-          atomicAdd(&seen[k].count, 1);
-        }
-    }
-  }
-  __syncthreads();
-  if (win >= nwin || pair >= 2 * A.H) return;
+  uint32_t starts = __ballot_sync(FULL, block >= 0);
   const int h = pair >> 1, kv = pair & 1;
-  for (int k = win * A.span; k < min((win + 1) * A.span, nrow); ++k) {
-    const int block = blocks[k];
-    int i = c0 + k;
-    if (block < 0 || seen[k].first != i) continue;
-    int left = seen[k].count;
-    for (;;) {
-      const int n = RunStore<CT, DT, HD>::store(A, kv, h, i, block);
-      left -= n;
+  Run<CT, DT, HD> run;
+  if (starts) {
+    const int k = __ffs(starts) - 1;
+    run.load(A, kv, h, c0 + win * A.span + k, __shfl_sync(FULL, block, k));
+  }
+  int first1 = 0x7fffffff, total1 = 0;
+  if (A.span == 1) {  // (T <= 256) each warp looks for itself, without a barrier
+    const int blk = __shfl_sync(FULL, block, 0);
+    int32_t s[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) s[u] = lane + 32 * u < A.T ? A.slot[lane + 32 * u] : -1;
+#pragma unroll
+    for (int u = 7; u >= 0; --u) {
+      const uint32_t m = __ballot_sync(FULL, s[u] >= 0 && (s[u] >> 4) == blk);
+      if (m) first1 = 32 * u + __ffs(m) - 1;
+      total1 += __popc(m);
+    }
+  } else {
+    look_up(A, block, mine && warp % A.ppc == 0, win, begun, seen, count);
+  }
+  bool loaded = true;
+  for (; starts; starts &= starts - 1, loaded = false) {
+    const int k = __ffs(starts) - 1, at = win * A.span + k, blk = __shfl_sync(FULL, block, k);
+    int i = c0 + at, left = A.span == 1 ? total1 : seen[at].count;
+    if ((A.span == 1 ? first1 : seen[at].first) != i) continue;  // an earlier run's warp takes this one
+    for (;;) {  // the block's runs, in map order
+      if (!loaded) run.load(A, kv, h, i, blk);
+      loaded = false;
+      run.store(A);
+      left -= run.n;
       if (left <= 0) break;
-      for (i += n; i < A.T; i += 32) {  // the block's next run
+      for (i += run.n; i < A.T; i += 32) {
         const int32_t s = i + lane < A.T ? A.slot[i + lane] : -1;
-        const uint32_t m = __ballot_sync(FULL, s >= 0 && (s >> 4) == block);
+        const uint32_t m = __ballot_sync(FULL, s >= 0 && (s >> 4) == blk);
         if (m) {
           i += __ffs(m) - 1;
           break;
@@ -508,6 +589,7 @@ extern "C" int ddl_kv8_append(const ddl_kv8* kv, int32_t H_kv, int32_t head_dim,
   a.H = H_kv;
   a.pshift = log2_of(kv->page_size);
   a.span = T > 256 ? APPEND_SPAN : 1;
+  a.vec = aligned16(slot);
   a.ppc = 2 * H_kv < 8 ? 2 * H_kv : 8;
   if (T > DDL_KV8_MAX_APPEND) return DDL_ERR_UNSUPPORTED;
   const int rows = 8 / a.ppc * a.span;  // of a CTA
