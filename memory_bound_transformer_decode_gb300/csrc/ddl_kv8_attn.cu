@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(ATT_WARPS * 32, 2) kv8_attention_kernel(const 
   }
   __shared__ int64_t wsum[ATT_WARPS];
   const int64_t W = unit_prefix<ATT_WARPS * 32>(A, pre, wsum);
-  const int64_t n = share_count(W, A.ctas);
+  const int64_t n = share_count(A, W);
   if ((int64_t)blockIdx.x >= n || W == 0) return;
   int64_t x, end;
   share_bounds(W, n, x, end);
@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(const __grid_constant__ A
 #pragma unroll
   for (int k = 0; k < E; ++k) acc[k] = 0.f;
   if (nb > 0) {
-    const int64_t n = share_count(W, A.ctas), lo = p0 + (int64_t)unit * (nb + UNIT_COST) + UNIT_COST;
+    const int64_t n = share_count(A, W), lo = p0 + (int64_t)unit * (nb + A.unit_cost) + A.unit_cost;
     int i0, i1;
     if (W < (1 << 22)) {
       i0 = (int)owner32((uint32_t)W, (uint32_t)n, (uint32_t)lo);
@@ -629,7 +629,7 @@ constexpr int WHOLE_BLOCKS = 32;
 
 struct AttPlan {
   int32_t nq, nqc, whole, ctas, deep;  // deep: a unit may have many shares
-  bool tc;                             // the tcgen05 kernel
+  int32_t unit_cost, min_share;        // of a CTA's share, in blocks
   int64_t rec_ml, prefix, total;       // workspace offsets
 };
 
@@ -649,7 +649,10 @@ int att_plan(bool tc, int32_t H_q, int32_t H_kv, int32_t hd, int32_t R, int32_t 
   if (st) return st;
   const int tiles = (max_rows * (H_q / H_kv) + 7) / 8;
   p.nq = 1;
-  p.tc = tc;
+  // Measured at 64 requests of up to 8192 tokens, 64/8 heads (tcgen05: cost 16 / 24 / 40 110 / 106 / 99 us; warp MMAs
+  // on 16 requests of 28/4 heads: cost 16 / 24 / 40 18 / 20 / 23 us).
+  p.unit_cost = tc ? 48 : 16;
+  p.min_share = p.unit_cost + (tc ? 8 : 16);
   while (p.nq < (tc ? 4 : ATT_WARPS) && p.nq < tiles) p.nq *= 2;
   p.nqc = (tiles + p.nq - 1) / p.nq;
   const int64_t blocks = ((int64_t)max_len + 15) / 16, units = (int64_t)R * H_kv * p.nqc;
@@ -659,7 +662,7 @@ int att_plan(bool tc, int32_t H_q, int32_t H_kv, int32_t hd, int32_t R, int32_t 
   p.ctas = (int32_t)units;
   p.deep = 0;
   if (p.whole) return DDL_OK;
-  const int64_t most = (units * (blocks + UNIT_COST) + MIN_SHARE - 1) / MIN_SHARE;
+  const int64_t most = (units * (blocks + p.unit_cost) + p.min_share - 1) / p.min_share;
   p.ctas = (int32_t)(most < 2 * sms ? most : 2 * sms);
   if (p.ctas > 1024) return DDL_ERR_UNSUPPORTED;  // (the kernels' 32-bit share arithmetic)
   p.deep = units * 8 <= p.ctas;
@@ -766,6 +769,8 @@ extern "C" int ddl_kv8_attention(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, i
   a.max_len = max_len;
   a.whole = pl.whole;
   a.ctas = pl.ctas;
+  a.unit_cost = pl.unit_cost;
+  a.min_share = pl.min_share;
   a.nq = pl.nq;
   a.nqc = pl.nqc;
   const bool ex = opts->softcap > 0.f || opts->slopes;

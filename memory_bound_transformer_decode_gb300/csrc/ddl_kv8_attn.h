@@ -28,20 +28,20 @@ struct AttArgs {
   int32_t R, T, Hq, Hkv, GH, gmul, hd, pshift, per, max_rows, max_len;
   int32_t whole;    // one CTA a unit, else shares
   int32_t ctas;     // shares at most
+  int32_t unit_cost, min_share;
   int32_t nq, nqc;  // query tiles of 8 a unit has (a power of two <= 8), units over a request's query tiles
 };
 
 // Shares.  Beginning and ending a unit (Q, the join of the warps, the record)
-// costs a CTA about as much as UNIT_COST blocks, so a unit of nb blocks weighs
-// UNIT_COST + nb, its block j standing at UNIT_COST + j; the weights of all
-// units, end to end, are cut (range_lo, owner_of) into equal parts of at least
-// MIN_SHARE.
-constexpr int UNIT_COST = 24, MIN_SHARE = UNIT_COST + 16;
-__device__ __forceinline__ int64_t share_count(int64_t W, int ctas) {
-  const int64_t most = (W + MIN_SHARE - 1) / MIN_SHARE;
-  return most < 1 ? 1 : most < ctas ? most : ctas;
+// costs a CTA about as much as unit_cost of its blocks, so a unit of nb blocks
+// weighs unit_cost + nb, its block j standing at unit_cost + j; the weights of
+// all units, end to end, are cut (range_lo, owner_of) into equal parts of at
+// least min_share.
+__device__ __forceinline__ int64_t share_count(const AttArgs& A, int64_t W) {
+  const int64_t most = W < (1ll << 31) ? ((uint32_t)W + A.min_share - 1) / (uint32_t)A.min_share
+                                       : (W + A.min_share - 1) / A.min_share;
+  return most < 1 ? 1 : most < A.ctas ? most : A.ctas;
 }
-
 __device__ __forceinline__ void share_bounds(int64_t W, int64_t n, int64_t& x, int64_t& end) {
   if (W < (1 << 22)) {  // (32-bit divisions: n <= 1024)
     x = (uint32_t)W * blockIdx.x / (uint32_t)n;
@@ -111,7 +111,7 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
 // Weight of request q's units.
 __device__ __forceinline__ int64_t req_weight(const AttArgs& A, const Req& q) {
   const int nb = q.b1 - q.b0;
-  return nb > 0 ? (int64_t)(nb + UNIT_COST) * A.Hkv * unit_groups(A, q) : 0;
+  return nb > 0 ? (int64_t)(nb + A.unit_cost) * A.Hkv * unit_groups(A, q) : 0;
 }
 // Row of a request that its query qi (row * group + head of the group) belongs to: qi / GH, qi < 512.
 __device__ __forceinline__ int group_row(const AttArgs& A, int qi) { return (int)((uint32_t)qi * (uint32_t)A.gmul >> 16); }
@@ -180,12 +180,12 @@ __device__ __forceinline__ int64_t unit_prefix(const AttArgs& A, int64_t* pre, i
 // run has no blocks.
 __device__ __forceinline__ bool share_segment(const AttArgs& A, const Req& q, int64_t p0, int64_t& x, int64_t end,
                                               int& unit, int& first, int& count) {
-  const int nb = q.b1 - q.b0, w = nb + UNIT_COST;
+  const int nb = q.b1 - q.b0, w = nb + A.unit_cost;
   const int64_t in = x - p0;
   unit = in < (1ll << 31) ? (int)((uint32_t)in / (uint32_t)w) : (int)(in / w);
   const int at = (int)(in - (int64_t)unit * w);
   const int to = end - x < w - at ? at + (int)(end - x) : w;
-  const int b0 = at > UNIT_COST ? at - UNIT_COST : 0, b1 = to > UNIT_COST ? to - UNIT_COST : 0;
+  const int b0 = at > A.unit_cost ? at - A.unit_cost : 0, b1 = to > A.unit_cost ? to - A.unit_cost : 0;
   first = q.b0 + b0;
   count = b1 - b0;
   x += to - at;

@@ -17,10 +17,14 @@
 // limbs exactly.  The B operand has 16 columns per 8 queries: group A holds
 // limbs 1 .. L (one MMA pass each, summed in the accumulator), group B the
 // next L, scaled by 16^L so that e4m3's narrow range does not cut them off, in
-// the same passes.  L = 2 for 16-bit rows (Q 2^-16, P three limbs: 2^-12, below
-// the output's own rounding), 3 for fp32 rows (2^-24).  What falls below
-// e4m3's smallest subnormal in group B is 2^-26 of a row's largest q and 2^-25
+// the same passes.  L = 2 for 16-bit rows (Q 2^-16; P rounded to fp16, 2^-11,
+// below the output's own rounding, in three limbs), 3 for fp32 rows (2^-24).  What falls below
+// e4m3's smallest subnormal in group B is 2^-26 of a row's largest q and 2^-23
 // of the largest weight (L = 2).
+//
+// A segment's tiles are taken from the newest token to the oldest: a distance
+// bias then raises the running maximum once and not with every tile (4 rows of
+// 16 requests, ALiBi: all 8 tiles of a share raised it, 1 does).
 //
 // Roles: one or two warpgroups softmax (thread = token of the tile, then head
 // dimension of the output; 8 or 16 queries each), a warp copies, a warp issues
@@ -37,9 +41,11 @@ namespace {
 constexpr int TOK = 128, TBLK = TOK / KV8_BLOCK;  // tokens and blocks of a tile
 constexpr uint32_t KBYTES = TOK * 128;
 
-// P carries 2^7; with the running maximum lagging by less than 2^1 it stays
-// within 2^8 <= 448.
-constexpr float TP_SCALE = 128.f, T_LAG = 1.f;
+// P carries 2^5; with the running maximum lagging by less than 2^3 it stays
+// within 2^8 <= 448.  (Raising it stops the softmax warps three times for the
+// exchange of the maxima and rescales O in tensor memory: with a lag of 2^1
+// every third tile of 16 queries did.)
+constexpr float TP_SCALE = 32.f, T_LAG = 3.f;
 
 struct TcAtt {
   AttArgs A;
@@ -70,6 +76,7 @@ template <int NT, int L>
 struct Shared {
   Meta meta[Geo<NT, L>::STAGES];
   alignas(16) float cf[8 * NT], slope[8 * NT], m[8 * NT], al[8 * NT];
+  alignas(16) float most[8 * NT], mref[8 * NT];  // m + T_LAG; m, 0 for -inf
   int32_t hi[8 * NT], lo[8 * NT];
   float wred[4][8 * NT];
   uint32_t nan[2][4];
@@ -139,6 +146,31 @@ __device__ __forceinline__ uint2 limb8(float (&v)[8], bool rest) {
   return make_uint2(w[0], w[1]);
 }
 
+// The same of eight fp16 values (pairs).
+__device__ __forceinline__ uint32_t hmul2_bits(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint2 limb8h(uint32_t (&h)[4], bool rest) {
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e4m3x2.f16x2 a, %1;\n\tcvt.rn.satfinite.e4m3x2.f16x2 b, %2;\n\t"
+        "mov.b32 %0, {a, b};\n\t}"
+        : "=r"(w[i])
+        : "r"(h[2 * i]), "r"(h[2 * i + 1]));
+    if (rest) {
+      uint32_t lo, hi;
+      e4m3x4_f16x2(w[i], lo, hi);
+      const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&h[2 * i]), *reinterpret_cast<const __half2*>(&lo));
+      const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&h[2 * i + 1]), *reinterpret_cast<const __half2*>(&hi));
+      h[2 * i] = *reinterpret_cast<const uint32_t*>(&x);
+      h[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&y);
+    }
+  }
+  return make_uint2(w[0], w[1]);
+}
+
 // A CTA's segments: runs of blocks of one unit.
 struct Segs {
   int64_t x, end;
@@ -187,7 +219,6 @@ struct Segs {
 template <int DT, bool EX, int NT>
 __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) kv8_tc_kernel(const __grid_constant__ TcAtt P) {
   constexpr int L = DT == DDL_T_F32 ? 3 : 2;
-  constexpr int PL = DT == DDL_T_F32 ? 6 : 3;  // limbs of P
   constexpr float BSCALE = DT == DDL_T_F32 ? 4096.f : 256.f;  // 16^L
   using G = Geo<NT, L>;
   constexpr int NQ = G::NQ, QW = G::QW, WG = G::WG, NS = 128 * WG;  // NS: softmax threads
@@ -229,7 +260,7 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
   first.r = 0;
   if (!A.whole) {
     const int64_t W = unit_prefix<G::THREADS>(A, pre, S.wsum);
-    const int64_t n = share_count(W, A.ctas);
+    const int64_t n = share_count(A, W);
     if ((int64_t)blockIdx.x >= n || W == 0) {
       first.end = 0;
     } else {
@@ -270,16 +301,16 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
     Segs s = first;
     while (ok && s.next(A, pre)) {
       const int nblk = s.c1 - s.c0;
-      auto page_of = [&](int i) -> int32_t {  // page of block i of the segment, -1: none
+      auto page_of = [&](int i) -> int32_t {  // page of the segment's block i from the newest, -1: none
         if (i >= nblk) return -1;
-        const int32_t page = A.table[(int64_t)s.r * A.per + ((s.c0 + i) >> bshift)];
+        const int32_t page = A.table[(int64_t)s.r * A.per + ((s.c1 - 1 - i) >> bshift)];
         if (page >= 0 && page < A.pages) return page;
         if (A.bad) atomicOr(A.bad, 1);
         return -1;
       };
       int32_t page = page_of(lane), page_n = -1;
       for (int g0 = 0; ok && g0 < nblk; g0 += 32) {  // lane l: block g0 + l
-        const int sub = (s.c0 + g0 + lane) & bmask;
+        const int sub = (s.c1 - 1 - g0 - lane) & bmask;
         const int64_t head = (int64_t)page * A.Hkv + s.h;
         float ks = 0.f, vs = 0.f;
         if (page >= 0) {
@@ -448,7 +479,8 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
           S.slope[x] = EX && A.slopes && has ? A.slopes[head] * LOG2E : 0.f;
           S.hi[x] = has ? p : -1;
           S.lo[x] = A.window > 0 ? p - A.window + 1 : 0;
-          S.m[x] = -INFINITY;
+          S.m[x] = S.most[x] = -INFINITY;
+          S.mref[x] = 0.f;
         }
       }
       fence_proxy_async_smem();
@@ -469,28 +501,31 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
         const int blk = tok >> 4;
         const float ks = M.ks[blk], vs = M.vs[blk], vmax = M.vmax;
         const uint32_t okm = M.ok;
-        const int key0 = (s.c0 + i * TBLK) * 16, key = key0 + tok;
+        const int newest = s.c1 - 1 - i * TBLK;  // block; the tile's others lie before it
+        const int key = (newest - blk) * 16 + (tok & 15);
         ok = ok && wait(sfull + 8 * (tc & 1), (tc >> 1) & 1);
         tc_fence_after();
         float sc[QW];
+        {
+          uint32_t v[QW / 8][16];
 #pragma unroll
-        for (int j = 0; j < QW / 8; ++j) {
-          uint32_t v[16];
-          tmem_ld_32x32b_x16(tSq + (tc & 1) * G::N + 16 * j, v);
+          for (int j = 0; j < QW / 8; ++j) tmem_ld_32x32b_x16(tSq + (tc & 1) * G::N + 16 * j, v[j]);
           tmem_ld_wait();
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            sc[8 * j + q] = fmaf(__uint_as_float(v[8 + q]), 1.f / BSCALE, __uint_as_float(v[q])) * ks;
+          for (int j = 0; j < QW / 8; ++j)
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              sc[8 * j + q] = fmaf(__uint_as_float(v[j][8 + q]), 1.f / BSCALE, __uint_as_float(v[j][q]));
         }
 #pragma unroll
         for (int q = 0; q < QW; ++q) {
-          sc[q] *= S.cf[x0 + q];
+          sc[q] *= ks * S.cf[x0 + q];
           if (EX) {
             if (A.softcap > 0.f) sc[q] = A.softcap * LOG2E * cap_tanh(sc[q]);
             sc[q] -= S.slope[x0 + q] * (float)(S.hi[x0 + q] - key);
           }
         }
-        if (okm != 0xffu || key0 + TOK - 1 > all_hi || key0 < all_lo) {  // some query does not see some token
+        if (okm != 0xffu || newest * 16 + 15 > all_hi || (newest - TBLK + 1) * 16 < all_lo) {  // some query does not see some token
           // V rows that no query sees must not hold NaN codes, and a NaN code of
           // one that some see reaches exactly those, through their scores
           const bool there = (okm >> blk) & 1u, dead = !there || key > any_hi;
@@ -519,7 +554,7 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
         }
         bool over = vmax > vref;
 #pragma unroll
-        for (int q = 0; q < QW; ++q) over = over || sc[q] > S.m[x0 + q] + T_LAG;
+        for (int q = 0; q < QW; ++q) over = over || sc[q] > S.most[x0 + q];
         bool waited = tc == 0;
         if (ssync_or(1 + wg, 128, over)) {  // raise the running maximum (and V's reference): O and l in the new units
 #pragma unroll
@@ -535,6 +570,8 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
             const float nm = fmaxf(old, top);
             S.al[x] = old == -INFINITY ? 0.f : exp2_fast(old - nm);
             S.m[x] = nm;
+            S.most[x] = nm + T_LAG;
+            S.mref[x] = nm == -INFINITY ? 0.f : nm;
           }
           if (!waited) ok = ok && wait(pvdone, (tc - 1) & 1);
           waited = true;
@@ -567,22 +604,32 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
           float w[8];
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
-            const float m = S.m[x0 + 8 * j + q];
-            const float p = exp2_fast(sc[8 * j + q] - (m == -INFINITY ? 0.f : m));
+            const float p = exp2_fast(sc[8 * j + q] - S.mref[x0 + 8 * j + q]);
             l[8 * j + q] += p;
             w[q] = p * wv;
           }
           uint2 a[L], b[L];
+          if (L == 2) {  // fp16 (2^-11) as three limbs: what each leaves is exact in fp16
+            uint32_t h[4];
 #pragma unroll
-          for (int p = 0; p < 2 * L; ++p) {
-            uint2 c = make_uint2(0u, 0u);
-            if (p < PL) c = limb8(w, p + 1 < PL);
-            if (p == L - 1) {
+            for (int q = 0; q < 4; ++q) h[q] = pack_f16x2(w[2 * q], w[2 * q + 1]);
+            a[0] = limb8h(h, true);
+            a[1] = limb8h(h, true);
 #pragma unroll
-              for (int q = 0; q < 8; ++q) w[q] *= BSCALE;
+            for (int q = 0; q < 4; ++q) h[q] = hmul2_bits(h[q], 0x5c005c00u);  // times 256
+            b[0] = limb8h(h, false);
+            b[1] = make_uint2(0u, 0u);
+          } else {
+#pragma unroll
+            for (int p = 0; p < 2 * L; ++p) {
+              const uint2 c = limb8(w, p + 1 < 2 * L);
+              if (p == L - 1) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) w[q] *= BSCALE;
+              }
+              if (p < L) a[p % L] = c;
+              else b[p % L] = c;
             }
-            if (p < L) a[p] = c;
-            else b[p - L] = c;
           }
 #pragma unroll
           for (int p = 0; p < L; ++p)

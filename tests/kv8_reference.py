@@ -140,9 +140,9 @@ def attention(pool, q, q_off, kv_len, table, scale, softcap=0.0, window=0, slope
     cap (tanh from exp within 2^-21 of the cap) and bias rounded in fp32; e^s
     within 2^-21 and the running maximum's rescaling within another 2^-21.
     The weights are rounded to at least 2^-11 of themselves for 16-bit outputs,
-    2^-21 for fp32 ones, but no finer than an absolute F = 2^-25 (fp32: 2^-29)
+    2^-21 for fp32 ones, but no finer than an absolute F = 2^-23 (fp32: 2^-27)
     of the largest weight, in units of the largest V scale: that is half the
-    smallest e4m3 step, 2^-10, over the weights' scale 2^7 and the last limbs'
+    smallest e4m3 step, 2^-10, over the weights' scale 2^5 and the last limbs'
     2^8 (2^12).  Such a weight p_j changes by at most min(p_j, F vmax / vs_j).
     (p_j relative to the running maximum: at most twice that to the true one;
     the sum of weights is at least 1.)  The sums over n keys are within n 2^-23
@@ -158,7 +158,7 @@ def attention(pool, q, q_off, kv_len, table, scale, softcap=0.0, window=0, slope
     lse = torch.full((T, H_q), math.nan, dtype=torch.float64, device=dev)
     tol, tol_l = torch.zeros_like(out), torch.zeros_like(lse)
     p_round = 2.0 ** -21 if q.dtype == torch.float32 else 2.0 ** -11
-    floor = 2.0 ** -29 if q.dtype == torch.float32 else 2.0 ** -25
+    floor = 2.0 ** -27 if q.dtype == torch.float32 else 2.0 ** -23
     eps = torch.finfo(q.dtype).eps / 2
     P = k.shape[2]
     table = np.asarray(table)
