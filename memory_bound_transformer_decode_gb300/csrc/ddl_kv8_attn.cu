@@ -777,7 +777,7 @@ extern "C" int ddl_kv8_attention(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, i
   const void* fn = nullptr;
   void* args[] = {&a};
   if (tc) {
-    st = kv8_tc_launch(a, dtype, ex, pool_rows, stream);
+    st = kv8_tc_launch(a, dtype, pool_rows, stream);
   } else {
     fn = kv->type == DDL_KV8_E4M3 ? att_fn<DDL_KV8_E4M3>(dtype, head_dim, ex) : att_fn<DDL_KV8_INT8>(dtype, head_dim, ex);
     const size_t smem = pl.whole ? 0 : (size_t)(R + 1) * 8;

@@ -226,6 +226,6 @@ __device__ __forceinline__ void store_elem(void* p, int64_t i, float v) {
 __device__ __forceinline__ float cap_tanh(float x) { return 1.f - __fdividef(2.f, __expf(2.f * x) + 1.f); }
 
 // The tcgen05 kernel (e4m3, head_dim 128): rows of the pool's view < 2^31.
-int kv8_tc_launch(const AttArgs& a, int dtype, bool ex, int64_t rows, void* stream);
+int kv8_tc_launch(const AttArgs& a, int dtype, int64_t rows, void* stream);
 
 }  // namespace ddl

@@ -75,9 +75,10 @@ struct Meta {  // of a stage's tile
 template <int NT, int L>
 struct Shared {
   Meta meta[Geo<NT, L>::STAGES];
-  alignas(16) float cf[8 * NT], slope[8 * NT], m[8 * NT], al[8 * NT];
+  alignas(16) float cf[8 * NT], slope[8 * NT], hif[8 * NT], m[8 * NT], al[8 * NT];
   alignas(16) float most[8 * NT], mref[8 * NT];  // m + T_LAG; m, 0 for -inf
   int32_t hi[8 * NT], lo[8 * NT];
+  int64_t place[8 * NT];
   float wred[4][8 * NT];
   uint32_t nan[2][4];
   uint64_t fullk[3], fullv[3], empty[3], sfull[2], pfull, pvdone, qfull, fin;
@@ -123,6 +124,24 @@ __device__ __forceinline__ float warp_fmax(float x) {
   const int b = __float_as_int(x), k = b ^ ((b >> 31) & 0x7fffffff);  // ordered as the values
   const int t = __reduce_max_sync(FULL, k);
   return __int_as_float(t ^ ((t >> 31) & 0x7fffffff));
+}
+
+// Sums over the warp of N values per lane: lane q ends with value q's in v[0].
+// Every step halves the values a lane carries (N + log2(32 / N) shuffles).
+template <int N>
+__device__ __forceinline__ void warp_sums(float (&v)[N]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int n = N / 2; n > 0; n >>= 1) {
+    const bool up = lane & n;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+      v[i] = keep + __shfl_xor_sync(FULL, give, n);
+    }
+  }
+#pragma unroll
+  for (int o = N; o < 32; o <<= 1) v[0] += __shfl_xor_sync(FULL, v[0], o);
 }
 
 // Eight values as e4m3 codes (byte i = value i), and what they leave.
@@ -216,7 +235,8 @@ struct Segs {
   }
 };
 
-template <int DT, bool EX, int NT>
+// EX: 0 plain scores, 1 a distance bias, 2 a cap (and a bias).
+template <int DT, int EX, int NT>
 __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) kv8_tc_kernel(const __grid_constant__ TcAtt P) {
   constexpr int L = DT == DDL_T_F32 ? 3 : 2;
   constexpr float BSCALE = DT == DDL_T_F32 ? 4096.f : 256.f;  // 16^L
@@ -427,22 +447,26 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
       const int nqueries = s.rq.n * A.GH, q0 = s.qc * NQ;
       const int nblk = s.c1 - s.c0, nt = (nblk + TBLK - 1) / TBLK;
       ssync(3, NS);  // the previous segment's readers of the shared values are done
-      // Q's limbs: 16 lanes a query, 8 head dimensions each
-#pragma unroll 1
-      for (int x = warp * 2 + (lane >> 4); x < NQ; x += 8 * WG) {
-        const int qi = q0 + x, c = lane & 15;
+      // Q's limbs: 16 lanes a query, 8 head dimensions each; the loads of all rounds go out together
+      constexpr int ROUNDS = NQ / (8 * WG);
+      float4 qv[ROUNDS][2];
+#pragma unroll
+      for (int u = 0; u < ROUNDS; ++u) {
+        const int qi = q0 + warp * 2 + (lane >> 4) + u * 8 * WG;
+        qv[u][0] = qv[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (qi < nqueries) {
+          const int row = group_row(A, qi), head = s.h * A.GH + qi - row * A.GH;
+          const int64_t at = (int64_t)(s.rq.row0 + row) * A.q_stride + (int64_t)head * 128 + (lane & 15) * 8;
+          qv[u][0] = load_elem4<DT>(A.q, at);
+          qv[u][1] = load_elem4<DT>(A.q, at + 4);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < ROUNDS; ++u) {
+        const int x = warp * 2 + (lane >> 4) + u * 8 * WG, qi = q0 + x, c = lane & 15;
         const bool has = qi < nqueries;
         const int row = has ? group_row(A, qi) : 0, head = s.h * A.GH + (has ? qi - row * A.GH : 0);
-        float v[8];
-        if (has) {
-          const int64_t at = (int64_t)(s.rq.row0 + row) * A.q_stride + (int64_t)head * 128 + c * 8;
-          const float4 a = load_elem4<DT>(A.q, at), b = load_elem4<DT>(A.q, at + 4);
-          v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-          v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = 0.f;
-        }
+        float v[8] = {qv[u][0].x, qv[u][0].y, qv[u][0].z, qv[u][0].w, qv[u][1].x, qv[u][1].y, qv[u][1].z, qv[u][1].w};
         float mx = 0.f;
         bool bad = false;
 #pragma unroll
@@ -473,10 +497,13 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
         if (c == 0) {
           const int p = s.rq.p0 + row;
           float cf = up * A.scale;
-          if (EX && A.softcap > 0.f) cf = __fdiv_rn(cf, A.softcap);
+          if (EX == 2) cf = __fdiv_rn(cf, A.softcap);
           else cf *= LOG2E;
           S.cf[x] = cf;
-          S.slope[x] = EX && A.slopes && has ? A.slopes[head] * LOG2E : 0.f;
+          if (EX) {
+            S.slope[x] = A.slopes && has ? A.slopes[head] * LOG2E : 0.f;
+            S.hif[x] = (float)(p - s.c1 * 16);
+          }
           S.hi[x] = has ? p : -1;
           S.lo[x] = A.window > 0 ? p - A.window + 1 : 0;
           S.m[x] = S.most[x] = -INFINITY;
@@ -503,6 +530,7 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
         const uint32_t okm = M.ok;
         const int newest = s.c1 - 1 - i * TBLK;  // block; the tile's others lie before it
         const int key = (newest - blk) * 16 + (tok & 15);
+        const float back_of = (float)(s.c1 * 16 - key);
         ok = ok && wait(sfull + 8 * (tc & 1), (tc >> 1) & 1);
         tc_fence_after();
         float sc[QW];
@@ -520,10 +548,8 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
 #pragma unroll
         for (int q = 0; q < QW; ++q) {
           sc[q] *= ks * S.cf[x0 + q];
-          if (EX) {
-            if (A.softcap > 0.f) sc[q] = A.softcap * LOG2E * cap_tanh(sc[q]);
-            sc[q] -= S.slope[x0 + q] * (float)(S.hi[x0 + q] - key);
-          }
+          if (EX == 2) sc[q] = A.softcap * LOG2E * cap_tanh(sc[q]);
+          if (EX) sc[q] = fmaf(-S.slope[x0 + q], S.hif[x0 + q] + back_of, sc[q]);  // (distances: exact to 2^24)
         }
         if (okm != 0xffu || newest * 16 + 15 > all_hi || (newest - TBLK + 1) * 16 < all_lo) {  // some query does not see some token
           // V rows that no query sees must not hold NaN codes, and a NaN code of
@@ -642,16 +668,31 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
         if (lane == 0) mbar_arrive(pfull);
       }
       // the result: thread = head dimension
-#pragma unroll
-      for (int q = 0; q < QW; ++q) {
-#pragma unroll
-        for (int o = 16; o; o >>= 1) l[q] += __shfl_xor_sync(FULL, l[q], o);
-        if (lane == 0) S.wred[warp & 3][x0 + q] = l[q];
-      }
+      warp_sums(l);  // lane q (and q + QW): the warp's sum of query q
+      if (lane < QW) S.wred[warp & 3][x0 + lane] = l[0];
       if (nt > 0) ok = ok && wait(pvdone, (tc - 1) & 1);
       tc_fence_after();
       if (ssync_or(3, NS, !ok)) break;
-      const float back = vref * (1.f / TP_SCALE);
+      if (tok < QW) {  // thread q: the query's place, factor and statistics
+        const int x = x0 + tok, qi = q0 + x;
+        const float lq = (S.wred[0][x] + S.wred[1][x]) + (S.wred[2][x] + S.wred[3][x]), m = S.m[x];
+        float f = vref * (1.f / TP_SCALE);
+        int64_t place = -1;
+        if (qi < nqueries) {
+          const int row = group_row(A, qi), head = s.h * A.GH + qi - row * A.GH;
+          if (s.direct) {
+            place = (int64_t)(s.rq.row0 + row) * A.out_stride + (int64_t)head * 128;
+            f = lq != 0.f ? f / lq : 0.f;  // (NaN stays NaN)
+            if (A.lse) A.lse[(int64_t)(s.rq.row0 + row) * A.Hq + head] = (m + log2f(lq)) * LN2;
+          } else {
+            place = (s.rec * NQ + x) * 128;
+            *reinterpret_cast<float2*>(A.rec_ml + (s.rec * NQ + x) * 2) = make_float2(m, lq);
+          }
+        }
+        S.al[x] = f;
+        S.place[x] = place;
+      }
+      ssync(1 + wg, 128);
 #pragma unroll
       for (int j = 0; j < QW / 8; ++j) {
         uint32_t v[16];
@@ -664,20 +705,12 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
         }
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          const int x = x0 + 8 * j + q, qi = q0 + x;
-          if (qi >= nqueries) continue;
-          const float o = fmaf(__uint_as_float(v[8 + q]), 1.f / BSCALE, __uint_as_float(v[q])) * back;
-          const float lq = (S.wred[0][x] + S.wred[1][x]) + (S.wred[2][x] + S.wred[3][x]);
-          if (s.direct) {
-            const int row = group_row(A, qi), head = s.h * A.GH + qi - row * A.GH;
-            const float inv = lq != 0.f ? 1.f / lq : 0.f;  // (NaN stays NaN)
-            store_elem<DT>(A.out, (int64_t)(s.rq.row0 + row) * A.out_stride + (int64_t)head * 128 + tok, o * inv);
-            if (tok == 0 && A.lse) A.lse[(int64_t)(s.rq.row0 + row) * A.Hq + head] = (S.m[x] + log2f(lq)) * LN2;
-          } else {
-            const int64_t at = s.rec * NQ + x;
-            A.rec_o[at * 128 + tok] = o;
-            if (tok == 0) *reinterpret_cast<float2*>(A.rec_ml + at * 2) = make_float2(S.m[x], lq);
-          }
+          const int x = x0 + 8 * j + q;
+          const int64_t place = S.place[x];
+          const float o = fmaf(__uint_as_float(v[8 + q]), 1.f / BSCALE, __uint_as_float(v[q])) * S.al[x];
+          if (place < 0) continue;
+          if (s.direct) store_elem<DT>(A.out, place + tok, o);
+          else A.rec_o[place + tok] = o;
         }
       }
       tc_fence_before();
@@ -691,10 +724,14 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
   }
 }
 
-template <int DT, bool EX>
+template <int DT, int EX>
 const void* tc_fn(int nt) {
   return nt == 1 ? (const void*)kv8_tc_kernel<DT, EX, 1> : nt == 2 ? (const void*)kv8_tc_kernel<DT, EX, 2>
                                                                    : (const void*)kv8_tc_kernel<DT, EX, 4>;
+}
+template <int DT>
+const void* tc_fn(int ex, int nt) {
+  return ex == 2 ? tc_fn<DT, 2>(nt) : ex == 1 ? tc_fn<DT, 1>(nt) : tc_fn<DT, 0>(nt);
 }
 template <int NT>
 size_t tc_smem(bool f32) {
@@ -717,16 +754,17 @@ int encode_map(CUtensorMap* m, const uint8_t* base, int64_t rows) {
 }  // namespace
 
 // rows: of the pool's [pages * H_kv * page_size][128] view, < 2^31.
-int kv8_tc_launch(const AttArgs& a, int dtype, bool ex, int64_t rows, void* stream) {
+int kv8_tc_launch(const AttArgs& a, int dtype, int64_t rows, void* stream) {
   TcAtt p;
   p.A = a;
   p.wait_ns = wait_limit_ns();
   int st;
   if ((st = encode_map(&p.kmap, a.k, rows)) || (st = encode_map(&p.vmap, a.v, rows))) return st;
   const int threads = a.nq == 1 ? Geo<1, 2>::THREADS : a.nq == 2 ? Geo<2, 2>::THREADS : Geo<4, 2>::THREADS;
-  const void* fn = dtype == DDL_T_F32    ? (ex ? tc_fn<DDL_T_F32, true>(a.nq) : tc_fn<DDL_T_F32, false>(a.nq))
-                   : dtype == DDL_T_BF16 ? (ex ? tc_fn<DDL_T_BF16, true>(a.nq) : tc_fn<DDL_T_BF16, false>(a.nq))
-                                         : (ex ? tc_fn<DDL_T_F16, true>(a.nq) : tc_fn<DDL_T_F16, false>(a.nq));
+  const int ex = a.softcap > 0.f ? 2 : a.slopes ? 1 : 0;
+  const void* fn = dtype == DDL_T_F32    ? tc_fn<DDL_T_F32>(ex, a.nq)
+                   : dtype == DDL_T_BF16 ? tc_fn<DDL_T_BF16>(ex, a.nq)
+                                         : tc_fn<DDL_T_F16>(ex, a.nq);
   const bool f32 = dtype == DDL_T_F32;
   const size_t smem = (a.nq == 1 ? tc_smem<1>(f32) : a.nq == 2 ? tc_smem<2>(f32) : tc_smem<4>(f32)) + 16 +
                       (a.whole ? 0 : (size_t)(a.R + 1) * 8);
