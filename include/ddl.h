@@ -281,7 +281,8 @@ int ddl_stack_decode_noalloc(const ddl_shape* shape, ddl_wtype wtype, const ddl_
  * A paged KV cache of half the bytes: 8-bit codes with one fp32 scale for
  * each block of DDL_KV8_BLOCK consecutive tokens and K/V head (value = code *
  * scale), and what a serving step does with it: place the step's rows
- * (ddl_page_plan), store them (ddl_kv8_append), attend (ddl_kv8_attention).
+ * (ddl_page_plan), store them (ddl_kv8_append), attend (ddl_kv8_attention);
+ * ddl_stack_step_kv8 is the layer stack on such caches.
  * Lengths, positions, page tables and slots are device arrays: no call of
  * this section copies from the host or waits for the device, so a captured
  * step can be replayed while they change.  None of these calls keeps anything
@@ -392,8 +393,9 @@ int ddl_kv8_append(const ddl_kv8* kv, int32_t H_kv, int32_t head_dim, ddl_dtype 
  *    (1 without q_off).  max_len >= 1: a bound on kv_len.  Both only size the
  *    launch; a request beyond them (or beyond its table row, or with rows
  *    outside [0, T)) is computed on what lies within them, and a page id
- *    outside the pool counts as a block without keys; either sets *bad_out
- *    (device int32, may be NULL, never cleared by the call) to 1.
+ *    outside the pool counts as a block without keys; either sets bit 0 of
+ *    *bad_out (device int32, may be NULL, never cleared by the call).  Bit 1:
+ *    a bounded device wait gave up (ddl_set_wait_limit_ns), the output is void.
  *  - scale: finite; softcap >= 0, window >= 0 (0: none); slopes: device fp32
  *    [H_q] or NULL.
  *  - workspace: device, >= ddl_kv8_attention_workspace_bytes(...) of the same
@@ -412,6 +414,34 @@ int ddl_kv8_attention(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, int32_t head
                       const int32_t* q_off, const int32_t* kv_len, const int32_t* page_table,
                       int32_t pages_per_seq, const void* q, int64_t q_stride, void* out, int64_t out_stride,
                       float* lse, int32_t* bad_out, void* workspace, size_t ws_bytes, void* stream);
+
+/* One step of an L-layer stack on 8-bit paged caches: the layers of
+ * ddl_stack_decode with ddl_kv8_append and ddl_kv8_attention in the place of
+ * the bf16 append and attention.  Takes ddl_page_plan's outputs as they are,
+ * so that decoding requests, prompt chunks and drafted rows go in one step and
+ * nothing of their lengths passes through the host:
+ *  - T rows (1 <= T <= DDL_MAX_BATCH; DDL_ERR_UNSUPPORTED) of R requests:
+ *    request r's rows are row_off[r] .. row_off[r + 1], the newest of its
+ *    kv_len[r] tokens; row i is at position row_pos[i] (its RoPE angle) and is
+ *    stored at slot[i].  Rows behind the last (slot and position -1) are
+ *    computed on an attention output of zeros and stored nowhere; the outputs'
+ *    rows for them have no meaning.
+ *  - kv: host array of L caches of one page_size and page count
+ *    (DDL_ERR_ARG).  k and v are rounded to bf16, then stored as
+ *    ddl_kv8_append says; q and the attention output are fp32.
+ *  - opts: NULL for scale = 1 / sqrt(head_dim) alone.
+ *  - max_rows, max_len, page_table, bad_out: as ddl_kv8_attention (and bit 1 of
+ *    *bad_out, value 2, where one of its bounded device waits gave up; the
+ *    other stages' waits: ddl_read_device_status with B = T and s_max = 1).
+ *  - resid_in / x_bf16, resid_out, out_bf16: [T][D], as ddl_stack_decode.
+ *  - workspace: >= ddl_stack_kv8_workspace_bytes(...) (0 for invalid sizes). */
+size_t ddl_stack_kv8_workspace_bytes(const ddl_shape* shape, int32_t R, int32_t T, int32_t max_rows, int32_t max_len);
+int ddl_stack_step_kv8(const ddl_shape* shape, ddl_wtype wtype, const ddl_layer_w* layers, const ddl_kv8* kv,
+                       int32_t L, const ddl_attn_opts* opts, int32_t R, int32_t T, int32_t max_rows, int32_t max_len,
+                       const int32_t* row_off, const int32_t* kv_len, const int32_t* row_pos, const int32_t* slot,
+                       const int32_t* page_table, int32_t pages_per_seq, const float* resid_in,
+                       const uint16_t* x_bf16, float* resid_out, uint16_t* out_bf16, int32_t* bad_out,
+                       void* workspace, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------ token step
  * The steps on either side of the layer stack in the primer's §1.2

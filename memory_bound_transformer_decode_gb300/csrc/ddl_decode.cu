@@ -38,6 +38,7 @@
 
 #include "ddl_device.cuh"
 #include "ddl_internal.h"
+#include "ddl_kv8.h"
 #include "ddl_tc.h"
 
 namespace ddl {
@@ -2670,16 +2671,60 @@ static int check_pages(const Paged& pg, int32_t B, const int64_t* posv, bool sha
   return DDL_OK;
 }
 
+// A step on the 8-bit paged cache (ddl_stack_step_kv8): the rows' placement
+// (device) and the scratch its QKV stages write K/V rows to, a bf16 cache of one
+// slot per row that ddl_kv8_append then stores from.
+struct Kv8Step {
+  const ddl_kv8* kv;
+  const ddl_attn_opts* opts;
+  int32_t R, max_rows, max_len, per;
+  const int32_t *row_off, *kv_len, *row_pos, *slot, *table;
+  int32_t* bad;
+  uint16_t *k, *v;  // [rows][H_kv][head_dim]
+  void* ws;
+  size_t ws_bytes;
+};
+
+// RoPE table of rows whose positions lie in device memory (a padding row's
+// negative one counts as 0), and position 0 of the scratch cache for all.
+__global__ void rope_rows_kernel(const int32_t* __restrict__ pos, double base, int hd, float* __restrict__ table,
+                                 int32_t* __restrict__ zero) {
+  const int b = blockIdx.x, i = threadIdx.x;
+  const int32_t p = pos[b] > 0 ? pos[b] : 0;
+  if (i < hd / 2) {
+    const double phi = (double)p * pow(base, -2.0 * i / (double)hd);
+    table[((int64_t)b * 64 + i) * 2] = (float)cos(phi);
+    table[((int64_t)b * 64 + i) * 2 + 1] = (float)sin(phi);
+  }
+  if (i == 0) zero[b] = 0;
+}
+
+// The wide-batch kernel's scale of its Wo input: the largest |attention output|
+// of each row (the attention stage it replaces leaves it there).
+__global__ void attn_max_kernel(const float* __restrict__ attn, int n, uint32_t* __restrict__ xmax) {
+  __shared__ float red[8];
+  float m = 0.f;
+  for (int i = threadIdx.x; i < n; i += 256) m = fmaxf(m, fabsf(attn[(int64_t)blockIdx.x * n + i]));
+  m = warp_max(m);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 8; ++w) m = fmaxf(m, red[w]);
+    xmax[blockIdx.x] = __float_as_uint(m);
+  }
+}
+
 // posv: NULL (every sequence at pos) or a host array of B positions (pos unused).
 // shared: the B rows are one sequence's consecutive tokens on one cache (prefill).
 // pg: paged caches (with posv), else NULL.
 static int decode(const ddl_shape* s, ddl_wtype wtype, const ddl_layer_w* layers, const ddl_kv* kv,
                   int32_t L, int32_t B, int64_t pos, const float* resid_in, const uint16_t* x_bf16,
                   float* resid_out, uint16_t* out_bf16, void* workspace, size_t ws_bytes,
-                  void* stream, const int64_t* posv = nullptr, bool shared = false, const Paged* pg = nullptr) {
+                  void* stream, const int64_t* posv = nullptr, bool shared = false, const Paged* pg = nullptr,
+                  const Kv8Step* k8 = nullptr) {
   int st = check_shape(s);
   if (st) return st;
-  if (!layers || !kv || L <= 0 || !workspace) return !workspace ? DDL_ERR_WORKSPACE : DDL_ERR_ARG;
+  if (!layers || (!kv && !k8) || L <= 0 || !workspace) return !workspace ? DDL_ERR_WORKSPACE : DDL_ERR_ARG;
   if (B < 1 || B > TC_MAX_B) return DDL_ERR_UNSUPPORTED;
   if (wtype != DDL_W_INT4 && wtype != DDL_W_BF16) return DDL_ERR_UNSUPPORTED;
   // the weight stages on the tcgen05 tensor cores: INT4 from TC_MIN_B
@@ -2687,7 +2732,8 @@ static int decode(const ddl_shape* s, ddl_wtype wtype, const ddl_layer_w* layers
   // activations, 8 bits, which miss the tolerance)
   const bool use_tc = (wtype == DDL_W_INT4 && B >= TC_MIN_B) || (wtype == DDL_W_BF16 && B > NARROW_B);
   if (!resid_in && !x_bf16) return DDL_ERR_ARG;
-  const int64_t s_max = kv[0].s_max;
+  auto cache = [&](int l) { return k8 ? ddl_kv{k8->k, k8->v, 1} : kv[l]; };
+  const int64_t s_max = cache(0).s_max;
   // rows of a layer's cache view (the TMA tensor map's outer dimension, 32-bit in the kernel)
   const int64_t kv_rows = pg ? pg->pages * s->H_kv * pg->page_size : (shared ? 1 : (int64_t)B) * s->H_kv * s_max;
   if (kv_rows >= (1ll << 31) || (int64_t)B * s->H_kv * s_max >= (1ll << 31)) return DDL_ERR_UNSUPPORTED;
@@ -2701,11 +2747,11 @@ static int decode(const ddl_shape* s, ddl_wtype wtype, const ddl_layer_w* layers
   if (pos < 0 || pos >= s_max) return DDL_ERR_POS;
   if (pg && (!posv || (st = check_pages(*pg, B, posv, shared)))) return posv ? st : DDL_ERR_ARG;
   for (int l = 0; l < L; ++l) {
-    if (!layers[l].packed || !layers[l].norm1 || !layers[l].norm2 || !kv[l].k || !kv[l].v)
-      return DDL_ERR_ARG;
-    if (kv[l].s_max != s_max) return DDL_ERR_ARG;
+    const ddl_kv c = cache(l);
+    if (!layers[l].packed || !layers[l].norm1 || !layers[l].norm2 || !c.k || !c.v) return DDL_ERR_ARG;
+    if (c.s_max != s_max) return DDL_ERR_ARG;
     if (!aligned16(layers[l].packed) || !aligned16(layers[l].norm1) || !aligned16(layers[l].norm2) ||
-        !aligned16(kv[l].k) || !aligned16(kv[l].v))
+        !aligned16(c.k) || !aligned16(c.v))
       return DDL_ERR_ALIGN;
   }
   if (!aligned16(workspace) || (resid_in && !aligned16(resid_in)) || (x_bf16 && !aligned16(x_bf16)) ||
@@ -2754,7 +2800,7 @@ static int decode(const ddl_shape* s, ddl_wtype wtype, const ddl_layer_w* layers
   P.q = (float*)(ws + w.q); P.attn = (float*)(ws + w.attn); P.y = (float*)(ws + w.y);
   P.a = (float*)(ws + w.a);
   P.ximg[0] = P.ximg[1] = nullptr;
-  if (w.ximg_bytes > 0 && (int64_t)s->D / 8 * B * 4 <= NW_HS_OFF) {  // (batches up to IMG_MAX_B)
+  if (!k8 && w.ximg_bytes > 0 && (int64_t)s->D / 8 * B * 4 <= NW_HS_OFF) {  // (batches up to IMG_MAX_B)
     P.ximg[0] = ws + w.ximg;
     P.ximg[1] = ws + w.ximg + w.ximg_bytes;
   }
@@ -2770,7 +2816,8 @@ static int decode(const ddl_shape* s, ddl_wtype wtype, const ddl_layer_w* layers
     rf.B = B;
     rf.table = (float*)(ws + w.rope);
     rf.pos = (int32_t*)(ws + w.rope + (int64_t)B * 64 * 2 * 4);
-    rope_fill_kernel<<<B, 64, 0, cs>>>(rf);
+    if (k8) rope_rows_kernel<<<B, 64, 0, cs>>>(k8->row_pos, rf.base, HD, rf.table, rf.pos);
+    else rope_fill_kernel<<<B, 64, 0, cs>>>(rf);
     if ((e = cudaGetLastError()) != cudaSuccess) return cuda_status(e);
     P.ragged = 1;
     for (int b = 0; b < B; ++b) P.posb[b] = (int32_t)posv[b];
@@ -2790,10 +2837,24 @@ static int decode(const ddl_shape* s, ddl_wtype wtype, const ddl_layer_w* layers
   // stay empty from stage to stage within a launch)
   if ((e = cudaMemsetAsync(ws + w.gpart, 0xFF, (size_t)(w.apart - w.gpart), cs)) != cudaSuccess)
     return cuda_status(e);
-  const bool coop = di.coop && g_launch_mode == 0 && !use_tc;
+  // (rows that belong to no request keep zeros for an attention output)
+  if (k8 && (e = cudaMemsetAsync(P.attn, 0, (size_t)B * s->H_q * HD * 4, cs)) != cudaSuccess) return cuda_status(e);
+  const bool coop = di.coop && g_launch_mode == 0 && !use_tc && !k8;
   const bool wide = B > NARROW_B;  // INT4, or only the attention stage (tensor-core path)
   // (bf16 weights past NARROW_B run only the attention stage, on the INT4 wide instance)
   const int wsel = (wide || wtype == DDL_W_INT4) ? DDL_W_INT4 : DDL_W_BF16;
+  // The attention of launch-local layer l (global layer gl) on its 8-bit cache.
+  auto attend_kv8 = [&](int l, int gl) -> int {
+    const int Nq = s->H_q * HD, Nkv = s->H_kv * HD;
+    int rc = ddl_kv8_append(&k8->kv[gl], s->H_kv, HD, DDL_T_BF16, k8->k, Nkv, k8->v, Nkv, k8->slot, B, k8->bad, stream);
+    if (rc) return rc;
+    rc = ddl_kv8_attention(&k8->kv[gl], s->H_q, s->H_kv, HD, DDL_T_F32, k8->opts, k8->R, B, k8->max_rows, k8->max_len,
+                           k8->row_off, k8->kv_len, k8->table, k8->per, P.q, Nq, P.attn, Nq, nullptr, k8->bad, k8->ws,
+                           k8->ws_bytes, stream);
+    if (rc || use_tc || !wide) return rc;
+    attn_max_kernel<<<B, 256, 0, cs>>>(P.attn, Nq, P.xmax + (l * NSTAGE + ST_WO) * MAX_B);
+    return cuda_status(cudaGetLastError());
+  };
   void* fn = nullptr;
 #define DDL_PICK(HDV, WTV, WIDEV)                                                                           \
   fn = posv ? (void*)decode_kernel<HDV, WTV, WIDEV, true> : (void*)decode_kernel<HDV, WTV, WIDEV, false>
@@ -2816,10 +2877,11 @@ static int decode(const ddl_shape* s, ddl_wtype wtype, const ddl_layer_w* layers
       P.layers[l].packed = (const uint8_t*)layers[l0 + l].packed;
       P.layers[l].norm1 = layers[l0 + l].norm1;
       P.layers[l].norm2 = layers[l0 + l].norm2;
-      P.layers[l].kc = kv[l0 + l].k;
-      P.layers[l].vc = kv[l0 + l].v;
-      if ((st = encode_kv_map(&P.kmap[l], kv[l0 + l].k, kv_rows, HD)) != DDL_OK ||
-          (st = encode_kv_map(&P.vmap[l], kv[l0 + l].v, kv_rows, HD)) != DDL_OK)
+      const ddl_kv c = cache(l0 + l);
+      P.layers[l].kc = c.k;
+      P.layers[l].vc = c.v;
+      if ((st = encode_kv_map(&P.kmap[l], c.k, kv_rows, HD)) != DDL_OK ||
+          (st = encode_kv_map(&P.vmap[l], c.v, kv_rows, HD)) != DDL_OK)
         return st;
     }
     const size_t need_trace = (size_t)nL * NSTAGE * C * TRACE_WORDS * 8;
@@ -2854,11 +2916,15 @@ static int decode(const ddl_shape* s, ddl_wtype wtype, const ddl_layer_w* layers
       P.trace = nullptr;
       for (int l = 0; l < nL; ++l) {
         if ((st = tc_stage(R, l, ST_QKV, stream))) return st;
-        P.stage_begin = l * NSTAGE + ST_ATT;
-        P.stage_end = P.stage_begin + 1;
-        void* args[] = {&P};
-        if ((e = launch_pdl(fn, dim3(C), dim3(NTHREADS_ALL), args, SM_TOTAL, cs)) != cudaSuccess)
-          return cuda_status(e);
+        if (k8) {
+          if ((st = attend_kv8(l, l0 + l))) return st;
+        } else {
+          P.stage_begin = l * NSTAGE + ST_ATT;
+          P.stage_end = P.stage_begin + 1;
+          void* args[] = {&P};
+          if ((e = launch_pdl(fn, dim3(C), dim3(NTHREADS_ALL), args, SM_TOTAL, cs)) != cudaSuccess)
+            return cuda_status(e);
+        }
         for (int stg : {ST_WO, ST_GU, ST_DOWN})
           if ((st = tc_stage(R, l, stg, stream))) return st;
       }
@@ -2873,6 +2939,10 @@ static int decode(const ddl_shape* s, ddl_wtype wtype, const ddl_layer_w* layers
     } else {
       P.cooperative = 0;
       for (int sidx = 0; sidx < nL * NSTAGE; ++sidx) {
+        if (k8 && sidx % NSTAGE == ST_ATT) {
+          if ((st = attend_kv8(sidx / NSTAGE, l0 + sidx / NSTAGE))) return st;
+          continue;
+        }
         P.stage_begin = sidx;
         P.stage_end = sidx + 1;
         if (P.trace) P.trace = g_trace + (size_t)sidx * C * TRACE_WORDS;
@@ -3006,6 +3076,57 @@ extern "C" int ddl_stack_prefill_paged(const ddl_shape* shape, ddl_wtype wtype, 
   for (int i = 0; i < S; ++i) pos[i] = p0 + i;
   return decode(shape, wtype, layers, views.data(), L, S, 0, resid_in, x_bf16, resid_out, out_bf16, workspace,
                 ws_bytes, stream, pos, true, &pg);
+}
+
+extern "C" size_t ddl_stack_kv8_workspace_bytes(const ddl_shape* shape, int32_t R, int32_t T, int32_t max_rows,
+                                                int32_t max_len) {
+  if (check_shape(shape)) return 0;
+  const size_t base = ddl_workspace_bytes(shape, T, 1);
+  const size_t att = ddl_kv8_attention_workspace_bytes(shape->H_q, shape->H_kv, shape->head_dim, R, T, max_rows, max_len);
+  if (!base || !att) return 0;
+  return (size_t)(align256((int64_t)base) + 2 * align256((int64_t)T * shape->H_kv * shape->head_dim * 2)) + att;
+}
+
+extern "C" int ddl_stack_step_kv8(const ddl_shape* shape, ddl_wtype wtype, const ddl_layer_w* layers,
+                                  const ddl_kv8* kv, int32_t L, const ddl_attn_opts* opts, int32_t R, int32_t T,
+                                  int32_t max_rows, int32_t max_len, const int32_t* row_off, const int32_t* kv_len,
+                                  const int32_t* row_pos, const int32_t* slot, const int32_t* page_table,
+                                  int32_t pages_per_seq, const float* resid_in, const uint16_t* x_bf16,
+                                  float* resid_out, uint16_t* out_bf16, int32_t* bad_out, void* workspace,
+                                  size_t ws_bytes, void* stream) {
+  int st = check_shape(shape);
+  if (st) return st;
+  if (!kv || L <= 0 || !row_off || !kv_len || !row_pos || !slot || !page_table) return DDL_ERR_ARG;
+  if (T < 1 || T > TC_MAX_B) return DDL_ERR_UNSUPPORTED;
+  for (const void* p : {(const void*)row_off, (const void*)kv_len, (const void*)row_pos, (const void*)slot,
+                        (const void*)page_table, (const void*)bad_out})
+    if ((uintptr_t)p & 3u) return DDL_ERR_ALIGN;
+  for (int l = 0; l < L; ++l) {
+    if ((st = check_kv8(kv + l, shape->H_kv, shape->head_dim))) return st;
+    if (kv[l].page_size != kv[0].page_size || kv[l].pages != kv[0].pages) return DDL_ERR_ARG;
+  }
+  if (!workspace) return DDL_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return DDL_ERR_ALIGN;
+  // the arguments that only the attention checks, before anything is launched
+  if (R < 1 || max_rows < 1 || max_len < 1 || pages_per_seq < 1) return DDL_ERR_ARG;
+  if (R > DDL_KV8_MAX_REQS || max_rows > DDL_KV8_MAX_ROWS || (int64_t)pages_per_seq * kv[0].page_size > 0x7fffffffLL)
+    return DDL_ERR_UNSUPPORTED;
+  ddl_attn_opts plain = {1.f / sqrtf((float)shape->head_dim), 0.f, 0, nullptr};
+  if (!opts) opts = &plain;
+  if ((st = check_attn_opts(opts))) return st;
+  DevInfo di;
+  if ((st = device_info(di))) return st;
+  const size_t need = ddl_stack_kv8_workspace_bytes(shape, R, T, max_rows, max_len);
+  if (need == 0) return DDL_ERR_UNSUPPORTED;
+  if (ws_bytes < need) return DDL_ERR_WORKSPACE;
+  const size_t base = (size_t)align256((int64_t)ddl_workspace_bytes(shape, T, 1));
+  const size_t rows = (size_t)align256((int64_t)T * shape->H_kv * shape->head_dim * 2);
+  uint8_t* extra = (uint8_t*)workspace + base;
+  const Kv8Step k8 = {kv, opts, R, max_rows, max_len, pages_per_seq, row_off, kv_len, row_pos, slot, page_table, bad_out,
+                      (uint16_t*)extra, (uint16_t*)(extra + rows), extra + 2 * rows, need - base - 2 * rows};
+  int64_t zero[TC_MAX_B] = {0};
+  return decode(shape, wtype, layers, nullptr, L, T, 0, resid_in, x_bf16, resid_out, out_bf16, workspace, base, stream,
+                zero, false, nullptr, &k8);
 }
 
 extern "C" int ddl_set_launch_mode(int32_t mode) {

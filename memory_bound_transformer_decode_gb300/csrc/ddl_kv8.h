@@ -2,6 +2,7 @@
 // checks of a pool descriptor and the code types' conversions.
 #pragma once
 #include <cuda_fp16.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "ddl_device.cuh"
@@ -24,6 +25,13 @@ inline int check_kv8(const ddl_kv8* kv, int32_t H_kv, int32_t hd) {
   if (!aligned16(kv->k) || !aligned16(kv->v) || !aligned16(kv->k_scale) || !aligned16(kv->v_scale))
     return DDL_ERR_ALIGN;
   return DDL_OK;
+}
+
+inline int check_attn_opts(const ddl_attn_opts* o) {
+  if (!o) return DDL_ERR_ARG;
+  if (!(fabsf(o->scale) < INFINITY) || !(o->softcap >= 0.f && o->softcap < INFINITY) || o->window < 0)
+    return DDL_ERR_ARG;
+  return ((uintptr_t)o->slopes & 3u) ? DDL_ERR_ALIGN : DDL_OK;
 }
 
 inline int log2_of(int32_t pow2) {

@@ -721,13 +721,12 @@ extern "C" int ddl_kv8_attention(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, i
   if (pages_per_seq < 1 || out == q) return DDL_ERR_ARG;
   if (!q_off && (max_rows != 1 || T < R)) return DDL_ERR_ARG;
   if ((int64_t)pages_per_seq * kv->page_size > 0x7fffffffLL) return DDL_ERR_UNSUPPORTED;
-  if (!(fabsf(opts->scale) < INFINITY) || !(opts->softcap >= 0.f && opts->softcap < INFINITY) || opts->window < 0)
-    return DDL_ERR_ARG;
+  if ((st = check_attn_opts(opts))) return st;
   const int64_t w = (int64_t)H_q * head_dim;
   if (q_stride < w || out_stride < w || q_stride % 8 || out_stride % 8) return DDL_ERR_ARG;
   if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return DDL_ERR_ALIGN;
   for (const void* p : {(const void*)q_off, (const void*)kv_len, (const void*)page_table, (const void*)lse,
-                        (const void*)bad_out, (const void*)opts->slopes})
+                        (const void*)bad_out})
     if ((uintptr_t)p & 3u) return DDL_ERR_ALIGN;
   AttPlan pl;
   const int64_t pool_rows = kv->pages * kv->page_size * H_kv;

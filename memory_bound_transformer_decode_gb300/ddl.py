@@ -28,7 +28,8 @@ EXPORTED = ("ddl_quantize_int4", "ddl_packed_layer_bytes", "ddl_pack_layer", "dd
             "ddl_last_cuda_error", "ddl_embed", "ddl_packed_head_bytes", "ddl_pack_head",
             "ddl_head_workspace_bytes", "ddl_lm_head", "ddl_stack_decode_ragged",
             "ddl_stack_prefill", "ddl_stack_decode_paged", "ddl_stack_prefill_paged",
-            "ddl_page_plan", "ddl_kv8_append", "ddl_kv8_attention_workspace_bytes", "ddl_kv8_attention")
+            "ddl_page_plan", "ddl_kv8_append", "ddl_kv8_attention_workspace_bytes", "ddl_kv8_attention",
+            "ddl_stack_kv8_workspace_bytes", "ddl_stack_step_kv8")
 
 
 class DDLError(RuntimeError):
@@ -150,6 +151,10 @@ def load(build_if_missing: bool = False):
         lib.ddl_kv8_attention_workspace_bytes.restype = sz
         lib.ddl_kv8_attention.argtypes = [P(KV8), i32, i32, i32, ctypes.c_int, P(AttnOpts), i32, i32, i32, i32, vp,
                                           vp, vp, i32, vp, i64, vp, i64, vp, vp, vp, sz, vp]
+        lib.ddl_stack_kv8_workspace_bytes.argtypes = [P(Shape), i32, i32, i32, i32]
+        lib.ddl_stack_kv8_workspace_bytes.restype = sz
+        lib.ddl_stack_step_kv8.argtypes = [P(Shape), ctypes.c_int, P(LayerW), P(KV8), i32, P(AttnOpts), i32, i32, i32,
+                                           i32, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, sz, vp]
         for name in EXPORTED:
             if not hasattr(lib, name):
                 raise RuntimeError(f"{path} does not export {name}")
@@ -581,6 +586,49 @@ def ddl_kv8_attention(pool, q: torch.Tensor, kv_len: torch.Tensor, page_table: t
             out.data_ptr(), os_, _f32("lse", lse, dev, T * H_q), None if bad is None else _i32("bad", bad, dev, 1),
             workspace.data_ptr(), workspace.nbytes)
     return out
+
+
+def ddl_stack_kv8_workspace_bytes(shape: Shape, R: int, T: int, max_rows: int, max_len: int) -> int:
+    n = int(load().ddl_stack_kv8_workspace_bytes(ctypes.byref(shape), R, T, max_rows, max_len))
+    if n == 0:
+        raise DDLError("ddl_stack_kv8_workspace_bytes", 1, _lib)
+    return n
+
+
+def ddl_stack_step_kv8(shape: Shape, wtype: int, layers: list, pools: list, *, row_off: torch.Tensor,
+                       kv_len: torch.Tensor, row_pos: torch.Tensor, slot: torch.Tensor, page_table: torch.Tensor,
+                       max_rows: int, max_len: int, x_bf16: torch.Tensor | None = None,
+                       resid_in: torch.Tensor | None = None, resid_out: torch.Tensor | None = None,
+                       out_bf16: torch.Tensor | None = None, scale: float | None = None, softcap: float = 0.0,
+                       window: int = 0, slopes: torch.Tensor | None = None, bad: torch.Tensor | None = None,
+                       workspace: torch.Tensor, stream=None):
+    """One step of len(layers) layers on 8-bit pools (one (k, v, k_scale,
+    v_scale) per layer) for the rows that ddl_page_plan has placed."""
+    lib = _lib or load()
+    x = x_bf16 if x_bf16 is not None else resid_in
+    T, R, L, dev = x.shape[0], kv_len.numel(), len(layers), x.get_device()
+    if len(pools) != L or page_table.dim() != 2 or page_table.shape[0] != R:
+        raise ValueError("a pool for each layer; page_table: [R, pages_per_seq]")
+    for name, t, dt in (("x_bf16", x_bf16, torch.bfloat16), ("resid_in", resid_in, torch.float32),
+                        ("resid_out", resid_out, torch.float32), ("out_bf16", out_bf16, torch.bfloat16)):
+        if t is not None and (t.dtype is not dt or t.get_device() != dev or not t.is_contiguous()
+                              or t.shape != (T, shape.D)):
+            raise ValueError(f"{name}: a contiguous [{T}, {shape.D}] {dt} tensor on cuda:{dev}")
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: contiguous, on cuda:{dev}")
+    lw, kv = (LayerW * L)(), (KV8 * L)()
+    for i, (layer, pool) in enumerate(zip(layers, pools)):
+        lw[i] = LayerW(layer["packed"].data_ptr(), layer["norm1"].data_ptr(), layer["norm2"].data_ptr())
+        kv[i], H, hd, d = _kv8(pool)
+        if H != shape.H_kv or hd != shape.head_dim or d != dev:
+            raise ValueError(f"pool {i}: [pages, {shape.H_kv}, page_size, {shape.head_dim}] on cuda:{dev}")
+    opts = AttnOpts(shape.head_dim ** -0.5 if scale is None else scale, softcap, window,
+                    _f32("slopes", slopes, dev, shape.H_q))
+    _run_on(dev, "ddl_stack_step_kv8", lib.ddl_stack_step_kv8, stream, shape, wtype, lw, kv, L, opts, R, T, max_rows,
+            max_len, _i32("row_off", row_off, dev, R + 1), _i32("kv_len", kv_len, dev, R),
+            _i32("row_pos", row_pos, dev, T), _i32("slot", slot, dev, T), _i32("page_table", page_table, dev, -1),
+            page_table.shape[1], *(None if t is None else t.data_ptr() for t in (resid_in, x_bf16, resid_out, out_bf16)),
+            None if bad is None else _i32("bad", bad, dev, 1), workspace.data_ptr(), workspace.nbytes)
 
 
 # ------------------------------------------------------------------ token step

@@ -147,6 +147,32 @@ def test_attention_refusals(lib):
     assert lib.ddl_kv8_attention_workspace_bytes(8, 2, 96, 1, 1, 1, 100) == 0
 
 
+def test_stack_step_refusals(lib):
+    if torch.cuda.is_available():
+        pytest.skip("host checks with fake pointers run without a GPU; tests/test_gpu_kv8_stack.py has real buffers")
+    v = lambda n: ctypes.c_void_p(256 * n)  # noqa: E731
+    shape = ddl.Shape(512, 8, 2, 64, 1408, 1e-6, 1e4)
+    lw = (ddl.LayerW * 2)(ddl.LayerW(256, 256, 256), ddl.LayerW(256, 256, 256))
+
+    def call(kv=None, opts=None, **kw):
+        kv = (ddl.KV8 * 2)(*(kv or [_kv(), _kv()]))
+        a = dict(kv=kv, L=2, opts=ddl.AttnOpts(*opts) if opts else None, R=2, T=3, rows=2, len=64, off=v(1), kl=v(2),
+                 pos=v(3), slot=v(4), tab=v(5), per=4, res=None, x=v(6), rout=None, out=v(7), bad=None, ws=v(8),
+                 n=1 << 30)
+        a.update(kw)
+        return lib.ddl_stack_step_kv8(ctypes.byref(shape), ddl.INT4, lw, *a.values(), None)
+
+    assert call() == 6  # past the host checks: no device here
+    for kw, code in BAD_POOLS:
+        assert call(kv=[_kv(), _kv(**kw)]) == code, kw
+    for kw, code in [(dict(kv=[_kv(), _kv(page_size=32)]), 8), (dict(kv=[_kv(), _kv(pages=11)]), 8), (dict(L=0), 8),
+                     (dict(T=0), 5), (dict(T=65), 5), (dict(off=None), 8), (dict(slot=None), 8), (dict(R=0), 8),
+                     (dict(rows=65), 5), (dict(rows=0), 8), (dict(len=0), 8), (dict(per=0), 8), (dict(per=1 << 28), 5),
+                     (dict(pos=ctypes.c_void_p(258)), 3), (dict(ws=None), 4), (dict(ws=ctypes.c_void_p(264)), 3),
+                     (dict(opts=(1.0, -1.0, 0, None)), 8), (dict(opts=(1.0, 0.0, 0, 258)), 3)]:
+        assert call(**kw) == code, kw
+
+
 def test_bindings_refuse_host_tensors(lib):
     pool = (torch.zeros((2, 1, 16, 64), dtype=torch.int8), torch.zeros((2, 1, 16, 64), dtype=torch.int8),
             torch.zeros((2, 1, 1)), torch.zeros((2, 1, 1)))
