@@ -1,7 +1,10 @@
-"""Builds the decode library (csrc/*.cu) for sm_103a into _build/libddl.so.
+"""Builds the decode library (csrc/*.cu) for sm_103a into _build/libddl.so, and
+the module of its per-layer calls for torch tensors (csrc/ddl_torch.cpp) into
+_build/_ddl_torch.so, which links against it.
 
-Plain nvcc, one translation unit per .cu file compiled in parallel, then a
-shared-library link; no CMake.  The result is loaded by ``ddl.py`` with ctypes.
+Plain nvcc and g++, one translation unit per file compiled in parallel, then the
+shared-library links; no CMake.  ``ddl.py`` loads the library with ctypes and
+imports the module.
 """
 from __future__ import annotations
 
@@ -10,11 +13,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libddl.so")
+TORCH_SRC = os.path.join(CSRC, "ddl_torch.cpp")
+TORCH_LIB = os.path.join(BUILD, "_ddl_torch.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xptxas", "-v"]
@@ -25,6 +31,17 @@ def _nvcc() -> str:
     if not os.path.exists(cand):
         raise RuntimeError("nvcc not found; the CUDA toolkit is required to build the library")
     return cand
+
+
+def _torch_dirs() -> tuple[list[str], str]:
+    """Include directories and the library directory of the installed torch."""
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    inc = os.path.join(root, "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    return [inc, os.path.join(inc, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"],
+            cuda], os.path.join(root, "lib")
 
 
 def sources() -> list[str]:
@@ -43,9 +60,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
     headers.append(os.path.join(HERE, "..", "include", "ddl.h"))
     srcs = sources()
-    if not force and not _stale(LIB, srcs + headers + [__file__]):
+    deps = srcs + headers + [__file__, TORCH_SRC]
+    if not force and not _stale(LIB, deps) and not _stale(TORCH_LIB, deps):
         return LIB
     nvcc = _nvcc()
+    incs, torch_lib = _torch_dirs()
+    tobj = os.path.join(BUILD, "ddl_torch.o")
 
     def compile_one(src: str) -> tuple[str, str]:
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
@@ -55,8 +75,16 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, len(srcs))) as ex:
+    def compile_torch() -> None:
+        cmd = ["g++", "-O2", "-std=c++20", "-fPIC", *[f"-I{i}" for i in incs], "-c", TORCH_SRC, "-o", tobj]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on {TORCH_SRC}:\n{r.stdout}\n{r.stderr}")
+
+    with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
+        module = ex.submit(compile_torch)
         results = list(ex.map(compile_one, srcs))
+        module.result()
     if verbose:
         for _, log in results:
             sys.stderr.write(log)
@@ -66,6 +94,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = TORCH_LIB + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, tobj, f"-L{BUILD}", "-lddl", f"-L{torch_lib}", "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TORCH_LIB)
     with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
         for _, log in results:
             f.write(log)

@@ -283,7 +283,7 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
       const int col = j & 1;
       float s = (c[j] + c2[j]) * ks * cf[col];
       if (EX) {
-        if (A.softcap > 0.f) s = A.softcap * LOG2E * cap_tanh(s);
+        if (A.softcap > 0.f) s = A.softcap * LOG2E * cap_tanh<DT>(s);
         s -= slope[col] * (float)(hi[col] - (key0 + g + (j >> 1) * 8));
       }
       c[j] = s;

@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
 #pragma unroll
         for (int q = 0; q < QW; ++q) {
           sc[q] *= ks * S.cf[x0 + q];
-          if (EX == 2) sc[q] = A.softcap * LOG2E * cap_tanh(sc[q]);
+          if (EX == 2) sc[q] = A.softcap * LOG2E * cap_tanh<DT>(sc[q]);
           if (EX) sc[q] = fmaf(-S.slope[x0 + q], S.hif[x0 + q] + back_of, sc[q]);  // (distances: exact to 2^24)
         }
         if (okm != 0xffu || newest * 16 + 15 > all_hi || (newest - TBLK + 1) * 16 < all_lo) {  // some query does not see some token

@@ -1,4 +1,5 @@
-"""ctypes binding of the C ABI in include/ddl.h (argument marshalling only).
+"""Binding of the C ABI in include/ddl.h (argument marshalling only): ctypes, and
+a compiled module for the 8-bit cache's per-layer calls.
 
 Every function here has the name of the C entry point it wraps, takes torch
 tensors (device memory owned by the caller) and passes their data pointers,
@@ -9,6 +10,7 @@ been built (``build.build()``); loading fails loudly otherwise.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -441,71 +443,28 @@ def ws_tensor(workspace: torch.Tensor, offset: int, n: int) -> torch.Tensor:
 
 
 # ------------------------------------------------------------------ 8-bit KV cache
-# A serving step makes these calls once a layer, and their kernels take a few
-# microseconds: the checks below cost about as much as the launch, so they
-# compare integers and types directly and build messages only on failure.
+# The calls that a serving step makes once a layer go through the compiled
+# module (csrc/ddl_torch.cpp), which checks the tensors and calls the library.
 
-T_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 KV8_TYPES = {torch.float8_e4m3fn: 0, torch.int8: 1}
+_mod = None
 
 
-def _i32(name: str, t, dev: int, n: int):
-    """Data pointer of a contiguous int32 tensor of n entries (n < 0: any) on CUDA device `dev`."""
-    if t.dtype is not torch.int32 or t.get_device() != dev or not t.is_contiguous() or (n >= 0 and t.numel() != n):
-        raise ValueError(f"{name}: a contiguous int32 tensor{f' of {n} entries' if n >= 0 else ''} on cuda:{dev}")
-    return t.data_ptr()
-
-
-def _f32(name: str, t, dev: int, n: int):
-    if t is None:
-        return None
-    if t.dtype is not torch.float32 or t.get_device() != dev or not t.is_contiguous() or t.numel() != n:
-        raise ValueError(f"{name}: a contiguous fp32 tensor of {n} entries on cuda:{dev}")
-    return t.data_ptr()
-
-
-def _run_on(dev: int, name: str, fn, stream, *args):
-    """fn(*args, stream) with CUDA device `dev` as the current one, on `stream`
-    or that device's current stream."""
-    s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
-    if torch._C._cuda_getDevice() == dev:
-        st = fn(*args, s)
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, s)
-    if st != 0:
-        raise DDLError(name, st, _lib)
-
-
-def _kv8(pool):
-    """(KV8, H_kv, head_dim, device index) of a pool (k, v, k_scale, v_scale):
-    codes [pages, H_kv, page_size, hd] float8_e4m3fn or int8, scales fp32
-    [pages, H_kv, page_size / 16], contiguous, on one CUDA device."""
-    k, v, ks, vs = pool
-    shape, dev, code = k.shape, k.get_device(), KV8_TYPES.get(k.dtype, -1)
-    if code < 0 or len(shape) != 4 or v.dtype is not k.dtype or v.shape != shape:
-        raise ValueError("pool: k and v [pages, H_kv, page_size, head_dim] of one 8-bit type")
-    pages, H, P, hd = shape
-    if (ks.dtype is not torch.float32 or vs.dtype is not torch.float32 or ks.shape != (pages, H, P // 16)
-            or vs.shape != ks.shape):
-        raise ValueError("pool: scales fp32 [pages, H_kv, page_size / 16]")
-    if not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
-        raise ValueError("pool: contiguous tensors")
-    if dev < 0 or v.get_device() != dev or ks.get_device() != dev or vs.get_device() != dev:
-        raise ValueError("pool: tensors of one CUDA device")
-    return KV8(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, P, code), H, hd, dev
-
-
-def _rows(name: str, x, dev: int, heads: int, hd: int, dtype, T: int) -> int:
-    """Row stride of rows [T, heads, hd] whose heads are contiguous."""
-    if x.dtype is not dtype or x.get_device() != dev or x.shape != (T, heads, hd) or dtype not in T_DTYPES:
-        raise ValueError(f"{name}: [{T}, {heads}, {hd}] {dtype} (fp32, bf16 or fp16) on cuda:{dev}")
-    if x.is_contiguous():
-        return heads * hd
-    st = x.stride()
-    if st[2] != 1 or (heads > 1 and st[1] != hd):
-        raise ValueError(f"{name}: a row's heads are contiguous")
-    return st[0] if T > 1 else heads * hd
+def _torch_module():
+    """The compiled module of the per-layer calls (loading the library first)."""
+    global _mod
+    load()
+    with _lock:
+        if _mod is None:
+            path = _build.TORCH_LIB
+            if not os.path.exists(path):
+                raise RuntimeError(f"CUDA decode library not built ({path} missing); "
+                                   "run __graft_entry__.build() first")
+            spec = importlib.util.spec_from_file_location("_ddl_torch", path)
+            m = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(m)
+            _mod = m
+        return _mod
 
 
 def ddl_page_plan(old_len: torch.Tensor, add_len: torch.Tensor, free_pages: torch.Tensor, page_table: torch.Tensor,
@@ -516,29 +475,22 @@ def ddl_page_plan(old_len: torch.Tensor, add_len: torch.Tensor, free_pages: torc
     add_len[r] rows.  Writes new pages from free_pages into page_table [R,
     pages_per_seq], and row_off [R + 1], kv_len [R], row_pos and slot [T],
     used [1], status [R]."""
-    lib = _lib or load()
-    dev, R, T, n_free = page_table.get_device(), old_len.numel(), slot.numel(), free_pages.numel()
-    if page_table.dim() != 2 or page_table.shape[0] != R or dev < 0:
-        raise ValueError("page_table: [R, pages_per_seq] on a CUDA device")
-    per = page_table.shape[1]
-    _run_on(dev, "ddl_page_plan", lib.ddl_page_plan, stream, _i32("old_len", old_len, dev, R),
-            _i32("add_len", add_len, dev, R), R, page_size, _i32("free_pages", free_pages, dev, n_free), n_free,
-            _i32("page_table", page_table, dev, -1), per, _i32("row_off", row_off, dev, R + 1),
-            _i32("kv_len", kv_len, dev, R), _i32("row_pos", row_pos, dev, T), _i32("slot", slot, dev, T), T,
-            _i32("used", used, dev, 1), _i32("status", status, dev, R))
+    st = (_mod or _torch_module()).page_plan(old_len, add_len, free_pages, page_table, page_size, row_off, kv_len,
+                                             row_pos, slot, used, status, stream and stream.cuda_stream)
+    if st:
+        raise DDLError("ddl_page_plan", st, _lib)
 
 
-def ddl_kv8_append(pool, k_new: torch.Tensor, v_new: torch.Tensor, slot: torch.Tensor,
+def ddl_kv8_append(pool: tuple, k_new: torch.Tensor, v_new: torch.Tensor, slot: torch.Tensor,
                    bad: torch.Tensor | None = None, stream=None):
-    """Quantize the rows k_new, v_new [T, H_kv, hd] into an 8-bit pool (k, v,
-    k_scale, v_scale) at the slot indices slot [T] (int32; negative: skipped).
+    """Quantize the rows k_new, v_new [T, H_kv, hd] (fp32, bf16 or fp16, heads
+    contiguous) into an 8-bit pool (k, v, k_scale, v_scale: codes [pages, H_kv,
+    page_size, hd] float8_e4m3fn or int8, scales fp32 [pages, H_kv,
+    page_size / 16]) at the slot indices slot [T] (int32; negative: skipped).
     bad: optional int32 [1] device flag set to 1 by a slot past the pool."""
-    lib = _lib or load()
-    kv, H, hd, dev = _kv8(pool)
-    T, dtype = slot.numel(), k_new.dtype
-    ks, vs = _rows("k_new", k_new, dev, H, hd, dtype, T), _rows("v_new", v_new, dev, H, hd, dtype, T)
-    _run_on(dev, "ddl_kv8_append", lib.ddl_kv8_append, stream, kv, H, hd, T_DTYPES[dtype], k_new.data_ptr(), ks,
-            v_new.data_ptr(), vs, _i32("slot", slot, dev, T), T, None if bad is None else _i32("bad", bad, dev, 1))
+    st = (_mod or _torch_module()).kv8_append(pool, k_new, v_new, slot, bad, stream and stream.cuda_stream)
+    if st:
+        raise DDLError("ddl_kv8_append", st, _lib)
 
 
 def ddl_kv8_attention_workspace_bytes(H_q: int, H_kv: int, hd: int, R: int, T: int, max_rows: int,
@@ -549,7 +501,7 @@ def ddl_kv8_attention_workspace_bytes(H_q: int, H_kv: int, hd: int, R: int, T: i
     return n
 
 
-def ddl_kv8_attention(pool, q: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor, max_len: int, *,
+def ddl_kv8_attention(pool: tuple, q: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor, max_len: int, *,
                       q_off: torch.Tensor | None = None, max_rows: int = 1, scale: float | None = None,
                       softcap: float = 0.0, window: int = 0, slopes: torch.Tensor | None = None,
                       out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
@@ -561,31 +513,39 @@ def ddl_kv8_attention(pool, q: torch.Tensor, kv_len: torch.Tensor, page_table: t
     max_len bounds kv_len, max_rows the rows of a request.  scale: 1 / sqrt(hd)
     by default; softcap, window, slopes as in ddl.h.  Returns out (zeros where
     a new one is made and a row belongs to no request)."""
-    lib = _lib or load()
-    kv, H, hd, dev = _kv8(pool)
-    if q.dim() != 3 or page_table.dim() != 2:
-        raise ValueError("q: [T, H_q, hd]; page_table: [R, pages_per_seq]")
-    T, H_q, _ = q.shape
-    R, dtype = kv_len.numel(), q.dtype
-    qs = _rows("q", q, dev, H_q, hd, dtype, T)
     if out is None:
-        out = torch.zeros((T, H_q, hd), dtype=dtype, device=q.device)
-    os_ = _rows("out", out, dev, H_q, hd, dtype, T)
-    rows_in_table, per = page_table.shape
-    if rows_in_table != R:
-        raise ValueError("page_table: a row for each entry of kv_len")
+        out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
     if workspace is None:
-        workspace = torch.empty(ddl_kv8_attention_workspace_bytes(H_q, H, hd, R, T, max_rows, max_len),
+        T, H_q, hd = q.shape
+        workspace = torch.empty(ddl_kv8_attention_workspace_bytes(H_q, pool[0].shape[1], hd, kv_len.numel(), T,
+                                                                  max_rows, max_len),
                                 dtype=torch.uint8, device=q.device)
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace: contiguous, on cuda:{dev}")
-    opts = AttnOpts(hd ** -0.5 if scale is None else scale, softcap, window, _f32("slopes", slopes, dev, H_q))
-    _run_on(dev, "ddl_kv8_attention", lib.ddl_kv8_attention, stream, kv, H_q, H, hd, T_DTYPES[dtype], opts, R, T,
-            max_rows, max_len, None if q_off is None else _i32("q_off", q_off, dev, R + 1),
-            _i32("kv_len", kv_len, dev, R), _i32("page_table", page_table, dev, -1), per, q.data_ptr(), qs,
-            out.data_ptr(), os_, _f32("lse", lse, dev, T * H_q), None if bad is None else _i32("bad", bad, dev, 1),
-            workspace.data_ptr(), workspace.nbytes)
+    st = (_mod or _torch_module()).kv8_attention(pool, q, kv_len, page_table, max_len, q_off, max_rows, scale, softcap,
+                                                 window, slopes, out, lse, workspace, bad,
+                                                 stream and stream.cuda_stream)
+    if st:
+        raise DDLError("ddl_kv8_attention", st, _lib)
     return out
+
+
+def _ptr_of(name: str, t, dtype, dev: int, shape):
+    """Data pointer of a contiguous tensor of `dtype` and `shape` on CUDA device `dev` (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or t.shape != shape:
+        raise ValueError(f"{name}: a contiguous {tuple(shape)} {dtype} tensor on cuda:{dev}")
+    return t.data_ptr()
+
+
+def _kv8(pool, dev: int, H: int, hd: int) -> KV8:
+    """Checks a pool (k, v, k_scale, v_scale) of H heads of hd on CUDA device `dev`."""
+    k, v, ks, vs = pool
+    if k.dim() != 4 or k.dtype not in KV8_TYPES or k.shape[1] != H or k.shape[3] != hd:
+        raise ValueError(f"pool: k and v [pages, {H}, page_size, {hd}] of one 8-bit type")
+    pages, _, P, _ = k.shape
+    return KV8(_ptr_of("k", k, k.dtype, dev, k.shape), _ptr_of("v", v, k.dtype, dev, k.shape),
+               _ptr_of("k_scale", ks, torch.float32, dev, (pages, H, P // 16)),
+               _ptr_of("v_scale", vs, torch.float32, dev, (pages, H, P // 16)), pages, P, KV8_TYPES[k.dtype])
 
 
 def ddl_stack_kv8_workspace_bytes(shape: Shape, R: int, T: int, max_rows: int, max_len: int) -> int:
@@ -604,31 +564,30 @@ def ddl_stack_step_kv8(shape: Shape, wtype: int, layers: list, pools: list, *, r
                        workspace: torch.Tensor, stream=None):
     """One step of len(layers) layers on 8-bit pools (one (k, v, k_scale,
     v_scale) per layer) for the rows that ddl_page_plan has placed."""
-    lib = _lib or load()
+    lib = load()
     x = x_bf16 if x_bf16 is not None else resid_in
     T, R, L, dev = x.shape[0], kv_len.numel(), len(layers), x.get_device()
-    if len(pools) != L or page_table.dim() != 2 or page_table.shape[0] != R:
-        raise ValueError("a pool for each layer; page_table: [R, pages_per_seq]")
-    for name, t, dt in (("x_bf16", x_bf16, torch.bfloat16), ("resid_in", resid_in, torch.float32),
-                        ("resid_out", resid_out, torch.float32), ("out_bf16", out_bf16, torch.bfloat16)):
-        if t is not None and (t.dtype is not dt or t.get_device() != dev or not t.is_contiguous()
-                              or t.shape != (T, shape.D)):
-            raise ValueError(f"{name}: a contiguous [{T}, {shape.D}] {dt} tensor on cuda:{dev}")
+    if dev < 0 or len(pools) != L or page_table.dim() != 2:
+        raise ValueError("tensors on a CUDA device, a pool for each layer, page_table [R, pages_per_seq]")
+    i32 = lambda name, t, shape: _ptr_of(name, t, torch.int32, dev, shape)  # noqa: E731
+    act = lambda name, t, dt: _ptr_of(name, t, dt, dev, (T, shape.D))  # noqa: E731
     if workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace: contiguous, on cuda:{dev}")
     lw, kv = (LayerW * L)(), (KV8 * L)()
     for i, (layer, pool) in enumerate(zip(layers, pools)):
         lw[i] = LayerW(layer["packed"].data_ptr(), layer["norm1"].data_ptr(), layer["norm2"].data_ptr())
-        kv[i], H, hd, d = _kv8(pool)
-        if H != shape.H_kv or hd != shape.head_dim or d != dev:
-            raise ValueError(f"pool {i}: [pages, {shape.H_kv}, page_size, {shape.head_dim}] on cuda:{dev}")
+        kv[i] = _kv8(pool, dev, shape.H_kv, shape.head_dim)
     opts = AttnOpts(shape.head_dim ** -0.5 if scale is None else scale, softcap, window,
-                    _f32("slopes", slopes, dev, shape.H_q))
-    _run_on(dev, "ddl_stack_step_kv8", lib.ddl_stack_step_kv8, stream, shape, wtype, lw, kv, L, opts, R, T, max_rows,
-            max_len, _i32("row_off", row_off, dev, R + 1), _i32("kv_len", kv_len, dev, R),
-            _i32("row_pos", row_pos, dev, T), _i32("slot", slot, dev, T), _i32("page_table", page_table, dev, -1),
-            page_table.shape[1], *(None if t is None else t.data_ptr() for t in (resid_in, x_bf16, resid_out, out_bf16)),
-            None if bad is None else _i32("bad", bad, dev, 1), workspace.data_ptr(), workspace.nbytes)
+                    _ptr_of("slopes", slopes, torch.float32, dev, (shape.H_q,)))
+    with torch.cuda.device(dev):
+        st = lib.ddl_stack_step_kv8(
+            ctypes.byref(shape), wtype, lw, kv, L, ctypes.byref(opts), R, T, max_rows, max_len,
+            i32("row_off", row_off, (R + 1,)), i32("kv_len", kv_len, (R,)), i32("row_pos", row_pos, (T,)),
+            i32("slot", slot, (T,)), i32("page_table", page_table, (R, page_table.shape[1])), page_table.shape[1],
+            act("resid_in", resid_in, torch.float32), act("x_bf16", x_bf16, torch.bfloat16),
+            act("resid_out", resid_out, torch.float32), act("out_bf16", out_bf16, torch.bfloat16),
+            i32("bad", bad, (1,)), _ptr(workspace), workspace.nbytes, _stream(stream))
+    _check("ddl_stack_step_kv8", st)
 
 
 # ------------------------------------------------------------------ token step
