@@ -304,10 +304,10 @@ typedef enum { DDL_T_F32 = 0, DDL_T_BF16 = 1, DDL_T_F16 = 2 } ddl_dtype;
 /* One layer's cache (device pointers).  k, v: codes [pages][H_kv][page_size]
  * [head_dim]; k_scale, v_scale: fp32 [pages][H_kv][page_size / 16].
  * page_size: a power of two in [16, 2^20] (DDL_ERR_ARG); pages * page_size <
- * 2^31 (DDL_ERR_UNSUPPORTED); head_dim 64 or 128, 1 <= H_kv <=
- * DDL_KV8_MAX_HEADS (DDL_ERR_SHAPE).  Slot t of a sequence is row t %
- * page_size of page page_table[t / page_size]; the *slot index* of a row is
- * page * page_size + t % page_size. */
+ * 2^31 and pages * H_kv * page_size / 16 < 2^31 (DDL_ERR_UNSUPPORTED);
+ * head_dim 64 or 128, 1 <= H_kv <= DDL_KV8_MAX_HEADS (DDL_ERR_SHAPE).  Slot t
+ * of a sequence is row t % page_size of page page_table[t / page_size]; the
+ * *slot index* of a row is page * page_size + t % page_size. */
 typedef struct {
     uint8_t* k;
     uint8_t* v;

@@ -189,6 +189,8 @@ struct AppendArgs {
   int32_t T, H, pshift, span, ppc, vec;  // vec: the map is 16-byte aligned
 };
 
+// (No load here is of the non-coherent kind: under dependent launches the kernel
+// is already resident while its predecessor writes.)
 // Four (hd 128) or two (hd 64) neighbouring elements of a row, as they are
 // stored (a 16-bit row takes half the registers until it is used), and as fp32.
 template <int DT, int W>
@@ -199,13 +201,13 @@ struct Raw {
     const uint32_t* p = reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint8_t*>(base) +
                                                           at * (DT == DDL_T_F32 ? 4 : 2));
     if (N == 4) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+      const uint4 u = *reinterpret_cast<const uint4*>(p);
       w[0] = u.x; w[N > 1 ? 1 : 0] = u.y; w[N > 2 ? 2 : 0] = u.z; w[N - 1] = u.w;
     } else if (N == 2) {
-      const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+      const uint2 u = *reinterpret_cast<const uint2*>(p);
       w[0] = u.x; w[N - 1] = u.y;
     } else {
-      w[0] = __ldg(p);
+      w[0] = *p;
     }
   }
   __device__ __forceinline__ void floats(float (&v)[W]) const {
@@ -431,7 +433,7 @@ __device__ __forceinline__ void look_up(const AppendArgs& A, int32_t block, bool
         const int f = e + 256 * u, left = A.T - 4 * f;  // (the last one may be cut)
         s[u] = make_int4(-1, -1, -1, -1);
         if (left >= 4) {
-          s[u] = __ldg(reinterpret_cast<const int4*>(A.slot) + f);
+          s[u] = *(reinterpret_cast<const int4*>(A.slot) + f);
         } else if (left > 0) {
           s[u].x = A.slot[4 * f];
           if (left > 1) s[u].y = A.slot[4 * f + 1];

@@ -22,6 +22,7 @@ inline int check_kv8(const ddl_kv8* kv, int32_t H_kv, int32_t hd) {
   if (kv->type != DDL_KV8_E4M3 && kv->type != DDL_KV8_INT8) return DDL_ERR_UNSUPPORTED;
   if (kv->page_size < 16 || kv->page_size > (1 << 20) || (kv->page_size & (kv->page_size - 1))) return DDL_ERR_ARG;
   if (kv->pages > 0x7fffffffLL / kv->page_size) return DDL_ERR_UNSUPPORTED;  // slots are int32
+  if (kv->pages > 0x7fffffffLL / (H_kv * (int64_t)(kv->page_size / KV8_BLOCK))) return DDL_ERR_UNSUPPORTED;  // and blocks
   if (!aligned16(kv->k) || !aligned16(kv->v) || !aligned16(kv->k_scale) || !aligned16(kv->v_scale))
     return DDL_ERR_ALIGN;
   return DDL_OK;

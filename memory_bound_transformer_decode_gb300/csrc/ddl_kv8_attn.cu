@@ -10,14 +10,17 @@
 //  - S^T = K Q^T on m16n8k16 MMAs with the 16 tokens as M.  The order of the
 //    head dimensions inside the contraction is free as long as K and Q agree,
 //    so lane (g, t) takes bytes 16t .. 16t + 15 of each 64 of token rows g and
-//    g + 8: the codes go from global memory straight into registers, 16 bytes a
-//    load, and each 4 of them become the lane's part of one k-step of A.
+//    g + 8: 16 bytes a load, each 4 of which become the lane's part of one
+//    k-step of A.
 //  - O^T += V^T P^T with the head dimensions as M.  Lane (g, t) takes the
 //    hd/8 neighbouring bytes at hd/8 g of tokens 2t, 2t+1, 2t+8, 2t+9; byte
 //    permutes pair the tokens and conversion gives A.  P^T comes from the S^T
 //    accumulators by movmatrix.
-// So no code passes through shared memory and both streams are read in whole
-// 128-byte rows.  e4m3 and int8 codes are exact in fp16.  Q is scaled by a
+// So no lane needs another's codes: each copies its own pieces (cp.async) into
+// its own places of a ring of three blocks per warp and reads them back without
+// a barrier or a bank conflict, both streams in whole 64- and 128-byte rows.
+// (Held in registers a block ahead instead, the loads covered less than one
+// memory latency per block.)  e4m3 and int8 codes are exact in fp16.  Q is scaled by a
 // power of two per query and split into fp16 high part and (fp32 rows only)
 // remainder: bf16 and fp16 values fit the high part (down to 2^-26 of the
 // row's largest).  P (with V's scale, relative to the largest seen by the warp)
@@ -56,19 +59,14 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
   return d;
 }
 
-// 16 (8) bytes of codes, read once by this warp (or again soon by the warps of
-// the same CTA that hold other queries).  Volatile: they are issued where they
-// stand, a block ahead of their use, and not moved down to it.
-__device__ __forceinline__ uint4 ld_codes16(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
+// Copy of 16 bytes through L1, which the warps of a CTA that hold other queries
+// of the same blocks find there.
+__device__ __forceinline__ void cp_async16_l1(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ uint2 ld_codes8(const uint8_t* p) {
-  uint2 v;
-  asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
-}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // Bytes lo16 / hi16 of w (two codes) as fp16 pairs.
 template <int CT>
@@ -93,8 +91,19 @@ struct Att {
   static constexpr int MT = HD / 16;  // M tiles of the output MMAs
   static constexpr bool HL = DT == DDL_T_F32;
   static constexpr int OROW = HD + 4;
+  // A warp's ring of blocks: each lane's own pieces of K and V, 16 (V of hd 64: 8)
+  // bytes at a time, so that a lane reads back only what it copied itself.
+  static constexpr int STAGES = 3;
+  static constexpr int KB = 2 * NV * 512, VB = HD == 128 ? 2048 : 1024, STAGE = KB + VB;
+  struct Warp {
+    union {
+      alignas(16) uint8_t ring[STAGES][STAGE];
+      float o[8][OROW];  // the warp's record, when its blocks are done
+    };
+  };
   struct Smem {
-    float o[ATT_WARPS][8][OROW];
+    Warp w[ATT_WARPS];
+    alignas(16) uint2 ql[HL ? ATT_WARPS : 1][HL ? KS * 32 : 1];  // the remainders of Q (fp32 rows)
     float ml[ATT_WARPS][8][2];
   };
   static __device__ __forceinline__ void segment(const AttArgs& A, Smem& S, int r, const Req& rq, int h, int qc,
@@ -114,48 +123,75 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
   const bool live = tile * 8 < nqueries;
 
   const int nb = live && c1 > c0 + kg ? (c1 - c0 - kg + groups - 1) / groups : 0;  // this warp's blocks
-  // block i of this warp: c0 + kg + i * groups; lane l holds the page row and
-  // the scales of blocks 32 w + l (this batch of 32) and the next batch's rows
+  // The query of this lane's column g of Q^T's fragments, on its way while the blocks are looked up.
+  const int my_q = tile * 8 + g, my_row = my_q < nqueries ? group_row(A, my_q) : 0;
+  float4 f[KS];
+  {
+    const int64_t at = (int64_t)(rq.row0 + my_row) * A.q_stride +
+                       (int64_t)(h * A.GH + my_q - my_row * A.GH) * HD + t * 16;
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+      f[s] = my_q < nqueries ? load_elem4<DT>(A.q, at + 64 * (s >> 2) + 4 * (s & 3)) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  // block i of this warp: c0 + kg + i * groups; lane l holds the place and the
+  // scales of blocks 32 w + l, of this batch of 32 and the next
   const int bshift = A.pshift - 4, bmask = (1 << bshift) - 1;
-  auto block_row = [&](int i) -> int32_t {  // the block's index in the pool's [page][head][block] view, -1: none
-    int64_t idx = -1;
+  auto block_row = [&](int i) -> int32_t {  // the block's index among all heads' blocks of the pool, -1: none
     if (i < nb) {
       const int b = c0 + kg + i * groups;
       const int32_t page = A.table[(int64_t)r * A.per + (b >> bshift)];
-      if (page >= 0 && page < A.pages) return page;
+      if (page >= 0 && page < A.pages) return (int32_t)((((int64_t)page * A.Hkv + h) << bshift) + (b & bmask));
       if (A.bad) atomicOr(A.bad, 1);
     }
-    return (int32_t)idx;
+    return -1;
   };
-  auto flat = [&](int32_t page, int i) -> int64_t {  // index of the block among all heads' blocks
-    const int b = c0 + kg + i * groups;
-    return (((int64_t)page * A.Hkv + h) << bshift) + (b & bmask);
-  };
-  int32_t page_l = block_row(lane), page_n = -1;
-  float ks_l = 0.f, vs_l = 0.f;
-  if (page_l >= 0) {
-    const int64_t f = flat(page_l, lane);
-    ks_l = A.ks[f];
-    vs_l = A.vs[f];
+  int32_t blk_l = block_row(lane), blk_n = -1;
+  float ks_l = 0.f, vs_l = 0.f, ks_n = 0.f, vs_n = 0.f;
+  if (blk_l >= 0) {
+    ks_l = A.ks[blk_l];
+    vs_l = A.vs[blk_l];
   }
-  // queries of this lane: column g of Q^T's fragments, columns 2t, 2t + 1 of the scores
-  // (the remainders wait in shared memory, in the place of the warp's later record)
+  // block i on its way into the ring; its place is lane i % 32's of this batch of 32 or the next
+  const uint32_t ring = smem_addr(&S.w[warp].ring[0][0]) + lane * 16;
+  const bool shared_codes = A.nq > 1;
+  const uint8_t *const k_lane = A.k + g * HD + t * 16, *const v_lane = A.v + 2 * t * HD + g * (HD / 8);
+  uint32_t slot_in = 0, slot_out = 0;  // ring places of the next block to fetch and to use
+  auto fetch = [&](int i, int32_t blks) {
+    const int32_t blk = __shfl_sync(FULL, blks, i & 31);
+    const uint32_t dst = ring + slot_in;
+    slot_in = slot_in == (STAGES - 1) * STAGE ? 0u : slot_in + STAGE;
+    if (blk >= 0) {  // (none past the last)
+      const int64_t f = (int64_t)blk * (16 * HD);
+      const uint8_t *pk = k_lane + f, *pv = v_lane + f;
+#pragma unroll
+      for (int j = 0; j < 2 * NV; ++j) {  // K: bytes 16 t of each 64 of rows g, g + 8
+        const uint8_t* p = pk + (j / NV) * 8 * HD + (j % NV) * 64;
+        if (shared_codes) cp_async16_l1(dst + j * 512, p);
+        else cp_async16(dst + j * 512, p);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // V: bytes hd/8 g of tokens 2t, 2t+1, 2t+8, 2t+9
+        const uint8_t* p = pv + ((j & 1) + (j >> 1) * 8) * HD;
+        if (HD == 64) cp_async8(dst + KB + j * 256 - lane * 8, p);
+        else if (shared_codes) cp_async16_l1(dst + KB + j * 512, p);
+        else cp_async16(dst + KB + j * 512, p);
+      }
+    }
+    cp_async_commit();
+  };
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < STAGES; ++i) fetch(i, blk_l);
+  // Q's fragments (column g), columns 2t, 2t + 1 of the scores
+  // (the remainders of fp32 rows wait in shared memory)
   uint32_t qh[KS][2];
-  uint2* const ql = reinterpret_cast<uint2*>(&S.o[warp][0][0]) + lane;
-  static_assert(KS * 32 * sizeof(uint2) <= sizeof(S.o[0]), "remainders of Q");
+  uint2* const ql = &S.ql[HL ? warp : 0][HL ? lane : 0];
   float qf = 0.f;  // 2^e of query g
   {
-    const int qi = tile * 8 + g;
-    const bool has = qi < nqueries;
-    const int row = has ? group_row(A, qi) : 0, head = h * A.GH + (has ? qi - row * A.GH : 0);
-    const int64_t at = (int64_t)(rq.row0 + row) * A.q_stride + (int64_t)head * HD + t * 16;
-    float4 f[KS];
     float mx = 0.f;
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      f[s] = has ? load_elem4<DT>(A.q, at + 64 * (s >> 2) + 4 * (s & 3)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < KS; ++s)
       mx = fmaxf(mx, fmaxf(fmaxf(fabsf(f[s].x), fabsf(f[s].y)), fmaxf(fabsf(f[s].z), fabsf(f[s].w))));
-    }
     mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
     int e = (int)((__float_as_uint(mx) >> 23) & 255u) - 127 - 12;  // the largest lands in [2^12, 2^13)
@@ -212,55 +248,27 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
   float mrun[2] = {-INFINITY, -INFINITY}, lrun[2] = {0.f, 0.f};
   float vref = 0.f, winv = 0.f;  // the largest V scale so far and P_SCALE / vref: P carries scale / vref
 
-  uint4 kb[2][NV], vb[4];  // K: rows g, g + 8; V: tokens 2t, 2t+1, 2t+8, 2t+9
-  auto load_k = [&](int64_t f) {
-    const uint8_t* p = A.k + f * (16 * HD) + t * 16;
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int u = 0; u < NV; ++u) kb[j][u] = ld_codes16(p + (g + 8 * j) * HD + 64 * u);
-  };
-  auto load_v = [&](int64_t f) {
-    const uint8_t* p = A.v + f * (16 * HD) + g * (HD / 8);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint8_t* row = p + (2 * t + (j & 1) + (j >> 1) * 8) * HD;
-      if (HD == 128) {
-        vb[j] = ld_codes16(row);
-      } else {
-        const uint2 x = ld_codes8(row);
-        vb[j].x = x.x;
-        vb[j].y = x.y;
-      }
-    }
-  };
-  int32_t page0 = __shfl_sync(FULL, page_l, 0);
-  if (nb > 0) {
-    const int64_t f = flat(page0 < 0 ? 0 : page0, 0);
-    load_k(f);
-    load_v(f);
-  }
-
 #pragma unroll 1
   for (int i = 0; i < nb; ++i) {
     const int l = i & 31;
-    if (l == 16) page_n = block_row((i & ~31) + 32 + lane);  // the next batch's rows, long before they are used
-    const int32_t page = __shfl_sync(FULL, page_l, l);
-    const float ks = __shfl_sync(FULL, ks_l, l), vs = __shfl_sync(FULL, vs_l, l);
-    if (l == 31) {  // on to the next batch
-      page_l = page_n;
-      ks_l = vs_l = 0.f;
-      if (page_l >= 0) {
-        const int64_t f = flat(page_l, i + 1 + lane);
-        ks_l = A.ks[f];
-        vs_l = A.vs[f];
+    if (l == 4) blk_n = block_row((i & ~31) + 32 + lane);  // the next batch, long before it is used
+    if (l == 16) {
+      ks_n = vs_n = 0.f;
+      if (blk_n >= 0) {
+        ks_n = A.ks[blk_n];
+        vs_n = A.vs[blk_n];
       }
     }
-    const int32_t pnext = __shfl_sync(FULL, page_l, (i + 1) & 31);
-    const int64_t fnext = flat(pnext < 0 ? 0 : pnext, i + 1);
-    const bool more = i + 1 < nb;
+    const bool none = __shfl_sync(FULL, blk_l, l) < 0;
+    const float ks = __shfl_sync(FULL, ks_l, l), vs = __shfl_sync(FULL, vs_l, l);
     const int key0 = (c0 + kg + i * groups) * 16;
 
+    cp_async_wait<STAGES - 1>();
+    const uint32_t src = ring + slot_out;
+    slot_out = slot_out == (STAGES - 1) * STAGE ? 0u : slot_out + STAGE;
+    uint4 kb[2][NV];
+#pragma unroll
+    for (int j = 0; j < 2 * NV; ++j) kb[j / NV][j % NV] = lds128(src + j * 512);
     // scores of tokens g (c 0, 1) and g + 8 (c 2, 3) for queries 2t, 2t + 1
     float c[4] = {0.f, 0.f, 0.f, 0.f}, c2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -277,7 +285,16 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
         mma_f16((s & 1) ? c2 : c, a0, a1, a2, a3, q2.x, q2.y);
       }
     }
-    if (more) load_k(fnext);
+    uint4 vb[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (HD == 128) {
+        vb[j] = lds128(src + KB + j * 512);
+      } else {
+        const uint2 x = lds64(src + KB + j * 256 - lane * 8);
+        vb[j] = make_uint4(x.x, x.y, 0u, 0u);
+      }
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int col = j & 1;
@@ -288,14 +305,13 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
       }
       c[j] = s;
     }
-    const bool edge = page < 0 || key0 + 15 > all_hi || key0 < all_lo;
+    const bool edge = none || key0 + 15 > all_hi || key0 < all_lo;
     if (edge) {  // some column does not see some token, or the block is missing
-      const int first = page < 0 ? 0x7fffffff : key0;
       uint32_t dead = 0;  // this lane's V tokens that nobody sees
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int key = key0 + 2 * t + (j & 1) + (j >> 1) * 8;
-        if (page < 0 || key > any_hi) dead |= 1u << j;
+        if (none || key > any_hi) dead |= 1u << j;
       }
       uint32_t nan = 0;  // ... that hold a NaN code
 #pragma unroll
@@ -322,7 +338,7 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int off = g + (j >> 1) * 8, key = key0 + off, col = j & 1;
-        if (first == 0x7fffffff || key > hi[col] || key < lo[col]) c[j] = -INFINITY;
+        if (none || key > hi[col] || key < lo[col]) c[j] = -INFINITY;
         else if ((nan >> off) & 1u) c[j] = __uint_as_float(0x7fffffffu);
       }
     }
@@ -393,8 +409,15 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
         mma_f16(o[2 * w + 1], b[0], b[1], b[2], b[3], pl0, pl1);
       }
     }
-    if (more) load_v(fnext);
+    // (the block's pieces are in registers: its place in the ring is free)
+    fetch(i + STAGES, l + STAGES < 32 ? blk_l : blk_n);
+    if (l == 31) {  // on to the next batch
+      blk_l = blk_n;
+      ks_l = ks_n;
+      vs_l = vs_n;
+    }
   }
+  cp_async_wait<0>();
 
   // the warp's record: lane (g, t) holds head dimensions hd/8 g + ... of queries 2t, 2t + 1
 #pragma unroll
@@ -406,7 +429,7 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
   __syncwarp();
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
-    float* row = &S.o[warp][2 * t + c][g * (HD / 8)];
+    float* row = &S.w[warp].o[2 * t + c][g * (HD / 8)];
 #pragma unroll
     for (int m = 0; m < MT; m += 2)
       *reinterpret_cast<float4*>(row + 2 * m) =
@@ -431,7 +454,7 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
     for (int w = 0; w < groups; ++w) {
       const int wp = tl + w * A.nq;
       const float f = exp2_fast(S.ml[wp][qq][0] - mref);
-      const float4 v = *reinterpret_cast<const float4*>(&S.o[wp][qq][4 * d]);
+      const float4 v = *reinterpret_cast<const float4*>(&S.w[wp].o[qq][4 * d]);
       l = fmaf(f, S.ml[wp][qq][1], l);
       acc.x = fmaf(f, v.x, acc.x);
       acc.y = fmaf(f, v.y, acc.y);
@@ -456,10 +479,11 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
 template <int CT, int DT, int HD, bool EX>
 __global__ void __launch_bounds__(ATT_WARPS * 32, 2) kv8_attention_kernel(const __grid_constant__ AttArgs A) {
   using K = Att<CT, DT, HD, EX>;
-  __shared__ typename K::Smem S;
-  extern __shared__ int64_t pre[];  // [R + 1], shares only
-  pdl_trigger();
+  extern __shared__ __align__(16) uint8_t att_smem[];
+  typename K::Smem& S = *reinterpret_cast<typename K::Smem*>(att_smem);
+  int64_t* const pre = reinterpret_cast<int64_t*>(att_smem + ((sizeof(typename K::Smem) + 15) & ~size_t(15)));  // [R + 1], shares only
   pdl_wait();
+  pdl_trigger();  // (after the wait: the join reads the lengths as soon as it starts)
   const int tid = threadIdx.x;
   if (A.whole) {
     int bid = blockIdx.x;
@@ -505,18 +529,34 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(const __grid_constant__ A
   constexpr int E = HD / 32;
   __shared__ float so[8][HD];
   __shared__ float2 sml[8];
-  pdl_trigger();
-  pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, par = warp % PAR;
   const int nq8 = A.nq * 8;
+  // Where the query's records are follows from the lengths alone.  They may be
+  // read ahead of the wait: this grid starts once the attention's CTAs have
+  // passed theirs, so what they read is complete.
   uint32_t id = blockIdx.x * (8 / PAR) + warp / PAR;  // (request, head, group of tiles, query)
-  const uint32_t per_req = (uint32_t)A.Hkv * A.nqc * nq8;
+  const uint32_t per_req = (uint32_t)A.Hkv * A.nqc * nq8;  // (a multiple of 8: a CTA's queries are of one request)
   const int r = (int)(id / per_req);
-  if (r >= A.R) return;  // (PAR = 1 only: a CTA's queries of one request are 8 / PAR times some)
   id -= (uint32_t)r * per_req;
   const int x = (int)(id % nq8), u = (int)(id / nq8), h = u / A.nqc, qc = u - h * A.nqc;
   const Req rq = load_req(A, r);
-  const int64_t W = A.prefix[A.R], p0 = A.prefix[r];
+  int64_t W = 0, p0 = 0;
+  if (A.R <= 32) {
+    int64_t w = lane < A.R ? req_weight(A, load_req(A, lane)) : 0, before = lane < r ? w : 0;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      w += __shfl_xor_sync(FULL, w, o);
+      before += __shfl_xor_sync(FULL, before, o);
+    }
+    W = w;
+    p0 = before;
+  }
+  pdl_trigger();
+  pdl_wait();
+  if (A.R > 32) {
+    W = A.prefix[A.R];
+    p0 = A.prefix[r];
+  }
   const int per_head = unit_groups(A, rq), nb = rq.b1 - rq.b0;
   const int qi = qc * nq8 + x, unit = h * per_head + qc;
   if (qc >= per_head || qi >= rq.n * A.GH) return;
@@ -686,6 +726,15 @@ const void* att_fn(int dt, int hd, bool ex) {
   return dt == DDL_T_F32 ? att_fn<CT, DDL_T_F32>(hd, ex) : dt == DDL_T_BF16 ? att_fn<CT, DDL_T_BF16>(hd, ex)
                                                                            : att_fn<CT, DDL_T_F16>(hd, ex);
 }
+// Shared memory ahead of the prefix (the code types' kernels have the same).
+size_t att_smem_bytes(int dt, int hd) {
+  const bool f32 = dt == DDL_T_F32;
+  const size_t n = hd == 128 ? (f32 ? sizeof(Att<DDL_KV8_INT8, DDL_T_F32, 128, false>::Smem)
+                                    : sizeof(Att<DDL_KV8_INT8, DDL_T_BF16, 128, false>::Smem))
+                             : (f32 ? sizeof(Att<DDL_KV8_INT8, DDL_T_F32, 64, false>::Smem)
+                                    : sizeof(Att<DDL_KV8_INT8, DDL_T_BF16, 64, false>::Smem));
+  return (n + 15) & ~size_t(15);
+}
 template <int DT>
 const void* join_fn(int hd, bool deep) {
   if (hd == 128) return deep ? (const void*)kv8_join_kernel<DT, 128, 8> : (const void*)kv8_join_kernel<DT, 128, 1>;
@@ -779,10 +828,8 @@ extern "C" int ddl_kv8_attention(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, i
     st = kv8_tc_launch(a, dtype, pool_rows, stream);
   } else {
     fn = kv->type == DDL_KV8_E4M3 ? att_fn<DDL_KV8_E4M3>(dtype, head_dim, ex) : att_fn<DDL_KV8_INT8>(dtype, head_dim, ex);
-    const size_t smem = pl.whole ? 0 : (size_t)(R + 1) * 8;
-    if (smem > 8192 && (st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                              (DDL_KV8_MAX_REQS + 1) * 8))))
-      return st;  // (beside the static 34 KB more than 48 KB)
+    const size_t smem = att_smem_bytes(dtype, head_dim) + (pl.whole ? 0 : (size_t)(R + 1) * 8);
+    if ((st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024)))) return st;
     st = cuda_status(launch_pdl(fn, dim3((unsigned)pl.ctas), dim3(ATT_WARPS * 32), args, smem, (cudaStream_t)stream));
   }
   if (st || pl.whole) return st;

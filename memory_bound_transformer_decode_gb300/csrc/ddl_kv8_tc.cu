@@ -76,7 +76,8 @@ template <int NT, int L>
 struct Shared {
   Meta meta[Geo<NT, L>::STAGES];
   alignas(16) float cf[8 * NT], slope[8 * NT], hif[8 * NT], m[8 * NT], al[8 * NT];
-  alignas(16) float most[8 * NT], mref[8 * NT];  // m + T_LAG; m, 0 for -inf
+  alignas(16) float mref[8 * NT], shift[8 * NT];  // m, 0 for -inf; what a raise moves it by
+  uint32_t fresh[2];  // per warpgroup: some query that may still meet a key has met none
   int32_t hi[8 * NT], lo[8 * NT];
   int64_t place[8 * NT];
   float wred[4][8 * NT];
@@ -143,6 +144,8 @@ __device__ __forceinline__ void warp_sums(float (&v)[N]) {
 #pragma unroll
   for (int o = N; o < 32; o <<= 1) v[0] += __shfl_xor_sync(FULL, v[0], o);
 }
+
+__device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
 // Eight values as e4m3 codes (byte i = value i), and what they leave.
 __device__ __forceinline__ uint2 limb8(float (&v)[8], bool rest) {
@@ -252,7 +255,6 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
   const uint32_t fullk = smem_addr(S.fullk), fullv = smem_addr(S.fullv), empty = smem_addr(S.empty);
   const uint32_t sfull = smem_addr(S.sfull), pfull = smem_addr(&S.pfull), pvdone = smem_addr(&S.pvdone);
   const uint32_t qfull = smem_addr(&S.qfull);
-  pdl_trigger();
   if (tid == 0) {
     for (int i = 0; i < G::STAGES; ++i) {
       mbar_init(fullk + 8 * i, 1);
@@ -274,6 +276,7 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
   tc_fence_after();
   const uint32_t tm = S.tslot, tO = tm + 2 * G::N;
   pdl_wait();
+  pdl_trigger();  // (after the wait: the join reads the lengths as soon as it starts)
   Segs first;
   first.x = 0;
   first.end = 1;
@@ -506,7 +509,7 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
           }
           S.hi[x] = has ? p : -1;
           S.lo[x] = A.window > 0 ? p - A.window + 1 : 0;
-          S.m[x] = S.most[x] = -INFINITY;
+          S.m[x] = -INFINITY;
           S.mref[x] = 0.f;
         }
       }
@@ -533,7 +536,7 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
         const float back_of = (float)(s.c1 * 16 - key);
         ok = ok && wait(sfull + 8 * (tc & 1), (tc >> 1) & 1);
         tc_fence_after();
-        float sc[QW];
+        float sc[QW];  // score less the running maximum's stand-in
         {
           uint32_t v[QW / 8][16];
 #pragma unroll
@@ -546,10 +549,24 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
               sc[8 * j + q] = fmaf(__uint_as_float(v[j][8 + q]), 1.f / BSCALE, __uint_as_float(v[j][q]));
         }
 #pragma unroll
-        for (int q = 0; q < QW; ++q) {
-          sc[q] *= ks * S.cf[x0 + q];
-          if (EX == 2) sc[q] = A.softcap * LOG2E * cap_tanh<DT>(sc[q]);
-          if (EX) sc[q] = fmaf(-S.slope[x0 + q], S.hif[x0 + q] + back_of, sc[q]);  // (distances: exact to 2^24)
+        for (int j = 0; j < QW; j += 4) {
+          const float4 cf = ld4(&S.cf[x0 + j]), mr = ld4(&S.mref[x0 + j]);
+          if (EX == 0) {
+            sc[j] = fmaf(sc[j], ks * cf.x, -mr.x);
+            sc[j + 1] = fmaf(sc[j + 1], ks * cf.y, -mr.y);
+            sc[j + 2] = fmaf(sc[j + 2], ks * cf.z, -mr.z);
+            sc[j + 3] = fmaf(sc[j + 3], ks * cf.w, -mr.w);
+          } else {
+            const float4 sl = ld4(&S.slope[x0 + j]), hf = ld4(&S.hif[x0 + j]);
+            const float f[4] = {cf.x, cf.y, cf.z, cf.w}, r[4] = {mr.x, mr.y, mr.z, mr.w};
+            const float w[4] = {sl.x, sl.y, sl.z, sl.w}, d[4] = {hf.x, hf.y, hf.z, hf.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              float x = sc[j + q] * (ks * f[q]);
+              if (EX == 2) x = A.softcap * LOG2E * cap_tanh<DT>(x);
+              sc[j + q] = fmaf(-w[q], d[q] + back_of, x) - r[q];  // (distances: exact to 2^24)
+            }
+          }
         }
         if (okm != 0xffu || newest * 16 + 15 > all_hi || (newest - TBLK + 1) * 16 < all_lo) {  // some query does not see some token
           // V rows that no query sees must not hold NaN codes, and a NaN code of
@@ -578,9 +595,9 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
             else if (nan) sc[q] = __uint_as_float(0x7fffffffu);
           }
         }
-        bool over = vmax > vref;
+        bool over = vmax > vref || i == 0 || S.fresh[wg];
 #pragma unroll
-        for (int q = 0; q < QW; ++q) over = over || sc[q] > S.most[x0 + q];
+        for (int q = 0; q < QW; ++q) over = over || sc[q] > T_LAG;
         bool waited = tc == 0;
         if (ssync_or(1 + wg, 128, over)) {  // raise the running maximum (and V's reference): O and l in the new units
 #pragma unroll
@@ -591,13 +608,16 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
           ssync(1 + wg, 128);
           if (tok < QW) {
             const int x = x0 + tok;
-            const float old = S.m[x];
-            const float top = fmaxf(fmaxf(S.wred[0][x], S.wred[1][x]), fmaxf(S.wred[2][x], S.wred[3][x]));
-            const float nm = fmaxf(old, top);
+            const float old = S.m[x], ref = S.mref[x];
+            const float up = fmaxf(fmaxf(S.wred[0][x], S.wred[1][x]), fmaxf(S.wred[2][x], S.wred[3][x]));
+            const float nm = fmaxf(old, ref + up), now = nm == -INFINITY ? 0.f : nm;
             S.al[x] = old == -INFINITY ? 0.f : exp2_fast(old - nm);
             S.m[x] = nm;
-            S.most[x] = nm + T_LAG;
-            S.mref[x] = nm == -INFINITY ? 0.f : nm;
+            S.mref[x] = now;
+            S.shift[x] = ref - now;
+            const bool none = nm == -INFINITY && S.hi[x] >= s.c0 * 16;
+            const uint32_t any = __ballot_sync((1u << QW) - 1u, none);
+            if (tok == 0) S.fresh[wg] = any;
           }
           if (!waited) ok = ok && wait(pvdone, (tc - 1) & 1);
           waited = true;
@@ -606,7 +626,10 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
           winv = nref > 0.f ? __fdiv_rn(TP_SCALE, nref) : 0.f;
           ssync(1 + wg, 128);
 #pragma unroll
-          for (int q = 0; q < QW; ++q) l[q] *= S.al[x0 + q];
+          for (int q = 0; q < QW; ++q) {
+            l[q] *= S.al[x0 + q];
+            sc[q] += S.shift[x0 + q];
+          }
           if (i > 0) {
             tc_fence_after();
 #pragma unroll
@@ -622,15 +645,16 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
             tmem_st_wait();
           }
         }
-        // the tile's weights, and their limbs as the PV operand
-        if (!waited) ok = ok && wait(pvdone, (tc - 1) & 1);
+        // the tile's weights, and their limbs as the PV operand (whose place is
+        // free once the previous tile's PV MMAs are done)
         const float wv = vs * winv;
+        uint4 pk[QW / 8][L];
 #pragma unroll
         for (int j = 0; j < QW / 8; ++j) {
           float w[8];
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
-            const float p = exp2_fast(sc[8 * j + q] - S.mref[x0 + 8 * j + q]);
+            const float p = exp2_fast(sc[8 * j + q]);
             l[8 * j + q] += p;
             w[q] = p * wv;
           }
@@ -658,10 +682,14 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
             }
           }
 #pragma unroll
-          for (int p = 0; p < L; ++p)
-            *reinterpret_cast<uint4*>(smem + G::P_OFF + p * G::OPB + (x0 / 8 + j) * 2048 + tok * 16) =
-                make_uint4(a[p].x, a[p].y, b[p].x, b[p].y);
+          for (int p = 0; p < L; ++p) pk[j][p] = make_uint4(a[p].x, a[p].y, b[p].x, b[p].y);
         }
+        if (!waited) ok = ok && wait(pvdone, (tc - 1) & 1);
+#pragma unroll
+        for (int j = 0; j < QW / 8; ++j)
+#pragma unroll
+          for (int p = 0; p < L; ++p)
+            *reinterpret_cast<uint4*>(smem + G::P_OFF + p * G::OPB + (x0 / 8 + j) * 2048 + tok * 16) = pk[j][p];
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
