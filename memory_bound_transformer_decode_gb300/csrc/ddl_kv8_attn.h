@@ -123,7 +123,13 @@ template <int NT>
 __device__ __forceinline__ int64_t unit_prefix(const AttArgs& A, int64_t* pre, int64_t* wsum) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int64_t base = 0;
-  if (A.R <= 32) {  // each warp for itself, without a barrier (all write the same values)
+  if (A.R == 1) {
+    const Req rq = load_req(A, 0);
+    base = req_weight(A, rq);
+    if (blockIdx.x == 0 && tid == 0 && rq.bad && A.bad) atomicOr(A.bad, 1);
+    if (lane < 2) pre[lane] = lane ? base : 0;
+    __syncwarp();
+  } else if (A.R <= 32) {  // each warp for itself, without a barrier (all write the same values)
     int64_t w = 0;
     if (lane < A.R) {
       const Req rq = load_req(A, lane);

@@ -50,6 +50,7 @@ constexpr float TP_SCALE = 32.f, T_LAG = 3.f;
 struct TcAtt {
   AttArgs A;
   uint64_t wait_ns;
+  int32_t rows;  // of the pool's view: a box that begins there reads zeros
   alignas(64) CUtensorMap kmap, vmap;
 };
 
@@ -340,7 +341,7 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
           ks = A.ks[(head << bshift) + sub];
           vs = A.vs[(head << bshift) + sub];
         }
-        const int32_t row = (int32_t)((head << A.pshift) + (sub << 4));
+        const int32_t row = page >= 0 ? (int32_t)((head << A.pshift) + (sub << 4)) : P.rows;  // (none: zeros)
         page_n = page_of(g0 + 32 + lane);
         float vmax = vs;  // of the lane's tile
 #pragma unroll
@@ -352,7 +353,7 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
             ok = false;
             break;
           }
-          const uint32_t okm = (there >> (t * TBLK)) & 0xffu, bytes = (uint32_t)__popc(okm) * 2048u;
+          const uint32_t okm = (there >> (t * TBLK)) & 0xffu;
           const bool mine = (lane / TBLK) == t;
           if (mine) {
             S.meta[st].ks[lane % TBLK] = ks;
@@ -364,11 +365,11 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
           }
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive_expect_tx(fullk + 8 * st, bytes);
-            mbar_arrive_expect_tx(fullv + 8 * st, bytes);
+            mbar_arrive_expect_tx(fullk + 8 * st, KBYTES);
+            mbar_arrive_expect_tx(fullv + 8 * st, KBYTES);
           }
           __syncwarp();
-          if (mine && page >= 0) {
+          if (mine) {
             const uint32_t dst = sb + st * 2 * KBYTES + (lane % TBLK) * 2048u;
             tensor2d_g2s(dst, &P.kmap, 0, row, fullk + 8 * st, policy);
             tensor2d_g2s(dst + KBYTES, &P.vmap, 0, row, fullv + 8 * st, policy);
@@ -568,10 +569,12 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
             }
           }
         }
-        if (okm != 0xffu || newest * 16 + 15 > all_hi || (newest - TBLK + 1) * 16 < all_lo) {  // some query does not see some token
+        const bool there = (okm >> blk) & 1u;
+        const int oldest = newest - TBLK + 1 > s.c0 ? newest - TBLK + 1 : s.c0;
+        if (newest * 16 + 15 > all_hi || oldest * 16 < all_lo) {  // some query does not see some token
           // V rows that no query sees must not hold NaN codes, and a NaN code of
           // one that some see reaches exactly those, through their scores
-          const bool there = (okm >> blk) & 1u, dead = !there || key > any_hi;
+          const bool dead = !there || key > any_hi;
           if (wg == 0) {
             ok = ok && wait(fullv + 8 * st, (tc / G::STAGES) & 1);
             uint4* row = reinterpret_cast<uint4*>(smem + st * 2 * KBYTES + KBYTES + tok * 128);
@@ -594,6 +597,9 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
             if (dead || key > S.hi[x0 + q] || key < S.lo[x0 + q]) sc[q] = -INFINITY;
             else if (nan) sc[q] = __uint_as_float(0x7fffffffu);
           }
+        } else if (!there) {  // past the segment's blocks, or a page that is none: zeros in K and V
+#pragma unroll
+          for (int q = 0; q < QW; ++q) sc[q] = -INFINITY;
         }
         bool over = vmax > vref || i == 0 || S.fresh[wg];
 #pragma unroll
@@ -786,6 +792,7 @@ int kv8_tc_launch(const AttArgs& a, int dtype, int64_t rows, void* stream) {
   TcAtt p;
   p.A = a;
   p.wait_ns = wait_limit_ns();
+  p.rows = (int32_t)rows;
   int st;
   if ((st = encode_map(&p.kmap, a.k, rows)) || (st = encode_map(&p.vmap, a.v, rows))) return st;
   const int threads = a.nq == 1 ? Geo<1, 2>::THREADS : a.nq == 2 ? Geo<2, 2>::THREADS : Geo<4, 2>::THREADS;
