@@ -99,12 +99,17 @@ struct Att {
     union {
       alignas(16) uint8_t ring[STAGES][STAGE];
       float o[8][OROW];  // the warp's record, when its blocks are done
+      struct {
+        float o_[8][OROW];
+        float rec[8][HD];  // the record of tile `warp` of the CTA, for the CTAs of its cluster
+      } rest;
     };
   };
   struct Smem {
     Warp w[ATT_WARPS];
     alignas(16) uint2 ql[HL ? ATT_WARPS : 1][HL ? KS * 32 : 1];  // the remainders of Q (fp32 rows)
     float ml[ATT_WARPS][8][2];
+    float2 rml[ATT_WARPS * 8];
   };
   static __device__ __forceinline__ void segment(const AttArgs& A, Smem& S, int r, const Req& rq, int h, int qc,
                                                  int c0, int c1, bool direct, int64_t rec);
@@ -463,7 +468,10 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
     }
     const int row = group_row(A, qi), head = h * A.GH + qi - row * A.GH;
     const int64_t rh = (int64_t)(rq.row0 + row) * A.Hq + head;
-    if (direct) {
+    if (A.cluster > 1) {
+      *reinterpret_cast<float4*>(&S.w[tl].rest.rec[qq][4 * d]) = acc;
+      if (d == 0) S.rml[tl * 8 + qq] = make_float2(m, l);
+    } else if (direct) {
       const float inv = l != 0.f ? 1.f / l : 0.f;  // (NaN stays NaN)
       store_elem4<DT>(A.out, (int64_t)(rq.row0 + row) * A.out_stride + (int64_t)head * HD + 4 * d,
                       make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
@@ -485,14 +493,23 @@ __global__ void __launch_bounds__(ATT_WARPS * 32, 2) kv8_attention_kernel(const 
   pdl_wait();
   pdl_trigger();  // (after the wait: the join reads the lengths as soon as it starts)
   const int tid = threadIdx.x;
-  if (A.whole) {
-    int bid = blockIdx.x;
-    const int qc = bid % A.nqc;
-    bid /= A.nqc;
-    const int h = bid % A.Hkv, r = bid / A.Hkv;
+  if (A.cluster) {
+    const ClusterPart part(A);
+    int u = part.unit;
+    const int qc = u % A.nqc;
+    u /= A.nqc;
+    const int h = u % A.Hkv, r = u / A.Hkv;
     const Req rq = load_req(A, r);
     if (rq.bad && A.bad && tid == 0) atomicOr(A.bad, 1);
-    if (qc < unit_groups(A, rq)) K::segment(A, S, r, rq, h, qc, rq.b0, rq.b1, true, 0);
+    if (qc >= unit_groups(A, rq)) return;  // (all CTAs of the cluster)
+    int c0, c1;
+    part.blocks(A, rq, c0, c1);
+    K::segment(A, S, r, rq, h, qc, c0, c1, A.cluster == 1, 0);
+    if (A.cluster > 1) {
+      __syncthreads();
+      cluster_join<DT, HD>(A, part, smem_addr(&S.w[0].rest.rec[0][0]), sizeof(S.w[0]), smem_addr(&S.rml[0]),
+                           ATT_WARPS * 32);
+    }
     return;
   }
   __shared__ int64_t wsum[ATT_WARPS];
@@ -665,12 +682,15 @@ int att_sms(int& sms) {
   return DDL_OK;
 }
 
-constexpr int WHOLE_BLOCKS = 32;
+// Clusters: CTAs of a unit at most (16 is past the portable 8, and two fit a
+// GPC's SMs side by side), blocks a CTA takes at least, and how many blocks in a
+// row are worth the shares' fixed cost (6 us).
+constexpr int MAX_CLUSTER = 16, MIN_PART = 16, CLUSTER_GAIN = 40;
 
 struct AttPlan {
-  int32_t nq, nqc, whole, ctas, deep;  // deep: a unit may have many shares
-  int32_t unit_cost, min_share;        // of a CTA's share, in blocks
-  int64_t rec_ml, prefix, total;       // workspace offsets
+  int32_t nq, nqc, cluster, ctas, deep;  // deep: a unit may have many shares
+  int32_t unit_cost, min_share;          // of a CTA's share, in blocks
+  int64_t rec_ml, prefix, total;         // workspace offsets
 };
 
 int check_sizes(int32_t H_q, int32_t H_kv, int32_t hd, int32_t R, int32_t T, int32_t max_rows, int32_t max_len) {
@@ -683,27 +703,41 @@ int check_sizes(int32_t H_q, int32_t H_kv, int32_t hd, int32_t R, int32_t T, int
 }
 
 int att_plan(bool tc, int32_t H_q, int32_t H_kv, int32_t hd, int32_t R, int32_t max_rows, int32_t max_len,
-             AttPlan& p) {
+             int32_t window, AttPlan& p) {
   int sms = 0;
   const int st = att_sms(sms);
   if (st) return st;
   const int tiles = (max_rows * (H_q / H_kv) + 7) / 8;
   p.nq = 1;
-  // Measured at 64 requests of up to 8192 tokens, 64/8 heads (tcgen05: cost 16 / 24 / 40 110 / 106 / 99 us; warp MMAs
-  // on 16 requests of 28/4 heads: cost 16 / 24 / 40 18 / 20 / 23 us).
-  p.unit_cost = tc ? 48 : 16;
-  p.min_share = p.unit_cost + (tc ? 8 : 16);
   while (p.nq < (tc ? 4 : ATT_WARPS) && p.nq < tiles) p.nq *= 2;
   p.nqc = (tiles + p.nq - 1) / p.nq;
-  const int64_t blocks = ((int64_t)max_len + 15) / 16, units = (int64_t)R * H_kv * p.nqc;
-  p.whole = blocks <= WHOLE_BLOCKS;
+  int64_t keys = max_len;
+  if (window > 0 && (int64_t)window + max_rows + 15 < keys) keys = (int64_t)window + max_rows + 15;
+  const int64_t blocks = (keys + 15) / 16, units = (int64_t)R * H_kv * p.nqc, slots = 2 * sms;
   p.rec_ml = p.prefix = 0;
   p.total = 256;
-  p.ctas = (int32_t)units;
   p.deep = 0;
-  if (p.whole) return DDL_OK;
-  const int64_t most = (units * (blocks + p.unit_cost) + p.min_share - 1) / p.min_share;
-  p.ctas = (int32_t)(most < 2 * sms ? most : 2 * sms);
+  p.unit_cost = p.min_share = 1;
+  // A cluster per unit, of as many CTAs as fill the machine once.  Against the
+  // shares it saves the sums of the lengths, the records' way through memory
+  // and a launch, and pays for every request what the longest costs.
+  p.cluster = 1;
+  while (p.cluster < MAX_CLUSTER && units * 2 * p.cluster <= slots && p.cluster * MIN_PART < blocks) p.cluster *= 2;
+  const int64_t waves = (units * p.cluster + slots - 1) / slots;
+  const int64_t alone = waves * ((blocks + p.cluster - 1) / p.cluster);     // blocks a CTA takes, one after the other
+  const int64_t shared = (units * blocks * (R > 1 ? 5 : 8) / 8 + slots - 1) / slots;  // (lengths up to the bound: about 5/8)
+  if (alone <= shared + CLUSTER_GAIN) {
+    p.ctas = (int32_t)(units * p.cluster);
+    return DDL_OK;
+  }
+  // Measured at 64 requests of up to 8192 tokens, 64/8 heads (tcgen05: cost 16 / 24 / 40 110 / 106 / 99 us; warp MMAs
+  // on 16 requests of 28/4 heads: cost 16 / 24 / 40 18 / 20 / 23 us).
+  p.cluster = 0;
+  p.unit_cost = tc ? 48 : 16;
+  p.min_share = p.unit_cost + (tc ? 8 : 16);
+  const int64_t all = ((int64_t)max_len + 15) / 16;
+  const int64_t most = (units * (all + p.unit_cost) + p.min_share - 1) / p.min_share;
+  p.ctas = (int32_t)(most < slots ? most : slots);
   if (p.ctas > 1024) return DDL_ERR_UNSUPPORTED;  // (the kernels' 32-bit share arithmetic)
   p.deep = units * 8 <= p.ctas;
   const int64_t queries = (units + p.ctas) * p.nq * 8;  // of all records
@@ -749,9 +783,9 @@ using namespace ddl;
 extern "C" size_t ddl_kv8_attention_workspace_bytes(int32_t H_q, int32_t H_kv, int32_t head_dim, int32_t R, int32_t T,
                                                     int32_t max_rows, int32_t max_len) {
   if (check_sizes(H_q, H_kv, head_dim, R, T, max_rows, max_len)) return 0;
-  AttPlan p, q;  // of either kernel: the code type is not known here
-  if (att_plan(false, H_q, H_kv, head_dim, R, max_rows, max_len, p)) return 0;
-  if (att_plan(true, H_q, H_kv, head_dim, R, max_rows, max_len, q)) return 0;
+  AttPlan p, q;  // of either kernel and without a window, the most any call of these sizes takes
+  if (att_plan(false, H_q, H_kv, head_dim, R, max_rows, max_len, 0, p)) return 0;
+  if (att_plan(true, H_q, H_kv, head_dim, R, max_rows, max_len, 0, q)) return 0;
   return (size_t)(p.total > q.total ? p.total : q.total);
 }
 
@@ -780,7 +814,7 @@ extern "C" int ddl_kv8_attention(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, i
   AttPlan pl;
   const int64_t pool_rows = kv->pages * kv->page_size * H_kv;
   const bool tc = kv->type == DDL_KV8_E4M3 && head_dim == 128 && pool_rows < (1ll << 31);
-  if ((st = att_plan(tc, H_q, H_kv, head_dim, R, max_rows, max_len, pl))) return st;
+  if ((st = att_plan(tc, H_q, H_kv, head_dim, R, max_rows, max_len, opts->window, pl))) return st;
   if (ws_bytes < (size_t)pl.total) return DDL_ERR_WORKSPACE;
   AttArgs a;
   a.k = kv->k;
@@ -815,7 +849,7 @@ extern "C" int ddl_kv8_attention(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, i
   a.per = pages_per_seq;
   a.max_rows = max_rows;
   a.max_len = max_len;
-  a.whole = pl.whole;
+  a.cluster = pl.cluster;
   a.ctas = pl.ctas;
   a.unit_cost = pl.unit_cost;
   a.min_share = pl.min_share;
@@ -828,11 +862,14 @@ extern "C" int ddl_kv8_attention(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, i
     st = kv8_tc_launch(a, dtype, pool_rows, stream);
   } else {
     fn = kv->type == DDL_KV8_E4M3 ? att_fn<DDL_KV8_E4M3>(dtype, head_dim, ex) : att_fn<DDL_KV8_INT8>(dtype, head_dim, ex);
-    const size_t smem = att_smem_bytes(dtype, head_dim) + (pl.whole ? 0 : (size_t)(R + 1) * 8);
+    const size_t smem = att_smem_bytes(dtype, head_dim) + (pl.cluster ? 0 : (size_t)(R + 1) * 8);
     if ((st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024)))) return st;
-    st = cuda_status(launch_pdl(fn, dim3((unsigned)pl.ctas), dim3(ATT_WARPS * 32), args, smem, (cudaStream_t)stream));
+    if (pl.cluster > 8 && (st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1))))
+      return st;
+    st = cuda_status(launch_pdl_cluster(fn, dim3((unsigned)pl.ctas), dim3(ATT_WARPS * 32), args, smem, pl.cluster,
+                                        (cudaStream_t)stream));
   }
-  if (st || pl.whole) return st;
+  if (st || pl.cluster) return st;
   fn = dtype == DDL_T_F32    ? join_fn<DDL_T_F32>(head_dim, pl.deep)
        : dtype == DDL_T_BF16 ? join_fn<DDL_T_BF16>(head_dim, pl.deep)
                              : join_fn<DDL_T_F16>(head_dim, pl.deep);

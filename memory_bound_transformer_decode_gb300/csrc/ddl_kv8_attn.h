@@ -26,8 +26,8 @@ struct AttArgs {
   float scale, softcap;
   int32_t window;
   int32_t R, T, Hq, Hkv, GH, gmul, hd, pshift, per, max_rows, max_len;
-  int32_t whole;    // one CTA a unit, else shares
-  int32_t ctas;     // shares at most
+  int32_t cluster;  // > 0: a cluster of so many CTAs a unit; 0: shares
+  int32_t ctas;     // CTAs: of the clusters, or shares at most
   int32_t unit_cost, min_share;
   int32_t nq, nqc;  // query tiles of 8 a unit has (a power of two <= 8), units over a request's query tiles
 };
@@ -233,6 +233,107 @@ __device__ __forceinline__ void store_elem(void* p, int64_t i, float v) {
 template <int DT>
 __device__ __forceinline__ float cap_tanh(float x) {
   return DT == DDL_T_F32 ? tanhf(x) : 1.f - __fdividef(2.f, __expf(2.f * x) + 1.f);
+}
+
+// ------------------------------------------------------------------ clusters
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// A CTA of a cluster and its run of the unit's blocks.
+struct ClusterPart {
+  int unit, rank;  // unit: ((request * H_kv) + head) * nqc + group of tiles
+  __device__ __forceinline__ explicit ClusterPart(const AttArgs& A) {
+    unit = blockIdx.x / A.cluster;
+    rank = blockIdx.x - unit * A.cluster;
+  }
+  __device__ __forceinline__ void blocks(const AttArgs& A, const Req& q, int& c0, int& c1) const {
+    const int64_t nb = q.b1 - q.b0;
+    c0 = q.b0 + (int)(nb * rank / A.cluster);
+    c1 = q.b0 + (int)(nb * (rank + 1) / A.cluster);
+  }
+};
+
+// Joins the records that the unit's CTAs hold in shared memory (query x: O at
+// rec + (x / 8) tile_stride + (x % 8) HD floats, (max, sum) at ml + 8 x bytes):
+// CTA `rank` takes every cluster-th query, a thread one head dimension, the
+// CTAs' values in rank order.  All threads of the cluster call it.
+template <int DT, int HD>
+__device__ __forceinline__ void cluster_join(const AttArgs& A, const ClusterPart& part, uint32_t rec,
+                                             uint32_t tile_stride, uint32_t ml, int threads) {
+  cluster_sync();
+  int u = part.unit;
+  const int qc = u % A.nqc;
+  u /= A.nqc;
+  const int h = u % A.Hkv, r = u / A.Hkv, nq8 = A.nq * 8, S = A.cluster;
+  const Req rq = load_req(A, r);
+  const int d = threadIdx.x % HD, step = S * (threads / HD);
+  if ((int)threadIdx.x < threads)
+    for (int x = part.rank + S * (threadIdx.x / HD); x < nq8; x += step) {
+      const int qi = qc * nq8 + x;
+      if (qi >= rq.n * A.GH) break;
+      const uint32_t ro = rec + (x >> 3) * tile_stride + ((x & 7) * HD + d) * 4, rm = ml + x * 8;
+      float m = -INFINITY, l = 0.f, acc = 0.f;
+      for (int k0 = 0; k0 < S; k0 += 8) {
+        float mk[8], lk[8], ok[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const bool in = k0 + k < S;
+          const uint32_t am = cluster_addr(rm, in ? k0 + k : 0), ao = cluster_addr(ro, in ? k0 + k : 0);
+          mk[k] = in ? ld_cluster(am) : -INFINITY;
+          lk[k] = in ? ld_cluster(am + 4) : 0.f;
+          ok[k] = in ? ld_cluster(ao) : 0.f;
+        }
+        float nm = m;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) nm = fmaxf(nm, mk[k]);
+        const float ref = nm == -INFINITY ? 0.f : nm, f0 = exp2_fast(m - ref);
+        l *= f0;
+        acc *= f0;
+        m = nm;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float f = exp2_fast(mk[k] - ref);
+          l = fmaf(f, lk[k], l);
+          acc = fmaf(f, ok[k], acc);
+        }
+      }
+      const int row = group_row(A, qi), head = h * A.GH + qi - row * A.GH;
+      const float inv = l != 0.f ? 1.f / l : 0.f;  // (NaN stays NaN)
+      store_elem<DT>(A.out, (int64_t)(rq.row0 + row) * A.out_stride + (int64_t)head * HD + d, acc * inv);
+      if (d == 0 && A.lse) A.lse[(int64_t)(rq.row0 + row) * A.Hq + head] = (m + log2f(l)) * LN2;
+    }
+  cluster_sync();  // (nobody's shared memory goes while another reads it)
+}
+
+// A dependent launch of a grid of clusters.
+inline cudaError_t launch_pdl_cluster(const void* fn, dim3 grid, dim3 block, void** args, size_t smem, int cluster,
+                                      cudaStream_t s) {
+  if (cluster <= 1) return launch_pdl(fn, grid, block, args, smem, s);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
 // The tcgen05 kernel (e4m3, head_dim 128): rows of the pool's view < 2^31.

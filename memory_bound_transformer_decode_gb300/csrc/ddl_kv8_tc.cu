@@ -81,6 +81,7 @@ struct Shared {
   uint32_t fresh[2];  // per warpgroup: some query that may still meet a key has met none
   int32_t hi[8 * NT], lo[8 * NT];
   int64_t place[8 * NT];
+  float2 ml[8 * NT];
   float wred[4][8 * NT];
   uint32_t nan[2][4];
   uint64_t fullk[3], fullv[3], empty[3], sfull[2], pfull, pvdone, qfull, fin;
@@ -205,18 +206,18 @@ struct Segs {
   int64_t rec;
   __device__ __forceinline__ bool next(const AttArgs& A, const int64_t* pre) {
     if (x >= end) return false;
-    if (A.whole) {
-      int bid = blockIdx.x;
-      qc = bid % A.nqc;
-      bid /= A.nqc;
-      h = bid % A.Hkv;
-      r = bid / A.Hkv;
+    if (A.cluster) {
+      const ClusterPart part(A);
+      int u = part.unit;
+      qc = u % A.nqc;
+      u /= A.nqc;
+      h = u % A.Hkv;
+      r = u / A.Hkv;
       rq = load_req(A, r);
       x = end;
       if (qc >= unit_groups(A, rq)) return false;
-      c0 = rq.b0;
-      c1 = rq.b1;
-      direct = true;
+      part.blocks(A, rq, c0, c1);
+      direct = A.cluster == 1;
       rec = 0;
       return true;
     }
@@ -282,7 +283,7 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
   first.x = 0;
   first.end = 1;
   first.r = 0;
-  if (!A.whole) {
+  if (!A.cluster) {
     const int64_t W = unit_prefix<G::THREADS>(A, pre, S.wsum);
     const int64_t n = share_count(A, W);
     if ((int64_t)blockIdx.x >= n || W == 0) {
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
       }
     }
   } else if (tid == 0 && A.bad) {
-    if (load_req(A, blockIdx.x / A.nqc / A.Hkv).bad) atomicOr(A.bad, 1);
+    if (load_req(A, blockIdx.x / A.cluster / A.nqc / A.Hkv).bad) atomicOr(A.bad, 1);
   }
   auto fail = [&]() {
     if (lane == 0 && A.bad) atomicOr(A.bad, 2);
@@ -718,13 +719,14 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
             place = (int64_t)(s.rq.row0 + row) * A.out_stride + (int64_t)head * 128;
             f = lq != 0.f ? f / lq : 0.f;  // (NaN stays NaN)
             if (A.lse) A.lse[(int64_t)(s.rq.row0 + row) * A.Hq + head] = (m + log2f(lq)) * LN2;
-          } else {
+          } else if (!A.cluster) {
             place = (s.rec * NQ + x) * 128;
             *reinterpret_cast<float2*>(A.rec_ml + (s.rec * NQ + x) * 2) = make_float2(m, lq);
           }
         }
         S.al[x] = f;
         S.place[x] = place;
+        S.ml[x] = make_float2(m, lq);
       }
       ssync(1 + wg, 128);
 #pragma unroll
@@ -742,6 +744,10 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
           const int x = x0 + 8 * j + q;
           const int64_t place = S.place[x];
           const float o = fmaf(__uint_as_float(v[8 + q]), 1.f / BSCALE, __uint_as_float(v[q])) * S.al[x];
+          if (A.cluster > 1) {  // (the ring of K and V is done with: its copies have landed and been used)
+            reinterpret_cast<float*>(smem)[x * 128 + tok] = o;
+            continue;
+          }
           if (place < 0) continue;
           if (s.direct) store_elem<DT>(A.out, place + tok, o);
           else A.rec_o[place + tok] = o;
@@ -752,6 +758,11 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
   }
   tc_fence_before();
   __syncthreads();
+  if (A.cluster > 1) {
+    const ClusterPart part(A);
+    if (part.unit % A.nqc < unit_groups(A, load_req(A, part.unit / A.nqc / A.Hkv)))  // (the same for all its CTAs)
+      cluster_join<DT, 128>(A, part, sb, 8 * 128 * 4, smem_addr(S.ml), NS);
+  }
   if (warp == MW) {
     tc_fence_after();
     tmem_dealloc(tm, G::COLS);
@@ -802,11 +813,14 @@ int kv8_tc_launch(const AttArgs& a, int dtype, int64_t rows, void* stream) {
                                          : tc_fn<DDL_T_F16>(ex, a.nq);
   const bool f32 = dtype == DDL_T_F32;
   const size_t smem = (a.nq == 1 ? tc_smem<1>(f32) : a.nq == 2 ? tc_smem<2>(f32) : tc_smem<4>(f32)) + 16 +
-                      (a.whole ? 0 : (size_t)(a.R + 1) * 8);
+                      (a.cluster ? 0 : (size_t)(a.R + 1) * 8);
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
   if (e != cudaSuccess) return cuda_status(e);
+  if (a.cluster > 8 && (e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+    return cuda_status(e);
   void* args[] = {&p};
-  return cuda_status(launch_pdl(fn, dim3((unsigned)a.ctas), dim3((unsigned)threads), args, smem, (cudaStream_t)stream));
+  return cuda_status(launch_pdl_cluster(fn, dim3((unsigned)a.ctas), dim3((unsigned)threads), args, smem, a.cluster,
+                                        (cudaStream_t)stream));
 }
 
 }  // namespace ddl
