@@ -683,14 +683,14 @@ int att_sms(int& sms) {
 }
 
 // Clusters: CTAs of a unit at most (16 is past the portable 8, and two fit a
-// GPC's SMs side by side), blocks a CTA takes at least, and how many blocks in a
-// row are worth the shares' fixed cost (6 us).
-constexpr int MAX_CLUSTER = 16, MIN_PART = 16, CLUSTER_GAIN = 40;
+// GPC's SMs side by side), blocks a CTA takes at least.
+constexpr int MAX_CLUSTER = 16, MIN_PART = 16;
 
 struct AttPlan {
   int32_t nq, nqc, cluster, ctas, deep;  // deep: a unit may have many shares
   int32_t unit_cost, min_share;          // of a CTA's share, in blocks
   int64_t rec_ml, prefix, total;         // workspace offsets
+  int64_t cost;                          // estimate, in 0.1 us
 };
 
 int check_sizes(int32_t H_q, int32_t H_kv, int32_t hd, int32_t R, int32_t T, int32_t max_rows, int32_t max_len) {
@@ -702,8 +702,8 @@ int check_sizes(int32_t H_q, int32_t H_kv, int32_t hd, int32_t R, int32_t T, int
   return DDL_OK;
 }
 
-int att_plan(bool tc, int32_t H_q, int32_t H_kv, int32_t hd, int32_t R, int32_t max_rows, int32_t max_len,
-             int32_t window, AttPlan& p) {
+int att_plan(bool tc, bool f32, int32_t H_q, int32_t H_kv, int32_t hd, int32_t R, int32_t max_rows, int32_t max_len,
+             int32_t window, bool clusters, AttPlan& p) {
   int sms = 0;
   const int st = att_sms(sms);
   if (st) return st;
@@ -718,23 +718,43 @@ int att_plan(bool tc, int32_t H_q, int32_t H_kv, int32_t hd, int32_t R, int32_t 
   p.total = 256;
   p.deep = 0;
   p.unit_cost = p.min_share = 1;
-  // A cluster per unit, of as many CTAs as fill the machine once.  Against the
-  // shares it saves the sums of the lengths, the records' way through memory
-  // and a launch, and pays for every request what the longest costs.
+  // What it will take, in 0.1 us, by what the two kernels measured (head_dim
+  // 128, one GB300): a call 4 us (tcgen05 7) apart from its blocks; 8 blocks in a
+  // row of a CTA, for each of its query tiles, 0.9 us while the ring's first fill
+  // lasts and 2.8 after it (fp32 rows 1.5 and 4), on tcgen05 1.0 us for one tile,
+  // 1.6 for two, 2.1 for four; a further wave of CTAs 2 us (5); a cluster's join
+  // 1.3 us; shares 6 to 8 us for the sums of the lengths, the records' way through
+  // memory and the second launch, and every unit a CTA begins as much as a wave.
+  // E.g. 1 request of 600 tokens, 8 K/V heads: clusters 7.1 us (tcgen05 9.3),
+  // shares 11.4 (12.5); of 8193: 14.2 (12.8), 15.4 (14.6); 64 requests of up to
+  // 2049: shares 50 (37).
+  const int64_t fixed = tc ? 70 : 40, again = fixed - 20;
+  auto in_a_row = [&](int64_t b) -> int64_t {
+    if (tc) return (b + 7) / 8 * (p.nq == 1 ? 10 : p.nq == 2 ? 16 : 21);
+    const int64_t groups = ATT_WARPS / p.nq, n = (b + groups - 1) / groups, first = n < 3 ? n : 3;
+    return f32 ? 15 * first + 40 * (n - first) : 9 * first + 28 * (n - first);
+  };
+  // A cluster per unit, of as many CTAs as fill the machine once; it pays for
+  // every request what the longest costs.
   p.cluster = 1;
   while (p.cluster < MAX_CLUSTER && units * 2 * p.cluster <= slots && p.cluster * MIN_PART < blocks) p.cluster *= 2;
   const int64_t waves = (units * p.cluster + slots - 1) / slots;
-  const int64_t alone = waves * ((blocks + p.cluster - 1) / p.cluster);     // blocks a CTA takes, one after the other
-  const int64_t shared = (units * blocks * (R > 1 ? 5 : 8) / 8 + slots - 1) / slots;  // (lengths up to the bound: about 5/8)
-  if (alone <= shared + CLUSTER_GAIN) {
+  p.cost = waves * (again + in_a_row((blocks + p.cluster - 1) / p.cluster)) + 20 + (p.cluster > 1 ? 13 : 0);
+  // (shares: ragged lengths up to the bound come to about 5/8 of it)
+  const int64_t least = tc ? 8 : 16;
+  int64_t share = (units * blocks * (R > 1 ? 5 : 8) / 8 + slots - 1) / slots;
+  share = share < least ? least : share;
+  const int64_t shares = fixed + (tc ? 60 : 80) + units * again / slots + in_a_row(share);
+  if (p.cost <= shares || clusters) {
     p.ctas = (int32_t)(units * p.cluster);
     return DDL_OK;
   }
+  p.cost = shares;
   // Measured at 64 requests of up to 8192 tokens, 64/8 heads (tcgen05: cost 16 / 24 / 40 110 / 106 / 99 us; warp MMAs
   // on 16 requests of 28/4 heads: cost 16 / 24 / 40 18 / 20 / 23 us).
   p.cluster = 0;
   p.unit_cost = tc ? 48 : 16;
-  p.min_share = p.unit_cost + (tc ? 8 : 16);
+  p.min_share = p.unit_cost + (int32_t)least;
   const int64_t all = ((int64_t)max_len + 15) / 16;
   const int64_t most = (units * (all + p.unit_cost) + p.min_share - 1) / p.min_share;
   p.ctas = (int32_t)(most < slots ? most : slots);
@@ -783,10 +803,13 @@ using namespace ddl;
 extern "C" size_t ddl_kv8_attention_workspace_bytes(int32_t H_q, int32_t H_kv, int32_t head_dim, int32_t R, int32_t T,
                                                     int32_t max_rows, int32_t max_len) {
   if (check_sizes(H_q, H_kv, head_dim, R, T, max_rows, max_len)) return 0;
-  AttPlan p, q;  // of either kernel and without a window, the most any call of these sizes takes
-  if (att_plan(false, H_q, H_kv, head_dim, R, max_rows, max_len, 0, p)) return 0;
-  if (att_plan(true, H_q, H_kv, head_dim, R, max_rows, max_len, 0, q)) return 0;
-  return (size_t)(p.total > q.total ? p.total : q.total);
+  int64_t most = 0;  // of either kernel and any row type, without a window: as much as any call of these sizes takes
+  for (int k = 0; k < 4; ++k) {
+    AttPlan p;
+    if (att_plan(k & 1, k >> 1, H_q, H_kv, head_dim, R, max_rows, max_len, 0, false, p)) return 0;
+    if (p.total > most) most = p.total;
+  }
+  return (size_t)most;
 }
 
 extern "C" int ddl_kv8_attention(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, int32_t head_dim, ddl_dtype dtype,
@@ -811,10 +834,22 @@ extern "C" int ddl_kv8_attention(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, i
   for (const void* p : {(const void*)q_off, (const void*)kv_len, (const void*)page_table, (const void*)lse,
                         (const void*)bad_out})
     if ((uintptr_t)p & 3u) return DDL_ERR_ALIGN;
+  // The plan; with a window, shares only where the call without one has room for them.
+  auto plan_of = [&](bool tcgen05, AttPlan& p) -> int {
+    const int rc = att_plan(tcgen05, dtype == DDL_T_F32, H_q, H_kv, head_dim, R, max_rows, max_len, 0, false, p);
+    if (rc || opts->window == 0) return rc;
+    return att_plan(tcgen05, dtype == DDL_T_F32, H_q, H_kv, head_dim, R, max_rows, max_len, opts->window, p.cluster > 0, p);
+  };
   AttPlan pl;
+  if ((st = plan_of(false, pl))) return st;
   const int64_t pool_rows = kv->pages * kv->page_size * H_kv;
-  const bool tc = kv->type == DDL_KV8_E4M3 && head_dim == 128 && pool_rows < (1ll << 31);
-  if ((st = att_plan(tc, H_q, H_kv, head_dim, R, max_rows, max_len, opts->window, pl))) return st;
+  bool tc = kv->type == DDL_KV8_E4M3 && head_dim == 128 && pool_rows < (1ll << 31);
+  if (tc) {
+    AttPlan p;
+    if ((st = plan_of(true, p))) return st;
+    tc = p.cost < pl.cost;
+    if (tc) pl = p;
+  }
   if (ws_bytes < (size_t)pl.total) return DDL_ERR_WORKSPACE;
   AttArgs a;
   a.k = kv->k;
