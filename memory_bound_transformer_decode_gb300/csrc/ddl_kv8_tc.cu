@@ -18,7 +18,7 @@
 // limbs 1 .. L (one MMA pass each, summed in the accumulator), group B the
 // next L, scaled by 16^L so that e4m3's narrow range does not cut them off, in
 // the same passes.  L = 2 for 16-bit rows (Q 2^-16; P rounded to fp16, 2^-11,
-// below the output's own rounding, in three limbs), 3 for fp32 rows (2^-24).  What falls below
+// below the output's own rounding), 3 for fp32 rows (2^-24).  What falls below
 // e4m3's smallest subnormal in group B is 2^-26 of a row's largest q and 2^-23
 // of the largest weight (L = 2).
 //
@@ -666,7 +666,7 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
             w[q] = p * wv;
           }
           uint2 a[L], b[L];
-          if (L == 2) {  // fp16 (2^-11) as three limbs: what each leaves is exact in fp16
+          if (L == 2) {  // fp16 (2^-11) as four limbs: what each leaves is exact in fp16
             uint32_t h[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) h[q] = pack_f16x2(w[2 * q], w[2 * q + 1]);
@@ -674,8 +674,8 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
             a[1] = limb8h(h, true);
 #pragma unroll
             for (int q = 0; q < 4; ++q) h[q] = hmul2_bits(h[q], 0x5c005c00u);  // times 256
-            b[0] = limb8h(h, false);
-            b[1] = make_uint2(0u, 0u);
+            b[0] = limb8h(h, true);
+            b[1] = limb8h(h, false);  // (small weights: what limb 3 leaves of them is up to 2^-19 of the largest)
           } else {
 #pragma unroll
             for (int p = 0; p < 2 * L; ++p) {

@@ -299,6 +299,36 @@ def test_attention_long_and_wide(R, L):
     check_attention(*setup(R, [1] * R, 16, 2, 128, 64, lens, "e4m3", "f32", seed=R))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("n_rows,opts", [([1] * 7, {}), ([1] * 7, dict(window=33, slopes=True)),
+                                         ([4, 0, 1, 64, 3, 17, 2], {}),
+                                         ([1, 33, 2, 9, 64, 0, 5], dict(softcap=4.0, window=100, slopes=True)),
+                                         ([2] * 7, dict(softcap=20.0))])
+@pytest.mark.parametrize("bound", [2000, 9000, 60000])
+def test_attention_every_split(dtype, n_rows, opts, bound):
+    """The bound on the lengths chooses kernel and split (clusters of several sizes, shares); the lengths stay
+    short, empty and ragged."""
+    opts = dict(opts)
+    if opts.get("slopes"):
+        opts["slopes"] = torch.exp2(-torch.arange(12, device="cuda").float() / 2)
+    check_attention(*setup(7, n_rows, 12, 2, 128, 32, [1, 0, 40, 129, 16, 1900, 257], "e4m3", dtype, seed=12),
+                    rows_given=max(n_rows) > 1, max_len=bound, **opts)
+
+
+@pytest.mark.parametrize("codes,hd", [("int8", 128), ("e4m3", 64)])
+@pytest.mark.parametrize("bound", [2000, 60000])
+def test_attention_every_split_of_the_warp_kernel(codes, hd, bound):
+    for n_rows in ([1] * 6, [3, 0, 1, 40, 2, 8]):
+        check_attention(*setup(6, n_rows, 14, 2, hd, 16, [1, 0, 40, 129, 1700, 257], codes, "f32", seed=13),
+                        rows_given=max(n_rows) > 1, max_len=bound)
+
+
+def test_attention_one_request_in_clusters_of_every_size():
+    for L, H in ((40, 1), (300, 1), (600, 2), (1100, 1), (5000, 1), (5000, 8), (20000, 4)):
+        for codes in ("e4m3", "int8"):
+            check_attention(*setup(1, [1], 4 * H, H, 128, 64, [L], codes, "bf16", seed=L))
+
+
 def test_attention_bound_far_above_the_lengths():
     """max_len only sizes the launch."""
     s = setup(3, [1, 1, 1], 8, 2, 64, 16, [5, 100, 17], "int8", "f32")
