@@ -307,7 +307,8 @@ typedef enum { DDL_T_F32 = 0, DDL_T_BF16 = 1, DDL_T_F16 = 2 } ddl_dtype;
  * 2^31 and pages * H_kv * page_size / 16 < 2^31 (DDL_ERR_UNSUPPORTED);
  * head_dim 64 or 128, 1 <= H_kv <= DDL_KV8_MAX_HEADS (DDL_ERR_SHAPE).  Slot t
  * of a sequence is row t % page_size of page page_table[t / page_size]; the
- * *slot index* of a row is page * page_size + t % page_size. */
+ * *slot index* of a row is page * page_size + t % page_size.  Scales are finite
+ * and not negative (ddl_kv8_append writes powers of two >= 2^-126, and zero). */
 typedef struct {
     uint8_t* k;
     uint8_t* v;
@@ -382,8 +383,8 @@ int ddl_kv8_append(const ddl_kv8* kv, int32_t H_kv, int32_t head_dim, ddl_dtype 
  *     out = sum_j exp(s_j) v_j / sum_j exp(s_j),  lse = log sum_j exp(s_j).
  * A row without keys gives zeros and lse = -inf.  Rows of q that belong to no
  * request are neither read nor written.  A NaN code among the keys a row sees
- * gives NaN in its output; whatever lies in slots it does not see has no
- * effect.
+ * gives NaN in its output, and so does a scale of one of their blocks that is not
+ * finite (V: or negative); whatever lies in slots it does not see has no effect.
  *  - H_q % H_kv == 0, H_q / H_kv <= 8, head_dim 64 or 128 (DDL_ERR_SHAPE).
  *  - q, out: device [T][H_q][head_dim] of `dtype`, heads contiguous, rows
  *    q_stride / out_stride elements apart (>= H_q * head_dim, a multiple of 8),

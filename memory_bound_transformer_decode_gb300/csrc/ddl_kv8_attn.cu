@@ -30,13 +30,14 @@
 // Work.  A *unit* is the blocks of one request for one K/V head and up to 8
 // tiles of 8 queries; a CTA of 8 warps gives each tile 8 / tiles warps, which
 // take the unit's blocks in turn and join their results in shared memory.
-// Short axes (at most WHOLE_BLOCKS blocks) take one CTA a unit and one launch.
-// Else the blocks of all units, laid end to end (request, head, tiles), are cut
-// into equal contiguous shares, one per CTA, two CTAs per SM: ragged lengths
-// and any number of requests fill the machine evenly, and a CTA pays for the
-// start and the end of a unit only two or three times.  A unit that lies in one
-// share is written at once; the others leave a record (max, sum, O in fp32)
-// per share, joined in share order by a second kernel.
+// Few units or short axes take a cluster of 1 to 16 CTAs a unit and one launch:
+// the CTAs' records (max, sum, O in fp32) are joined in their shared memory, in
+// rank order.  Else the blocks of all units, laid end to end (request, head,
+// tiles), are cut into equal contiguous shares, one per CTA, two CTAs per SM:
+// ragged lengths and any number of requests fill the machine evenly, and a CTA
+// pays for the start and the end of a unit only two or three times.  A unit that
+// lies in one share is written at once; the others leave a record per share,
+// joined in share order by a second kernel.  att_plan estimates which costs less.
 #include <cuda_bf16.h>
 
 #include <mutex>
@@ -155,6 +156,7 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
   if (blk_l >= 0) {
     ks_l = A.ks[blk_l];
     vs_l = A.vs[blk_l];
+    check_scales(ks_l, vs_l);
   }
   // block i on its way into the ring; its place is lane i % 32's of this batch of 32 or the next
   const uint32_t ring = smem_addr(&S.w[warp].ring[0][0]) + lane * 16;
@@ -251,7 +253,7 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
 #pragma unroll
   for (int m = 0; m < MT; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
   float mrun[2] = {-INFINITY, -INFINITY}, lrun[2] = {0.f, 0.f};
-  float vref = 0.f, winv = 0.f;  // the largest V scale so far and P_SCALE / vref: P carries scale / vref
+  float vref = 0.f, vinv = 0.f;  // the largest V scale so far (and VREF_MIN) and its inverse: P carries scale / vref
 
 #pragma unroll 1
   for (int i = 0; i < nb; ++i) {
@@ -262,6 +264,7 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
       if (blk_n >= 0) {
         ks_n = A.ks[blk_n];
         vs_n = A.vs[blk_n];
+        check_scales(ks_n, vs_n);
       }
     }
     const bool none = __shfl_sync(FULL, blk_l, l) < 0;
@@ -303,7 +306,7 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int col = j & 1;
-      float s = (c[j] + c2[j]) * ks * cf[col];
+      float s = (c[j] + c2[j]) * (ks * cf[col]);
       if (EX) {
         if (A.softcap > 0.f) s = A.softcap * LOG2E * cap_tanh<DT>(s);
         s -= slope[col] * (float)(hi[col] - (key0 + g + (j >> 1) * 8));
@@ -373,15 +376,15 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
       }
     }
     if (vs > vref) {  // O is in units of vref
-      const float f = __fdiv_rn(vref, vs);
+      const float nref = fmaxf(vs, VREF_MIN), f = __fdiv_rn(vref, nref);
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int x = 0; x < 4; ++x) o[m][x] *= f;
-      vref = vs;
-      winv = __fdiv_rn(P_SCALE, vs);
+      vref = nref;
+      vinv = __frcp_rn(nref);
     }
-    const float wv = vs * winv;
+    const float wv = vs * vinv * P_SCALE;
     const float m0 = mrun[0] == -INFINITY ? 0.f : mrun[0], m1 = mrun[1] == -INFINITY ? 0.f : mrun[1];
     const float p0 = exp2_fast(c[0] - m0), p1 = exp2_fast(c[1] - m1), p2 = exp2_fast(c[2] - m0), p3 = exp2_fast(c[3] - m1);
     lrun[0] += p0 + p2;
@@ -430,7 +433,6 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
     lrun[0] += __shfl_xor_sync(FULL, lrun[0], x);
     lrun[1] += __shfl_xor_sync(FULL, lrun[1], x);
   }
-  const float back = vref * (1.f / P_SCALE);
   __syncwarp();
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
@@ -438,7 +440,8 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
 #pragma unroll
     for (int m = 0; m < MT; m += 2)
       *reinterpret_cast<float4*>(row + 2 * m) =
-          make_float4(o[m][c] * back, o[m][2 + c] * back, o[m + 1][c] * back, o[m + 1][2 + c] * back);
+          make_float4(o[m][c] * (1.f / P_SCALE) * vref, o[m][2 + c] * (1.f / P_SCALE) * vref,
+                      o[m + 1][c] * (1.f / P_SCALE) * vref, o[m + 1][2 + c] * (1.f / P_SCALE) * vref);
     if (g == 0) {
       S.ml[warp][2 * t + c][0] = mrun[c];
       S.ml[warp][2 * t + c][1] = lrun[c];
@@ -834,11 +837,12 @@ extern "C" int ddl_kv8_attention(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, i
   for (const void* p : {(const void*)q_off, (const void*)kv_len, (const void*)page_table, (const void*)lse,
                         (const void*)bad_out})
     if ((uintptr_t)p & 3u) return DDL_ERR_ALIGN;
+  const int32_t window = opts->window >= max_len ? 0 : opts->window;  // (a window as long as the bound hides nothing)
   // The plan; with a window, shares only where the call without one has room for them.
   auto plan_of = [&](bool tcgen05, AttPlan& p) -> int {
     const int rc = att_plan(tcgen05, dtype == DDL_T_F32, H_q, H_kv, head_dim, R, max_rows, max_len, 0, false, p);
-    if (rc || opts->window == 0) return rc;
-    return att_plan(tcgen05, dtype == DDL_T_F32, H_q, H_kv, head_dim, R, max_rows, max_len, opts->window, p.cluster > 0, p);
+    if (rc || window == 0) return rc;
+    return att_plan(tcgen05, dtype == DDL_T_F32, H_q, H_kv, head_dim, R, max_rows, max_len, window, p.cluster > 0, p);
   };
   AttPlan pl;
   if ((st = plan_of(false, pl))) return st;
@@ -872,7 +876,7 @@ extern "C" int ddl_kv8_attention(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, i
   a.out_stride = out_stride;
   a.scale = opts->scale;
   a.softcap = opts->softcap;
-  a.window = opts->window;
+  a.window = window;
   a.R = R;
   a.T = T;
   a.Hq = H_q;

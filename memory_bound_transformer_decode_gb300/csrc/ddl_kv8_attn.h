@@ -102,6 +102,17 @@ __device__ __forceinline__ int unit_groups(const AttArgs& A, const Req& q) {
   return (q.n * A.GH + 8 * A.nq - 1) / (8 * A.nq);
 }
 
+// A scale that is not finite, or negative for V: NaN for the rows that see one of
+// the block's tokens, through their scores, and nothing for the others (V's, as a
+// weight's factor or in the units of O, would reach every row of the tile).
+__device__ __forceinline__ void check_scales(float& ks, float& vs) {
+  if (fabsf(ks) < INFINITY && vs >= 0.f && vs < INFINITY) return;
+  vs = 0.f;
+  ks = __uint_as_float(0x7fffffffu);
+}
+// O is kept in units of the largest V scale met, at least this: its inverse is finite.
+constexpr float VREF_MIN = 0x1p-126f;
+
 // Byte mask of the e4m3 NaN codes (low 7 bits all set) of four codes.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   const uint32_t top = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;

@@ -341,6 +341,7 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
         if (page >= 0) {
           ks = A.ks[(head << bshift) + sub];
           vs = A.vs[(head << bshift) + sub];
+          check_scales(ks, vs);
         }
         const int32_t row = page >= 0 ? (int32_t)((head << A.pshift) + (sub << 4)) : P.rows;  // (none: zeros)
         page_n = page_of(g0 + 32 + lane);
@@ -525,7 +526,7 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
       float l[QW];
 #pragma unroll
       for (int q = 0; q < QW; ++q) l[q] = 0.f;
-      float vref = 0.f, winv = 0.f;
+      float vref = 0.f, vinv = 0.f;  // the largest V scale so far (and VREF_MIN) and its inverse
       for (int i = 0; i < nt; ++i, ++tc) {
         const uint32_t st = tc % G::STAGES;
         ok = ok && wait(fullk + 8 * st, (tc / G::STAGES) & 1);  // (the tile's scales)
@@ -628,9 +629,9 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
           }
           if (!waited) ok = ok && wait(pvdone, (tc - 1) & 1);
           waited = true;
-          const float nref = fmaxf(vmax, vref), fv = nref > 0.f ? __fdiv_rn(vref, nref) : 0.f;
+          const float nref = fmaxf(fmaxf(vmax, vref), VREF_MIN), fv = __fdiv_rn(vref, nref);
           vref = nref;
-          winv = nref > 0.f ? __fdiv_rn(TP_SCALE, nref) : 0.f;
+          vinv = __frcp_rn(nref);
           ssync(1 + wg, 128);
 #pragma unroll
           for (int q = 0; q < QW; ++q) {
@@ -654,7 +655,7 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
         }
         // the tile's weights, and their limbs as the PV operand (whose place is
         // free once the previous tile's PV MMAs are done)
-        const float wv = vs * winv;
+        const float wv = vs * vinv * TP_SCALE;
         uint4 pk[QW / 8][L];
 #pragma unroll
         for (int j = 0; j < QW / 8; ++j) {
@@ -711,7 +712,7 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
       if (tok < QW) {  // thread q: the query's place, factor and statistics
         const int x = x0 + tok, qi = q0 + x;
         const float lq = (S.wred[0][x] + S.wred[1][x]) + (S.wred[2][x] + S.wred[3][x]), m = S.m[x];
-        float f = vref * (1.f / TP_SCALE);
+        float f = 1.f / TP_SCALE;
         int64_t place = -1;
         if (qi < nqueries) {
           const int row = group_row(A, qi), head = s.h * A.GH + qi - row * A.GH;
@@ -743,7 +744,7 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
         for (int q = 0; q < 8; ++q) {
           const int x = x0 + 8 * j + q;
           const int64_t place = S.place[x];
-          const float o = fmaf(__uint_as_float(v[8 + q]), 1.f / BSCALE, __uint_as_float(v[q])) * S.al[x];
+          const float o = fmaf(__uint_as_float(v[8 + q]), 1.f / BSCALE, __uint_as_float(v[q])) * S.al[x] * vref;
           if (A.cluster > 1) {  // (the ring of K and V is done with: its copies have landed and been used)
             reinterpret_cast<float*>(smem)[x * 128 + tok] = o;
             continue;

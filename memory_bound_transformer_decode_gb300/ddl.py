@@ -513,13 +513,15 @@ def ddl_kv8_attention(pool: tuple, q: torch.Tensor, kv_len: torch.Tensor, page_t
     max_len bounds kv_len, max_rows the rows of a request.  scale: 1 / sqrt(hd)
     by default; softcap, window, slopes as in ddl.h.  Returns out (zeros where
     a new one is made and a row belongs to no request)."""
-    if out is None:
-        out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
-    if workspace is None:
-        T, H_q, hd = q.shape
-        workspace = torch.empty(ddl_kv8_attention_workspace_bytes(H_q, pool[0].shape[1], hd, kv_len.numel(), T,
-                                                                  max_rows, max_len),
-                                dtype=torch.uint8, device=q.device)
+    if out is None or workspace is None:  # made on the device and the stream that use them
+        with torch.cuda.device(q.device), torch.cuda.stream(stream):
+            if out is None:
+                out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+            if workspace is None:
+                T, H_q, hd = q.shape
+                workspace = torch.empty(ddl_kv8_attention_workspace_bytes(H_q, pool[0].shape[1], hd, kv_len.numel(),
+                                                                          T, max_rows, max_len),
+                                        dtype=torch.uint8, device=q.device)
     st = (_mod or _torch_module()).kv8_attention(pool, q, kv_len, page_table, max_len, q_off, max_rows, scale, softcap,
                                                  window, slopes, out, lse, workspace, bad,
                                                  stream and stream.cuda_stream)
@@ -566,6 +568,8 @@ def ddl_stack_step_kv8(shape: Shape, wtype: int, layers: list, pools: list, *, r
     v_scale) per layer) for the rows that ddl_page_plan has placed."""
     lib = load()
     x = x_bf16 if x_bf16 is not None else resid_in
+    if x is None:
+        raise ValueError("x_bf16 or resid_in")
     T, R, L, dev = x.shape[0], kv_len.numel(), len(layers), x.get_device()
     if dev < 0 or len(pools) != L or page_table.dim() != 2:
         raise ValueError("tensors on a CUDA device, a pool for each layer, page_table [R, pages_per_seq]")

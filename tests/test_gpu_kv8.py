@@ -351,6 +351,70 @@ def test_attention_scales_of_any_size():
     check_attention(pool, q, q_off, lens, table)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("codes,hd,H_kv,lens,bound", [
+    ("e4m3", 128, 1, [200, 64], None), ("int8", 64, 1, [200, 64], None), ("e4m3", 128, 8, [4000, 300, 2100], None),
+    ("int8", 128, 8, [4000, 300, 2100], 60000), ("e4m3", 128, 8, [4000, 300, 2100], 60000)])
+def test_attention_smallest_v_scales(dtype, codes, hd, H_kv, lens, bound):
+    """V scales at the smallest a call writes (2^-126), above it and, subnormal, below it."""
+    pool, q, q_off, lens, table = setup(len(lens), [1] * len(lens), 4 * H_kv, H_kv, hd, 16, lens, codes, dtype, seed=9)
+    vs = pool[3]
+    small = torch.tensor([2.0 ** -126, 1.37 * 2.0 ** -125, 2.0 ** -130, 2.0 ** -119], device="cuda")
+    for some in (small, small[2:3]):
+        i = torch.arange(vs.numel(), device="cuda") * 7 % len(some)
+        vs.copy_(some[i].view(vs.shape))
+        check_attention(pool, q, q_off, lens, table, max_len=bound)
+
+
+@pytest.mark.parametrize("scale", [math.inf, -math.inf, math.nan, -1.0])
+@pytest.mark.parametrize("codes,hd,bound", [("e4m3", 128, 1000), ("int8", 128, 1000), ("e4m3", 64, 60000),
+                                            ("e4m3", 128, 60000)])
+def test_attention_bad_scale_reaches_only_the_rows_that_see_its_block(scale, codes, hd, bound):
+    n, L, window = 40, 300, 64
+    pool, q, q_off, lens, table = setup(2, [n, 1], 8, 1, hd, 16, [L, 90], codes, "bf16", seed=14)
+    args = (q, dev(lens), dev(table), bound)
+    kw = dict(q_off=dev(q_off), max_rows=n, window=window)
+    want, _, tol, _ = ref.attention(pool, q, q_off, lens, table, hd ** -0.5, 0.0, window, None)
+    for which in (2, 3):
+        if which == 2 and scale == -1.0:
+            continue  # (a factor of the scores like any other)
+        for block in (12, 13, 17):  # tokens 16 b .. 16 b + 15; row i sees 197 + i .. 260 + i
+            bad_pool = [t.clone() for t in pool]
+            bad_pool[which][int(table[0, block]), 0, 0] = scale
+            out = ddl.ddl_kv8_attention(tuple(bad_pool), *args, **kw)
+            p = np.arange(L - n, L)
+            sees = torch.from_numpy(np.concatenate([(p >= 16 * block) & (p - window + 1 <= 16 * block + 15), [False]]))
+            assert 0 < int(sees.sum()) < n + 1
+            assert out[sees.cuda()].isnan().all()
+            # The others: not the clean run's bits (the running maximum and the unit of the weights' rounding
+            # follow the tiles' scales, and the bad one counts as zero there), but within the same bound: it
+            # holds for any running maximum, and a smaller largest V scale only lowers its floor.
+            err = (out.double() - want).abs() - tol
+            assert (err[~sees.cuda()] <= 0).all(), f"out past its bound by {float(err[~sees.cuda()].max()):.3g}"
+
+
+def test_attention_window_as_long_as_can_be():
+    s = setup(3, [4, 0, 7], 8, 2, 128, 16, [3, 20, 400], "e4m3", "bf16", seed=6)  # (a request with more rows than tokens)
+    want = check_attention(*s)
+    for window in (400, 401, 2 ** 31 - 1):
+        assert torch.equal(check_attention(*s, window=window), want)
+
+
+def test_attention_makes_its_tensors_on_the_stream_that_uses_them():
+    pool, q, q_off, lens, table = setup(3, [1] * 3, 8, 2, 128, 16, [500, 40, 9], "e4m3", "bf16", seed=3)
+    want = check_attention(pool, q, q_off, lens, table)
+    kl, tb = dev(lens), dev(table)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)  # the current stream is busy: zeros made there would come too late
+    out = ddl.ddl_kv8_attention(pool, q, kl, tb, 60000, stream=s)
+    s.synchronize()
+    torch.cuda.synchronize()
+    ref_out = ddl.ddl_kv8_attention(pool, q, kl, tb, 60000)
+    assert torch.equal(out, ref_out)
+    assert (want.float() - out.float()).abs().max() < 0.1
+
+
 def test_attention_q_of_any_size():
     s = setup(4, [1] * 4, 4, 2, 64, 16, [40, 70, 3, 100], "e4m3", "f32", seed=2)
     q = s[1]
