@@ -12,15 +12,18 @@
 // bound by them and not by HBM); here 128 tokens and 8 queries cost four warps
 // about 200 each.
 //
-// Q and P, which are not e4m3, are split into e4m3 limbs, each the rounding of
-// what the ones before leave: a limb holds 4 significant bits, so bf16 is two
-// limbs exactly.  The B operand has 16 columns per 8 queries: group A holds
-// limbs 1 .. L (one MMA pass each, summed in the accumulator), group B the
-// next L, scaled by 16^L so that e4m3's narrow range does not cut them off, in
-// the same passes.  L = 2 for 16-bit rows (Q 2^-16; P rounded to fp16, 2^-11,
-// below the output's own rounding), 3 for fp32 rows (2^-24).  What falls below
-// e4m3's smallest subnormal in group B is 2^-26 of a row's largest q and 2^-23
-// of the largest weight (L = 2).
+// Q and P, which are not 8-bit, are split into 8-bit limbs.  The B operand has 16
+// columns per 8 queries: group A holds limbs 1 .. L (one MMA pass each, summed
+// in the accumulator), group B the next L, scaled by 16^L so that the type's
+// narrow range does not cut them off, in the same passes.
+//  - Q: e4m3, each limb the rounding of what the ones before leave, 4
+//    significant bits; L = 2 for 16-bit rows (2^-16 of a value, 2^-26 of the
+//    row's largest), 3 for fp32 rows (2^-24).
+//  - P of 16-bit rows: fp16 (2^-11, below the output's own rounding; 2^-30 of the
+//    largest weight) in four e5m2 limbs of 3 bits, exactly.  (As e4m3, whose
+//    conversions both ways the limbs then need: 64 rows on 8192 tokens 64.6 us,
+//    so 63.4, and 61.6 with two scores an instruction.)
+//  - P of fp32 rows: e4m3 as Q (2^-24; 2^-27 of the largest weight).
 //
 // A segment's tiles are taken from the newest token to the oldest: a distance
 // bias then raises the running maximum once and not with every tile (4 rows of
@@ -76,8 +79,8 @@ struct Meta {  // of a stage's tile
 template <int NT, int L>
 struct Shared {
   Meta meta[Geo<NT, L>::STAGES];
-  alignas(16) float cf[8 * NT], slope[8 * NT], hif[8 * NT], m[8 * NT], al[8 * NT];
-  alignas(16) float mref[8 * NT], shift[8 * NT];  // m, 0 for -inf; what a raise moves it by
+  alignas(16) float cf[8 * NT], nslope[8 * NT], hif[8 * NT], m[8 * NT], al[8 * NT];  // nslope: negated
+  alignas(16) float nref[8 * NT], shift[8 * NT];  // -m, 0 for -inf; what a raise moves scores by
   uint32_t fresh[2];  // per warpgroup: some query that may still meet a key has met none
   int32_t hi[8 * NT], lo[8 * NT];
   int64_t place[8 * NT];
@@ -94,7 +97,7 @@ struct Shared {
 __device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo, uint32_t sbo, uint32_t layout) {
   return umma_sdesc(addr, lbo, sbo) | ((uint64_t)layout << 61);
 }
-// kind::f8f6f4 with e4m3 operands and fp32 accumulators.
+// kind::f8f6f4 (e4m3 A; e4m3 or e5m2 B, by the descriptor), fp32 accumulators.
 __device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -147,7 +150,31 @@ __device__ __forceinline__ void warp_sums(float (&v)[N]) {
   for (int o = N; o < 32; o <<= 1) v[0] += __shfl_xor_sync(FULL, v[0], o);
 }
 
-__device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+// Two fp32 values in a register pair and the instructions that take both.
+struct F2 {
+  uint64_t u;
+  __device__ __forceinline__ F2() {}
+  __device__ __forceinline__ F2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(u) : "f"(a), "f"(b)); }
+  __device__ __forceinline__ explicit F2(float a) : F2(a, a) {}
+  __device__ __forceinline__ void get(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(u)); }
+};
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.u) : "l"(a.u), "l"(b.u), "l"(c.u));
+  return d;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.u) : "l"(a.u), "l"(b.u));
+  return d;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.u) : "l"(a.u), "l"(b.u));
+  return d;
+}
+
+__device__ __forceinline__ float2 ld2(const float* p) { return *reinterpret_cast<const float2*>(p); }
 
 // Eight values as e4m3 codes (byte i = value i), and what they leave.
 __device__ __forceinline__ uint2 limb8(float (&v)[8], bool rest) {
@@ -170,29 +197,17 @@ __device__ __forceinline__ uint2 limb8(float (&v)[8], bool rest) {
   return make_uint2(w[0], w[1]);
 }
 
-// The same of eight fp16 values (pairs).
-__device__ __forceinline__ uint32_t hmul2_bits(uint32_t a, uint32_t b) {
-  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
+// fp16 values (pairs) as e5m2 limbs.  e5m2 is the top byte of fp16, so that a
+// limb is a byte permute and what it leaves one exact subtraction: positive
+// values, each limb the next 3 significant bits, cut off.
+__device__ __forceinline__ uint32_t h2_bits(__half2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
+__device__ __forceinline__ __half2 h2_of(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
+__device__ __forceinline__ uint2 limb8h(const uint32_t (&h)[4]) {
+  return make_uint2(__byte_perm(h[0], h[1], 0x7531), __byte_perm(h[2], h[3], 0x7531));
 }
-__device__ __forceinline__ uint2 limb8h(uint32_t (&h)[4], bool rest) {
-  uint32_t w[2];
+__device__ __forceinline__ void drop_limb(uint32_t (&h)[4]) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e4m3x2.f16x2 a, %1;\n\tcvt.rn.satfinite.e4m3x2.f16x2 b, %2;\n\t"
-        "mov.b32 %0, {a, b};\n\t}"
-        : "=r"(w[i])
-        : "r"(h[2 * i]), "r"(h[2 * i + 1]));
-    if (rest) {
-      uint32_t lo, hi;
-      e4m3x4_f16x2(w[i], lo, hi);
-      const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&h[2 * i]), *reinterpret_cast<const __half2*>(&lo));
-      const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&h[2 * i + 1]), *reinterpret_cast<const __half2*>(&hi));
-      h[2 * i] = *reinterpret_cast<const uint32_t*>(&x);
-      h[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&y);
-    }
-  }
-  return make_uint2(w[0], w[1]);
+  for (int i = 0; i < 4; ++i) h[i] = h2_bits(__hsub2(h2_of(h[i]), h2_of(h[i] & 0xff00ff00u)));
 }
 
 // A CTA's segments: runs of blocks of one unit.
@@ -388,7 +403,8 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
       }
   } else if (warp == MW) {  // ------------------------------------------ MMA issue
     constexpr uint32_t IDESC_S = (1u << 4) | ((uint32_t)(G::N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-    constexpr uint32_t IDESC_O = IDESC_S | (1u << 15) | (1u << 16);  // A and B M/N-major
+    // P e5m2 (16-bit rows) or e4m3; A and B M/N-major
+    constexpr uint32_t IDESC_O = IDESC_S | (L == 2 ? 1u << 10 : 0u) | (1u << 15) | (1u << 16);
     const uint64_t kd = sdesc(sb, 16, 1024, 2), vd = sdesc(sb + KBYTES, 16384, 1024, 2);
     const uint64_t qd = sdesc(sb + G::Q_OFF, 16, 1024, 2), pd = sdesc(sb + G::P_OFF, 128, 2048, 0);
     uint32_t tc = 0, sg = 0;
@@ -507,13 +523,13 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
           else cf *= LOG2E;
           S.cf[x] = cf;
           if (EX) {
-            S.slope[x] = A.slopes && has ? A.slopes[head] * LOG2E : 0.f;
+            S.nslope[x] = A.slopes && has ? -A.slopes[head] * LOG2E : 0.f;
             S.hif[x] = (float)(p - s.c1 * 16);
           }
           S.hi[x] = has ? p : -1;
           S.lo[x] = A.window > 0 ? p - A.window + 1 : 0;
           S.m[x] = -INFINITY;
-          S.mref[x] = 0.f;
+          S.nref[x] = 0.f;
         }
       }
       fence_proxy_async_smem();
@@ -523,9 +539,9 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
       const int all_hi = s.rq.p0 + group_row(A, q0), any_hi = s.rq.p0 + group_row(A, last);
       const int all_lo = A.window > 0 ? any_hi - A.window + 1 : 0;
 
-      float l[QW];
+      F2 l[QW / 2];
 #pragma unroll
-      for (int q = 0; q < QW; ++q) l[q] = 0.f;
+      for (int q = 0; q < QW / 2; ++q) l[q] = F2(0.f);
       float vref = 0.f, vinv = 0.f;  // the largest V scale so far (and VREF_MIN) and its inverse
       for (int i = 0; i < nt; ++i, ++tc) {
         const uint32_t st = tc % G::STAGES;
@@ -545,30 +561,27 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
 #pragma unroll
           for (int j = 0; j < QW / 8; ++j) tmem_ld_32x32b_x16(tSq + (tc & 1) * G::N + 16 * j, v[j]);
           tmem_ld_wait();
+          const F2 ks2(ks), far2(back_of), down2(1.f / BSCALE);
 #pragma unroll
-          for (int j = 0; j < QW / 8; ++j)
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              sc[8 * j + q] = fmaf(__uint_as_float(v[j][8 + q]), 1.f / BSCALE, __uint_as_float(v[j][q]));
-        }
-#pragma unroll
-        for (int j = 0; j < QW; j += 4) {
-          const float4 cf = ld4(&S.cf[x0 + j]), mr = ld4(&S.mref[x0 + j]);
-          if (EX == 0) {
-            sc[j] = fmaf(sc[j], ks * cf.x, -mr.x);
-            sc[j + 1] = fmaf(sc[j + 1], ks * cf.y, -mr.y);
-            sc[j + 2] = fmaf(sc[j + 2], ks * cf.z, -mr.z);
-            sc[j + 3] = fmaf(sc[j + 3], ks * cf.w, -mr.w);
-          } else {
-            const float4 sl = ld4(&S.slope[x0 + j]), hf = ld4(&S.hif[x0 + j]);
-            const float f[4] = {cf.x, cf.y, cf.z, cf.w}, r[4] = {mr.x, mr.y, mr.z, mr.w};
-            const float w[4] = {sl.x, sl.y, sl.z, sl.w}, d[4] = {hf.x, hf.y, hf.z, hf.w};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              float x = sc[j + q] * (ks * f[q]);
-              if (EX == 2) x = A.softcap * LOG2E * cap_tanh<DT>(x);
-              sc[j + q] = fmaf(-w[q], d[q] + back_of, x) - r[q];  // (distances: exact to 2^24)
+          for (int q = 0; q < QW; q += 2) {
+            const uint32_t* w = &v[q / 8][q & 7];
+            const float2 cf = ld2(&S.cf[x0 + q]), nr = ld2(&S.nref[x0 + q]);
+            const F2 f = mul2(ks2, F2(cf.x, cf.y));
+            F2 x = fma2(F2(__uint_as_float(w[8]), __uint_as_float(w[9])), down2, F2(__uint_as_float(w[0]), __uint_as_float(w[1])));
+            if (EX == 0) {
+              x = fma2(x, f, F2(nr.x, nr.y));
+            } else {
+              const float2 ns = ld2(&S.nslope[x0 + q]), hf = ld2(&S.hif[x0 + q]);
+              x = mul2(x, f);
+              if (EX == 2) {
+                float a, b;
+                x.get(a, b);
+                x = mul2(F2(A.softcap * LOG2E), F2(cap_tanh<DT>(a), cap_tanh<DT>(b)));
+              }
+              x = fma2(F2(ns.x, ns.y), add2(F2(hf.x, hf.y), far2), x);  // (distances: exact to 2^24)
+              x = add2(x, F2(nr.x, nr.y));
             }
+            x.get(sc[q], sc[q + 1]);
           }
         }
         const bool there = (okm >> blk) & 1u;
@@ -604,8 +617,10 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
           for (int q = 0; q < QW; ++q) sc[q] = -INFINITY;
         }
         bool over = vmax > vref || i == 0 || S.fresh[wg];
+        float top = sc[0];
 #pragma unroll
-        for (int q = 0; q < QW; ++q) over = over || sc[q] > T_LAG;
+        for (int q = 1; q < QW; ++q) top = fmaxf(top, sc[q]);
+        over = over || top > T_LAG;
         bool waited = tc == 0;
         if (ssync_or(1 + wg, 128, over)) {  // raise the running maximum (and V's reference): O and l in the new units
 #pragma unroll
@@ -616,12 +631,12 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
           ssync(1 + wg, 128);
           if (tok < QW) {
             const int x = x0 + tok;
-            const float old = S.m[x], ref = S.mref[x];
+            const float old = S.m[x], ref = -S.nref[x];
             const float up = fmaxf(fmaxf(S.wred[0][x], S.wred[1][x]), fmaxf(S.wred[2][x], S.wred[3][x]));
             const float nm = fmaxf(old, ref + up), now = nm == -INFINITY ? 0.f : nm;
             S.al[x] = old == -INFINITY ? 0.f : exp2_fast(old - nm);
             S.m[x] = nm;
-            S.mref[x] = now;
+            S.nref[x] = -now;
             S.shift[x] = ref - now;
             const bool none = nm == -INFINITY && S.hi[x] >= s.c0 * 16;
             const uint32_t any = __ballot_sync((1u << QW) - 1u, none);
@@ -635,9 +650,10 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
           ssync(1 + wg, 128);
 #pragma unroll
           for (int q = 0; q < QW; ++q) {
-            l[q] *= S.al[x0 + q];
             sc[q] += S.shift[x0 + q];
           }
+#pragma unroll
+          for (int q = 0; q < QW; q += 2) l[q / 2] = mul2(l[q / 2], F2(S.al[x0 + q], S.al[x0 + q + 1]));
           if (i > 0) {
             tc_fence_after();
 #pragma unroll
@@ -655,28 +671,31 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
         }
         // the tile's weights, and their limbs as the PV operand (whose place is
         // free once the previous tile's PV MMAs are done)
-        const float wv = vs * vinv * TP_SCALE;
+        const F2 wv2(vs * vinv * TP_SCALE);
         uint4 pk[QW / 8][L];
 #pragma unroll
         for (int j = 0; j < QW / 8; ++j) {
           float w[8];
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float p = exp2_fast(sc[8 * j + q]);
-            l[8 * j + q] += p;
-            w[q] = p * wv;
+          for (int q = 0; q < 8; q += 2) {
+            const F2 p(exp2_fast(sc[8 * j + q]), exp2_fast(sc[8 * j + q + 1]));
+            l[4 * j + q / 2] = add2(l[4 * j + q / 2], p);
+            mul2(p, wv2).get(w[q], w[q + 1]);
           }
           uint2 a[L], b[L];
-          if (L == 2) {  // fp16 (2^-11) as four limbs: what each leaves is exact in fp16
+          if (L == 2) {  // fp16 (2^-11), 11 bits, as four limbs: exactly
             uint32_t h[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) h[q] = pack_f16x2(w[2 * q], w[2 * q + 1]);
-            a[0] = limb8h(h, true);
-            a[1] = limb8h(h, true);
+            a[0] = limb8h(h);
+            drop_limb(h);
+            a[1] = limb8h(h);
+            drop_limb(h);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) h[q] = hmul2_bits(h[q], 0x5c005c00u);  // times 256
-            b[0] = limb8h(h, true);
-            b[1] = limb8h(h, false);  // (small weights: what limb 3 leaves of them is up to 2^-19 of the largest)
+            for (int q = 0; q < 4; ++q) h[q] = h2_bits(__hmul2(h2_of(h[q]), h2_of(0x5c005c00u)));  // times 256
+            b[0] = limb8h(h);
+            drop_limb(h);
+            b[1] = limb8h(h);
           } else {
 #pragma unroll
             for (int p = 0; p < 2 * L; ++p) {
@@ -704,8 +723,11 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
         if (lane == 0) mbar_arrive(pfull);
       }
       // the result: thread = head dimension
-      warp_sums(l);  // lane q (and q + QW): the warp's sum of query q
-      if (lane < QW) S.wred[warp & 3][x0 + lane] = l[0];
+      float ls[QW];
+#pragma unroll
+      for (int q = 0; q < QW; q += 2) l[q / 2].get(ls[q], ls[q + 1]);
+      warp_sums(ls);  // lane q (and q + QW): the warp's sum of query q
+      if (lane < QW) S.wred[warp & 3][x0 + lane] = ls[0];
       if (nt > 0) ok = ok && wait(pvdone, (tc - 1) & 1);
       tc_fence_after();
       if (ssync_or(3, NS, !ok)) break;
