@@ -16,6 +16,11 @@ namespace {
 // so that one launch without any hand-over between CTAs does it all; then the
 // CTAs share out the step's rows and new pages, each of which finds its
 // request by binary search in the sums in shared memory.
+//
+// Bound by its round trips (launch, lengths, sums, table, store): 64 requests
+// 3.1 us on one GB300, 1000 with 65536 rows 5.5 (writing those takes 0.1 of HBM).
+// CTAs of 128 threads up to 512 requests, else 512: 64 requests 3.1 against 4.4
+// us, 300 3.8 against 4.7, 1000 (of a row each) 5.7 against 5.5.
 struct PlanArgs {
   const int32_t *old_len, *add_len, *free_pages;
   int32_t *table, *row_off, *kv_len, *row_pos, *slot, *used, *status;
@@ -186,7 +191,7 @@ struct AppendArgs {
   const int32_t* slot;
   int32_t* bad;
   int64_t slots;       // pages * page_size
-  int32_t T, H, pshift, span, ppc, vec;  // vec: the map is 16-byte aligned
+  int32_t T, H, pshift, span, ppc, vec, small;  // vec: the map is 16-byte aligned; small: T <= 256 (and span 1)
 };
 
 // (No load here is of the non-coherent kind: under dependent launches the kernel
@@ -274,10 +279,14 @@ struct Divider {
 // row takes it.  The rows stay in registers between the maximum and the codes,
 // so each is read once; the earlier tokens' codes are touched only when the
 // scale grows.  A CTA takes a window of `span` rows for up to 8 (head, K or V)
-// pairs: 1 row for decode steps, which are bound by their dependent round
-// trips (slot; rows and old scale; store) and want every block in a warp of its
-// own; 16 for prompts, which are bound by HBM and where 15 of 16 rows begin no
-// run.
+// pairs.  Decode steps are bound by their dependent round trips (slot; rows and
+// old scale; store) and want every block in a warp of its own; in prompts 15 of
+// 16 rows begin no run, and warps without one cost their launch.  So 1 row up to
+// 256 rows, then 2, 4 and, where one row a request is impossible, 16.  One GB300,
+// 8 K/V heads, bf16, spans 1 / 2 / 4 / 8 / 16: 257 requests of a row 7.9 / 7.4 /
+// 11.2 / 18.7 / 35 us, 1024 20.2 / 19.2 / 22.2 / 24.9 / 39.9; prompts of 600 rows
+// in all 7.9 / 7.4 / 7.0 / 6.5 / 9.6, of 2000 11.3 / 9.5 / 8.8 / 9.6 / 10.0, of
+// 8165 44.8 / 34.2 / 28.9 / 25.8 / 24.6.
 //
 // Rows of one block that are apart in the slot map (a page given to two
 // requests) must not race: every CTA looks through the whole map for the
@@ -490,7 +499,7 @@ __global__ void __launch_bounds__(256, DT == DDL_T_F32 && HD == 128 ? 2 : 3) kv8
     run.load(A, kv, h, c0 + win * A.span + k, __shfl_sync(FULL, block, k));
   }
   int first1 = 0x7fffffff, total1 = 0;
-  if (A.span == 1) {  // (T <= 256) each warp looks for itself, without a barrier
+  if (A.small) {  // each warp looks for itself, without a barrier
     const int blk = __shfl_sync(FULL, block, 0);
     int32_t s[8];
 #pragma unroll
@@ -502,13 +511,14 @@ __global__ void __launch_bounds__(256, DT == DDL_T_F32 && HD == 128 ? 2 : 3) kv8
       total1 += __popc(m);
     }
   } else {
+    if (!__syncthreads_or(starts != 0)) return;
     look_up(A, block, mine && warp % A.ppc == 0, win, begun, seen, count);
   }
   bool loaded = true;
   for (; starts; starts &= starts - 1, loaded = false) {
     const int k = __ffs(starts) - 1, at = win * A.span + k, blk = __shfl_sync(FULL, block, k);
-    int i = c0 + at, left = A.span == 1 ? total1 : seen[at].count;
-    if ((A.span == 1 ? first1 : seen[at].first) != i) continue;  // an earlier run's warp takes this one
+    int i = c0 + at, left = A.small ? total1 : seen[at].count;
+    if ((A.small ? first1 : seen[at].first) != i) continue;  // an earlier run's warp takes this one
     for (;;) {  // the block's runs, in map order
       if (!loaded) run.load(A, kv, h, i, blk);
       loaded = false;
@@ -556,9 +566,10 @@ extern "C" int ddl_page_plan(const int32_t* old_len, const int32_t* add_len, int
     if (!aligned4(p)) return DDL_ERR_ALIGN;
   PlanArgs a = {old_len, add_len, free_pages, page_table, row_off, kv_len, row_pos, slot, used, status,
                 R, log2_of(page_size), n_free, pages_per_seq, T};
-  const int nt = R <= 128 && T <= 1024 ? 128 : 512;
+  const int nt = R <= 512 ? 128 : 512;
   int64_t ctas = ((int64_t)T + nt - 1) / nt;  // (a new page has a row, so there are at most T of them)
-  ctas = ctas < 1 ? 1 : ctas > 152 ? 152 : ctas;
+  const int most = 152 * (512 / nt);
+  ctas = ctas < 1 ? 1 : ctas > most ? most : ctas;
   void* args[] = {&a};
   const size_t smem = (size_t)(2 * (R + 1)) * 4;
   const void* fn = nt == 128 ? (const void*)page_plan_kernel<128> : (const void*)page_plan_kernel<512>;
@@ -590,8 +601,9 @@ extern "C" int ddl_kv8_append(const ddl_kv8* kv, int32_t H_kv, int32_t head_dim,
   a.T = T;
   a.H = H_kv;
   a.pshift = log2_of(kv->page_size);
-  a.span = T > 256 ? APPEND_SPAN : 1;
+  a.span = T <= 256 ? 1 : T <= 512 ? 2 : T <= 4096 ? 4 : APPEND_SPAN;
   a.vec = aligned16(slot);
+  a.small = T <= 256;
   a.ppc = 2 * H_kv < 8 ? 2 * H_kv : 8;
   if (T > DDL_KV8_MAX_APPEND) return DDL_ERR_UNSUPPORTED;
   const int rows = 8 / a.ppc * a.span;  // of a CTA

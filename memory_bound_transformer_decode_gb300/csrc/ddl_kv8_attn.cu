@@ -160,7 +160,7 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
   }
   // block i on its way into the ring; its place is lane i % 32's of this batch of 32 or the next
   const uint32_t ring = smem_addr(&S.w[warp].ring[0][0]) + lane * 16;
-  const bool shared_codes = A.nq > 1;
+  const bool shared_codes = A.nq > 1;  // (4 requests of up to 16 rows, 4096 int8 tokens: 65 us through L1, 70 past it)
   const uint8_t *const k_lane = A.k + g * HD + t * 16, *const v_lane = A.v + 2 * t * HD + g * (HD / 8);
   uint32_t slot_in = 0, slot_out = 0;  // ring places of the next block to fetch and to use
   auto fetch = [&](int i, int32_t blks) {
@@ -543,7 +543,9 @@ __global__ void __launch_bounds__(ATT_WARPS * 32, 2) kv8_attention_kernel(const 
 // apart and are a unit's shares, two or three in a full batch and tens when one
 // request is spread over the machine: the time is that of one round trip to L2
 // if their loads go out together.  So PAR warps take a query, warp w of them
-// every PAR-th record, four at a time, each lane hd / 32 head dimensions.
+// every PAR-th record, four at a time, each lane hd / 32 head dimensions: 8 where
+// a unit has 8 shares and more, else 1 (the whole call, 1 request of 32768 tokens
+// 24.2 us against 30.7; 64 of up to 8192 105.8 against 96.9).
 template <int DT, int HD, int PAR>
 __global__ void __launch_bounds__(256) kv8_join_kernel(const __grid_constant__ AttArgs A) {
   constexpr int E = HD / 32;
@@ -561,7 +563,7 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(const __grid_constant__ A
   const int x = (int)(id % nq8), u = (int)(id / nq8), h = u / A.nqc, qc = u - h * A.nqc;
   const Req rq = load_req(A, r);
   int64_t W = 0, p0 = 0;
-  if (A.R <= 32) {
+  if (A.R <= 32) {  // (1 request of 32768 tokens: 24.3 us for the call, 24.7 with the prefix read after the wait)
     int64_t w = lane < A.R ? req_weight(A, load_req(A, lane)) : 0, before = lane < r ? w : 0;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {

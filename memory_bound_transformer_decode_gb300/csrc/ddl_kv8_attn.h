@@ -134,18 +134,13 @@ template <int NT>
 __device__ __forceinline__ int64_t unit_prefix(const AttArgs& A, int64_t* pre, int64_t* wsum) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int64_t base = 0;
-  if (A.R == 1) {
-    const Req rq = load_req(A, 0);
-    base = req_weight(A, rq);
-    if (blockIdx.x == 0 && tid == 0 && rq.bad && A.bad) atomicOr(A.bad, 1);
-    if (lane < 2) pre[lane] = lane ? base : 0;
-    __syncwarp();
-  } else if (A.R <= 32) {  // each warp for itself, without a barrier (all write the same values)
+  for (int r0 = 0; r0 < A.R; r0 += NT) {
+    const int r = r0 + tid;
     int64_t w = 0;
-    if (lane < A.R) {
-      const Req rq = load_req(A, lane);
+    if (r < A.R) {
+      const Req rq = load_req(A, r);
       w = req_weight(A, rq);
-      if (blockIdx.x == 0 && warp == 0 && rq.bad && A.bad) atomicOr(A.bad, 1);
+      if (blockIdx.x == 0 && rq.bad && A.bad) atomicOr(A.bad, 1);
     }
     int64_t inc = w;
 #pragma unroll
@@ -153,40 +148,20 @@ __device__ __forceinline__ int64_t unit_prefix(const AttArgs& A, int64_t* pre, i
       const int64_t y = __shfl_up_sync(FULL, inc, o);
       if (lane >= o) inc += y;
     }
-    if (lane < A.R) pre[lane + 1] = inc;
-    if (lane == 0) pre[0] = 0;
-    base = __shfl_sync(FULL, inc, 31);
-    __syncwarp();
-  } else {
-    for (int r0 = 0; r0 < A.R; r0 += NT) {
-      const int r = r0 + tid;
-      int64_t w = 0;
-      if (r < A.R) {
-        const Req rq = load_req(A, r);
-        w = req_weight(A, rq);
-        if (blockIdx.x == 0 && rq.bad && A.bad) atomicOr(A.bad, 1);
-      }
-      int64_t inc = w;
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    int64_t before = base, all = 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(FULL, inc, o);
-        if (lane >= o) inc += y;
-      }
-      if (lane == 31) wsum[warp] = inc;
-      __syncthreads();
-      int64_t before = base, all = 0;
-#pragma unroll
-      for (int v = 0; v < NT / 32; ++v) {
-        if (v < warp) before += wsum[v];
-        all += wsum[v];
-      }
-      if (r < A.R) pre[r] = before + inc - w;
-      base += all;
-      __syncthreads();
+    for (int v = 0; v < NT / 32; ++v) {
+      if (v < warp) before += wsum[v];
+      all += wsum[v];
     }
-    if (tid == 0) pre[A.R] = base;
+    if (r < A.R) pre[r] = before + inc - w;
+    base += all;
     __syncthreads();
   }
+  if (tid == 0) pre[A.R] = base;
+  __syncthreads();
   if (blockIdx.x == 0)
     for (int r = tid; r <= A.R; r += NT) A.prefix[r] = pre[r];
   return base;

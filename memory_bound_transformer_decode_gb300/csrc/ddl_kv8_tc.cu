@@ -334,6 +334,8 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
   };
 
   if (warp == CW) {  // -------------------------------------------------- copies
+    // Codes that one unit alone reads leave L2 first (64 requests of up to 8192 tokens 96.9 us, else 100.8), others not
+    // (64 rows of 16 requests 286 us, else 295).
     const uint64_t policy = A.nqc == 1 ? policy_evict_first() : policy_evict_normal();
     const int bshift = A.pshift - 4, bmask = (1 << bshift) - 1;
     uint32_t tc = 0;

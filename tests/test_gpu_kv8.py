@@ -189,6 +189,24 @@ def test_append_blocks_met_again(T, H):
     check_append(pool, k, v, np.maximum(slot, -1))
 
 
+@pytest.mark.parametrize("T", [256, 257, 512, 513, 4096, 4097, 9001])
+@pytest.mark.parametrize("H,dtype", [(1, "f32"), (4, "bf16")])
+def test_append_decode_rows_and_prompts_in_one_map(T, H, dtype):
+    """Rows of many requests, most of them one and some up to 100, from any place of a block on, padding between."""
+    g = np.random.RandomState(T)
+    slot, block = [], 0
+    while len(slot) < T:
+        n, at = (1 if g.rand() < 0.8 else g.randint(1, 101)), g.randint(16)
+        slot += [block * 16 + at + i for i in range(n)] + [-1] * (g.rand() < 0.1)
+        block += (at + n + 15) // 16 + g.randint(2)
+    pages = block // 2 + 2
+    slot = np.array(slot[:T])
+    slot = np.where(slot >= 0, g.permutation(2 * pages)[np.maximum(slot, 0) // 16] * 16 + slot % 16, -1)
+    pool = make_pool(pages, H, 32, 64, "e4m3", seed=T)
+    k, v = rows(T, H, 64, dtype, 5, 4.0)
+    check_append(pool, k, v, slot)
+
+
 def test_append_scale_steps_are_exact():
     """amax just at and past the largest code's multiples; ties of the rounding."""
     for codes, top in (("e4m3", 448.0), ("int8", 127.0)):
