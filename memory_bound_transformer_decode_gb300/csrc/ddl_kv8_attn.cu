@@ -32,7 +32,8 @@
 // take the unit's blocks in turn and join their results in shared memory.
 // Few units or short axes take a cluster of 1 to 16 CTAs a unit and one launch:
 // the CTAs' records (max, sum, O in fp32) are joined in their shared memory, in
-// rank order.  Else the blocks of all units, laid end to end (request, head,
+// rank order; many short units one CTA for up to 8 K/V heads of a request, its
+// warps divided among them.  Else the blocks of all units, laid end to end (request, head,
 // tiles), are cut into equal contiguous shares, one per CTA, two CTAs per SM:
 // ragged lengths and any number of requests fill the machine evenly, and a CTA
 // pays for the start and the end of a unit only two or three times.  A unit that
@@ -108,15 +109,17 @@ struct Att {
   };
   struct Smem {
     Warp w[ATT_WARPS];
-    alignas(16) uint2 ql[HL ? ATT_WARPS : 1][HL ? KS * 32 : 1];  // the remainders of Q (fp32 rows)
+    union {  // (so that two CTAs of fp32 rows fit an SM)
+      alignas(16) uint2 ql[HL ? ATT_WARPS : 1][HL ? KS * 32 : 1];  // the remainders of Q (fp32 rows)
+      float2 rml[ATT_WARPS * 8];  // the record's (max, sum), when the blocks are done
+    };
     float ml[ATT_WARPS][8][2];
-    float2 rml[ATT_WARPS * 8];
   };
   static __device__ __forceinline__ void segment(const AttArgs& A, Smem& S, int r, const Req& rq, int h, int qc,
                                                  int c0, int c1, bool direct, int64_t rec);
 };
 
-// Blocks [c0, c1) of the unit (request r, K/V head h, query tiles qc); the
+// Blocks [c0, c1) of the unit (request r, K/V heads h .. h + A.hp - 1, query tiles qc); the
 // result goes to the output (direct: they are all of the unit's blocks) or to
 // record `rec`.
 template <int CT, int DT, int HD, bool EX>
@@ -124,8 +127,8 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
                                                              int qc, int c0, int c1, bool direct, int64_t rec) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int nqueries = rq.n * A.GH;
-  const int groups = ATT_WARPS / A.nq;   // warps that share a tile's blocks
-  const int tile = qc * A.nq + warp % A.nq, kg = warp / A.nq;
+  const int tiles = A.nq * A.hp, groups = ATT_WARPS / tiles;  // warps that share a tile's blocks
+  const int wt = warp % tiles, tile = qc * A.nq + wt % A.nq, hw = h + wt / A.nq, kg = warp / tiles;
   const bool live = tile * 8 < nqueries;
 
   const int nb = live && c1 > c0 + kg ? (c1 - c0 - kg + groups - 1) / groups : 0;  // this warp's blocks
@@ -134,7 +137,7 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
   float4 f[KS];
   {
     const int64_t at = (int64_t)(rq.row0 + my_row) * A.q_stride +
-                       (int64_t)(h * A.GH + my_q - my_row * A.GH) * HD + t * 16;
+                       (int64_t)(hw * A.GH + my_q - my_row * A.GH) * HD + t * 16;
 #pragma unroll
     for (int s = 0; s < KS; ++s)
       f[s] = my_q < nqueries ? load_elem4<DT>(A.q, at + 64 * (s >> 2) + 4 * (s & 3)) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -146,7 +149,7 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
     if (i < nb) {
       const int b = c0 + kg + i * groups;
       const int32_t page = A.table[(int64_t)r * A.per + (b >> bshift)];
-      if (page >= 0 && page < A.pages) return (int32_t)((((int64_t)page * A.Hkv + h) << bshift) + (b & bmask));
+      if (page >= 0 && page < A.pages) return (int32_t)((((int64_t)page * A.Hkv + hw) << bshift) + (b & bmask));
       if (A.bad) atomicOr(A.bad, 1);
     }
     return -1;
@@ -230,7 +233,7 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
     lo[c] = A.window > 0 ? p - A.window + 1 : 0;
     const float q2 = __shfl_sync(FULL, qf, 4 * (2 * t + c));
     cf[c] = q2 * A.scale;
-    slope[c] = EX && A.slopes && has ? A.slopes[h * A.GH + qi - row * A.GH] * LOG2E : 0.f;
+    slope[c] = EX && A.slopes && has ? A.slopes[hw * A.GH + qi - row * A.GH] * LOG2E : 0.f;
     if (!EX) cf[c] *= LOG2E;
     else if (A.softcap > 0.f) cf[c] = __fdiv_rn(cf[c], A.softcap);
     else cf[c] *= LOG2E;
@@ -450,17 +453,17 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
   __syncthreads();
   // the tile's warps joined (in warp order): thread = (tile, query, 4 head dimensions)
   constexpr int DQ = HD / 4;
-  for (int x = threadIdx.x; x < A.nq * 8 * DQ; x += ATT_WARPS * 32) {
+  for (int x = threadIdx.x; x < tiles * 8 * DQ; x += ATT_WARPS * 32) {
     const int d = x % DQ, qq = (x / DQ) & 7, tl = x / (8 * DQ);
-    const int qi = (qc * A.nq + tl) * 8 + qq;
+    const int qi = (qc * A.nq + tl % A.nq) * 8 + qq;
     if (qi >= nqueries) continue;
     float m = -INFINITY;
-    for (int w = 0; w < groups; ++w) m = fmaxf(m, S.ml[tl + w * A.nq][qq][0]);
+    for (int w = 0; w < groups; ++w) m = fmaxf(m, S.ml[tl + w * tiles][qq][0]);
     const float mref = m == -INFINITY ? 0.f : m;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
     for (int w = 0; w < groups; ++w) {
-      const int wp = tl + w * A.nq;
+      const int wp = tl + w * tiles;
       const float f = exp2_fast(S.ml[wp][qq][0] - mref);
       const float4 v = *reinterpret_cast<const float4*>(&S.w[wp].o[qq][4 * d]);
       l = fmaf(f, S.ml[wp][qq][1], l);
@@ -469,7 +472,7 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
       acc.z = fmaf(f, v.z, acc.z);
       acc.w = fmaf(f, v.w, acc.w);
     }
-    const int row = group_row(A, qi), head = h * A.GH + qi - row * A.GH;
+    const int row = group_row(A, qi), head = (h + tl / A.nq) * A.GH + qi - row * A.GH;
     const int64_t rh = (int64_t)(rq.row0 + row) * A.Hq + head;
     if (A.cluster > 1) {
       *reinterpret_cast<float4*>(&S.w[tl].rest.rec[qq][4 * d]) = acc;
@@ -501,7 +504,7 @@ __global__ void __launch_bounds__(ATT_WARPS * 32, 2) kv8_attention_kernel(const 
     int u = part.unit;
     const int qc = u % A.nqc;
     u /= A.nqc;
-    const int h = u % A.Hkv, r = u / A.Hkv;
+    const int hg = A.Hkv / A.hp, r = u / hg, h = (u - r * hg) * A.hp;
     const Req rq = load_req(A, r);
     if (rq.bad && A.bad && tid == 0) atomicOr(A.bad, 1);
     if (qc >= unit_groups(A, rq)) return;  // (all CTAs of the cluster)
@@ -690,9 +693,15 @@ int att_sms(int& sms) {
 // Clusters: CTAs of a unit at most (16 is past the portable 8, and two fit a
 // GPC's SMs side by side), blocks a CTA takes at least.
 constexpr int MAX_CLUSTER = 16, MIN_PART = 16;
+// fp32 rows of 128: two CTAs fit an SM while the weights before so many requests fit beside the rings (64 requests of
+// up to 2049 in shares: 75 us, one CTA an SM; whole units of two heads a CTA: 58).
+constexpr int F32_TWO_CTAS_R = 55;
+static_assert(2 * (sizeof(Att<DDL_KV8_INT8, DDL_T_F32, 128, false>::Smem) + (F32_TWO_CTAS_R + 1) * 8 + ATT_WARPS * 8 + 1024) <=
+                  228 * 1024,
+              "two CTAs an SM");
 
 struct AttPlan {
-  int32_t nq, nqc, cluster, ctas, deep;  // deep: a unit may have many shares
+  int32_t nq, nqc, hp, cluster, ctas, deep;  // deep: a unit may have many shares
   int32_t unit_cost, min_share;          // of a CTA's share, in blocks
   int64_t rec_ml, prefix, total;         // workspace offsets
   int64_t cost;                          // estimate, in 0.1 us
@@ -718,7 +727,8 @@ int att_plan(bool tc, bool f32, int32_t H_q, int32_t H_kv, int32_t hd, int32_t R
   p.nqc = (tiles + p.nq - 1) / p.nq;
   int64_t keys = max_len;
   if (window > 0 && (int64_t)window + max_rows + 15 < keys) keys = (int64_t)window + max_rows + 15;
-  const int64_t blocks = (keys + 15) / 16, units = (int64_t)R * H_kv * p.nqc, slots = 2 * sms;
+  const int64_t blocks = (keys + 15) / 16, units = (int64_t)R * H_kv * p.nqc;
+  const int64_t slots = tc && f32 && p.nq == 4 ? sms : 2 * sms;  // CTAs that run at once (their shared memory)
   p.rec_ml = p.prefix = 0;
   p.total = 256;
   p.deep = 0;
@@ -726,38 +736,58 @@ int att_plan(bool tc, bool f32, int32_t H_q, int32_t H_kv, int32_t hd, int32_t R
   // What it will take, in 0.1 us, by what the two kernels measured (head_dim
   // 128, one GB300): a call 4 us (tcgen05 7) apart from its blocks; 8 blocks in a
   // row of a CTA, for each of its query tiles, 0.9 us while the ring's first fill
-  // lasts and 2.8 after it (fp32 rows 1.5 and 4), on tcgen05 1.0 us for one tile,
+  // lasts and 2.8 after it (1.4 where tiles share the codes; fp32 rows 1.5 and 4, in shares 1.0 and 3.1, at least 1.6), on tcgen05 1.0 us for one tile,
   // 1.6 for two, 2.1 for four; a further wave of CTAs 2 us (5); a cluster's join
   // 1.3 us; shares 6 to 8 us for the sums of the lengths, the records' way through
-  // memory and the second launch, and every unit a CTA begins as much as a wave.
+  // memory and the second launch, and every unit a CTA begins 3.5 us (5).
   // E.g. 1 request of 600 tokens, 8 K/V heads: clusters 7.1 us (tcgen05 9.3),
   // shares 11.4 (12.5); of 8193: 14.2 (12.8), 15.4 (14.6); 64 requests of up to
   // 2049: shares 50 (37).
   const int64_t fixed = tc ? 70 : 40, again = fixed - 20;
-  auto in_a_row = [&](int64_t b) -> int64_t {
+  auto in_a_row = [&](int64_t b, int64_t filling, int64_t after) -> int64_t {
     if (tc) return (b + 7) / 8 * (p.nq == 1 ? 10 : p.nq == 2 ? 16 : 21);
     const int64_t groups = ATT_WARPS / p.nq, n = (b + groups - 1) / groups, first = n < 3 ? n : 3;
-    return f32 ? 15 * first + 40 * (n - first) : 9 * first + 28 * (n - first);
+    const int64_t each = after / p.nq, least = f32 ? 16 : 14;
+    return filling * first + (each < least ? least : each) * (n - first);
   };
   // A cluster per unit, of as many CTAs as fill the machine once; it pays for
   // every request what the longest costs.
   p.cluster = 1;
   while (p.cluster < MAX_CLUSTER && units * 2 * p.cluster <= slots && p.cluster * MIN_PART < blocks) p.cluster *= 2;
-  const int64_t waves = (units * p.cluster + slots - 1) / slots;
-  p.cost = waves * (again + in_a_row((blocks + p.cluster - 1) / p.cluster)) + 20 + (p.cluster > 1 ? 13 : 0);
+  p.hp = 1;
+  if (p.cluster > 1 || tc) {
+    const int64_t waves = (units * p.cluster + slots - 1) / slots;
+    p.cost = waves * (again + in_a_row((blocks + p.cluster - 1) / p.cluster, f32 ? 15 : 9, f32 ? 40 : 28)) + 20 + (p.cluster > 1 ? 13 : 0);
+  } else {
+    // Many units: the CTA's warps are shared by hp K/V heads, whichever hp costs least: a wave of CTAs 3.5 us and
+    // its rounds of 8 blocks 0.9 us where it is one CTA an SM, else 1.6 (fp32 rows a tenth more).  E.g. 64
+    // requests of up to 512 int8 tokens, 32/8 heads: hp 1 / 2 / 4 / 8 21.1 / 18.0 / 19.4 / 32.6 us; 1000 of up to 128
+    // 148 / 102 / 78 / 68.
+    for (int hp = 1; hp == 1 || (hp * p.nq <= ATT_WARPS && H_kv % hp == 0); hp *= 2) {
+      const int64_t ctas = units / hp, waves = (ctas + slots - 1) / slots;
+      const int64_t rounds = (blocks * p.nq * hp + ATT_WARPS - 1) / ATT_WARPS, two = ctas > sms;
+      const int64_t cost = waves * (35 + 2 * hp + (two ? 16 : 9) * rounds) * (f32 ? 11 : 10) / 10 + 20;
+      if (hp > 1 && cost >= p.cost) continue;
+      p.cost = cost;
+      p.hp = hp;
+    }
+  }
   // (shares: ragged lengths up to the bound come to about 5/8 of it)
   const int64_t least = tc ? 8 : 16;
   int64_t share = (units * blocks * (R > 1 ? 5 : 8) / 8 + slots - 1) / slots;
   share = share < least ? least : share;
-  const int64_t shares = fixed + (tc ? 60 : 80) + units * again / slots + in_a_row(share);
+  int64_t shares = units * (tc ? again : 35) / slots + in_a_row(share, f32 ? 10 : 9, f32 ? 31 : 28);
+  if (!tc && f32 && hd == 128 && R > F32_TWO_CTAS_R) shares = shares * 5 / 2;
+  shares += fixed + (tc ? 60 : 80);
   if (p.cost <= shares || clusters) {
-    p.ctas = (int32_t)(units * p.cluster);
+    p.ctas = (int32_t)(units / p.hp * p.cluster);
     return DDL_OK;
   }
   p.cost = shares;
   // Measured at 64 requests of up to 8192 tokens, 64/8 heads (tcgen05: cost 16 / 24 / 40 110 / 106 / 99 us; warp MMAs
   // on 16 requests of 28/4 heads: cost 16 / 24 / 40 18 / 20 / 23 us).
   p.cluster = 0;
+  p.hp = 1;
   p.unit_cost = tc ? 48 : 16;
   p.min_share = p.unit_cost + (int32_t)least;
   const int64_t all = ((int64_t)max_len + 15) / 16;
@@ -896,6 +926,7 @@ extern "C" int ddl_kv8_attention(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, i
   a.min_share = pl.min_share;
   a.nq = pl.nq;
   a.nqc = pl.nqc;
+  a.hp = pl.hp;
   const bool ex = opts->softcap > 0.f || opts->slopes;
   const void* fn = nullptr;
   void* args[] = {&a};

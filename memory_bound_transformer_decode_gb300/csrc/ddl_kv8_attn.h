@@ -29,6 +29,7 @@ struct AttArgs {
   int32_t cluster;  // > 0: a cluster of so many CTAs a unit; 0: shares
   int32_t ctas;     // CTAs: of the clusters, or shares at most
   int32_t unit_cost, min_share;
+  int32_t hp;       // K/V heads of a CTA (a power of two, nq hp <= 8; 1 but for whole units of the warp kernel)
   int32_t nq, nqc;  // query tiles of 8 a unit has (a power of two <= 8), units over a request's query tiles
 };
 

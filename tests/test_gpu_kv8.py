@@ -347,6 +347,19 @@ def test_attention_one_request_in_clusters_of_every_size():
             check_attention(*setup(1, [1], 4 * H, H, 128, 64, [L], codes, "bf16", seed=L))
 
 
+@pytest.mark.parametrize("codes,dtype,hd", [("int8", "bf16", 128), ("e4m3", "f32", 64), ("int8", "f32", 128)])
+@pytest.mark.parametrize("H_q,H_kv", [(32, 8), (12, 12), (18, 6), (64, 8)])
+@pytest.mark.parametrize("R,most,rows", [(40, 60, 1), (150, 300, 1), (400, 16, 1), (70, 100, 3)])
+def test_attention_many_short_requests(codes, dtype, hd, H_q, H_kv, R, most, rows):
+    """Several K/V heads a CTA (1 to 8, by the sizes), with and without options, empty requests among them."""
+    g = np.random.RandomState(R + H_q)
+    n = g.randint(0, rows + 1, R) if rows > 1 else np.ones(R, int)
+    s = setup(R, n, H_q, H_kv, hd, 16, g.randint(0, most + 1, R), codes, dtype, seed=R)
+    check_attention(*s, max_len=most, rows_given=rows > 1)
+    slopes = torch.exp2(-torch.arange(H_q, device="cuda").float() / 2)
+    check_attention(*s, max_len=most, rows_given=rows > 1, window=19, slopes=slopes, softcap=9.0)
+
+
 def test_attention_bound_far_above_the_lengths():
     """max_len only sizes the launch."""
     s = setup(3, [1, 1, 1], 8, 2, 64, 16, [5, 100, 17], "int8", "f32")
