@@ -127,8 +127,9 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
                                                              int qc, int c0, int c1, bool direct, int64_t rec) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int nqueries = rq.n * A.GH;
-  const int tiles = A.nq * A.hp, groups = ATT_WARPS / tiles;  // warps that share a tile's blocks
-  const int wt = warp % tiles, tile = qc * A.nq + wt % A.nq, hw = h + wt / A.nq, kg = warp / tiles;
+  const int nqs = __ffs(A.nq) - 1, ts = nqs + __ffs(A.hp) - 1, tiles = 1 << ts;  // (powers of two)
+  const int groups = ATT_WARPS >> ts;  // warps that share a tile's blocks
+  const int wt = warp & (tiles - 1), tile = qc * A.nq + (wt & (A.nq - 1)), hw = h + (wt >> nqs), kg = warp >> ts;
   const bool live = tile * 8 < nqueries;
 
   const int nb = live && c1 > c0 + kg ? (c1 - c0 - kg + groups - 1) / groups : 0;  // this warp's blocks
@@ -455,7 +456,7 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
   constexpr int DQ = HD / 4;
   for (int x = threadIdx.x; x < tiles * 8 * DQ; x += ATT_WARPS * 32) {
     const int d = x % DQ, qq = (x / DQ) & 7, tl = x / (8 * DQ);
-    const int qi = (qc * A.nq + tl % A.nq) * 8 + qq;
+    const int qi = (qc * A.nq + (tl & (A.nq - 1))) * 8 + qq;
     if (qi >= nqueries) continue;
     float m = -INFINITY;
     for (int w = 0; w < groups; ++w) m = fmaxf(m, S.ml[tl + w * tiles][qq][0]);
@@ -472,7 +473,7 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
       acc.z = fmaf(f, v.z, acc.z);
       acc.w = fmaf(f, v.w, acc.w);
     }
-    const int row = group_row(A, qi), head = (h + tl / A.nq) * A.GH + qi - row * A.GH;
+    const int row = group_row(A, qi), head = (h + (tl >> nqs)) * A.GH + qi - row * A.GH;
     const int64_t rh = (int64_t)(rq.row0 + row) * A.Hq + head;
     if (A.cluster > 1) {
       *reinterpret_cast<float4*>(&S.w[tl].rest.rec[qq][4 * d]) = acc;
@@ -504,7 +505,7 @@ __global__ void __launch_bounds__(ATT_WARPS * 32, 2) kv8_attention_kernel(const 
     int u = part.unit;
     const int qc = u % A.nqc;
     u /= A.nqc;
-    const int hg = A.Hkv / A.hp, r = u / hg, h = (u - r * hg) * A.hp;
+    const int hg = A.Hkv >> (__ffs(A.hp) - 1), r = u / hg, h = (u - r * hg) * A.hp;
     const Req rq = load_req(A, r);
     if (rq.bad && A.bad && tid == 0) atomicOr(A.bad, 1);
     if (qc >= unit_groups(A, rq)) return;  // (all CTAs of the cluster)
