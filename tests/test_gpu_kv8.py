@@ -360,6 +360,29 @@ def test_attention_many_short_requests(codes, dtype, hd, H_q, H_kv, R, most, row
     check_attention(*s, max_len=most, rows_given=rows > 1, window=19, slopes=slopes, softcap=9.0)
 
 
+def test_attention_calls_on_three_streams_at_once():
+    """Clusters, shares and many rows side by side, each with its own workspace: the bits of the calls alone."""
+    cases = [(setup(1, [1], 16, 2, 128, 64, [9000], "e4m3", "f32", seed=1), 9000),
+             (setup(20, [1] * 20, 32, 8, 128, 16, [40 + 90 * i for i in range(20)], "e4m3", "bf16", seed=2), 30000),
+             (setup(2, [64, 33], 16, 2, 128, 32, [700, 1900], "e4m3", "bf16", seed=3), 2000)]
+    calls = []
+    for (pool, q, off, lens, table), bound in cases:
+        kw = dict(q_off=dev(off), max_rows=int(np.diff(off).max()))
+        n = ddl.ddl_kv8_attention_workspace_bytes(q.shape[1], pool[0].shape[1], 128, len(lens), q.shape[0],
+                                                  kw["max_rows"], bound)
+        args = (pool, q, dev(lens), dev(table), bound)
+        calls.append((args, kw, torch.empty(n, dtype=torch.uint8, device="cuda"),
+                      ddl.ddl_kv8_attention(*args, **kw), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(15):
+        for args, kw, ws, want, s in calls:
+            outs.append((ddl.ddl_kv8_attention(*args, **kw, workspace=ws, stream=s), want))
+    torch.cuda.synchronize()
+    for got, want in outs:
+        assert torch.equal(got, want)
+
+
 def test_attention_bound_far_above_the_lengths():
     """max_len only sizes the launch."""
     s = setup(3, [1, 1, 1], 8, 2, 64, 16, [5, 100, 17], "int8", "f32")
