@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
   tc_fence_after();
   const uint32_t tm = S.tslot, tO = tm + 2 * G::N;
   pdl_wait();
-  pdl_trigger();  // (after the wait: the join reads the lengths as soon as it starts)
+  pdl_trigger();
   Segs first;
   first.x = 0;
   first.end = 1;

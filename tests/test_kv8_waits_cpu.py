@@ -1,0 +1,40 @@
+"""What the kernels of the 8-bit cache read, and when, from their sources: under
+a dependent launch a grid runs beside its predecessors, and only its own wait
+makes what they wrote visible to it."""
+import os
+import re
+
+import pytest
+
+from memory_bound_transformer_decode_gb300 import build
+
+FILES = ("ddl_kv8.cu", "ddl_kv8_attn.cu", "ddl_kv8_tc.cu")
+# the launch's arguments that are device memory, and the helpers that read it
+READS = re.compile(r"load_req\s*\(|req_weight\s*\(|unit_prefix\s*<|load_elem4\s*<|"
+                   r"\bA\.(old_len|add_len|free_pages|q_off|kv_len|table|prefix|slot|scale|slopes|rec_o|rec_ml|ks|vs)\s*\[")
+
+
+def kernels():
+    for name in FILES:
+        src = re.sub(r"//[^\n]*", "", open(os.path.join(build.CSRC, name)).read())
+        for m in re.finditer(r"__global__[^;{]*?(\w+)\(const __grid_constant__", src):
+            at = src.index("{", src.index(")", m.end()))
+            depth, end = 0, at
+            for end in range(at, len(src)):
+                depth += {"{": 1, "}": -1}.get(src[end], 0)
+                if depth == 0:
+                    break
+            yield name, m.group(1), src[at:end]
+
+
+def test_the_kernels_are_found():
+    assert sorted(k for _, k, _ in kernels()) == ["kv8_append_kernel", "kv8_attention_kernel", "kv8_join_kernel",
+                                                  "kv8_tc_kernel", "page_plan_kernel"]
+
+
+@pytest.mark.parametrize("name,kernel,body", [pytest.param(*k, id=k[1]) for k in kernels()])
+def test_nothing_is_read_ahead_of_the_wait(name, kernel, body):
+    before, wait, after = body.partition("pdl_wait();")
+    assert wait, f"{kernel} ({name}) has no wait"
+    assert not READS.search(before), f"{kernel} ({name}) reads ahead of its wait: {READS.search(before).group(0)}"
+    assert READS.search(after)
