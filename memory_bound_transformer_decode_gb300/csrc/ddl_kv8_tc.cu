@@ -50,6 +50,11 @@ constexpr uint32_t KBYTES = TOK * 128;
 // every third tile of 16 queries did.)
 constexpr float TP_SCALE = 32.f, T_LAG = 3.f;
 
+// How long a CTA that leaves waits for its copies and MMAs in flight.  They end
+// by themselves, and until then they write shared and tensor memory that the next
+// CTA may get; so the caller's limit, which may be short, does not hold here.
+constexpr uint64_t DRAIN_NS = 10000000000ull;
+
 struct TcAtt {
   AttArgs A;
   uint64_t wait_ns;
@@ -400,8 +405,8 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
     // copies in flight land before the CTA leaves (bounded)
     if (lane == 0)
       for (uint32_t j = tc > G::STAGES ? tc - G::STAGES : 0; j < tc; ++j) {
-        if (!mbar_wait_thread(fullk + 8 * (j % G::STAGES), (j / G::STAGES) & 1, P.wait_ns)) break;
-        if (!mbar_wait_thread(fullv + 8 * (j % G::STAGES), (j / G::STAGES) & 1, P.wait_ns)) break;
+        if (!mbar_wait_thread(fullk + 8 * (j % G::STAGES), (j / G::STAGES) & 1, DRAIN_NS)) break;
+        if (!mbar_wait_thread(fullv + 8 * (j % G::STAGES), (j / G::STAGES) & 1, DRAIN_NS)) break;
       }
   } else if (warp == MW) {  // ------------------------------------------ MMA issue
     constexpr uint32_t IDESC_S = (1u << 4) | ((uint32_t)(G::N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
@@ -457,7 +462,7 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
     // every MMA issued has completed before tensor memory is released
     if (elect_one()) umma_commit(smem_addr(&S.fin));
     __syncwarp();
-    mbar_wait_thread(smem_addr(&S.fin), 0, P.wait_ns);
+    mbar_wait_thread(smem_addr(&S.fin), 0, DRAIN_NS);
     __syncwarp();
   } else {  // ------------------------------------------------------------ softmax
     const int wg = warp >> 2, tok = tid & 127, x0 = wg * QW;  // queries x0 .. x0 + QW - 1 of the unit

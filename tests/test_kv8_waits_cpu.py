@@ -38,3 +38,12 @@ def test_nothing_is_read_ahead_of_the_wait(name, kernel, body):
     assert wait, f"{kernel} ({name}) has no wait"
     assert not READS.search(before), f"{kernel} ({name}) reads ahead of its wait: {READS.search(before).group(0)}"
     assert READS.search(after)
+
+
+def test_a_leaving_cta_waits_for_its_copies_whatever_the_limit():
+    """ddl_set_wait_limit_ns may be a nanosecond: what is in flight (tensor copies, MMAs) is waited for by a limit
+    of its own before the CTA's shared and tensor memory goes to another."""
+    src = open(os.path.join(build.CSRC, "ddl_kv8_tc.cu")).read()
+    limits = re.findall(r"mbar_wait_thread\(.*, (?:[^,]*& 1|0), ([\w.]+)\)", src)
+    assert limits == ["DRAIN_NS"] * 3
+    assert int(re.search(r"DRAIN_NS = (\d+)ull", src).group(1)) >= 2 * 10 ** 9
