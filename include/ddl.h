@@ -396,7 +396,8 @@ int ddl_kv8_append(const ddl_kv8* kv, int32_t H_kv, int32_t head_dim, ddl_dtype 
  *    outside [0, T)) is computed on what lies within them, and a page id
  *    outside the pool counts as a block without keys; either sets bit 0 of
  *    *bad_out (device int32, may be NULL, never cleared by the call).  Bit 1:
- *    a bounded device wait gave up (ddl_set_wait_limit_ns), the output is void.
+ *    a bounded device wait gave up (ddl_set_wait_limit_ns); out and lse of the
+ *    requests it concerned are NaN, whether bad_out is given or not.
  *  - scale: finite; softcap >= 0, window >= 0 (0: none); slopes: device fp32
  *    [H_q] or NULL.
  *  - workspace: device, >= ddl_kv8_attention_workspace_bytes(...) of the same

@@ -470,8 +470,9 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
     bool ok = true;
     Segs s = first;
     const uint32_t tlane = (uint32_t)(32 * (warp & 3)) << 16, tSq = tm + tlane + 2 * x0, tOq = tO + tlane + 2 * x0;
-    // A wait that gives up makes its warp go on without waiting; the warps
-    // leave together at the segment's end (so none is left at a barrier).
+    // A wait that gives up makes its warp go on without waiting, so that none is
+    // left at a barrier; the results of that segment and of the CTA's later ones
+    // become NaN, also in the records that the join adds up.
     while (s.next(A, pre)) {
       const int nqueries = s.rq.n * A.GH, q0 = s.qc * NQ;
       const int nblk = s.c1 - s.c0, nt = (nblk + TBLK - 1) / TBLK;
@@ -737,11 +738,12 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
       if (lane < QW) S.wred[warp & 3][x0 + lane] = ls[0];
       if (nt > 0) ok = ok && wait(pvdone, (tc - 1) & 1);
       tc_fence_after();
-      if (ssync_or(3, NS, !ok)) break;
+      ok = !ssync_or(3, NS, !ok);
       if (tok < QW) {  // thread q: the query's place, factor and statistics
         const int x = x0 + tok, qi = q0 + x;
-        const float lq = (S.wred[0][x] + S.wred[1][x]) + (S.wred[2][x] + S.wred[3][x]), m = S.m[x];
-        float f = 1.f / TP_SCALE;
+        const float valid = ok ? 1.f : __uint_as_float(0x7fffffffu);
+        const float lq = ((S.wred[0][x] + S.wred[1][x]) + (S.wred[2][x] + S.wred[3][x])) * valid, m = S.m[x];
+        float f = 1.f / TP_SCALE * valid;
         int64_t place = -1;
         if (qi < nqueries) {
           const int row = group_row(A, qi), head = s.h * A.GH + qi - row * A.GH;

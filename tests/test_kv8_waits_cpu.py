@@ -47,3 +47,15 @@ def test_a_leaving_cta_waits_for_its_copies_whatever_the_limit():
     limits = re.findall(r"mbar_wait_thread\(.*, (?:[^,]*& 1|0), ([\w.]+)\)", src)
     assert limits == ["DRAIN_NS"] * 3
     assert int(re.search(r"DRAIN_NS = (\d+)ull", src).group(1)) >= 2 * 10 ** 9
+
+
+def test_a_wait_that_gives_up_makes_the_results_nan():
+    """Without bad_out nothing else tells the caller: the softmax warps that gave up still reach the segment's end,
+    and sum and factor of its queries (output, record, and the record in a cluster) are NaN there."""
+    src = open(os.path.join(build.CSRC, "ddl_kv8_tc.cu")).read()
+    end = src[src.index("// the result: thread = head dimension"):src.index("template <int DT, int EX>\nconst void* tc_fn")]
+    assert "break;" not in end
+    assert "ok = !ssync_or(3, NS, !ok);" in end
+    nan = re.search(r"const float (\w+) = ok \? 1\.f : __uint_as_float\(0x7fffffffu\);", end).group(1)
+    assert re.search(rf"lq = \(.*\) \* {nan}, m", end) and re.search(rf"float f = .* \* {nan};", end)
+    assert "S.al[x] = f;" in end and "S.ml[x] = make_float2(m, lq);" in end and "make_float2(m, lq);" in end
