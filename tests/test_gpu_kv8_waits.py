@@ -19,11 +19,11 @@ def test_replayed_shares_follow_the_lengths():
     """plan and attention in one graph, its blocks cut into shares and joined: every replay with other lengths has the
     bits of the call alone."""
     page, per = 64, 160
-    pool, q, _, _, _ = setup(1, [1], 16, 2, 128, page, [per * page], "e4m3", "bf16", seed=7)
+    pool, q, _, _, ids = setup(1, [1], 16, 2, 128, page, [per * page], "e4m3", "bf16", seed=7)
     i32 = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
     old, add = i32(1), dev([1])
-    table = torch.arange(per, dtype=torch.int32, device="cuda").view(1, per)
-    free = torch.arange(per, dtype=torch.int32, device="cuda")
+    table = dev(ids[:, :per])  # (the pool's other pages hold NaN codes)
+    free = table[0].clone()
     p = dict(row_off=i32(2), kv_len=i32(1), row_pos=i32(1), slot=i32(1), used=i32(1), status=i32(1))
     bound = 60000
     ws = torch.empty(ddl.ddl_kv8_attention_workspace_bytes(16, 2, 128, 1, 1, 1, bound), dtype=torch.uint8, device="cuda")
