@@ -715,7 +715,7 @@ int att_plan(bool tc, bool f32, int32_t H_q, int32_t H_kv, int32_t hd, int32_t R
   int64_t keys = max_len;
   if (window > 0 && (int64_t)window + max_rows + 15 < keys) keys = (int64_t)window + max_rows + 15;
   const int64_t blocks = (keys + 15) / 16, units = (int64_t)R * H_kv * p.nqc;
-  const int64_t slots = tc && f32 && p.nq == 4 ? sms : 2 * sms;  // CTAs that run at once (their shared memory)
+  int64_t slots = (tc ? kv8_tc_ctas(p.nq, f32, 0) : 2) * sms;  // CTAs that run at once (their shared memory)
   p.rec_ml = p.prefix = 0;
   p.total = 256;
   p.deep = 0;
@@ -760,6 +760,7 @@ int att_plan(bool tc, bool f32, int32_t H_q, int32_t H_kv, int32_t hd, int32_t R
     }
   }
   // (shares: ragged lengths up to the bound come to about 5/8 of it)
+  if (tc) slots = kv8_tc_ctas(p.nq, f32, R) * sms;
   const int64_t least = tc ? 8 : 16;
   int64_t share = (units * blocks * (R > 1 ? 5 : 8) / 8 + slots - 1) / slots;
   share = share < least ? least : share;

@@ -325,5 +325,7 @@ inline cudaError_t launch_pdl_cluster(const void* fn, dim3 grid, dim3 block, voi
 
 // The tcgen05 kernel (e4m3, head_dim 128): rows of the pool's view < 2^31.
 int kv8_tc_launch(const AttArgs& a, int dtype, int64_t rows, void* stream);
+// Its CTAs an SM, by their shared memory; `reqs` requests' weights beside it (shares), 0: none.
+int kv8_tc_ctas(int nq, bool f32, int reqs);
 
 }  // namespace ddl

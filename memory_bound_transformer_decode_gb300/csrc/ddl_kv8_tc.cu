@@ -23,7 +23,10 @@
 //    largest weight) in four e5m2 limbs of 3 bits, exactly.  (As e4m3, whose
 //    conversions both ways the limbs then need: 64 rows on 8192 tokens 64.6 us,
 //    so 63.4, and 61.6 with two scores an instruction.)
-//  - P of fp32 rows: e4m3 as Q (2^-24; 2^-27 of the largest weight).
+//  - P of fp32 rows: an fp16 in the e5m2 limbs of group A, L = 4 of them, and what
+//    it leaves, times 2^12 and again in fp16, in those of group B: 2^-22 of a weight,
+//    2^-39 of the largest.  (Six e4m3 limbs ended at 2^-27 of the largest: the
+//    weights of a long tail that lie below it were in the sum but not in O.)
 //
 // A segment's tiles are taken from the newest token to the oldest: a distance
 // bias then raises the running maximum once and not with every tile (4 rows of
@@ -44,11 +47,14 @@ namespace {
 constexpr int TOK = 128, TBLK = TOK / KV8_BLOCK;  // tokens and blocks of a tile
 constexpr uint32_t KBYTES = TOK * 128;
 
-// P carries 2^5; with the running maximum lagging by less than 2^3 it stays
-// within 2^8 <= 448.  (Raising it stops the softmax warps three times for the
+// P carries 2^5 (fp32 rows 2^11, within e5m2's 2^15); with the running maximum
+// lagging by less than 2^3 what the limbs of 16-bit rows leave, times 2^8, stays
+// within fp16.  (Raising it stops the softmax warps three times for the
 // exchange of the maxima and rescales O in tensor memory: with a lag of 2^1
 // every third tile of 16 queries did.)
-constexpr float TP_SCALE = 32.f, T_LAG = 3.f;
+constexpr float T_LAG = 3.f;
+template <int L>  // (Q's passes: 2 or, for fp32 rows, 3)
+constexpr float TP_SCALE = L == 2 ? 32.f : 2048.f;
 
 // How long a CTA that leaves waits for its copies and MMAs in flight.  They end
 // by themselves, and until then they write shared and tensor memory that the next
@@ -70,8 +76,9 @@ struct Geo {
   static constexpr int WG = NQ / QW;            // softmax warpgroups
   static constexpr int THREADS = 128 * WG + 64;
   static constexpr int N = 16 * NT;             // B columns
+  static constexpr int LP = L == 2 ? 2 : 4;     // passes of P (L: of Q)
   static constexpr uint32_t OPB = NT * 2048u;   // bytes of one pass's Q or P operand
-  static constexpr uint32_t Q_OFF = STAGES * 2 * KBYTES, P_OFF = Q_OFF + L * OPB, SH_OFF = P_OFF + L * OPB;
+  static constexpr uint32_t Q_OFF = STAGES * 2 * KBYTES, P_OFF = Q_OFF + L * OPB, SH_OFF = P_OFF + LP * OPB;
   static constexpr uint32_t COLS = NT == 1 ? 64 : NT == 2 ? 128 : 256;  // S twice, O: 48 NT columns
 };
 
@@ -203,8 +210,8 @@ __device__ __forceinline__ uint2 limb8(float (&v)[8], bool rest) {
 }
 
 // fp16 values (pairs) as e5m2 limbs.  e5m2 is the top byte of fp16, so that a
-// limb is a byte permute and what it leaves one exact subtraction: positive
-// values, each limb the next 3 significant bits, cut off.
+// limb is a byte permute and what it leaves one exact subtraction: each limb the
+// next 3 significant bits, cut off.
 __device__ __forceinline__ uint32_t h2_bits(__half2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
 __device__ __forceinline__ __half2 h2_of(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
 __device__ __forceinline__ uint2 limb8h(const uint32_t (&h)[4]) {
@@ -264,9 +271,9 @@ struct Segs {
 template <int DT, int EX, int NT>
 __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) kv8_tc_kernel(const __grid_constant__ TcAtt P) {
   constexpr int L = DT == DDL_T_F32 ? 3 : 2;
-  constexpr float BSCALE = DT == DDL_T_F32 ? 4096.f : 256.f;  // 16^L
+  constexpr float BSCALE = DT == DDL_T_F32 ? 4096.f : 256.f;  // 16^L (of Q and of P)
   using G = Geo<NT, L>;
-  constexpr int NQ = G::NQ, QW = G::QW, WG = G::WG, NS = 128 * WG;  // NS: softmax threads
+  constexpr int NQ = G::NQ, QW = G::QW, WG = G::WG, NS = 128 * WG, LP = G::LP;  // NS: softmax threads
   constexpr int CW = 4 * WG, MW = 4 * WG + 1;                         // the copying and the MMA warp
   extern __shared__ __align__(1024) uint8_t smem[];
   Shared<NT, L>& S = *reinterpret_cast<Shared<NT, L>*>(smem + G::SH_OFF);
@@ -410,8 +417,8 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
       }
   } else if (warp == MW) {  // ------------------------------------------ MMA issue
     constexpr uint32_t IDESC_S = (1u << 4) | ((uint32_t)(G::N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-    // P e5m2 (16-bit rows) or e4m3; A and B M/N-major
-    constexpr uint32_t IDESC_O = IDESC_S | (L == 2 ? 1u << 10 : 0u) | (1u << 15) | (1u << 16);
+    // P e5m2; A and B M/N-major
+    constexpr uint32_t IDESC_O = IDESC_S | (1u << 10) | (1u << 15) | (1u << 16);
     const uint64_t kd = sdesc(sb, 16, 1024, 2), vd = sdesc(sb + KBYTES, 16384, 1024, 2);
     const uint64_t qd = sdesc(sb + G::Q_OFF, 16, 1024, 2), pd = sdesc(sb + G::P_OFF, 128, 2048, 0);
     uint32_t tc = 0, sg = 0;
@@ -448,7 +455,7 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
         if (elect_one()) {
           const uint64_t a = vd + (uint64_t)(st * (2 * KBYTES >> 4));
 #pragma unroll
-          for (int p = 0; p < L; ++p)
+          for (int p = 0; p < LP; ++p)
 #pragma unroll
             for (int k = 0; k < 4; ++k)  // 32 tokens each
               umma_f8(tO, a + k * (4096 >> 4), pd + (uint64_t)(p * (G::OPB >> 4)) + k * (512 >> 4), IDESC_O,
@@ -679,8 +686,8 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
         }
         // the tile's weights, and their limbs as the PV operand (whose place is
         // free once the previous tile's PV MMAs are done)
-        const F2 wv2(vs * vinv * TP_SCALE);
-        uint4 pk[QW / 8][L];
+        const F2 wv2(vs * vinv * TP_SCALE<L>);
+        uint4 pk[QW / 8][LP];
 #pragma unroll
         for (int j = 0; j < QW / 8; ++j) {
           float w[8];
@@ -690,11 +697,11 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
             l[4 * j + q / 2] = add2(l[4 * j + q / 2], p);
             mul2(p, wv2).get(w[q], w[q + 1]);
           }
-          uint2 a[L], b[L];
-          if (L == 2) {  // fp16 (2^-11), 11 bits, as four limbs: exactly
-            uint32_t h[4];
+          uint2 a[LP], b[LP];
+          uint32_t h[4];  // fp16 (2^-11), 11 bits, as four limbs: exactly
 #pragma unroll
-            for (int q = 0; q < 4; ++q) h[q] = pack_f16x2(w[2 * q], w[2 * q + 1]);
+          for (int q = 0; q < 4; ++q) h[q] = pack_f16x2(w[2 * q], w[2 * q + 1]);
+          if (L == 2) {
             a[0] = limb8h(h);
             drop_limb(h);
             a[1] = limb8h(h);
@@ -706,24 +713,35 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
             b[1] = limb8h(h);
           } else {
 #pragma unroll
-            for (int p = 0; p < 2 * L; ++p) {
-              const uint2 c = limb8(w, p + 1 < 2 * L);
-              if (p == L - 1) {
+            for (int q = 0; q < 4; ++q) {  // what the fp16 leaves
+              const float2 f = __half22float2(h2_of(h[q]));
+              w[2 * q] -= f.x;
+              w[2 * q + 1] -= f.y;
+            }
 #pragma unroll
-                for (int q = 0; q < 8; ++q) w[q] *= BSCALE;
-              }
-              if (p < L) a[p % L] = c;
-              else b[p % L] = c;
+            for (int p = 0; p < LP; ++p) {
+              a[p] = limb8h(h);
+              drop_limb(h);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {  // (and its last limb below e5m2's smallest step)
+              const float2 f = __half22float2(h2_of(h[q]));
+              h[q] = pack_f16x2((w[2 * q] + f.x) * BSCALE, (w[2 * q + 1] + f.y) * BSCALE);
+            }
+#pragma unroll
+            for (int p = 0; p < LP; ++p) {
+              b[p] = limb8h(h);
+              if (p + 1 < LP) drop_limb(h);
             }
           }
 #pragma unroll
-          for (int p = 0; p < L; ++p) pk[j][p] = make_uint4(a[p].x, a[p].y, b[p].x, b[p].y);
+          for (int p = 0; p < LP; ++p) pk[j][p] = make_uint4(a[p].x, a[p].y, b[p].x, b[p].y);
         }
         if (!waited) ok = ok && wait(pvdone, (tc - 1) & 1);
 #pragma unroll
         for (int j = 0; j < QW / 8; ++j)
 #pragma unroll
-          for (int p = 0; p < L; ++p)
+          for (int p = 0; p < LP; ++p)
             *reinterpret_cast<uint4*>(smem + G::P_OFF + p * G::OPB + (x0 / 8 + j) * 2048 + tok * 16) = pk[j][p];
         fence_proxy_async_smem();
         tc_fence_before();
@@ -743,7 +761,7 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
         const int x = x0 + tok, qi = q0 + x;
         const float valid = ok ? 1.f : __uint_as_float(0x7fffffffu);
         const float lq = ((S.wred[0][x] + S.wred[1][x]) + (S.wred[2][x] + S.wred[3][x])) * valid, m = S.m[x];
-        float f = 1.f / TP_SCALE * valid;
+        float f = 1.f / TP_SCALE<L> * valid;
         int64_t place = -1;
         if (qi < nqueries) {
           const int row = group_row(A, qi), head = s.h * A.GH + qi - row * A.GH;
@@ -815,6 +833,11 @@ size_t tc_smem(bool f32) {
   return f32 ? Geo<NT, 3>::SH_OFF + sizeof(Shared<NT, 3>) : Geo<NT, 2>::SH_OFF + sizeof(Shared<NT, 2>);
 }
 
+size_t tc_smem(int nq, bool f32, int reqs) {
+  return (nq == 1 ? tc_smem<1>(f32) : nq == 2 ? tc_smem<2>(f32) : tc_smem<4>(f32)) + 16 +
+         (reqs ? (size_t)(reqs + 1) * 8 : 0);
+}
+
 int encode_map(CUtensorMap* m, const uint8_t* base, int64_t rows) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) return DDL_ERR_CUDA;
@@ -830,6 +853,10 @@ int encode_map(CUtensorMap* m, const uint8_t* base, int64_t rows) {
 
 }  // namespace
 
+int kv8_tc_ctas(int nq, bool f32, int reqs) {
+  return 2 * (tc_smem(nq, f32, reqs) + 1024) <= 228 * 1024 ? 2 : 1;
+}
+
 // rows: of the pool's [pages * H_kv * page_size][128] view, < 2^31.
 int kv8_tc_launch(const AttArgs& a, int dtype, int64_t rows, void* stream) {
   TcAtt p;
@@ -844,8 +871,7 @@ int kv8_tc_launch(const AttArgs& a, int dtype, int64_t rows, void* stream) {
                    : dtype == DDL_T_BF16 ? tc_fn<DDL_T_BF16>(ex, a.nq)
                                          : tc_fn<DDL_T_F16>(ex, a.nq);
   const bool f32 = dtype == DDL_T_F32;
-  const size_t smem = (a.nq == 1 ? tc_smem<1>(f32) : a.nq == 2 ? tc_smem<2>(f32) : tc_smem<4>(f32)) + 16 +
-                      (a.cluster ? 0 : (size_t)(a.R + 1) * 8);
+  const size_t smem = tc_smem(a.nq, f32, a.cluster ? 0 : a.R);
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
   if (e != cudaSuccess) return cuda_status(e);
   if (a.cluster > 8 && (e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
