@@ -384,7 +384,9 @@ int ddl_kv8_append(const ddl_kv8* kv, int32_t H_kv, int32_t head_dim, ddl_dtype 
  * A row without keys gives zeros and lse = -inf.  Rows of q that belong to no
  * request are neither read nor written.  A NaN code among the keys a row sees
  * gives NaN in its output, and so does a scale of one of their blocks that is not
- * finite (V: or negative); whatever lies in slots it does not see has no effect.
+ * finite (V: or negative); whatever lies in slots it does not see has no effect
+ * (V scales that the rows of one request see may be up to 2^90 apart; below
+ * that a row's smaller ones lose bits).
  *  - H_q % H_kv == 0, H_q / H_kv <= 8, head_dim 64 or 128 (DDL_ERR_SHAPE).
  *  - q, out: device [T][H_q][head_dim] of `dtype`, heads contiguous, rows
  *    q_stride / out_stride elements apart (>= H_q * head_dim, a multiple of 8),

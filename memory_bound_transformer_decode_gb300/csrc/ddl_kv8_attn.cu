@@ -23,9 +23,10 @@
 // memory latency per block.)  e4m3 and int8 codes are exact in fp16.  Q is scaled by a
 // power of two per query and split into fp16 high part and (fp32 rows only)
 // remainder: bf16 and fp16 values fit the high part (down to 2^-26 of the
-// row's largest).  P (with V's scale, relative to the largest seen by the warp)
-// is likewise one fp16 (16-bit outputs: its 2^-12 is below their own rounding)
-// or two.  Scores, m, l and O are fp32.
+// row's largest).  P (with V's scale, relative to the query's largest such
+// product: ddl_kv8_attn.h) is likewise one fp16 (16-bit outputs: its 2^-11 is no
+// more than their own rounding) or two (2^-22; 2^-36 of the largest product).
+// Scores, their reference, l and O are fp32.
 //
 // Work.  A *unit* is the blocks of one request for one K/V head and up to 8
 // tiles of 8 queries; a CTA of 8 warps gives each tile 8 / tiles warps, which
@@ -49,9 +50,9 @@ namespace ddl {
 namespace {
 
 constexpr int ATT_WARPS = 8;
-// P's fp16 values carry 2^11: with the running maximum allowed to lag by
+// P's fp16 values carry 2^11: with the reference allowed to lag by
 // 2^M_LAG they stay below 2^16, and what rounds off below fp16's smallest
-// subnormal is 2^-36 of the largest weight.
+// subnormal is 2^-36 of the largest product.
 constexpr float P_SCALE = 2048.f;
 constexpr float M_LAG = 4.f;
 
@@ -155,13 +156,21 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
     }
     return -1;
   };
+  auto block_scales = [&](int i, int32_t blk, float& ks, float& vs) {
+    ks = vs = 0.f;
+    if (blk < 0) return;
+    ks = A.ks[blk];
+    vs = A.vs[blk];
+    check_scales(ks, vs);
+    // V scales of blocks that no query of the tile sees do not count
+    const int key = (c0 + kg + i * groups) * 16, last = min(tile * 8 + 7, nqueries - 1);
+    if (key > rq.p0 + group_row(A, last) ||
+        (A.window > 0 && key + 15 < rq.p0 + group_row(A, tile * 8) - A.window + 1))
+      vs = 0.f;
+  };
   int32_t blk_l = block_row(lane), blk_n = -1;
-  float ks_l = 0.f, vs_l = 0.f, ks_n = 0.f, vs_n = 0.f;
-  if (blk_l >= 0) {
-    ks_l = A.ks[blk_l];
-    vs_l = A.vs[blk_l];
-    check_scales(ks_l, vs_l);
-  }
+  float ks_l, vs_l, ks_n = 0.f, vs_n = 0.f;
+  block_scales(lane, blk_l, ks_l, vs_l);
   // block i on its way into the ring; its place is lane i % 32's of this batch of 32 or the next
   const uint32_t ring = smem_addr(&S.w[warp].ring[0][0]) + lane * 16;
   const bool shared_codes = A.nq > 1;  // (4 requests of up to 16 rows, 4096 int8 tokens: 65 us through L1, 70 past it)
@@ -256,24 +265,17 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
   float o[MT][4];
 #pragma unroll
   for (int m = 0; m < MT; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
-  float mrun[2] = {-INFINITY, -INFINITY}, lrun[2] = {0.f, 0.f};
-  float vref = 0.f, vinv = 0.f;  // the largest V scale so far (and VREF_MIN) and its inverse: P carries scale / vref
+  float mrun[2] = {-INFINITY, -INFINITY}, lrun[2] = {0.f, 0.f};  // reference R, sum
+  float vref = 0.f, vinv = 0.f;  // unit of O and its inverse
 
 #pragma unroll 1
   for (int i = 0; i < nb; ++i) {
     const int l = i & 31;
     if (l == 4) blk_n = block_row((i & ~31) + 32 + lane);  // the next batch, long before it is used
-    if (l == 16) {
-      ks_n = vs_n = 0.f;
-      if (blk_n >= 0) {
-        ks_n = A.ks[blk_n];
-        vs_n = A.vs[blk_n];
-        check_scales(ks_n, vs_n);
-      }
-    }
+    if (l == 16) block_scales((i & ~31) + 32 + lane, blk_n, ks_n, vs_n);
     const bool none = __shfl_sync(FULL, blk_l, l) < 0;
-    const float ks = __shfl_sync(FULL, ks_l, l), vs = __shfl_sync(FULL, vs_l, l);
     const int key0 = (c0 + kg + i * groups) * 16;
+    const float ks = __shfl_sync(FULL, ks_l, l), vs = __shfl_sync(FULL, vs_l, l);
 
     cp_async_wait<STAGES - 1>();
     const uint32_t src = ring + slot_out;
@@ -354,17 +356,41 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
         else if ((nan >> off) & 1u) c[j] = __uint_as_float(0x7fffffffu);
       }
     }
-    // running maximum: raised only when some score passes it by M_LAG
+    if (vs >= 2.f * vref && vs > 0.f) {  // O moves to the unit of this block's scale, and with it the reference
+      const float nref = pow2_floor(vs);
+      if (vref > 0.f) {
+        const float down = pow2_log_ratio(nref, vref), f = vref * pow2_inv(nref);
+        float a[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float top = lrun[q];  // (a weight is at most its lane's sum)
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, x));
+          const float nr = mrun[q] + fmaxf(-down, __log2f(top) - P_SPAN);
+          a[q] = mrun[q] == -INFINITY ? 1.f : exp2_fast(mrun[q] - nr);
+          mrun[q] = nr;
+          lrun[q] *= a[q];
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) o[m][x] *= a[x & 1] * f;
+      }
+      vref = nref;
+      vinv = pow2_inv(nref);
+    }
+    // the reference: raised only when some product passes it by M_LAG (or a weight by P_TOP)
+    const float vn = vs * vinv, lv = scale_log(vn), thr = fminf(M_LAG - lv, P_TOP);
     const float t0 = fmaxf(c[0], c[2]), t1 = fmaxf(c[1], c[3]);
-    if (__any_sync(FULL, t0 > mrun[0] + M_LAG || t1 > mrun[1] + M_LAG)) {
+    if (__any_sync(FULL, t0 > mrun[0] + thr || t1 > mrun[1] + thr)) {
       float n0 = t0, n1 = t1;
 #pragma unroll
       for (int x = 4; x < 32; x <<= 1) {
         n0 = fmaxf(n0, __shfl_xor_sync(FULL, n0, x));
         n1 = fmaxf(n1, __shfl_xor_sync(FULL, n1, x));
       }
-      n0 = fmaxf(n0, mrun[0]);
-      n1 = fmaxf(n1, mrun[1]);
+      n0 = fmaxf(mrun[0], n0 + lv);
+      n1 = fmaxf(mrun[1], n1 + lv);
       const float a0 = mrun[0] == -INFINITY ? 0.f : exp2_fast(mrun[0] - n0);
       const float a1 = mrun[1] == -INFINITY ? 0.f : exp2_fast(mrun[1] - n1);
       mrun[0] = n0;
@@ -379,16 +405,7 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
         o[m][3] *= a1;
       }
     }
-    if (vs > vref) {  // O is in units of vref
-      const float nref = fmaxf(vs, VREF_MIN), f = __fdiv_rn(vref, nref);
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) o[m][x] *= f;
-      vref = nref;
-      vinv = __frcp_rn(nref);
-    }
-    const float wv = vs * vinv * P_SCALE;
+    const float wv = vn * P_SCALE;
     const float m0 = mrun[0] == -INFINITY ? 0.f : mrun[0], m1 = mrun[1] == -INFINITY ? 0.f : mrun[1];
     const float p0 = exp2_fast(c[0] - m0), p1 = exp2_fast(c[1] - m1), p2 = exp2_fast(c[2] - m0), p3 = exp2_fast(c[3] - m1);
     lrun[0] += p0 + p2;

@@ -111,8 +111,35 @@ __device__ __forceinline__ void check_scales(float& ks, float& vs) {
   vs = 0.f;
   ks = __uint_as_float(0x7fffffffu);
 }
-// O is kept in units of the largest V scale met, at least this: its inverse is finite.
-constexpr float VREF_MIN = 0x1p-126f;
+// The weights' reference.  A key contributes p_j vs_j code_j, p_j = e^{s_j - ..}.
+// What a weight loses when it is rounded to the MMA's type is measured by the
+// largest product p_j vs_j of the *query*, so that neither a block that other
+// queries of the tile see nor a seen one of small weight costs it bits:
+//  - O and the products are in units of vref, the power of two at or below the
+//    largest V scale met in a block that some query sees (a unit only);
+//  - per query the running reference is R = max_j (s_j + log2(vs_j / vref)) over
+//    the keys it sees (base 2), p_j = 2^(s_j - R): the largest product is about 1,
+//    and p_j itself above 1 where its block's scale lies below vref;
+//  - p_j stays below 2^P_TOP and the logarithm is taken as -P_SPAN at least, so
+//    that the sum of p_j is finite: blocks whose scale is down to 2^-P_SPAN of vref
+//    keep all bits, smaller ones lose them gradually.
+constexpr float P_SPAN = 90.f, P_TOP = 95.f;
+constexpr float VREF_MIN = 0x1p-126f;          // (its inverse is finite)
+// Power of two at or below a scale, at least VREF_MIN.
+__device__ __forceinline__ float pow2_floor(float vs) {
+  const uint32_t e = __float_as_uint(vs) & 0x7f800000u;
+  return e < 0x00800000u ? VREF_MIN : __uint_as_float(e);
+}
+// 1 / x of a power of two in [2^-126, 2^127], log2 of the quotient of two.
+__device__ __forceinline__ float pow2_inv(float x) {
+  const uint32_t e = __float_as_uint(x);
+  return e == 0x7f000000u ? 0x1p-127f : __uint_as_float(0x7f000000u - e);
+}
+__device__ __forceinline__ float pow2_log_ratio(float a, float b) {
+  return (float)((int)(__float_as_uint(a) >> 23) - (int)(__float_as_uint(b) >> 23));
+}
+// log2 of a block's scale over vref.
+__device__ __forceinline__ float scale_log(float vs_over_ref) { return fmaxf(__log2f(vs_over_ref), -P_SPAN); }
 
 // Byte mask of the e4m3 NaN codes (low 7 bits all set) of four codes.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {

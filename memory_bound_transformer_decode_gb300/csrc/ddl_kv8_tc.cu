@@ -19,8 +19,8 @@
 //  - Q: e4m3, each limb the rounding of what the ones before leave, 4
 //    significant bits; L = 2 for 16-bit rows (2^-16 of a value, 2^-26 of the
 //    row's largest), 3 for fp32 rows (2^-24).
-//  - P of 16-bit rows: fp16 (2^-11, below the output's own rounding; 2^-30 of the
-//    largest weight) in four e5m2 limbs of 3 bits, exactly.  (As e4m3, whose
+//  - P of 16-bit rows: fp16 (2^-11, no more than the output's own rounding; 2^-30 of
+//    the query's largest product of weight and V scale) in four e5m2 limbs of 3 bits, exactly.  (As e4m3, whose
 //    conversions both ways the limbs then need: 64 rows on 8192 tokens 64.6 us,
 //    so 63.4, and 61.6 with two scores an instruction.)
 //  - P of fp32 rows: an fp16 in the e5m2 limbs of group A, L = 4 of them, and what
@@ -47,7 +47,7 @@ namespace {
 constexpr int TOK = 128, TBLK = TOK / KV8_BLOCK;  // tokens and blocks of a tile
 constexpr uint32_t KBYTES = TOK * 128;
 
-// P carries 2^5 (fp32 rows 2^11, within e5m2's 2^15); with the running maximum
+// P carries 2^5 (fp32 rows 2^11, within e5m2's 2^15); with the reference
 // lagging by less than 2^3 what the limbs of 16-bit rows leave, times 2^8, stays
 // within fp16.  (Raising it stops the softmax warps three times for the
 // exchange of the maxima and rescales O in tensor memory: with a lag of 2^1
@@ -91,13 +91,14 @@ struct Meta {  // of a stage's tile
 template <int NT, int L>
 struct Shared {
   Meta meta[Geo<NT, L>::STAGES];
-  alignas(16) float cf[8 * NT], nslope[8 * NT], hif[8 * NT], m[8 * NT], al[8 * NT];  // nslope: negated
+  alignas(16) float cf[8 * NT], nslope[8 * NT], hif[8 * NT], m[8 * NT], al[8 * NT];  // nslope: negated; m: reference R
   alignas(16) float nref[8 * NT], shift[8 * NT];  // -m, 0 for -inf; what a raise moves scores by
+  float over[8 * NT];  // a bound on (largest score - m)
   uint32_t fresh[2];  // per warpgroup: some query that may still meet a key has met none
   int32_t hi[8 * NT], lo[8 * NT];
   int64_t place[8 * NT];
   float2 ml[8 * NT];
-  float wred[4][8 * NT];
+  float wred[4][8 * NT], wtop[4 * NT];
   uint32_t nan[2][4];
   uint64_t fullk[3], fullv[3], empty[3], sfull[2], pfull, pvdone, qfull, fin;
   int64_t wsum[12];
@@ -362,6 +363,10 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
         if (A.bad) atomicOr(A.bad, 1);
         return -1;
       };
+      // tokens that some query of the unit sees: V scales of blocks without any do not count
+      const int qa = s.qc * NQ, qb = (s.rq.n * A.GH < qa + NQ ? s.rq.n * A.GH : qa + NQ) - 1;
+      const int last_key = s.rq.p0 + group_row(A, qb);
+      const int first_key = A.window > 0 ? s.rq.p0 + group_row(A, qa) - A.window + 1 : 0;
       int32_t page = page_of(lane), page_n = -1;
       for (int g0 = 0; ok && g0 < nblk; g0 += 32) {  // lane l: block g0 + l
         const int sub = (s.c1 - 1 - g0 - lane) & bmask;
@@ -371,6 +376,8 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
           ks = A.ks[(head << bshift) + sub];
           vs = A.vs[(head << bshift) + sub];
           check_scales(ks, vs);
+          const int key = (s.c1 - 1 - g0 - lane) * 16;
+          if (key > last_key || key + 15 < first_key) vs = 0.f;
         }
         const int32_t row = page >= 0 ? (int32_t)((head << A.pshift) + (sub << 4)) : P.rows;  // (none: zeros)
         page_n = page_of(g0 + 32 + lane);
@@ -545,6 +552,7 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
           S.lo[x] = A.window > 0 ? p - A.window + 1 : 0;
           S.m[x] = -INFINITY;
           S.nref[x] = 0.f;
+          S.over[x] = -INFINITY;
         }
       }
       fence_proxy_async_smem();
@@ -557,7 +565,8 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
       F2 l[QW / 2];
 #pragma unroll
       for (int q = 0; q < QW / 2; ++q) l[q] = F2(0.f);
-      float vref = 0.f, vinv = 0.f;  // the largest V scale so far (and VREF_MIN) and its inverse
+      float vref = 0.f, vinv = 0.f;  // unit of O and its inverse
+      float tops = -INFINITY;        // largest score less its reference since that was last raised
       for (int i = 0; i < nt; ++i, ++tc) {
         const uint32_t st = tc % G::STAGES;
         ok = ok && wait(fullk + 8 * st, (tc / G::STAGES) & 1);  // (the tile's scales)
@@ -631,24 +640,39 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
 #pragma unroll
           for (int q = 0; q < QW; ++q) sc[q] = -INFINITY;
         }
-        bool over = vmax > vref || i == 0 || S.fresh[wg];
+        const bool unit_up = vmax > 0.f && vmax >= 2.f * vref;
+        float lv = scale_log(vs * vinv);
+        bool over = unit_up || i == 0 || S.fresh[wg];
         float top = sc[0];
 #pragma unroll
         for (int q = 1; q < QW; ++q) top = fmaxf(top, sc[q]);
-        over = over || top > T_LAG;
+        over = over || top > fminf(T_LAG - lv, P_TOP);
         bool waited = tc == 0;
-        if (ssync_or(1 + wg, 128, over)) {  // raise the running maximum (and V's reference): O and l in the new units
+        if (ssync_or(1 + wg, 128, over)) {  // raise the reference (and V's unit): O and l in the new units
+          const float nref = unit_up ? pow2_floor(vmax) : vref, fv = unit_up ? vref * pow2_inv(nref) : 1.f;
+          const float down = unit_up && vref > 0.f ? pow2_log_ratio(nref, vref) : 0.f;
+          if (unit_up) {
+            vref = nref;
+            vinv = pow2_inv(nref);
+            lv = scale_log(vs * vinv);
+          }
 #pragma unroll
           for (int q = 0; q < QW; ++q) {
-            const float x = warp_fmax(sc[q]);
+            const float x = warp_fmax(sc[q] + lv);
             if (lane == 0) S.wred[warp & 3][x0 + q] = x;
           }
+          tops = warp_fmax(tops);
+          if (lane == 0) S.wtop[warp] = tops;
           ssync(1 + wg, 128);
           if (tok < QW) {
             const int x = x0 + tok;
             const float old = S.m[x], ref = -S.nref[x];
             const float up = fmaxf(fmaxf(S.wred[0][x], S.wred[1][x]), fmaxf(S.wred[2][x], S.wred[3][x]));
-            const float nm = fmaxf(old, ref + up), now = nm == -INFINITY ? 0.f : nm;
+            const float* const wt = &S.wtop[4 * wg];
+            const float most = fmaxf(S.over[x], fmaxf(fmaxf(wt[0], wt[1]), fmaxf(wt[2], wt[3])));
+            const float kept = old + fmaxf(-down, most - P_SPAN);  // (a new unit makes all products so far smaller)
+            const float nm = fmaxf(down > 0.f ? kept : old, ref + up), now = nm == -INFINITY ? 0.f : nm;
+            S.over[x] = old == -INFINITY ? -INFINITY : most + (old - nm);
             S.al[x] = old == -INFINITY ? 0.f : exp2_fast(old - nm);
             S.m[x] = nm;
             S.nref[x] = -now;
@@ -659,13 +683,13 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
           }
           if (!waited) ok = ok && wait(pvdone, (tc - 1) & 1);
           waited = true;
-          const float nref = fmaxf(fmaxf(vmax, vref), VREF_MIN), fv = __fdiv_rn(vref, nref);
-          vref = nref;
-          vinv = __frcp_rn(nref);
           ssync(1 + wg, 128);
+          top = -INFINITY;
+          tops = -INFINITY;
 #pragma unroll
           for (int q = 0; q < QW; ++q) {
             sc[q] += S.shift[x0 + q];
+            top = fmaxf(top, sc[q]);
           }
 #pragma unroll
           for (int q = 0; q < QW; q += 2) l[q / 2] = mul2(l[q / 2], F2(S.al[x0 + q], S.al[x0 + q + 1]));
@@ -684,6 +708,7 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
             tmem_st_wait();
           }
         }
+        tops = fmaxf(tops, top);
         // the tile's weights, and their limbs as the PV operand (whose place is
         // free once the previous tile's PV MMAs are done)
         const F2 wv2(vs * vinv * TP_SCALE<L>);
