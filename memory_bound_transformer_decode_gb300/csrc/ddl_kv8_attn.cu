@@ -314,7 +314,8 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
       const int col = j & 1;
       float s = (c[j] + c2[j]) * (ks * cf[col]);
       if (EX) {
-        if (A.softcap > 0.f) s = A.softcap * LOG2E * cap_tanh<DT>(s);
+        // (relative to the score at any cap, as 1 - 2 / (e^{2x} + 1) is not: a cap of 1e6 must not change a score of 3)
+        if (A.softcap > 0.f) s = A.softcap * LOG2E * tanhf(s);
         s -= slope[col] * (float)(hi[col] - (key0 + g + (j >> 1) * 8));
       }
       c[j] = s;
@@ -912,7 +913,7 @@ extern "C" int ddl_kv8_attention(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, i
   a.q_stride = q_stride;
   a.out_stride = out_stride;
   a.scale = opts->scale;
-  a.softcap = opts->softcap;
+  a.softcap = fminf(opts->softcap, 0x1p100f);  // (a score over more than that would be subnormal)
   a.window = window;
   a.R = R;
   a.T = T;

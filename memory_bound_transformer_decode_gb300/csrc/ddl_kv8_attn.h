@@ -241,14 +241,6 @@ __device__ __forceinline__ void store_elem(void* p, int64_t i, float v) {
   else reinterpret_cast<__half*>(p)[i] = __float2half_rn(v);
 }
 
-// tanh of a score over its cap.  For 16-bit rows from its definition 1 - 2 /
-// (e^{2x} + 1): an absolute error of a few 2^-24, times the cap some 2^-17 of
-// a weight.  fp32 rows, whose small scores that would cost bits, take tanhf.
-template <int DT>
-__device__ __forceinline__ float cap_tanh(float x) {
-  return DT == DDL_T_F32 ? tanhf(x) : 1.f - __fdividef(2.f, __expf(2.f * x) + 1.f);
-}
-
 // ------------------------------------------------------------------ clusters
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");

@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
               if (EX == 2) {
                 float a, b;
                 x.get(a, b);
-                x = mul2(F2(A.softcap * LOG2E), F2(cap_tanh<DT>(a), cap_tanh<DT>(b)));
+                x = mul2(F2(A.softcap * LOG2E), F2(tanhf(a), tanhf(b)));
               }
               x = fma2(F2(ns.x, ns.y), add2(F2(hf.x, hf.y), far2), x);  // (distances: exact to 2^24)
               x = add2(x, F2(nr.x, nr.y));

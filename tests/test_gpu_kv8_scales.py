@@ -106,3 +106,14 @@ def test_bound_by_hand():
     out, _, tol, _ = kv8_bounds.attention((k, v, torch.ones_like(vs), vs), q, [0, 2], [17], [[0, 1]], 1.0)
     assert torch.allclose(out[0], torch.ones_like(out[0])) and float(tol[0].max()) < 2.0 ** -7
     assert torch.allclose(out[1], torch.full_like(out[1], (16 + 2.0 ** 20) / 17))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("codes,hd,bound", KERNELS)
+@pytest.mark.parametrize("cap", [30.0, 1e3, 1e4, 1e6, 1e12, 3e38])
+def test_a_cap_far_above_the_scores_changes_nothing(dtype, codes, hd, bound, cap):
+    pool, q, off, lens, table = setup(2, [3, 1], 8, 2, hd, 16, [300, 900], codes, dtype, seed=27)
+    got, _ = check(pool, q, off, lens, table, max_len=bound, softcap=cap, scale=1.0 / hd)
+    if cap >= 1e6:
+        plain, want = check(pool, q, off, lens, table, max_len=bound, scale=1.0 / hd)
+        assert (got.double() - plain.double()).abs().max() <= 4 * torch.finfo(q.dtype).eps * want.abs().max()
