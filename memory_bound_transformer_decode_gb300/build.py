@@ -1,6 +1,7 @@
 """Builds the decode library (csrc/*.cu) for sm_103a into _build/libddl.so, and
 the module of its per-layer calls for torch tensors (csrc/ddl_torch.cpp) into
-_build/_ddl_torch.so, which links against it.
+_build/_ddl_torch.so, which links against it.  Without torch the library alone
+is built (``python build.py``), with nothing but nvcc.
 
 Plain nvcc and g++, one translation unit per file compiled in parallel, then the
 shared-library links; no CMake.  ``ddl.py`` loads the library with ctypes and
@@ -33,10 +34,13 @@ def _nvcc() -> str:
     return cand
 
 
-def _torch_dirs() -> tuple[list[str], str]:
-    """Include directories and the library directory of the installed torch."""
-    import torch
-
+def _torch_dirs() -> tuple[list[str], str] | None:
+    """Include directories and the library directory of the installed torch;
+    None where there is none: the C library is built all the same."""
+    try:
+        import torch
+    except ImportError:
+        return None
     root = os.path.dirname(torch.__file__)
     inc = os.path.join(root, "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
@@ -58,13 +62,14 @@ def _stale(out: str, deps: list[str]) -> bool:
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
-    headers.append(os.path.join(HERE, "..", "include", "ddl.h"))
+    api = os.path.join(HERE, "..", "include", "ddl.h")
     srcs = sources()
-    deps = srcs + headers + [__file__, TORCH_SRC]
-    if not force and not _stale(LIB, deps) and not _stale(TORCH_LIB, deps):
+    lib = force or _stale(LIB, srcs + headers + [api, __file__])
+    module = force or _stale(TORCH_LIB, [TORCH_SRC, api, __file__])
+    dirs = _torch_dirs() if module else None
+    if not lib and not dirs:
         return LIB
-    nvcc = _nvcc()
-    incs, torch_lib = _torch_dirs()
+    nvcc = _nvcc() if lib else ""
     tobj = os.path.join(BUILD, "ddl_torch.o")
 
     def compile_one(src: str) -> tuple[str, str]:
@@ -76,35 +81,37 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj, r.stderr
 
     def compile_torch() -> None:
-        cmd = ["g++", "-O2", "-std=c++20", "-fPIC", *[f"-I{i}" for i in incs], "-c", TORCH_SRC, "-o", tobj]
+        cmd = ["g++", "-O2", "-std=c++20", "-fPIC", *[f"-I{i}" for i in dirs[0]], "-c", TORCH_SRC, "-o", tobj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"g++ failed on {TORCH_SRC}:\n{r.stdout}\n{r.stderr}")
 
     with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
-        module = ex.submit(compile_torch)
-        results = list(ex.map(compile_one, srcs))
-        module.result()
+        binding = ex.submit(compile_torch) if dirs else None
+        results = list(ex.map(compile_one, srcs)) if lib else []
+        if lib:
+            _link(LIB, [nvcc, *ARCH, "-shared"], [o for o, _ in results])
+        if binding:  # (the library does not need it: its own link comes first)
+            binding.result()
+            _link(TORCH_LIB, ["g++", "-shared"],
+                  [tobj, f"-L{BUILD}", "-lddl", f"-L{dirs[1]}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+                   "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{dirs[1]}"])
     if verbose:
         for _, log in results:
             sys.stderr.write(log)
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *[o for o, _ in results]]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    tmp = TORCH_LIB + f".tmp{os.getpid()}"
-    cmd = ["g++", "-shared", "-o", tmp, tobj, f"-L{BUILD}", "-lddl", f"-L{torch_lib}", "-ltorch_python", "-ltorch_cpu",
-           "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, TORCH_LIB)
-    with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
-        for _, log in results:
-            f.write(log)
+    if lib:
+        with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
+            for _, log in results:
+                f.write(log)
     return LIB
+
+
+def _link(out: str, linker: list[str], inputs: list[str]) -> None:
+    tmp = out + f".tmp{os.getpid()}"
+    r = subprocess.run([*linker, "-o", tmp, *inputs], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, out)
 
 
 if __name__ == "__main__":
