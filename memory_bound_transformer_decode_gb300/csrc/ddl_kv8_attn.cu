@@ -164,9 +164,7 @@ __device__ __forceinline__ void Att<CT, DT, HD, EX>::segment(const AttArgs& A, S
     check_scales(ks, vs);
     // V scales of blocks that no query of the tile sees do not count
     const int key = (c0 + kg + i * groups) * 16, last = min(tile * 8 + 7, nqueries - 1);
-    if (key > rq.p0 + group_row(A, last) ||
-        (A.window > 0 && key + 15 < rq.p0 + group_row(A, tile * 8) - A.window + 1))
-      vs = 0.f;
+    if (key > rq.p0 + group_row(A, last) || key + 15 < first_seen(A, rq, tile * 8)) vs = 0.f;
   };
   int32_t blk_l = block_row(lane), blk_n = -1;
   float ks_l, vs_l, ks_n = 0.f, vs_n = 0.f;

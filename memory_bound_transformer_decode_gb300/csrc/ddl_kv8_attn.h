@@ -147,13 +147,17 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return (top >> 7) * 255u;
 }
 
+// Row of a request that its query qi (row * group + head of the group) belongs to: qi / GH, qi < 512.
+__device__ __forceinline__ int group_row(const AttArgs& A, int qi) { return (int)((uint32_t)qi * (uint32_t)A.gmul >> 16); }
+// First token that the request's query qi sees (a window may reach back past any 32-bit number).
+__device__ __forceinline__ int64_t first_seen(const AttArgs& A, const Req& q, int qi) {
+  return A.window > 0 ? (int64_t)q.p0 + group_row(A, qi) - A.window + 1 : 0;
+}
 // Weight of request q's units.
 __device__ __forceinline__ int64_t req_weight(const AttArgs& A, const Req& q) {
   const int nb = q.b1 - q.b0;
   return nb > 0 ? (int64_t)(nb + A.unit_cost) * A.Hkv * unit_groups(A, q) : 0;
 }
-// Row of a request that its query qi (row * group + head of the group) belongs to: qi / GH, qi < 512.
-__device__ __forceinline__ int group_row(const AttArgs& A, int qi) { return (int)((uint32_t)qi * (uint32_t)A.gmul >> 16); }
 
 // Weights before each request into pre[0 .. R] (every CTA adds them up: R <=
 // 4096 lengths from L2); returns their sum.  CTA 0 leaves them for the join

@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
       // tokens that some query of the unit sees: V scales of blocks without any do not count
       const int qa = s.qc * NQ, qb = (s.rq.n * A.GH < qa + NQ ? s.rq.n * A.GH : qa + NQ) - 1;
       const int last_key = s.rq.p0 + group_row(A, qb);
-      const int first_key = A.window > 0 ? s.rq.p0 + group_row(A, qa) - A.window + 1 : 0;
+      const int64_t first_key = first_seen(A, s.rq, qa);
       int32_t page = page_of(lane), page_n = -1;
       for (int g0 = 0; ok && g0 < nblk; g0 += 32) {  // lane l: block g0 + l
         const int sub = (s.c1 - 1 - g0 - lane) & bmask;

@@ -117,3 +117,14 @@ def test_a_cap_far_above_the_scores_changes_nothing(dtype, codes, hd, bound, cap
     if cap >= 1e6:
         plain, want = check(pool, q, off, lens, table, max_len=bound, scale=1.0 / hd)
         assert (got.double() - plain.double()).abs().max() <= 4 * torch.finfo(q.dtype).eps * want.abs().max()
+
+
+@pytest.mark.parametrize("codes,hd", [("e4m3", 128), ("int8", 64)])
+def test_the_longest_window_of_rows_before_the_first_token(codes, hd):
+    """More rows than tokens and a window that reaches 2^31 back from a negative position hide nothing."""
+    for n, L in ((7, 3), (64, 40)):
+        pool, q, off, lens, table = setup(2, [n, 1], 8, 2, hd, 16, [L, 90], codes, "bf16", seed=28)
+        for window in (2 ** 31 - 2, 2 ** 31 - 5):
+            got, _ = check(pool, q, off, lens, table, max_len=2 ** 31 - 1, window=window)
+            plain, _ = check(pool, q, off, lens, table, max_len=2 ** 31 - 1)
+            assert torch.equal(got, plain)
