@@ -71,10 +71,16 @@ __device__ __forceinline__ Req load_req(const AttArgs& A, int r) {
   int64_t len = A.kv_len[r];
   const int64_t cap = (int64_t)A.per << A.pshift;
   q.bad = false;
+  // rows outside [0, T) are left out, the others keep their positions: `skip`
+  // rows before the first one that is computed, `n` from there to the newest
+  int64_t skip = 0, take = n;
   if (row0 < 0 || n < 0 || row0 + n > A.T) {
     q.bad = true;
-    n = 0;
-    row0 = 0;
+    skip = row0 < 0 ? -row0 : 0;
+    take = (row0 + n < A.T ? row0 + n : A.T) - (row0 + skip);
+    if (take <= 0) skip = n = take = 0;
+    row0 = take > 0 ? row0 + skip : 0;
+    n -= skip;
   }
   if (len < 0 || len > A.max_len || len > cap) {
     q.bad = true;
@@ -84,13 +90,15 @@ __device__ __forceinline__ Req load_req(const AttArgs& A, int r) {
   }
   q.row0 = (int32_t)row0;
   q.len = (int32_t)len;
-  q.p0 = (int32_t)(len - n);  // (n <= T)
+  const int64_t p0 = len - n;  // (n < 2^32 where rows lie outside)
+  q.p0 = (int32_t)(p0 < -(1 << 30) ? -(1 << 30) : p0);  // (so far from any key as its first 64 rows)
   int64_t lo = A.window > 0 ? len - n - A.window + 1 : 0;
   lo = lo < 0 ? 0 : lo;
-  if (n > A.max_rows) {
+  if (take > A.max_rows) {
     q.bad = true;
-    n = A.max_rows;  // its first rows
+    take = A.max_rows;  // its first rows
   }
+  n = take;
   q.n = (int32_t)n;
   q.b0 = (int32_t)(lo >> 4);
   q.b1 = n > 0 ? (int32_t)((len + 15) >> 4) : q.b0;
