@@ -493,8 +493,16 @@ def ddl_kv8_append(pool: tuple, k_new: torch.Tensor, v_new: torch.Tensor, slot: 
         raise DDLError("ddl_kv8_append", st, _lib)
 
 
+def _int32(**sizes: int) -> None:
+    """ctypes would cut a larger number down to 32 bits without a word."""
+    for name, v in sizes.items():
+        if not -2 ** 31 <= v < 2 ** 31:
+            raise ValueError(f"{name}: a 32-bit integer")
+
+
 def ddl_kv8_attention_workspace_bytes(H_q: int, H_kv: int, hd: int, R: int, T: int, max_rows: int,
                                       max_len: int) -> int:
+    _int32(H_q=H_q, H_kv=H_kv, hd=hd, R=R, T=T, max_rows=max_rows, max_len=max_len)
     n = int(load().ddl_kv8_attention_workspace_bytes(H_q, H_kv, hd, R, T, max_rows, max_len))
     if n == 0:
         raise DDLError("ddl_kv8_attention_workspace_bytes", 1, _lib)
@@ -551,6 +559,7 @@ def _kv8(pool, dev: int, H: int, hd: int) -> KV8:
 
 
 def ddl_stack_kv8_workspace_bytes(shape: Shape, R: int, T: int, max_rows: int, max_len: int) -> int:
+    _int32(R=R, T=T, max_rows=max_rows, max_len=max_len)
     n = int(load().ddl_stack_kv8_workspace_bytes(ctypes.byref(shape), R, T, max_rows, max_len))
     if n == 0:
         raise DDLError("ddl_stack_kv8_workspace_bytes", 1, _lib)
@@ -567,6 +576,7 @@ def ddl_stack_step_kv8(shape: Shape, wtype: int, layers: list, pools: list, *, r
     """One step of len(layers) layers on 8-bit pools (one (k, v, k_scale,
     v_scale) per layer) for the rows that ddl_page_plan has placed."""
     lib = load()
+    _int32(max_rows=max_rows, max_len=max_len, window=window)
     x = x_bf16 if x_bf16 is not None else resid_in
     if x is None:
         raise ValueError("x_bf16 or resid_in")
