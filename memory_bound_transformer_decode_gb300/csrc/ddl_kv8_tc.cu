@@ -23,10 +23,12 @@
 //    the query's largest product of weight and V scale) in four e5m2 limbs of 3 bits, exactly.  (As e4m3, whose
 //    conversions both ways the limbs then need: 64 rows on 8192 tokens 64.6 us,
 //    so 63.4, and 61.6 with two scores an instruction.)
-//  - P of fp32 rows: an fp16 in the e5m2 limbs of group A, L = 4 of them, and what
-//    it leaves, times 2^12 and again in fp16, in those of group B: 2^-22 of a weight,
-//    2^-39 of the largest.  (Six e4m3 limbs ended at 2^-27 of the largest: the
-//    weights of a long tail that lie below it were in the sum but not in O.)
+//  - P of fp32 rows: an fp16 in four e5m2 limbs, groups A and B, and what it
+//    leaves, times 2^12 and again in fp16, in those of two more groups, C and D: 2^-22
+//    of a weight, 2^-39 of the largest.  (Six e4m3 limbs ended at 2^-27 of the largest:
+//    the weights of a long tail that lie below it were in the sum but not in O.)  Each
+//    MMA rounds its accumulator off, by up to 2^-23 of it; with the largest limbs in an
+//    accumulator of their own that is 8 times a tile, not 16.
 //
 // A segment's tiles are taken from the newest token to the oldest: a distance
 // bias then raises the running maximum once and not with every tile (4 rows of
@@ -76,10 +78,12 @@ struct Geo {
   static constexpr int WG = NQ / QW;            // softmax warpgroups
   static constexpr int THREADS = 128 * WG + 64;
   static constexpr int N = 16 * NT;             // B columns
-  static constexpr int LP = L == 2 ? 2 : 4;     // passes of P (L: of Q)
-  static constexpr uint32_t OPB = NT * 2048u;   // bytes of one pass's Q or P operand
-  static constexpr uint32_t Q_OFF = STAGES * 2 * KBYTES, P_OFF = Q_OFF + L * OPB, SH_OFF = P_OFF + LP * OPB;
-  static constexpr uint32_t COLS = NT == 1 ? 64 : NT == 2 ? 128 : 256;  // S twice, O: 48 NT columns
+  static constexpr int LP = 2, PG = L == 2 ? 2 : 4;  // passes of P (L: of Q) and its groups of limbs
+  static constexpr int ON = 8 * PG * NT;             // columns of O
+  static constexpr uint32_t OPB = NT * 2048u;        // bytes of one pass's Q operand
+  static constexpr uint32_t OPP = ON * 128u;         // and P operand
+  static constexpr uint32_t Q_OFF = STAGES * 2 * KBYTES, P_OFF = Q_OFF + L * OPB, SH_OFF = P_OFF + LP * OPP;
+  static constexpr uint32_t COLS = NT == 1 ? 64 : NT == 2 ? 128 : 256;  // S twice, O: 48 NT or 64 NT columns
 };
 
 struct Meta {  // of a stage's tile
@@ -274,7 +278,7 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
   constexpr int L = DT == DDL_T_F32 ? 3 : 2;
   constexpr float BSCALE = DT == DDL_T_F32 ? 4096.f : 256.f;  // 16^L (of Q and of P)
   using G = Geo<NT, L>;
-  constexpr int NQ = G::NQ, QW = G::QW, WG = G::WG, NS = 128 * WG, LP = G::LP;  // NS: softmax threads
+  constexpr int NQ = G::NQ, QW = G::QW, WG = G::WG, NS = 128 * WG, LP = G::LP, PG = G::PG;  // NS: softmax threads
   constexpr int CW = 4 * WG, MW = 4 * WG + 1;                         // the copying and the MMA warp
   extern __shared__ __align__(1024) uint8_t smem[];
   Shared<NT, L>& S = *reinterpret_cast<Shared<NT, L>*>(smem + G::SH_OFF);
@@ -425,7 +429,8 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
   } else if (warp == MW) {  // ------------------------------------------ MMA issue
     constexpr uint32_t IDESC_S = (1u << 4) | ((uint32_t)(G::N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
     // P e5m2; A and B M/N-major
-    constexpr uint32_t IDESC_O = IDESC_S | (1u << 10) | (1u << 15) | (1u << 16);
+    constexpr uint32_t IDESC_O = (1u << 4) | ((uint32_t)(G::ON >> 3) << 17) | ((uint32_t)(128 >> 4) << 24) | (1u << 10) |
+                                 (1u << 15) | (1u << 16);
     const uint64_t kd = sdesc(sb, 16, 1024, 2), vd = sdesc(sb + KBYTES, 16384, 1024, 2);
     const uint64_t qd = sdesc(sb + G::Q_OFF, 16, 1024, 2), pd = sdesc(sb + G::P_OFF, 128, 2048, 0);
     uint32_t tc = 0, sg = 0;
@@ -465,7 +470,7 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
           for (int p = 0; p < LP; ++p)
 #pragma unroll
             for (int k = 0; k < 4; ++k)  // 32 tokens each
-              umma_f8(tO, a + k * (4096 >> 4), pd + (uint64_t)(p * (G::OPB >> 4)) + k * (512 >> 4), IDESC_O,
+              umma_f8(tO, a + k * (4096 >> 4), pd + (uint64_t)(p * (G::OPP >> 4)) + k * (512 >> 4), IDESC_O,
                       i + p + k > 0 ? 1u : 0u);
           umma_commit(empty + 8 * st);
           umma_commit(pvdone);
@@ -483,7 +488,7 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
     uint32_t tc = 0;
     bool ok = true;
     Segs s = first;
-    const uint32_t tlane = (uint32_t)(32 * (warp & 3)) << 16, tSq = tm + tlane + 2 * x0, tOq = tO + tlane + 2 * x0;
+    const uint32_t tlane = (uint32_t)(32 * (warp & 3)) << 16, tSq = tm + tlane + 2 * x0, tOq = tO + tlane + PG * x0;
     // A wait that gives up makes its warp go on without waiting, so that none is
     // left at a barrier; the results of that segment and of the CTA's later ones
     // become NaN, also in the records that the join adds up.
@@ -696,13 +701,13 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
           if (i > 0) {
             tc_fence_after();
 #pragma unroll
-            for (int j = 0; j < QW / 8; ++j) {
+            for (int j = 0; j < QW * PG / 16; ++j) {  // 16 columns: two groups of 8 queries
               uint32_t v[16];
               tmem_ld_32x32b_x16(tOq + 16 * j, v);
               tmem_ld_wait();
 #pragma unroll
               for (int q = 0; q < 16; ++q)
-                v[q] = __float_as_uint(__uint_as_float(v[q]) * (S.al[x0 + 8 * j + (q & 7)] * fv));
+                v[q] = __float_as_uint(__uint_as_float(v[q]) * (S.al[x0 + 8 * (j / (PG / 2)) + (q & 7)] * fv));
               tmem_st_32x32b_x16(tOq + 16 * j, v);
             }
             tmem_st_wait();
@@ -712,7 +717,7 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
         // the tile's weights, and their limbs as the PV operand (whose place is
         // free once the previous tile's PV MMAs are done)
         const F2 wv2(vs * vinv * TP_SCALE<L>);
-        uint4 pk[QW / 8][LP];
+        uint4 pk[QW / 8][LP][PG / 2];
 #pragma unroll
         for (int j = 0; j < QW / 8; ++j) {
           float w[8];
@@ -722,20 +727,20 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
             l[4 * j + q / 2] = add2(l[4 * j + q / 2], p);
             mul2(p, wv2).get(w[q], w[q + 1]);
           }
-          uint2 a[LP], b[LP];
+          uint2 limb[PG][LP];
           uint32_t h[4];  // fp16 (2^-11), 11 bits, as four limbs: exactly
 #pragma unroll
           for (int q = 0; q < 4; ++q) h[q] = pack_f16x2(w[2 * q], w[2 * q + 1]);
           if (L == 2) {
-            a[0] = limb8h(h);
+            limb[0][0] = limb8h(h);
             drop_limb(h);
-            a[1] = limb8h(h);
+            limb[0][1] = limb8h(h);
             drop_limb(h);
 #pragma unroll
             for (int q = 0; q < 4; ++q) h[q] = h2_bits(__hmul2(h2_of(h[q]), h2_of(0x5c005c00u)));  // times 256
-            b[0] = limb8h(h);
+            limb[1][0] = limb8h(h);
             drop_limb(h);
-            b[1] = limb8h(h);
+            limb[1][1] = limb8h(h);
           } else {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {  // what the fp16 leaves
@@ -744,8 +749,8 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
               w[2 * q + 1] -= f.y;
             }
 #pragma unroll
-            for (int p = 0; p < LP; ++p) {
-              a[p] = limb8h(h);
+            for (int p = 0; p < 4; ++p) {
+              limb[p / 2][p & 1] = limb8h(h);
               drop_limb(h);
             }
 #pragma unroll
@@ -754,20 +759,26 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
               h[q] = pack_f16x2((w[2 * q] + f.x) * BSCALE, (w[2 * q + 1] + f.y) * BSCALE);
             }
 #pragma unroll
-            for (int p = 0; p < LP; ++p) {
-              b[p] = limb8h(h);
-              if (p + 1 < LP) drop_limb(h);
+            for (int p = 0; p < 4; ++p) {
+              limb[(2 + p / 2) % PG][p & 1] = limb8h(h);
+              if (p < 3) drop_limb(h);
             }
           }
 #pragma unroll
-          for (int p = 0; p < LP; ++p) pk[j][p] = make_uint4(a[p].x, a[p].y, b[p].x, b[p].y);
+          for (int p = 0; p < LP; ++p)
+#pragma unroll
+            for (int g = 0; g < PG; g += 2)
+              pk[j][p][g / 2] = make_uint4(limb[g][p].x, limb[g][p].y, limb[g + 1][p].x, limb[g + 1][p].y);
         }
         if (!waited) ok = ok && wait(pvdone, (tc - 1) & 1);
 #pragma unroll
         for (int j = 0; j < QW / 8; ++j)
 #pragma unroll
           for (int p = 0; p < LP; ++p)
-            *reinterpret_cast<uint4*>(smem + G::P_OFF + p * G::OPB + (x0 / 8 + j) * 2048 + tok * 16) = pk[j][p];
+#pragma unroll
+            for (int g = 0; g < PG / 2; ++g)
+              *reinterpret_cast<uint4*>(smem + G::P_OFF + p * G::OPP + ((x0 / 8 + j) * (PG / 2) + g) * 2048 + tok * 16) =
+                  pk[j][p][g];
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -806,19 +817,26 @@ __global__ void __launch_bounds__(Geo<NT, DT == DDL_T_F32 ? 3 : 2>::THREADS, 2) 
       ssync(1 + wg, 128);
 #pragma unroll
       for (int j = 0; j < QW / 8; ++j) {
-        uint32_t v[16];
+        float sum[8];
         if (nt > 0) {
-          tmem_ld_32x32b_x16(tOq + 16 * j, v);
+          uint32_t v[PG / 2][16];
+#pragma unroll
+          for (int g = 0; g < PG / 2; ++g) tmem_ld_32x32b_x16(tOq + 8 * PG * j + 16 * g, v[g]);
           tmem_ld_wait();
+          auto at = [&](int g, int q) { return __uint_as_float(v[g / 2][8 * (g & 1) + q]); };
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            sum[q] = PG == 2 ? fmaf(at(1, q), 1.f / BSCALE, at(0, q))
+                             : fmaf(at(2 % PG, q) + at(3 % PG, q), 1.f / BSCALE, at(0, q) + at(1, q));
         } else {
 #pragma unroll
-          for (int q = 0; q < 16; ++q) v[q] = 0u;
+          for (int q = 0; q < 8; ++q) sum[q] = 0.f;
         }
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           const int x = x0 + 8 * j + q;
           const int64_t place = S.place[x];
-          const float o = fmaf(__uint_as_float(v[8 + q]), 1.f / BSCALE, __uint_as_float(v[q])) * S.al[x] * vref;
+          const float o = sum[q] * S.al[x] * vref;
           if (A.cluster > 1) {  // (the ring of K and V is done with: its copies have landed and been used)
             reinterpret_cast<float*>(smem)[x * 128 + tok] = o;
             continue;
