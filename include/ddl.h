@@ -390,8 +390,16 @@ int ddl_kv8_append(const ddl_kv8* kv, int32_t H_kv, int32_t head_dim, ddl_dtype 
  *  - H_q % H_kv == 0, H_q / H_kv <= 8, head_dim 64 or 128 (DDL_ERR_SHAPE).
  *  - q, out: device [T][H_q][head_dim] of `dtype`, heads contiguous, rows
  *    q_stride / out_stride elements apart (>= H_q * head_dim, a multiple of 8),
- *    16-byte aligned.  Scores, softmax and sums are fp32.  lse: device fp32
- *    [T][H_q] or NULL.  out must not overlap q.
+ *    16-byte aligned.  lse: device fp32 [T][H_q] or NULL.  out must not
+ *    overlap q.
+ *  - Precision.  Scores, their maximum, sums and lse are fp32.  What enters
+ *    the tensor cores is rounded: q of 16-bit rows not at all, of fp32 rows to
+ *    2^-22 of an element, neither finer than 2^-25 (fp32 2^-29) of the row's
+ *    largest element; a key's weight exp(s_j) times its V scale to 2^-11 of
+ *    itself for 16-bit rows, 2^-22 for fp32 rows, no finer than 2^-30 (fp32
+ *    2^-36) of the row's largest such product (lse and the divisor take the
+ *    weight unrounded).  Sums of V round off 2^-23 of themselves with each
+ *    MMA, some 8 to 16 times for 128 tokens.
  *  - 1 <= R <= DDL_KV8_MAX_REQS.  max_rows: a bound on n, <= DDL_KV8_MAX_ROWS
  *    (1 without q_off).  max_len >= 1: a bound on kv_len.  Both only size the
  *    launch; a request beyond them (or beyond its table row, or with rows

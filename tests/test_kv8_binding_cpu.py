@@ -34,3 +34,17 @@ def test_stack_step(name, value):
               x_bf16=torch.zeros((1, 64), dtype=torch.bfloat16))
     with pytest.raises(ValueError, match=f"^{name}: a 32-bit integer"):
         ddl.ddl_stack_step_kv8(ddl.make_shape(configs.SMALL_LAYER), ddl.INT4, [], [], **{**kw, name: value})
+
+
+def test_the_header_states_the_precision_of_the_weights():
+    """The tests' bounds take the roundings that the header gives, and it claims no more than the kernels hold."""
+    import os
+
+    import kv8_bounds
+
+    text = " ".join(open(os.path.join(build.HERE, "..", "include", "ddl.h")).read().replace("*", " ").split())
+    assert "Scores, softmax and sums are fp32" not in text
+    assert ("times its V scale to 2^-11 of itself for 16-bit rows, 2^-22 for fp32 rows, no finer than 2^-30 (fp32 2^-36) of "
+            "the row's largest such product") in text
+    for t, step, floor in ((torch.bfloat16, -11, -30), (torch.float16, -11, -30), (torch.float32, -22, -36)):
+        assert kv8_bounds.STEP[t] == 2.0 ** step and kv8_bounds.FLOOR[t] == 2.0 ** (floor + 1)
