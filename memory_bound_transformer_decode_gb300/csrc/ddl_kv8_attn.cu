@@ -697,7 +697,7 @@ int att_sms(int& sms) {
 // GPC's SMs side by side), blocks a CTA takes at least.
 constexpr int MAX_CLUSTER = 16, MIN_PART = 16;
 // fp32 rows of 128: two CTAs fit an SM while the weights before so many requests fit beside the rings (64 requests of
-// up to 2049 in shares: 75 us, one CTA an SM; whole units of two heads a CTA: 58).
+// up to 2049 in shares: 72 us, one CTA an SM; whole units of two heads a CTA: 55).
 constexpr int F32_TWO_CTAS_R = 55;
 static_assert(2 * (sizeof(Att<DDL_KV8_INT8, DDL_T_F32, 128, false>::Smem) + (F32_TWO_CTAS_R + 1) * 8 + ATT_WARPS * 8 + 1024) <=
                   228 * 1024,
@@ -743,9 +743,12 @@ int att_plan(bool tc, bool f32, int32_t H_q, int32_t H_kv, int32_t hd, int32_t R
   // 1.6 for two, 2.1 for four; a further wave of CTAs 2 us (5); a cluster's join
   // 1.3 us; shares 6 to 8 us for the sums of the lengths, the records' way through
   // memory and the second launch, and every unit a CTA begins 3.5 us (5).
-  // E.g. 1 request of 600 tokens, 8 K/V heads: clusters 7.1 us (tcgen05 9.3),
-  // shares 11.4 (12.5); of 8193: 14.2 (12.8), 15.4 (14.6); 64 requests of up to
-  // 2049: shares 50 (37).
+  // E.g. (bf16 rows, 64/8 heads, calls in a graph) 1 request of 600 int8 tokens:
+  // clusters 7.4 us, shares 12.3 (e4m3 on tcgen05 in clusters 9.2); of 8193: 14.7,
+  // 16.6 (12.5); 64 requests of up to 2049: shares 48 (38).  40 drawn sizes of e4m3
+  // codes and head_dim 128: 0.4 % above the better kernel in the geometric mean,
+  // 20 % at worst (26 requests of 6 rows on 119 tokens: 9.2 us against 7.7).  The same
+  // costs choose the split for head_dim 64.
   const int64_t fixed = tc ? 70 : 40, again = fixed - 20;
   auto in_a_row = [&](int64_t b, int64_t filling, int64_t after) -> int64_t {
     if (tc) return (b + 7) / 8 * (p.nq == 1 ? 10 : p.nq == 2 ? 16 : 21);

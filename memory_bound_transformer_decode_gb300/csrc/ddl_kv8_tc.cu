@@ -22,7 +22,8 @@
 //  - P of 16-bit rows: fp16 (2^-11, no more than the output's own rounding; 2^-30 of
 //    the query's largest product of weight and V scale) in four e5m2 limbs of 3 bits, exactly.  (As e4m3, whose
 //    conversions both ways the limbs then need: 64 rows on 8192 tokens 64.6 us,
-//    so 63.4, and 61.6 with two scores an instruction.)
+//    so 63.4, and 61.6 with two scores an instruction; 65.3 since the
+//    weights' reference follows the V scales.)
 //  - P of fp32 rows: an fp16 in four e5m2 limbs, groups A and B, and what it
 //    leaves, times 2^12 and again in fp16, in those of two more groups, C and D: 2^-22
 //    of a weight, 2^-39 of the largest.  (Six e4m3 limbs ended at 2^-27 of the largest:
