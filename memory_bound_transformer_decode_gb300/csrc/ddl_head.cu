@@ -23,8 +23,6 @@
 #include <cuda_fp16.h>
 #include <math.h>
 
-#include <mutex>
-
 #include "ddl_device.cuh"
 #include "ddl_internal.h"
 
@@ -35,25 +33,6 @@ constexpr int HEAD_THREADS = 256;  // 8 warps a CTA
 constexpr int HEAD_CTAS_PER_SM = 2;
 constexpr int SEL_THREADS = 1024;
 constexpr int PREP_THREADS = 256;
-
-int g_head_sms[64];
-std::mutex g_head_mu;
-
-int head_sms(int& sms) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_status(e);
-  if (dev < 0 || dev >= 64) return DDL_ERR_UNSUPPORTED;
-  std::lock_guard<std::mutex> lk(g_head_mu);
-  if (!g_head_sms[dev]) {
-    int n = 0;
-    if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
-      return cuda_status(e);
-    g_head_sms[dev] = n;
-  }
-  sms = g_head_sms[dev];
-  return DDL_OK;
-}
 
 // n-tiles of 8 columns: two columns (hi, lo) per sequence, a power of two.
 int head_ntn(int B) {
@@ -69,7 +48,7 @@ struct HeadLayout {
 
 int head_layout(int32_t D, int64_t V, int32_t B, HeadLayout& h) {
   int sms = 0;
-  const int st = head_sms(sms);
+  const int st = device_sms(sms);
   if (st) return st;
   h.ctas = sms * HEAD_CTAS_PER_SM;
   h.nwarps = h.ctas * (HEAD_THREADS / 32);

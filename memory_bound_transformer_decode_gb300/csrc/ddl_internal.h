@@ -6,6 +6,8 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <atomic>
+
 #include "../../include/ddl.h"
 #include "ddl_plan.h"
 
@@ -20,6 +22,22 @@ inline int cuda_status(cudaError_t e) {
   if (e == cudaSuccess) return DDL_OK;
   set_cuda_error(e);
   return DDL_ERR_CUDA;
+}
+
+// SMs of the current device (asked for once a device).
+inline int device_sms(int& sms) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_status(e);
+  if (dev < 0 || dev >= 64) return DDL_ERR_UNSUPPORTED;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (!n) {
+    if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return cuda_status(e);
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  sms = n;
+  return DDL_OK;
 }
 
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
@@ -128,6 +146,26 @@ inline cudaError_t launch_pdl(const void* fn, dim3 grid, dim3 block, void** args
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
+  return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+// A dependent launch of a grid of clusters.
+inline cudaError_t launch_pdl_cluster(const void* fn, dim3 grid, dim3 block, void** args, size_t smem, int cluster,
+                                      cudaStream_t s) {
+  if (cluster <= 1) return launch_pdl(fn, grid, block, args, smem, s);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelExC(&cfg, fn, args);
 }
 

@@ -246,33 +246,6 @@ __device__ __forceinline__ void store_codes(uint8_t* p, uint32_t c) {
   else *reinterpret_cast<uint16_t*>(p) = (uint16_t)c;
 }
 
-// The smallest power of two s >= 2^-126 with amax / s <= the largest code
-// (448 = 1.75 * 2^8 or 127 = 1.984375 * 2^6): from amax = m * 2^e its exponent
-// is e - 8 (e - 6), one more where m is above 1.75 (1.984375).  A power of two
-// makes x / s exact, so a code is x rounded once, and moves e4m3 codes to a
-// larger scale without rounding them again (unless they become subnormal).
-template <int CT>
-__device__ __forceinline__ float pow2_scale(float amax) {
-  if (!(amax > 0.f)) return 0.f;
-  const uint32_t b = __float_as_uint(amax), frac = b & 0x7fffffu;
-  int e = (int)(b >> 23) - (CT == DDL_KV8_E4M3 ? 8 : 6) + (frac > (CT == DDL_KV8_E4M3 ? 0x600000u : 0x7e0000u) ? 1 : 0);
-  e = e < 1 ? 1 : e;
-  return __uint_as_float((uint32_t)e << 23);
-}
-
-// x / s: a product with 1 / s where s is a power of two whose inverse is
-// normal (both exact), else a division.
-struct Divider {
-  float s, inv;
-  bool pow2;
-  __device__ __forceinline__ explicit Divider(float scale) : s(scale) {
-    const uint32_t b = __float_as_uint(scale), e = b >> 23;
-    pow2 = (b & 0x7fffffu) == 0u && e >= 1u && e <= 253u;
-    inv = __uint_as_float((254u - (e < 254u ? e : 253u)) << 23);
-  }
-  __device__ __forceinline__ float operator()(float x) const { return pow2 ? x * inv : s > 0.f ? __fdiv_rn(x, s) : x; }
-};
-
 // One warp stores the rows of one 16-token block of one head of K or of V:
 // each lane W neighbouring elements of every row.  A block's rows are normally
 // one run of neighbours in the slot map; the warp that owns the run's first

@@ -75,4 +75,47 @@ __device__ __forceinline__ uint32_t f32_int8(float v) {
   return v == v ? (uint32_t)(uint8_t)(int8_t)__float2int_rn(c) : 0u;
 }
 
+// Bytes lo16 / hi16 of w (two codes) as fp16 pairs.
+template <int CT>
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if (CT == DDL_KV8_E4M3) {
+    e4m3x4_f16x2(w, lo, hi);
+  } else {  // 1024 + (c + 128) - 1152 = c, exact in fp16
+    const uint32_t u = w ^ 0x80808080u;
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+  }
+}
+
+// The smallest power of two s >= 2^-126 with amax / s <= the largest code
+// (448 = 1.75 * 2^8 or 127 = 1.984375 * 2^6): from amax = m * 2^e its exponent
+// is e - 8 (e - 6), one more where m is above 1.75 (1.984375).  A power of two
+// makes x / s exact, so a code is x rounded once, and moves e4m3 codes to a
+// larger scale without rounding them again (unless they become subnormal).
+template <int CT>
+__device__ __forceinline__ float pow2_scale(float amax) {
+  if (!(amax > 0.f)) return 0.f;
+  const uint32_t b = __float_as_uint(amax), frac = b & 0x7fffffu;
+  int e = (int)(b >> 23) - (CT == DDL_KV8_E4M3 ? 8 : 6) + (frac > (CT == DDL_KV8_E4M3 ? 0x600000u : 0x7e0000u) ? 1 : 0);
+  e = e < 1 ? 1 : e;
+  return __uint_as_float((uint32_t)e << 23);
+}
+
+// x / s: a product with 1 / s where s is a power of two whose inverse is
+// normal (both exact), else a division.
+struct Divider {
+  float s, inv;
+  bool pow2;
+  __device__ __forceinline__ explicit Divider(float scale) : s(scale) {
+    const uint32_t b = __float_as_uint(scale), e = b >> 23;
+    pow2 = (b & 0x7fffffu) == 0u && e >= 1u && e <= 253u;
+    inv = __uint_as_float((254u - (e < 254u ? e : 253u)) << 23);
+  }
+  __device__ __forceinline__ float operator()(float x) const { return pow2 ? x * inv : s > 0.f ? __fdiv_rn(x, s) : x; }
+};
+
 }  // namespace ddl

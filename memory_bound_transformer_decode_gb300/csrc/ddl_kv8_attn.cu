@@ -42,8 +42,6 @@
 // joined in share order by a second kernel.  att_plan estimates which costs less.
 #include <cuda_bf16.h>
 
-#include <mutex>
-
 #include "ddl_kv8_attn.h"
 
 namespace ddl {
@@ -70,22 +68,6 @@ __device__ __forceinline__ void cp_async16_l1(uint32_t dst, const void* src) {
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-// Bytes lo16 / hi16 of w (two codes) as fp16 pairs.
-template <int CT>
-__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  if (CT == DDL_KV8_E4M3) {
-    e4m3x4_f16x2(w, lo, hi);
-  } else {  // 1024 + (c + 128) - 1152 = c, exact in fp16
-    const uint32_t u = w ^ 0x80808080u;
-    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-    const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
-    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
-    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
-    lo = *reinterpret_cast<const uint32_t*>(&x);
-    hi = *reinterpret_cast<const uint32_t*>(&y);
-  }
-}
 
 template <int CT, int DT, int HD, bool EX>
 struct Att {
@@ -675,24 +657,6 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(const __grid_constant__ A
 }
 
 // ------------------------------------------------------------------ host
-int g_att_sms[64];
-std::mutex g_att_mu;
-
-int att_sms(int& sms) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_status(e);
-  if (dev < 0 || dev >= 64) return DDL_ERR_UNSUPPORTED;
-  std::lock_guard<std::mutex> lk(g_att_mu);
-  if (!g_att_sms[dev]) {
-    int n = 0;
-    if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return cuda_status(e);
-    g_att_sms[dev] = n;
-  }
-  sms = g_att_sms[dev];
-  return DDL_OK;
-}
-
 // Clusters: CTAs of a unit at most (16 is past the portable 8, and two fit a
 // GPC's SMs side by side), blocks a CTA takes at least.
 constexpr int MAX_CLUSTER = 16, MIN_PART = 16;
@@ -722,7 +686,7 @@ int check_sizes(int32_t H_q, int32_t H_kv, int32_t hd, int32_t R, int32_t T, int
 int att_plan(bool tc, bool f32, int32_t H_q, int32_t H_kv, int32_t hd, int32_t R, int32_t max_rows, int32_t max_len,
              int32_t window, bool clusters, AttPlan& p) {
   int sms = 0;
-  const int st = att_sms(sms);
+  const int st = device_sms(sms);
   if (st) return st;
   const int tiles = (max_rows * (H_q / H_kv) + 7) / 8;
   p.nq = 1;

@@ -254,20 +254,6 @@ __device__ __forceinline__ void store_elem(void* p, int64_t i, float v) {
 }
 
 // ------------------------------------------------------------------ clusters
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int rank) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-  return a;
-}
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-
 // A CTA of a cluster and its run of the unit's blocks.
 struct ClusterPart {
   int unit, rank;  // unit: ((request * H_kv) + head) * nqc + group of tiles
@@ -332,26 +318,6 @@ __device__ __forceinline__ void cluster_join(const AttArgs& A, const ClusterPart
       if (d == 0 && A.lse) A.lse[(int64_t)(rq.row0 + row) * A.Hq + head] = (m + log2f(l)) * LN2;
     }
   cluster_sync();  // (nobody's shared memory goes while another reads it)
-}
-
-// A dependent launch of a grid of clusters.
-inline cudaError_t launch_pdl_cluster(const void* fn, dim3 grid, dim3 block, void** args, size_t smem, int cluster,
-                                      cudaStream_t s) {
-  if (cluster <= 1) return launch_pdl(fn, grid, block, args, smem, s);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = (unsigned)cluster;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
 // The tcgen05 kernel (e4m3, head_dim 128): rows of the pool's view < 2^31.
