@@ -427,6 +427,70 @@ int ddl_kv8_attention(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, int32_t head
                       int32_t pages_per_seq, const void* q, int64_t q_stride, void* out, int64_t out_stride,
                       float* lse, int32_t* bad_out, void* workspace, size_t ws_bytes, void* stream);
 
+/* Attention weight drawn by each cached token, per K/V head: score [R][H_kv]
+ * [score_stride] (device fp32; request r's tokens 0 .. kv_len[r] - 1 lie at the
+ * front of its rows) becomes
+ *     score_j = decay * score_j + sum over the request's rows i and the heads h of
+ *               the K/V head's group of exp(s_ij - lse_ih)
+ * with the scores s_ij and rows of ddl_kv8_attention (same requests, options and
+ * masks) and lse [T][H_q] (device fp32) as that call returned it.  Tokens of the
+ * step itself (positions kv_len[r] - n and later) begin at zero, whatever score
+ * holds for them.  decay: in [0, 1]; 0 does not read the old scores.  Requests
+ * without rows, and entries behind kv_len[r], are left as they were.
+ *  - A row with lse = -inf adds nothing; NaN in lse, or a NaN code or a scale that
+ *    is not finite among a row's keys, gives NaN in the scores of the tokens
+ *    concerned (a NaN score stays NaN until decay is 0).
+ *  - Precision: scores and weights as in ddl_kv8_attention (q of fp32 rows to
+ *    2^-22), sums in fp32, in a fixed order: two calls give the same bits.
+ *  - Limits, max_rows, max_len, page_table, bad_out (bit 0): as ddl_kv8_attention.
+ *    score_stride >= max_len (DDL_ERR_ARG).  A token of a page outside the pool
+ *    draws nothing. */
+int ddl_kv8_score(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, int32_t head_dim, ddl_dtype dtype,
+                  const ddl_attn_opts* opts, int32_t R, int32_t T, int32_t max_rows, int32_t max_len,
+                  const int32_t* q_off, const int32_t* kv_len, const int32_t* page_table,
+                  int32_t pages_per_seq, const void* q, int64_t q_stride, const float* lse, float decay,
+                  float* score, int64_t score_stride, int32_t* bad_out, void* stream);
+
+/* Requests cut to their heaviest tokens.  Request r with 0 <= keep_len[r] <
+ * kv_len[r] keeps, in each K/V head by itself, its newest rc = min(recent, keep)
+ * tokens, its first sc = min(sinks, keep - rc), and of the others the keep - rc - sc
+ * of the largest score (equal scores: the lower index first; both zeros are equal, NaN
+ * comes last).  Any other request stays as it is.  For the requests that are cut:
+ *  - kept [R][H_kv][max_keep] (device int32): kept[r][g][i] is the index, ascending,
+ *    of the token that is now token i of head g.
+ *  - K and V: token i goes to row i of the pages that new_table [R]
+ *    [new_pages_per_seq] names for the request (device int32, of the same pool).
+ *    Each block of 16 kept tokens gets a scale of its own, as ddl_kv8_append
+ *    chooses it (the smallest power of two, >= 2^-126, at which the largest value
+ *    fits; 0 if all are zero); a code is value / scale rounded to nearest, ties to
+ *    even, and the code itself where the token's scale is the new one.  NaN codes
+ *    stay NaN.  A source scale that is negative or not finite makes the block's
+ *    scale NaN.  The last block's rows behind token keep - 1 are zero.
+ *  - Nothing else is written: the old pages stay as they were (other requests may
+ *    share them) and are the caller's to free.  New pages are distinct and no
+ *    page that any request of the call reads.
+ * score_out [R][H_kv][score_stride]: the kept tokens' scores, in order (of a request
+ * that stays: its kv_len[r] scores); entries behind them are left as they were.
+ * After the call a cut request has keep_len[r] tokens in its new_table row
+ * (ddl_page_plan with old lengths of 0 and keep_len to add takes such rows from the
+ * free list).  Keys keep the rotation of the position at which they came: later rows
+ * go on with their own positions, while ddl_kv8_attention's window and distance bias
+ * count cached tokens.  All layers of a stack have one length per request, so they
+ * are cut by the same keep_len.
+ *  - 1 <= R <= DDL_KV8_MAX_REQS; max_len bounds kv_len and score_stride >= max_len
+ *    (DDL_ERR_ARG); 1 <= max_keep <= max_len bounds keep_len of the requests that are
+ *    cut; sinks, recent >= 0; score_out is not score, new_table not page_table
+ *    (DDL_ERR_ARG), nor may they overlap.
+ *  - A request beyond these bounds or its table rows is computed on what lies within
+ *    them; a token of a page outside the pool becomes zeros and a block whose new page
+ *    is outside is not written; either sets bit 0 of *bad_out (device int32, may be
+ *    NULL, never cleared by the call). */
+int ddl_kv8_evict(const ddl_kv8* kv, int32_t H_kv, int32_t head_dim, int32_t R, int32_t max_len,
+                  const float* score, int64_t score_stride, const int32_t* kv_len, const int32_t* keep_len,
+                  int32_t sinks, int32_t recent, const int32_t* page_table, int32_t pages_per_seq,
+                  const int32_t* new_table, int32_t new_pages_per_seq, int32_t max_keep, int32_t* kept,
+                  float* score_out, int32_t* bad_out, void* stream);
+
 /* One step of an L-layer stack on 8-bit paged caches: the layers of
  * ddl_stack_decode with ddl_kv8_append and ddl_kv8_attention in the place of
  * the bf16 append and attention.  Takes ddl_page_plan's outputs as they are,
@@ -510,6 +574,37 @@ int ddl_lm_head(int32_t D, int64_t V, ddl_wtype wtype, const void* head_packed, 
                 float eps, int32_t B, const float* x, int32_t top_k, float temperature, const float* u,
                 int32_t* token_out, float* logits_out, float* lse_out, void* workspace, size_t ws_bytes,
                 void* stream);
+
+/* Tokens drawn from logits, every row with settings of its own.  Row b of logits
+ * (device [B][V] of `dtype`, rows `stride` elements apart) has the candidates whose
+ * logit is neither NaN nor -inf, with weights w_v = exp((l_v - l_max) / T),
+ * T = temperature[b] (NULL: 1); in the order (logit descending, id ascending)
+ *  - top_k[b] > 0 keeps the first top_k[b] (else, or top_k NULL: all);
+ *  - top_p[b] < 1 keeps those before which less than top_p[b] of the sum of the
+ *    weights that top_k leaves lies (NULL, >= 1 or NaN: all);
+ *  - min_p[b] > 0 keeps those with w_v >= min_p[b] (NULL, <= 0 or NaN: all);
+ *    the first candidate always stays.
+ * token_out[b] is the first kept id, in ascending order, at which the running sum of
+ * the kept weights exceeds u[b] times their sum (u: device fp32 [B] in [0, 1), drawn
+ * by the caller; NaN and values below count as 0, 1 and above as the largest number
+ * below 1).  logp_out[b] (device fp32, may be NULL): the natural logarithm of the
+ * probability with which that token was drawn.
+ *  - A temperature that is not at least 2^-60 (0, negative, NaN) is greedy: the
+ *    lowest id of the largest logit, logp 0.  Infinite T: equal weights.  Where the
+ *    largest logit is +inf only such logits have weight, all the same.  A logit whose
+ *    distance from the largest overflows fp32 has none.
+ *  - A row without candidates gives token -1 and logp -inf.
+ *  - Weights are held to 2^-33 of themselves, in units of 2^-42 of the largest
+ *    (smaller ones than half of that are zero), and added without rounding: the same
+ *    bits in every call.
+ *  - 1 <= B <= DDL_SAMPLE_MAX_ROWS, 1 <= V <= DDL_SAMPLE_MAX_VOCAB
+ *    (DDL_ERR_UNSUPPORTED above), stride >= V; logits aligned to its elements, the
+ *    others 4-byte aligned.  No workspace. */
+#define DDL_SAMPLE_MAX_ROWS 65536
+#define DDL_SAMPLE_MAX_VOCAB (1 << 20)
+int ddl_sample(const void* logits, ddl_dtype dtype, int64_t stride, int32_t B, int32_t V, const float* temperature,
+               const int32_t* top_k, const float* top_p, const float* min_p, const float* u, int32_t* token_out,
+               float* logp_out, void* stream);
 
 /* Launch mode of the decode calls: 0 = automatic (persistent cooperative
  * kernel when possible), 1 = one launch per fused stage. */

@@ -1,5 +1,5 @@
-// ddl_torch.cpp -- the per-layer calls of the 8-bit cache for torch tensors, as
-// a CPython module: argument checks and the call of the C entry point.
+// ddl_torch.cpp -- the per-layer calls of the 8-bit cache and the draw of the next
+// tokens for torch tensors, as a CPython module: argument checks and the call of the C entry point.
 //
 // A serving step makes these calls once a layer and their kernels take 3 us
 // and more, while the same checks in Python and a ctypes call took 5 to 9 us
@@ -123,6 +123,12 @@ int64_t rows_of(const at::Tensor& x, const char* name, int dev, int64_t heads, i
   return T > 1 ? x.stride(0) : heads * hd;
 }
 
+// Scores [R, H_kv, length], fp32.
+float* scores(const at::Tensor& t, const char* name, int dev, int64_t R, int64_t H) {
+  if (t.dim() != 3 || t.size(0) != R || t.size(1) != H) bad(std::string(name) + ": [R, H_kv, length]");
+  return (float*)data(t, name, at::kFloat, dev, -1);
+}
+
 // `device` current for the call, and the stream it goes to.
 struct On {
   std::optional<c10::cuda::CUDAGuard> guard;
@@ -220,9 +226,91 @@ PyObject* kv8_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// (pool, q, lse, kv_len, page_table, max_len, score, q_off, max_rows, decay, scale, softcap, window, slopes, bad,
+// stream); scale None: 1 / sqrt(head_dim)
+PyObject* kv8_score(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call([&]() -> int {
+    if (n != 16) bad("kv8_score: 16 arguments");
+    const Pool p = pool_of(a[0]);
+    const at::Tensor &q = tensor(a[1], "q"), &table = tensor(a[4], "page_table"), &score = tensor(a[6], "score");
+    if (q.dim() != 3 || table.dim() != 2) bad("q: [T, H_q, hd]; page_table: [R, pages_per_seq]");
+    const int64_t T = q.size(0), Hq = q.size(1), R = tensor(a[3], "kv_len").numel();
+    if (T > INT32_MAX || Hq > INT32_MAX || R > INT32_MAX || table.size(1) > INT32_MAX) bad("q: too large");
+    const int64_t qs = rows_of(q, "q", p.dev, Hq, p.hd, q.scalar_type(), T);
+    if (table.size(0) != R) bad("page_table: a row for each entry of kv_len");
+    ddl_attn_opts o;
+    o.scale = a[10] == Py_None ? 1.f / std::sqrt((float)p.hd) : number(a[10], "scale");
+    o.softcap = number(a[11], "softcap");
+    o.window = int32(a[12], "window");
+    o.slopes = f32_or_null(a[13], "slopes", p.dev, Hq);
+    const float* lse = f32_or_null(a[2], "lse", p.dev, T * Hq);
+    const int32_t *len = i32(a[3], "kv_len", p.dev, R), *tab = i32(a[4], "page_table", p.dev, -1);
+    const int32_t* off = i32_or_null(a[7], "q_off", p.dev, R + 1);
+    float* s = scores(score, "score", p.dev, R, p.H);
+    int32_t* flag = i32_or_null(a[14], "bad", p.dev, 1);
+    const int32_t max_len = int32(a[5], "max_len"), max_rows = int32(a[8], "max_rows");
+    const float decay = number(a[9], "decay");
+    On on(p.dev, a[15]);
+    return ddl_kv8_score(&p.kv, (int32_t)Hq, p.H, p.hd, (ddl_dtype)dtype_of(q), &o, (int32_t)R, (int32_t)T, max_rows,
+                         max_len, off, len, tab, (int32_t)table.size(1), q.data_ptr(), qs, lse, decay, s, score.size(2),
+                         flag, on.stream);
+  });
+}
+
+// (pool, score, kv_len, keep_len, page_table, new_table, max_len, kept, score_out, sinks, recent, bad, stream)
+PyObject* kv8_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call([&]() -> int {
+    if (n != 13) bad("kv8_evict: 13 arguments");
+    const Pool p = pool_of(a[0]);
+    const at::Tensor &score = tensor(a[1], "score"), &table = tensor(a[4], "page_table");
+    const at::Tensor &to = tensor(a[5], "new_table"), &kept = tensor(a[7], "kept"), &out = tensor(a[8], "score_out");
+    const int64_t R = tensor(a[2], "kv_len").numel();
+    if (table.dim() != 2 || table.size(0) != R || to.dim() != 2 || to.size(0) != R)
+      bad("page_table, new_table: a row for each entry of kv_len");
+    if (kept.dim() != 3 || kept.size(0) != R || kept.size(1) != p.H) bad("kept: [R, H_kv, max_keep]");
+    if (R > INT32_MAX || table.size(1) > INT32_MAX || to.size(1) > INT32_MAX || kept.size(2) > INT32_MAX)
+      bad("kv8_evict: too large");
+    const float* s = scores(score, "score", p.dev, R, p.H);
+    float* so = scores(out, "score_out", p.dev, R, p.H);
+    if (out.size(2) != score.size(2)) bad("score_out: as long as score");
+    const int32_t *len = i32(a[2], "kv_len", p.dev, R), *keep = i32(a[3], "keep_len", p.dev, R);
+    const int32_t *tab = i32(a[4], "page_table", p.dev, -1), *ntab = i32(a[5], "new_table", p.dev, -1);
+    int32_t* k = i32(a[7], "kept", p.dev, -1);
+    int32_t* flag = i32_or_null(a[11], "bad", p.dev, 1);
+    const int32_t max_len = int32(a[6], "max_len"), sinks = int32(a[9], "sinks"), recent = int32(a[10], "recent");
+    On on(p.dev, a[12]);
+    return ddl_kv8_evict(&p.kv, p.H, p.hd, (int32_t)R, max_len, s, score.size(2), len, keep, sinks, recent, tab,
+                         (int32_t)table.size(1), ntab, (int32_t)to.size(1), (int32_t)kept.size(2), k, so, flag, on.stream);
+  });
+}
+
+// (logits, u, temperature, top_k, top_p, min_p, tokens, logp, stream)
+PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call([&]() -> int {
+    if (n != 9) bad("sample: 9 arguments");
+    const at::Tensor& l = tensor(a[0], "logits");
+    if (l.dim() != 2 || dtype_of(l) < 0 || !l.is_cuda()) bad("logits: [B, V] fp32, bf16 or fp16 on a CUDA device");
+    const int64_t B = l.size(0), V = l.size(1);
+    if (B > INT32_MAX || V > INT32_MAX) bad("logits: too large");
+    if (V > 1 && l.stride(1) != 1) bad("logits: a row's entries are contiguous");
+    const int dev = (int)l.get_device();
+    const float *u = f32_or_null(a[1], "u", dev, B), *t = f32_or_null(a[2], "temperature", dev, B);
+    const int32_t* k = i32_or_null(a[3], "top_k", dev, B);
+    const float *p = f32_or_null(a[4], "top_p", dev, B), *m = f32_or_null(a[5], "min_p", dev, B);
+    int32_t* tok = i32(a[6], "tokens", dev, B);
+    float* lp = f32_or_null(a[7], "logp", dev, B);
+    On on(dev, a[8]);
+    return ddl_sample(l.data_ptr(), (ddl_dtype)dtype_of(l), B > 1 ? l.stride(0) : V, (int32_t)B, (int32_t)V, t, k, p, m, u,
+                      tok, lp, on.stream);
+  });
+}
+
 PyMethodDef methods[] = {{"page_plan", (PyCFunction)(void (*)(void))page_plan, METH_FASTCALL, nullptr},
                          {"kv8_append", (PyCFunction)(void (*)(void))kv8_append, METH_FASTCALL, nullptr},
                          {"kv8_attention", (PyCFunction)(void (*)(void))kv8_attention, METH_FASTCALL, nullptr},
+                         {"kv8_score", (PyCFunction)(void (*)(void))kv8_score, METH_FASTCALL, nullptr},
+                         {"kv8_evict", (PyCFunction)(void (*)(void))kv8_evict, METH_FASTCALL, nullptr},
+                         {"sample", (PyCFunction)(void (*)(void))sample, METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_ddl_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

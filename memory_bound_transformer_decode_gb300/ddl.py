@@ -31,7 +31,7 @@ EXPORTED = ("ddl_quantize_int4", "ddl_packed_layer_bytes", "ddl_pack_layer", "dd
             "ddl_head_workspace_bytes", "ddl_lm_head", "ddl_stack_decode_ragged",
             "ddl_stack_prefill", "ddl_stack_decode_paged", "ddl_stack_prefill_paged",
             "ddl_page_plan", "ddl_kv8_append", "ddl_kv8_attention_workspace_bytes", "ddl_kv8_attention",
-            "ddl_stack_kv8_workspace_bytes", "ddl_stack_step_kv8")
+            "ddl_stack_kv8_workspace_bytes", "ddl_stack_step_kv8", "ddl_kv8_score", "ddl_kv8_evict", "ddl_sample")
 
 
 class DDLError(RuntimeError):
@@ -157,6 +157,11 @@ def load(build_if_missing: bool = False):
         lib.ddl_stack_kv8_workspace_bytes.restype = sz
         lib.ddl_stack_step_kv8.argtypes = [P(Shape), ctypes.c_int, P(LayerW), P(KV8), i32, P(AttnOpts), i32, i32, i32,
                                            i32, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+        lib.ddl_kv8_score.argtypes = [P(KV8), i32, i32, i32, ctypes.c_int, P(AttnOpts), i32, i32, i32, i32, vp, vp, vp,
+                                      i32, vp, i64, vp, ctypes.c_float, vp, i64, vp, vp]
+        lib.ddl_kv8_evict.argtypes = [P(KV8), i32, i32, i32, i32, vp, i64, vp, vp, i32, i32, vp, i32, vp, i32, i32, vp,
+                                      vp, vp, vp]
+        lib.ddl_sample.argtypes = [vp, ctypes.c_int, i64, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp]
         for name in EXPORTED:
             if not hasattr(lib, name):
                 raise RuntimeError(f"{path} does not export {name}")
@@ -538,6 +543,36 @@ def ddl_kv8_attention(pool: tuple, q: torch.Tensor, kv_len: torch.Tensor, page_t
     return out
 
 
+def ddl_kv8_score(pool: tuple, q: torch.Tensor, lse: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor,
+                  max_len: int, score: torch.Tensor, *, q_off: torch.Tensor | None = None, max_rows: int = 1,
+                  decay: float = 1.0, scale: float | None = None, softcap: float = 0.0, window: int = 0,
+                  slopes: torch.Tensor | None = None, bad: torch.Tensor | None = None, stream=None) -> None:
+    """Attention weight that each cached token has drawn, per K/V head: score
+    (fp32 [R, H_kv, length], length >= max_len) times decay, plus the weights
+    of this call's rows, summed over rows and the group's heads; tokens of the
+    rows themselves begin at zero.  lse [T, H_q]: as ddl_kv8_attention returned
+    it for the same rows; other arguments as there."""
+    st = (_mod or _torch_module()).kv8_score(pool, q, lse, kv_len, page_table, max_len, score, q_off, max_rows, decay,
+                                             scale, softcap, window, slopes, bad, stream and stream.cuda_stream)
+    if st:
+        raise DDLError("ddl_kv8_score", st, _lib)
+
+
+def ddl_kv8_evict(pool: tuple, score: torch.Tensor, kv_len: torch.Tensor, keep_len: torch.Tensor,
+                  page_table: torch.Tensor, new_table: torch.Tensor, max_len: int, *, kept: torch.Tensor,
+                  score_out: torch.Tensor, sinks: int = 0, recent: int = 0, bad: torch.Tensor | None = None,
+                  stream=None) -> None:
+    """Cut every request with 0 <= keep_len < kv_len to keep_len tokens, each
+    K/V head by itself: the first `sinks`, the newest `recent` and the others
+    of the largest score [R, H_kv, length].  Their rows go, in order, to the
+    pages of new_table [R, new_pages_per_seq]; their indices to kept [R, H_kv,
+    max_keep] (int32), their scores to score_out (like score)."""
+    st = (_mod or _torch_module()).kv8_evict(pool, score, kv_len, keep_len, page_table, new_table, max_len, kept,
+                                             score_out, sinks, recent, bad, stream and stream.cuda_stream)
+    if st:
+        raise DDLError("ddl_kv8_evict", st, _lib)
+
+
 def _ptr_of(name: str, t, dtype, dev: int, shape):
     """Data pointer of a contiguous tensor of `dtype` and `shape` on CUDA device `dev` (None: NULL)."""
     if t is None:
@@ -667,4 +702,22 @@ def ddl_lm_head(D: int, V: int, wtype: int, head_packed: torch.Tensor, x: torch.
                                           _ptr(x), int(top_k), float(temperature), _ptr(u),
                                           _ptr(tokens), _ptr(logits), _ptr(lse), _ptr(workspace),
                                           workspace.numel(), _stream(stream)))
+    return tokens
+
+
+def ddl_sample(logits: torch.Tensor, u: torch.Tensor, *, temperature: torch.Tensor | None = None,
+               top_k: torch.Tensor | None = None, top_p: torch.Tensor | None = None,
+               min_p: torch.Tensor | None = None, tokens: torch.Tensor | None = None,
+               logp: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Token ids (int32 [B]) drawn from logits [B, V] (fp32, bf16 or fp16) with
+    the uniforms u (fp32 [B]), every row with its own temperature, top_p, min_p
+    (fp32 [B]) and top_k (int32 [B]); what is not given does not filter.  logp
+    (fp32 [B]) gets the log probabilities with which they were drawn."""
+    if tokens is None:  # made on the device and the stream that use it
+        with torch.cuda.device(logits.device), torch.cuda.stream(stream):
+            tokens = torch.empty(logits.shape[0], dtype=torch.int32, device=logits.device)
+    st = (_mod or _torch_module()).sample(logits, u, temperature, top_k, top_p, min_p, tokens, logp,
+                                          stream and stream.cuda_stream)
+    if st:
+        raise DDLError("ddl_sample", st, _lib)
     return tokens

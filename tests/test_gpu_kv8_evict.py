@@ -1,0 +1,211 @@
+"""Requests cut to their heaviest tokens (ddl_kv8_evict) against a 64-bit
+reference: which tokens stay, their codes and scales on the new pages, and what
+is left as it was."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import kv8_reference as ref
+import serving_reference as sref
+from memory_bound_transformer_decode_gb300 import ddl
+from test_gpu_kv8 import dev, make_pool
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    return ddl.load(build_if_missing=True)
+
+
+def tables(lens, keep, page, seed):
+    rng = np.random.RandomState(seed)
+    need = [max(0, -(-n // page)) for n in lens]
+    new = [-(-k // page) if 0 <= k < n else 0 for n, k in zip(lens, keep)]
+    pages = sum(need) + sum(new) + 3
+    ids = rng.permutation(pages)
+    a = np.full((len(lens), max(need) + 1), -9, np.int32)
+    b = np.full((len(lens), max(new + [1])), -9, np.int32)
+    at = 0
+    for r, n in enumerate(need):
+        a[r, :n] = ids[at:at + n]
+        at += n
+    for r, n in enumerate(new):
+        b[r, :n] = ids[at:at + n]
+        at += n
+    return a, b, pages
+
+
+def host(t):
+    return (t.view(torch.uint8) if t.element_size() == 1 else t).cpu().numpy()
+
+
+def check(lens, keep, H, hd, page, codes, sinks=0, recent=0, score=None, seed=0, max_keep=None, pool=None, table=None,
+          new_table=None, want_bad=0, max_len=None):
+    a, b, pages = tables(lens, keep, page, seed)
+    table, new_table = a if table is None else table, b if new_table is None else new_table
+    pool = make_pool(pages, H, page, hd, codes, seed) if pool is None else pool
+    R, most = len(lens), max(max(lens), 1) if max_len is None else max_len
+    g = torch.Generator(device="cuda").manual_seed(seed + 1)
+    if score is None:
+        score = torch.exp(3 * torch.randn((R, H, most + 3), generator=g, device="cuda"))
+        score[torch.rand(score.shape, generator=g, device="cuda") < 0.2] = 0.0
+    cut = [k for n, k in zip(lens, keep) if 0 <= k < n]
+    max_keep = max(cut + [1]) if max_keep is None else max_keep
+    kept = torch.full((R, H, max_keep), -3, dtype=torch.int32, device="cuda")
+    out = torch.full_like(score, -1.0)
+    bad = torch.zeros(1, dtype=torch.int32, device="cuda")
+    int8 = codes == "int8"
+    want = sref.evict([host(pool[0]), host(pool[1])], [host(pool[i]).astype(np.float64) for i in (2, 3)],
+                      score.cpu().numpy(), np.clip(lens, 0, most), [min(k, max_keep) if k < n else k for n, k in zip(lens, keep)],
+                      table, new_table, sinks, recent, page, int8, kept.cpu().numpy(), out.cpu().numpy())
+    ddl.ddl_kv8_evict(pool, score, dev(lens), dev(keep), dev(table), dev(new_table), most, kept=kept, score_out=out,
+                      sinks=sinks, recent=recent, bad=bad)
+    torch.cuda.synchronize()
+    assert int(bad) == want_bad
+    assert np.array_equal(kept.cpu().numpy(), want[2])
+    assert np.array_equal(out.cpu().numpy(), want[3], equal_nan=True)
+    for i in range(2):
+        sc = host(pool[i + 2]).astype(np.float64)
+        assert np.array_equal(sc, want[1][i], equal_nan=True)
+        x, y = ref.decode(host(pool[i]), int8), ref.decode(want[0][i], int8)
+        broken = np.isnan(sc).repeat(16, -1)[..., None]
+        assert np.array_equal(np.where(broken, 0, x), np.where(broken, 0, y), equal_nan=True)
+    return pool, kept, out
+
+
+@pytest.mark.parametrize("codes", ["e4m3", "int8"])
+@pytest.mark.parametrize("H,hd,page", [(1, 128, 16), (3, 64, 32), (2, 128, 256)])
+@pytest.mark.parametrize("sinks,recent", [(0, 0), (4, 16), (1, 33), (100, 7)])
+def test_cut(codes, H, hd, page, sinks, recent):
+    lens = [200, 17, 1, 64, 90]
+    keep = [77, 16, 0, 64, -1]
+    check(lens, keep, H, hd, page, codes, sinks, recent, seed=hd + sinks)
+
+
+@pytest.mark.parametrize("L,keep", [(2, 1), (16, 15), (17, 16), (33, 32), (513, 512), (700, 1), (1024, 1000), (5000, 2501)])
+def test_lengths(L, keep):
+    check([L, 3, 0], [keep, 1, 0], 2, 64, 64, "e4m3", 1, 5, seed=L)
+
+
+@pytest.mark.parametrize("kind", ["equal", "zeros", "nan", "inf", "negative", "tiny"])
+def test_scores(kind):
+    """Ties go to the lower index, NaN comes last, both zeros are one."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    s = torch.rand((2, 2, 300), generator=g, device="cuda")
+    hit = torch.rand(s.shape, generator=g, device="cuda") < 0.5
+    if kind == "equal":
+        s.fill_(0.5)
+    elif kind == "zeros":
+        s = torch.where(hit, 0.0, -0.0)
+    elif kind == "nan":
+        s[hit] = math.nan
+        s[1] = math.nan
+    elif kind == "inf":
+        s[hit] = math.inf
+        s[1][torch.rand((2, 300), generator=g, device="cuda") < 0.9] = -math.inf
+    elif kind == "negative":
+        s = torch.round(s * 20 - 10)
+    else:
+        s = s * 1e-44
+    check([300, 280], [101, 150], 2, 64, 16, "int8", 3, 9, score=s)
+
+
+def test_a_long_request():
+    """Past the keys that fit shared memory."""
+    check([60000], [700], 1, 64, 256, "e4m3", 4, 20)
+
+
+def test_extreme_scales():
+    pool = make_pool(40, 1, 16, 64, "e4m3", 3)
+    for i in (2, 3):
+        e = torch.randint(-126, 115, pool[i].shape, device="cuda", generator=torch.Generator(device="cuda").manual_seed(i))
+        pool[i].copy_(torch.exp2(e.float()))
+        pool[i][::5] = 0.0
+        pool[i][1::5] *= 1.37
+    a, b, _ = tables([200, 150], [90, 60], 16, 5)
+    check([200, 150], [90, 60], 1, 64, 16, "e4m3", pool=pool, table=a, new_table=b, seed=5)
+
+
+def test_nan_codes_and_broken_scales():
+    pool = make_pool(60, 2, 16, 128, "e4m3", 4, junk=True)
+    a, b, _ = tables([200, 150], [90, 60], 16, 6)
+    pool[2][a[0, 3], 1] = math.inf
+    pool[3][a[1, 2], 0] = -1.0
+    pool[2][a[1, 5], 0] = math.nan
+    check([200, 150], [90, 60], 2, 128, 16, "e4m3", pool=pool, table=a, new_table=b, seed=6)
+
+
+def test_outside_the_bounds():
+    a, b, pages = tables([100, 80], [40, 30], 16, 7)
+    holes = a.copy()
+    holes[0, 2] = -1
+    holes[1, 0] = pages + 4
+    check([100, 80], [40, 30], 2, 64, 16, "int8", seed=7, table=holes, new_table=b, want_bad=1)
+    lost = b.copy()
+    lost[0, 1] = pages
+    check([100, 80], [40, 30], 2, 64, 16, "int8", seed=7, table=a, new_table=lost, want_bad=1)
+    check([100, 80], [40, 30], 2, 64, 16, "int8", seed=7, max_keep=25, want_bad=1)
+    check([100, 80], [40, 30], 2, 64, 16, "int8", seed=7, max_len=96, want_bad=1)  # kv_len past max_len
+
+
+def test_shared_pages_are_left_alone_and_a_cut_request_attends_as_before():
+    """Two requests on one prefix, one of them cut: the other's attention keeps its bits, and the cut one's
+    attention equals that over its kept tokens."""
+    H, hd, page = 2, 64, 16
+    pool = make_pool(30, H, page, hd, "e4m3", 8)
+    for i in (2, 3):
+        pool[i].fill_(2.0 ** -8)
+    table = np.array([[3, 9, 4, 7], [3, 9, 12, -1]], np.int32)
+    lens, keep = [60, 41], [-1, 20]
+    q = torch.randn((2, H * 4, hd), device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)).bfloat16()
+    before = ddl.ddl_kv8_attention(pool, q, dev(lens), dev(table), 64)
+    score = torch.rand((2, H, 64), device="cuda")
+    new = np.array([[-1, -1, -1, -1], [20, 21, -1, -1]], np.int32)
+    kept = torch.zeros((2, H, 20), dtype=torch.int32, device="cuda")
+    ddl.ddl_kv8_evict(pool, score, dev(lens), dev(keep), dev(table), dev(new), 64, kept=kept,
+                      score_out=torch.zeros_like(score), sinks=2, recent=4)
+    after = ddl.ddl_kv8_attention(pool, q, dev([60, 20]), dev([table[0].tolist(), new[1].tolist()]), 64)
+    assert torch.equal(before[0], after[0])
+    full = [ref.gather(pool[i], pool[i + 2], table[1, :3].tolist(), 41) for i in (0, 1)]
+    for h in range(H):
+        k, v = (x[h][kept[1, h].long()] for x in full)
+        w = torch.softmax(q[1, 4 * h:4 * h + 4].double() @ k.T * hd ** -0.5, -1) @ v
+        # (e4m3 codes move to the new scale exactly; bf16 outputs: half a step, and weights to 2^-11)
+        assert float((after[1, 4 * h:4 * h + 4].double() - w).abs().max()) <= float(w.abs().max()) * (2 ** -8 + 2 ** -10)
+
+
+def test_replayed_with_other_lengths():
+    H, hd, page = 2, 128, 16
+    lens, keep = [100, 90], [50, 40]
+    a, b, pages = tables([128, 128], [64, 64], page, 1)
+    pool = make_pool(pages, H, page, hd, "int8", 1)
+    kv_len, keep_len, tab, new = dev(lens), dev(keep), dev(a), dev(b)
+    score = torch.rand((2, H, 128), device="cuda")
+    kept = torch.full((2, H, 64), -1, dtype=torch.int32, device="cuda")
+    out = torch.zeros_like(score)
+
+    def call():
+        ddl.ddl_kv8_evict(pool, score, kv_len, keep_len, tab, new, 128, kept=kept, score_out=out, sinks=1, recent=8)
+
+    call()
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        call()
+    kv_len.copy_(dev([128, 33]))
+    keep_len.copy_(dev([64, 33]))
+    score.copy_(torch.rand_like(score))
+    kept.fill_(-1)
+    out.zero_()
+    before = [t.clone() for t in pool]
+    want = sref.evict([host(before[0]), host(before[1])], [host(before[i]).astype(np.float64) for i in (2, 3)],
+                      score.cpu().numpy(), [128, 33], [64, 33], a, b, 1, 8, page, True, kept.cpu().numpy(), out.cpu().numpy())
+    graph.replay()
+    torch.cuda.synchronize()
+    assert np.array_equal(kept.cpu().numpy(), want[2]) and np.array_equal(out.cpu().numpy(), want[3])
+    for i in range(2):
+        assert np.array_equal(host(pool[i]), want[0][i]) and np.array_equal(host(pool[i + 2]), want[1][i])
