@@ -594,9 +594,8 @@ int ddl_lm_head(int32_t D, int64_t V, ddl_wtype wtype, const void* head_packed, 
  *    largest logit is +inf only such logits have weight, all the same.  A logit whose
  *    distance from the largest overflows fp32 has none.
  *  - A row without candidates gives token -1 and logp -inf.
- *  - Weights are held to 2^-33 of themselves, in units of 2^-42 of the largest
- *    (smaller ones than half of that are zero), and added without rounding: the same
- *    bits in every call.
+ *  - Weights are held to 2^-33 of themselves and 2^-43 of the largest (smaller ones are
+ *    zero), and added without rounding: the same bits in every call.
  *  - 1 <= B <= DDL_SAMPLE_MAX_ROWS, 1 <= V <= DDL_SAMPLE_MAX_VOCAB
  *    (DDL_ERR_UNSUPPORTED above), stride >= V; logits aligned to its elements, the
  *    others 4-byte aligned.  No workspace. */

@@ -9,22 +9,24 @@
 // Every filter keeps a head of one order, so what the filters decide is one element,
 // the last that stays; no sort is needed, and the draw in id order needs sums only.
 //
-// Weights are integers, rn(w 2^42), and so are their sums: neither the order of
+// Weights are integers in units of 2^-43, and so are their sums: neither the order of
 // additions nor the split over CTAs changes a bit.  An fp32 exponential would be
 // wrong by 2^-23 of a weight, and a draw over V tokens meets a border within d of
-// its number about V d of the time; so w comes from a table of 2^(i/256) with 2^42
-// as its unit and a cubic in fp32 for the remaining factor of less than 2^(1/512), its
-// argument in two floats: 2^-33 of w.  (Double precision: 152 SMs do 2 operations
-// a clock each; 64 rows of 152064 would take 160 us.)
+// its number about V d of the time; so w comes from a table of 2^(i/64) and a cubic for
+// the remaining factor of less than 2^(1/128), argument, table and product in two
+// floats each: 2^-33 of w before it is rounded to the unit.  Adding 6 and 1.5 2^-20
+// rounds the two parts to multiples of 2^-21 and 2^-43, which then lie in the low bits:
+// integers without a conversion.  (Double precision: 152 SMs do 2 operations a clock
+// each; 64 rows of 152064 would take 160 us.)
 //
 // A cluster of 1 to 16 CTAs takes a row; a warp a contiguous run of ids.
 //  1. The maximum (greedy rows end here).
 //  2. Rows with top-k or top-p: a histogram of log2 w in 2048 bins of 1/47.6 octave:
 //     how many elements, and the sum of their places inside the bin, which bounds the
-//     bin's sum of weights to 2^-12.  Where the k-th element and the end of the top-p
+//     bin's sum of weights to 2^-13.  Where the k-th element and the end of the top-p
 //     head may lie is then known to a bin or two.
-//  3. Weights, exact: sums per warp of what certainly stays; the elements of the open
-//     bins go to a list.
+//  3. Weights: sums per warp of what certainly stays; the elements of the open bins go
+//     to a list.
 //  4. The list decides both borders (radix select by number, then by sum of weights,
 //     ties by id), in one CTA.  Lists that overflow (all logits alike, say) are
 //     replaced by the row itself: the same selection by the whole cluster.
@@ -43,35 +45,38 @@ constexpr int SM_THREADS = 512, SM_WARPS = SM_THREADS / 32;
 constexpr int SM_MAX_CLUSTER = 16;
 constexpr int SM_BINS = 2048;
 constexpr float SM_PER_OCTAVE = 47.6f;       // 2048 bins over 43 octaves
-constexpr float SM_OCTAVES = 43.f;           // weights below 2^-43 are 0
-constexpr int SM_UNIT = 42;                  // weights are multiples of 2^-42; 2^20 of them fit 62 bits
+constexpr float SM_OCTAVES = 43.f;           // weights below 2^-43 are 0; 2^20 of them up to 1 + 2^-30 fit 64 bits
 constexpr int SM_FRAC = 1024;                // places inside a bin
 constexpr int SM_LIST = 4096;                // elements of a CTA's list, and of the row's
+constexpr uint32_t SM_ALL_IDS = 0xfffffu;
 static_assert(DDL_SAMPLE_MAX_VOCAB <= 1 << 20, "sums of weights, ids in 20 bits of a list entry");
 
-// 2^(i/256) in units of 2^-42: by repeated square roots of 2 (Newton), multiplied up, in double.
+// 2^(i/64) as two floats: by repeated square roots of 2 (Newton), multiplied up, in double.
 struct ExpTable {
-  unsigned long long v[256];
+  float hi[64], lo[64];
 };
 constexpr ExpTable make_exp_table() {
-  double root[8] = {};
+  double root[6] = {};
   double x = 2.0;
-  for (int k = 0; k < 8; ++k) {  // root[k] = 2^(1 / 2^(k + 1))
+  for (int k = 0; k < 6; ++k) {  // root[k] = 2^(1 / 2^(k + 1))
     double y = x;
     for (int n = 0; n < 60; ++n) y = 0.5 * (y + x / y);
     root[k] = y;
     x = y;
   }
   ExpTable t = {};
-  for (int i = 0; i < 256; ++i) {
+  for (int i = 0; i < 64; ++i) {
     double p = 1.0;
-    for (int k = 0; k < 8; ++k)
-      if (i & (128 >> k)) p *= root[k];
-    t.v[i] = (unsigned long long)(p * 4398046511104.0 + 0.5);
+    for (int k = 0; k < 6; ++k)
+      if (i & (32 >> k)) p *= root[k];
+    t.hi[i] = (float)p;
+    t.lo[i] = i ? (float)(p - (double)(float)p) : 0x1p-60f;  // (never zero: its exponent is changed by addition)
   }
   return t;
 }
 __device__ const ExpTable g_exp_table = make_exp_table();
+
+constexpr float LOG2E_HI = 1.44269502162933349609375f, LOG2E_LO = 1.92596299e-8f;  // log2 e
 
 struct SampleArgs {
   const void* logits;
@@ -89,7 +94,7 @@ struct Entry {
 
 // The shared memory of a CTA that others of its cluster read, and its own.
 struct SampleSmem {
-  unsigned long long table[256];
+  ExpTable table;
   union {
     struct {
       uint32_t count[SM_BINS], place[SM_BINS];    // histogram of the CTA's elements
@@ -100,13 +105,15 @@ struct SampleSmem {
   unsigned long long warp_sum[SM_WARPS];      // per warp: weights that certainly stay
   unsigned long long sums[2];                 // weights above the open bins, and between them and the k-th element's
   unsigned long long chunk[SM_MAX_CLUSTER * SM_WARPS];
-  unsigned long long mass[256];
-  uint32_t num[256];
+  uint32_t num[256], mass_lo[256], mass_hi[256];  // a digit's elements and their weights
+  uint32_t range[2];
+  unsigned long long red64b[SM_WARPS];
   unsigned long long red64[SM_WARPS];
   float redf[SM_WARPS], redg[SM_WARPS];
   uint32_t redu[SM_WARPS];
   float top;
-  int32_t top_id;
+  uint32_t top_id;
+  double log_m;
   uint32_t list_n;
   struct {
     uint32_t key, id;          // the last element that stays
@@ -142,30 +149,58 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
 // The weights of a row.
 struct Weigher {
   float top, ch, cl;  // log2 e / T in two floats
-  const unsigned long long* table;
-  // log2 of the weight, rounded: not increasing with falling logits.  NaN for what is no candidate.
-  __device__ __forceinline__ float log2w(float l) const { return l == top ? 0.f : (l - top) * ch; }
-  // the weight in units of 2^-42; p = log2w(l) > -43
-  __device__ __forceinline__ unsigned long long weight(float l, float p) const {
-    if (l == top) return 1ull << SM_UNIT;
-    // l - top = d + e exactly
+  bool inf;           // the row's largest logit is +inf: such logits count as 0, all others as none
+  const ExpTable* table;
+  template <int N>
+  __device__ __forceinline__ void fix(float (&l)[N]) const {
+    if (inf) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) l[i] = l[i] == INFINITY ? 0.f : -INFINITY;
+    }
+  }
+  // log2 of the weight, rounded: not increasing with falling logits.  Not above -43 (or NaN): no weight.
+  __device__ __forceinline__ float log2w(float l) const { return (l - top) * ch; }
+  static __device__ __forceinline__ bool has(float p) { return p > -SM_OCTAVES; }
+  // The weight, as 2^22 hi + lo units of 2^-43; p = log2w(l) (not above -43: of no meaning).
+  __device__ __forceinline__ void parts(float l, float p, uint32_t& hi, int32_t& low) const {
+    // l - top = d + e exactly, log2 of the weight p + lo
     const float d = l - top, b = d - l, e = (l - (d - b)) + (-top - b);
     const float lo = fmaf(d, ch, -p) + fmaf(d, cl, e * ch);
-    const float k = rintf(p * 256.f);
-    const float r = fmaf(-k, 0x1p-8f, p) + lo;  // p = k / 256 + r
-    const int ki = (int)k;
-    const unsigned long long t = table[ki & 255];
-    const float z = r * 0.693147180559945f;
-    const float q = z * fmaf(z, fmaf(z, 0.16666667f, 0.5f), 1.f);  // 2^r - 1
-    const float tq = __uint2float_rn((uint32_t)(t >> 11)) * q;      // of t in units of 2^-31, in [2^31, 2^32)
-    const long long w = (long long)t + ((long long)__float2int_rn(tq * 0x1p7f) << 4);
-    const int s = -(ki >> 8);
-    return ((unsigned long long)w + ((1ull << s) >> 1)) >> s;
+    const float m = fmaf(p, 64.f, 0x1.8p23f);  // (rounds 64 p to an integer k in the low bits)
+    const uint32_t k = __float_as_uint(m);
+    const float r = fmaf(0x1.8p23f - m, 0x1p-6f, p);  // p = k / 64 + r, exactly
+    const uint32_t n = k >> 6 << 23;                  // whole octaves, as an exponent
+    const float th = __uint_as_float(__float_as_uint(table->hi[k & 63]) + n);
+    const float tl = __uint_as_float(__float_as_uint(table->lo[k & 63]) + n);
+    // 2^(r + lo) = 1 + z + t, z a float
+    constexpr float LN2F = 0.693147180559945f;
+    const float z = r * LN2F;
+    const float zl = fmaf(lo, LN2F, fmaf(r, LN2F, -z));
+    const float t = fmaf(z * z, fmaf(z, 0.16666667f, 0.5f), fmaf(zl, z, zl));
+    // (th + tl) (1 + z + t) = wh + wl
+    const float x = th * z, wh = th + x;
+    const float wl = (x - (wh - th)) + (fmaf(th, z, -x) + fmaf(th, t, fmaf(tl, z, tl)));
+    const float ah = (wh + wl) + 6.f, al = ((wh - (ah - 6.f)) + wl) + 0x1.8p-20f;
+    hi = __float_as_uint(ah) - 0x40c00000u;
+    low = (int32_t)(__float_as_uint(al) - 0x35c00000u);
   }
+  static __device__ __forceinline__ unsigned long long units(uint32_t h, int32_t s) {
+    return ((unsigned long long)h << 22) + (long long)s;
+  }
+  __device__ __forceinline__ unsigned long long weight(float l) const {
+    const float p = log2w(l);
+    uint32_t h;
+    int32_t s;
+    parts(l, p, h, s);
+    return has(p) ? units(h, s) : 0ull;
+  }
+  // log2 w = p to bins, from the top: the nearest integer to 47.6 |p|, as the low bits of a float
+  static __device__ __forceinline__ float bin_bits(float p) { return fmaf(p, -SM_PER_OCTAVE, 0x1p23f); }
+  static __device__ __forceinline__ int bin_of(float p) { return (int)(__float_as_uint(bin_bits(p)) - 0x4b000000u); }
 };
 
-// The elements of a warp's run: f(id, logit) for ids in ascending order within a lane,
-// 16 bytes a lane and load; the row's ends and unaligned rows element by element.
+// The elements of a warp's run: f(id of the first, logits) for 16 bytes a lane, in ascending
+// order within a lane; the row's ends and unaligned rows element by element (-inf outside).
 template <int DT>
 struct Row {
   static constexpr int VEC = DT == DDL_T_F32 ? 4 : 8;
@@ -187,46 +222,54 @@ struct Row {
     if (DT == DDL_T_BF16) return bf16_bits_to_f32(x);
     return __half2float(__ushort_as_half(x));
   }
-  __device__ __forceinline__ bool whole(int v) const { return v * VEC >= off && (int64_t)(v + 1) * VEC <= (int64_t)V + off; }
-  __device__ __forceinline__ uint4 load(int v, int end) const {
-    if (v < end && whole(v)) return *reinterpret_cast<const uint4*>(base + (int64_t)v * 16);
-    return make_uint4(0u, 0u, 0u, 0u);
-  }
-  __device__ __forceinline__ void values(int v, const uint4& x, float (&l)[VEC]) const {
-    if (whole(v)) {
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  static __device__ __forceinline__ void unpack(const uint4& x, float (&l)[VEC]) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        if (DT == DDL_T_F32) l[i] = __uint_as_float(w[i & 3]);
-        else if (DT == DDL_T_BF16) l[i] = i & 1 ? bf16hi_f32(w[i / 2]) : bf16lo_f32(w[i / 2]);
-        else {
-          const __half2 h2 = *reinterpret_cast<const __half2*>(&w[i / 2]);
-          l[i] = i & 1 ? __high2float(h2) : __low2float(h2);
-        }
+    for (int i = 0; i < VEC; ++i) {
+      if (DT == DDL_T_F32) l[i] = __uint_as_float(w[i & 3]);
+      else if (DT == DDL_T_BF16) l[i] = i & 1 ? bf16hi_f32(w[i / 2]) : bf16lo_f32(w[i / 2]);
+      else {
+        const __half2 h2 = *reinterpret_cast<const __half2*>(&w[i / 2]);
+        l[i] = i & 1 ? __high2float(h2) : __low2float(h2);
       }
+    }
+  }
+  __device__ __forceinline__ uint4 load(int v) const { return *reinterpret_cast<const uint4*>(base + (int64_t)v * 16); }
+  // The logits of vector v, -inf from v1 on and outside the row.
+  __device__ __forceinline__ void values(int v, int v1, float (&l)[VEC]) const {
+    if (v < v1 && v * VEC >= off && (int64_t)(v + 1) * VEC <= (int64_t)V + off) {
+      unpack(load(v), l);
     } else {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
         const int64_t q = (int64_t)v * VEC + i;
-        l[i] = q >= off && q < (int64_t)V + off ? one(q) : -INFINITY;
+        l[i] = v < v1 && q >= off && q < (int64_t)V + off ? one(q) : -INFINITY;
       }
     }
   }
+  // All lanes of the warp take part in every f.
   template <class F>
   __device__ __forceinline__ void each(int v0, int v1, F&& f) const {
     constexpr int U = 4;  // loads on their way
-    const int lane = threadIdx.x & 31;
-    for (int v = v0 + lane; v < v1; v += 32 * U) {
-      uint4 x[U];
+    const int lane = threadIdx.x & 31, w0 = off > 0 ? 1 : 0, w1 = min(v1, (V + off) / VEC);  // whole: [w0, w1)
+    for (int v = v0; v < v1; v += 32 * U) {
+      if (v >= w0 && v + 32 * U <= w1) {
+        uint4 x[U];
 #pragma unroll
-      for (int j = 0; j < U; ++j) x[j] = load(v + 32 * j, v1);
+        for (int j = 0; j < U; ++j) x[j] = load(v + 32 * j + lane);
 #pragma unroll
-      for (int j = 0; j < U; ++j) {
-        if (v + 32 * j >= v1) break;
-        float l[VEC];
-        values(v + 32 * j, x[j], l);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) f((v + 32 * j) * VEC + i - off, l[i]);
+        for (int j = 0; j < U; ++j) {
+          float l[VEC];
+          unpack(x[j], l);
+          f((v + 32 * j + lane) * VEC - off, l);
+        }
+      } else {
+#pragma unroll 1
+        for (int j = v; j < min(v + 32 * U, v1); j += 32) {
+          float l[VEC];
+          values(j + lane, v1, l);
+          f((j + lane) * VEC - off, l);
+        }
       }
     }
   }
@@ -236,6 +279,15 @@ __device__ __forceinline__ unsigned long long warp_add(unsigned long long x) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(FULL, x, o);
   return x;
+}
+// Sum of a word of every CTA of the cluster (all lanes of a warp call it; C <= 32).
+__device__ __forceinline__ uint32_t cluster_add(const uint32_t* p, int C) {
+  const int lane = threadIdx.x & 31;
+  return __reduce_add_sync(FULL, lane < C ? ldu_cluster(cluster_addr(smem_addr(p), lane)) : 0u);
+}
+__device__ __forceinline__ unsigned long long cluster_add(const unsigned long long* p, int C) {
+  const int lane = threadIdx.x & 31;
+  return warp_add(lane < C ? ldl_cluster(cluster_addr(smem_addr(p), lane)) : 0ull);
 }
 // Exclusive sum over the CTA of a value per thread; `all` gets the sum of all.
 template <class T>
@@ -260,122 +312,193 @@ __device__ __forceinline__ T block_before(T x, T* ws, T& all) {
   return before + inc - x;
 }
 
+// Sum of 64 bits in shared memory by two 32-bit additions (lo's old value tells its carry).
+__device__ __forceinline__ void add64(uint32_t* lo, uint32_t* hi, unsigned long long x) {
+  const uint32_t l = (uint32_t)x, was = atomicAdd(lo, l), h = (uint32_t)(x >> 32) + (was + l < was ? 1u : 0u);
+  if (h) atomicAdd(hi, h);
+}
+
 // Where the elements of a selection come from: a list in this CTA's shared memory, or the
 // whole cluster's runs of the row (which of them: in()).
 template <int DT, bool LIST>
 struct Source {
   SampleSmem& S;
-  const Entry* list;
   int n;
   const Row<DT>& row;
   const Weigher& W;
   int v0, v1, C;
+  __device__ __forceinline__ void sync() const {
+    if (LIST) __syncthreads();
+    else cluster_sync();
+  }
+  __device__ __forceinline__ uint32_t all(uint32_t* p) const {  // a word's sum over the CTAs
+    if (LIST) return *p;
+    uint32_t s = 0;
+    for (int c = 0; c < C; ++c) s += ldu_cluster(cluster_addr(smem_addr(p), c));
+    return s;
+  }
   // f(key, id) for every element
   template <class F>
   __device__ __forceinline__ void each(F&& f) const {
     if (LIST) {
-      for (int i = threadIdx.x; i < n; i += SM_THREADS) f(list[i].key, list[i].id & 0xfffffu);
+      for (int i = threadIdx.x; i < n; i += SM_THREADS) f(S.all[i].key, S.all[i].id & SM_ALL_IDS);
     } else {
-      row.each(v0, v1, [&](int id, float l) {
-        if (W.log2w(l) > -SM_OCTAVES) f(logit_key(l), (uint32_t)id);
+      row.each(v0, v1, [&](int id, float(&l)[Row<DT>::VEC]) {
+        W.fix(l);
+#pragma unroll
+        for (int i = 0; i < Row<DT>::VEC; ++i)
+          if (W.has(W.log2w(l[i]))) f(logit_key(l[i]), (uint32_t)(id + i));
       });
     }
   }
-  // The counts and sums of digit threadIdx.x, of all CTAs.
-  __device__ __forceinline__ void gather(uint32_t& num, unsigned long long& mass) const {
-    const int i = threadIdx.x;
-    num = 0;
-    mass = 0;
-    if (LIST) {
-      __syncthreads();
-      if (i < 256) {
-        num = S.num[i];
-        mass = S.mass[i];
-      }
-    } else {
-      cluster_sync();
-      if (i < 256)
-        for (int c = 0; c < C; ++c) {
-          num += ldu_cluster(cluster_addr(smem_addr(&S.num[i]), c));
-          mass += ldl_cluster(cluster_addr(smem_addr(&S.mass[i]), c));
-        }
-      cluster_sync();  // (before they are cleared)
-    }
-  }
-  // The digit, from the top, in which the running number (BY_MASS: sum of weights) reaches `want`; what
-  // lies before it is taken off `want`, the number of elements in it is left in `inside`.
-  template <bool BY_MASS, bool DOWN, class F>
-  __device__ __forceinline__ uint32_t digit(F&& classify, unsigned long long& want, uint32_t& inside) const {
-    __syncthreads();
-    for (int i = threadIdx.x; i < 256; i += SM_THREADS) {
-      S.num[i] = 0;
-      S.mass[i] = 0;
-    }
+  // One digit of 256: the first, in ascending order, at which the running number of the elements (BY_MASS: of
+  // their weights) reaches `want`; what lies before it is taken off `want`, the number of elements in it is left in
+  // `inside`.  classify: an element's digit, or -1.
+  template <bool BY_MASS, class F>
+  __device__ __forceinline__ int digit(F&& classify, unsigned long long& want, uint32_t& inside) const {
+    const int tid = threadIdx.x, lane = tid & 31;
+    if (tid < 256) S.num[tid] = S.mass_lo[tid] = S.mass_hi[tid] = 0;
     __syncthreads();
     each([&](uint32_t key, uint32_t id) {
       const int d = classify(key, id);
       if (d < 0) return;
       atomicAdd(&S.num[d], 1u);
-      if (BY_MASS) {
-        const float l = key_logit(key);
-        atomicAdd(&S.mass[d], W.weight(l, W.log2w(l)));
-      }
+      if (BY_MASS) add64(&S.mass_lo[d], &S.mass_hi[d], W.weight(key_logit(key)));
     });
-    uint32_t num;
-    unsigned long long mass;
-    gather(num, mass);
-    // place x of the order holds digit 255 - x (DOWN) or x: back through shared memory
-    __syncthreads();
-    if (threadIdx.x < 256) {
-      S.num[threadIdx.x] = num;
-      S.mass[threadIdx.x] = mass;
+    sync();
+    if (tid < 32) {  // eight digits a lane
+      uint32_t num[8];
+      unsigned long long mine[8], sum = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        num[j] = all(&S.num[lane * 8 + j]);
+        mine[j] = num[j];
+        if (BY_MASS) {
+          if (LIST) {
+            mine[j] = S.mass_lo[lane * 8 + j] + ((unsigned long long)S.mass_hi[lane * 8 + j] << 32);
+          } else {
+            mine[j] = 0;
+            for (int c = 0; c < C; ++c)
+              mine[j] += ldu_cluster(cluster_addr(smem_addr(&S.mass_lo[lane * 8 + j]), c)) +
+                         ((unsigned long long)ldu_cluster(cluster_addr(smem_addr(&S.mass_hi[lane * 8 + j]), c)) << 32);
+          }
+        }
+        sum += mine[j];
+      }
+      unsigned long long inc = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long y = __shfl_up_sync(FULL, inc, o);
+        if (lane >= o) inc += y;
+      }
+      const unsigned long long total = __shfl_sync(FULL, inc, 31);
+      if (want > total) want = total;  // (never, by the bounds of the bins)
+      unsigned long long before = inc - sum;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (before < want && before + mine[j] >= want) {
+          S.sel_i[0] = lane * 8 + j;
+          S.sel_i[1] = (int)num[j];
+          S.sel_u[0] = want - before;
+        }
+        before += mine[j];
+      }
     }
-    __syncthreads();
-    const int x = DOWN ? 255 - threadIdx.x : threadIdx.x;
-    num = threadIdx.x < 256 ? S.num[x] : 0u;
-    unsigned long long mine = threadIdx.x < 256 ? (BY_MASS ? S.mass[x] : (unsigned long long)num) : 0ull, all;
-    const unsigned long long before = block_before(mine, S.red64, all);
-    if (want > all) want = all;  // (never, by the bounds of the bins)
-    if (threadIdx.x == 0) {
-      S.sel_i[0] = S.sel_i[1] = 0;
-      S.sel_u[0] = 1;
-    }
-    __syncthreads();
-    if (threadIdx.x < 256 && num && before < want && before + mine >= want) {
-      S.sel_i[0] = x;
-      S.sel_i[1] = (int)num;
-      S.sel_u[0] = want - before;
-    }
-    __syncthreads();
+    sync();  // (the cluster's numbers are read before they are cleared)
     const int d = S.sel_i[0];
     inside = (uint32_t)S.sel_i[1];
     want = S.sel_u[0];
-    return (uint32_t)d;
+    return d;
   }
   // The last element that stays of those `in` accepts: the `want`-th (BY_MASS: the first at which
-  // the running sum of weights reaches `want`), in the order (key descending, id ascending).
+  // the running sum of weights reaches `want`), in the order (key descending, id ascending); id
+  // SM_ALL_IDS where all accepted ones of its key stay.
   template <bool BY_MASS, class F>
   __device__ __forceinline__ Entry select(F&& in, unsigned long long want) const {
-    Entry e = {0u, 0u};
-    uint32_t inside = 0;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      const uint32_t hi = shift == 24 ? 0u : ~0u << (shift + 8);
-      e.key |= digit<BY_MASS, true>(
-                   [&](uint32_t key, uint32_t id) {
-                     return in(key, id) && ((key ^ e.key) & hi) == 0 ? (int)((key >> shift) & 255u) : -1;
-                   },
-                   want, inside)
-               << shift;
+    // the range of keys: what its numbers share needs no digit
+    uint32_t top = 0u, low = ~0u;
+    each([&](uint32_t key, uint32_t id) {
+      if (in(key, id)) {
+        top = max(top, key);
+        low = min(low, key);
+      }
+    });
+    top = __reduce_max_sync(FULL, top);
+    low = __reduce_min_sync(FULL, low);
+    __syncthreads();  // (earlier readers of these words)
+    if (threadIdx.x == 0) {
+      S.range[0] = 0u;
+      S.range[1] = ~0u;
+    }
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) {
+      atomicMax(&S.range[0], top);
+      atomicMin(&S.range[1], low);
+    }
+    sync();
+    top = S.range[0];
+    low = S.range[1];
+    if (!LIST) {
+      for (int c = 0; c < C; ++c) {
+        top = max(top, ldu_cluster(cluster_addr(smem_addr(&S.range[0]), c)));
+        low = min(low, ldu_cluster(cluster_addr(smem_addr(&S.range[1]), c)));
+      }
+    }
+    sync();
+    // digits of top - key, ascending
+    Entry e = {top, SM_ALL_IDS};
+    uint32_t inside = 0, at = 0;  // top - key of the element sought, its digits so far
+    int bits = top > low ? 32 - __clz(top - low) : 0;
+    bool first = true;
+    while (bits > 0) {
+      const int shift = bits > 8 ? bits - 8 : 0;
+      at |= (uint32_t)digit<BY_MASS>(
+                [&](uint32_t key, uint32_t id) {
+                  const uint32_t x = top - key;
+                  return in(key, id) && (first || (x ^ at) >> bits == 0) ? (int)((x >> shift) & 255u) : -1;
+                },
+                want, inside)
+            << shift;
+      bits = shift;
+      first = false;
+      if (inside == 1 && bits > 0) break;  // one element left: its key is in range below
+    }
+    if (bits > 0) {  // the element's own key
+      if (threadIdx.x == 0) S.range[1] = ~0u;
+      sync();
+      each([&](uint32_t key, uint32_t id) {
+        const uint32_t x = top - key;
+        if (in(key, id) && (x ^ at) >> bits == 0) S.range[1] = x;
+      });
+      sync();
+      at = S.range[1];
+      if (!LIST)
+        for (int c = 0; c < C; ++c) at = min(at, ldu_cluster(cluster_addr(smem_addr(&S.range[1]), c)));
+      sync();
+      e.key = top - at;
+      return e;  // (no other has its key)
+    }
+    e.key = top - at;
+    if (first) {  // all keys are one
+      uint32_t n = 0;
+      each([&](uint32_t key, uint32_t id) { n += in(key, id); });
+      n = __reduce_add_sync(FULL, n);
+      if (threadIdx.x == 0) S.range[0] = 0u;
+      __syncthreads();
+      if ((threadIdx.x & 31) == 0) atomicAdd(&S.range[0], n);
+      sync();
+      inside = all(&S.range[0]);
+      sync();
     }
     if (BY_MASS) {  // elements of one key weigh the same
-      const float l = key_logit(e.key);
-      const unsigned long long w = W.weight(l, W.log2w(l));
+      const unsigned long long w = W.weight(key_logit(e.key));
       want = w ? (want + w - 1) / w : 1;
-      want = want < inside ? want : inside;
     }
+    if (want >= inside) return e;  // all of its key stay
+    e.id = 0;
     for (int shift = 16; shift >= 0; shift -= 8) {
       const uint32_t hi = shift == 16 ? 0u : ~0u << (shift + 8);
-      e.id |= digit<false, false>(
+      e.id |= (uint32_t)digit<false>(
                   [&](uint32_t key, uint32_t id) {
                     return in(key, id) && key == e.key && ((id ^ e.id) & hi) == 0 ? (int)((id >> shift) & 255u) : -1;
                   },
@@ -387,22 +510,19 @@ struct Source {
   // Sum of the weights of the elements that `in` accepts.
   template <class F>
   __device__ __forceinline__ unsigned long long sum(F&& in) const {
-    unsigned long long s = 0, all;
+    unsigned long long s = 0, whole;
     each([&](uint32_t key, uint32_t id) {
-      if (in(key, id)) {
-        const float l = key_logit(key);
-        s += W.weight(l, W.log2w(l));
-      }
+      if (in(key, id)) s += W.weight(key_logit(key));
     });
-    block_before(s, S.red64, all);
+    block_before(s, S.red64, whole);
     if (!LIST) {
-      if (threadIdx.x == 0) S.sel_u[1] = all;
+      if (threadIdx.x == 0) S.sel_u[1] = whole;
       cluster_sync();
-      all = 0;
-      for (int c = 0; c < C; ++c) all += ldl_cluster(cluster_addr(smem_addr(&S.sel_u[1]), c));
+      whole = 0;
+      for (int c = 0; c < C; ++c) whole += ldl_cluster(cluster_addr(smem_addr(&S.sel_u[1]), c));
       cluster_sync();
     }
-    return all;
+    return whole;
   }
 };
 
@@ -427,49 +547,68 @@ template <int DT>
 __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const __grid_constant__ SampleArgs A) {
   extern __shared__ __align__(16) uint8_t sample_smem[];
   SampleSmem& S = *reinterpret_cast<SampleSmem*>(sample_smem);
+  constexpr int VEC = Row<DT>::VEC;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = A.cluster, b = blockIdx.x / C, rank = blockIdx.x % C, runs = C * SM_WARPS;
-  for (int i = tid; i < 256; i += SM_THREADS) S.table[i] = g_exp_table.v[i];
+  if (tid < 64) {
+    S.table.hi[tid] = g_exp_table.hi[tid];
+    S.table.lo[tid] = g_exp_table.lo[tid];
+  }
+  for (int i = tid; i < SM_BINS; i += SM_THREADS) S.count[i] = S.place[i] = 0;
   pdl_trigger();
   pdl_wait();
   const Row<DT> row(A, b);
   const int v0 = row.run_begin(rank * SM_WARPS + warp, runs), v1 = row.run_begin(rank * SM_WARPS + warp + 1, runs);
   const float T = A.temperature ? A.temperature[b] : 1.f;
+  const int32_t K = A.top_k ? A.top_k[b] : 0;
+  const float P = A.top_p ? A.top_p[b] : 1.f, M = A.min_p ? A.min_p[b] : 0.f;
   const bool greedy = !(T >= 0x1p-60f);
+  const bool by_k = K > 0 && K < A.V, by_p = P < 1.f, by_m = M > 0.f && M < 1.f && T < INFINITY;
   // 1. the maximum, and its lowest id
   float top = -INFINITY;
   int top_id = 0x7fffffff;
-  row.each(v0, v1, [&](int id, float l) {
-    if (l > top) {
-      top = l;
-      top_id = id;
-    }
+  row.each(v0, v1, [&](int id, float(&l)[VEC]) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      if (l[i] > top) {
+        top = l[i];
+        top_id = id + i;
+      }
   });
-  auto better = [](float l, int i, float& m, int& mi) {
-    if (l > m || (l == m && i < mi)) {
-      m = l;
-      mi = i;
+  auto better = [&](float l, int i) {
+    if (l > top || (l == top && i < top_id)) {
+      top = l;
+      top_id = i;
     }
   };
+  auto warp_best = [&]() {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) better(__shfl_xor_sync(FULL, top, o), __shfl_xor_sync(FULL, top_id, o), top, top_id);
+    for (int o = 16; o; o >>= 1) {
+      const float l = __shfl_xor_sync(FULL, top, o);
+      better(l, __shfl_xor_sync(FULL, top_id, o));
+    }
+  };
+  warp_best();
   if (lane == 0) {
     S.redf[warp] = top;
     S.redu[warp] = (uint32_t)top_id;
   }
+  if (tid == 32 && by_m) S.log_m = (double)T * log((double)M);
   __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < SM_WARPS; ++w) better(S.redf[w], (int)S.redu[w], top, top_id);
-    S.top = top;
-    S.top_id = top_id;
-    S.list_n = 0;
+  if (warp == 0) {
+    top = lane < SM_WARPS ? S.redf[lane] : -INFINITY;
+    top_id = lane < SM_WARPS ? (int)S.redu[lane] : 0x7fffffff;
+    warp_best();
+    if (lane == 0) {
+      S.top = top;
+      S.top_id = (uint32_t)top_id;
+      S.list_n = 0;
+    }
   }
-  for (int i = tid; i < SM_BINS; i += SM_THREADS) S.count[i] = S.place[i] = 0;
   cluster_sync();
-  top = -INFINITY;
-  top_id = 0x7fffffff;
-  for (int c = 0; c < C; ++c)
-    better(ld_cluster(cluster_addr(smem_addr(&S.top), c)), (int)ldu_cluster(cluster_addr(smem_addr(&S.top_id), c)), top, top_id);
+  top = lane < C ? ld_cluster(cluster_addr(smem_addr(&S.top), lane)) : -INFINITY;
+  top_id = lane < C ? (int)ldu_cluster(cluster_addr(smem_addr(&S.top_id), lane)) : 0x7fffffff;
+  warp_best();
   if (greedy || top == -INFINITY) {
     if (rank == 0 && tid == 0) {
       const bool none = top == -INFINITY;
@@ -480,38 +619,36 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const __grid_cons
     return;
   }
   Weigher W;
-  {
-    const double c = 1.4426950408889634 / (double)T;
-    W.top = top;
-    W.ch = (float)c;
-    W.cl = (float)(c - (double)W.ch);
-    W.table = S.table;
-  }
-  const int32_t K = A.top_k ? A.top_k[b] : 0;
-  const float P = A.top_p ? A.top_p[b] : 1.f, M = A.min_p ? A.min_p[b] : 0.f;
-  const bool by_k = K > 0 && K < A.V, by_p = P < 1.f;
-  // min-p as a bound on the logit (T below infinity: the weights of all are 1 otherwise)
-  double least = -INFINITY;
-  if (M > 0.f) least = M >= 1.f ? (double)top : (double)T < INFINITY ? (double)top + (double)T * log((double)M) : -INFINITY;
-  // log2 w to bins, from the top
-  auto bin_of = [&](float p) { return min((int)(-p * SM_PER_OCTAVE), SM_BINS - 1); };
+  W.inf = top == INFINITY;
+  W.top = W.inf ? 0.f : top;
+  W.ch = LOG2E_HI / T;  // log2 e / T: quotient and, from its exact remainder, the rest
+  W.cl = T < INFINITY ? (fmaf(-W.ch, T, LOG2E_HI) + LOG2E_LO) / T : 0.f;
+  W.table = &S.table;
+  // min-p as a bound on the logit: the smallest fp32 number at or above top + T ln(min_p)
+  // (an infinite T makes all weights 1)
+  const float least = by_m ? __double2float_ru((double)W.top + S.log_m) : M >= 1.f && T < INFINITY ? W.top : -INFINITY;
 
   // 2. the histogram
   Open o = {SM_BINS, 0u, SM_BINS, -1};
   if (by_k || by_p) {
-    row.each(v0, v1, [&](int, float l) {
-      const float p = W.log2w(l);
-      if (p > -SM_OCTAVES) {
-        const float x = -p * SM_PER_OCTAVE;
-        const int i = min((int)x, SM_BINS - 1);
-        atomicAdd(&S.count[i], 1u);
-        if (by_p) atomicAdd(&S.place[i], (uint32_t)((x - (float)i) * SM_FRAC));
+    row.each(v0, v1, [&](int, float(&l)[VEC]) {
+      W.fix(l);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const float p = W.log2w(l[i]), m = W.bin_bits(p);
+        const uint32_t at = __float_as_uint(m) - 0x4b000000u;
+        if (W.has(p)) atomicAdd(&S.count[at], 1u);
+        // the place, -1/2 .. 1/2 of the bin, in units of 1/1024 from its upper end
+        const float f = fmaf(p, -SM_PER_OCTAVE, 0x1p23f - m);
+        if (by_p && W.has(p))
+          atomicAdd(&S.place[at], __float_as_uint(fmaf(f, (float)SM_FRAC, 0x1p23f + SM_FRAC / 2)) - 0x4b000000u);
       }
     });
     cluster_sync();
     const int per = SM_BINS / C;
     for (int i = tid; i < per; i += SM_THREADS) {
       uint32_t n = 0, q = 0;
+#pragma unroll 8
       for (int c = 0; c < C; ++c) {
         n += ldu_cluster(cluster_addr(smem_addr(&S.count[rank * per + i]), c));
         if (by_p) q += ldu_cluster(cluster_addr(smem_addr(&S.place[rank * per + i]), c));
@@ -553,30 +690,28 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const __grid_cons
     o.k_bin = S.sel_i[0];
     o.k_in = (uint32_t)S.sel_i[1];
     if (by_p) {
-      // A bin's sum: n 2^-(i + mean place) / 47.6, the mean place between the sum of the rounded-down places
-      // and 1 / 1024 more, the curvature inside a bin at most (ln 2 / 47.6)^2 / 8 = 2.7e-5 more, and the places'
-      // own rounding (log2 w up to 43 in fp32: 2^-12 of a bin).  Of the k-th element's bin, k_in elements of any place.
+      // A bin's sum is n 2^-(i - 1/2 + mean place) / 47.6, up to the rounding of the places (1 / 2048 of a bin each:
+      // 7e-6 of the sum), the curvature inside a bin ((ln 2 / 47.6)^2 / 8 = 2.7e-5) and log2 w's own rounding
+      // (2^-19: 2e-6): within 1e-4.  Of the k-th element's bin, k_in elements of any place.
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
         const int i = tid * PER + j;
-        const float cnt = (float)n[j];
+        const float cnt = (float)n[j], at = (float)i - 0.5f;
         if (i > o.k_bin || n[j] == 0) {
           lo[j] = hi[j] = 0.f;
         } else if (i == o.k_bin) {
-          lo[j] = (float)o.k_in * exp2f(-(float)(i + 1) / SM_PER_OCTAVE) * 0.9999f;
-          hi[j] = (float)o.k_in * exp2f(-(float)i / SM_PER_OCTAVE) * 1.0001f;
+          lo[j] = (float)o.k_in * exp2f(-(at + 1.f) / SM_PER_OCTAVE) * 0.9999f;
+          hi[j] = (float)o.k_in * exp2f(-at / SM_PER_OCTAVE) * 1.0001f;
         } else {
-          const float mean = lo[j] / (cnt * SM_FRAC);
-          const float w = cnt * exp2f(-((float)i + mean) / SM_PER_OCTAVE);
-          lo[j] = w * 0.9999f;  // (1 / 1024 of a bin: 1.4e-5)
+          const float w = cnt * exp2f(-(at + lo[j] / (cnt * SM_FRAC)) / SM_PER_OCTAVE);
+          lo[j] = w * 0.9999f;
           hi[j] = w * 1.0001f;
-          if (i == SM_BINS - 1) lo[j] = 0.f;
         }
         slo += lo[j];
         shi += hi[j];
       }
       float blo = block_before(slo, S.redf, all_lo), bhi = block_before(shi, S.redg, all_hi);
-      // sums of 2048 fp32 numbers: within 1e-4 (2^-24 each addition)
+      // sums of 2048 fp32 numbers: within 1e-4 (some 40 additions in a row, 2^-24 each)
       const float want_lo = P * all_lo * 0.9998f, want_hi = P * all_hi * 1.0002f;
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
@@ -593,110 +728,156 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const __grid_cons
     }
     __syncthreads();
   }
+  // Bins before `sure` stay (as far as top-k and top-p go).  Where min-p's bound lies in one of them it comes first,
+  // and what the open bins would decide does not matter; else it hides none of them.
+  const int sure = by_p ? o.p_lo : o.k_bin;
+  bool open = o.k_bin < SM_BINS || by_p;
+  if (open && least > -INFINITY && W.has(W.log2w(least)) && W.bin_of(W.log2w(least)) < sure) open = false;
 
   // 3. exact sums of what certainly stays, the list of the open bins
-  // (bins above p_lo, without top-p above k_bin: stay; between p_hi and k_bin: count for top-p's total only)
-  const int sure = by_p ? o.p_lo : o.k_bin;
-  unsigned long long above = 0, chosen = 0, between = 0;
-  row.each(v0, v1, [&](int id, float l) {
-    const float p = W.log2w(l);
-    if (!(p > -SM_OCTAVES)) return;
-    const int i = bin_of(p);
-    if (i > o.k_bin) return;
-    if (i == o.k_bin || (i >= o.p_lo && i <= o.p_hi)) {
-      const uint32_t at = atomicAdd(&S.list_n, 1u);
-      if (at < SM_LIST) S.list[at] = {logit_key(l), (uint32_t)id | ((uint32_t)(rank * SM_WARPS + warp) << 20)};
-      return;
-    }
-    const unsigned long long w = W.weight(l, p);
-    if (i < sure) {
-      above += w;
-      if ((double)l >= least) chosen += w;
-    } else {
-      between += w;
-    }
-  });
+  unsigned long long above = 0, between = 0;  // before the open bins; between them and the k-th element's
+  if (!open) {
+    row.each(v0, v1, [&](int, float(&l)[VEC]) {
+      W.fix(l);
+      uint32_t h = 0;
+      int32_t s = 0;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const float p = W.log2w(l[i]);
+        uint32_t hi;
+        int32_t low;
+        W.parts(l[i], p, hi, low);
+        if (W.has(p) && l[i] >= least) {
+          h += hi;
+          s += low;
+        }
+      }
+      above += W.units(h, s);
+    });
+  } else {
+    const int p_lo = by_p ? o.p_lo : o.k_bin, p_hi = by_p ? o.p_hi : o.k_bin;
+    row.each(v0, v1, [&](int id, float(&l)[VEC]) {
+      W.fix(l);
+      float p[VEC];
+      int at[VEC];
+      bool in = false, some = false;  // of the open bins; before them or between
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        p[i] = W.log2w(l[i]);
+        at[i] = W.has(p[i]) ? W.bin_of(p[i]) : SM_BINS + 1;
+        const bool listed = (at[i] >= p_lo && at[i] <= p_hi) || at[i] == o.k_bin;
+        in |= listed;
+        some |= at[i] < o.k_bin && !listed;
+      }
+      if (in) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+          if ((at[i] >= p_lo && at[i] <= p_hi) || at[i] == o.k_bin) {
+            const uint32_t to = atomicAdd(&S.list_n, 1u);
+            if (to < SM_LIST) S.list[to] = {logit_key(l[i]), (uint32_t)(id + i) | ((uint32_t)(rank * SM_WARPS + warp) << 20)};
+          }
+      }
+      if (__any_sync(FULL, some)) {
+        uint32_t h = 0, h2 = 0;
+        int32_t s = 0, s2 = 0;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          uint32_t hi;
+          int32_t low;
+          W.parts(l[i], p[i], hi, low);
+          if (at[i] < p_lo) {
+            h += hi;
+            s += low;
+          }
+          if (at[i] > p_hi && at[i] < o.k_bin) {
+            h2 += hi;
+            s2 += low;
+          }
+        }
+        above += W.units(h, s);
+        between += W.units(h2, s2);
+      }
+    });
+  }
   above = warp_add(above);
-  chosen = warp_add(chosen);
   between = warp_add(between);
   if (lane == 0) {
-    S.warp_sum[warp] = chosen;
-    S.red64[warp] = above;
-    S.mass[warp] = between;
+    S.warp_sum[warp] = above;
+    S.red64[warp] = between;
   }
   __syncthreads();
-  if (tid < 2) {
-    unsigned long long s = 0;
-    for (int w = 0; w < SM_WARPS; ++w) s += tid ? S.mass[w] : S.red64[w];
-    S.sums[tid] = s;
+  if (warp < 2) {
+    const unsigned long long s = warp_add(lane < SM_WARPS ? (warp ? S.red64[lane] : S.warp_sum[lane]) : 0ull);
+    if (lane == 0) S.sums[warp] = s;
   }
   cluster_sync();
   // 4. the borders
+  Entry last = {0u, SM_ALL_IDS};  // all stay
   uint32_t listed = 0;
-  for (int c = 0; c < C; ++c) listed += ldu_cluster(cluster_addr(smem_addr(&S.list_n), c));
-  above = between = 0;
-  for (int c = 0; c < C; ++c) {
-    above += ldl_cluster(cluster_addr(smem_addr(&S.sums[0]), c));
-    between += ldl_cluster(cluster_addr(smem_addr(&S.sums[1]), c));
-  }
-  Entry last = {0u, 0xffffffffu};  // all stay
-  const bool open = o.k_bin < SM_BINS || by_p, fits = listed <= SM_LIST;
-  auto bin_of_key = [&](uint32_t key) { return bin_of(W.log2w(key_logit(key))); };
-  auto borders = [&](auto src) {
-    if (o.k_bin < SM_BINS)
-      last = src.template select<false>([&](uint32_t key, uint32_t) { return bin_of_key(key) == o.k_bin; }, o.k_in);
-    if (by_p) {
-      const Entry kth = last;
-      auto inside = [&](uint32_t key, uint32_t id) {
-        const int i = bin_of_key(key);
-        return (i == o.k_bin || (i >= o.p_lo && i <= o.p_hi)) && stays(key, id, kth);
-      };
-      const unsigned long long total = above + between + src.sum(inside);
-      const unsigned long long want = P > 0.f ? ceil_mul(frac64(P), total) : 0ull;
-      // (bins from p_lo on hold the first element whose running sum reaches `want`, by the bounds)
-      unsigned long long more = want > above ? want - above : 1ull;
-      last = src.template select<true>(
-          [&](uint32_t key, uint32_t id) { return bin_of_key(key) <= o.p_hi && inside(key, id); }, more);
-    }
-  };
-  if (open && fits) {
-    if (rank == 0) {  // (the others wait below)
-      int n = 0;
-      for (int c = 0; c < C; ++c) {
-        const int m = (int)ldu_cluster(cluster_addr(smem_addr(&S.list_n), c));
-        const uint32_t from = cluster_addr(smem_addr(&S.list[0]), c);
-        for (int i = tid; i < m; i += SM_THREADS) {
-          const unsigned long long e = ldl_cluster(from + i * 8);
-          S.all[n + i] = {(uint32_t)e, (uint32_t)(e >> 32)};
-        }
-        n += m;
+  bool fits = true;
+  if (open) {
+    listed = cluster_add(&S.list_n, C);
+    fits = listed <= SM_LIST;
+    above = cluster_add(&S.sums[0], C);
+    between = cluster_add(&S.sums[1], C);
+    auto bin_of_key = [&](uint32_t key) { return W.bin_of(W.log2w(key_logit(key))); };
+    auto borders = [&](auto src) {
+      if (o.k_bin < SM_BINS)
+        last = src.template select<false>([&](uint32_t key, uint32_t) { return bin_of_key(key) == o.k_bin; }, o.k_in);
+      if (by_p) {
+        const Entry kth = last;
+        auto inside = [&](uint32_t key, uint32_t id) {
+          const int i = bin_of_key(key);
+          return (i == o.k_bin || (i >= o.p_lo && i <= o.p_hi)) && stays(key, id, kth);
+        };
+        const unsigned long long total = above + between + src.sum(inside);
+        const unsigned long long want = P > 0.f ? ceil_mul(frac64(P), total) : 0ull;
+        // (bins from p_lo on hold the first element whose running sum reaches `want`, by the bounds)
+        const unsigned long long more = want > above ? want - above : 1ull;
+        last = src.template select<true>(
+            [&](uint32_t key, uint32_t id) { return bin_of_key(key) <= o.p_hi && inside(key, id); }, more);
+        if (last.key == kth.key) last.id = min(last.id, kth.id);
       }
-      __syncthreads();
-      borders(Source<DT, true>{S, S.all, n, row, W, v0, v1, C});
-      listed = n;
+    };
+    if (fits) {
+      if (rank == 0) {  // (the others wait below)
+        // warp c copies CTA c's list
+        const uint32_t mine = lane < C ? ldu_cluster(cluster_addr(smem_addr(&S.list_n), lane)) : 0u;
+        const uint32_t from = __reduce_add_sync(FULL, lane < warp ? mine : 0u), m = __shfl_sync(FULL, mine, warp);
+        if (warp < C) {
+          const uint32_t src = cluster_addr(smem_addr(&S.list[0]), warp);
+          for (uint32_t i = lane; i < m; i += 32) {
+            const unsigned long long e = ldl_cluster(src + i * 8);
+            S.all[from + i] = {(uint32_t)e, (uint32_t)(e >> 32)};
+          }
+        }
+        __syncthreads();
+        borders(Source<DT, true>{S, (int)listed, row, W, v0, v1, C});
+      }
+    } else {
+      borders(Source<DT, false>{S, 0, row, W, v0, v1, C});
+      // the runs' sums, with the borders known
+      unsigned long long sum = 0;
+      row.each(v0, v1, [&](int id, float(&l)[VEC]) {
+        W.fix(l);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+          if (l[i] >= least && stays(logit_key(l[i]), (uint32_t)(id + i), last)) sum += W.weight(l[i]);
+      });
+      sum = warp_add(sum);
+      if (lane == 0) S.warp_sum[warp] = sum;
+      cluster_sync();
     }
-  } else if (open) {
-    borders(Source<DT, false>{S, nullptr, 0, row, W, v0, v1, C});
-    // the runs' sums, with the borders known
-    unsigned long long s = 0;
-    row.each(v0, v1, [&](int id, float l) {
-      const float p = W.log2w(l);
-      if (p > -SM_OCTAVES && stays(logit_key(l), (uint32_t)id, last) && (double)l >= least) s += W.weight(l, p);
-    });
-    s = warp_add(s);
-    if (lane == 0) S.warp_sum[warp] = s;
-    cluster_sync();
   }
   // 5. the run that holds the draw
   if (rank == 0) {
-    for (int i = tid; i < runs; i += SM_THREADS)
-      S.chunk[i] = ldl_cluster(cluster_addr(smem_addr(&S.warp_sum[i % SM_WARPS]), i / SM_WARPS));
-    __syncthreads();
+    if (tid < runs) S.chunk[tid] = ldl_cluster(cluster_addr(smem_addr(&S.warp_sum[tid % SM_WARPS]), tid / SM_WARPS));
     if (open && fits) {
+      __syncthreads();
       for (int i = tid; i < (int)listed; i += SM_THREADS) {
         const Entry e = S.all[i];
         const float l = key_logit(e.key);
-        if (stays(e.key, e.id & 0xfffffu, last) && (double)l >= least) atomicAdd(&S.chunk[e.id >> 20], W.weight(l, W.log2w(l)));
+        if (l >= least && stays(e.key, e.id & SM_ALL_IDS, last)) atomicAdd(&S.chunk[e.id >> 20], W.weight(l));
       }
       __syncthreads();
     }
@@ -715,65 +896,62 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const __grid_cons
     }
   }
   cluster_sync();
-  {
-    last.key = ldu_cluster(cluster_addr(smem_addr(&S.end.key), 0));
-    last.id = ldu_cluster(cluster_addr(smem_addr(&S.end.id), 0));
-    const unsigned long long total = ldl_cluster(cluster_addr(smem_addr(&S.end.total), 0));
-    unsigned long long rest = ldl_cluster(cluster_addr(smem_addr(&S.end.rest), 0));
-    const int run = (int)ldu_cluster(cluster_addr(smem_addr(&S.end.run), 0));
-    cluster_sync();  // (nobody's shared memory goes while another reads it)
-    if (run / SM_WARPS != rank) return;
-    // the run's elements, a part a warp
-    auto weight_if = [&](int id, float l) -> unsigned long long {
-      const float p = W.log2w(l);
-      return p > -SM_OCTAVES && stays(logit_key(l), (uint32_t)id, last) && (double)l >= least ? W.weight(l, p) : 0ull;
-    };
-    const int r0 = row.run_begin(run, runs), r1 = row.run_begin(run + 1, runs);
-    const int p0 = r0 + (int)((int64_t)(r1 - r0) * warp / SM_WARPS), p1 = r0 + (int)((int64_t)(r1 - r0) * (warp + 1) / SM_WARPS);
-    unsigned long long s = 0;
-    row.each(p0, p1, [&](int id, float l) { s += weight_if(id, l); });
-    s = warp_add(s);
-    if (lane == 0) S.red64[warp] = s;
-    __syncthreads();
-    unsigned long long before = 0;
-    for (int w = 0; w < warp; ++w) before += S.red64[w];
-    if (!(before <= rest && before + s > rest)) return;
-    rest -= before;
-    constexpr int VEC = Row<DT>::VEC;
-    for (int v = p0; v < p1; v += 32) {
-      unsigned long long w[VEC], sum = 0;
-      float l[VEC];
-      const bool has = v + lane < p1;
-      if (has) row.values(v + lane, row.load(v + lane, p1), l);
+  last.key = ldu_cluster(cluster_addr(smem_addr(&S.end.key), 0));
+  last.id = ldu_cluster(cluster_addr(smem_addr(&S.end.id), 0));
+  const unsigned long long total = ldl_cluster(cluster_addr(smem_addr(&S.end.total), 0));
+  unsigned long long rest = ldl_cluster(cluster_addr(smem_addr(&S.end.rest), 0));
+  const int run = (int)ldu_cluster(cluster_addr(smem_addr(&S.end.run), 0));
+  cluster_sync();  // (nobody's shared memory goes while another reads it)
+  if (run / SM_WARPS != rank) return;
+  // the run's elements, a part a warp
+  auto weight_if = [&](int id, float l) -> unsigned long long {
+    return l >= least && stays(logit_key(l), (uint32_t)id, last) ? W.weight(l) : 0ull;
+  };
+  const int r0 = row.run_begin(run, runs), r1 = row.run_begin(run + 1, runs);
+  const int p0 = r0 + (int)((int64_t)(r1 - r0) * warp / SM_WARPS), p1 = r0 + (int)((int64_t)(r1 - r0) * (warp + 1) / SM_WARPS);
+  unsigned long long s = 0;
+  row.each(p0, p1, [&](int id, float(&l)[VEC]) {
+    W.fix(l);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) s += weight_if(id + i, l[i]);
+  });
+  s = warp_add(s);
+  if (lane == 0) S.red64[warp] = s;
+  __syncthreads();
+  const unsigned long long before = warp_add(lane < warp ? S.red64[lane] : 0ull);
+  if (!(before <= rest && before + s > rest)) return;
+  rest -= before;
+  for (int v = p0; v < p1; v += 32) {
+    unsigned long long w[VEC], sum = 0;
+    float l[VEC];
+    row.values(v + lane, p1, l);
+    W.fix(l);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      w[i] = weight_if((v + lane) * VEC + i - row.off, l[i]);
+      sum += w[i];
+    }
+    unsigned long long inc = sum;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const unsigned long long y = __shfl_up_sync(FULL, inc, k);
+      if (lane >= k) inc += y;
+    }
+    unsigned long long at = inc - sum;
+    if (sum && at <= rest && inc > rest) {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        w[i] = has ? weight_if((v + lane) * VEC + i - row.off, l[i]) : 0ull;
-        sum += w[i];
-      }
-      unsigned long long inc = sum;
-#pragma unroll
-      for (int k = 1; k < 32; k <<= 1) {
-        const unsigned long long y = __shfl_up_sync(FULL, inc, k);
-        if (lane >= k) inc += y;
-      }
-      unsigned long long at = inc - sum;
-      if (sum && at <= rest && inc > rest) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          if (w[i] && at <= rest && at + w[i] > rest) {
-            A.token[b] = (v + lane) * VEC + i - row.off;
-            if (A.logp) {
-              const double x = l[i] == top ? 0.0 : ((double)l[i] - (double)top) / (double)T;
-              A.logp[b] = (float)(x - log((double)total * 0x1p-42));
-            }
-          }
-          at += w[i];
+        if (w[i] && at <= rest && at + w[i] > rest) {
+          A.token[b] = (v + lane) * VEC + i - row.off;
+          // (no cancellation: both terms are <= 0)
+          if (A.logp) A.logp[b] = (l[i] - W.top) / T - logf(__ull2float_rn(total) * 0x1p-43f);
         }
+        at += w[i];
       }
-      const unsigned long long whole = __shfl_sync(FULL, inc, 31);
-      if (whole > rest) break;
-      rest -= whole;
     }
+    const unsigned long long whole = __shfl_sync(FULL, inc, 31);
+    if (whole > rest) break;
+    rest -= whole;
   }
 }
 
