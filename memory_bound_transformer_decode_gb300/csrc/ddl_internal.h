@@ -40,6 +40,12 @@ inline int device_sms(int& sms) {
   return DDL_OK;
 }
 
+inline int log2_of(int32_t pow2) {
+  int s = 0;
+  while ((1 << s) < pow2) ++s;
+  return s;
+}
+
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 // Shape rules of ddl.h.

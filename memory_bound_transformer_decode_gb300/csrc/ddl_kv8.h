@@ -35,12 +35,6 @@ inline int check_attn_opts(const ddl_attn_opts* o) {
   return ((uintptr_t)o->slopes & 3u) ? DDL_ERR_ALIGN : DDL_OK;
 }
 
-inline int log2_of(int32_t pow2) {
-  int s = 0;
-  while ((1 << s) < pow2) ++s;
-  return s;
-}
-
 inline int dtype_bytes(int32_t t) { return t == DDL_T_F32 ? 4 : (t == DDL_T_BF16 || t == DDL_T_F16) ? 2 : 0; }
 
 // Two e4m3 codes (bytes 0 and 1 of w, or 2 and 3) as fp16: exact.

@@ -20,7 +20,11 @@
 // each; 64 rows of 152064 would take 160 us.)
 //
 // A cluster of 1 to 16 CTAs takes a row; a warp a contiguous run of ids.
-//  1. The maximum (greedy rows end here).
+//  1. The maximum (greedy rows end here), and each lane's own.
+//  1b. top-k of fewer elements than half the lanes: the k-th largest of the lanes' maxima
+//     is a bound of the k-th logit, and nearly it where ids and logits are unrelated.  A
+//     histogram of the maxima gives it, the elements above it go to the list, and 4 does
+//     the rest.  (If they are too many: 2.)
 //  2. Rows with top-k or top-p: a histogram of log2 w in 2048 bins of 1/47.6 octave:
 //     how many elements, and the sum of their places inside the bin, which bounds the
 //     bin's sum of weights to 2^-13.  Where the k-th element and the end of the top-p
@@ -588,6 +592,7 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const __grid_cons
       better(l, __shfl_xor_sync(FULL, top_id, o));
     }
   };
+  const float mine_top = top;
   warp_best();
   if (lane == 0) {
     S.redf[warp] = top;
@@ -628,9 +633,59 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const __grid_cons
   // (an infinite T makes all weights 1)
   const float least = by_m ? __double2float_ru((double)W.top + S.log_m) : M >= 1.f && T < INFINITY ? W.top : -INFINITY;
 
-  // 2. the histogram
+  // 1b. the bound by the lanes' maxima, in bins of 8; all elements from there up to the list
   Open o = {SM_BINS, 0u, SM_BINS, -1};
-  if (by_k || by_p) {
+  uint32_t listed = 0;
+  bool heads = by_k && K <= min(C * SM_THREADS / 2, SM_LIST / 2);  // the list holds all elements of the top-k head
+  if (heads) {
+    float own[1] = {mine_top};
+    W.fix(own);
+    const float p = W.log2w(own[0]);
+    if (tid < 256) S.num[tid] = 0;
+    __syncthreads();
+    if (W.has(p)) atomicAdd(&S.num[W.bin_of(p) >> 3], 1u);
+    cluster_sync();
+    uint32_t n = 0;
+    if (tid < 256) {
+#pragma unroll 8
+      for (int c = 0; c < C; ++c) n += ldu_cluster(cluster_addr(smem_addr(&S.num[tid]), c));
+    }
+    uint32_t all;
+    const uint32_t before = block_before(n, S.redu, all);
+    if (before < (uint32_t)K && before + n >= (uint32_t)K) S.sel_i[0] = tid * 8 + 7;
+    __syncthreads();
+    heads = all >= (uint32_t)K;
+    if (heads) {
+      const int from = S.sel_i[0];
+      row.each(v0, v1, [&](int id, float(&l)[VEC]) {
+        W.fix(l);
+        float top = l[0];
+#pragma unroll
+        for (int i = 1; i < VEC; ++i) top = fmaxf(top, l[i]);
+        const float p = W.log2w(top);
+        if (!W.has(p) || W.bin_of(p) > from) return;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const float q = W.log2w(l[i]);
+          if (W.has(q) && W.bin_of(q) <= from) {
+            const uint32_t to = atomicAdd(&S.list_n, 1u);
+            if (to < SM_LIST) S.list[to] = {logit_key(l[i]), (uint32_t)(id + i) | ((uint32_t)(rank * SM_WARPS + warp) << 20)};
+          }
+        }
+      });
+      if (tid < SM_WARPS) S.warp_sum[tid] = 0;
+      cluster_sync();
+      listed = cluster_add(&S.list_n, C);
+      heads = listed <= SM_LIST;
+      if (!heads) {
+        cluster_sync();  // (all have read list_n)
+        if (tid == 0) S.list_n = 0;
+      }
+    }
+  }
+
+  // 2. the histogram
+  if (!heads && (by_k || by_p)) {
     row.each(v0, v1, [&](int, float(&l)[VEC]) {
       W.fix(l);
 #pragma unroll
@@ -731,12 +786,14 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const __grid_cons
   // Bins before `sure` stay (as far as top-k and top-p go).  Where min-p's bound lies in one of them it comes first,
   // and what the open bins would decide does not matter; else it hides none of them.
   const int sure = by_p ? o.p_lo : o.k_bin;
-  bool open = o.k_bin < SM_BINS || by_p;
-  if (open && least > -INFINITY && W.has(W.log2w(least)) && W.bin_of(W.log2w(least)) < sure) open = false;
+  bool open = heads || o.k_bin < SM_BINS || by_p;
+  if (open && !heads && least > -INFINITY && W.has(W.log2w(least)) && W.bin_of(W.log2w(least)) < sure) open = false;
 
   // 3. exact sums of what certainly stays, the list of the open bins
   unsigned long long above = 0, between = 0;  // before the open bins; between them and the k-th element's
-  if (!open) {
+  if (heads) {
+    // (nothing to add up)
+  } else if (!open) {
     row.each(v0, v1, [&](int, float(&l)[VEC]) {
       W.fix(l);
       uint32_t h = 0;
@@ -799,43 +856,47 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const __grid_cons
       }
     });
   }
-  above = warp_add(above);
-  between = warp_add(between);
-  if (lane == 0) {
-    S.warp_sum[warp] = above;
-    S.red64[warp] = between;
+  if (!heads) {
+    above = warp_add(above);
+    between = warp_add(between);
+    if (lane == 0) {
+      S.warp_sum[warp] = above;
+      S.red64[warp] = between;
+    }
+    __syncthreads();
+    if (warp < 2) {
+      const unsigned long long s = warp_add(lane < SM_WARPS ? (warp ? S.red64[lane] : S.warp_sum[lane]) : 0ull);
+      if (lane == 0) S.sums[warp] = s;
+    }
+    cluster_sync();
   }
-  __syncthreads();
-  if (warp < 2) {
-    const unsigned long long s = warp_add(lane < SM_WARPS ? (warp ? S.red64[lane] : S.warp_sum[lane]) : 0ull);
-    if (lane == 0) S.sums[warp] = s;
-  }
-  cluster_sync();
   // 4. the borders
   Entry last = {0u, SM_ALL_IDS};  // all stay
-  uint32_t listed = 0;
   bool fits = true;
   if (open) {
-    listed = cluster_add(&S.list_n, C);
-    fits = listed <= SM_LIST;
-    above = cluster_add(&S.sums[0], C);
-    between = cluster_add(&S.sums[1], C);
+    if (!heads) {
+      listed = cluster_add(&S.list_n, C);
+      fits = listed <= SM_LIST;
+      above = cluster_add(&S.sums[0], C);
+      between = cluster_add(&S.sums[1], C);
+    }
     auto bin_of_key = [&](uint32_t key) { return W.bin_of(W.log2w(key_logit(key))); };
     auto borders = [&](auto src) {
-      if (o.k_bin < SM_BINS)
-        last = src.template select<false>([&](uint32_t key, uint32_t) { return bin_of_key(key) == o.k_bin; }, o.k_in);
+      if (heads || o.k_bin < SM_BINS)
+        last = src.template select<false>([&](uint32_t key, uint32_t) { return heads || bin_of_key(key) == o.k_bin; },
+                                          heads ? (uint32_t)K : o.k_in);
       if (by_p) {
         const Entry kth = last;
         auto inside = [&](uint32_t key, uint32_t id) {
           const int i = bin_of_key(key);
-          return (i == o.k_bin || (i >= o.p_lo && i <= o.p_hi)) && stays(key, id, kth);
+          return (heads || i == o.k_bin || (i >= o.p_lo && i <= o.p_hi)) && stays(key, id, kth);
         };
         const unsigned long long total = above + between + src.sum(inside);
         const unsigned long long want = P > 0.f ? ceil_mul(frac64(P), total) : 0ull;
         // (bins from p_lo on hold the first element whose running sum reaches `want`, by the bounds)
         const unsigned long long more = want > above ? want - above : 1ull;
         last = src.template select<true>(
-            [&](uint32_t key, uint32_t id) { return bin_of_key(key) <= o.p_hi && inside(key, id); }, more);
+            [&](uint32_t key, uint32_t id) { return (heads || bin_of_key(key) <= o.p_hi) && inside(key, id); }, more);
         if (last.key == kth.key) last.id = min(last.id, kth.id);
       }
     };
@@ -903,59 +964,65 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const __grid_cons
   const int run = (int)ldu_cluster(cluster_addr(smem_addr(&S.end.run), 0));
   cluster_sync();  // (nobody's shared memory goes while another reads it)
   if (run / SM_WARPS != rank) return;
-  // the run's elements, a part a warp
+  // the run's elements, a part a thread
   auto weight_if = [&](int id, float l) -> unsigned long long {
     return l >= least && stays(logit_key(l), (uint32_t)id, last) ? W.weight(l) : 0ull;
   };
-  const int r0 = row.run_begin(run, runs), r1 = row.run_begin(run + 1, runs);
-  const int p0 = r0 + (int)((int64_t)(r1 - r0) * warp / SM_WARPS), p1 = r0 + (int)((int64_t)(r1 - r0) * (warp + 1) / SM_WARPS);
-  unsigned long long s = 0;
-  row.each(p0, p1, [&](int id, float(&l)[VEC]) {
+  const int r0 = row.run_begin(run, runs), nv = row.run_begin(run + 1, runs) - r0;
+  const int p0 = r0 + (int)((int64_t)nv * tid / SM_THREADS), p1 = r0 + (int)((int64_t)nv * (tid + 1) / SM_THREADS);
+  unsigned long long s = 0, all;
+  for (int v = p0; v < p1; ++v) {
+    float l[VEC];
+    row.values(v, p1, l);
     W.fix(l);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) s += weight_if(id + i, l[i]);
-  });
-  s = warp_add(s);
-  if (lane == 0) S.red64[warp] = s;
-  __syncthreads();
-  const unsigned long long before = warp_add(lane < warp ? S.red64[lane] : 0ull);
-  if (!(before <= rest && before + s > rest)) return;
-  rest -= before;
-  for (int v = p0; v < p1; v += 32) {
-    unsigned long long w[VEC], sum = 0;
+    for (int i = 0; i < VEC; ++i) s += weight_if(v * VEC + i - row.off, l[i]);
+  }
+  unsigned long long at = block_before(s, S.red64, all);
+  if (!(s && at <= rest && at + s > rest)) return;
+  for (int v = p0; v < p1; ++v) {
     float l[VEC];
-    row.values(v + lane, p1, l);
+    row.values(v, p1, l);
     W.fix(l);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-      w[i] = weight_if((v + lane) * VEC + i - row.off, l[i]);
-      sum += w[i];
-    }
-    unsigned long long inc = sum;
-#pragma unroll
-    for (int k = 1; k < 32; k <<= 1) {
-      const unsigned long long y = __shfl_up_sync(FULL, inc, k);
-      if (lane >= k) inc += y;
-    }
-    unsigned long long at = inc - sum;
-    if (sum && at <= rest && inc > rest) {
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        if (w[i] && at <= rest && at + w[i] > rest) {
-          A.token[b] = (v + lane) * VEC + i - row.off;
-          // (no cancellation: both terms are <= 0)
-          if (A.logp) A.logp[b] = (l[i] - W.top) / T - logf(__ull2float_rn(total) * 0x1p-43f);
-        }
-        at += w[i];
+      const unsigned long long w = weight_if(v * VEC + i - row.off, l[i]);
+      if (w && at <= rest && at + w > rest) {
+        A.token[b] = v * VEC + i - row.off;
+        // (no cancellation: both terms are <= 0)
+        if (A.logp) A.logp[b] = (l[i] - W.top) / T - logf(__ull2float_rn(total) * 0x1p-43f);
       }
+      at += w;
     }
-    const unsigned long long whole = __shfl_sync(FULL, inc, 31);
-    if (whole > rest) break;
-    rest -= whole;
   }
 }
 
 const size_t SAMPLE_SMEM = sizeof(SampleSmem);
+
+// Clusters of `c` CTAs that the current device runs at once (asked for once a device).
+int rows_at_once(const void* fn, int dtype, int c, int& rows) {
+  static std::atomic<int> known[64][3][5];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_status(e);
+  if (dev < 0 || dev >= 64) return DDL_ERR_UNSUPPORTED;
+  std::atomic<int>& k = known[dev][dtype][log2_of(c)];
+  rows = k.load(std::memory_order_relaxed);
+  if (rows) return DDL_OK;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)c);
+  cfg.blockDim = dim3(SM_THREADS);
+  cfg.dynamicSmemBytes = SAMPLE_SMEM;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)c;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if ((e = cudaOccupancyMaxActiveClusters(&rows, fn, &cfg)) != cudaSuccess) return cuda_status(e);
+  k.store(rows, std::memory_order_relaxed);
+  return DDL_OK;
+}
 
 }  // namespace
 }  // namespace ddl
@@ -973,17 +1040,21 @@ extern "C" int ddl_sample(const void* logits, ddl_dtype dtype, int64_t stride, i
   for (const void* p : {(const void*)temperature, (const void*)top_k, (const void*)top_p, (const void*)min_p,
                         (const void*)u, (const void*)token_out, (const void*)logp_out})
     if ((uintptr_t)p & 3u) return DDL_ERR_ALIGN;
-  int sms = 0, st;
-  if ((st = device_sms(sms))) return st;
+  int st;
   SampleArgs a = {logits, stride, temperature, top_p, min_p, u, top_k, token_out, logp_out, V, 1};
-  // CTAs a row: as many as the machine holds at once (two an SM), each with 2048 elements at least
-  while (a.cluster < SM_MAX_CLUSTER && (int64_t)B * a.cluster * 2 <= 2 * sms && V / (a.cluster * 2) >= 2048) a.cluster *= 2;
   const void* fn = dtype == DDL_T_F32    ? (const void*)sample_kernel<DDL_T_F32>
                    : dtype == DDL_T_BF16 ? (const void*)sample_kernel<DDL_T_BF16>
                                          : (const void*)sample_kernel<DDL_T_F16>;
   if ((st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SAMPLE_SMEM)))) return st;
-  if (a.cluster > 8 && (st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1))))
-    return st;
+  if ((st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)))) return st;
+  // CTAs a row: as many as let all rows run at once (of 16: 14 rows, of 8: 36, of 4: 74; 17 rows of 50257 in clusters
+  // of 16, in two waves, 34.3 us with top-k, of 8 25.6), each with 2048 elements at least
+  for (int c = 2; c <= SM_MAX_CLUSTER && V / c >= 2048; c *= 2) {
+    int rows = 0;
+    if ((st = rows_at_once(fn, dtype, c, rows))) return st;
+    if (rows < B) break;
+    a.cluster = c;
+  }
   void* args[] = {&a};
   return cuda_status(launch_pdl_cluster(fn, dim3((unsigned)(B * a.cluster)), dim3(SM_THREADS), args, SAMPLE_SMEM, a.cluster,
                                         (cudaStream_t)stream));
