@@ -21,14 +21,15 @@
 namespace ddl {
 namespace {
 
-constexpr int SC_WARPS = 8;
+constexpr int SC_MAX_BLOCKS = 12;  // blocks of 16 tokens a warp takes at most (a lane each)
 
 struct ScoreArgs {
   AttArgs a;
   float* score;    // [R][H_kv][stride]
   int64_t stride;
   float decay;
-  int32_t wb;      // blocks of 16 tokens a warp takes (<= 32)
+  int32_t wb;      // blocks a warp takes
+  int32_t tiles;   // query tiles whose fragments fit shared memory at a time (several-tile kernel)
 };
 
 // What the queries of a tile need apart from their fragments.
@@ -41,7 +42,7 @@ struct Column {
 
 // Query qi of request rq for K/V head h.
 template <bool EX>
-__device__ __forceinline__ Column column_of(const AttArgs& A, const Req& rq, int h, int qi, float qf, float lse) {
+__device__ __forceinline__ Column column_of(const AttArgs& A, const Req& rq, int h, int qi, float qf) {
   Column c;
   const bool has = qi < rq.n * A.GH;
   const int row = has ? group_row(A, qi) : 0;
@@ -52,30 +53,118 @@ __device__ __forceinline__ Column column_of(const AttArgs& A, const Req& rq, int
   c.cf = qf * A.scale;
   if (EX && A.softcap > 0.f) c.cf = __fdiv_rn(c.cf, A.softcap);
   else c.cf *= LOG2E;
+  const float lse = has ? A.lse[(int64_t)(rq.row0 + row) * A.Hq + h * A.GH + qi - row * A.GH] : 0.f;
   c.lse2 = lse == -INFINITY ? INFINITY : lse * LOG2E;
   return c;
 }
 
-// exp of a score (MMA sum `s`, block scale `ks`) less its query's lse.
-template <bool EX>
-__device__ __forceinline__ float weight_of(const AttArgs& A, const Column& c, float s, float ks, int key) {
-  if (!EX) return exp2_fast(fmaf(s, ks * c.cf, -c.lse2));
-  const float x = s * (ks * c.cf);
-  const float y = A.softcap > 0.f ? A.softcap * LOG2E * tanhf(x) : x;
-  return exp2_fast(fmaf(-c.slope, (float)(c.hi - key), y) - c.lse2);
+// tanh of four numbers: below 0.3 its series up to x^9 (the next term is 2^-24 of it), which is
+// relative to x at any cap; else, where a lane of the warp has a larger one, tanhf.
+__device__ __forceinline__ void tanh4(float (&x)[4]) {
+  const float top = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+  if (__any_sync(FULL, !(top < 0.3f))) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = tanhf(x[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float y = x[j] * x[j];
+      x[j] = fmaf(x[j] * y, fmaf(y, fmaf(y, fmaf(y, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f), x[j]);
+    }
+  }
 }
 
-// 16 bytes of row g (and g + 8) of a block, one load per 64 bytes of the row.
+// Weights exp(score - lse) of tokens key, key + 8 (c 0, 1 and 2, 3) for two queries: c are the MMA's sums.
+// All lanes of the warp call it.
+template <bool EX>
+__device__ __forceinline__ void weights(const AttArgs& A, float (&c)[4], const Column& x, const Column& y, float ks,
+                                        int key, bool edge) {
+  const float fx = ks * x.cf, fy = ks * y.cf;
+  if (!EX) {
+    c[0] = exp2_fast(fmaf(c[0], fx, -x.lse2));
+    c[1] = exp2_fast(fmaf(c[1], fy, -y.lse2));
+    c[2] = exp2_fast(fmaf(c[2], fx, -x.lse2));
+    c[3] = exp2_fast(fmaf(c[3], fy, -y.lse2));
+  } else {
+    c[0] *= fx;
+    c[1] *= fy;
+    c[2] *= fx;
+    c[3] *= fy;
+    if (A.softcap > 0.f) {
+      tanh4(c);
+      const float cap = A.softcap * LOG2E;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) c[j] *= cap;
+    }
+    c[0] = exp2_fast(fmaf(-x.slope, (float)(x.hi - key), c[0]) - x.lse2);
+    c[1] = exp2_fast(fmaf(-y.slope, (float)(y.hi - key), c[1]) - y.lse2);
+    c[2] = exp2_fast(fmaf(-x.slope, (float)(x.hi - key - 8), c[2]) - x.lse2);
+    c[3] = exp2_fast(fmaf(-y.slope, (float)(y.hi - key - 8), c[3]) - y.lse2);
+  }
+  if (edge) {
+    c[0] = key <= x.hi && key >= x.lo ? c[0] : 0.f;
+    c[1] = key <= y.hi && key >= y.lo ? c[1] : 0.f;
+    c[2] = key + 8 <= x.hi && key + 8 >= x.lo ? c[2] : 0.f;
+    c[3] = key + 8 <= y.hi && key + 8 >= y.lo ? c[3] : 0.f;
+  }
+}
+
+// The CTA's part of the tokens of request r for K/V head h: blocks c0 .. c0 + W wb, block
+// c0 + warp + W i being this warp's i-th.
+template <int W>
+struct Part {
+  Req rq;
+  int r, h, c0, nb, first, mine;  // first block that changes, blocks of this warp
+  int32_t place;                  // lane i: of this warp's block i among all heads' blocks of the pool (-1: nobody sees it)
+  float scale;
+  float* out;
+  // False: nothing to do for the CTA.
+  __device__ __forceinline__ bool load(const ScoreArgs& S) {
+    const AttArgs& A = S.a;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    r = blockIdx.z;
+    h = blockIdx.y;
+    rq = load_req(A, r);
+    if (rq.bad && A.bad && blockIdx.x == 0 && h == 0 && threadIdx.x == 0) atomicOr(A.bad, 1);
+    if (rq.n <= 0) return false;
+    nb = (rq.len + 15) >> 4;
+    c0 = blockIdx.x * W * S.wb;
+    first = S.decay == 1.f ? rq.b0 : 0;  // blocks before rq.b0 only decay
+    if (c0 >= nb || c0 + W * S.wb <= first) return false;
+    mine = c0 + warp < nb ? min(S.wb, (nb - c0 - warp + W - 1) / W) : 0;
+    place = -1;
+    scale = 0.f;
+    if (lane < mine) {
+      const int b = block(lane), bshift = A.pshift - 4;
+      if (b >= rq.b0 && b < rq.b1) {
+        const int32_t page = A.table[(int64_t)r * A.per + (b >> bshift)];
+        if (page >= 0 && page < A.pages) {
+          place = (int32_t)((((int64_t)page * A.Hkv + h) << bshift) + (b & ((1 << bshift) - 1)));
+          scale = A.ks[place];
+          if (!(fabsf(scale) < INFINITY)) scale = __uint_as_float(0x7fffffffu);
+        } else if (A.bad) {
+          atomicOr(A.bad, 1);
+        }
+      }
+    }
+    out = S.score + ((int64_t)r * A.Hkv + h) * S.stride;
+    return true;
+  }
+  __device__ __forceinline__ int block(int i) const { return c0 + (int)(threadIdx.x >> 5) + W * i; }
+  // the score that token `key` brings along
+  __device__ __forceinline__ float old(const ScoreArgs& S, int key) const {
+    return key < rq.p0 && key < rq.len && S.decay != 0.f ? out[key] : 0.f;
+  }
+  __device__ __forceinline__ void put(const ScoreArgs& S, int key, float was, float sum) const {
+    if (key < rq.len) out[key] = fmaf(S.decay, was, sum);
+  }
+};
+
+// A block's K codes in a lane: 16 bytes of rows g and g + 8 for each 64 of a row.
 template <int HD>
 struct KBlock {
   static constexpr int NV = HD / 64;
   uint4 v[2][NV];
-  __device__ __forceinline__ void load(const uint8_t* k, int32_t blk, int lane) {
-    const uint8_t* p = k + (int64_t)blk * (16 * HD) + (lane >> 2) * HD + (lane & 3) * 16;
-#pragma unroll
-    for (int j = 0; j < 2 * NV; ++j)
-      v[j / NV][j % NV] = *reinterpret_cast<const uint4*>(p + (j / NV) * 8 * HD + (j % NV) * 64);
-  }
   template <int CT>
   __device__ __forceinline__ void frag(int s, uint32_t (&a)[4]) const {
     const uint4 x = v[0][s / 4], y = v[1][s / 4];
@@ -83,6 +172,10 @@ struct KBlock {
     const uint32_t wy = (s & 3) == 0 ? y.x : (s & 3) == 1 ? y.y : (s & 3) == 2 ? y.z : y.w;
     codes_f16<CT>(wx, a[0], a[2]);
     codes_f16<CT>(wy, a[1], a[3]);
+  }
+  static __device__ __forceinline__ const uint8_t* piece(const uint8_t* k, int32_t blk, int j) {
+    const int lane = threadIdx.x & 31;
+    return k + (int64_t)blk * (16 * HD) + ((lane >> 2) + (j / NV) * 8) * HD + (lane & 3) * 16 + (j % NV) * 64;
   }
 };
 
@@ -126,219 +219,264 @@ struct QTile {
   }
 };
 
-// Shared memory of the kernel for several tiles: their fragments (and remainders) and columns.
+__device__ __forceinline__ void reduce_rows(float& s0, float& s1) {  // over the four lanes of a row
+  s0 += __shfl_xor_sync(FULL, s0, 1);
+  s1 += __shfl_xor_sync(FULL, s1, 1);
+  s0 += __shfl_xor_sync(FULL, s0, 2);
+  s1 += __shfl_xor_sync(FULL, s1, 2);
+}
+
+// Fragments and columns of several tiles in shared memory.
 template <int DT, int HD>
 struct TileSmem {
   static constexpr int KS = HD / 16, PARTS = DT == DDL_T_F32 ? 2 : 1;
   static constexpr int PER = PARTS * KS * 32 * 8 + 8 * (int)sizeof(Column);  // bytes a tile
-};
-constexpr int TILE_SMEM = 142 * 1024;  // 64 tiles of 16-bit rows of 128
-
-// One CTA: 8 wb blocks of a request's tokens for one K/V head.
-//   ONE: the request has one tile of queries (8 rows x heads), whose fragments stay in
-//   registers; else the tiles' fragments go through shared memory, smem_tiles at a time.
-template <int CT, int DT, int HD, bool EX, bool ONE>
-__global__ void __launch_bounds__(SC_WARPS * 32, ONE ? 3 : 1) kv8_score_kernel(const __grid_constant__ ScoreArgs S,
-                                                                               int smem_tiles) {
-  extern __shared__ __align__(16) uint8_t sc_smem[];
-  __shared__ float sums[ONE ? 1 : SC_WARPS * 32 * 16];
-  const AttArgs& A = S.a;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int r = blockIdx.z, h = blockIdx.y;
-  constexpr int KS = HD / 16;
-  pdl_trigger();
-  pdl_wait();
-  const Req rq = load_req(A, r);
-  if (rq.bad && A.bad && blockIdx.x == 0 && h == 0 && threadIdx.x == 0) atomicOr(A.bad, 1);
-  if (rq.n <= 0) return;
-  const int nb = (rq.len + 15) >> 4, c0 = blockIdx.x * SC_WARPS * S.wb;
-  const int first = S.decay == 1.f ? rq.b0 : 0;  // blocks before rq.b0 only decay
-  if (c0 >= nb || c0 + SC_WARPS * S.wb <= first) return;
-  // block i of this warp: c0 + warp + 8 i; lane l holds the place and scale of block l
-  auto block_of = [&](int i) { return c0 + warp + SC_WARPS * i; };
-  const int mine = c0 + warp < nb ? min(S.wb, (nb - c0 - warp + SC_WARPS - 1) / SC_WARPS) : 0;
-  int32_t place = -1;
-  float scale = 0.f;
-  if (lane < mine) {
-    const int b = block_of(lane), bshift = A.pshift - 4;
-    if (b >= rq.b0 && b < rq.b1) {
-      const int32_t page = A.table[(int64_t)r * A.per + (b >> bshift)];
-      if (page >= 0 && page < A.pages) {
-        place = (int32_t)((((int64_t)page * A.Hkv + h) << bshift) + (b & ((1 << bshift) - 1)));
-        scale = A.ks[place];
-        if (!(fabsf(scale) < INFINITY)) scale = __uint_as_float(0x7fffffffu);
-      } else if (A.bad) {
-        atomicOr(A.bad, 1);
+  uint2* frags;  // [tile][part][k-step][lane]
+  Column* cols;  // [tile][8]
+  __device__ __forceinline__ TileSmem(uint8_t* p, int tiles)
+      : frags(reinterpret_cast<uint2*>(p)), cols(reinterpret_cast<Column*>(p + (size_t)tiles * PARTS * KS * 32 * 8)) {}
+  // tiles t0 .. t0 + nt - 1, a warp each
+  template <bool EX>
+  __device__ __forceinline__ void load(const AttArgs& A, const Req& rq, int h, int t0, int nt, int warps) const {
+    const int lane = threadIdx.x & 31;
+    for (int x = threadIdx.x >> 5; x < nt; x += warps) {
+      QTile<DT, HD> q;
+      q.load(A, rq, h, t0 + x, lane);
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        frags[((x * PARTS) * KS + s) * 32 + lane] = make_uint2(q.hi[s][0], q.hi[s][1]);
+        if (PARTS == 2)
+          frags[((x * PARTS + 1) * KS + s) * 32 + lane] =
+              make_uint2(q.lo[PARTS == 2 ? s : 0][0], q.lo[PARTS == 2 ? s : 0][1]);
       }
+      if ((lane & 3) == 0) cols[x * 8 + (lane >> 2)] = column_of<EX>(A, rq, h, (t0 + x) * 8 + (lane >> 2), q.qf);
     }
   }
-  float* const out = S.score + ((int64_t)r * A.Hkv + h) * S.stride;
-  // score of token `key` from the sum of its weights
-  auto put = [&](int key, float sum) {
-    if (key >= rq.len) return;
-    const float old = key < rq.p0 && S.decay != 0.f ? out[key] : 0.f;
-    out[key] = fmaf(S.decay, old, sum);
-  };
-  // weights of one block for one tile: tokens g and g + 8
-  auto tile_sum = [&](const float (&c)[4], const Column& x, const Column& y, float ks, int key0, bool edge, float& s0,
-                      float& s1) {
-    float w[4];
-    w[0] = weight_of<EX>(A, x, c[0], ks, key0 + g);
-    w[1] = weight_of<EX>(A, y, c[1], ks, key0 + g);
-    w[2] = weight_of<EX>(A, x, c[2], ks, key0 + g + 8);
-    w[3] = weight_of<EX>(A, y, c[3], ks, key0 + g + 8);
-    if (edge) {
-      w[0] = key0 + g <= x.hi && key0 + g >= x.lo ? w[0] : 0.f;
-      w[1] = key0 + g <= y.hi && key0 + g >= y.lo ? w[1] : 0.f;
-      w[2] = key0 + g + 8 <= x.hi && key0 + g + 8 >= x.lo ? w[2] : 0.f;
-      w[3] = key0 + g + 8 <= y.hi && key0 + g + 8 >= y.lo ? w[3] : 0.f;
-    }
-    s0 += w[0] + w[1];
-    s1 += w[2] + w[3];
-  };
-  const int nq = rq.n * A.GH, tiles = (nq + 7) >> 3;
-  if (ONE) {
-    QTile<DT, HD> q;
-    q.load(A, rq, h, 0, lane);
-    Column col[2];
+};
+
+// Requests of a few tiles of queries (8 rows x heads each).  Each warp's codes go through a ring of its own in
+// shared memory: a lane copies its own pieces (cp.async) and reads them back, without a barrier.  ONE: a single
+// tile, whose fragments stay in registers (remainders of fp32 rows in shared memory); else they lie in
+// shared memory, behind the ring.
+template <int HD>
+struct Ring {
+  static constexpr int STAGES = 4, STAGE = 16 * HD, BYTES = 8 * STAGES * STAGE;  // of 8 warps
+};
+
+template <int CT, int DT, int HD, bool EX, bool ONE>
+__global__ void __launch_bounds__(256, 3) kv8_score_few_kernel(const __grid_constant__ ScoreArgs S) {
+  constexpr int W = 8, KS = HD / 16, NV = HD / 64, PARTS = DT == DDL_T_F32 ? 2 : 1;
+  constexpr bool HL = DT == DDL_T_F32;
+  using Rg = Ring<HD>;
+  extern __shared__ __align__(16) uint8_t sc_smem[];
+  const AttArgs& A = S.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  pdl_trigger();
+  pdl_wait();
+  Part<W> part;
+  if (!part.load(S)) return;
+  const Req& rq = part.rq;
+  const int nq = rq.n * A.GH;
+  const uint32_t ring = smem_addr(sc_smem) + warp * Rg::STAGES * Rg::STAGE + lane * 16;
+  auto fetch = [&](int i) {
+    const int32_t blk = i < SC_MAX_BLOCKS ? __shfl_sync(FULL, part.place, i) : -1;
+    if (blk >= 0) {  // (none past the last)
+      const uint32_t dst = ring + (i % Rg::STAGES) * Rg::STAGE;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int qi = 2 * t + c, row = qi < nq ? group_row(A, qi) : 0;
-      const float lse = qi < nq ? A.lse[(int64_t)(rq.row0 + row) * A.Hq + h * A.GH + qi - row * A.GH] : 0.f;
-      col[c] = column_of<EX>(A, rq, h, qi, __shfl_sync(FULL, q.qf, 4 * qi), lse);
+      for (int j = 0; j < 2 * NV; ++j) cp_async16(dst + j * 512, KBlock<HD>::piece(A.k, blk, j));
     }
-    // tokens that every query sees: blocks inside need no masks
-    const int all_hi = nq == 8 ? rq.p0 : -1;
-    const int64_t lo64 = first_seen(A, rq, nq - 1);
-    KBlock<HD> k, n;
-    int32_t blk = __shfl_sync(FULL, place, 0);
-    if (blk >= 0) n.load(A.k, blk, lane);
-    for (int i = 0; i < mine; ++i) {
-      const int32_t at = blk;
-      k = n;
-      blk = i + 1 < 32 ? __shfl_sync(FULL, place, (i + 1) & 31) : -1;
-      if (blk >= 0) n.load(A.k, blk, lane);
-      const int key0 = block_of(i) * 16;
-      const float ks = __shfl_sync(FULL, scale, i);
-      float s0 = 0.f, s1 = 0.f;
-      if (at >= 0) {
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < Rg::STAGES - 1; ++i) fetch(i);
+  // the token of this lane (t 0: g, t 1: g + 8) of block i, and its old score two blocks ahead
+  auto key_of = [&](int i) { return part.block(i) * 16 + g + (t == 1 ? 8 : 0); };
+  auto old_of = [&](int i) { return t < 2 && i < part.mine ? part.old(S, key_of(i)) : 0.f; };
+  float was = old_of(0), next = old_of(1);
+  const TileSmem<DT, HD> tile(sc_smem + Rg::BYTES, S.tiles);
+  uint2* const lo = tile.frags + warp * KS * 32;  // ONE: the warp's own
+  QTile<DT, HD> q;
+  Column col[2];
+  if (ONE) {
+    q.load(A, rq, part.h, 0, lane);
+    if (HL) {
+#pragma unroll
+      for (int s = 0; s < KS; ++s) lo[s * 32 + lane] = make_uint2(q.lo[HL ? s : 0][0], q.lo[HL ? s : 0][1]);
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) col[c] = column_of<EX>(A, rq, part.h, 2 * t + c, __shfl_sync(FULL, q.qf, 4 * (2 * t + c)));
+  } else {
+    tile.template load<EX>(A, rq, part.h, 0, (nq + 7) >> 3, W);
+    __syncthreads();
+  }
+#pragma unroll 1
+  for (int i = 0; i < part.mine; ++i) {
+    fetch(i + Rg::STAGES - 1);
+    const float ahead = old_of(i + 2);
+    const int32_t at = __shfl_sync(FULL, part.place, i);
+    const float ks = __shfl_sync(FULL, part.scale, i);
+    const int key0 = part.block(i) * 16;
+    float s0 = 0.f, s1 = 0.f;
+    cp_async_wait<Rg::STAGES - 1>();
+    if (at >= 0) {
+      KBlock<HD> k;
+      const uint32_t src = ring + (i % Rg::STAGES) * Rg::STAGE;
+#pragma unroll
+      for (int j = 0; j < 2 * NV; ++j) k.v[j / NV][j % NV] = lds128(src + j * 512);
+      uint32_t a[KS][4];
+#pragma unroll
+      for (int s = 0; s < KS; ++s) k.template frag<CT>(s, a[s]);
+#pragma unroll 1
+      for (int x = 0; x < (ONE ? 1 : (nq + 7) >> 3); ++x) {
+        const int q0 = x * 8, q1 = min(q0 + 7, nq - 1);
+        if (!ONE && (key0 > rq.p0 + group_row(A, q1) || key0 + 15 < first_seen(A, rq, q0))) continue;  // nobody sees it
         float c[4] = {0.f, 0.f, 0.f, 0.f}, c2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-          uint32_t a[4];
-          k.template frag<CT>(s, a);
-          mma_f16((s & 1) ? c2 : c, a[0], a[1], a[2], a[3], q.hi[s][0], q.hi[s][1]);
-          if (QTile<DT, HD>::HL)
-            mma_f16((s & 1) ? c2 : c, a[0], a[1], a[2], a[3], q.lo[QTile<DT, HD>::HL ? s : 0][0],
-                    q.lo[QTile<DT, HD>::HL ? s : 0][1]);
+          const uint2 b = ONE ? make_uint2(q.hi[s][0], q.hi[s][1]) : tile.frags[(x * PARTS * KS + s) * 32 + lane];
+          mma_f16((s & 1) ? c2 : c, a[s][0], a[s][1], a[s][2], a[s][3], b.x, b.y);
+          if (HL) {
+            const uint2 b2 = ONE ? lo[s * 32 + lane] : tile.frags[((x * PARTS + 1) * KS + s) * 32 + lane];
+            mma_f16((s & 1) ? c2 : c, a[s][0], a[s][1], a[s][2], a[s][3], b2.x, b2.y);
+          }
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) c[j] += c2[j];
-        const bool edge = key0 + 15 > all_hi || key0 < lo64;
-        tile_sum(c, col[0], col[1], ks, key0, edge, s0, s1);
-        s0 += __shfl_xor_sync(FULL, s0, 1);
-        s1 += __shfl_xor_sync(FULL, s1, 1);
-        s0 += __shfl_xor_sync(FULL, s0, 2);
-        s1 += __shfl_xor_sync(FULL, s1, 2);
+        // blocks that every query sees, in full tiles, need no masks
+        const bool edge = q0 + 7 >= nq || key0 + 15 > rq.p0 + group_row(A, q0) || key0 < first_seen(A, rq, q1);
+        if (ONE) weights<EX>(A, c, col[0], col[1], ks, key0 + g, edge);
+        else weights<EX>(A, c, tile.cols[q0 + 2 * t], tile.cols[q0 + 2 * t + 1], ks, key0 + g, edge);
+        s0 += c[0] + c[1];
+        s1 += c[2] + c[3];
       }
-      if (block_of(i) < first) continue;
-      if (t == 0) put(key0 + g, s0);
-      if (t == 1) put(key0 + g + 8, s1);
+      reduce_rows(s0, s1);
     }
-  } else {
-    constexpr int PARTS = TileSmem<DT, HD>::PARTS;
-    uint2* const frags = reinterpret_cast<uint2*>(sc_smem);  // [tile][part][k-step][lane]
-    Column* const cols = reinterpret_cast<Column*>(sc_smem + (size_t)smem_tiles * PARTS * KS * 32 * 8);
-    for (int i = threadIdx.x; i < SC_WARPS * S.wb * 16; i += SC_WARPS * 32) sums[ONE ? 0 : i] = 0.f;
-    for (int t0 = 0; t0 < tiles; t0 += smem_tiles) {
-      const int nt = min(smem_tiles, tiles - t0);
-      __syncthreads();
-      for (int x = warp; x < nt; x += SC_WARPS) {
-        QTile<DT, HD> q;
-        q.load(A, rq, h, t0 + x, lane);
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          frags[((x * PARTS) * KS + s) * 32 + lane] = make_uint2(q.hi[s][0], q.hi[s][1]);
-          if (PARTS == 2)
-            frags[((x * PARTS + 1) * KS + s) * 32 + lane] =
-                make_uint2(q.lo[PARTS == 2 ? s : 0][0], q.lo[PARTS == 2 ? s : 0][1]);
-        }
-        if (t == 0) {
-          const int qi = (t0 + x) * 8 + g, row = qi < nq ? group_row(A, qi) : 0;
-          const float lse = qi < nq ? A.lse[(int64_t)(rq.row0 + row) * A.Hq + h * A.GH + qi - row * A.GH] : 0.f;
-          cols[x * 8 + g] = column_of<EX>(A, rq, h, qi, q.qf, lse);
-        }
-      }
-      __syncthreads();
-      for (int i = 0; i < mine; ++i) {
-        const int32_t at = __shfl_sync(FULL, place, i);
-        if (at < 0) continue;
-        const int key0 = block_of(i) * 16;
-        const float ks = __shfl_sync(FULL, scale, i);
-        KBlock<HD> k;
-        k.load(A.k, at, lane);
-        uint32_t a[KS][4];
-#pragma unroll
-        for (int s = 0; s < KS; ++s) k.template frag<CT>(s, a[s]);
-        float s0 = 0.f, s1 = 0.f;
-        for (int x = 0; x < nt; ++x) {
-          const int q0 = (t0 + x) * 8, q1 = min(q0 + 7, nq - 1);
-          const int last = rq.p0 + group_row(A, q1);
-          const int64_t from = first_seen(A, rq, q0);
-          if (key0 > last || key0 + 15 < from) continue;  // no query of the tile sees the block
-          float c[4] = {0.f, 0.f, 0.f, 0.f}, c2[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int s = 0; s < KS; ++s) {
-            const uint2 b = frags[((x * PARTS) * KS + s) * 32 + lane];
-            mma_f16((s & 1) ? c2 : c, a[s][0], a[s][1], a[s][2], a[s][3], b.x, b.y);
-            if (PARTS == 2) {
-              const uint2 b2 = frags[((x * PARTS + 1) * KS + s) * 32 + lane];
-              mma_f16((s & 1) ? c2 : c, a[s][0], a[s][1], a[s][2], a[s][3], b2.x, b2.y);
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) c[j] += c2[j];
-          const bool edge = q0 + 7 >= nq || key0 + 15 > rq.p0 + group_row(A, q0) || key0 < first_seen(A, rq, q1);
-          tile_sum(c, cols[x * 8 + 2 * t], cols[x * 8 + 2 * t + 1], ks, key0, edge, s0, s1);
-        }
-        s0 += __shfl_xor_sync(FULL, s0, 1);
-        s1 += __shfl_xor_sync(FULL, s1, 1);
-        s0 += __shfl_xor_sync(FULL, s0, 2);
-        s1 += __shfl_xor_sync(FULL, s1, 2);
-        float* const mysum = sums + (ONE ? 0 : (warp + SC_WARPS * i) * 16);
-        if (t == 0) mysum[g] += s0;
-        if (t == 1) mysum[g + 8] += s1;
-      }
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < SC_WARPS * S.wb * 16; i += SC_WARPS * 32)
-      if (c0 + (i >> 4) >= first) put(c0 * 16 + i, sums[ONE ? 0 : i]);
+    if (t < 2 && part.block(i) >= part.first) part.put(S, key_of(i), was, t ? s1 : s0);
+    was = next;
+    next = ahead;
   }
 }
 
-template <int CT, int DT, int HD>
-const void* score_fn(bool ex, bool one) {
-  if (one) return ex ? (const void*)kv8_score_kernel<CT, DT, HD, true, true> : (const void*)kv8_score_kernel<CT, DT, HD, false, true>;
-  return ex ? (const void*)kv8_score_kernel<CT, DT, HD, true, false> : (const void*)kv8_score_kernel<CT, DT, HD, false, false>;
-}
-template <int CT>
-const void* score_fn(int dt, int hd, bool ex, bool one) {
-  if (hd == 128)
-    return dt == DDL_T_F32    ? score_fn<CT, DDL_T_F32, 128>(ex, one)
-           : dt == DDL_T_BF16 ? score_fn<CT, DDL_T_BF16, 128>(ex, one)
-                              : score_fn<CT, DDL_T_F16, 128>(ex, one);
-  return dt == DDL_T_F32    ? score_fn<CT, DDL_T_F32, 64>(ex, one)
-         : dt == DDL_T_BF16 ? score_fn<CT, DDL_T_BF16, 64>(ex, one)
-                            : score_fn<CT, DDL_T_F16, 64>(ex, one);
+// Requests of several tiles of queries.  The tiles' fragments lie in shared memory, S.tiles at a time;
+// each warp holds the fragments of two blocks of K in registers and takes them past every tile.
+constexpr int MANY_WARPS = 16, MANY_BLOCKS = 16;  // blocks a warp takes at most
+constexpr int TILE_SMEM = 142 * 1024;  // 64 tiles of 16-bit rows of 128
+constexpr int FEW_16 = 16, FEW_F32 = 8;  // tiles of the ring kernel at most
+
+template <int CT, int DT, int HD, bool EX>
+__global__ void __launch_bounds__(MANY_WARPS * 32, 1) kv8_score_many_kernel(const __grid_constant__ ScoreArgs S) {
+  constexpr int W = MANY_WARPS, KS = HD / 16, NV = HD / 64, PARTS = TileSmem<DT, HD>::PARTS;
+  extern __shared__ __align__(16) uint8_t sc_smem[];
+  __shared__ float sums[W * MANY_BLOCKS * 16];
+  const AttArgs& A = S.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  pdl_trigger();
+  pdl_wait();
+  Part<W> part;
+  if (!part.load(S)) return;
+  const Req& rq = part.rq;
+  const int nq = rq.n * A.GH, tiles = (nq + 7) >> 3;
+  const TileSmem<DT, HD> tile(sc_smem, S.tiles);
+  const uint2* const frags = tile.frags;
+  const Column* const cols = tile.cols;
+  for (int i = threadIdx.x; i < W * S.wb * 16; i += W * 32) sums[i] = 0.f;
+  for (int t0 = 0; t0 < tiles; t0 += S.tiles) {
+    const int nt = min(S.tiles, tiles - t0);
+    __syncthreads();
+    tile.template load<EX>(A, rq, part.h, t0, nt, W);
+    __syncthreads();
+    for (int i = 0; i < part.mine; i += 2) {
+      const int32_t at0 = __shfl_sync(FULL, part.place, i), at1 = __shfl_sync(FULL, part.place, i + 1);
+      if (at0 < 0 && at1 < 0) continue;
+      const float ks0 = __shfl_sync(FULL, part.scale, i), ks1 = __shfl_sync(FULL, part.scale, i + 1);
+      const int key0 = part.block(i) * 16, key1 = key0 + W * 16;
+      uint32_t a[2][KS][4];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        KBlock<HD> k;
+        const int32_t at = b ? at1 : at0;
+#pragma unroll
+        for (int j = 0; j < 2 * NV; ++j)
+          k.v[j / NV][j % NV] = at >= 0 ? *reinterpret_cast<const uint4*>(KBlock<HD>::piece(A.k, at, j)) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) k.template frag<CT>(s, a[b][s]);
+      }
+      float s[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll 1
+      for (int x = 0; x < nt; ++x) {
+        const int q0 = (t0 + x) * 8, q1 = min(q0 + 7, nq - 1);
+        const int last = rq.p0 + group_row(A, q1), seen = rq.p0 + group_row(A, q0);  // any sees up to, all see up to
+        const int64_t from = first_seen(A, rq, q0), all = first_seen(A, rq, q1);
+        const bool in0 = at0 >= 0 && key0 <= last && key0 + 15 >= from, in1 = at1 >= 0 && key1 <= last && key1 + 15 >= from;
+        if (!in0 && !in1) continue;  // no query of the tile sees the blocks
+        float c[2][4];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) c[b][j] = 0.f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const uint2 f = frags[((x * PARTS) * KS + k) * 32 + lane];
+          mma_f16(c[0], a[0][k][0], a[0][k][1], a[0][k][2], a[0][k][3], f.x, f.y);
+          mma_f16(c[1], a[1][k][0], a[1][k][1], a[1][k][2], a[1][k][3], f.x, f.y);
+          if (PARTS == 2) {
+            const uint2 f2 = frags[((x * PARTS + 1) * KS + k) * 32 + lane];
+            mma_f16(c[0], a[0][k][0], a[0][k][1], a[0][k][2], a[0][k][3], f2.x, f2.y);
+            mma_f16(c[1], a[1][k][0], a[1][k][1], a[1][k][2], a[1][k][3], f2.x, f2.y);
+          }
+        }
+        const Column cx = cols[x * 8 + 2 * t], cy = cols[x * 8 + 2 * t + 1];
+        const bool cut = q0 + 7 >= nq;
+        if (in0) {
+          weights<EX>(A, c[0], cx, cy, ks0, key0 + g, cut || key0 + 15 > seen || key0 < all);
+          s[0][0] += c[0][0] + c[0][1];
+          s[0][1] += c[0][2] + c[0][3];
+        }
+        if (in1) {
+          weights<EX>(A, c[1], cx, cy, ks1, key1 + g, cut || key1 + 15 > seen || key1 < all);
+          s[1][0] += c[1][0] + c[1][1];
+          s[1][1] += c[1][2] + c[1][3];
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        reduce_rows(s[b][0], s[b][1]);
+        if (i + b < part.mine) {
+          float* const to = sums + (warp + W * (i + b)) * 16;
+          if (t == 0) to[g] += s[b][0];
+          if (t == 1) to[g + 8] += s[b][1];
+        }
+      }
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < W * S.wb * 16; i += W * 32) {
+    const int key = part.c0 * 16 + i;
+    if (part.c0 + (i >> 4) >= part.first) part.put(S, key, part.old(S, key), sums[i]);
+  }
 }
 
-template <int HD>
-int tile_bytes(int dt, int need, int& tiles) {
-  const bool f32 = dt == DDL_T_F32;
-  const int per = f32 ? TileSmem<DDL_T_F32, HD>::PER : TileSmem<DDL_T_BF16, HD>::PER;
-  tiles = need < TILE_SMEM / per ? need : TILE_SMEM / per;
-  return tiles * per;
+enum { ONE_TILE, FEW_TILES, MANY_TILES };
+template <int CT, int DT, int HD>
+const void* score_fn(bool ex, int kind) {
+  if (kind == ONE_TILE)
+    return ex ? (const void*)kv8_score_few_kernel<CT, DT, HD, true, true> : (const void*)kv8_score_few_kernel<CT, DT, HD, false, true>;
+  if (kind == FEW_TILES)
+    return ex ? (const void*)kv8_score_few_kernel<CT, DT, HD, true, false> : (const void*)kv8_score_few_kernel<CT, DT, HD, false, false>;
+  return ex ? (const void*)kv8_score_many_kernel<CT, DT, HD, true> : (const void*)kv8_score_many_kernel<CT, DT, HD, false>;
 }
+template <int CT>
+const void* score_fn(int dt, int hd, bool ex, int kind) {
+  if (hd == 128)
+    return dt == DDL_T_F32    ? score_fn<CT, DDL_T_F32, 128>(ex, kind)
+           : dt == DDL_T_BF16 ? score_fn<CT, DDL_T_BF16, 128>(ex, kind)
+                              : score_fn<CT, DDL_T_F16, 128>(ex, kind);
+  return dt == DDL_T_F32    ? score_fn<CT, DDL_T_F32, 64>(ex, kind)
+         : dt == DDL_T_BF16 ? score_fn<CT, DDL_T_BF16, 64>(ex, kind)
+                            : score_fn<CT, DDL_T_F16, 64>(ex, kind);
+}
+// Bytes of a tile's fragments and columns.
+int tile_bytes(bool f32, int hd) { return (f32 ? 2 : 1) * hd / 16 * 32 * 8 + 8 * (int)sizeof(Column); }
 
 }  // namespace
 }  // namespace ddl
@@ -399,23 +537,37 @@ extern "C" int ddl_kv8_score(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, int32
   s.score = score;
   s.stride = score_stride;
   s.decay = decay;
-  const int tiles = (max_rows * a.GH + 7) / 8;
-  const bool one = tiles == 1, ex = opts->softcap > 0.f || opts->slopes;
-  // Blocks a warp takes: as many as leave the machine a few CTAs an SM, since each CTA
-  // begins with a chain of dependent loads (lengths, page, scale, codes) and its queries.
-  const int64_t blocks = ((int64_t)max_len + 15) / 16;
-  s.wb = 1;
-  while (s.wb < 32 && (int64_t)R * H_kv * ((blocks + 2 * SC_WARPS * s.wb - 1) / (2 * SC_WARPS * s.wb)) >= 8 * sms) s.wb *= 2;
-  const int64_t chunks = (blocks + SC_WARPS * s.wb - 1) / (SC_WARPS * s.wb);
-  if (chunks > 0x7fffffffLL) return DDL_ERR_UNSUPPORTED;
-  int smem_tiles = 0, smem = 0;
-  if (!one) smem = head_dim == 128 ? tile_bytes<128>(dtype, tiles, smem_tiles) : tile_bytes<64>(dtype, tiles, smem_tiles);
-  const void* fn = kv->type == DDL_KV8_E4M3 ? score_fn<DDL_KV8_E4M3>(dtype, head_dim, ex, one)
-                                            : score_fn<DDL_KV8_INT8>(dtype, head_dim, ex, one);
-  if (smem > 32 * 1024 &&
-      (st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, TILE_SMEM))))
-    return st;
-  void* args[] = {&s, &smem_tiles};
-  return cuda_status(launch_pdl(fn, dim3((unsigned)chunks, (unsigned)H_kv, (unsigned)R), dim3(SC_WARPS * 32), args,
-                                (size_t)smem, (cudaStream_t)stream));
+  const int tiles = (max_rows * a.GH + 7) / 8, per = tile_bytes(dtype == DDL_T_F32, head_dim);
+  const bool f32 = dtype == DDL_T_F32, ex = opts->softcap > 0.f || opts->slopes;
+  const int kind = tiles == 1 ? ONE_TILE : tiles <= (f32 ? FEW_F32 : FEW_16) ? FEW_TILES : MANY_TILES;
+  const int64_t blocks = ((int64_t)max_len + 15) / 16, units = (int64_t)R * H_kv;
+  size_t smem;
+  int warps;
+  if (kind == MANY_TILES) {
+    warps = MANY_WARPS;
+    s.tiles = tiles < TILE_SMEM / per ? tiles : TILE_SMEM / per;
+    smem = (size_t)s.tiles * per;
+    // about one CTA an SM: the fragments of all queries are what a CTA begins with
+    s.wb = 2;
+    while (s.wb < MANY_BLOCKS && units * ((blocks + warps * s.wb - 1) / (warps * s.wb)) > sms) s.wb += 2;
+  } else {
+    // A CTA begins with a chain of dependent loads (lengths, page, scale, codes) and its queries: as many blocks a warp as
+    // leave one wave of CTAs (ragged lengths come to about 5/8 of the bound), but no more than 12, so that long
+    // requests spread.  Blocks a warp 2 / 4 / 8 / 12 / 16: 64 requests of up to 8192, 64/8 heads 86 / 64 / 55 / 53 / 55 us, 16 of up
+    // to 4096 13.8 / 11.8 / 10.1 / 13.0 / 15.1, 1 of 8192 5.4 / 5.8 / 6.7 / 8.5 / 9.7.
+    warps = 8;
+    s.tiles = tiles;
+    smem = (size_t)(head_dim == 128 ? Ring<128>::BYTES : Ring<64>::BYTES) +
+           (kind == FEW_TILES ? (size_t)tiles * per : f32 ? (size_t)8 * head_dim / 16 * 32 * 8 : 0);
+    const int64_t ctas = sms * (smem > 74 * 1024 ? 2 : 3) * (R > 1 ? 8 : 5) / 5;
+    const int64_t chunks = ctas / units > 1 ? ctas / units : 1, wb = (blocks + warps * chunks - 1) / (warps * chunks);
+    s.wb = (int32_t)(wb < SC_MAX_BLOCKS ? wb : SC_MAX_BLOCKS);
+  }
+  const int64_t chunks = (blocks + warps * s.wb - 1) / (warps * s.wb);
+  const void* fn = kv->type == DDL_KV8_E4M3 ? score_fn<DDL_KV8_E4M3>(dtype, head_dim, ex, kind)
+                                            : score_fn<DDL_KV8_INT8>(dtype, head_dim, ex, kind);
+  if ((st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))) return st;
+  void* args[] = {&s};
+  return cuda_status(launch_pdl(fn, dim3((unsigned)chunks, (unsigned)H_kv, (unsigned)R), dim3((unsigned)warps * 32), args,
+                                smem, (cudaStream_t)stream));
 }
