@@ -16,63 +16,12 @@
 // after the last query.
 #include <cuda_bf16.h>
 
-#include "ddl_kv8_attn.h"
+#include "ddl_kv8_score.h"
 
 namespace ddl {
 namespace {
 
 constexpr int SC_MAX_BLOCKS = 12;  // blocks of 16 tokens a warp takes at most (a lane each)
-
-struct ScoreArgs {
-  AttArgs a;
-  float* score;    // [R][H_kv][stride]
-  int64_t stride;
-  float decay;
-  int32_t wb;      // blocks a warp takes
-  int32_t tiles;   // query tiles whose fragments fit shared memory at a time (several-tile kernel)
-};
-
-// What the queries of a tile need apart from their fragments.
-struct Column {
-  float cf;       // factor of the MMA's sum (times the block's scale): log2 units, or softcap's argument
-  float lse2;     // log2 e times lse; +inf for a query without keys
-  float slope;    // log2 units a token
-  int hi, lo;     // last and first token it sees
-};
-
-// Query qi of request rq for K/V head h.
-template <bool EX>
-__device__ __forceinline__ Column column_of(const AttArgs& A, const Req& rq, int h, int qi, float qf) {
-  Column c;
-  const bool has = qi < rq.n * A.GH;
-  const int row = has ? group_row(A, qi) : 0;
-  const int64_t p = (int64_t)rq.p0 + row, lo = A.window > 0 ? p - A.window + 1 : 0;
-  c.hi = has ? (int)p : -1;
-  c.lo = lo > 0 ? (int)lo : 0;
-  c.slope = EX && A.slopes && has ? A.slopes[h * A.GH + qi - row * A.GH] * LOG2E : 0.f;
-  c.cf = qf * A.scale;
-  if (EX && A.softcap > 0.f) c.cf = __fdiv_rn(c.cf, A.softcap);
-  else c.cf *= LOG2E;
-  const float lse = has ? A.lse[(int64_t)(rq.row0 + row) * A.Hq + h * A.GH + qi - row * A.GH] : 0.f;
-  c.lse2 = lse == -INFINITY ? INFINITY : lse * LOG2E;
-  return c;
-}
-
-// tanh of four numbers: below 0.3 its series up to x^9 (the next term is 2^-24 of it), which is
-// relative to x at any cap; else, where a lane of the warp has a larger one, tanhf.
-__device__ __forceinline__ void tanh4(float (&x)[4]) {
-  const float top = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
-  if (__any_sync(FULL, !(top < 0.3f))) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = tanhf(x[j]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float y = x[j] * x[j];
-      x[j] = fmaf(x[j] * y, fmaf(y, fmaf(y, fmaf(y, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f), x[j]);
-    }
-  }
-}
 
 // Weights exp(score - lse) of tokens key, key + 8 (c 0, 1 and 2, 3) for two queries: c are the MMA's sums.
 // All lanes of the warp call it.
@@ -91,7 +40,7 @@ __device__ __forceinline__ void weights(const AttArgs& A, float (&c)[4], const C
     c[2] *= fx;
     c[3] *= fy;
     if (A.softcap > 0.f) {
-      tanh4(c);
+      tanh_of(c);
       const float cap = A.softcap * LOG2E;
 #pragma unroll
       for (int j = 0; j < 4; ++j) c[j] *= cap;
@@ -357,113 +306,14 @@ __global__ void __launch_bounds__(256, 3) kv8_score_few_kernel(const __grid_cons
   }
 }
 
-// Requests of several tiles of queries.  The tiles' fragments lie in shared memory, S.tiles at a time;
-// each warp holds the fragments of two blocks of K in registers and takes them past every tile.
-constexpr int MANY_WARPS = 16, MANY_BLOCKS = 16;  // blocks a warp takes at most
-constexpr int TILE_SMEM = 142 * 1024;  // 64 tiles of 16-bit rows of 128
-constexpr int FEW_16 = 16, FEW_F32 = 8;  // tiles of the ring kernel at most
-
-template <int CT, int DT, int HD, bool EX>
-__global__ void __launch_bounds__(MANY_WARPS * 32, 1) kv8_score_many_kernel(const __grid_constant__ ScoreArgs S) {
-  constexpr int W = MANY_WARPS, KS = HD / 16, NV = HD / 64, PARTS = TileSmem<DT, HD>::PARTS;
-  extern __shared__ __align__(16) uint8_t sc_smem[];
-  __shared__ float sums[W * MANY_BLOCKS * 16];
-  const AttArgs& A = S.a;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  pdl_trigger();
-  pdl_wait();
-  Part<W> part;
-  if (!part.load(S)) return;
-  const Req& rq = part.rq;
-  const int nq = rq.n * A.GH, tiles = (nq + 7) >> 3;
-  const TileSmem<DT, HD> tile(sc_smem, S.tiles);
-  const uint2* const frags = tile.frags;
-  const Column* const cols = tile.cols;
-  for (int i = threadIdx.x; i < W * S.wb * 16; i += W * 32) sums[i] = 0.f;
-  for (int t0 = 0; t0 < tiles; t0 += S.tiles) {
-    const int nt = min(S.tiles, tiles - t0);
-    __syncthreads();
-    tile.template load<EX>(A, rq, part.h, t0, nt, W);
-    __syncthreads();
-    for (int i = 0; i < part.mine; i += 2) {
-      const int32_t at0 = __shfl_sync(FULL, part.place, i), at1 = __shfl_sync(FULL, part.place, i + 1);
-      if (at0 < 0 && at1 < 0) continue;
-      const float ks0 = __shfl_sync(FULL, part.scale, i), ks1 = __shfl_sync(FULL, part.scale, i + 1);
-      const int key0 = part.block(i) * 16, key1 = key0 + W * 16;
-      uint32_t a[2][KS][4];
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        KBlock<HD> k;
-        const int32_t at = b ? at1 : at0;
-#pragma unroll
-        for (int j = 0; j < 2 * NV; ++j)
-          k.v[j / NV][j % NV] = at >= 0 ? *reinterpret_cast<const uint4*>(KBlock<HD>::piece(A.k, at, j)) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int s = 0; s < KS; ++s) k.template frag<CT>(s, a[b][s]);
-      }
-      float s[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-#pragma unroll 1
-      for (int x = 0; x < nt; ++x) {
-        const int q0 = (t0 + x) * 8, q1 = min(q0 + 7, nq - 1);
-        const int last = rq.p0 + group_row(A, q1), seen = rq.p0 + group_row(A, q0);  // any sees up to, all see up to
-        const int64_t from = first_seen(A, rq, q0), all = first_seen(A, rq, q1);
-        const bool in0 = at0 >= 0 && key0 <= last && key0 + 15 >= from, in1 = at1 >= 0 && key1 <= last && key1 + 15 >= from;
-        if (!in0 && !in1) continue;  // no query of the tile sees the blocks
-        float c[2][4];
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) c[b][j] = 0.f;
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const uint2 f = frags[((x * PARTS) * KS + k) * 32 + lane];
-          mma_f16(c[0], a[0][k][0], a[0][k][1], a[0][k][2], a[0][k][3], f.x, f.y);
-          mma_f16(c[1], a[1][k][0], a[1][k][1], a[1][k][2], a[1][k][3], f.x, f.y);
-          if (PARTS == 2) {
-            const uint2 f2 = frags[((x * PARTS + 1) * KS + k) * 32 + lane];
-            mma_f16(c[0], a[0][k][0], a[0][k][1], a[0][k][2], a[0][k][3], f2.x, f2.y);
-            mma_f16(c[1], a[1][k][0], a[1][k][1], a[1][k][2], a[1][k][3], f2.x, f2.y);
-          }
-        }
-        const Column cx = cols[x * 8 + 2 * t], cy = cols[x * 8 + 2 * t + 1];
-        const bool cut = q0 + 7 >= nq;
-        if (in0) {
-          weights<EX>(A, c[0], cx, cy, ks0, key0 + g, cut || key0 + 15 > seen || key0 < all);
-          s[0][0] += c[0][0] + c[0][1];
-          s[0][1] += c[0][2] + c[0][3];
-        }
-        if (in1) {
-          weights<EX>(A, c[1], cx, cy, ks1, key1 + g, cut || key1 + 15 > seen || key1 < all);
-          s[1][0] += c[1][0] + c[1][1];
-          s[1][1] += c[1][2] + c[1][3];
-        }
-      }
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        reduce_rows(s[b][0], s[b][1]);
-        if (i + b < part.mine) {
-          float* const to = sums + (warp + W * (i + b)) * 16;
-          if (t == 0) to[g] += s[b][0];
-          if (t == 1) to[g + 8] += s[b][1];
-        }
-      }
-    }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < W * S.wb * 16; i += W * 32) {
-    const int key = part.c0 * 16 + i;
-    if (part.c0 + (i >> 4) >= part.first) part.put(S, key, part.old(S, key), sums[i]);
-  }
-}
+constexpr int FEW_16 = 4, FEW_F32 = 4;  // tiles of the ring kernel at most
 
 enum { ONE_TILE, FEW_TILES, MANY_TILES };
 template <int CT, int DT, int HD>
 const void* score_fn(bool ex, int kind) {
   if (kind == ONE_TILE)
     return ex ? (const void*)kv8_score_few_kernel<CT, DT, HD, true, true> : (const void*)kv8_score_few_kernel<CT, DT, HD, false, true>;
-  if (kind == FEW_TILES)
-    return ex ? (const void*)kv8_score_few_kernel<CT, DT, HD, true, false> : (const void*)kv8_score_few_kernel<CT, DT, HD, false, false>;
-  return ex ? (const void*)kv8_score_many_kernel<CT, DT, HD, true> : (const void*)kv8_score_many_kernel<CT, DT, HD, false>;
+  return ex ? (const void*)kv8_score_few_kernel<CT, DT, HD, true, false> : (const void*)kv8_score_few_kernel<CT, DT, HD, false, false>;
 }
 template <int CT>
 const void* score_fn(int dt, int hd, bool ex, int kind) {
@@ -541,28 +391,31 @@ extern "C" int ddl_kv8_score(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, int32
   const bool f32 = dtype == DDL_T_F32, ex = opts->softcap > 0.f || opts->slopes;
   const int kind = tiles == 1 ? ONE_TILE : tiles <= (f32 ? FEW_F32 : FEW_16) ? FEW_TILES : MANY_TILES;
   const int64_t blocks = ((int64_t)max_len + 15) / 16, units = (int64_t)R * H_kv;
-  size_t smem;
-  int warps;
   if (kind == MANY_TILES) {
-    warps = MANY_WARPS;
-    s.tiles = tiles < TILE_SMEM / per ? tiles : TILE_SMEM / per;
-    smem = (size_t)s.tiles * per;
-    // about one CTA an SM: the fragments of all queries are what a CTA begins with
-    s.wb = 2;
-    while (s.wb < MANY_BLOCKS && units * ((blocks + warps * s.wb - 1) / (warps * s.wb)) > sms) s.wb += 2;
-  } else {
-    // A CTA begins with a chain of dependent loads (lengths, page, scale, codes) and its queries: as many blocks a warp as
-    // leave one wave of CTAs (ragged lengths come to about 5/8 of the bound), but no more than 12, so that long
-    // requests spread.  Blocks a warp 2 / 4 / 8 / 12 / 16: 64 requests of up to 8192, 64/8 heads 86 / 64 / 55 / 53 / 55 us, 16 of up
-    // to 4096 13.8 / 11.8 / 10.1 / 13.0 / 15.1, 1 of 8192 5.4 / 5.8 / 6.7 / 8.5 / 9.7.
-    warps = 8;
-    s.tiles = tiles;
-    smem = (size_t)(head_dim == 128 ? Ring<128>::BYTES : Ring<64>::BYTES) +
-           (kind == FEW_TILES ? (size_t)tiles * per : f32 ? (size_t)8 * head_dim / 16 * 32 * 8 : 0);
-    const int64_t ctas = sms * (smem > 74 * 1024 ? 2 : 3) * (R > 1 ? 8 : 5) / 5;
-    const int64_t chunks = ctas / units > 1 ? ctas / units : 1, wb = (blocks + warps * chunks - 1) / (warps * chunks);
-    s.wb = (int32_t)(wb < SC_MAX_BLOCKS ? wb : SC_MAX_BLOCKS);
+    // queries at a time: what 128 KB hold (with remainders of fp32 rows)
+    const int most = 128 * 1024 / (head_dim * 2 * (f32 ? 2 : 1)), nq = (max_rows * a.GH + 15) & ~15;
+    s.tiles = nq < most ? nq : most;
+    s.wait_ns = wait_limit_ns();
+    // tiles of 128 tokens a warpgroup takes: about one wave of CTAs, each of which begins with all queries
+    const int64_t tok_tiles = ((int64_t)max_len + 127) / 128;
+    int64_t ctas = sms * (R > 1 ? 8 : 5) / 5 / units;
+    ctas = ctas < 1 ? 1 : ctas;
+    const int64_t wb = (tok_tiles + 2 * ctas - 1) / (2 * ctas);
+    s.wb = (int32_t)(wb < SCORE_TC_TILES ? wb : SCORE_TC_TILES);
+    const int64_t chunks = (tok_tiles + 2 * s.wb - 1) / (2 * s.wb);
+    return kv8_score_tc_launch(s, kv->type, dtype, ex, (unsigned)chunks, stream);
   }
+  // A CTA begins with a chain of dependent loads (lengths, page, scale, codes) and its queries: as many blocks a warp as
+  // leave one wave of CTAs (ragged lengths come to about 5/8 of the bound), but no more than 12, so that long
+  // requests spread.  Blocks a warp 2 / 4 / 8 / 12 / 16: 64 requests of up to 8192, 64/8 heads 86 / 64 / 55 / 53 / 55 us, 16 of up
+  // to 4096 13.8 / 11.8 / 10.1 / 13.0 / 15.1, 1 of 8192 5.4 / 5.8 / 6.7 / 8.5 / 9.7.
+  constexpr int warps = 8;
+  s.tiles = tiles;
+  const size_t smem = (size_t)(head_dim == 128 ? Ring<128>::BYTES : Ring<64>::BYTES) +
+                      (kind == FEW_TILES ? (size_t)tiles * per : f32 ? (size_t)8 * head_dim / 16 * 32 * 8 : 0);
+  const int64_t ctas = sms * (smem > 74 * 1024 ? 2 : 3) * (R > 1 ? 8 : 5) / 5;
+  const int64_t each = ctas / units > 1 ? ctas / units : 1, wb = (blocks + warps * each - 1) / (warps * each);
+  s.wb = (int32_t)(wb < SC_MAX_BLOCKS ? wb : SC_MAX_BLOCKS);
   const int64_t chunks = (blocks + warps * s.wb - 1) / (warps * s.wb);
   const void* fn = kv->type == DDL_KV8_E4M3 ? score_fn<DDL_KV8_E4M3>(dtype, head_dim, ex, kind)
                                             : score_fn<DDL_KV8_INT8>(dtype, head_dim, ex, kind);
