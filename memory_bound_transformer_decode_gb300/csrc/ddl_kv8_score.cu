@@ -89,8 +89,7 @@ struct Part {
         const int32_t page = A.table[(int64_t)r * A.per + (b >> bshift)];
         if (page >= 0 && page < A.pages) {
           place = (int32_t)((((int64_t)page * A.Hkv + h) << bshift) + (b & ((1 << bshift) - 1)));
-          scale = A.ks[place];
-          if (!(fabsf(scale) < INFINITY)) scale = __uint_as_float(0x7fffffffu);
+          scale = A.ks[place];  // (looked at where it is used, when the codes are on their way)
         } else if (A.bad) {
           atomicOr(A.bad, 1);
         }
@@ -263,7 +262,8 @@ __global__ void __launch_bounds__(256, 3) kv8_score_few_kernel(const __grid_cons
     fetch(i + Rg::STAGES - 1);
     const float ahead = old_of(i + 2);
     const int32_t at = __shfl_sync(FULL, part.place, i);
-    const float ks = __shfl_sync(FULL, part.scale, i);
+    float ks = __shfl_sync(FULL, part.scale, i);
+    if (!(fabsf(ks) < INFINITY)) ks = __uint_as_float(0x7fffffffu);
     const int key0 = part.block(i) * 16;
     float s0 = 0.f, s1 = 0.f;
     cp_async_wait<Rg::STAGES - 1>();
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(256, 3) kv8_score_few_kernel(const __grid_cons
   }
 }
 
-constexpr int FEW_16 = 4, FEW_F32 = 4;  // tiles of the ring kernel at most
+constexpr int FEW_16 = 8, FEW_F32 = 4;  // tiles of the ring kernel at most
 
 enum { ONE_TILE, FEW_TILES, MANY_TILES };
 template <int CT, int DT, int HD>
@@ -392,18 +392,8 @@ extern "C" int ddl_kv8_score(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, int32
   const int kind = tiles == 1 ? ONE_TILE : tiles <= (f32 ? FEW_F32 : FEW_16) ? FEW_TILES : MANY_TILES;
   const int64_t blocks = ((int64_t)max_len + 15) / 16, units = (int64_t)R * H_kv;
   if (kind == MANY_TILES) {
-    // queries at a time: what 128 KB hold (with remainders of fp32 rows)
-    const int most = 128 * 1024 / (head_dim * 2 * (f32 ? 2 : 1)), nq = (max_rows * a.GH + 15) & ~15;
-    s.tiles = nq < most ? nq : most;
     s.wait_ns = wait_limit_ns();
-    // tiles of 128 tokens a warpgroup takes: about one wave of CTAs, each of which begins with all queries
-    const int64_t tok_tiles = ((int64_t)max_len + 127) / 128;
-    int64_t ctas = sms * (R > 1 ? 8 : 5) / 5 / units;
-    ctas = ctas < 1 ? 1 : ctas;
-    const int64_t wb = (tok_tiles + 2 * ctas - 1) / (2 * ctas);
-    s.wb = (int32_t)(wb < SCORE_TC_TILES ? wb : SCORE_TC_TILES);
-    const int64_t chunks = (tok_tiles + 2 * s.wb - 1) / (2 * s.wb);
-    return kv8_score_tc_launch(s, kv->type, dtype, ex, (unsigned)chunks, stream);
+    return kv8_score_tc_launch(s, kv->type, dtype, ex, sms, stream);
   }
   // A CTA begins with a chain of dependent loads (lengths, page, scale, codes) and its queries: as many blocks a warp as
   // leave one wave of CTAs (ragged lengths come to about 5/8 of the bound), but no more than 12, so that long

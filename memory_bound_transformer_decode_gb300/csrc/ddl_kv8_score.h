@@ -10,7 +10,7 @@ struct ScoreArgs {
   float* score;    // [R][H_kv][stride]
   int64_t stride;
   float decay;
-  int32_t wb;      // warp kernel: blocks of 16 tokens a warp takes; tcgen05: tiles of 128 tokens a warpgroup takes
+  int32_t wb;      // warp kernel: blocks of 16 tokens a warp takes; tcgen05: tiles of 128 tokens a CTA takes
   int32_t tiles;   // warp kernel: query tiles in shared memory; tcgen05: queries there at a time (a multiple of 16)
   uint64_t wait_ns;
 };
@@ -60,9 +60,8 @@ __device__ __forceinline__ void tanh_of(float (&x)[N]) {
   }
 }
 
-// The tcgen05 kernel: smem bytes of `queries` at a time and `tiles` a warpgroup, and its launch.
-size_t kv8_score_tc_smem(bool f32, int hd, int queries, int tiles);
-int kv8_score_tc_launch(const ScoreArgs& s, int type, int dtype, bool ex, unsigned chunks, void* stream);
-constexpr int SCORE_TC_TILES = 8;  // tiles a warpgroup takes at most
+// Launch of the tcgen05 kernel (s.wb, s.tiles are its own to choose).
+int kv8_score_tc_launch(const ScoreArgs& s, int type, int dtype, bool ex, int sms, void* stream);
+constexpr int SCORE_TC_TILES = 16;  // tiles of 128 tokens a CTA takes at most
 
 }  // namespace ddl

@@ -1,18 +1,18 @@
 // ddl_kv8_score_tc.cu -- the cache scores of requests with many queries (prompt chunks, drafted
 // rows) on the tcgen05 tensor cores.
 //
-// S = K Q^T with 128 tokens as M and up to 128 queries as N, fp16 operands and fp32 accumulators in
+// S = K Q^T with 128 tokens as M and up to 256 queries as N, fp16 operands and fp32 accumulators in
 // tensor memory: a thread then has one token and walks over its queries' scores, so that the sum of
 // weights needs no other thread.  Codes (e4m3 and int8 alike) are exact in fp16; Q is scaled by a power
 // of two per query and split as in the warp kernel, the remainders of fp32 rows as a second set of MMAs.
 //
-// A CTA takes one K/V head of a request, all its queries in shared memory (512 16-bit or 256 fp32 ones of 128
-// at a time), and two independent warpgroups of 128 threads, each with tiles of 128 tokens of its own: while
-// one waits for its MMAs or converts codes, the other takes exponentials.  Each has two accumulators of 128
-// columns: the MMAs of the next 128 queries run while it goes over the last ones.
-//
-// Bound by the exponentials (one MUFU operation a pair: 16 a clock and SM) and the issue of some six instructions
-// a pair.
+// A CTA of four warpgroups takes one K/V head of a request, all its queries in shared memory (512 16-bit or 256
+// fp32 ones of 128 at a time), and tiles of 128 tokens one after the other.  Two accumulators of 256 columns: the
+// MMAs of the next 256 queries run while the warpgroups, each with every fourth 16 columns, go over the last ones;
+// K tiles are converted a tile ahead, their codes and pages loaded two and three ahead.  N is as wide as it goes, since A
+// and B both come from shared memory (128 bytes a clock: 128 x 128 is even with the MMA's own time).  64 rows of 64/8
+// heads on 8192 tokens: warpgroups with tiles and accumulators of their own, two of 2 x 128 columns 31.7 us (two warps a
+// scheduler: issue slots at 31 %), four of 128 21.8 (all wait at once), four of 2 x 64 24.8.
 #include <cuda_bf16.h>
 
 #include "ddl_kv8_score.h"
@@ -20,8 +20,9 @@
 namespace ddl {
 namespace {
 
-constexpr int TOK = 128, QC = 128;     // tokens of a tile, queries of a chunk
-constexpr int TMEM = 512;              // columns: 2 warpgroups x 2 accumulators x QC
+constexpr int TOK = 128, QC = 256;     // tokens of a tile, queries of a chunk
+constexpr int WGS = 4, THREADS = 128 * WGS;
+constexpr int TMEM = 2 * QC;           // columns
 constexpr uint64_t DRAIN_NS = 10000000000ull;
 
 // D (+)= A B from shared memory, kind::f16.
@@ -40,194 +41,191 @@ __device__ __forceinline__ void landed(uint32_t (&v)[16]) {
                :
                : "memory");
 }
-__device__ __forceinline__ void wg_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
-__device__ __forceinline__ bool wg_or(int id, bool x) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbar.red.or.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"((uint32_t)x)
-      : "memory");
-  return r != 0;
+// Operands in shared memory: panels of 64 elements, a row of a panel 128 bytes whose 16-byte pieces are exchanged by
+// the row's low bits (the 128-byte swizzle of the MMA's descriptor): a row's pieces, written by neighbouring lanes as they
+// read them, and a column of 8 rows both fall on different banks.
+__device__ __forceinline__ uint32_t piece_at(int rows, int row, int k8) {  // k8: piece of 8 elements
+  return (uint32_t)(k8 >> 3) * rows * 128 + row * 128 + (((k8 & 7) ^ (row & 7)) << 4);
 }
+__device__ __forceinline__ uint64_t panel_desc(uint32_t addr) { return umma_sdesc(addr, 16, 1024) | (2ull << 61); }
 
-// Operands in shared memory: cores of 8 rows x 16 bytes, those of a row's HD elements side by side.
-template <int HD>
-struct Core {
-  static constexpr uint32_t LBO = 128, SBO = HD / 8 * 128;
-  static __device__ __forceinline__ uint32_t at(int row, int k) {
-    return (uint32_t)(row >> 3) * SBO + (uint32_t)(k >> 3) * LBO + (row & 7) * 16 + (k & 7) * 2;
-  }
-};
-
-// Dynamic shared memory: Q (and its remainders), each warpgroup's K tile, the columns, the sums.
+// Dynamic shared memory: Q (and its remainders), two K tiles, the columns, the warpgroups' sums of two tiles.
 struct Layout {
   uint32_t qlo, k, cn, slope, range, part, total;
-  __host__ __device__ Layout(bool f32, int hd, int nq, int tiles) {
+  __host__ __device__ Layout(bool f32, int hd, int nq) {
     const uint32_t q = (uint32_t)nq * hd * 2;
     qlo = q;
-    k = f32 ? 2 * q : q;
+    k = f32 ? 2 * q : q;  // (multiples of 1024: nq is one of 16)
     cn = k + 2u * TOK * hd * 2;
     slope = cn + (uint32_t)nq * 8;
     range = slope + (uint32_t)nq * 4;
     part = range + (uint32_t)nq * 8;
-    total = part + 2u * tiles * TOK * 4;
+    total = part + 2u * WGS * TOK * 4;
   }
 };
 
-template <int CT, int DT, int HD, bool EX>
-__global__ void __launch_bounds__(256, 1) kv8_score_tc_kernel(const __grid_constant__ ScoreArgs S) {
+template <int DT, int HD, bool EX>
+__global__ void __launch_bounds__(THREADS, 1) kv8_score_tc_kernel(const __grid_constant__ ScoreArgs S, const int type) {
   constexpr bool HL = DT == DDL_T_F32;
-  constexpr int NV = HD / 16;  // 16-byte pieces of a token's codes
-  using C = Core<HD>;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t bars[2][2];
+  constexpr int KL = HD / 16, RPL = 32 / KL, NG = 8 / RPL;  // lanes a token's codes take; tokens a load; loads (a warp: 8 tokens)
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ __align__(8) uint64_t bars[2];
   __shared__ uint32_t tslot;
   const AttArgs& A = S.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wg = warp >> 2, tok = tid & 127;
-  const Layout M(HL, HD, S.tiles, S.wb);
-  if (tid == 0) {
-    for (int i = 0; i < 4; ++i) mbar_init(smem_addr(&bars[i >> 1][i & 1]), 1);
-  }
-  mbar_init_fence();
-  if (warp == 0) tmem_alloc(smem_addr(&tslot), TMEM);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tm = tslot;
+  const Layout M(HL, HD, S.tiles);
   pdl_wait();
-  pdl_trigger();
   const int r = blockIdx.z, h = blockIdx.y;
   const Req rq = load_req(A, r);
   if (rq.bad && A.bad && blockIdx.x == 0 && h == 0 && tid == 0) atomicOr(A.bad, 1);
-  const int ntile = (rq.len + TOK - 1) / TOK, c0 = blockIdx.x * 2 * S.wb;
-  const int first = S.decay == 1.f ? rq.b0 >> 3 : 0;  // tiles before it do not change
   const int nq = rq.n * A.GH;
   float* const out = S.score + ((int64_t)r * A.Hkv + h) * S.stride;
-  float* const part = reinterpret_cast<float*>(smem + M.part) + (size_t)wg * S.wb * TOK + tok;  // [tile][token]
-  if (rq.n > 0 && c0 < ntile && c0 + 2 * S.wb > first) {  // (the same for the whole CTA)
-    const int mine = c0 + wg < ntile ? min(S.wb, (ntile - c0 - wg + 1) / 2) : 0;  // tiles c0 + wg + 2 i
-    auto key_of = [&](int i) { return (c0 + wg + 2 * i) * TOK + tok; };
-    auto seen = [&](int i) {  // does any row see a token of the tile?
-      const int b = (c0 + wg + 2 * i) * (TOK / 16);
-      return i < mine && b < rq.b1 && b + TOK / 16 > rq.b0;
-    };
-    // the scores that the tokens bring along
-#pragma unroll
-    for (int i = 0; i < SCORE_TC_TILES; ++i) {
-      if (i >= mine) break;
-      const int key = key_of(i);
-      part[i * TOK] = key < rq.p0 && key < rq.len && S.decay != 0.f ? S.decay * out[key] : 0.f;
-    }
-    // this thread's token of a tile: its codes and scale
-    uint4 raw[NV];
-    float ks = 0.f;
+  // tiles [t0, t1) change, [s0, s1) of them hold tokens that some row sees
+  const int ntile = (rq.len + TOK - 1) / TOK;
+  const int t0 = max((int)(blockIdx.x * S.wb), S.decay == 1.f ? rq.b0 >> 3 : 0), t1 = min((int)((blockIdx.x + 1) * S.wb), ntile);
+  const int s0 = max(t0, rq.b0 >> 3), s1 = min(t1, (rq.b1 + 7) >> 3);
+  if (rq.n <= 0 || t0 >= t1) return;  // (the same for the whole CTA)
+  if (tid < 2) mbar_init(smem_addr(&bars[tid]), 1);
+  mbar_init_fence();
+  if (warp == 0) tmem_alloc(smem_addr(&tslot), TMEM);
+  pdl_trigger();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t acc = tslot, bar = smem_addr(&bars[0]);
+  uint32_t flying = 0, phase = 0;  // bit a: MMAs into accumulator a are on their way; the parity of their commit
+  {
+    // the score that a token brings along
+    auto old_of = [&](int key) { return key < rq.p0 && key < rq.len && S.decay != 0.f ? out[key] : 0.f; };
+    if (wg == 0)  // tiles that nobody sees only decay
+      for (int t = t0; t < t1; ++t) {
+        const int key = t * TOK + tok;
+        if ((t < s0 || t >= s1) && key < rq.len) out[key] = S.decay * old_of(key);
+      }
+    // This thread's token of a tile: its scale.  The codes of 8 tokens a warp: KL neighbouring lanes a token, so that
+    // a load meets whole rows (16 bytes of each of 8 rows a quarter of a warp took four times as long).  All of a
+    // tile's loads are on their way before any is used, its pages (of the warp's 8 tokens' block, of the thread's own) a
+    // tile ahead.
+    const int wtok = warp * 8;  // first token whose codes this warp converts
+    uint4 raw[NG];
+    float ks = 0.f, was = 0.f;
     bool live = false;
-    auto load_codes = [&](int i) {
-      const int key = key_of(i), b = key >> 4, bshift = A.pshift - 4;
-      live = false;
-      ks = 0.f;
-      if (b >= rq.b0 && b < rq.b1) {
-        const int32_t page = A.table[(int64_t)r * A.per + (b >> bshift)];
-        live = page >= 0 && page < A.pages;
-        if (!live && A.bad) atomicOr(A.bad, 1);
-        if (live) {
-          const int64_t row = (((int64_t)page * A.Hkv + h) << A.pshift) + (key & ((1 << A.pshift) - 1));
-          ks = A.ks[row >> 4];
-          if (!(fabsf(ks) < INFINITY)) ks = __uint_as_float(0x7fffffffu);
-#pragma unroll
-          for (int j = 0; j < NV; ++j) raw[j] = *reinterpret_cast<const uint4*>(A.k + row * HD + j * 16);
-        }
-      }
-      if (!live) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j) raw[j] = make_uint4(0u, 0u, 0u, 0u);
-      }
+    auto load_page = [&](int t, int x) -> int32_t {  // of token x of tile t
+      const int b = (t * TOK + x) >> 4;
+      return t < s1 && b >= rq.b0 && b < rq.b1 ? A.table[(int64_t)r * A.per + (b >> (A.pshift - 4))] : -2;
     };
-    const uint32_t kbuf = smem_addr(smem + M.k) + (uint32_t)wg * TOK * HD * 2;
-    auto store_codes = [&]() {
+    auto row_of = [&](int32_t page, int t, int x) -> int64_t {
+      return page >= 0 && page < A.pages ? (((int64_t)page * A.Hkv + h) << A.pshift) + ((t * TOK + x) & ((1 << A.pshift) - 1)) : -1;
+    };
+    int32_t page = load_page(s0, tok), wpage = load_page(s0, wtok);
+    auto load_codes = [&](int t, bool again) {  // (of tile t, with its pages; then the pages of the next)
+      const int64_t row = row_of(page, t, tok), from = row_of(wpage, t, wtok);
+      live = row >= 0;
+      if (!live && page != -2 && A.bad) atomicOr(A.bad, 1);
+      ks = live ? A.ks[row >> 4] : 0.f;
+      // (again: the next queries, onto what the first left)
+      const int key = t * TOK + tok;
+      was = wg > 0 ? 0.f : !again ? old_of(key) : key < rq.len ? out[key] : 0.f;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+      for (int g = 0; g < NG; ++g)
+        raw[g] = from >= 0 ? *reinterpret_cast<const uint4*>(A.k + (from + RPL * g + lane / KL) * HD + (lane % KL) * 16)
+                           : make_uint4(0u, 0u, 0u, 0u);
+      page = load_page(t + 1, tok);
+      wpage = load_page(t + 1, wtok);
+    };
+    const uint32_t kbuf = smem_addr(smem + M.k);
+    auto store_codes = [&](int t) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const uint32_t w[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
         uint32_t f[8];
+        if (type == DDL_KV8_E4M3) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) codes_f16<CT>(w[q], f[2 * q], f[2 * q + 1]);
-        sts128(kbuf + C::at(tok, 16 * j), make_uint4(f[0], f[1], f[2], f[3]));
-        sts128(kbuf + C::at(tok, 16 * j + 8), make_uint4(f[4], f[5], f[6], f[7]));
+          for (int q = 0; q < 4; ++q) codes_f16<DDL_KV8_E4M3>(w[q], f[2 * q], f[2 * q + 1]);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) codes_f16<DDL_KV8_INT8>(w[q], f[2 * q], f[2 * q + 1]);
+        }
+        const int x = wtok + RPL * g + lane / KL, k8 = 2 * (lane % KL);
+        const uint32_t to = kbuf + (uint32_t)(t & 1) * TOK * HD * 2;
+        sts128(to + piece_at(TOK, x, k8), make_uint4(f[0], f[1], f[2], f[3]));
+        sts128(to + piece_at(TOK, x, k8 + 1), make_uint4(f[4], f[5], f[6], f[7]));
       }
     };
-    const uint32_t bar0 = smem_addr(&bars[wg][0]);
-    uint32_t flying = 0, phase = 0;  // bit a: MMAs into accumulator a are on their way; the parity of their commit
-    bool ok = true;
+    bool ok = true;  // no wait of the CTA gave up
     float2* const cn = reinterpret_cast<float2*>(smem + M.cn);
     float* const slope = reinterpret_cast<float*>(smem + M.slope);
     int2* const range = reinterpret_cast<int2*>(smem + M.range);
-    for (int g0 = 0; g0 < nq; g0 += S.tiles) {
+    float* const part = reinterpret_cast<float*>(smem + M.part);  // [tile & 1][warpgroup][token]
+    for (int g0 = 0; s0 < s1 && g0 < nq; g0 += S.tiles) {
       const int n = min(S.tiles, nq - g0), npad = (n + 15) & ~15, nch = (npad + QC - 1) / QC;
-      __syncthreads();  // (the last queries' MMAs are done: both warpgroups have waited for them)
-      if (g0 == 0 && seen(0)) load_codes(0);
-      for (int x = tid; x < npad; x += 256) {
-        const Column c = column_of<EX>(A, rq, h, x < n ? g0 + x : nq, 1.f);  // (nq: none)
-        cn[x].y = x < n ? c.lse2 : INFINITY;
-        if (EX) slope[x] = c.slope;
-        range[x] = make_int2(c.hi, c.lo);
+      if (g0 > 0) {
+        __syncthreads();  // (the last queries' MMAs are done, their scores written)
+        page = load_page(s0, tok);
+        wpage = load_page(s0, wtok);
       }
       const float unit = EX && A.softcap > 0.f ? __fdiv_rn(A.scale, A.softcap) : A.scale * LOG2E;
-      // Q: a warp takes 8 queries, lane (query, c) the pieces of 8 elements c, c + 4, ..: stores without bank
-      // conflicts; four rounds' loads on their way
-      constexpr int PC = HD / 32, PW = HL ? 2 : 1;  // pieces a lane, 16-byte words a piece
-      const int qr = lane & 7, qp = lane >> 3;
-      constexpr int U = 4;
-      for (int x0 = warp * 8; x0 < npad; x0 += 64 * U) {
+      // Q: a warp takes 4 queries, 8 lanes each, a lane the pieces of 8 elements c and c + 8; all rounds' loads on their
+      // way (512 16-bit or 256 fp32 queries of 128)
+      constexpr int PC = HD / 64, PW = HL ? 2 : 1, U = HL ? 4 : 8;  // pieces a lane, 16-byte words a piece, rounds
+      constexpr int STEP = 4 * 4 * WGS;                             // queries of a round
+      const int qr = lane >> 3, qp = lane & 7;
+      for (int x0 = warp * 4; x0 == warp * 4 || x0 < npad; x0 += STEP * U) {  // (every warp comes once)
         uint4 in[U][PC][PW];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int qi = g0 + min(x0 + 64 * u + qr, n - 1), row = group_row(A, qi);  // (past the last: not used)
+          const int qi = g0 + min(x0 + STEP * u + qr, n - 1), row = group_row(A, qi);  // (past the last: not used)
           const uint8_t* const from = reinterpret_cast<const uint8_t*>(A.q) +
               ((int64_t)(rq.row0 + row) * A.q_stride + (int64_t)(h * A.GH + qi - row * A.GH) * HD) * (HL ? 4 : 2);
 #pragma unroll
           for (int p = 0; p < PC; ++p)
 #pragma unroll
-            for (int w = 0; w < PW; ++w) in[u][p][w] = *reinterpret_cast<const uint4*>(from + ((qp + 4 * p) * PW + w) * 16);
+            for (int w = 0; w < PW; ++w) in[u][p][w] = *reinterpret_cast<const uint4*>(from + ((qp + 8 * p) * PW + w) * 16);
+        }
+        if (x0 == warp * 4) {  // (beside the first round's loads)
+          if (tid < npad) {
+            const Column c = column_of<EX>(A, rq, h, tid < n ? g0 + tid : nq, 1.f);  // (nq: none)
+            cn[tid].y = tid < n ? c.lse2 : INFINITY;
+            if (EX) slope[tid] = c.slope;
+            range[tid] = make_int2(c.hi, c.lo);
+          }
+          load_codes(s0, g0 > 0);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int x = x0 + 64 * u + qr;
-          float v[PC][8], mx = 0.f;
+          const int x = x0 + STEP * u + qr;
+          auto element = [&](int p, int e) -> float {
+            const uint4 a = in[u][p][HL ? e >> 2 : 0];
+            const int i = HL ? e & 3 : e >> 1;
+            const uint32_t w = i == 0 ? a.x : i == 1 ? a.y : i == 2 ? a.z : a.w;
+            if (HL) return __uint_as_float(w);
+            if (DT == DDL_T_BF16) return e & 1 ? bf16hi_f32(w) : bf16lo_f32(w);
+            const __half2 h2 = *reinterpret_cast<const __half2*>(&w);
+            return e & 1 ? __high2float(h2) : __low2float(h2);
+          };
+          float mx = 0.f;
 #pragma unroll
-          for (int p = 0; p < PC; ++p) {
-            const uint32_t w[8] = {in[u][p][0].x, in[u][p][0].y, in[u][p][0].z, in[u][p][0].w,
-                                   in[u][p][PW - 1].x, in[u][p][PW - 1].y, in[u][p][PW - 1].z, in[u][p][PW - 1].w};
+          for (int p = 0; p < PC; ++p)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              if (HL) v[p][e] = __uint_as_float(w[e]);
-              else if (DT == DDL_T_BF16) v[p][e] = e & 1 ? bf16hi_f32(w[e / 2]) : bf16lo_f32(w[e / 2]);
-              else {
-                const __half2 h2 = *reinterpret_cast<const __half2*>(&w[e / 2]);
-                v[p][e] = e & 1 ? __high2float(h2) : __low2float(h2);
-              }
-              if (x >= n) v[p][e] = 0.f;
-              if (DT != DDL_T_F16) mx = fmaxf(mx, fabsf(v[p][e]));
-            }
-          }
-          mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 16));
+            for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(element(p, e)));
+          mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
+          mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 4));
           int e2 = (int)((__float_as_uint(mx) >> 23) & 255u) - 127 - 12;  // the largest lands in [2^12, 2^13)
           e2 = e2 < -100 ? -100 : e2 > 115 ? 115 : e2;
-          if (DT == DDL_T_F16) e2 = 0;  // (as they are)
-          const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
+          const float down = x < n ? __uint_as_float((uint32_t)(127 - e2) << 23) : 0.f;
           if (x < npad) {
 #pragma unroll
             for (int p = 0; p < PC; ++p) {
               uint32_t hi[4], lo[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const float a = v[p][2 * e] * down, b = v[p][2 * e + 1] * down;
+                const float a = x < n ? element(p, 2 * e) * down : 0.f, b = x < n ? element(p, 2 * e + 1) * down : 0.f;
                 hi[e] = pack_f16x2(a, b);
                 const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi[e]));
                 lo[e] = pack_f16x2(a - f.x, b - f.y);
               }
-              const uint32_t to = smem_addr(smem) + C::at(x, 8 * (qp + 4 * p));
+              const uint32_t to = smem_addr(smem) + piece_at(S.tiles, x, qp + 8 * p);
               sts128(to, make_uint4(hi[0], hi[1], hi[2], hi[3]));
               if (HL) sts128(to + M.qlo, make_uint4(lo[0], lo[1], lo[2], lo[3]));
             }
@@ -235,73 +233,96 @@ __global__ void __launch_bounds__(256, 1) kv8_score_tc_kernel(const __grid_const
           }
         }
       }
-      fence_proxy_async_smem();
-      __syncthreads();
-      // the MMAs of chunk c into accumulator c & 1
-      const uint64_t adesc = umma_sdesc(kbuf, C::LBO, C::SBO), bdesc = umma_sdesc(smem_addr(smem), C::LBO, C::SBO);
-      auto issue = [&](int c) {
-        const uint32_t d = tm + wg * 2 * QC + (c & 1) * QC;
+      // the MMAs of chunk c of tile t into accumulator a
+      auto issue = [&](int t, int c, uint32_t a) {
         const uint32_t idesc = umma_idesc_f16(TOK, min(QC, npad - c * QC));
-        if ((warp & 3) == 0) {
+        if (warp == 0) {
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t b = bdesc + (uint64_t)(c * (QC / 8) * C::SBO >> 4);
+            const uint64_t k0 = panel_desc(kbuf) + ((uint32_t)(t & 1) * TOK * HD * 2 >> 4);
+            const uint64_t b = panel_desc(smem_addr(smem)) + (uint64_t)(c * QC * 128 >> 4);
+            const uint32_t bp = (uint32_t)S.tiles * 128 >> 4;  // from panel to panel of Q
 #pragma unroll
-            for (int k = 0; k < HD / 16; ++k) umma_f16_ss(d, adesc + 16 * k, b + 16 * k, idesc, k ? 1u : 0u);
+            for (int k = 0; k < HD / 16; ++k)
+              umma_f16_ss(acc + a * QC, k0 + (k >> 2) * (TOK * 128 >> 4) + 2 * (k & 3), b + (k >> 2) * bp + 2 * (k & 3), idesc,
+                          k ? 1u : 0u);
             if (HL) {
               const uint64_t b2 = b + (M.qlo >> 4);
 #pragma unroll
-              for (int k = 0; k < HD / 16; ++k) umma_f16_ss(d, adesc + 16 * k, b2 + 16 * k, idesc, 1u);
+              for (int k = 0; k < HD / 16; ++k)
+                umma_f16_ss(acc + a * QC, k0 + (k >> 2) * (TOK * 128 >> 4) + 2 * (k & 3), b2 + (k >> 2) * bp + 2 * (k & 3), idesc, 1u);
             }
-            umma_commit(bar0 + 8 * (c & 1));
+            umma_commit(bar + 8 * a);
           }
           __syncwarp();
         }
-        flying |= 1u << (c & 1);
+        flying |= 1u << a;
       };
-      for (int i = 0; ok && i < mine; ++i) {
-        if (!seen(i)) {
-          if (seen(i + 1)) load_codes(i + 1);
-          continue;
-        }
-        store_codes();
-        const float f = ks;
-        const bool has = live;
-        fence_proxy_async_smem();
-        tc_fence_before();
-        wg_sync(1 + wg);  // codes there; the accumulators have been read
-        issue(0);
-        if (seen(i + 1)) load_codes(i + 1);
-        else if (g0 + S.tiles < nq && seen(0)) load_codes(0);  // (the next queries begin there, or behind unseen tiles)
-        const int key0 = (c0 + wg + 2 * i) * TOK, key = key0 + tok;
+      auto put = [&](int t, float base) {  // the sums of tile t (a barrier after they were left)
+        const int key = t * TOK + tok;
+        const float* const p = part + (t & 1) * WGS * TOK + tok;
+        const float s = (p[0] + p[TOK]) + (p[2 * TOK] + p[3 * TOK]);
+        if (key < rq.len) out[key] = base + s;
+      };
+      store_codes(s0);
+      float f = ks, base = was;
+      bool has = live;
+      fence_proxy_async_smem();
+      __syncthreads();
+      if (ok) issue(s0, 0, 0);
+      if (s0 + 1 < s1) load_codes(s0 + 1, g0 > 0);
+      uint32_t a = 0;
+      float last = 0.f;  // (warpgroup 0) what the last tile's token brought along
+      bool late = false;
+      for (int t = s0; t < s1; ++t) {
+        f = fabsf(f) < INFINITY ? f : __uint_as_float(0x7fffffffu);
+        base = g0 == 0 ? S.decay * base : base;
+        const int key0 = t * TOK, key = key0 + tok;
+        float nf = 0.f, nbase = 0.f;
+        bool nhas = false;
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int c = 0; c < nch; ++c) {
-          if (c + 1 < nch) issue(c + 1);
-          bool late = false;
+        for (int c = 0; c < nch; ++c, a ^= 1) {
+          // what comes next: its K, and its MMAs into the accumulator that all have read
+          const bool more = c + 1 < nch, next = !more && t + 1 < s1;
+          if (next) {
+            store_codes(t + 1);
+            nf = ks;
+            nbase = was;
+            nhas = live;
+            fence_proxy_async_smem();
+          }
+          tc_fence_before();
+          ok = !__syncthreads_or(late) && ok;
+          if (c == 0 && t > s0 && wg == 0) put(t - 1, last);
+          if (ok && more) issue(t, c + 1, a ^ 1);
+          if (ok && next) issue(t + 1, 0, a ^ 1);
+          if (next && t + 2 < s1) load_codes(t + 2, g0 > 0);
+          if (!ok) continue;
           {  // (bounded)
-            uint64_t t0 = 0;
-            for (uint32_t it = 1; !__all_sync(FULL, mbar_try_wait(bar0 + 8 * (c & 1), phase >> (c & 1) & 1)); ++it)
+            uint64_t since = 0;
+            for (uint32_t it = 1; !__all_sync(FULL, mbar_try_wait(bar + 8 * a, phase >> a & 1)); ++it)
               if ((it & 1023u) == 0) {
                 const uint64_t now = __shfl_sync(FULL, globaltimer(), 0);
-                if (t0 == 0) t0 = now;
-                else if (now - t0 > S.wait_ns) {
+                if (since == 0) since = now;
+                else if (now - since > S.wait_ns) {
                   late = true;
                   break;
                 }
               }
           }
-          ok = !wg_or(1 + wg, late);
-          if (!ok) break;
-          flying &= ~(1u << (c & 1));
-          phase ^= 1u << (c & 1);
+          if (late) continue;
+          flying &= ~(1u << a);
+          phase ^= 1u << a;
           tc_fence_after();
-          const uint32_t d = tm + ((uint32_t)(warp & 3) << 21) + wg * 2 * QC + (c & 1) * QC;
+          const uint32_t d = acc + a * QC + ((uint32_t)(warp & 3) << 21);
           const int q0 = g0 + c * QC, nc = min(QC, npad - c * QC), q1 = min(q0 + nc, nq) - 1;
           // tokens that every query of the chunk sees need no masks
           const bool edge = key0 + TOK - 1 > rq.p0 + group_row(A, q0) || key0 < first_seen(A, rq, q1);
           const float2* const cc = cn + c * QC;
-          auto add = [&](const uint32_t (&v)[16], int x) {  // queries x .. x + 15 of the chunk
-            float w[16];
+#pragma unroll 1
+          for (int x = 16 * wg; x < nc; x += 16 * WGS) {
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(d + x, v);
             float2 q[16];  // (two a load)
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
@@ -309,6 +330,8 @@ __global__ void __launch_bounds__(256, 1) kv8_score_tc_kernel(const __grid_const
               q[j] = make_float2(two.x, two.y);
               q[j + 1] = make_float2(two.z, two.w);
             }
+            landed(v);
+            float w[16];
             if (!EX) {
 #pragma unroll
               for (int j = 0; j < 16; ++j) w[j] = exp2_fast(fmaf(__uint_as_float(v[j]) * f, q[j].x, -q[j].y));
@@ -337,69 +360,65 @@ __global__ void __launch_bounds__(256, 1) kv8_score_tc_kernel(const __grid_const
             }
 #pragma unroll
             for (int j = 0; j < 16; ++j) sum[j & 3] += w[j];
-          };
-          // 16 columns' loads on their way while the last 16 are gone over
-          uint32_t u[16], v[16];
-          tmem_ld_32x32b_x16(d, u);
-          for (int x = 0; x < nc; x += 32) {
-            landed(u);
-            if (x + 16 < nc) tmem_ld_32x32b_x16(d + x + 16, v);
-            add(u, x);
-            if (x + 16 >= nc) break;
-            landed(v);
-            if (x + 32 < nc) tmem_ld_32x32b_x16(d + x + 32, u);
-            add(v, x + 16);
           }
-          tc_fence_before();
-          wg_sync(1 + wg);  // the accumulator has been read
         }
-        const float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        if (has) part[i * TOK] += all;
+        part[((t & 1) * WGS + wg) * TOK + tok] =
+            late || !ok ? __uint_as_float(0x7fffffffu) : has ? (sum[0] + sum[1]) + (sum[2] + sum[3]) : 0.f;
+        last = base;
+        f = nf;
+        base = nbase;
+        has = nhas;
       }
+      tc_fence_before();
+      ok = !__syncthreads_or(late) && ok;
+      if (wg == 0) put(s1 - 1, last);
     }
-    if (!ok) {  // a wait gave up: what this warpgroup has not finished is NaN
-      if (A.bad && tok == 0) atomicOr(A.bad, 2);
-      for (int i = 0; i < mine; ++i)
-        if (seen(i)) part[i * TOK] = __uint_as_float(0x7fffffffu);
-    }
-    for (int i = 0; i < mine; ++i) {
-      const int key = key_of(i);
-      if (key < rq.len && c0 + wg + 2 * i >= first) out[key] = part[i * TOK];
-    }
+    if (!ok && A.bad && tid == 0) atomicOr(A.bad, 2);
     // MMAs in flight end before their memory goes to another
-    for (int a = 0; a < 2; ++a)
-      if (flying >> a & 1) mbar_wait_thread(bar0 + 8 * a, phase >> a & 1, DRAIN_NS);
+    for (int x = 0; x < 2; ++x)
+      if (flying >> x & 1) mbar_wait_thread(bar + 8 * x, phase >> x & 1, DRAIN_NS);
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tm, TMEM);
+    tmem_dealloc(tslot, TMEM);
   }
 }
 
-template <int CT, int DT>
+template <int DT>
 const void* tc_fn(int hd, bool ex) {
-  if (hd == 128) return ex ? (const void*)kv8_score_tc_kernel<CT, DT, 128, true> : (const void*)kv8_score_tc_kernel<CT, DT, 128, false>;
-  return ex ? (const void*)kv8_score_tc_kernel<CT, DT, 64, true> : (const void*)kv8_score_tc_kernel<CT, DT, 64, false>;
-}
-template <int CT>
-const void* tc_fn(int dt, int hd, bool ex) {
-  return dt == DDL_T_F32 ? tc_fn<CT, DDL_T_F32>(hd, ex) : dt == DDL_T_BF16 ? tc_fn<CT, DDL_T_BF16>(hd, ex) : tc_fn<CT, DDL_T_F16>(hd, ex);
+  if (hd == 128) return ex ? (const void*)kv8_score_tc_kernel<DT, 128, true> : (const void*)kv8_score_tc_kernel<DT, 128, false>;
+  return ex ? (const void*)kv8_score_tc_kernel<DT, 64, true> : (const void*)kv8_score_tc_kernel<DT, 64, false>;
 }
 
 }  // namespace
 
-size_t kv8_score_tc_smem(bool f32, int hd, int queries, int tiles) { return Layout(f32, hd, queries, tiles).total; }
-
-int kv8_score_tc_launch(const ScoreArgs& s, int type, int dtype, bool ex, unsigned chunks, void* stream) {
+int kv8_score_tc_launch(const ScoreArgs& s, int type, int dtype, bool ex, int sms, void* stream) {
   ScoreArgs a = s;
-  const void* fn = type == DDL_KV8_E4M3 ? tc_fn<DDL_KV8_E4M3>(dtype, a.a.hd, ex) : tc_fn<DDL_KV8_INT8>(dtype, a.a.hd, ex);
-  const size_t smem = kv8_score_tc_smem(dtype == DDL_T_F32, a.a.hd, a.tiles, a.wb);
+  const bool f32 = dtype == DDL_T_F32;
+  const int hd = a.a.hd, nq = (a.a.max_rows * a.a.GH + 15) & ~15;
+  // queries at a time: what 128 KB hold (with remainders of fp32 rows), a column a thread
+  int most = 128 * 1024 / (hd * 2 * (f32 ? 2 : 1));
+  most = most < THREADS ? most : THREADS;
+  a.tiles = nq < most ? nq : most;
+  // tiles a CTA takes: about one wave of CTAs, each of which begins with all queries (several requests, whose lengths come
+  // to 5/8 of the bound: 8/5 waves of the bound); four for few queries, for the sake of balance
+  const int64_t tiles = ((int64_t)a.a.max_len + TOK - 1) / TOK, units = (int64_t)a.a.R * a.a.Hkv;
+  int64_t ctas = (int64_t)sms * (a.a.R == 1 ? 5 : nq <= 128 ? 20 : 8) / 5 / units;
+  ctas = ctas < 1 ? 1 : ctas;
+  a.wb = (int32_t)((tiles + ctas - 1) / ctas);
+  if (a.wb > SCORE_TC_TILES) a.wb = SCORE_TC_TILES;
+  const int64_t chunks = (tiles + a.wb - 1) / a.wb;
+  const void* fn = dtype == DDL_T_F32    ? tc_fn<DDL_T_F32>(hd, ex)
+                   : dtype == DDL_T_BF16 ? tc_fn<DDL_T_BF16>(hd, ex)
+                                         : tc_fn<DDL_T_F16>(hd, ex);
+  const size_t smem = Layout(f32, hd, a.tiles).total;
   const int st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
   if (st) return st;
-  void* args[] = {&a};
-  return cuda_status(launch_pdl(fn, dim3(chunks, (unsigned)a.a.Hkv, (unsigned)a.a.R), dim3(256), args, smem, (cudaStream_t)stream));
+  void* args[] = {&a, &type};
+  return cuda_status(launch_pdl(fn, dim3((unsigned)chunks, (unsigned)a.a.Hkv, (unsigned)a.a.R), dim3(THREADS), args, smem,
+                                (cudaStream_t)stream));
 }
 
 }  // namespace ddl
