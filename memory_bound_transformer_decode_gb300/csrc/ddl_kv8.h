@@ -63,6 +63,12 @@ __device__ __forceinline__ uint32_t f32x2_e4m3x2(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// Two fp16 values as e4m3 codes, likewise.
+__device__ __forceinline__ uint32_t f16x2_e4m3x2(uint32_t v) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(v));
+  return r;
+}
 // fp32 as an 8-bit integer code in [-127, 127], round to nearest even; NaN 0.
 __device__ __forceinline__ uint32_t f32_int8(float v) {
   const float c = fminf(fmaxf(v, -127.f), 127.f);  // (NaN becomes -127 here)

@@ -2,14 +2,14 @@
 // heaviest tokens (ddl_kv8_evict): which tokens of each K/V head stay, and their
 // move to new pages.
 //
-// Two kernels.  The first chooses, one CTA per request and head: the m-th largest
-// score among the tokens that may go, by radix select on order-preserving keys
-// (digits of 11, 11 and 10 bits, histograms in shared memory), then the kept
-// tokens in order: each warp counts those of its run of tokens, and with the sums
-// of the warps before it writes their indices and scores.  The second moves the
-// codes, a warp per block of 16 kept tokens and head: 16 rows of K and of V in
-// registers, their largest value, the block's new power-of-two scale, and the
-// codes in it.  Rows whose scale already is the new one keep their codes.
+// Two kernels.  The first chooses: a cluster of 1 to 16 CTAs takes a request and head, each CTA a run of tokens whose
+// scores it keeps in shared memory.  The m-th largest by radix select on order-preserving keys, digits of 10 bits of its
+// distance from the largest (so that neither digits nor histogram bins go to what all keys share), the histograms added
+// up in distributed shared memory; it ends early where all of a digit stay.  Then the kept tokens in order: each warp
+// counts those of its run, and with the sums of the warps before it writes their indices and scores.
+// The second moves the codes, a warp per block of 16 kept tokens and head: 16 rows of K and of V in registers, their
+// largest value, the block's new power-of-two scale, and the codes in it.  Between powers of two that is a product in
+// fp16, exact but for the one rounding of the code; rows whose scale already is the new one keep their codes.
 #include <cuda_bf16.h>
 
 #include "ddl_kv8.h"
@@ -61,116 +61,184 @@ __device__ __forceinline__ uint32_t score_key(float x) {
   return x == x ? (b & 0x80000000u ? ~b : b | 0x80000000u) : 0u;
 }
 
-constexpr int SEL_BINS = 2048;
+constexpr int SEL_BITS = 10, SEL_BINS = 1 << SEL_BITS, SEL_THREADS = 512, SEL_WARPS = SEL_THREADS / 32;
+constexpr int SEL_PASSES = (32 + SEL_BITS - 1) / SEL_BITS;
 
-template <int NT, bool SM>
-__global__ void __launch_bounds__(NT) kv8_select_kernel(const __grid_constant__ EvictArgs A) {
-  extern __shared__ uint32_t sel_keys[];  // SM: the tokens' keys
-  __shared__ uint32_t hist[SEL_BINS];
-  __shared__ uint32_t wsum[2][NT / 32];
-  __shared__ uint32_t sh_digit, sh_need;
+__device__ __forceinline__ uint32_t ldu_cluster(const uint32_t* p, int rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(smem_addr(p), rank)) : "memory");
+  return v;
+}
+
+template <bool SM>
+__global__ void __launch_bounds__(SEL_THREADS) kv8_select_kernel(const __grid_constant__ EvictArgs A, const int C) {
+  extern __shared__ float sel_scores[];  // SM: the scores of the CTA's tokens
+  __shared__ uint32_t hist[SEL_PASSES][SEL_BINS], sums[SEL_PASSES][SEL_BINS / 2];  // sums: of the cluster, SEL_BINS / C of them
+  __shared__ uint32_t wsum[2][SEL_WARPS];
+  __shared__ uint32_t cta_top, cta_low, cta_sure, cta_ties, sh_digit, sh_need, sh_inside;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h = blockIdx.x, r = blockIdx.y;
+  const int rank = blockIdx.x % C, h = blockIdx.x / C, r = blockIdx.y;
+  for (int i = tid; i < SEL_PASSES * SEL_BINS; i += SEL_THREADS) hist[0][i] = 0;
   pdl_trigger();
   pdl_wait();
   const Cut c = load_cut(A, r);
-  if (c.bad && A.bad && h == 0 && tid == 0) atomicOr(A.bad, 1);
+  if (c.bad && A.bad && blockIdx.x == 0 && tid == 0) atomicOr(A.bad, 1);
   const float* const score = A.score + ((int64_t)r * A.H + h) * A.stride;
   float* const out = A.score_out + ((int64_t)r * A.H + h) * A.stride;
-  if (c.keep < 0) {
-    for (int i = tid; i < c.len; i += NT) out[i] = score[i];
+  const int n0 = (int)((int64_t)c.len * rank / C), n1 = (int)((int64_t)c.len * (rank + 1) / C);  // the CTA's tokens
+  if (c.keep < 0) {  // (the same for the whole cluster)
+    for (int i = n0 + tid; i < n1; i += SEL_THREADS) out[i] = score[i];
     return;
   }
   const int lo = c.sinks, hi = c.len - c.recent;  // the tokens that may go: [lo, hi)
-  auto key = [&](int i) -> uint32_t { return SM ? sel_keys[i] : score_key(score[i]); };
-  if (SM) {
-    for (int i = tid; i < c.len; i += NT) sel_keys[i] = score_key(score[i]);
-  }
-  // the m-th largest key, and how many tokens of that key stay
-  uint32_t need = (uint32_t)(c.keep - c.sinks - c.recent), thr = 0xffffffffu;
-  if (need > 0) {
-    uint32_t prefix = 0, mask = 0;
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-      for (int i = tid; i < SEL_BINS; i += NT) hist[i] = 0;
-      __syncthreads();
-      for (int i = lo + tid; i < hi; i += NT) {
-        const uint32_t k = key(i);
-        if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1u);
-      }
-      __syncthreads();
-      // bins from the top: thread i takes bins SEL_BINS - 1 - i * PER ...
-      constexpr int PER = SEL_BINS / NT;
-      uint32_t n[PER], sum = 0;
+  const int m0 = max(n0, lo), m1 = min(n1, hi);
+  auto score_of = [&](int i) -> float { return SM ? sel_scores[i - n0] : score[i]; };
+  auto key = [&](int i) -> uint32_t { return score_key(score_of(i)); };
+  // the range of the keys
+  uint32_t top = 0u, low = ~0u;
+  for (int i = n0 + tid; i < n1; i += 4 * SEL_THREADS) {
+    float s[4];
 #pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        n[j] = hist[SEL_BINS - 1 - (tid * PER + j)];
-        sum += n[j];
-      }
-      uint32_t inc = sum;
+    for (int j = 0; j < 4; ++j) s[j] = i + j * SEL_THREADS < n1 ? score[i + j * SEL_THREADS] : 0.f;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(FULL, inc, o);
-        if (lane >= o) inc += y;
+    for (int j = 0; j < 4; ++j) {
+      const int x = i + j * SEL_THREADS;
+      if (SM && x < n1) sel_scores[x - n0] = s[j];
+      if (x >= m0 && x < m1) {
+        const uint32_t k = score_key(s[j]);
+        top = max(top, k);
+        low = min(low, k);
       }
-      if (lane == 31) wsum[0][warp] = inc;
-      __syncthreads();
-      for (int w = 0; w < warp; ++w) inc += wsum[0][w];
-      uint32_t before = inc - sum;
-#pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        if (before < need && before + n[j] >= need) {
-          sh_digit = (uint32_t)(SEL_BINS - 1 - (tid * PER + j));
-          sh_need = need - before;
-        }
-        before += n[j];
-      }
-      __syncthreads();
-      prefix |= sh_digit << shift;
-      mask |= ((1u << bits) - 1) << shift;
-      need = sh_need;
     }
-    thr = prefix;
   }
-  __syncthreads();  // (the keys, where nothing was chosen)
+  top = __reduce_max_sync(FULL, top);
+  low = __reduce_min_sync(FULL, low);
+  if (lane == 0) {
+    wsum[0][warp] = top;
+    wsum[1][warp] = low;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    top = __reduce_max_sync(FULL, lane < SEL_WARPS ? wsum[0][lane] : 0u);
+    low = __reduce_min_sync(FULL, lane < SEL_WARPS ? wsum[1][lane] : ~0u);
+    if (lane == 0) {
+      cta_top = top;
+      cta_low = low;
+    }
+  }
+  cluster_sync();
+  top = __reduce_max_sync(FULL, lane < C ? ldu_cluster(&cta_top, lane) : 0u);
+  low = __reduce_min_sync(FULL, lane < C ? ldu_cluster(&cta_low, lane) : ~0u);
+  // the distance `at` from the largest key, but for its last `bits` bits, at which `need` tokens are reached: those
+  // nearer stay, and of those at it `need` (all: every one)
+  uint32_t need = (uint32_t)(c.keep - c.sinks - c.recent), at = 0;
+  int bits = top > low ? 32 - __clz(top - low) : 0;
+  bool all = false;
+  for (int pass = 0; need > 0 && !all && bits > 0; ++pass) {
+    const int shift = bits > SEL_BITS ? bits - SEL_BITS : 0;
+    uint32_t* const bins = hist[pass];
+    for (int i = m0 + tid; i < m1; i += SEL_THREADS) {
+      const uint32_t x = top - key(i);
+      if (pass == 0 || (x ^ at) >> bits == 0) atomicAdd(&bins[(x >> shift) & (SEL_BINS - 1)], 1u);
+    }
+    // (in two steps: 16 CTAs that read all 16 histograms took 10 us a digit)
+    constexpr int PER = SEL_BINS / SEL_THREADS;
+    uint32_t n[PER], sum = 0;
+    if (C > 1) {
+      const int per = SEL_BINS / C;
+      cluster_sync();
+      for (int i = tid; i < per; i += SEL_THREADS) {
+        uint32_t s = 0;
+#pragma unroll 8
+        for (int k = 0; k < C; ++k) s += ldu_cluster(&bins[rank * per + i], k);
+        sums[pass][i] = s;
+      }
+      cluster_sync();
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        const int i = tid + j * SEL_THREADS, k = i / per;  // (neighbouring lanes, neighbouring words)
+        bins[i] = ldu_cluster(&sums[pass][i - k * per], k);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      n[j] = bins[tid * PER + j];
+      sum += n[j];
+    }
+    uint32_t inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(FULL, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) wsum[0][warp] = inc;
+    __syncthreads();
+    uint32_t before = inc - sum + __reduce_add_sync(FULL, lane < warp ? wsum[0][lane] : 0u);
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      if (before < need && before + n[j] >= need) {
+        sh_digit = (uint32_t)(tid * PER + j);
+        sh_need = need - before;
+        sh_inside = n[j];
+      }
+      before += n[j];
+    }
+    __syncthreads();
+    at |= sh_digit << shift;
+    need = sh_need;
+    all = need == sh_inside;
+    bits = shift;
+  }
+  const bool none = c.keep == c.sinks + c.recent;
+  // 2: stays, 1: one of those at the distance, 0: goes
+  auto state = [&](int i) -> int {
+    if (i < lo || i >= hi) return 2;
+    if (none) return 0;
+    const uint32_t x = (top - key(i)) >> bits, y = at >> bits;
+    return x < y || (all && x == y) ? 2 : x == y ? 1 : 0;
+  };
   // the kept tokens in order: run of tokens [w0, w1) per warp
-  const int w0 = (int)((int64_t)c.len * warp / (NT / 32)), w1 = (int)((int64_t)c.len * (warp + 1) / (NT / 32));
-  auto sure = [&](int i, uint32_t k) { return i < lo || i >= hi || k > thr; };
+  const int w0 = n0 + (int)((int64_t)(n1 - n0) * warp / SEL_WARPS), w1 = n0 + (int)((int64_t)(n1 - n0) * (warp + 1) / SEL_WARPS);
   uint32_t ns = 0, nt = 0;
+  if (SM) __syncthreads();  // (the keys, where no digit was needed)
   for (int i = w0 + lane; i < w1; i += 32) {
-    const uint32_t k = key(i);
-    const bool s = sure(i, k);
-    ns += s;
-    nt += !s && k == thr;
+    const int s = state(i);
+    ns += s == 2;
+    nt += s == 1;
   }
   ns = __reduce_add_sync(FULL, ns);
   nt = __reduce_add_sync(FULL, nt);
+  __syncthreads();  // (wsum's last readers)
   if (lane == 0) {
     wsum[0][warp] = ns;
     wsum[1][warp] = nt;
   }
   __syncthreads();
-  uint32_t at = 0, ties = 0;  // kept for sure, and tokens of the threshold's key, before this warp's
-  for (int w = 0; w < warp; ++w) {
-    at += wsum[0][w];
-    ties += wsum[1][w];
+  uint32_t to = __reduce_add_sync(FULL, lane < warp ? wsum[0][lane] : 0u);
+  uint32_t ties = __reduce_add_sync(FULL, lane < warp ? wsum[1][lane] : 0u);
+  if (C > 1) {
+    if (tid == SEL_THREADS - 32) {  // (the last warp's first lane)
+      cta_sure = to + ns;
+      cta_ties = ties + nt;
+    }
+    cluster_sync();
+    to += __reduce_add_sync(FULL, lane < rank ? ldu_cluster(&cta_sure, lane) : 0u);
+    ties += __reduce_add_sync(FULL, lane < rank ? ldu_cluster(&cta_ties, lane) : 0u);
+    cluster_sync();  // (nobody's shared memory goes while another reads it)
   }
   int32_t* const kept = A.kept + ((int64_t)r * A.H + h) * A.max_keep;
   const uint32_t below = (1u << lane) - 1;
   for (int i0 = w0; i0 < w1; i0 += 32) {
-    const int i = i0 + lane;
-    const bool in = i < w1;
-    const uint32_t k = in ? key(i) : 0u;
-    const bool s = in && sure(i, k), e = in && !s && k == thr;
-    const uint32_t ms = __ballot_sync(FULL, s), me = __ballot_sync(FULL, e);
+    const int i = i0 + lane, s = i < w1 ? state(i) : 0;
+    const uint32_t ms = __ballot_sync(FULL, s == 2), me = __ballot_sync(FULL, s == 1);
     const uint32_t tie = ties + __popc(me & below);
-    const bool take = s || (e && tie < need);
-    if (take) {
-      const uint32_t to = at + __popc(ms & below) + (tie < need ? tie : need);
-      kept[to] = i;
-      out[to] = score[i];
+    if (s == 2 || (s == 1 && tie < need)) {
+      const uint32_t x = to + __popc(ms & below) + (tie < need ? tie : need);
+      kept[x] = i;
+      out[x] = score_of(i);
     }
-    at += __popc(ms);
+    to += __popc(ms);
     ties += __popc(me);
   }
 }
@@ -182,43 +250,78 @@ struct Rows {
   static constexpr int LPR = HD / 16, RPL = 32 / LPR, NI = 16 / RPL;
 };
 
+// A row's codes in a warp's registers, and the block that they become.
 template <int CT, int HD>
-__device__ __forceinline__ void move_block(const EvictArgs& A, int kv, int64_t src_row, float src_scale, int64_t dst_row) {
+struct Block {
   using G = Rows<HD>;
-  const int lane = threadIdx.x & 31, sub = lane % G::LPR;
-  const uint8_t* const base = A.code[kv];
   uint4 x[G::NI];
-  float f[G::NI];
+  // rows' places (of lane's row; -1: zeros)
+  __device__ __forceinline__ void load(const uint8_t* base, int64_t row) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int j = 0; j < G::NI; ++j) {
-    const int64_t row = __shfl_sync(FULL, src_row, j * G::RPL + lane / G::LPR);
-    f[j] = __shfl_sync(FULL, src_scale, j * G::RPL + lane / G::LPR);
-    x[j] = row >= 0 ? *reinterpret_cast<const uint4*>(base + row * HD + sub * 16) : make_uint4(0u, 0u, 0u, 0u);
-  }
-  // the largest value: per row the largest |code| (exact in fp16; NaN does not count) times its scale
-  float top = 0.f;
-#pragma unroll
-  for (int j = 0; j < G::NI; ++j) {
-    const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-    __half2 m = __float2half2_rn(0.f);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t a, b;
-      codes_f16<CT>(w[q], a, b);
-      m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&a)));
-      m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&b)));
+    for (int j = 0; j < G::NI; ++j) {
+      const int64_t from = __shfl_sync(FULL, row, j * G::RPL + lane / G::LPR);
+      x[j] = from >= 0 ? *reinterpret_cast<const uint4*>(base + from * HD + lane % G::LPR * 16) : make_uint4(0u, 0u, 0u, 0u);
     }
-    top = fmaxf(top, fmaxf(__low2float(m), __high2float(m)) * f[j]);
   }
-  const float amax = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(top)));
-  const bool broken = __any_sync(FULL, !(src_scale >= 0.f && src_scale < INFINITY));
-  const float now = broken ? __uint_as_float(0x7fffffffu) : pow2_scale<CT>(amax);
-  const Divider by(now);
+  // scale: of lane's row (0 for none); returns the block's new one and leaves its codes in x
+  __device__ __forceinline__ float rescale(float scale) {
+    const int lane = threadIdx.x & 31;
+    // the largest value: per row the largest |code| (exact in fp16; NaN does not count) times its scale
+    float top = 0.f;
 #pragma unroll
-  for (int j = 0; j < G::NI; ++j) {
-    const int64_t row = __shfl_sync(FULL, src_row, j * G::RPL + lane / G::LPR);
-    uint4 y = x[j];
-    if (row >= 0 && f[j] != now) {
+    for (int j = 0; j < G::NI; ++j) {
+      const float f = __shfl_sync(FULL, scale, j * G::RPL + lane / G::LPR);
+      const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+      __half2 m = __float2half2_rn(0.f);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t a, b;
+        codes_f16<CT>(w[q], a, b);
+        m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&a)));
+        m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&b)));
+      }
+      top = fmaxf(top, fmaxf(__low2float(m), __high2float(m)) * f);
+    }
+    const float amax = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(top)));
+    const uint32_t bits = __float_as_uint(scale);
+    const bool broken = __any_sync(FULL, !(scale >= 0.f && scale < INFINITY));
+    const float now = broken ? __uint_as_float(0x7fffffffu) : pow2_scale<CT>(amax);
+    // all scales powers of two, none more than 2^15 above the new one (nor subnormal): factors in fp16
+    const bool pow2 = (bits & 0x7fffffu) == 0 && (bits == 0 || bits >= 0x00800000u) &&
+                      (int)(bits >> 23) - (int)(__float_as_uint(now) >> 23) <= 15;
+    if (!broken && now > 0.f && __all_sync(FULL, pow2)) {
+      // a code times 2^k (k <= 15): exact in fp16, or so small that the code is 0 whichever way it is rounded
+      const int k = (int)(bits >> 23) - (int)(__float_as_uint(now) >> 23);
+      const uint32_t mine = bits == 0 || k < -24 ? 0u : k < -14 ? 1u << (k + 24) : (uint32_t)(k + 15) << 10;
+#pragma unroll
+      for (int j = 0; j < G::NI; ++j) {
+        const uint32_t f = __shfl_sync(FULL, mine | (mine << 16), j * G::RPL + lane / G::LPR);
+        if (f == 0x3c003c00u) continue;  // 1
+        const __half2 f2 = *reinterpret_cast<const __half2*>(&f);
+        uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t a, b;
+          codes_f16<CT>(w[q], a, b);
+          if (CT == DDL_KV8_E4M3) {
+            const __half2 u = __hmul2(*reinterpret_cast<const __half2*>(&a), f2), v = __hmul2(*reinterpret_cast<const __half2*>(&b), f2);
+            w[q] = f16x2_e4m3x2(*reinterpret_cast<const uint32_t*>(&u)) | (f16x2_e4m3x2(*reinterpret_cast<const uint32_t*>(&v)) << 16);
+          } else {  // 1536 + c 2^k, rounded to whole numbers by the addition: the code in the low byte
+            const __half2 big = __half2(__ushort_as_half(0x6600), __ushort_as_half(0x6600));
+            const __half2 u = __hfma2(*reinterpret_cast<const __half2*>(&a), f2, big), v = __hfma2(*reinterpret_cast<const __half2*>(&b), f2, big);
+            w[q] = __byte_perm(*reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&v), 0x6420);
+          }
+        }
+        x[j] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      return now;
+    }
+    const Divider by(now);
+#pragma unroll
+    for (int j = 0; j < G::NI; ++j) {
+      const float f = __shfl_sync(FULL, scale, j * G::RPL + lane / G::LPR);
+      if (f == now) continue;
       uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -226,19 +329,25 @@ __device__ __forceinline__ void move_block(const EvictArgs& A, int kv, int64_t s
         codes_f16<CT>(w[q], a, b);
         const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&a));
         const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&b));
-        const float v[4] = {by(lo.x * f[j]), by(lo.y * f[j]), by(hi.x * f[j]), by(hi.y * f[j])};
+        const float v[4] = {by(lo.x * f), by(lo.y * f), by(hi.x * f), by(hi.y * f)};
         w[q] = CT == DDL_KV8_E4M3 ? f32x2_e4m3x2(v[0], v[1]) | (f32x2_e4m3x2(v[2], v[3]) << 16)
                                   : f32_int8(v[0]) | (f32_int8(v[1]) << 8) | (f32_int8(v[2]) << 16) | (f32_int8(v[3]) << 24);
       }
-      y = make_uint4(w[0], w[1], w[2], w[3]);
+      x[j] = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    *reinterpret_cast<uint4*>(A.code[kv] + (dst_row + j * G::RPL + lane / G::LPR) * HD + sub * 16) = y;
+    return now;
   }
-  if (lane == 0) A.scale[kv][dst_row >> 4] = now;
-}
+  __device__ __forceinline__ void store(uint8_t* base, float* scales, int64_t row, float scale) const {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < G::NI; ++j)
+      *reinterpret_cast<uint4*>(base + (row + j * G::RPL + lane / G::LPR) * HD + lane % G::LPR * 16) = x[j];
+    if (lane == 0) scales[row >> 4] = scale;
+  }
+};
 
 template <int CT, int HD>
-__global__ void __launch_bounds__(256) kv8_move_kernel(const __grid_constant__ EvictArgs A) {
+__global__ void __launch_bounds__(256, 3) kv8_move_kernel(const __grid_constant__ EvictArgs A) {
   const int lane = threadIdx.x & 31, b = blockIdx.x * 8 + (threadIdx.x >> 5), h = blockIdx.y, r = blockIdx.z;
   pdl_trigger();
   pdl_wait();
@@ -264,11 +373,16 @@ __global__ void __launch_bounds__(256) kv8_move_kernel(const __grid_constant__ E
   if (lost && A.bad) atomicOr(A.bad, 1);
   if (!to) return;
   const int64_t dst = (((int64_t)page * A.H + h) << A.pshift) + ((b * 16) & mask);
-  move_block<CT, HD>(A, 0, row, scale[0], dst);
-  move_block<CT, HD>(A, 1, row, scale[1], dst);
+  Block<CT, HD> k, v;  // (both on their way before either is looked at)
+  k.load(A.code[0], row);
+  v.load(A.code[1], row);
+  const float ks = k.rescale(scale[0]);
+  k.store(A.code[0], A.scale[0], dst, ks);
+  const float vs = v.rescale(scale[1]);
+  v.store(A.code[1], A.scale[1], dst, vs);
 }
 
-constexpr int SEL_SMEM_KEYS = 50 * 1024;  // keys that fit shared memory (200 KB)
+constexpr int SEL_SMEM_KEYS = 48 * 1024;  // scores that fit shared memory beside the histograms (192 KB)
 
 }  // namespace
 }  // namespace ddl
@@ -317,18 +431,28 @@ extern "C" int ddl_kv8_evict(const ddl_kv8* kv, int32_t H_kv, int32_t head_dim, 
   a.max_keep = max_keep;
   a.sinks = sinks;
   a.recent = recent;
-  void* args[] = {&a};
-  const bool sm = max_len <= SEL_SMEM_KEYS;
-  const void* fn = sm ? (const void*)kv8_select_kernel<512, true> : (const void*)kv8_select_kernel<512, false>;
-  const size_t smem = sm ? (size_t)max_len * 4 : 0;
-  if (smem > 32 * 1024 &&
+  int sms = 0;
+  if ((st = device_sms(sms))) return st;
+  // CTAs a request and head: as many as run at once, two an SM, each with 1024 tokens at least
+  int clusters = 1;
+  while (clusters < 16 && (int64_t)R * H_kv * clusters <= sms && max_len / (2 * clusters) >= 1024) clusters *= 2;
+  const int64_t keys = ((int64_t)max_len + clusters - 1) / clusters;  // of a CTA
+  const bool sm = keys <= SEL_SMEM_KEYS;
+  const void* fn = sm ? (const void*)kv8_select_kernel<true> : (const void*)kv8_select_kernel<false>;
+  const size_t smem = sm ? (size_t)keys * 4 : 0;
+  if (smem > 16 * 1024 &&
       (st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, SEL_SMEM_KEYS * 4))))
     return st;
-  if ((st = cuda_status(launch_pdl(fn, dim3((unsigned)H_kv, (unsigned)R), dim3(512), args, smem, (cudaStream_t)stream))))
+  if (clusters > 8 && (st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1))))
+    return st;
+  void* sargs[] = {&a, &clusters};
+  if ((st = cuda_status(launch_pdl_cluster(fn, dim3((unsigned)(H_kv * clusters), (unsigned)R), dim3(SEL_THREADS), sargs, smem,
+                                           clusters, (cudaStream_t)stream))))
     return st;
   fn = kv->type == DDL_KV8_E4M3
            ? head_dim == 128 ? (const void*)kv8_move_kernel<DDL_KV8_E4M3, 128> : (const void*)kv8_move_kernel<DDL_KV8_E4M3, 64>
            : head_dim == 128 ? (const void*)kv8_move_kernel<DDL_KV8_INT8, 128> : (const void*)kv8_move_kernel<DDL_KV8_INT8, 64>;
   const unsigned ctas = (unsigned)(((int64_t)max_keep + 127) / 128);
+  void* args[] = {&a};
   return cuda_status(launch_pdl(fn, dim3(ctas, (unsigned)H_kv, (unsigned)R), dim3(256), args, 0, (cudaStream_t)stream));
 }
