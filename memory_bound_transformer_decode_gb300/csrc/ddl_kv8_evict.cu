@@ -2,7 +2,7 @@
 // heaviest tokens (ddl_kv8_evict): which tokens of each K/V head stay, and their
 // move to new pages.
 //
-// Two kernels.  The first chooses: a cluster of 1 to 16 CTAs takes a request and head, each CTA a run of tokens whose
+// Two kernels.  The first chooses: a cluster of 1 to 8 CTAs takes a request and head, each CTA a run of tokens whose
 // scores it keeps in shared memory.  The m-th largest by radix select on order-preserving keys, digits of 10 bits of its
 // distance from the largest (so that neither digits nor histogram bins go to what all keys share), the histograms added
 // up in distributed shared memory; it ends early where all of a digit stay.  Then the kept tokens in order: each warp
@@ -96,12 +96,13 @@ __global__ void __launch_bounds__(SEL_THREADS) kv8_select_kernel(const __grid_co
   auto key = [&](int i) -> uint32_t { return score_key(score_of(i)); };
   // the range of the keys
   uint32_t top = 0u, low = ~0u;
-  for (int i = n0 + tid; i < n1; i += 4 * SEL_THREADS) {
-    float s[4];
+  constexpr int U = 8;  // loads on their way
+  for (int i = n0 + tid; i < n1; i += U * SEL_THREADS) {
+    float s[U];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s[j] = i + j * SEL_THREADS < n1 ? score[i + j * SEL_THREADS] : 0.f;
+    for (int j = 0; j < U; ++j) s[j] = i + j * SEL_THREADS < n1 ? score[i + j * SEL_THREADS] : 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < U; ++j) {
       const int x = i + j * SEL_THREADS;
       if (SM && x < n1) sel_scores[x - n0] = s[j];
       if (x >= m0 && x < m1) {
@@ -190,25 +191,34 @@ __global__ void __launch_bounds__(SEL_THREADS) kv8_select_kernel(const __grid_co
     all = need == sh_inside;
     bits = shift;
   }
-  const bool none = c.keep == c.sinks + c.recent;
-  // 2: stays, 1: one of those at the distance, 0: goes
-  auto state = [&](int i) -> int {
+  // keys above k_stay stay, those from k_tie up to it are the ties (64 bits: none may be above, or all)
+  int64_t k_stay = (int64_t)top - (int64_t)(at >> bits << bits), k_tie = k_stay - ((int64_t)1 << bits) + 1;
+  if (all) k_stay = k_tie - 1;
+  if (c.keep == c.sinks + c.recent) k_stay = k_tie = 1ll << 32;
+  // 2: stays, 1: a tie, 0: goes
+  const uint32_t stay_from = (uint32_t)(k_stay + 1 < 0 ? 0 : k_stay + 1 > 0xffffffffll ? 0xffffffffll : k_stay + 1);
+  const uint32_t tie_from = (uint32_t)(k_tie < 0 ? 0 : k_tie > 0xffffffffll ? 0xffffffffll : k_tie);
+  auto state = [&](int i) -> int {  // (no key is 0xffffffff)
     if (i < lo || i >= hi) return 2;
-    if (none) return 0;
-    const uint32_t x = (top - key(i)) >> bits, y = at >> bits;
-    return x < y || (all && x == y) ? 2 : x == y ? 1 : 0;
+    const uint32_t k = key(i);
+    return k >= stay_from ? 2 : k >= tie_from ? 1 : 0;
   };
   // the kept tokens in order: run of tokens [w0, w1) per warp
   const int w0 = n0 + (int)((int64_t)(n1 - n0) * warp / SEL_WARPS), w1 = n0 + (int)((int64_t)(n1 - n0) * (warp + 1) / SEL_WARPS);
   uint32_t ns = 0, nt = 0;
   if (SM) __syncthreads();  // (the keys, where no digit was needed)
-  for (int i = w0 + lane; i < w1; i += 32) {
-    const int s = state(i);
-    ns += s == 2;
-    nt += s == 1;
+  // 32 tokens a step: which stay and which are ties; lane l keeps step l's for the second time (of 32 steps)
+  uint32_t my_stay = 0, my_tie = 0;
+  for (int i0 = w0, k = 0; i0 < w1; i0 += 32, ++k) {
+    const int s = i0 + lane < w1 ? state(i0 + lane) : 0;
+    const uint32_t ms = __ballot_sync(FULL, s == 2), me = __ballot_sync(FULL, s == 1);
+    if (k == lane) {
+      my_stay = ms;
+      my_tie = me;
+    }
+    ns += __popc(ms);
+    nt += __popc(me);
   }
-  ns = __reduce_add_sync(FULL, ns);
-  nt = __reduce_add_sync(FULL, nt);
   __syncthreads();  // (wsum's last readers)
   if (lane == 0) {
     wsum[0][warp] = ns;
@@ -229,11 +239,16 @@ __global__ void __launch_bounds__(SEL_THREADS) kv8_select_kernel(const __grid_co
   }
   int32_t* const kept = A.kept + ((int64_t)r * A.H + h) * A.max_keep;
   const uint32_t below = (1u << lane) - 1;
-  for (int i0 = w0; i0 < w1; i0 += 32) {
-    const int i = i0 + lane, s = i < w1 ? state(i) : 0;
-    const uint32_t ms = __ballot_sync(FULL, s == 2), me = __ballot_sync(FULL, s == 1);
+  for (int i0 = w0, k = 0; i0 < w1; i0 += 32, ++k) {
+    const int i = i0 + lane;
+    uint32_t ms = __shfl_sync(FULL, my_stay, k & 31), me = __shfl_sync(FULL, my_tie, k & 31);
+    if (k >= 32) {
+      const int s = i < w1 ? state(i) : 0;
+      ms = __ballot_sync(FULL, s == 2);
+      me = __ballot_sync(FULL, s == 1);
+    }
     const uint32_t tie = ties + __popc(me & below);
-    if (s == 2 || (s == 1 && tie < need)) {
+    if ((ms >> lane & 1) || ((me >> lane & 1) && tie < need)) {
       const uint32_t x = to + __popc(ms & below) + (tie < need ? tie : need);
       kept[x] = i;
       out[x] = score_of(i);
@@ -433,17 +448,16 @@ extern "C" int ddl_kv8_evict(const ddl_kv8* kv, int32_t H_kv, int32_t head_dim, 
   a.recent = recent;
   int sms = 0;
   if ((st = device_sms(sms))) return st;
-  // CTAs a request and head: as many as run at once, two an SM, each with 1024 tokens at least
+  // CTAs a request and head: as many as run at once, with 2048 tokens each at least (a barrier of 16 CTAs costs 1 us: 1
+  // request of 32769 tokens, 8 heads, in clusters of 1 / 4 / 8 / 16 47 / 30 / 24 / 27 us)
   int clusters = 1;
-  while (clusters < 16 && (int64_t)R * H_kv * clusters <= sms && max_len / (2 * clusters) >= 1024) clusters *= 2;
+  while (clusters < 8 && (int64_t)R * H_kv * clusters <= sms && max_len / (2 * clusters) >= 2048) clusters *= 2;
   const int64_t keys = ((int64_t)max_len + clusters - 1) / clusters;  // of a CTA
   const bool sm = keys <= SEL_SMEM_KEYS;
   const void* fn = sm ? (const void*)kv8_select_kernel<true> : (const void*)kv8_select_kernel<false>;
   const size_t smem = sm ? (size_t)keys * 4 : 0;
   if (smem > 16 * 1024 &&
       (st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, SEL_SMEM_KEYS * 4))))
-    return st;
-  if (clusters > 8 && (st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1))))
     return st;
   void* sargs[] = {&a, &clusters};
   if ((st = cuda_status(launch_pdl_cluster(fn, dim3((unsigned)(H_kv * clusters), (unsigned)R), dim3(SEL_THREADS), sargs, smem,
