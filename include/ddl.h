@@ -519,6 +519,21 @@ int ddl_stack_step_kv8(const ddl_shape* shape, ddl_wtype wtype, const ddl_layer_
                        const uint16_t* x_bf16, float* resid_out, uint16_t* out_bf16, int32_t* bad_out,
                        void* workspace, size_t ws_bytes, void* stream);
 
+/* ddl_stack_step_kv8 that also keeps the scores of every layer's tokens: after a
+ * layer's attention ddl_kv8_score is made of its rows.  score: host array of L
+ * device pointers, each [R][H_kv][score_stride] fp32; decay as there.  When
+ * requests are cut, all layers are cut by the same keep_len (ddl_kv8_evict with
+ * each layer's own scores); row_pos goes on with the rows' true positions.
+ * workspace: >= ddl_stack_kv8_scored_workspace_bytes(...). */
+size_t ddl_stack_kv8_scored_workspace_bytes(const ddl_shape* shape, int32_t R, int32_t T, int32_t max_rows, int32_t max_len);
+int ddl_stack_step_kv8_scored(const ddl_shape* shape, ddl_wtype wtype, const ddl_layer_w* layers, const ddl_kv8* kv,
+                              int32_t L, const ddl_attn_opts* opts, int32_t R, int32_t T, int32_t max_rows,
+                              int32_t max_len, const int32_t* row_off, const int32_t* kv_len, const int32_t* row_pos,
+                              const int32_t* slot, const int32_t* page_table, int32_t pages_per_seq,
+                              const float* resid_in, const uint16_t* x_bf16, float* resid_out, uint16_t* out_bf16,
+                              float* const* score, int64_t score_stride, float decay, int32_t* bad_out,
+                              void* workspace, size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------ token step
  * The steps on either side of the layer stack in the primer's §1.2
  * decode step: the last token's embedding row before it, and after it a token

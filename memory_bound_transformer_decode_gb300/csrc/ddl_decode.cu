@@ -2683,6 +2683,10 @@ struct Kv8Step {
   uint16_t *k, *v;  // [rows][H_kv][head_dim]
   void* ws;
   size_t ws_bytes;
+  float* const* score;  // per layer the tokens' drawn weight, or NULL
+  int64_t score_stride;
+  float decay;
+  float* lse;           // [rows][H_q] with score
 };
 
 // RoPE table of rows whose positions lie in device memory (a padding row's
@@ -2849,8 +2853,12 @@ static int decode(const ddl_shape* s, ddl_wtype wtype, const ddl_layer_w* layers
     int rc = ddl_kv8_append(&k8->kv[gl], s->H_kv, HD, DDL_T_BF16, k8->k, Nkv, k8->v, Nkv, k8->slot, B, k8->bad, stream);
     if (rc) return rc;
     rc = ddl_kv8_attention(&k8->kv[gl], s->H_q, s->H_kv, HD, DDL_T_F32, k8->opts, k8->R, B, k8->max_rows, k8->max_len,
-                           k8->row_off, k8->kv_len, k8->table, k8->per, P.q, Nq, P.attn, Nq, nullptr, k8->bad, k8->ws,
+                           k8->row_off, k8->kv_len, k8->table, k8->per, P.q, Nq, P.attn, Nq, k8->lse, k8->bad, k8->ws,
                            k8->ws_bytes, stream);
+    if (!rc && k8->score)
+      rc = ddl_kv8_score(&k8->kv[gl], s->H_q, s->H_kv, HD, DDL_T_F32, k8->opts, k8->R, B, k8->max_rows, k8->max_len,
+                         k8->row_off, k8->kv_len, k8->table, k8->per, P.q, Nq, k8->lse, k8->decay, k8->score[gl],
+                         k8->score_stride, k8->bad, stream);
     if (rc || use_tc || !wide) return rc;
     attn_max_kernel<<<B, 256, 0, cs>>>(P.attn, Nq, P.xmax + (l * NSTAGE + ST_WO) * MAX_B);
     return cuda_status(cudaGetLastError());
@@ -3087,12 +3095,18 @@ extern "C" size_t ddl_stack_kv8_workspace_bytes(const ddl_shape* shape, int32_t 
   return (size_t)(align256((int64_t)base) + 2 * align256((int64_t)T * shape->H_kv * shape->head_dim * 2)) + att;
 }
 
-extern "C" int ddl_stack_step_kv8(const ddl_shape* shape, ddl_wtype wtype, const ddl_layer_w* layers,
+// With the scores' log-sum-exp behind the step's own workspace of `need` bytes.
+static size_t scored_bytes(const ddl_shape* shape, int32_t T, size_t need) {
+  return (size_t)(align256((int64_t)need) + align256((int64_t)T * shape->H_q * 4));
+}
+
+static int stack_step_kv8(const ddl_shape* shape, ddl_wtype wtype, const ddl_layer_w* layers,
                                   const ddl_kv8* kv, int32_t L, const ddl_attn_opts* opts, int32_t R, int32_t T,
                                   int32_t max_rows, int32_t max_len, const int32_t* row_off, const int32_t* kv_len,
                                   const int32_t* row_pos, const int32_t* slot, const int32_t* page_table,
                                   int32_t pages_per_seq, const float* resid_in, const uint16_t* x_bf16,
-                                  float* resid_out, uint16_t* out_bf16, int32_t* bad_out, void* workspace,
+                                  float* resid_out, uint16_t* out_bf16, float* const* score,
+                                  int64_t score_stride, float decay, int32_t* bad_out, void* workspace,
                                   size_t ws_bytes, void* stream) {
   int st = check_shape(shape);
   if (st) return st;
@@ -3114,19 +3128,59 @@ extern "C" int ddl_stack_step_kv8(const ddl_shape* shape, ddl_wtype wtype, const
   ddl_attn_opts plain = {1.f / sqrtf((float)shape->head_dim), 0.f, 0, nullptr};
   if (!opts) opts = &plain;
   if ((st = check_attn_opts(opts))) return st;
+  if (score) {
+    if (score_stride < max_len || !(decay >= 0.f && decay <= 1.f)) return DDL_ERR_ARG;
+    for (int l = 0; l < L; ++l) {
+      if (!score[l]) return DDL_ERR_ARG;
+      if ((uintptr_t)score[l] & 3u) return DDL_ERR_ALIGN;
+    }
+  }
   DevInfo di;
   if ((st = device_info(di))) return st;
   const size_t need = ddl_stack_kv8_workspace_bytes(shape, R, T, max_rows, max_len);
   if (need == 0) return DDL_ERR_UNSUPPORTED;
-  if (ws_bytes < need) return DDL_ERR_WORKSPACE;
+  if (ws_bytes < (score ? scored_bytes(shape, T, need) : need)) return DDL_ERR_WORKSPACE;
   const size_t base = (size_t)align256((int64_t)ddl_workspace_bytes(shape, T, 1));
   const size_t rows = (size_t)align256((int64_t)T * shape->H_kv * shape->head_dim * 2);
   uint8_t* extra = (uint8_t*)workspace + base;
   const Kv8Step k8 = {kv, opts, R, max_rows, max_len, pages_per_seq, row_off, kv_len, row_pos, slot, page_table, bad_out,
-                      (uint16_t*)extra, (uint16_t*)(extra + rows), extra + 2 * rows, need - base - 2 * rows};
+                      (uint16_t*)extra, (uint16_t*)(extra + rows), extra + 2 * rows, need - base - 2 * rows,
+                      score, score_stride, decay, score ? (float*)((uint8_t*)workspace + align256((int64_t)need)) : nullptr};
   int64_t zero[TC_MAX_B] = {0};
   return decode(shape, wtype, layers, nullptr, L, T, 0, resid_in, x_bf16, resid_out, out_bf16, workspace, base, stream,
                 zero, false, nullptr, &k8);
+}
+
+extern "C" int ddl_stack_step_kv8(const ddl_shape* shape, ddl_wtype wtype, const ddl_layer_w* layers,
+                                  const ddl_kv8* kv, int32_t L, const ddl_attn_opts* opts, int32_t R, int32_t T,
+                                  int32_t max_rows, int32_t max_len, const int32_t* row_off, const int32_t* kv_len,
+                                  const int32_t* row_pos, const int32_t* slot, const int32_t* page_table,
+                                  int32_t pages_per_seq, const float* resid_in, const uint16_t* x_bf16,
+                                  float* resid_out, uint16_t* out_bf16, int32_t* bad_out, void* workspace,
+                                  size_t ws_bytes, void* stream) {
+  return stack_step_kv8(shape, wtype, layers, kv, L, opts, R, T, max_rows, max_len, row_off, kv_len, row_pos, slot, page_table,
+                        pages_per_seq, resid_in, x_bf16, resid_out, out_bf16, nullptr, 0, 1.f, bad_out, workspace, ws_bytes,
+                        stream);
+}
+
+extern "C" size_t ddl_stack_kv8_scored_workspace_bytes(const ddl_shape* shape, int32_t R, int32_t T, int32_t max_rows,
+                                                       int32_t max_len) {
+  const size_t need = ddl_stack_kv8_workspace_bytes(shape, R, T, max_rows, max_len);
+  return need ? scored_bytes(shape, T, need) : 0;
+}
+
+extern "C" int ddl_stack_step_kv8_scored(const ddl_shape* shape, ddl_wtype wtype, const ddl_layer_w* layers,
+                                         const ddl_kv8* kv, int32_t L, const ddl_attn_opts* opts, int32_t R, int32_t T,
+                                         int32_t max_rows, int32_t max_len, const int32_t* row_off,
+                                         const int32_t* kv_len, const int32_t* row_pos, const int32_t* slot,
+                                         const int32_t* page_table, int32_t pages_per_seq, const float* resid_in,
+                                         const uint16_t* x_bf16, float* resid_out, uint16_t* out_bf16,
+                                         float* const* score, int64_t score_stride, float decay, int32_t* bad_out,
+                                         void* workspace, size_t ws_bytes, void* stream) {
+  if (!score) return DDL_ERR_ARG;
+  return stack_step_kv8(shape, wtype, layers, kv, L, opts, R, T, max_rows, max_len, row_off, kv_len, row_pos, slot, page_table,
+                        pages_per_seq, resid_in, x_bf16, resid_out, out_bf16, score, score_stride, decay, bad_out, workspace,
+                        ws_bytes, stream);
 }
 
 extern "C" int ddl_set_launch_mode(int32_t mode) {

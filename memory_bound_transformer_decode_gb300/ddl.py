@@ -31,7 +31,8 @@ EXPORTED = ("ddl_quantize_int4", "ddl_packed_layer_bytes", "ddl_pack_layer", "dd
             "ddl_head_workspace_bytes", "ddl_lm_head", "ddl_stack_decode_ragged",
             "ddl_stack_prefill", "ddl_stack_decode_paged", "ddl_stack_prefill_paged",
             "ddl_page_plan", "ddl_kv8_append", "ddl_kv8_attention_workspace_bytes", "ddl_kv8_attention",
-            "ddl_stack_kv8_workspace_bytes", "ddl_stack_step_kv8", "ddl_kv8_score", "ddl_kv8_evict", "ddl_sample")
+            "ddl_stack_kv8_workspace_bytes", "ddl_stack_step_kv8", "ddl_kv8_score", "ddl_kv8_evict", "ddl_sample",
+            "ddl_stack_kv8_scored_workspace_bytes", "ddl_stack_step_kv8_scored")
 
 
 class DDLError(RuntimeError):
@@ -157,6 +158,11 @@ def load(build_if_missing: bool = False):
         lib.ddl_stack_kv8_workspace_bytes.restype = sz
         lib.ddl_stack_step_kv8.argtypes = [P(Shape), ctypes.c_int, P(LayerW), P(KV8), i32, P(AttnOpts), i32, i32, i32,
                                            i32, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+        lib.ddl_stack_kv8_scored_workspace_bytes.argtypes = [P(Shape), i32, i32, i32, i32]
+        lib.ddl_stack_kv8_scored_workspace_bytes.restype = sz
+        lib.ddl_stack_step_kv8_scored.argtypes = [P(Shape), ctypes.c_int, P(LayerW), P(KV8), i32, P(AttnOpts), i32, i32,
+                                                  i32, i32, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, P(vp), i64,
+                                                  ctypes.c_float, vp, vp, sz, vp]
         lib.ddl_kv8_score.argtypes = [P(KV8), i32, i32, i32, ctypes.c_int, P(AttnOpts), i32, i32, i32, i32, vp, vp, vp,
                                       i32, vp, i64, vp, ctypes.c_float, vp, i64, vp, vp]
         lib.ddl_kv8_evict.argtypes = [P(KV8), i32, i32, i32, i32, vp, i64, vp, vp, i32, i32, vp, i32, vp, i32, i32, vp,
@@ -601,15 +607,21 @@ def ddl_stack_kv8_workspace_bytes(shape: Shape, R: int, T: int, max_rows: int, m
     return n
 
 
-def ddl_stack_step_kv8(shape: Shape, wtype: int, layers: list, pools: list, *, row_off: torch.Tensor,
-                       kv_len: torch.Tensor, row_pos: torch.Tensor, slot: torch.Tensor, page_table: torch.Tensor,
-                       max_rows: int, max_len: int, x_bf16: torch.Tensor | None = None,
-                       resid_in: torch.Tensor | None = None, resid_out: torch.Tensor | None = None,
-                       out_bf16: torch.Tensor | None = None, scale: float | None = None, softcap: float = 0.0,
-                       window: int = 0, slopes: torch.Tensor | None = None, bad: torch.Tensor | None = None,
-                       workspace: torch.Tensor, stream=None):
-    """One step of len(layers) layers on 8-bit pools (one (k, v, k_scale,
-    v_scale) per layer) for the rows that ddl_page_plan has placed."""
+def ddl_stack_kv8_scored_workspace_bytes(shape: Shape, R: int, T: int, max_rows: int, max_len: int) -> int:
+    _int32(R=R, T=T, max_rows=max_rows, max_len=max_len)
+    n = int(load().ddl_stack_kv8_scored_workspace_bytes(ctypes.byref(shape), R, T, max_rows, max_len))
+    if n == 0:
+        raise DDLError("ddl_stack_kv8_scored_workspace_bytes", 1, _lib)
+    return n
+
+
+def _stack_step_kv8(name: str, shape: Shape, wtype: int, layers: list, pools: list, scores, decay, *,
+                    row_off: torch.Tensor, kv_len: torch.Tensor, row_pos: torch.Tensor, slot: torch.Tensor,
+                    page_table: torch.Tensor, max_rows: int, max_len: int, x_bf16: torch.Tensor | None = None,
+                    resid_in: torch.Tensor | None = None, resid_out: torch.Tensor | None = None,
+                    out_bf16: torch.Tensor | None = None, scale: float | None = None, softcap: float = 0.0,
+                    window: int = 0, slopes: torch.Tensor | None = None, bad: torch.Tensor | None = None,
+                    workspace: torch.Tensor, stream=None):
     lib = load()
     _int32(max_rows=max_rows, max_len=max_len, window=window)
     x = x_bf16 if x_bf16 is not None else resid_in
@@ -626,17 +638,47 @@ def ddl_stack_step_kv8(shape: Shape, wtype: int, layers: list, pools: list, *, r
     for i, (layer, pool) in enumerate(zip(layers, pools)):
         lw[i] = LayerW(layer["packed"].data_ptr(), layer["norm1"].data_ptr(), layer["norm2"].data_ptr())
         kv[i] = _kv8(pool, dev, shape.H_kv, shape.head_dim)
+    more = ()
+    if scores is not None:
+        if len(scores) != L or scores[0].dim() != 3:
+            raise ValueError("scores: [R, H_kv, length] for each layer")
+        length = scores[0].shape[2]
+        ptrs = (ctypes.c_void_p * L)(*[_ptr_of("scores", s, torch.float32, dev, (R, shape.H_kv, length)) for s in scores])
+        more = (ptrs, length, float(decay))
     opts = AttnOpts(shape.head_dim ** -0.5 if scale is None else scale, softcap, window,
                     _ptr_of("slopes", slopes, torch.float32, dev, (shape.H_q,)))
     with torch.cuda.device(dev):
-        st = lib.ddl_stack_step_kv8(
+        st = getattr(lib, name)(
             ctypes.byref(shape), wtype, lw, kv, L, ctypes.byref(opts), R, T, max_rows, max_len,
             i32("row_off", row_off, (R + 1,)), i32("kv_len", kv_len, (R,)), i32("row_pos", row_pos, (T,)),
             i32("slot", slot, (T,)), i32("page_table", page_table, (R, page_table.shape[1])), page_table.shape[1],
             act("resid_in", resid_in, torch.float32), act("x_bf16", x_bf16, torch.bfloat16),
-            act("resid_out", resid_out, torch.float32), act("out_bf16", out_bf16, torch.bfloat16),
+            act("resid_out", resid_out, torch.float32), act("out_bf16", out_bf16, torch.bfloat16), *more,
             i32("bad", bad, (1,)), _ptr(workspace), workspace.nbytes, _stream(stream))
-    _check("ddl_stack_step_kv8", st)
+    _check(name, st)
+
+
+def ddl_stack_step_kv8(shape: Shape, wtype: int, layers: list, pools: list, *, row_off: torch.Tensor,
+                       kv_len: torch.Tensor, row_pos: torch.Tensor, slot: torch.Tensor, page_table: torch.Tensor,
+                       max_rows: int, max_len: int, x_bf16: torch.Tensor | None = None,
+                       resid_in: torch.Tensor | None = None, resid_out: torch.Tensor | None = None,
+                       out_bf16: torch.Tensor | None = None, scale: float | None = None, softcap: float = 0.0,
+                       window: int = 0, slopes: torch.Tensor | None = None, bad: torch.Tensor | None = None,
+                       workspace: torch.Tensor, stream=None):
+    """One step of len(layers) layers on 8-bit pools (one (k, v, k_scale,
+    v_scale) per layer) for the rows that ddl_page_plan has placed."""
+    _stack_step_kv8("ddl_stack_step_kv8", shape, wtype, layers, pools, None, None, row_off=row_off, kv_len=kv_len,
+                    row_pos=row_pos, slot=slot, page_table=page_table, max_rows=max_rows, max_len=max_len, x_bf16=x_bf16,
+                    resid_in=resid_in, resid_out=resid_out, out_bf16=out_bf16, scale=scale, softcap=softcap, window=window,
+                    slopes=slopes, bad=bad, workspace=workspace, stream=stream)
+
+
+def ddl_stack_step_kv8_scored(shape: Shape, wtype: int, layers: list, pools: list, scores: list, decay: float = 1.0,
+                              **step):
+    """ddl_stack_step_kv8 (its other arguments by name) that also brings up to
+    date the attention weight that each layer's cached tokens have drawn:
+    scores, one fp32 [R, H_kv, length] per layer, as ddl_kv8_score does."""
+    _stack_step_kv8("ddl_stack_step_kv8_scored", shape, wtype, layers, pools, scores, decay, **step)
 
 
 # ------------------------------------------------------------------ token step

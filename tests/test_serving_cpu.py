@@ -121,3 +121,24 @@ def test_reference_evict():
     assert kept.tolist() == [[[0, 2, 5, 6]]] and out[0, 0, :4].tolist() == [5, 3, 9, 2]
     x = codes[0][0, 0, [0, 2, 5, 6]].astype(float) * 0.5
     assert np.array_equal(c[0][1, 0, :4].astype(float) * s[0][1, 0, 0], x) and not c[0][1, 0, 4:].any()
+
+
+def test_scored_stack_refusals(lib):
+    needs_no_gpu()
+    shape = ddl.Shape(512, 8, 2, 64, 1408, 1e-6, 1e4)
+    lw = (ddl.LayerW * 2)(ddl.LayerW(256, 256, 256), ddl.LayerW(256, 256, 256))
+    kv = (ddl.KV8 * 2)(_kv(), _kv())
+
+    def call(scores=(2560, 2816), **kw):
+        ptrs = (ctypes.c_void_p * 2)(*scores) if scores else None
+        a = dict(kv=kv, L=2, opts=None, R=2, T=3, rows=2, len=64, off=v(1), kl=v(2), pos=v(3), slot=v(4), tab=v(5), per=4,
+                 res=None, x=v(6), rout=None, out=v(7), score=ptrs, stride=64, decay=1.0, bad=None, ws=v(8), n=1 << 30)
+        a.update(kw)
+        return lib.ddl_stack_step_kv8_scored(ctypes.byref(shape), ddl.INT4, lw, *a.values(), None)
+
+    assert call() == 6
+    assert call(scores=None) == 8 and call(scores=(2560, None)) == 8 and call(scores=(2560, 2818)) == 3
+    for kw, code in [(dict(stride=63), 8), (dict(decay=1.1), 8), (dict(decay=math.nan), 8), (dict(L=0), 8), (dict(T=65), 5),
+                     (dict(ws=None), 4), (dict(slot=None), 8)]:
+        assert call(**kw) == code, kw
+    assert lib.ddl_stack_kv8_scored_workspace_bytes(ctypes.byref(shape), 0, 3, 2, 64) == 0
