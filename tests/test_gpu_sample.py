@@ -109,6 +109,22 @@ def test_two_values_and_coarse_logits():
     check(y, t=8.0, p=[0.99, 0.97, 0.5, 0.9999])
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_many_rows_of_nearly_flat_logits(dtype):
+    """A CTA a row, thousands of its elements within 1/50 octave: more than a bin of the histogram can hold, some with
+    a part of the row above them, masked tokens, and a top-k of more than there are."""
+    B, V = 160, 24000
+    g = np.random.RandomState(3)
+    x = logits(B, V, 5, spread=1.0, peaks=40)
+    few = torch.arange(V, device="cuda") % 3 == 0
+    x[1::2] = torch.where(few, x[1::2], x[1::2] * 1e-4)
+    x[2::4] = torch.where(few, float("-inf"), x[2::4])
+    t = np.where(np.arange(B) % 2 == 0, 1e4, 1.0)
+    check(x.to(DTYPES[dtype]), t=t, k=g.choice([0, 7, 5000, 13000, 17000, 24000], B), p=g.choice([0.2, 0.9, 1.0], B),
+          m=g.choice([0.0, 0.5], B), seed=B)
+    check(x.to(DTYPES[dtype]), t=t, p=0.6, seed=V)
+
+
 @pytest.mark.parametrize("t", [1e-18, 1e-6, 1e6, 1e30, math.inf, math.nan, -1.0, 2.0 ** -60, 2.0 ** -61])
 def test_temperatures(t):
     x = logits(2, 3000, 2)
