@@ -107,7 +107,7 @@ struct SampleSmem {
     Entry all[SM_LIST];  // the row's list, when the histogram is done with
   };
   unsigned long long warp_sum[SM_WARPS];      // per warp: weights that certainly stay
-  unsigned long long sums[2];                 // weights above the open bins, and between them and the k-th element's
+  unsigned long long sums[2];                 // weights before the open bins, and before the k-th element's
   unsigned long long chunk[SM_MAX_CLUSTER * SM_WARPS];
   uint32_t num[256], mass_lo[256], mass_hi[256];  // a digit's elements and their weights
   uint32_t range[2];
@@ -251,10 +251,14 @@ struct Row {
       }
     }
   }
-  // All lanes of the warp take part in every f.
+  // All lanes of the warp take part in every f, and in g, which comes after U of them at most.
   template <class F>
   __device__ __forceinline__ void each(int v0, int v1, F&& f) const {
-    constexpr int U = 4;  // loads on their way
+    each(v0, v1, f, []() {});
+  }
+  // U: loads on their way.
+  template <int U = 4, class F, class G>
+  __device__ __forceinline__ void each(int v0, int v1, F&& f, G&& g) const {
     const int lane = threadIdx.x & 31, w0 = off > 0 ? 1 : 0, w1 = min(v1, (V + off) / VEC);  // whole: [w0, w1)
     for (int v = v0; v < v1; v += 32 * U) {
       if (v >= w0 && v + 32 * U <= w1) {
@@ -267,6 +271,7 @@ struct Row {
           unpack(x[j], l);
           f((v + 32 * j + lane) * VEC - off, l);
         }
+        g();
       } else {
 #pragma unroll 1
         for (int j = v; j < min(v + 32 * U, v1); j += 32) {
@@ -274,6 +279,7 @@ struct Row {
           values(j + lane, v1, l);
           f((j + lane) * VEC - off, l);
         }
+        g();
       }
     }
   }
@@ -288,10 +294,6 @@ __device__ __forceinline__ unsigned long long warp_add(unsigned long long x) {
 __device__ __forceinline__ uint32_t cluster_add(const uint32_t* p, int C) {
   const int lane = threadIdx.x & 31;
   return __reduce_add_sync(FULL, lane < C ? ldu_cluster(cluster_addr(smem_addr(p), lane)) : 0u);
-}
-__device__ __forceinline__ unsigned long long cluster_add(const unsigned long long* p, int C) {
-  const int lane = threadIdx.x & 31;
-  return warp_add(lane < C ? ldl_cluster(cluster_addr(smem_addr(p), lane)) : 0ull);
 }
 // Exclusive sum over the CTA of a value per thread; `all` gets the sum of all.
 template <class T>
@@ -552,13 +554,14 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const __grid_cons
   extern __shared__ __align__(16) uint8_t sample_smem[];
   SampleSmem& S = *reinterpret_cast<SampleSmem*>(sample_smem);
   constexpr int VEC = Row<DT>::VEC;
+  constexpr int U = 16 / VEC;  // loads on their way where registers are short (256 rows of 128256 bf16, top-p: 164 us, with 4 186)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = A.cluster, b = blockIdx.x / C, rank = blockIdx.x % C, runs = C * SM_WARPS;
   if (tid < 64) {
     S.table.hi[tid] = g_exp_table.hi[tid];
     S.table.lo[tid] = g_exp_table.lo[tid];
   }
-  for (int i = tid; i < SM_BINS; i += SM_THREADS) S.count[i] = S.place[i] = 0;
+  for (int i = tid; i < SM_BINS; i += SM_THREADS) S.count[i] = S.place[i] = S.rcount[i] = S.rplace[i] = 0;
   pdl_trigger();
   pdl_wait();
   const Row<DT> row(A, b);
@@ -700,16 +703,17 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const __grid_cons
       }
     });
     cluster_sync();
-    const int per = SM_BINS / C;
-    for (int i = tid; i < per; i += SM_THREADS) {
+    // bins [rank per, (rank + 1) per) of the cluster's CTAs: each of `split` parts of the threads adds up as many of them
+    const int per = SM_BINS / C, split = max(SM_THREADS / per, 1), step = C / split;
+    for (int i = tid & (per - 1), c0 = tid / per * step; i < per; i += SM_THREADS) {
       uint32_t n = 0, q = 0;
-#pragma unroll 8
-      for (int c = 0; c < C; ++c) {
+#pragma unroll 4
+      for (int c = c0; c < c0 + step; ++c) {
         n += ldu_cluster(cluster_addr(smem_addr(&S.count[rank * per + i]), c));
         if (by_p) q += ldu_cluster(cluster_addr(smem_addr(&S.place[rank * per + i]), c));
       }
-      S.rcount[i] = n;
-      S.rplace[i] = q;
+      atomicAdd(&S.rcount[i], n);
+      if (by_p) atomicAdd(&S.rplace[i], q);
     }
     cluster_sync();
     // every CTA: the bins' numbers and bounds of their sums of weights; thread i has bins 4 i .. 4 i + 3
@@ -755,10 +759,10 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const __grid_cons
         if (i > o.k_bin || n[j] == 0) {
           lo[j] = hi[j] = 0.f;
         } else if (i == o.k_bin) {
-          lo[j] = (float)o.k_in * exp2f(-(at + 1.f) / SM_PER_OCTAVE) * 0.9999f;
-          hi[j] = (float)o.k_in * exp2f(-at / SM_PER_OCTAVE) * 1.0001f;
+          lo[j] = (float)o.k_in * exp2f(-(at + 1.f) * (1.f / SM_PER_OCTAVE)) * 0.9999f;
+          hi[j] = (float)o.k_in * exp2f(-at * (1.f / SM_PER_OCTAVE)) * 1.0001f;
         } else {
-          const float w = cnt * exp2f(-(at + lo[j] / (cnt * SM_FRAC)) / SM_PER_OCTAVE);
+          const float w = cnt * exp2f(-(at + __fdividef(lo[j], cnt * SM_FRAC)) * (1.f / SM_PER_OCTAVE));
           lo[j] = w * 0.9999f;
           hi[j] = w * 1.0001f;
         }
@@ -768,13 +772,20 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const __grid_cons
       float blo = block_before(slo, S.redf, all_lo), bhi = block_before(shi, S.redg, all_hi);
       // sums of 2048 fp32 numbers: within 1e-4 (some 40 additions in a row, 2^-24 each)
       const float want_lo = P * all_lo * 0.9998f, want_hi = P * all_hi * 1.0002f;
+      int first_lo = SM_BINS, first_hi = SM_BINS;
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
         const int i = tid * PER + j;
         blo += lo[j];
         bhi += hi[j];
-        if (n[j] && i <= o.k_bin && bhi >= want_lo) atomicMin(&S.sel_i[2], i);
-        if (n[j] && i <= o.k_bin && blo >= want_hi) atomicMin(&S.sel_i[3], i);
+        if (n[j] && i <= o.k_bin && bhi >= want_lo) first_lo = min(first_lo, i);
+        if (n[j] && i <= o.k_bin && blo >= want_hi) first_hi = min(first_hi, i);
+      }
+      first_lo = __reduce_min_sync(FULL, first_lo);
+      first_hi = __reduce_min_sync(FULL, first_hi);
+      if (lane == 0) {
+        atomicMin(&S.sel_i[2], first_lo);
+        atomicMin(&S.sel_i[3], first_hi);
       }
       __syncthreads();
       o.p_lo = min(S.sel_i[2], SM_BINS - 1);
@@ -790,78 +801,79 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const __grid_cons
   if (open && !heads && least > -INFINITY && W.has(W.log2w(least)) && W.bin_of(W.log2w(least)) < sure) open = false;
 
   // 3. exact sums of what certainly stays, the list of the open bins
-  unsigned long long above = 0, between = 0;  // before the open bins; between them and the k-th element's
+  unsigned long long above = 0, to_k = 0;  // before the open bins; before the k-th element's bin, open ones among them
+  uint32_t hs = 0, hs2 = 0;                // of a few elements: high and low parts
+  int32_t ls = 0, ls2 = 0;
   if (heads) {
     // (nothing to add up)
   } else if (!open) {
-    row.each(v0, v1, [&](int, float(&l)[VEC]) {
-      W.fix(l);
-      uint32_t h = 0;
-      int32_t s = 0;
+    row.template each<U>(
+        v0, v1,
+        [&](int, float(&l)[VEC]) {
+          W.fix(l);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const float p = W.log2w(l[i]);
-        uint32_t hi;
-        int32_t low;
-        W.parts(l[i], p, hi, low);
-        if (W.has(p) && l[i] >= least) {
-          h += hi;
-          s += low;
-        }
-      }
-      above += W.units(h, s);
-    });
+          for (int i = 0; i < VEC; ++i) {
+            const float p = W.log2w(l[i]);
+            uint32_t hi;
+            int32_t low;
+            W.parts(l[i], p, hi, low);
+            if (W.has(p) && l[i] >= least) {
+              hs += hi;
+              ls += low;
+            }
+          }
+        },
+        [&]() {
+          above += W.units(hs, ls);
+          hs = 0;
+          ls = 0;
+        });
   } else {
-    const int p_lo = by_p ? o.p_lo : o.k_bin, p_hi = by_p ? o.p_hi : o.k_bin;
-    row.each(v0, v1, [&](int id, float(&l)[VEC]) {
-      W.fix(l);
-      float p[VEC];
-      int at[VEC];
-      bool in = false, some = false;  // of the open bins; before them or between
+    // bins as the floats that bin_bits gives
+    const float p_lo = 0x1p23f + (float)sure, p_hi = 0x1p23f + (float)(by_p ? o.p_hi : o.k_bin), k_bin = 0x1p23f + (float)o.k_bin;
+    row.template each<U>(
+        v0, v1,
+        [&](int id, float(&l)[VEC]) {
+          W.fix(l);
+          uint32_t in = 0;  // which are of the open bins
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        p[i] = W.log2w(l[i]);
-        at[i] = W.has(p[i]) ? W.bin_of(p[i]) : SM_BINS + 1;
-        const bool listed = (at[i] >= p_lo && at[i] <= p_hi) || at[i] == o.k_bin;
-        in |= listed;
-        some |= at[i] < o.k_bin && !listed;
-      }
-      if (in) {
+          for (int i = 0; i < VEC; ++i) {
+            const float p = W.log2w(l[i]), m = W.has(p) ? W.bin_bits(p) : INFINITY;
+            uint32_t hi;
+            int32_t low;
+            W.parts(l[i], p, hi, low);
+            if (m < p_lo) {
+              hs += hi;
+              ls += low;
+            }
+            if (m < k_bin) {
+              hs2 += hi;
+              ls2 += low;
+            }
+            if ((m >= p_lo && m <= p_hi) || m == k_bin) in |= 1u << i;
+          }
+          if (in) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i)
-          if ((at[i] >= p_lo && at[i] <= p_hi) || at[i] == o.k_bin) {
-            const uint32_t to = atomicAdd(&S.list_n, 1u);
-            if (to < SM_LIST) S.list[to] = {logit_key(l[i]), (uint32_t)(id + i) | ((uint32_t)(rank * SM_WARPS + warp) << 20)};
+            for (int i = 0; i < VEC; ++i)
+              if (in >> i & 1) {
+                const uint32_t to = atomicAdd(&S.list_n, 1u);
+                if (to < SM_LIST) S.list[to] = {logit_key(l[i]), (uint32_t)(id + i) | ((uint32_t)(rank * SM_WARPS + warp) << 20)};
+              }
           }
-      }
-      if (__any_sync(FULL, some)) {
-        uint32_t h = 0, h2 = 0;
-        int32_t s = 0, s2 = 0;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          uint32_t hi;
-          int32_t low;
-          W.parts(l[i], p[i], hi, low);
-          if (at[i] < p_lo) {
-            h += hi;
-            s += low;
-          }
-          if (at[i] > p_hi && at[i] < o.k_bin) {
-            h2 += hi;
-            s2 += low;
-          }
-        }
-        above += W.units(h, s);
-        between += W.units(h2, s2);
-      }
-    });
+        },
+        [&]() {
+          above += W.units(hs, ls);
+          to_k += W.units(hs2, ls2);
+          hs = hs2 = 0;
+          ls = ls2 = 0;
+        });
   }
   if (!heads) {
     above = warp_add(above);
-    between = warp_add(between);
+    to_k = warp_add(to_k);
     if (lane == 0) {
       S.warp_sum[warp] = above;
-      S.red64[warp] = between;
+      S.red64[warp] = to_k;
     }
     __syncthreads();
     if (warp < 2) {
@@ -875,10 +887,14 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const __grid_cons
   bool fits = true;
   if (open) {
     if (!heads) {
-      listed = cluster_add(&S.list_n, C);
+      // (all three on their way before the first is waited for)
+      const uint32_t n = lane < C ? ldu_cluster(cluster_addr(smem_addr(&S.list_n), lane)) : 0u;
+      above = lane < C ? ldl_cluster(cluster_addr(smem_addr(&S.sums[0]), lane)) : 0ull;
+      to_k = lane < C ? ldl_cluster(cluster_addr(smem_addr(&S.sums[1]), lane)) : 0ull;
+      listed = __reduce_add_sync(FULL, n);
+      above = warp_add(above);
+      to_k = warp_add(to_k);
       fits = listed <= SM_LIST;
-      above = cluster_add(&S.sums[0], C);
-      between = cluster_add(&S.sums[1], C);
     }
     auto bin_of_key = [&](uint32_t key) { return W.bin_of(W.log2w(key_logit(key))); };
     auto borders = [&](auto src) {
@@ -891,7 +907,9 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const __grid_cons
           const int i = bin_of_key(key);
           return (heads || i == o.k_bin || (i >= o.p_lo && i <= o.p_hi)) && stays(key, id, kth);
         };
-        const unsigned long long total = above + between + src.sum(inside);
+        unsigned long long total = to_k;
+        if (heads || o.k_bin < SM_BINS)
+          total += src.sum([&](uint32_t key, uint32_t id) { return (heads || bin_of_key(key) == o.k_bin) && stays(key, id, kth); });
         const unsigned long long want = P > 0.f ? ceil_mul(frac64(P), total) : 0ull;
         // (bins from p_lo on hold the first element whose running sum reaches `want`, by the bounds)
         const unsigned long long more = want > above ? want - above : 1ull;
@@ -978,22 +996,37 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const __grid_cons
 #pragma unroll
     for (int i = 0; i < VEC; ++i) s += weight_if(v * VEC + i - row.off, l[i]);
   }
-  unsigned long long at = block_before(s, S.red64, all);
-  if (!(s && at <= rest && at + s > rest)) return;
-  for (int v = p0; v < p1; ++v) {
-    float l[VEC];
-    row.values(v, p1, l);
+  if (tid == 0) S.sel_i[0] = S.sel_i[1] = 0;
+  const unsigned long long at = block_before(s, S.red64, all);
+  if (s && at <= rest && at + s > rest) {  // (one thread)
+    S.sel_i[0] = p0;
+    S.sel_i[1] = p1;
+    S.sel_u[0] = rest - at;
+  }
+  __syncthreads();
+  // its part, an element a lane (one thread alone took 16 elements' weights one after the other)
+  if (warp > 0) return;
+  rest = S.sel_u[0];
+  const int64_t q0 = (int64_t)S.sel_i[0] * VEC, q1 = (int64_t)S.sel_i[1] * VEC;
+  for (int64_t q = q0; q < q1; q += 32) {
+    const int64_t x = q + lane;
+    float l[1] = {x < q1 && x >= row.off && x < (int64_t)row.V + row.off ? row.one(x) : -INFINITY};
     W.fix(l);
+    const unsigned long long w = weight_if((int)(x - row.off), l[0]);
+    unsigned long long inc = w;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const unsigned long long w = weight_if(v * VEC + i - row.off, l[i]);
-      if (w && at <= rest && at + w > rest) {
-        A.token[b] = v * VEC + i - row.off;
-        // (no cancellation: both terms are <= 0)
-        if (A.logp) A.logp[b] = (l[i] - W.top) / T - logf(__ull2float_rn(total) * 0x1p-43f);
-      }
-      at += w;
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long y = __shfl_up_sync(FULL, inc, o);
+      if (lane >= o) inc += y;
     }
+    if (inc > rest && inc - w <= rest) {
+      A.token[b] = (int)(x - row.off);
+      // (no cancellation: both terms are <= 0)
+      if (A.logp) A.logp[b] = (l[0] - W.top) / T - logf(__ull2float_rn(total) * 0x1p-43f);
+    }
+    inc = __shfl_sync(FULL, inc, 31);
+    if (inc > rest) return;
+    rest -= inc;
   }
 }
 
