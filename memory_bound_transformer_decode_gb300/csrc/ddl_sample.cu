@@ -113,7 +113,7 @@ struct SampleSmem {
   uint32_t range[2];
   unsigned long long red64b[SM_WARPS];
   unsigned long long red64[SM_WARPS];
-  float redf[SM_WARPS], redg[SM_WARPS];
+  float redf[SM_WARPS];
   uint32_t redu[SM_WARPS];
   float top;
   uint32_t top_id;
@@ -134,6 +134,9 @@ __device__ __forceinline__ uint32_t ldu_cluster(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
+}
+__device__ __forceinline__ void ldu4_cluster(uint32_t a, uint32_t (&v)[4]) {
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(a) : "memory");
 }
 __device__ __forceinline__ unsigned long long ldl_cluster(uint32_t a) {
   unsigned long long v;
@@ -731,23 +734,20 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const __grid_cons
     cluster_sync();
     // every CTA: the bins' numbers and bounds of their sums of weights; thread i has bins 4 i .. 4 i + 3
     constexpr int PER = SM_BINS / SM_THREADS;
-    uint32_t n[PER], sum = 0, all_n;
-    float lo[PER], hi[PER], slo = 0.f, shi = 0.f, all_lo, all_hi;
+    static_assert(PER == 4, "16 bytes a thread, of one CTA's bins");
+    uint32_t n[PER], place[PER] = {}, sum = 0, all_n;
+    {
+      const int c = tid * PER / per, at = tid * PER - c * per;
+      ldu4_cluster(cluster_addr(smem_addr(&S.rcount[at]), c), n);
+      if (by_p) ldu4_cluster(cluster_addr(smem_addr(&S.rplace[at]), c), place);
+    }
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int i = tid * PER + j, c = i / per, at = i - c * per;
-      n[j] = ldu_cluster(cluster_addr(smem_addr(&S.rcount[at]), c));
-      lo[j] = by_p ? (float)ldu_cluster(cluster_addr(smem_addr(&S.rplace[at]), c)) : 0.f;
-      sum += n[j];
+    for (int j = 0; j < PER; ++j) sum += n[j];
+    if (tid == 0) {
+      S.sel_i[0] = S.sel_i[2] = S.sel_i[3] = SM_BINS;
+      S.sel_i[1] = 0;
     }
     uint32_t before = block_before(sum, S.redu, all_n);
-    if (tid == 0) {
-      S.sel_i[0] = SM_BINS;
-      S.sel_i[1] = 0;
-      S.sel_i[2] = SM_BINS;
-      S.sel_i[3] = SM_BINS;
-    }
-    __syncthreads();
     if (by_k && (uint32_t)K < all_n) {
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
@@ -764,35 +764,28 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const __grid_cons
     if (by_p) {
       // A bin's sum is n 2^-(i - 1/2 + mean place) / 47.6, up to the rounding of the places (1 / 2048 of a bin each:
       // 7e-6 of the sum), the curvature inside a bin ((ln 2 / 47.6)^2 / 8 = 2.7e-5) and log2 w's own rounding
-      // (2^-19: 2e-6): within 1e-4.  Of the k-th element's bin, k_in elements of any place.
+      // (2^-19: 2e-6): within 1e-4.  Of the k-th element's bin, the last one, k_in elements of any place.
+      float w[PER], sw = 0.f, all_w;
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
         const int i = tid * PER + j;
         const float cnt = (float)n[j], at = (float)i - 0.5f;
-        if (i > o.k_bin || n[j] == 0) {
-          lo[j] = hi[j] = 0.f;
-        } else if (i == o.k_bin) {
-          lo[j] = (float)o.k_in * exp2f(-(at + 1.f) * (1.f / SM_PER_OCTAVE)) * 0.9999f;
-          hi[j] = (float)o.k_in * exp2f(-at * (1.f / SM_PER_OCTAVE)) * 1.0001f;
-        } else {
-          const float w = cnt * exp2f(-(at + __fdividef(lo[j], cnt * SM_FRAC)) * (1.f / SM_PER_OCTAVE));
-          lo[j] = w * 0.9999f;
-          hi[j] = w * 1.0001f;
-        }
-        slo += lo[j];
-        shi += hi[j];
+        w[j] = i < o.k_bin && n[j]
+                   ? cnt * exp2f(-(at + __fdividef((float)place[j], cnt * SM_FRAC)) * (1.f / SM_PER_OCTAVE)) : 0.f;
+        sw += w[j];
       }
-      float blo = block_before(slo, S.redf, all_lo), bhi = block_before(shi, S.redg, all_hi);
+      float bw = block_before(sw, S.redf, all_w);
+      const float k_top = o.k_bin < SM_BINS ? (float)o.k_in * exp2f(((float)o.k_bin - 0.5f) * (-1.f / SM_PER_OCTAVE)) : 0.f;
+      const float k_low = k_top * exp2f(-1.f / SM_PER_OCTAVE);
       // sums of 2048 fp32 numbers: within 1e-4 (some 40 additions in a row, 2^-24 each)
-      const float want_lo = P * all_lo * 0.9998f, want_hi = P * all_hi * 1.0002f;
+      const float want_lo = P * (all_w + k_low) * 0.9997f, want_hi = P * (all_w + k_top) * 1.0003f;
       int first_lo = SM_BINS, first_hi = SM_BINS;
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
         const int i = tid * PER + j;
-        blo += lo[j];
-        bhi += hi[j];
-        if (n[j] && i <= o.k_bin && bhi >= want_lo) first_lo = min(first_lo, i);
-        if (n[j] && i <= o.k_bin && blo >= want_hi) first_hi = min(first_hi, i);
+        bw += w[j];
+        if (w[j] > 0.f && bw * 1.0001f >= want_lo) first_lo = min(first_lo, i);
+        if (w[j] > 0.f && bw * 0.9999f >= want_hi) first_hi = min(first_hi, i);
       }
       first_lo = __reduce_min_sync(FULL, first_lo);
       first_hi = __reduce_min_sync(FULL, first_hi);
@@ -801,9 +794,8 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const __grid_cons
         atomicMin(&S.sel_i[3], first_hi);
       }
       __syncthreads();
-      o.p_lo = min(S.sel_i[2], SM_BINS - 1);
       o.p_hi = min(min(S.sel_i[3], o.k_bin), SM_BINS - 1);
-      if (o.p_lo > o.p_hi) o.p_lo = o.p_hi;
+      o.p_lo = min(S.sel_i[2], o.p_hi);
     }
     __syncthreads();
   }
