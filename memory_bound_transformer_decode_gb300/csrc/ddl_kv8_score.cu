@@ -178,7 +178,6 @@ __device__ __forceinline__ void reduce_rows(float& s0, float& s1) {  // over the
 template <int DT, int HD>
 struct TileSmem {
   static constexpr int KS = HD / 16, PARTS = DT == DDL_T_F32 ? 2 : 1;
-  static constexpr int PER = PARTS * KS * 32 * 8 + 8 * (int)sizeof(Column);  // bytes a tile
   uint2* frags;  // [tile][part][k-step][lane]
   Column* cols;  // [tile][8]
   __device__ __forceinline__ TileSmem(uint8_t* p, int tiles)
