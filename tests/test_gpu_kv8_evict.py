@@ -118,6 +118,13 @@ def test_a_long_request():
     check([60000], [700], 1, 64, 256, "e4m3", 4, 20)
 
 
+@pytest.mark.parametrize("lens,keep,H", [([10001, 9], [6000, 3], 3), ([400001], [701], 1),
+                                         ([60001, 300, 7] + [100] * 17, [123, 299, 7] + [50] * 17, 8)])
+def test_clusters_of_four_and_scores_left_in_global_memory(lens, keep, H):
+    """A cluster's shared memory holds 393216 scores, that of a CTA (many requests and heads) 49152."""
+    check(lens, keep, H, 64, 256, "int8", 2, 11, seed=len(lens))
+
+
 def test_extreme_scales():
     pool = make_pool(40, 1, 16, 64, "e4m3", 3)
     for i in (2, 3):

@@ -219,3 +219,35 @@ def test_after_the_lm_head():
     best = ddl.ddl_lm_head(D, V, ddl.BF16, head, h, logits=out)
     got, _ = check(out, t=[0.0, 0.8, 1.0, 1.0], k=[0, 20, 0, 50], p=[1.0, 1.0, 0.9, 0.9])
     assert int(got[0]) == int(best[0])
+
+
+def test_the_most_rows_and_one_more():
+    B, V = 65536, 5
+    x = logits(B, V, 1, peaks=2)
+    u = torch.rand(B, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda")
+    got = ddl.ddl_sample(x, u)
+    w = torch.softmax(x.double(), -1).cumsum(-1)
+    want = (w <= u.double()[:, None] * w[:, -1:]).sum(-1)
+    # (a draw within 2^-30 of a border may go either way: softmax's sums are rounded, 5 * 2^-53, the weights to 2^-33)
+    near = ((w - u.double()[:, None] * w[:, -1:]).abs() < 2.0 ** -30).any(-1)
+    assert torch.equal(got[~near].long(), want[~near]) and int(near.sum()) < 10
+    with pytest.raises(Exception):
+        ddl.ddl_sample(logits(B + 1, V, 1, peaks=2), torch.rand(B + 1, device="cuda"))
+
+
+def test_two_streams_at_once():
+    """No state is shared: calls that run side by side give what each gives alone."""
+    xs = [logits(b, 60000, b) for b in (3, 20)]
+    us = [torch.rand(len(x), device="cuda") for x in xs]
+    kw = [dict(top_p=torch.full((3,), 0.9, device="cuda")), dict(top_k=torch.full((20,), 3000, dtype=torch.int32, device="cuda"))]
+    alone = [ddl.ddl_sample(x, u, **k) for x, u, k in zip(xs, us, kw)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i].append(ddl.ddl_sample(xs[i], us[i], **kw[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, alone[i]) for o in outs[i])
