@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const __grid_cons
   const float T = A.temperature ? A.temperature[b] : 1.f;
   const int32_t K = A.top_k ? A.top_k[b] : 0;
   const float P = A.top_p ? A.top_p[b] : 1.f, M = A.min_p ? A.min_p[b] : 0.f;
-  const bool greedy = !(T >= 0x1p-60f);
+  const bool greedy = !(T >= 0x1p-60f) || M > 1.f;  // (no weight reaches a min-p above 1: the first candidate alone)
   const bool by_k = K > 0 && K < A.V, by_p = P < 1.f, by_m = M > 0.f && M < 1.f && T < INFINITY;
   // 1. the maximum, and its lowest id
   float top = -INFINITY;
@@ -654,7 +654,7 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const __grid_cons
   W.table = &S.table;
   // min-p as a bound on the logit: the smallest fp32 number at or above top + T ln(min_p)
   // (an infinite T makes all weights 1)
-  const float least = by_m ? __double2float_ru((double)W.top + S.log_m) : M >= 1.f && T < INFINITY ? W.top : -INFINITY;
+  const float least = by_m ? __double2float_ru((double)W.top + S.log_m) : M == 1.f && T < INFINITY ? W.top : -INFINITY;
 
   // 1b. the bound by the lanes' maxima, in bins of 8; all elements from there up to the list
   Open o = {SM_BINS, 0u, SM_BINS, -1};

@@ -251,3 +251,22 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(o, alone[i]) for o in outs[i])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("V", [2, 40, 9000, 152064])
+def test_a_min_p_above_one_leaves_the_first_candidate(dtype, V):
+    """No weight reaches it, so of several largest logits the lowest id alone stays; a min-p of 1 keeps them all."""
+    inf = math.inf
+    x = torch.round(logits(9, V, V)).clamp(max=3).to(DTYPES[dtype])  # many largest ones
+    x[6, V // 2:] = inf
+    x[7, :] = -inf
+    m = [2.0, inf, 1.0, 1 + 2.0 ** -23, 2.0, 1.0, 2.0, 2.0, 1.0]
+    t = [1.0, 1.0, 1.0, 0.5, inf, inf, 1.0, 1.0, 1e-3]
+    for kw in (dict(), dict(k=7), dict(p=0.6)):
+        got, logp = check(x, t=t, m=m, u=0.9, **kw)
+        first = torch.where(x == x.amax(-1, keepdim=True), torch.arange(V, device="cuda"), V).amin(-1)
+        for b in (0, 1, 3, 4, 6):
+            assert int(got[b]) == int(first[b]) and float(logp[b]) == 0.0
+        assert int(got[7]) == -1
+    check(torch.zeros((3, V), device="cuda").to(DTYPES[dtype]), m=[2.0, 1.0, 1.5], u=0.9)
