@@ -404,15 +404,17 @@ extern "C" int ddl_kv8_score(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, int32
   // to 4096 13.8 / 11.8 / 10.1 / 13.0 / 15.1, 1 of 8192 5.4 / 5.8 / 6.7 / 8.5 / 9.7.
   constexpr int warps = 8;
   s.tiles = tiles;
-  const size_t smem = (size_t)(head_dim == 128 ? Ring<128>::BYTES : Ring<64>::BYTES) +
-                      (kind == FEW_TILES ? (size_t)tiles * per : f32 ? (size_t)8 * head_dim / 16 * 32 * 8 : 0);
+  const size_t ring = (size_t)(head_dim == 128 ? Ring<128>::BYTES : Ring<64>::BYTES);
+  const size_t smem = ring + (kind == FEW_TILES ? (size_t)tiles * per : f32 ? (size_t)8 * head_dim / 16 * 32 * 8 : 0);
   const int64_t ctas = sms * (smem > 74 * 1024 ? 2 : 3) * (R > 1 ? 8 : 5) / 5;
   const int64_t each = ctas / units > 1 ? ctas / units : 1, wb = (blocks + warps * each - 1) / (warps * each);
   s.wb = (int32_t)(wb < SC_MAX_BLOCKS ? wb : SC_MAX_BLOCKS);
   const int64_t chunks = (blocks + warps * s.wb - 1) / (warps * s.wb);
   const void* fn = kv->type == DDL_KV8_E4M3 ? score_fn<DDL_KV8_E4M3>(dtype, head_dim, ex, kind)
                                             : score_fn<DDL_KV8_INT8>(dtype, head_dim, ex, kind);
-  if ((st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))) return st;
+  // (the function's limit, which calls of other threads set too: the most that any call of it takes)
+  const size_t most = kind == FEW_TILES ? ring + (size_t)(f32 ? FEW_F32 : FEW_16) * per : smem;
+  if ((st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most)))) return st;
   void* args[] = {&s};
   return cuda_status(launch_pdl(fn, dim3((unsigned)chunks, (unsigned)H_kv, (unsigned)R), dim3((unsigned)warps * 32), args,
                                 smem, (cudaStream_t)stream));

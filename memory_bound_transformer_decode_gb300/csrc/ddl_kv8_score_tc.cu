@@ -417,7 +417,8 @@ int kv8_score_tc_launch(const ScoreArgs& s, int type, int dtype, bool ex, int sm
                    : dtype == DDL_T_BF16 ? tc_fn<DDL_T_BF16>(hd, ex)
                                          : tc_fn<DDL_T_F16>(hd, ex);
   const size_t smem = Layout(f32, hd, a.tiles).total;
-  const int st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  // (the function's limit, which calls of other threads set too: the most that any call of it takes)
+  const int st = cuda_status(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout(f32, hd, most).total));
   if (st) return st;
   void* args[] = {&a, &type};
   return cuda_status(launch_pdl(fn, dim3((unsigned)chunks, (unsigned)a.a.Hkv, (unsigned)a.a.R), dim3(THREADS), args, smem,

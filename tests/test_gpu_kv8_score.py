@@ -1,6 +1,8 @@
 """Attention weight drawn by cached tokens (ddl_kv8_score) against a 64-bit
 reference, where masks, lengths, placements and types can go wrong."""
+import ctypes
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -252,3 +254,49 @@ def test_no_scores_past_32_bits():
     want, tol = sref.score(pool, q, lse, off, lens, table, small, 1.0, 0.1)
     assert float(((score[..., :20].double() - want).abs() - tol).max()) <= 0
     assert float(score[-1, :, 20:].abs().max()) == 0
+
+
+@pytest.mark.parametrize("dtype,rows", [("bf16", (2, 8)), ("f32", (2, 4)), ("bf16", (9, 64)), ("f32", (5, 32))])
+def test_two_host_threads_with_other_numbers_of_rows(dtype, rows):
+    """Calls of one kernel with unlike sizes of shared memory, from threads that do not wait for one another, are all
+    launched and give what each gives alone."""
+    lens, H, G, hd = [200], 1, 8, 128
+    cases, lib = [], ddl.load()
+    for n in rows:
+        pool, table, q, off = case(lens, [n], H, G, hd, 16, "e4m3", dtype, seed=n)
+        lse = lse_of(pool, q, off, lens, table, hd ** -0.5)
+        keep = dict(pool=pool, q=q, lse=lse, off=dev(off), lens=dev(lens), table=dev(table), n=n)
+        keep["kv"] = ddl._kv8(pool, 0, H, hd)
+        keep["opts"] = ddl.AttnOpts(hd ** -0.5, 0.0, 0, None)
+        cases.append(keep)
+    wrong = []
+
+    def call(c, score, stream):
+        return lib.ddl_kv8_score(ctypes.byref(c["kv"]), H * G, H, hd, {"f32": 0, "bf16": 1}[dtype], ctypes.byref(c["opts"]),
+                                 1, c["n"], c["n"], 200, c["off"].data_ptr(), c["lens"].data_ptr(), c["table"].data_ptr(),
+                                 c["table"].shape[1], c["q"].data_ptr(), H * G * hd, c["lse"].data_ptr(), 0.0,
+                                 score.data_ptr(), 200, None, stream.cuda_stream)
+
+    torch.cuda.synchronize()
+    alone = [torch.zeros((1, H, 200), device="cuda") for _ in cases]
+    for c, s in zip(cases, alone):
+        assert call(c, s, torch.cuda.current_stream()) == 0
+    torch.cuda.synchronize()
+    many = [torch.zeros((1, H, 200), device="cuda") for _ in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+
+    def loop(i):
+        for _ in range(3000):
+            st = call(cases[i], many[i], streams[i])
+            if st:
+                wrong.append((i, st, lib.ddl_last_cuda_error()))
+                return
+
+    threads = [threading.Thread(target=loop, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not wrong, wrong
+    assert all(torch.equal(a, b) for a, b in zip(alone, many))
