@@ -295,9 +295,10 @@ __global__ void __launch_bounds__(256, 3) kv8_score_few_kernel(const __grid_cons
 #pragma unroll
         for (int j = 0; j < 4; ++j) c[j] += c2[j];
         // blocks that every query sees, in full tiles, need no masks
-        const bool edge = q0 + 7 >= nq || key0 + 15 > rq.p0 + group_row(A, q0) || key0 < first_seen(A, rq, q1);
-        if (ONE) weights<EX>(A, c, col[0], col[1], ks, key0 + g, edge);
-        else weights<EX>(A, c, tile.cols[q0 + 2 * t], tile.cols[q0 + 2 * t + 1], ks, key0 + g, edge);
+        const Column &cx = ONE ? col[0] : tile.cols[q0 + 2 * t], &cy = ONE ? col[1] : tile.cols[q0 + 2 * t + 1];
+        const bool edge = q0 + 7 >= nq || key0 + 15 > rq.p0 + group_row(A, q0) || key0 < first_seen(A, rq, q1) ||
+                          (cx.hi | cy.hi) < 0;
+        weights<EX>(A, c, cx, cy, ks, key0 + g, edge);
         s0 += c[0] + c[1];
         s1 += c[2] + c[3];
       }

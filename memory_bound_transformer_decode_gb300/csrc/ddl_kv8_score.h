@@ -20,7 +20,7 @@ struct Column {
   float cf;       // factor of the MMA's sum (times the block's scale): log2 units, or softcap's argument
   float lse2;     // log2 e times lse; +inf for a query without keys
   float slope;    // log2 units a token
-  int hi, lo;     // last and first token it sees
+  int hi, lo;     // last and first token it sees; hi < 0: it adds nothing (masks are looked at then, whatever its scores)
 };
 
 // Query qi of request rq for K/V head h.
@@ -30,13 +30,13 @@ __device__ __forceinline__ Column column_of(const AttArgs& A, const Req& rq, int
   const bool has = qi < rq.n * A.GH;
   const int row = has ? group_row(A, qi) : 0;
   const int64_t p = (int64_t)rq.p0 + row, lo = A.window > 0 ? p - A.window + 1 : 0;
-  c.hi = has ? (int)p : -1;
+  const float lse = has ? A.lse[(int64_t)(rq.row0 + row) * A.Hq + h * A.GH + qi - row * A.GH] : -INFINITY;
+  c.hi = has && lse != -INFINITY ? (int)p : -1;
   c.lo = lo > 0 ? (int)lo : 0;
   c.slope = EX && A.slopes && has ? A.slopes[h * A.GH + qi - row * A.GH] * LOG2E : 0.f;
   c.cf = qf * A.scale;
   if (EX && A.softcap > 0.f) c.cf = __fdiv_rn(c.cf, A.softcap);
   else c.cf *= LOG2E;
-  const float lse = has ? A.lse[(int64_t)(rq.row0 + row) * A.Hq + h * A.GH + qi - row * A.GH] : 0.f;
   c.lse2 = lse == -INFINITY ? INFINITY : lse * LOG2E;
   return c;
 }

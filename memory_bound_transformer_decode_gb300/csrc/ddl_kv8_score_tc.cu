@@ -74,6 +74,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_score_tc_kernel(const __grid_c
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[2];
   __shared__ uint32_t tslot;
+  __shared__ int silent;  // some query adds nothing (its log-sum-exp is -inf)
   const AttArgs& A = S.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wg = warp >> 2, tok = tid & 127;
   const Layout M(HL, HD, S.tiles);
@@ -88,6 +89,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_score_tc_kernel(const __grid_c
   const int t0 = max((int)(blockIdx.x * S.wb), S.decay == 1.f ? rq.b0 >> 3 : 0), t1 = min((int)((blockIdx.x + 1) * S.wb), ntile);
   const int s0 = max(t0, rq.b0 >> 3), s1 = min(t1, (rq.b1 + 7) >> 3);
   if (rq.n <= 0 || t0 >= t1) return;  // (the same for the whole CTA)
+  if (tid == 0) silent = 0;
   if (tid < 2) mbar_init(smem_addr(&bars[tid]), 1);
   mbar_init_fence();
   if (warp == 0) tmem_alloc(smem_addr(&tslot), TMEM);
@@ -191,6 +193,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_score_tc_kernel(const __grid_c
             cn[tid].y = tid < n ? c.lse2 : INFINITY;
             if (EX) slope[tid] = c.slope;
             range[tid] = make_int2(c.hi, c.lo);
+            if (tid < n && c.hi < 0) silent = 1;
           }
           load_codes(s0, g0 > 0);
         }
@@ -272,6 +275,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_score_tc_kernel(const __grid_c
       bool has = live;
       fence_proxy_async_smem();
       __syncthreads();
+      const bool masks = silent != 0;
       if (ok) issue(s0, 0, 0);
       if (s0 + 1 < s1) load_codes(s0 + 1, g0 > 0);
       uint32_t a = 0;
@@ -320,7 +324,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_score_tc_kernel(const __grid_c
           const uint32_t d = acc + a * QC + ((uint32_t)(warp & 3) << 21);
           const int q0 = g0 + c * QC, nc = min(QC, npad - c * QC), q1 = min(q0 + nc, nq) - 1;
           // tokens that every query of the chunk sees need no masks
-          const bool edge = key0 + TOK - 1 > rq.p0 + group_row(A, q0) || key0 < first_seen(A, rq, q1);
+          const bool edge = masks || key0 + TOK - 1 > rq.p0 + group_row(A, q0) || key0 < first_seen(A, rq, q1);
           const float2* const cc = cn + c * QC;
 #pragma unroll 1
           for (int x = 16 * wg; x < nc; x += 16 * WGS) {

@@ -300,3 +300,36 @@ def test_two_host_threads_with_other_numbers_of_rows(dtype, rows):
     torch.cuda.synchronize()
     assert not wrong, wrong
     assert all(torch.equal(a, b) for a, b in zip(alone, many))
+
+
+@pytest.mark.parametrize("dtype,rows", [("bf16", 1), ("f32", 3), ("f16", 8), ("bf16", 20), ("f32", 40)])
+@pytest.mark.parametrize("opts", [dict(), dict(softcap=15.0)])
+def test_rows_of_minus_infinite_lse_add_nothing_whatever_they_see(dtype, rows, opts):
+    """Not even NaN: of codes and scales among their keys, or of their own q.  (One tile of queries, a few, many.)"""
+    lens, H, G, hd, scale = [200, 200], 2, 4, 128, 128 ** -0.5
+    pool, table, q, off = case(lens, [rows, rows], H, G, hd, 16, "e4m3", dtype, seed=rows)
+    lse = lse_of(pool, q, off, lens, table, scale, **opts)
+    last = 2 * rows - 1
+    lse[:rows] = -math.inf                 # request 0: no row adds anything
+    q[0] = math.nan
+    lse[last, :G] = -math.inf              # request 1: the newest row's heads of K/V head 0
+    clean = [t.clone() for t in pool]
+    old = torch.rand((2, H, 200), device="cuda")
+    want, tol = sref.score(clean, q.nan_to_num(nan=0.0), lse, off, lens, table, old, 0.5, scale, **opts)
+    raw = pool[0].view(torch.uint8)
+    raw[table[0, 3]] = 127
+    pool[2][table[0, 5]] = math.inf
+    pool[2][table[0, 6]] = math.nan
+    if rows == 1:                          # (else other rows see it)
+        raw[table[1, 4], 0, 7] = 255
+    got = old.clone()
+    bad = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ddl.ddl_kv8_score(pool, q, lse, dev(lens), dev(table), 200, got, q_off=dev(off), max_rows=rows, decay=0.5, scale=scale,
+                      bad=bad, **opts)
+    assert int(bad) == 0 and float(((got.double() - want).abs() - tol).max()) <= 0
+    assert torch.equal(got[0, :, :200 - rows], 0.5 * old[0, :, :200 - rows])
+    if rows > 1:                           # a token that a row with weights sees
+        raw[table[1, 4], 0, 7] = 255
+        ddl.ddl_kv8_score(pool, q, lse, dev(lens), dev(table), 200, got, q_off=dev(off), max_rows=rows, decay=0.0, scale=scale,
+                          **opts)
+        assert got[1, 0, 71].isnan() and int(got.isnan().sum()) == 1
