@@ -463,7 +463,7 @@ int ddl_kv8_score(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, int32_t head_dim
  *    [new_pages_per_seq] names for the request (device int32, of the same pool).
  *    Each block of 16 kept tokens gets a scale of its own, as ddl_kv8_append
  *    chooses it (the smallest power of two, >= 2^-126, at which the largest value
- *    fits; 0 if all are zero); a code is value / scale rounded to nearest, ties to
+ *    fits, 2^127 if that takes more; 0 if all are zero); a code is value / scale rounded to nearest, ties to
  *    even, and the code itself where the token's scale is the new one.  NaN codes
  *    stay NaN.  A source scale that is negative or not finite makes the block's
  *    scale NaN.  The last block's rows behind token keep - 1 are zero.

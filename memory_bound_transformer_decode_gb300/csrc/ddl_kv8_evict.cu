@@ -286,26 +286,34 @@ struct Block {
   // scale: of lane's row (0 for none); returns the block's new one and leaves its codes in x
   __device__ __forceinline__ float rescale(float scale) {
     const int lane = threadIdx.x & 31;
-    // the largest value: per row the largest |code| (exact in fp16; NaN does not count) times its scale
-    float top = 0.f;
+    // the largest value: per row the largest |code| (exact in fp16; NaN does not count) times its scale; where a product
+    // passes fp32, once more with the scales 2^-16 of themselves (the smaller ones do not matter then)
+    float amax, down = 1.f;
+#pragma unroll 1
+    for (;; down = 0x1p-16f) {
+      float top = 0.f;
 #pragma unroll
-    for (int j = 0; j < G::NI; ++j) {
-      const float f = __shfl_sync(FULL, scale, j * G::RPL + lane / G::LPR);
-      const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-      __half2 m = __float2half2_rn(0.f);
+      for (int j = 0; j < G::NI; ++j) {
+        const float f = __shfl_sync(FULL, scale * down, j * G::RPL + lane / G::LPR);
+        const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+        __half2 m = __float2half2_rn(0.f);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t a, b;
-        codes_f16<CT>(w[q], a, b);
-        m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&a)));
-        m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&b)));
+        for (int q = 0; q < 4; ++q) {
+          uint32_t a, b;
+          codes_f16<CT>(w[q], a, b);
+          m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&a)));
+          m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&b)));
+        }
+        top = fmaxf(top, fmaxf(__low2float(m), __high2float(m)) * f);
       }
-      top = fmaxf(top, fmaxf(__low2float(m), __high2float(m)) * f);
+      amax = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(top)));
+      if (amax < INFINITY || down < 1.f) break;
     }
-    const float amax = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(top)));
     const uint32_t bits = __float_as_uint(scale);
     const bool broken = __any_sync(FULL, !(scale >= 0.f && scale < INFINITY));
-    const float now = broken ? __uint_as_float(0x7fffffffu) : pow2_scale<CT>(amax);
+    // (the largest power of two is 2^127, of which the largest value may be more than the largest code)
+    const float now = broken ? __uint_as_float(0x7fffffffu)
+                             : down < 1.f ? fminf(pow2_scale<CT>(amax) * 0x1p16f, 0x1p127f) : pow2_scale<CT>(amax);
     // all scales powers of two, none more than 2^15 above the new one (nor subnormal): factors in fp16
     const bool pow2 = (bits & 0x7fffffu) == 0 && (bits == 0 || bits >= 0x00800000u) &&
                       (int)(bits >> 23) - (int)(__float_as_uint(now) >> 23) <= 15;
@@ -336,11 +344,12 @@ struct Block {
       }
       return now;
     }
-    const Divider by(now);
+    const Divider by(now * down);
 #pragma unroll
     for (int j = 0; j < G::NI; ++j) {
-      const float f = __shfl_sync(FULL, scale, j * G::RPL + lane / G::LPR);
+      float f = __shfl_sync(FULL, scale, j * G::RPL + lane / G::LPR);
       if (f == now) continue;
+      f *= down;
       uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {

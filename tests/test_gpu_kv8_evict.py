@@ -216,3 +216,44 @@ def test_replayed_with_other_lengths():
     assert np.array_equal(kept.cpu().numpy(), want[2]) and np.array_equal(out.cpu().numpy(), want[3])
     for i in range(2):
         assert np.array_equal(host(pool[i]), want[0][i]) and np.array_equal(host(pool[i + 2]), want[1][i])
+
+
+@pytest.mark.parametrize("codes", ["e4m3", "int8"])
+@pytest.mark.parametrize("odd", [False, True])
+def test_scales_up_to_the_largest_power_of_two(codes, odd):
+    """Values past fp32: as those of scales 2^64 times smaller, whose products fit."""
+    H, hd, page, lens, keep = 2, 64, 16, [200, 150], [90, 60]
+    a, b, pages = tables(lens, keep, page, 11)
+    pool = make_pool(pages, H, page, hd, codes, 11)
+    for i in (2, 3):
+        g = torch.Generator(device="cuda").manual_seed(i)
+        e = torch.randint(80, 128, pool[i].shape, device="cuda", generator=g).float()
+        pool[i].copy_(torch.exp2(e))
+        if odd:
+            pool[i].copy_(torch.exp2(e - 1) * (1 + torch.rand(e.shape, device="cuda", generator=g) * 0.9))
+        pool[i][::7] = 0.0
+    score = torch.rand((2, H, 200), device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
+    kept = torch.full((2, H, 90), -1, dtype=torch.int32, device="cuda")
+    out = torch.zeros_like(score)
+    want = sref.evict([host(pool[0]), host(pool[1])], [host(pool[i]).astype(np.float64) * 2.0 ** -64 for i in (2, 3)],
+                      score.cpu().numpy(), lens, keep, a, b, 1, 2, page, codes == "int8", kept.cpu().numpy(), out.cpu().numpy())
+    ddl.ddl_kv8_evict(pool, score, dev(lens), dev(keep), dev(a), dev(b), 200, kept=kept, score_out=out, sinks=1, recent=2)
+    for i in range(2):
+        sc = host(pool[i + 2]).astype(np.float64)
+        assert np.isfinite(sc).all() and np.array_equal(sc, want[1][i] * 2.0 ** 64)
+        assert np.array_equal(ref.decode(host(pool[i]), codes == "int8"), ref.decode(want[0][i], codes == "int8"))
+
+
+def test_a_value_past_the_largest_code_of_the_largest_scale():
+    pool = make_pool(4, 1, 16, 64, "e4m3", 2)
+    for i in (2, 3):
+        pool[i].fill_(1.5 * 2.0 ** 127)
+    score = torch.arange(16, device="cuda").float().view(1, 1, 16)
+    x = [ref.decode(host(pool[i]), False)[1, 0, 8:] * 1.5 for i in range(2)]
+    kept = torch.zeros((1, 1, 8), dtype=torch.int32, device="cuda")
+    assert max(np.abs(x[0]).max(), np.abs(x[1]).max()) > 448
+    ddl.ddl_kv8_evict(pool, score, dev([16]), dev([8]), dev([[1]]), dev([[3]]), 16, kept=kept, score_out=torch.zeros_like(score))
+    for i in range(2):
+        assert float(pool[i + 2][3]) == 2.0 ** 127
+        want = ref.decode(ref.encode_e4m3(np.clip(x[i], -448, 448)), False)
+        assert np.array_equal(ref.decode(host(pool[i]), False)[3, 0, :8], want)
