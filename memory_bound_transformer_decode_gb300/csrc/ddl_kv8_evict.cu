@@ -309,7 +309,7 @@ struct Block {
       amax = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(top)));
       if (amax < INFINITY || down < 1.f) break;
     }
-    const uint32_t bits = __float_as_uint(scale);
+    const uint32_t bits = __float_as_uint(scale + 0.f);  // (a scale of -0 is zero)
     const bool broken = __any_sync(FULL, !(scale >= 0.f && scale < INFINITY));
     // (the largest power of two is 2^127, of which the largest value may be more than the largest code)
     const float now = broken ? __uint_as_float(0x7fffffffu)

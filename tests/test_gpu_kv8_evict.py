@@ -257,3 +257,23 @@ def test_a_value_past_the_largest_code_of_the_largest_scale():
         assert float(pool[i + 2][3]) == 2.0 ** 127
         want = ref.decode(ref.encode_e4m3(np.clip(x[i], -448, 448)), False)
         assert np.array_equal(ref.decode(host(pool[i]), False)[3, 0, :8], want)
+
+
+@pytest.mark.parametrize("codes", ["e4m3", "int8"])
+@pytest.mark.parametrize("e", [0, 112, 118, 124, 127])
+def test_a_scale_of_minus_zero_is_zero(codes, e):
+    """Its rows move as zeros beside rows of any scale."""
+    pool = make_pool(4, 1, 16, 64, codes, 2)
+    for i in (2, 3):
+        pool[i].fill_(2.0 ** e)
+        pool[i][2] = -0.0
+    score = torch.zeros((1, 1, 32), device="cuda")
+    score[0, 0, 10:24] = 1.0
+    kept = torch.zeros((1, 1, 14), dtype=torch.int32, device="cuda")
+    src = [ref.decode(host(pool[i]), codes == "int8")[1, 0, 10:16] for i in range(2)]
+    ddl.ddl_kv8_evict(pool, score, dev([32]), dev([14]), dev([[1, 2]]), dev([[3]]), 32, kept=kept,
+                      score_out=torch.zeros_like(score))
+    assert kept[0, 0].tolist() == list(range(10, 24))
+    for i in range(2):
+        x = ref.decode(host(pool[i]), codes == "int8")[3, 0]
+        assert np.array_equal(x[:6] * float(pool[i + 2][3]), src[i] * 2.0 ** e) and not x[6:].any()
