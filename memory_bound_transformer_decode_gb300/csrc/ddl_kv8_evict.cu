@@ -89,9 +89,10 @@ __global__ void __launch_bounds__(SEL_THREADS) kv8_select_kernel(const __grid_co
   if (c.bad && A.bad && blockIdx.x == 0 && tid == 0) atomicOr(A.bad, 1);
   const float* const score = A.score + ((int64_t)r * A.H + h) * A.stride;
   float* const out = A.score_out + ((int64_t)r * A.H + h) * A.stride;
-  const int n0 = (int)((int64_t)c.len * rank / C), n1 = (int)((int64_t)c.len * (rank + 1) / C);  // the CTA's tokens
+  // the CTA's tokens (loops count in 32 bits without sign: their last step may end past 2^31)
+  const int n0 = (int)((int64_t)c.len * rank / C), n1 = (int)((int64_t)c.len * (rank + 1) / C);
   if (c.keep < 0) {  // (the same for the whole cluster)
-    for (int i = n0 + tid; i < n1; i += SEL_THREADS) out[i] = score[i];
+    for (uint32_t i = n0 + tid; i < (uint32_t)n1; i += SEL_THREADS) out[i] = score[i];
     return;
   }
   const int lo = c.sinks, hi = c.len - c.recent;  // the tokens that may go: [lo, hi)
@@ -101,15 +102,15 @@ __global__ void __launch_bounds__(SEL_THREADS) kv8_select_kernel(const __grid_co
   // the range of the keys
   uint32_t top = 0u, low = ~0u;
   constexpr int U = 8;  // loads on their way
-  for (int i = n0 + tid; i < n1; i += U * SEL_THREADS) {
+  for (uint32_t i = n0 + tid; i < (uint32_t)n1; i += U * SEL_THREADS) {
     float s[U];
 #pragma unroll
-    for (int j = 0; j < U; ++j) s[j] = i + j * SEL_THREADS < n1 ? score[i + j * SEL_THREADS] : 0.f;
+    for (int j = 0; j < U; ++j) s[j] = i + j * SEL_THREADS < (uint32_t)n1 ? score[i + j * SEL_THREADS] : 0.f;
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      const int x = i + j * SEL_THREADS;
-      if (SM && x < n1) sel_scores[x - n0] = s[j];
-      if (x >= m0 && x < m1) {
+      const uint32_t x = i + j * SEL_THREADS;
+      if (SM && x < (uint32_t)n1) sel_scores[x - n0] = s[j];
+      if (x >= (uint32_t)m0 && x < (uint32_t)m1) {
         const uint32_t k = score_key(s[j]);
         top = max(top, k);
         low = min(low, k);
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(SEL_THREADS) kv8_select_kernel(const __grid_co
   for (int pass = 0; need > 0 && !all && bits > 0; ++pass) {
     const int shift = bits > SEL_BITS ? bits - SEL_BITS : 0;
     uint32_t* const bins = hist[pass];
-    for (int i = m0 + tid; i < m1; i += SEL_THREADS) {
+    for (uint32_t i = m0 + tid; i < (uint32_t)m1; i += SEL_THREADS) {
       const uint32_t x = top - key(i);
       if (pass == 0 || (x ^ at) >> bits == 0) atomicAdd(&bins[(x >> shift) & (SEL_BINS - 1)], 1u);
     }
@@ -213,8 +214,9 @@ __global__ void __launch_bounds__(SEL_THREADS) kv8_select_kernel(const __grid_co
   if (SM) __syncthreads();  // (the keys, where no digit was needed)
   // 32 tokens a step: which stay and which are ties; lane l keeps step l's for the second time (of 32 steps)
   uint32_t my_stay = 0, my_tie = 0;
-  for (int i0 = w0, k = 0; i0 < w1; i0 += 32, ++k) {
-    const int s = i0 + lane < w1 ? state(i0 + lane) : 0;
+  int k = 0;
+  for (uint32_t i0 = w0; i0 < (uint32_t)w1; i0 += 32, ++k) {
+    const int s = i0 + lane < (uint32_t)w1 ? state(i0 + lane) : 0;
     const uint32_t ms = __ballot_sync(FULL, s == 2), me = __ballot_sync(FULL, s == 1);
     if (k == lane) {
       my_stay = ms;
@@ -243,18 +245,19 @@ __global__ void __launch_bounds__(SEL_THREADS) kv8_select_kernel(const __grid_co
   }
   int32_t* const kept = A.kept + ((int64_t)r * A.H + h) * A.max_keep;
   const uint32_t below = (1u << lane) - 1;
-  for (int i0 = w0, k = 0; i0 < w1; i0 += 32, ++k) {
-    const int i = i0 + lane;
+  k = 0;
+  for (uint32_t i0 = w0; i0 < (uint32_t)w1; i0 += 32, ++k) {
+    const uint32_t i = i0 + lane;
     uint32_t ms = __shfl_sync(FULL, my_stay, k & 31), me = __shfl_sync(FULL, my_tie, k & 31);
     if (k >= 32) {
-      const int s = i < w1 ? state(i) : 0;
+      const int s = i < (uint32_t)w1 ? state(i) : 0;
       ms = __ballot_sync(FULL, s == 2);
       me = __ballot_sync(FULL, s == 1);
     }
     const uint32_t tie = ties + __popc(me & below);
     if ((ms >> lane & 1) || ((me >> lane & 1) && tie < need)) {
       const uint32_t x = to + __popc(ms & below) + (tie < need ? tie : need);
-      kept[x] = i;
+      kept[x] = (int32_t)i;
       out[x] = score_of(i);
     }
     to += __popc(ms);

@@ -277,3 +277,43 @@ def test_a_scale_of_minus_zero_is_zero(codes, e):
     for i in range(2):
         x = ref.decode(host(pool[i]), codes == "int8")[3, 0]
         assert np.array_equal(x[:6] * float(pool[i + 2][3]), src[i] * 2.0 ** e) and not x[6:].any()
+
+
+def test_a_request_as_long_as_32_bits_allow():
+    """Every page of it the same one; its last tokens lie nearer to 2^31 than a step of any loop."""
+    page, hd, keep, sinks, recent = 1024, 64, 300, 3, 5
+    per = 2 ** 21 - 1
+    L = per * page
+    pool = make_pool(3, 1, page, hd, "int8", 5)
+    pool[2][0], pool[3][0] = 2.0 ** -7, 2.0 ** -8
+    table = torch.zeros((1, per), dtype=torch.int32, device="cuda")
+    score = torch.zeros((1, 1, L), device="cuda")
+    at = np.unique(np.concatenate([np.random.RandomState(1).randint(0, L, 250), [sinks, 77, L - 900, L - recent - 1, L - 1]]))
+    score[0, 0, torch.from_numpy(at).cuda()] = torch.rand(len(at), device="cuda") + 0.5
+    out = torch.full_like(score, -1.0)
+    kept = torch.full((1, 1, keep), -1, dtype=torch.int32, device="cuda")
+    bad = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def call(k):
+        ddl.ddl_kv8_evict(pool, score, dev([L]), dev([k]), table, dev([[2]]), L, kept=kept, score_out=out, sinks=sinks,
+                          recent=recent, bad=bad)
+        torch.cuda.synchronize()
+
+    call(keep)
+    edge = set(range(sinks)) | set(range(L - recent, L))
+    mid = [i for i in at.tolist() if i not in edge]
+    rest, zeros = keep - len(edge) - len(mid), []
+    i = sinks
+    while len(zeros) < rest:  # ties of zero: the lowest indices
+        if i not in mid:
+            zeros.append(i)
+        i += 1
+    want = np.array(sorted(edge | set(mid) | set(zeros)))
+    assert int(bad) == 0 and np.array_equal(kept[0, 0].cpu().numpy(), want)
+    assert torch.equal(out[0, 0, :keep], score[0, 0, torch.from_numpy(want).cuda()]) and float(out[0, 0, keep:].max()) == -1.0
+    for i in range(2):
+        src = ref.decode(host(pool[i]), True)[0, 0, want % page] * float(pool[i + 2][0, 0, 0])
+        got = ref.decode(host(pool[i]), True)[2, 0, :keep]
+        assert np.array_equal(got * host(pool[i + 2])[2, 0].repeat(16)[:keep, None], src)
+    call(-1)
+    assert torch.equal(out, score)
