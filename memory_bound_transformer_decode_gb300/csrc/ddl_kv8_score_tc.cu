@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_score_tc_kernel(const __grid_c
   const int nq = rq.n * A.GH;
   float* const out = S.score + ((int64_t)r * A.Hkv + h) * S.stride;
   // tiles [t0, t1) change, [s0, s1) of them hold tokens that some row sees
-  const int ntile = (rq.len + TOK - 1) / TOK;
+  const int ntile = (int)(((int64_t)rq.len + TOK - 1) / TOK);  // (lengths up to 2^31 - 16: a tile's last token fits 32 bits)
   const int t0 = max((int)(blockIdx.x * S.wb), S.decay == 1.f ? rq.b0 >> 3 : 0), t1 = min((int)((blockIdx.x + 1) * S.wb), ntile);
   const int s0 = max(t0, rq.b0 >> 3), s1 = min(t1, (rq.b1 + 7) >> 3);
   if (rq.n <= 0 || t0 >= t1) return;  // (the same for the whole CTA)
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_score_tc_kernel(const __grid_c
     float ks = 0.f, was = 0.f;
     bool live = false;
     auto load_page = [&](int t, int x) -> int32_t {  // of token x of tile t
-      const int b = (t * TOK + x) >> 4;
+      const int b = (int)(((uint32_t)t * TOK + x) >> 4);  // (t may be one past the last)
       return t < s1 && b >= rq.b0 && b < rq.b1 ? A.table[(int64_t)r * A.per + (b >> (A.pshift - 4))] : -2;
     };
     auto row_of = [&](int32_t page, int t, int x) -> int64_t {

@@ -333,3 +333,28 @@ def test_rows_of_minus_infinite_lse_add_nothing_whatever_they_see(dtype, rows, o
         ddl.ddl_kv8_score(pool, q, lse, dev(lens), dev(table), 200, got, q_off=dev(off), max_rows=rows, decay=0.0, scale=scale,
                           **opts)
         assert got[1, 0, 71].isnan() and int(got.isnan().sum()) == 1
+
+
+@pytest.mark.parametrize("rows", [1, 9])
+def test_a_request_as_long_as_32_bits_allow(rows):
+    """Every page of it the same one, by one tile of queries and by many (tiles of 128 tokens: the last one ends at 2^31)."""
+    page, hd, H, G = 16, 64, 1, 8
+    per = 2 ** 27 - 1
+    L = per * page
+    pool = make_pool(2, H, page, hd, "int8", 3)
+    pool[2].fill_(2.0 ** -8)
+    table = torch.ones((1, per), dtype=torch.int32, device="cuda")
+    q = torch.randn((rows, G, hd), generator=torch.Generator(device="cuda").manual_seed(rows), device="cuda").bfloat16()
+    lse = torch.zeros((rows, G), device="cuda")
+    score = torch.full((1, H, L), -1.0, device="cuda")
+    bad = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ddl.ddl_kv8_score(pool, q, lse, dev([L]), table, L, score, q_off=dev([0, rows]), max_rows=rows, decay=0.0, scale=0.1, bad=bad)
+    torch.cuda.synchronize()
+    # the same keys in a request of four pages: its last page is that of this one, the others all alike
+    small = torch.zeros((1, H, 64), device="cuda")
+    want, tol = sref.score(pool, q, lse, [0, rows], [64], np.ones((1, 4), int), small, 0.0, 0.1)
+    assert int(bad) == 0
+    got = score.view(-1, page)
+    assert bool((got[:-1] == got[0]).all())
+    assert float(((got[0].double() - want[0, 0, :page]).abs() - tol[0, 0, :page]).max()) <= 0
+    assert float(((got[-1].double() - want[0, 0, -page:]).abs() - tol[0, 0, -page:]).max()) <= 0
