@@ -201,3 +201,92 @@ def test_refusals():
         with pytest.raises((ValueError, ddl.DDLError)):
             ddl.ddl_stack_step_kv8_scored(sv.shape, sv.wtype, sv.layers, sv.pools, scores, decay, **{**base, **kw})
     torch.cuda.synchronize()
+
+
+def test_a_captured_loop_that_cuts():
+    """Plan, scored step, cut of the requests that outgrow their budget and draw in one graph without a number from
+    the device: replayed, requests are cut time and again, and later rows attend to the new pages at their true
+    positions, with the bits of the same calls made one by one."""
+    R, T, page, per, budget, keep = 3, 4, 16, 4, 37, 21
+
+    class Loop(Bounded):
+        def __init__(self):
+            super().__init__(config(64), ddl.INT4, R, T, page, per, "e4m3", max_rows=2)
+            i32 = lambda *n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+            pages = 64  # more than the loop takes
+            self.all_free, self.given = dev(np.random.RandomState(2).permutation(pages)), i32(1)
+            self.window = self.all_free.clone()
+            self.pools = [tuple(torch.zeros((pages, *t.shape[1:]), dtype=torch.uint8 if t.element_size() == 1 else t.dtype,
+                                            device="cuda").view(t.dtype) for t in p) for p in self.pools]
+            self.new, self.zero = i32(R, per), i32(R)
+            self.cut_plan = dict(row_off=i32(R + 1), kv_len=i32(R), row_pos=i32(R * keep), slot=i32(R * keep))
+            self.kept, self.cut_len = i32(R, self.cfg.H_kv, keep), i32(R)
+            self.next_scores = [torch.zeros_like(s) for s in self.scores]
+            for s in self.scores:
+                s.zero_()
+            self.at, self.tok = torch.arange(T, device="cuda", dtype=torch.int32), i32(T)
+
+        def take(self):  # the free pages from the next one on
+            self.given += self.used
+            at = torch.arange(len(self.all_free), device="cuda") + self.given
+            self.window.copy_(self.all_free[at.clamp(max=len(self.all_free) - 1)])
+
+        def one(self, add, x, u):
+            ddl.ddl_page_plan(self.old, add, self.window, self.table, page, used=self.used, status=self.status, **self.p)
+            self.take()
+            of = torch.searchsorted(self.p["row_off"][1:], self.at, right=True).clamp(max=R - 1)  # each row's request
+            pos = self.p["row_pos"]
+            pos.copy_(torch.where(pos >= 0, pos + self.gone[of], pos))
+            ddl.ddl_stack_step_kv8_scored(self.shape, self.wtype, self.layers, self.pools, self.scores, 0.9,
+                                          page_table=self.table, max_rows=2, max_len=per * page, x_bf16=x,
+                                          resid_out=self.res, bad=self.bad, workspace=self.ws, **self.p)
+            ddl.ddl_sample(self.res, u, tokens=self.tok)
+            lens = self.p["kv_len"]
+            over = lens > budget
+            self.cut_len.copy_(torch.where(over, keep, -1))
+            self.new.fill_(-1)
+            ddl.ddl_page_plan(self.zero, torch.where(over, keep, 0).int(), self.window, self.new, page, used=self.used,
+                              status=self.status, **self.cut_plan)
+            self.take()
+            for l, pool in enumerate(self.pools):
+                self.next_scores[l].copy_(self.scores[l])
+                ddl.ddl_kv8_evict(pool, self.scores[l], lens, self.cut_len, self.table, self.new, per * page, kept=self.kept,
+                                  score_out=self.next_scores[l], sinks=2, recent=5, bad=self.bad)
+                self.scores[l].copy_(self.next_scores[l])
+            self.gone += torch.where(over, lens - keep, 0)
+            self.table.copy_(torch.where(over[:, None], self.new, self.table))
+            self.old.copy_(torch.where(over, keep, lens))
+
+        def state(self):
+            return [self.old, self.gone, self.table, self.given, self.window, *self.scores, *(t for p in self.pools for t in p)]
+
+    sv, ev = Loop(), Loop()
+    add, x, u = dev([1, 1, 1]), torch.zeros((T, sv.cfg.D), dtype=torch.bfloat16, device="cuda"), torch.zeros(T, device="cuda")
+    start = [t.clone() for t in sv.state()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        sv.one(add, x, u)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sv.one(add, x, u)
+    for a, b in zip(sv.state(), start):
+        a.copy_(b)
+    total, g = np.zeros(R, int), np.random.RandomState(7)
+    for i in range(60):
+        n = np.array([1, 1, 2]) if i < 30 else g.permutation([0, 1, 2]) if i % 4 else np.array([1, 1, 1])
+        add.copy_(dev(n))
+        x.copy_(torch.randn((T, sv.cfg.D), generator=torch.Generator("cuda").manual_seed(i), device="cuda"))
+        u.copy_(torch.rand(T, generator=torch.Generator("cuda").manual_seed(i), device="cuda"))
+        graph.replay()
+        ev.one(add, x, u)
+        torch.cuda.synchronize()
+        rows = int(n.sum())
+        assert torch.equal(sv.res[:rows], ev.res[:rows]) and torch.equal(sv.tok[:rows], ev.tok[:rows]), i
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(sv.state(), ev.state())), i
+        true = [p for r in range(R) for p in range(total[r], total[r] + n[r])]
+        total += n
+        assert sv.p["row_pos"][:rows].tolist() == true and (sv.p["row_pos"][rows:] == -1).all()
+        assert np.array_equal(sv.old.cpu().numpy() + sv.gone.cpu().numpy(), total)
+    assert int(sv.bad) == 0 and int(sv.gone.min()) > 0 and int(sv.given) <= 64 and (sv.gone > 32).any()
