@@ -16,6 +16,8 @@
 // to 2048, 8 heads: 65 us, choice 19 and move 43 at 51 % of the DRAM rate; its bytes would take 33).
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "ddl_kv8.h"
 
 namespace ddl {
@@ -74,12 +76,14 @@ __device__ __forceinline__ uint32_t ldu_cluster(const uint32_t* p, int rank) {
   return v;
 }
 
+// SM: the scores fit shared memory.  (If not, loops count without sign: their last step may end past 2^31.)
 template <bool SM>
 __global__ void __launch_bounds__(SEL_THREADS) kv8_select_kernel(const __grid_constant__ EvictArgs A, const int C) {
   extern __shared__ float sel_scores[];  // SM: the scores of the CTA's tokens
   __shared__ uint32_t hist[SEL_PASSES][SEL_BINS], sums[SEL_PASSES][SEL_BINS / 2];  // sums: of the cluster, SEL_BINS / C of them
   __shared__ uint32_t wsum[2][SEL_WARPS];
   __shared__ uint32_t cta_top, cta_low, cta_sure, cta_ties, sh_digit, sh_need, sh_inside;
+  using Id = std::conditional_t<SM, int, uint32_t>;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = blockIdx.x % C, h = blockIdx.x / C, r = blockIdx.y;
   for (int i = tid; i < SEL_PASSES * SEL_BINS; i += SEL_THREADS) hist[0][i] = 0;
@@ -89,10 +93,10 @@ __global__ void __launch_bounds__(SEL_THREADS) kv8_select_kernel(const __grid_co
   if (c.bad && A.bad && blockIdx.x == 0 && tid == 0) atomicOr(A.bad, 1);
   const float* const score = A.score + ((int64_t)r * A.H + h) * A.stride;
   float* const out = A.score_out + ((int64_t)r * A.H + h) * A.stride;
-  // the CTA's tokens (loops count in 32 bits without sign: their last step may end past 2^31)
+  // the CTA's tokens
   const int n0 = (int)((int64_t)c.len * rank / C), n1 = (int)((int64_t)c.len * (rank + 1) / C);
   if (c.keep < 0) {  // (the same for the whole cluster)
-    for (uint32_t i = n0 + tid; i < (uint32_t)n1; i += SEL_THREADS) out[i] = score[i];
+    for (Id i = n0 + tid; i < (Id)n1; i += SEL_THREADS) out[i] = score[i];
     return;
   }
   const int lo = c.sinks, hi = c.len - c.recent;  // the tokens that may go: [lo, hi)
@@ -102,15 +106,15 @@ __global__ void __launch_bounds__(SEL_THREADS) kv8_select_kernel(const __grid_co
   // the range of the keys
   uint32_t top = 0u, low = ~0u;
   constexpr int U = 8;  // loads on their way
-  for (uint32_t i = n0 + tid; i < (uint32_t)n1; i += U * SEL_THREADS) {
+  for (Id i = n0 + tid; i < (Id)n1; i += U * SEL_THREADS) {
     float s[U];
 #pragma unroll
-    for (int j = 0; j < U; ++j) s[j] = i + j * SEL_THREADS < (uint32_t)n1 ? score[i + j * SEL_THREADS] : 0.f;
+    for (int j = 0; j < U; ++j) s[j] = i + j * SEL_THREADS < (Id)n1 ? score[i + j * SEL_THREADS] : 0.f;
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      const uint32_t x = i + j * SEL_THREADS;
-      if (SM && x < (uint32_t)n1) sel_scores[x - n0] = s[j];
-      if (x >= (uint32_t)m0 && x < (uint32_t)m1) {
+      const Id x = i + j * SEL_THREADS;
+      if (SM && x < (Id)n1) sel_scores[x - n0] = s[j];
+      if (x >= (Id)m0 && x < (Id)m1) {
         const uint32_t k = score_key(s[j]);
         top = max(top, k);
         low = min(low, k);
@@ -143,7 +147,7 @@ __global__ void __launch_bounds__(SEL_THREADS) kv8_select_kernel(const __grid_co
   for (int pass = 0; need > 0 && !all && bits > 0; ++pass) {
     const int shift = bits > SEL_BITS ? bits - SEL_BITS : 0;
     uint32_t* const bins = hist[pass];
-    for (uint32_t i = m0 + tid; i < (uint32_t)m1; i += SEL_THREADS) {
+    for (Id i = m0 + tid; i < (Id)m1; i += SEL_THREADS) {
       const uint32_t x = top - key(i);
       if (pass == 0 || (x ^ at) >> bits == 0) atomicAdd(&bins[(x >> shift) & (SEL_BINS - 1)], 1u);
     }
@@ -215,8 +219,8 @@ __global__ void __launch_bounds__(SEL_THREADS) kv8_select_kernel(const __grid_co
   // 32 tokens a step: which stay and which are ties; lane l keeps step l's for the second time (of 32 steps)
   uint32_t my_stay = 0, my_tie = 0;
   int k = 0;
-  for (uint32_t i0 = w0; i0 < (uint32_t)w1; i0 += 32, ++k) {
-    const int s = i0 + lane < (uint32_t)w1 ? state(i0 + lane) : 0;
+  for (Id i0 = w0; i0 < (Id)w1; i0 += 32, ++k) {
+    const int s = i0 + lane < (Id)w1 ? state(i0 + lane) : 0;
     const uint32_t ms = __ballot_sync(FULL, s == 2), me = __ballot_sync(FULL, s == 1);
     if (k == lane) {
       my_stay = ms;
@@ -246,11 +250,11 @@ __global__ void __launch_bounds__(SEL_THREADS) kv8_select_kernel(const __grid_co
   int32_t* const kept = A.kept + ((int64_t)r * A.H + h) * A.max_keep;
   const uint32_t below = (1u << lane) - 1;
   k = 0;
-  for (uint32_t i0 = w0; i0 < (uint32_t)w1; i0 += 32, ++k) {
-    const uint32_t i = i0 + lane;
+  for (Id i0 = w0; i0 < (Id)w1; i0 += 32, ++k) {
+    const Id i = i0 + lane;
     uint32_t ms = __shfl_sync(FULL, my_stay, k & 31), me = __shfl_sync(FULL, my_tie, k & 31);
     if (k >= 32) {
-      const int s = i < (uint32_t)w1 ? state(i) : 0;
+      const int s = i < (Id)w1 ? state(i) : 0;
       ms = __ballot_sync(FULL, s == 2);
       me = __ballot_sync(FULL, s == 1);
     }
@@ -289,34 +293,32 @@ struct Block {
   // scale: of lane's row (0 for none); returns the block's new one and leaves its codes in x
   __device__ __forceinline__ float rescale(float scale) {
     const int lane = threadIdx.x & 31;
-    // the largest value: per row the largest |code| (exact in fp16; NaN does not count) times its scale; where a product
-    // passes fp32, once more with the scales 2^-16 of themselves (the smaller ones do not matter then)
-    float amax, down = 1.f;
-#pragma unroll 1
-    for (;; down = 0x1p-16f) {
-      float top = 0.f;
+    // the largest value: per row the largest |code| (exact in fp16; NaN does not count) times its scale; and 2^-16 of it, for
+    // products past fp32
+    float top = 0.f, far = 0.f;
 #pragma unroll
-      for (int j = 0; j < G::NI; ++j) {
-        const float f = __shfl_sync(FULL, scale * down, j * G::RPL + lane / G::LPR);
-        const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-        __half2 m = __float2half2_rn(0.f);
+    for (int j = 0; j < G::NI; ++j) {
+      const float f = __shfl_sync(FULL, scale, j * G::RPL + lane / G::LPR);
+      const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+      __half2 m = __float2half2_rn(0.f);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t a, b;
-          codes_f16<CT>(w[q], a, b);
-          m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&a)));
-          m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&b)));
-        }
-        top = fmaxf(top, fmaxf(__low2float(m), __high2float(m)) * f);
+      for (int q = 0; q < 4; ++q) {
+        uint32_t a, b;
+        codes_f16<CT>(w[q], a, b);
+        m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&a)));
+        m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&b)));
       }
-      amax = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(top)));
-      if (amax < INFINITY || down < 1.f) break;
+      const float most = fmaxf(__low2float(m), __high2float(m));
+      top = fmaxf(top, most * f);
+      far = fmaxf(far, most * (f * 0x1p-16f));
     }
+    const float amax = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(top)));
     const uint32_t bits = __float_as_uint(scale + 0.f);  // (a scale of -0 is zero)
     const bool broken = __any_sync(FULL, !(scale >= 0.f && scale < INFINITY));
     // (the largest power of two is 2^127, of which the largest value may be more than the largest code)
     const float now = broken ? __uint_as_float(0x7fffffffu)
-                             : down < 1.f ? fminf(pow2_scale<CT>(amax) * 0x1p16f, 0x1p127f) : pow2_scale<CT>(amax);
+                             : amax < INFINITY ? pow2_scale<CT>(amax)
+                                               : fminf(pow2_scale<CT>(__uint_as_float(__reduce_max_sync(FULL, __float_as_uint(far)))) * 0x1p16f, 0x1p127f);
     // all scales powers of two, none more than 2^15 above the new one (nor subnormal): factors in fp16
     const bool pow2 = (bits & 0x7fffffu) == 0 && (bits == 0 || bits >= 0x00800000u) &&
                       (int)(bits >> 23) - (int)(__float_as_uint(now) >> 23) <= 15;
@@ -347,12 +349,13 @@ struct Block {
       }
       return now;
     }
-    const Divider by(now * down);
+    const bool large = now > 0x1p110f;  // (products past fp32: both sides 2^-16 of themselves)
+    const float unit = large ? now * 0x1p-16f : now, mine = large ? scale * 0x1p-16f : scale;
+    const Divider by(unit);
 #pragma unroll
     for (int j = 0; j < G::NI; ++j) {
-      float f = __shfl_sync(FULL, scale, j * G::RPL + lane / G::LPR);
-      if (f == now) continue;
-      f *= down;
+      const float f = __shfl_sync(FULL, mine, j * G::RPL + lane / G::LPR);
+      if (f == unit) continue;
       uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
