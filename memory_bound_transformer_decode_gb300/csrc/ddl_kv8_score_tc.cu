@@ -409,10 +409,12 @@ int kv8_score_tc_launch(const ScoreArgs& s, int type, int dtype, bool ex, int sm
   int most = 128 * 1024 / (hd * 2 * (f32 ? 2 : 1));
   most = most < THREADS ? most : THREADS;
   a.tiles = nq < most ? nq : most;
-  // tiles a CTA takes: about one wave of CTAs, each of which begins with all queries (several requests, whose lengths come
-  // to 5/8 of the bound: 8/5 waves of the bound); four for few queries, for the sake of balance
+  // tiles a CTA takes: about one wave of CTAs, each of which begins with all queries (several requests, whose lengths are
+  // taken to come to 5/8 of the bound: 8/5 waves of it).  Four waves, of 128 bf16 queries a head: 2 requests of up to
+  // 8192, 4 heads 21.9 us for 12.7, 16 of 2048 20.3 for 16.8, 16 of 8192, 1 head 25.0 for 14.8, but 2 of 32768, 2 heads
+  // 27.6 for 28.5; of 512: 33.0 for 21.4, 31.2 for 32.1.
   const int64_t tiles = ((int64_t)a.a.max_len + TOK - 1) / TOK, units = (int64_t)a.a.R * a.a.Hkv;
-  int64_t ctas = (int64_t)sms * (a.a.R == 1 ? 5 : nq <= 128 ? 20 : 8) / 5 / units;
+  int64_t ctas = (int64_t)sms * (a.a.R == 1 ? 5 : 8) / 5 / units;
   ctas = ctas < 1 ? 1 : ctas;
   a.wb = (int32_t)((tiles + ctas - 1) / ctas);
   if (a.wb > SCORE_TC_TILES) a.wb = SCORE_TC_TILES;
