@@ -70,12 +70,6 @@ __device__ __forceinline__ uint32_t score_key(float x) {
 constexpr int SEL_BITS = 10, SEL_BINS = 1 << SEL_BITS, SEL_THREADS = 512, SEL_WARPS = SEL_THREADS / 32;
 constexpr int SEL_PASSES = (32 + SEL_BITS - 1) / SEL_BITS;
 
-__device__ __forceinline__ uint32_t ldu_cluster(const uint32_t* p, int rank) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(smem_addr(p), rank)) : "memory");
-  return v;
-}
-
 // SM: the scores fit shared memory.  (If not, loops count without sign: their last step may end past 2^31.)
 template <bool SM>
 __global__ void __launch_bounds__(SEL_THREADS) kv8_select_kernel(const __grid_constant__ EvictArgs A, const int C) {

@@ -115,7 +115,6 @@ struct SampleSmem {
   unsigned long long chunk[SM_MAX_CLUSTER * SM_WARPS];
   uint32_t num[256], mass_lo[256], mass_hi[256];  // a digit's elements and their weights
   uint32_t range[2];
-  unsigned long long red64b[SM_WARPS];
   unsigned long long red64[SM_WARPS];
   float redf[SM_WARPS];
   uint32_t redu[SM_WARPS];
@@ -134,11 +133,6 @@ struct SampleSmem {
   Entry list[SM_LIST];
 };
 
-__device__ __forceinline__ uint32_t ldu_cluster(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
 __device__ __forceinline__ void ldu4_cluster(uint32_t a, uint32_t (&v)[4]) {
   asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(a) : "memory");
 }
