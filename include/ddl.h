@@ -475,8 +475,9 @@ int ddl_kv8_score(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, int32_t head_dim
  * After the call a cut request has keep_len[r] tokens in its new_table row
  * (ddl_page_plan with old lengths of 0 and keep_len to add takes such rows from the
  * free list).  Keys keep the rotation of the position at which they came: later rows
- * go on with their own positions, while ddl_kv8_attention's window and distance bias
- * count cached tokens.  All layers of a stack have one length per request, so they
+ * go on with their own positions (ddl_page_plan's row_pos, which counts cached tokens,
+ * plus the tokens that the row's request has lost so far), while ddl_kv8_attention's
+ * window and distance bias count cached tokens.  All layers of a stack have one length per request, so they
  * are cut by the same keep_len.
  *  - 1 <= R <= DDL_KV8_MAX_REQS; max_len bounds kv_len and score_stride >= max_len
  *    (DDL_ERR_ARG); 1 <= max_keep <= max_len bounds keep_len of the requests that are

@@ -12,8 +12,9 @@
 // fp16, exact but for the one rounding of the code; rows whose scale already is the new one keep their codes.
 //
 // What bounds it: few requests, the chain of barriers and dependent loads (1 of 32769 tokens to 8193, 8 heads: 23 us, with
-// cold caches 30); many, the move's rows of 64 or 128 bytes, each an access of its own, behind the choice (32 of up to 8192
-// to 2048, 8 heads: 65 us, choice 19 and move 43 at 51 % of the DRAM rate; its bytes would take 33).
+// cold caches 30); many, the move behind the choice (32 of up to 8192 to 2048, 8 heads: 65 us, choice 19 and move 44 at 50 %
+// of the DRAM rate; its bytes would take 33): a warp moves one block after four dependent loads (lengths, indices, pages,
+// scale and codes), and with a third of the warps that an SM holds too few bytes are on their way.
 #include <cuda_bf16.h>
 
 #include <type_traits>

@@ -310,7 +310,12 @@ __global__ void __launch_bounds__(256, 3) kv8_score_few_kernel(const __grid_cons
   }
 }
 
-constexpr int FEW_16 = 8, FEW_F32 = 4;  // tiles of the ring kernel at most
+// Tiles of the ring kernel at most, which passes over the queries' fragments once a block; more go to the tcgen05 kernel, whose
+// time grows little with them.  Ring and tcgen05, 1 request of 8192 with 64/8 heads, 16 of up to 2048 and 64 of up to 4096 with
+// 32/4: bf16, 4 tiles 8.7 and 11.7 us, 8.0 and 19.5, 35 and 74; 8: 10.4 and 12.3, 12.8 and 19.9, 59 and 74; 12: 13.8 and 13.0,
+// 18.2 and 25.4, 74 and 77; 16: 16.9 and 13.6, 21.5 and 20.4, 87 and 76.  fp32, 4: 9.0 and 11.9, 11.2 and 19.3, 49 and 77;
+// 8: 13.7 and 12.8, 16.9 and 19.8, 77 and 78; 12: 29 and 13.7, 28 and 25.7, 137 and 83 (one CTA an SM).
+constexpr int FEW_16 = 8, FEW_F32 = 4;
 
 enum { ONE_TILE, FEW_TILES, MANY_TILES };
 template <int CT, int DT, int HD>

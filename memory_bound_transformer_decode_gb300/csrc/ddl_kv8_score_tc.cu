@@ -2,9 +2,14 @@
 // rows) on the tcgen05 tensor cores.
 //
 // S = K Q^T with 128 tokens as M and up to 256 queries as N, fp16 operands and fp32 accumulators in
-// tensor memory: a thread then has one token and walks over its queries' scores, so that the sum of
-// weights needs no other thread.  Codes (e4m3 and int8 alike) are exact in fp16; Q is scaled by a power
-// of two per query and split as in the warp kernel, the remainders of fp32 rows as a second set of MMAs.
+// tensor memory: a thread then has one token and adds up the weights of its queries without shuffles.
+// Codes (e4m3 and int8 alike) are exact in fp16; Q is scaled by a power of two per query and split as
+// in the warp kernel, the remainders of fp32 rows as a second set of MMAs.
+//
+// Four threads share a token, one of each warpgroup, with every fourth 16 of its queries.  Their sums meet in shared
+// memory (`part`), where the first warpgroup adds them up in a fixed order after the CTA's next barrier, the first one of
+// the next tile; two tiles' sums lie there, so that the next tile's are left beside those still being read, and the
+// barrier of the tile after that orders the ones that take their place.
 //
 // A CTA of four warpgroups takes one K/V head of a request, all its queries in shared memory (512 16-bit or 256
 // fp32 ones of 128 at a time), and tiles of 128 tokens one after the other.  Two accumulators of 256 columns: the
@@ -15,7 +20,8 @@
 // scheduler: issue slots at 31 %), four of 128 21.8 (all wait at once), four of 2 x 64 24.8.
 //
 // What bounds it: exponentials (and tanh) of tokens x queries: 64 rows of 28/4 heads of two requests of up to 8192, capped
-// scores, 28 us, issue slots at 60 %, tensor pipe at 10 %.
+// scores, 28 us, issue slots at 59 %, tensor pipe at 10 %; without cap 20; fp32 rows (the layer stack's), half as many
+// queries at a time, 35 and 28.
 #include <cuda_bf16.h>
 
 #include "ddl_kv8_score.h"
@@ -410,9 +416,9 @@ int kv8_score_tc_launch(const ScoreArgs& s, int type, int dtype, bool ex, int sm
   most = most < THREADS ? most : THREADS;
   a.tiles = nq < most ? nq : most;
   // tiles a CTA takes: about one wave of CTAs, each of which begins with all queries (several requests, whose lengths are
-  // taken to come to 5/8 of the bound: 8/5 waves of it).  Four waves, of 128 bf16 queries a head: 2 requests of up to
-  // 8192, 4 heads 21.9 us for 12.7, 16 of 2048 20.3 for 16.8, 16 of 8192, 1 head 25.0 for 14.8, but 2 of 32768, 2 heads
-  // 27.6 for 28.5; of 512: 33.0 for 21.4, 31.2 for 32.1.
+  // taken to come to 5/8 of the bound: 8/5 waves of it; with other lengths the grain is another, the results are not).
+  // Four waves, of 128 bf16 queries a head: 2 requests of up to 8192, 4 heads 21.9 us for 12.7, 16 of 2048 20.3 for 16.8,
+  // 16 of 8192, 2 heads 25.9 for 23.8, but 2 of 32768 27.6 for 28.5; of 512, 4 heads: 33.0 for 21.4, 31.2 for 32.1.
   const int64_t tiles = ((int64_t)a.a.max_len + TOK - 1) / TOK, units = (int64_t)a.a.R * a.a.Hkv;
   int64_t ctas = (int64_t)sms * (a.a.R == 1 ? 5 : 8) / 5 / units;
   ctas = ctas < 1 ? 1 : ctas;

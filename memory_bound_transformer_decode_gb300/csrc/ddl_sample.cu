@@ -32,14 +32,17 @@
 //  3. Weights: sums per warp of what certainly stays; the elements of the open bins go
 //     to a list.
 //  4. The list decides both borders (radix select by number, then by sum of weights,
-//     ties by id), in one CTA.  Lists that overflow (all logits alike, say) are
-//     replaced by the row itself: the same selection by the whole cluster.
+//     ties by id), in one CTA.  Lists that overflow (all logits alike, or top-p so near
+//     1 that its border lies among very many small weights) are replaced by the row
+//     itself: the same selection by the whole cluster, a pass over the row a digit.
 //  5. The warps' sums, in id order, give the run that holds the draw, which its CTA
 //     looks through again.
 //
-// What bounds it: one row, the chain of passes and cluster barriers (152064 fp32, greedy 4.8 us, unfiltered 12.8,
+// What bounds it: one row, the chain of passes and cluster barriers (152064 fp32, greedy 5.2 us, unfiltered 13,
 // top-k 50 16, top-p 0.9 27); many, instructions: some 50 for each weight that counts, shared-memory atomics of the
-// histogram (256 rows of 128256 bf16: 15.5, 81, 38, 167 us; reading them once from HBM would take 9.7).
+// histogram (256 rows of 128256 bf16: 15.7, 82, 38, 167 us; reading them once from HBM would take 9.7).  Top-p near 1,
+// logits N(0, 2) and 32 high ones, T 1, at 0.9 / 0.99 / 0.995 / 0.999 / 0.9999: one row 27 / 32 / 36 / 90 / 93 us, 64 of
+// 152064 68 / 80 / 112 / 218 / 226, the 256 167 / 184 / 371 / 796 / 839: from 0.995 or 0.999 on lists overflow.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -568,7 +571,7 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const __grid_cons
   extern __shared__ __align__(16) uint8_t sample_smem[];
   SampleSmem& S = *reinterpret_cast<SampleSmem*>(sample_smem);
   constexpr int VEC = Row<DT>::VEC;
-  constexpr int U = 16 / VEC;  // loads on their way where registers are short (256 rows of 128256 bf16, top-p: 164 us, with 4 186)
+  constexpr int U = 16 / VEC;  // loads on their way where registers are short (256 rows of 128256 bf16, top-p 0.9: 167 us, with 4 187)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = A.cluster, b = blockIdx.x / C, rank = blockIdx.x % C, runs = C * SM_WARPS;
   if (tid < 64) {
@@ -650,7 +653,10 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const __grid_cons
   // (an infinite T makes all weights 1)
   const float least = by_m ? __double2float_ru((double)W.top + S.log_m) : M == 1.f && T < INFINITY ? W.top : -INFINITY;
 
-  // 1b. the bound by the lanes' maxima, in bins of 8; all elements from there up to the list
+  // 1b. the bound by the lanes' maxima, in bins of 8; all elements from there up to the list.  For a k of up to half the
+  // lanes (and half the list): among so many maxima the k-th largest is near the row's k-th, and there are enough of them.  It and the
+  // histogram's way, 256 rows of 128256 bf16 (lanes 512), k 50 / 256: 38 and 83 us / 48 and 87; 64 of 152064 fp32
+  // (2048), k 50 / 1000: 25 and 44 / 36 and 48; one row (8192), k 50 / 2000: 16 and 21 / 22.0 and 22.4.
   Open o = {SM_BINS, 0u, SM_BINS, -1};
   uint32_t listed = 0;
   bool heads = by_k && K <= min(C * SM_THREADS / 2, SM_LIST / 2);  // the list holds all elements of the top-k head
@@ -775,7 +781,8 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const __grid_cons
       float bw = block_before(sw, S.redf, all_w);
       const float k_top = o.k_bin < SM_BINS ? (float)o.k_in * exp2f(((float)o.k_bin - 0.5f) * (-1.f / SM_PER_OCTAVE)) : 0.f;
       const float k_low = k_top * exp2f(-1.f / SM_PER_OCTAVE);
-      // sums of 2048 fp32 numbers: within 1e-4 (some 40 additions in a row, 2^-24 each)
+      // sums of 2048 fp32 numbers: some 40 additions in a row, 2^-24 each: within 1e-5.  Taken with room: 3e-4 for the
+      // bins' sums on both sides of the total, 1e-4 for the running sum.
       const float want_lo = P * (all_w + k_low) * 0.9997f, want_hi = P * (all_w + k_top) * 1.0003f;
       int first_lo = SM_BINS, first_hi = SM_BINS;
 #pragma unroll
@@ -888,8 +895,8 @@ __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const __grid_cons
       hs = hs2 = 0;
       ls = ls2 = 0;
     };
-    // all weights; of top-k that leaves few elements, only theirs (256 rows of 128256 bf16: top-k 5000 108 us, all weights
-    // 135; 100000: 184, 148)
+    // all weights; of top-k that leaves few elements, only theirs (256 rows of 128256 bf16, theirs and all weights: top-k
+    // 5000 108 and 135 us, 16032 128 and 139, 19008 132 and 140, 30000 146 and 144, 100000 184 and 144)
     if (o.k_bin == SM_BINS || K > A.V / 8) {
       row.template each<U>(
           v0, v1,

@@ -572,7 +572,13 @@ def ddl_kv8_evict(pool: tuple, score: torch.Tensor, kv_len: torch.Tensor, keep_l
     K/V head by itself: the first `sinks`, the newest `recent` and the others
     of the largest score [R, H_kv, length].  Their rows go, in order, to the
     pages of new_table [R, new_pages_per_seq]; their indices to kept [R, H_kv,
-    max_keep] (int32), their scores to score_out (like score)."""
+    max_keep] (int32), their scores to score_out (like score).
+
+    Later rows of a cut request keep their true positions: ddl_page_plan's
+    row_pos plus the tokens `gone` [R] cut off so far.  On the device, without
+    a size from it, so that a step can be captured:
+        of = torch.searchsorted(row_off[1:], torch.arange(T, ...), right=True)
+        row_pos += torch.where(row_pos >= 0, gone[of.clamp(max=R - 1)], 0)"""
     st = (_mod or _torch_module()).kv8_evict(pool, score, kv_len, keep_len, page_table, new_table, max_len, kept,
                                              score_out, sinks, recent, bad, stream and stream.cuda_stream)
     if st:
