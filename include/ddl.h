@@ -441,7 +441,8 @@ int ddl_kv8_attention(const ddl_kv8* kv, int32_t H_q, int32_t H_kv, int32_t head
  *    is not finite among a row's keys, gives NaN in the scores of the tokens
  *    concerned (a NaN score stays NaN until decay is 0).
  *  - Precision: scores and weights as in ddl_kv8_attention (q of fp32 rows to
- *    2^-22), sums in fp32, in a fixed order: two calls give the same bits.
+ *    2^-22; weights below 2^-126 are zero), sums in fp32, in a fixed order: two
+ *    calls give the same bits.
  *  - Limits, max_rows, max_len, page_table, bad_out: as ddl_kv8_attention (bit 1: an
  *    internal wait gave up; the scores of the tokens concerned are NaN).
  *    score_stride >= max_len (DDL_ERR_ARG).  A token of a page outside the pool
